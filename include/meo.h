@@ -65,7 +65,7 @@
 extern "C" {
 #endif
 
-#define MEO_VERSION 8
+#define MEO_VERSION 9
 
 /* Return codes. */
 #define MEO_OK          0
@@ -84,6 +84,7 @@ extern "C" {
 #define MEO_F32  0
 #define MEO_BF16 1
 #define MEO_I8   2   /* state_dtype only: 8-bit group-quantized first moment */
+#define MEO_MX4  3   /* grad_dtype of meo_galore_mx4_step only: 4-bit microscaled codes */
 
 /*
  * One parameter tensor and its gradient, viewed as [batch, rows, cols]:
@@ -504,6 +505,103 @@ int     meo_galore_step(const meo_galore_hparams* hp, int64_t step, int32_t n, c
 int     meo_galore_refresh(const meo_galore_hparams* hp, int32_t n, const meo_tensor* tensors,
                            const meo_galore_state* states, void* workspace, size_t workspace_bytes,
                            void* stream);
+
+/* ----------------------------------------------------------------------- MX4 */
+
+/*
+ * MX4: 4-bit microscaled matrices, the MXFP4 format of the OCP Microscaling Formats
+ * specification (v1.0). A matrix [rows][cols] is cut into blocks of 32 consecutive
+ * values of a row. A block has one scale 2^(e - 127), held as the byte e, and a 4-bit
+ * code per value: a sign (bit 3) and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (E2M1) times
+ * the scale.
+ *   codes   uint8 [rows][16 * nb], nb = ceil(cols / 32): value 2i of a block in the low
+ *           half of its byte i, value 2i + 1 in the high half; 16-byte aligned
+ *   scales  uint8 [rows][nb]
+ * A last block with fewer than 32 values is filled up with zero codes. Zeroed codes and
+ * scales are a matrix of zeros.
+ *
+ * Quantization (the specification's conversion): e - 127 = floor(log2 max|v|) - 2,
+ * clamped to [-127, 125], over the block's values; each value times 2^(127 - e) to the
+ * nearest code, ties to the even one, magnitudes past 6 to 6 (the block's largest may lie
+ * between 6 and 8 scales). A block of zeros has e = 0; zeros keep their sign. A block
+ * holding a NaN or an infinity has e = 255 and codes 0, and reads back as NaN.
+ *
+ * meo_mx4_quantize writes codes and scales of each of n matrices, meo_mx4_dequantize
+ * reads them and writes the values: exact in float32 and bfloat16 for every e that
+ * quantization writes (past it a product beyond the type's range becomes an infinity).
+ * The values are [rows][cols] with `ld` elements between rows, or, with `transposed`,
+ * [cols][rows] with `ld` elements between their rows (blocks then run down the values'
+ * columns). All matrices of a call share `transposed`. Elements between rows
+ * (ld > row length) are neither read nor written.
+ *
+ * meo_mx4_matmul computes C = A B^T for each of n products: A [m][k] and B [n][k] in
+ * MX4, C [m][n] float32 or bfloat16 with `ldc` elements between rows. Products of codes
+ * are exact, sums are float32 (bfloat16 outputs are rounded once, to nearest even).
+ * k = 0 gives zeros. A NaN scale makes every output that its block enters NaN.
+ *
+ * The calls take no workspace and allocate nothing; descriptors travel as kernel
+ * arguments, 32 matrices per launch, so the calls can be captured into a graph and run
+ * concurrently on any streams. Matrices without elements are skipped. Errors as for the
+ * steps: MEO_ESHAPE for negative sizes, sizes past 2^31 - 1 or a leading dimension below
+ * the row length, MEO_EALIGN for codes that are not 16-byte aligned.
+ */
+typedef struct meo_mx4_matrix {
+    void*   data;       /* values; read by quantize, written by dequantize      */
+    void*   codes;      /* uint8 [rows][16 * ceil(cols / 32)]                    */
+    void*   scales;     /* uint8 [rows][ceil(cols / 32)]                         */
+    int64_t rows, cols; /* of the MX4 matrix; blocks run along cols              */
+    int64_t ld;         /* elements between rows of `data`                       */
+    int32_t dtype;      /* of `data`: MEO_F32 or MEO_BF16                        */
+    int32_t reserved;   /* 0                                                     */
+} meo_mx4_matrix;
+
+typedef struct meo_mx4_product {
+    const void* a_codes;  /* A [m][k] */
+    const void* a_scales;
+    const void* b_codes;  /* B [n][k] */
+    const void* b_scales;
+    void*   c;            /* [m][ldc] */
+    int64_t m, n, k, ldc;
+    int32_t dtype;        /* of c: MEO_F32 or MEO_BF16 */
+    int32_t reserved;     /* 0 */
+} meo_mx4_product;
+
+int meo_mx4_quantize(int32_t n, const meo_mx4_matrix* matrices, int32_t transposed, void* stream);
+int meo_mx4_dequantize(int32_t n, const meo_mx4_matrix* matrices, int32_t transposed, void* stream);
+int meo_mx4_matmul(int32_t n, const meo_mx4_product* products, void* stream);
+
+/*
+ * GaLore's step with its projector in MX4 (the ms-swift page's Q-GaLore section keeps the
+ * projection quantized; the format here is MX4). The method, hyperparameters, defaults and
+ * errors are meo_galore_step's; what differs is storage:
+ *   - the projector is held once, as U^T [r][d] in MX4 (`projector`, `projector_scale`),
+ *     and both products use the values that the codes stand for;
+ *   - a refresh computes the projector as meo_galore_refresh does, starting from the
+ *     stored values, and quantizes its bf16 transpose [r][d];
+ *   - a projected tensor's gradient may be MX4 (grad_dtype MEO_MX4): `grad` then holds the
+ *     codes of the gradient oriented [D][d], blocks along the contraction (right side: G
+ *     itself; left side: G^T, i.e. G quantized with `transposed`), 16-byte aligned, and
+ *     `grad_scale` its scales. R = G U is then the product of the two MX4 matrices.
+ *     A call that refreshes the projectors needs bf16 gradients (MEO_EDTYPE).
+ * Tensors that are not 2-D take AdamW as in meo_galore_step (projector pointers NULL).
+ */
+typedef struct meo_galore_mx4_state {
+    float*      exp_avg;         /* [D][r] projected, [numel] otherwise               */
+    float*      exp_avg_sq;      /* [D][r] projected, [numel] otherwise               */
+    void*       projector;       /* codes [r][16 * ceil(d / 32)]; 2-D tensors only    */
+    void*       projector_scale; /* scales [r][ceil(d / 32)]; 2-D tensors only        */
+    const void* grad_scale;      /* scales [D][ceil(d / 32)] of an MX4 gradient       */
+} meo_galore_mx4_state;
+
+size_t meo_galore_mx4_workspace_size(const meo_galore_hparams* hp, int32_t n, const meo_tensor* tensors);
+int    meo_galore_mx4_validate(const meo_galore_hparams* hp, int64_t step, int32_t n, const meo_tensor* tensors,
+                               const meo_galore_mx4_state* states);
+int    meo_galore_mx4_step(const meo_galore_hparams* hp, int64_t step, int32_t n, const meo_tensor* tensors,
+                           const meo_galore_mx4_state* states, void* workspace, size_t workspace_bytes,
+                           void* stream);
+int    meo_galore_mx4_refresh(const meo_galore_hparams* hp, int32_t n, const meo_tensor* tensors,
+                              const meo_galore_mx4_state* states, void* workspace, size_t workspace_bytes,
+                              void* stream);
 
 /* ------------------------------------------------------- per-tensor scalars */
 

@@ -25,7 +25,7 @@ c_float_p = ctypes.POINTER(ctypes.c_float)
 
 MEO_OK, MEO_EINVAL, MEO_ESHAPE, MEO_EDTYPE, MEO_ENULL, MEO_EWORKSPACE, MEO_EALIGN, MEO_EHIP, MEO_EMEMORY = (
     0, -1, -2, -3, -4, -5, -6, -7, -8)
-MEO_F32, MEO_BF16, MEO_I8 = 0, 1, 2
+MEO_F32, MEO_BF16, MEO_I8, MEO_MX4 = 0, 1, 2, 3
 I8_GROUP = 128  # values per scale of an 8-bit first moment
 ERROR_NAMES = {MEO_EINVAL: "MEO_EINVAL", MEO_ESHAPE: "MEO_ESHAPE", MEO_EDTYPE: "MEO_EDTYPE",
                MEO_ENULL: "MEO_ENULL", MEO_EWORKSPACE: "MEO_EWORKSPACE", MEO_EALIGN: "MEO_EALIGN",
@@ -45,6 +45,8 @@ EXPORTS = [
     "meo_galore_step", "meo_galore_refresh",
     "meo_adafactor_scalar_offsets", "meo_came_scalar_offsets", "meo_lamb_scalar_offsets",
     "meo_adafactor_step_noalloc",
+    "meo_mx4_quantize", "meo_mx4_dequantize", "meo_mx4_matmul",
+    "meo_galore_mx4_workspace_size", "meo_galore_mx4_validate", "meo_galore_mx4_step", "meo_galore_mx4_refresh",
 ]
 MEO_NOALLOC_SCRATCH_BYTES = 64 << 20
 MEO_NUM_PASSES = 17
@@ -115,6 +117,22 @@ class meo_galore_hparams(ctypes.Structure):
 class meo_galore_state(ctypes.Structure):
     _fields_ = [("exp_avg", c_void_p), ("exp_avg_sq", c_void_p), ("projector", c_void_p),
                 ("projector_t", c_void_p)]
+
+
+class meo_mx4_matrix(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("codes", c_void_p), ("scales", c_void_p), ("rows", c_int64), ("cols", c_int64),
+                ("ld", c_int64), ("dtype", c_int32), ("reserved", c_int32)]
+
+
+class meo_mx4_product(ctypes.Structure):
+    _fields_ = [("a_codes", c_void_p), ("a_scales", c_void_p), ("b_codes", c_void_p), ("b_scales", c_void_p),
+                ("c", c_void_p), ("m", c_int64), ("n", c_int64), ("k", c_int64), ("ldc", c_int64),
+                ("dtype", c_int32), ("reserved", c_int32)]
+
+
+class meo_galore_mx4_state(ctypes.Structure):
+    _fields_ = [("exp_avg", c_void_p), ("exp_avg_sq", c_void_p), ("projector", c_void_p),
+                ("projector_scale", c_void_p), ("grad_scale", c_void_p)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -204,6 +222,20 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.meo_galore_step.restype = ctypes.c_int
     lib.meo_galore_refresh.argtypes = [GH, c_int32, T, GS, c_void_p, c_size_t, c_void_p]
     lib.meo_galore_refresh.restype = ctypes.c_int
+    GX, MM, MP = (ctypes.POINTER(c) for c in (meo_galore_mx4_state, meo_mx4_matrix, meo_mx4_product))
+    lib.meo_galore_mx4_workspace_size.argtypes = [GH, c_int32, T]
+    lib.meo_galore_mx4_workspace_size.restype = c_size_t
+    lib.meo_galore_mx4_validate.argtypes = [GH, c_int64, c_int32, T, GX]
+    lib.meo_galore_mx4_validate.restype = ctypes.c_int
+    lib.meo_galore_mx4_step.argtypes = [GH, c_int64, c_int32, T, GX, c_void_p, c_size_t, c_void_p]
+    lib.meo_galore_mx4_step.restype = ctypes.c_int
+    lib.meo_galore_mx4_refresh.argtypes = [GH, c_int32, T, GX, c_void_p, c_size_t, c_void_p]
+    lib.meo_galore_mx4_refresh.restype = ctypes.c_int
+    for name, arr in (("meo_mx4_quantize", MM), ("meo_mx4_dequantize", MM)):
+        getattr(lib, name).argtypes = [c_int32, arr, c_int32, c_void_p]
+        getattr(lib, name).restype = ctypes.c_int
+    lib.meo_mx4_matmul.argtypes = [c_int32, MP, c_void_p]
+    lib.meo_mx4_matmul.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -771,6 +803,183 @@ def galore_init_state(param: torch.Tensor, rank: int, proj_type: str = "std") ->
     return {k: torch.zeros(s, dtype=torch.bfloat16 if k.startswith("projector") else torch.float32,
                            device=param.device)
             for k, s in galore_state_shapes(param.shape, rank, proj_type).items()}
+
+
+# ----------------------------------------------------------------------------- MX4
+
+MX4_BLOCK = 32  # values per scale
+
+
+class MX4Tensor:
+    """An MX4 matrix [rows][cols] (meo.h): uint8 ``codes`` [rows][16 * blocks] and uint8
+    ``scales`` [rows][blocks], blocks = ceil(cols / 32) along the columns. Both contiguous
+    and on one device."""
+
+    __slots__ = ("codes", "scales", "cols")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+            raise TypeError("MX4 codes and scales must be uint8")
+        blocks = -(-int(cols) // MX4_BLOCK)
+        if codes.dim() != 2 or scales.dim() != 2 or codes.shape[0] != scales.shape[0] or cols < 0 or \
+                codes.shape[1] != 16 * blocks or scales.shape[1] != blocks:
+            raise ValueError(f"MX4 codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not hold rows of "
+                             f"{cols} values")
+        if not (codes.is_contiguous() and scales.is_contiguous()):
+            raise ValueError("MX4 codes and scales must be contiguous (row-major)")
+        if codes.device != scales.device:
+            raise ValueError("MX4 codes and scales must be on one device")
+        self.codes, self.scales, self.cols = codes, scales, int(cols)
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device) -> "MX4Tensor":
+        blocks = -(-int(cols) // MX4_BLOCK)
+        return cls(torch.empty((rows, 16 * blocks), dtype=torch.uint8, device=device),
+                   torch.empty((rows, blocks), dtype=torch.uint8, device=device), cols)
+
+    @property
+    def shape(self):
+        return (self.codes.shape[0], self.cols)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def _mx4_matrices(values: Sequence[torch.Tensor], mx: Sequence[MX4Tensor], transposed: bool):
+    if len(values) != len(mx):
+        raise ValueError("values and MX4 tensors differ in length")
+    arr = (meo_mx4_matrix * max(len(mx), 1))()
+    for i, (v, q) in enumerate(zip(values, mx)):
+        if v.dtype not in _DTYPE:
+            raise TypeError("values must be float32 or bfloat16")
+        rows, cols = q.shape
+        want = (cols, rows) if transposed else (rows, cols)
+        if tuple(v.shape) != want:
+            raise ValueError(f"values of shape {tuple(v.shape)}, expected {want}")
+        if v.device != q.device:
+            raise ValueError("values and MX4 tensors must be on one device")
+        ld = v.stride(0) if v.shape[0] > 1 else max(v.shape[1], 1)
+        if v.numel() and ((v.shape[1] > 1 and v.stride(1) != 1) or ld < v.shape[1]):
+            raise ValueError("values must be row-major (rows may be strided)")
+        arr[i] = meo_mx4_matrix(v.data_ptr(), q.codes.data_ptr(), q.scales.data_ptr(), rows, cols,
+                                max(ld, v.shape[1]), _DTYPE[v.dtype], 0)
+    return arr
+
+
+def meo_mx4_quantize(values, mx, transposed: bool = False, stream=None) -> None:
+    """Each of ``values`` into the MX4Tensor of ``mx`` beside it."""
+    _check(load().meo_mx4_quantize(len(mx), _mx4_matrices(values, mx, transposed), int(bool(transposed)),
+                                   _stream(stream)))
+
+
+def meo_mx4_dequantize(values, mx, transposed: bool = False, stream=None) -> None:
+    """Writes each of ``values`` from the MX4Tensor of ``mx`` beside it."""
+    _check(load().meo_mx4_dequantize(len(mx), _mx4_matrices(values, mx, transposed), int(bool(transposed)),
+                                     _stream(stream)))
+
+
+def meo_mx4_matmul(a, b, c, stream=None) -> None:
+    """c[i] = a[i] b[i]^T for lists of MX4 tensors and their float32 or bfloat16 outputs."""
+    if not len(a) == len(b) == len(c):
+        raise ValueError("a, b and c differ in length")
+    arr = (meo_mx4_product * max(len(c), 1))()
+    for i, (x, y, z) in enumerate(zip(a, b, c)):
+        (m, k), (n, k2) = x.shape, y.shape
+        if k != k2 or tuple(z.shape) != (m, n):
+            raise ValueError(f"product of {x.shape} and {y.shape} transposed into {tuple(z.shape)}")
+        if z.dtype not in _DTYPE:
+            raise TypeError("outputs must be float32 or bfloat16")
+        if not x.device == y.device == z.device:
+            raise ValueError("operands and output must be on one device")
+        ld = z.stride(0) if m > 1 else max(n, 1)
+        if z.numel() and ((n > 1 and z.stride(1) != 1) or ld < n):
+            raise ValueError("outputs must be row-major (rows may be strided)")
+        arr[i] = meo_mx4_product(x.codes.data_ptr(), x.scales.data_ptr(), y.codes.data_ptr(), y.scales.data_ptr(),
+                                 z.data_ptr(), m, n, k, max(ld, n), _DTYPE[z.dtype], 0)
+    _check(load().meo_mx4_matmul(len(c), arr, _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- GaLore, MX4 projector
+
+GALORE_MX4_KEYS = ["exp_avg", "exp_avg_sq", "projector", "projector_scale"]
+
+
+def _galore_mx4_args(hp, params, grads, states):
+    """The C arrays of a call; ``grads`` may hold MX4Tensors, oriented [D][d] (meo.h)."""
+    if not len(params) == len(grads) == len(states):
+        raise ValueError("params, grads and states differ in length")
+    tensors = (meo_tensor * max(len(params), 1))()
+    arr = (meo_galore_mx4_state * max(len(states), 1))()
+    for i, (p, g, st) in enumerate(zip(params, grads, states)):
+        right = p.dim() == 2 and (p.shape[0] >= p.shape[1]) == (hp.proj_type == MEO_GALORE_STD)
+        scale = None
+        if isinstance(g, MX4Tensor):
+            if p.dim() != 2:
+                raise ValueError("only a 2-D parameter takes an MX4 gradient")
+            want = tuple(p.shape) if right else (p.shape[1], p.shape[0])
+            if g.shape != want:
+                raise ValueError(f"MX4 gradient of shape {g.shape}, expected {want} (blocks along the contraction)")
+            tensors[i] = tensor_struct(p, p)
+            tensors[i].grad, tensors[i].grad_dtype = g.codes.data_ptr(), MEO_MX4
+            scale = g.scales.data_ptr()
+        else:
+            tensors[i] = tensor_struct(p, g)
+        shapes = galore_mx4_state_shapes(p.shape, hp.rank, "std" if hp.proj_type == MEO_GALORE_STD else "reverse_std")
+        for k in GALORE_MX4_KEYS:
+            t = st.get(k)
+            dt = torch.uint8 if k.startswith("projector") else torch.float32
+            if t is None:
+                continue
+            if t.dtype != dt:
+                raise TypeError(f"GaLore state {k} must be {dt}")
+            if not t.is_contiguous():
+                raise ValueError(f"GaLore state {k} must be contiguous (row-major)")
+            if k in shapes and tuple(t.shape) != tuple(shapes[k]):
+                raise ValueError(f"GaLore state {k} of shape {tuple(t.shape)}, expected {tuple(shapes[k])}")
+        arr[i] = meo_galore_mx4_state(*[_ptr(st.get(k)) for k in GALORE_MX4_KEYS], scale)
+    return tensors, arr
+
+
+def meo_galore_mx4_workspace_size(hp, params, grads) -> int:
+    tensors = (meo_tensor * max(len(params), 1))()
+    for i, p in enumerate(params):
+        tensors[i] = tensor_struct(p, p)
+    return int(load().meo_galore_mx4_workspace_size(ctypes.byref(hp), len(params), tensors))
+
+
+def meo_galore_mx4_validate(hp, step, params, grads, states) -> None:
+    tensors, arr = _galore_mx4_args(hp, params, grads, states)
+    _check(load().meo_galore_mx4_validate(ctypes.byref(hp), step, len(params), tensors, arr))
+
+
+def meo_galore_mx4_step(hp, step, params, grads, states, workspace=None, stream=None) -> None:
+    ws, nb = _ws(workspace)
+    tensors, arr = _galore_mx4_args(hp, params, grads, states)
+    _check(load().meo_galore_mx4_step(ctypes.byref(hp), step, len(params), tensors, arr, ws, nb, _stream(stream)))
+
+
+def meo_galore_mx4_refresh(hp, params, grads, states, workspace=None, stream=None) -> None:
+    ws, nb = _ws(workspace)
+    tensors, arr = _galore_mx4_args(hp, params, grads, states)
+    _check(load().meo_galore_mx4_refresh(ctypes.byref(hp), len(params), tensors, arr, ws, nb, _stream(stream)))
+
+
+def galore_mx4_state_shapes(shape, rank: int, proj_type: str = "std") -> Dict[str, tuple]:
+    """As galore_state_shapes, with the projector's transpose [r][d] in MX4."""
+    st: Dict[str, tuple] = galore_state_shapes(shape, rank, proj_type)
+    if "projector" in st:
+        d, r = st["projector"]
+        del st["projector_t"]
+        blocks = -(-d // MX4_BLOCK)
+        st["projector"], st["projector_scale"] = (r, 16 * blocks), (r, blocks)
+    return st
+
+
+def galore_mx4_init_state(param: torch.Tensor, rank: int, proj_type: str = "std") -> Dict[str, torch.Tensor]:
+    """Zero GaLore states for one parameter (projector in MX4)."""
+    return {k: torch.zeros(s, dtype=torch.uint8 if k.startswith("projector") else torch.float32, device=param.device)
+            for k, s in galore_mx4_state_shapes(param.shape, rank, proj_type).items()}
 
 
 # ----------------------------------------------------------------------------- state allocation

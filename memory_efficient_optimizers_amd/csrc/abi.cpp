@@ -20,6 +20,7 @@
 #include "meo.h"
 #include "internal.h"
 #include "galore.h"
+#include "mx4.h"
 
 using namespace meo;
 
@@ -1606,9 +1607,11 @@ int meo_came_shard_apply(const meo_came_hparams* hp, int64_t step, int32_t n, co
 
 // ----------------------------------------------------------------------------- GaLore
 
+}  // extern "C"
+
 namespace {
 
-enum GaList { kGaProjR = 0, kGaProjL, kGaBackR, kGaBackL, kGaFlat,
+enum GaList { kGaProjR = 0, kGaProjL, kGaBackR, kGaBackL, kGaFlat, kGxProjM /* MX4 gradients */,
               // projector refresh
               kRfInit, kRfG0N, kRfG0T, kRfG1N, kRfG1T, kRfGram, kRfOne, kRfCols, kRfStore, kGaListCount };
 
@@ -1617,6 +1620,8 @@ struct GaPlan {
     int device = 0;
     void* mem = nullptr;  // [GDesc right..., left...][TDesc flat...][RDesc...][item tables]
     const GDesc* gdesc = nullptr;
+    const GxDesc* gxdesc = nullptr;   // in gdesc's place when the projectors are MX4
+    std::vector<MxMat> quant;         // MX4: the refreshed projectors' quantization
     const TDesc* fdesc = nullptr;
     const RDesc* rdesc = nullptr;
     const int2* items[kGaListCount] = {};
@@ -1639,6 +1644,41 @@ void release_galore_plans() {  // caller holds g_mu
     g_ga_plans.clear();
 }
 
+// The per-tensor state pointers of a step with bf16 projectors (u, ut) or MX4 ones (uc,
+// us; gs: the scales of an MX4 gradient).
+struct GaState {
+    float* em = nullptr;
+    float* ev = nullptr;
+    void* u = nullptr;
+    void* ut = nullptr;
+    const void* uc = nullptr;
+    const void* us = nullptr;
+    const void* gs = nullptr;
+};
+
+std::vector<GaState> ga_states(int32_t n, const meo_galore_state* st) {
+    std::vector<GaState> out(st && n > 0 ? n : 0);
+    for (size_t k = 0; k < out.size(); ++k) {
+        out[k].em = st[k].exp_avg;
+        out[k].ev = st[k].exp_avg_sq;
+        out[k].u = st[k].projector;
+        out[k].ut = st[k].projector_t;
+    }
+    return out;
+}
+
+std::vector<GaState> ga_states(int32_t n, const meo_galore_mx4_state* st) {
+    std::vector<GaState> out(st && n > 0 ? n : 0);
+    for (size_t k = 0; k < out.size(); ++k) {
+        out[k].em = st[k].exp_avg;
+        out[k].ev = st[k].exp_avg_sq;
+        out[k].uc = st[k].projector;
+        out[k].us = st[k].projector_scale;
+        out[k].gs = st[k].grad_scale;
+    }
+    return out;
+}
+
 bool ga_projected(const meo_tensor& t) { return t.ndim == 2 && t.rows > 0 && t.cols > 0; }
 
 int32_t ga_rank(const meo_galore_hparams* hp, const meo_tensor& t) {
@@ -1658,9 +1698,9 @@ int64_t align256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
 // Workspace, per projected tensor, every array at a 256-byte boundary (offsets in
 // bytes): the step's two bf16 planes of N, [D][r] each; then, for the projector
-// refresh, two fp32 [r][d] iterates, one fp32 [r][D] product, and four fp64
-// [r][r] matrices.
-int64_t ga_layout(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, std::vector<int64_t>* offs,
+// refresh, two fp32 [r][d] iterates, one fp32 [r][D] product, four fp64 [r][r]
+// matrices and (mx: MX4 projectors) the refreshed projector in bf16, [d][r] and [r][d].
+int64_t ga_layout(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, bool mx, std::vector<int64_t>* offs,
                   std::vector<int64_t>* roffs = nullptr) {
     int64_t off = 0;
     if (offs) offs->assign(n, -1);
@@ -1678,7 +1718,7 @@ int64_t ga_layout(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts,
         const int64_t d = ga_basis(hp, ts[k]), D = ga_rows(hp, ts[k]);
         // the product buffer [r][D] later holds the basis [r][d] too
         off += 2 * align256(static_cast<int64_t>(r) * d * 4) + align256(static_cast<int64_t>(r) * std::max(D, d) * 4) +
-               4 * align256(static_cast<int64_t>(r) * r * 8);
+               4 * align256(static_cast<int64_t>(r) * r * 8) + (mx ? 2 * align256(d * r * 2) : 0);
     }
     return off;
 }
@@ -1700,7 +1740,7 @@ int check_galore_hp(const meo_galore_hparams* hp) {
 }
 
 int check_galore_tensors(const meo_galore_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts,
-                         const meo_galore_state* st) {
+                         const GaState* st, bool mx) {
     if (step < 1) return fail(MEO_EINVAL, "step must be >= 1 (1-based index of the step being taken)");
     if (n < 0) return fail(MEO_EINVAL, "negative tensor count");
     if (n == 0) return MEO_OK;
@@ -1719,34 +1759,45 @@ int check_galore_tensors(const meo_galore_hparams* hp, int64_t step, int32_t n, 
         if (t.ndim == 2 && numel > 0 && t.batch != 1) return fail(MEO_ESHAPE, who + "a 2-D tensor has batch 1");
         if (t.param_dtype != MEO_F32 && t.param_dtype != MEO_BF16)
             return fail(MEO_EDTYPE, who + "param_dtype must be MEO_F32 or MEO_BF16");
-        if (t.grad_dtype != MEO_F32 && t.grad_dtype != MEO_BF16)
-            return fail(MEO_EDTYPE, who + "grad_dtype must be MEO_F32 or MEO_BF16");
+        const bool g4 = mx && t.grad_dtype == MEO_MX4;
+        if (t.grad_dtype != MEO_F32 && t.grad_dtype != MEO_BF16 && !g4)
+            return fail(MEO_EDTYPE, who + (mx ? "grad_dtype must be MEO_F32, MEO_BF16 or MEO_MX4"
+                                              : "grad_dtype must be MEO_F32 or MEO_BF16"));
         if (t.state_dtype != MEO_F32) return fail(MEO_EDTYPE, who + "GaLore states are float32 (state_dtype MEO_F32)");
         if (numel == 0) continue;
         if (!t.param) return fail(MEO_ENULL, who + "param is NULL");
         if (!t.grad) return fail(MEO_ENULL, who + "grad is NULL");
         if (reinterpret_cast<uintptr_t>(t.param) % (t.param_dtype == MEO_BF16 ? 2 : 4))
             return fail(MEO_EALIGN, who + "param misaligned for its dtype");
-        if (reinterpret_cast<uintptr_t>(t.grad) % (t.grad_dtype == MEO_BF16 ? 2 : 4))
+        if (reinterpret_cast<uintptr_t>(t.grad) % (g4 ? 16 : t.grad_dtype == MEO_BF16 ? 2 : 4))
             return fail(MEO_EALIGN, who + "grad misaligned for its dtype");
-        const meo_galore_state& s = st[k];
-        if (!s.exp_avg) return fail(MEO_ENULL, who + "exp_avg is NULL");
-        if (!s.exp_avg_sq) return fail(MEO_ENULL, who + "exp_avg_sq is NULL");
-        if (reinterpret_cast<uintptr_t>(s.exp_avg) % 4 || reinterpret_cast<uintptr_t>(s.exp_avg_sq) % 4)
+        const GaState& s = st[k];
+        if (!s.em) return fail(MEO_ENULL, who + "exp_avg is NULL");
+        if (!s.ev) return fail(MEO_ENULL, who + "exp_avg_sq is NULL");
+        if (reinterpret_cast<uintptr_t>(s.em) % 4 || reinterpret_cast<uintptr_t>(s.ev) % 4)
             return fail(MEO_EALIGN, who + "exp_avg or exp_avg_sq misaligned");
         if (ga_projected(t)) {
-            if (t.grad_dtype != MEO_BF16)
-                return fail(MEO_EDTYPE, who + "a projected (2-D) tensor needs a bf16 gradient");
+            if (t.grad_dtype != MEO_BF16 && !g4)
+                return fail(MEO_EDTYPE, who + (mx ? "a projected (2-D) tensor needs a bf16 or MX4 gradient"
+                                                  : "a projected (2-D) tensor needs a bf16 gradient"));
+            if (g4 && !s.gs) return fail(MEO_ENULL, who + "grad_scale is NULL (MX4 gradient)");
             if (t.rows > kMaxDim || t.cols > kMaxDim) return fail(MEO_ESHAPE, who + "rows or cols exceed 2^31 - 1");
             const int32_t r = ga_rank(hp, t);
             if (r > kGaWide) return fail(MEO_EINVAL, who + "effective rank " + std::to_string(r) + " exceeds 256");
-            if (!s.projector || !s.projector_t) return fail(MEO_ENULL, who + "projector or projector_t is NULL");
-            if (reinterpret_cast<uintptr_t>(s.projector) % 2 || reinterpret_cast<uintptr_t>(s.projector_t) % 2)
-                return fail(MEO_EALIGN, who + "projector misaligned");
+            if (mx) {
+                if (!s.uc || !s.us) return fail(MEO_ENULL, who + "projector or projector_scale is NULL");
+                if (reinterpret_cast<uintptr_t>(s.uc) % 16)
+                    return fail(MEO_EALIGN, who + "MX4 projector codes not 16-byte aligned");
+            } else {
+                if (!s.u || !s.ut) return fail(MEO_ENULL, who + "projector or projector_t is NULL");
+                if (reinterpret_cast<uintptr_t>(s.u) % 2 || reinterpret_cast<uintptr_t>(s.ut) % 2)
+                    return fail(MEO_EALIGN, who + "projector misaligned");
+            }
             const int64_t D = ga_rows(hp, t);
             blocks[kGaProjR] += ceil_div(D, kGaTile);
             blocks[kGaBackR] += ceil_div(t.rows, kGaTile) * ceil_div(t.cols, kGaTile);
         } else {
+            if (g4) return fail(MEO_EDTYPE, who + "only projected (2-D) tensors take an MX4 gradient");
             blocks[kGaFlat] += ceil_div(numel, kFlatTile);
         }
     }
@@ -1755,7 +1806,7 @@ int check_galore_tensors(const meo_galore_hparams* hp, int64_t step, int32_t n, 
     return MEO_OK;
 }
 
-int check_galore_memory(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, const meo_galore_state* st,
+int check_galore_memory(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, const GaState* st, bool mx,
                         int dev) {
     for (int32_t k = 0; k < n; ++k) {
         const meo_tensor& t = ts[k];
@@ -1766,14 +1817,21 @@ int check_galore_memory(const meo_galore_hparams* hp, int32_t n, const meo_tenso
         const size_t ne = static_cast<size_t>(numel);
         const int32_t r = ga_rank(hp, t);
         const size_t mom = r ? static_cast<size_t>(ga_rows(hp, t)) * r : ne;
+        const bool g4 = t.grad_dtype == MEO_MX4;
+        const size_t nb = r ? static_cast<size_t>(ceil_div(ga_basis(hp, t), kMxBlock)) : 0;  // MX4 blocks along d
+        const size_t gb = g4 ? static_cast<size_t>(ga_rows(hp, t)) * nb : 0;
         struct Range { const void* p; size_t bytes; const char* name; };
         std::vector<Range> rs = {{t.param, ne * (t.param_dtype == MEO_BF16 ? 2 : 4), "param"},
-                                 {t.grad, ne * (t.grad_dtype == MEO_BF16 ? 2 : 4), "grad"},
-                                 {st[k].exp_avg, mom * 4, "exp_avg"}, {st[k].exp_avg_sq, mom * 4, "exp_avg_sq"}};
-        if (r) {
+                                 {t.grad, g4 ? gb * 16 : ne * (t.grad_dtype == MEO_BF16 ? 2 : 4), "grad"},
+                                 {st[k].em, mom * 4, "exp_avg"}, {st[k].ev, mom * 4, "exp_avg_sq"}};
+        if (g4) rs.push_back({st[k].gs, gb, "grad_scale"});
+        if (r && mx) {
+            rs.push_back({st[k].uc, nb * r * 16, "projector"});
+            rs.push_back({st[k].us, nb * r, "projector_scale"});
+        } else if (r) {
             const size_t pu = static_cast<size_t>(ga_basis(hp, t)) * r * 2;
-            rs.push_back({st[k].projector, pu, "projector"});
-            rs.push_back({st[k].projector_t, pu, "projector_t"});
+            rs.push_back({st[k].u, pu, "projector"});
+            rs.push_back({st[k].ut, pu, "projector_t"});
         }
         for (const Range& rg : rs) {
             const int rc = check_device_range(rg.p, rg.bytes, dev, who + rg.name, MEO_EMEMORY);
@@ -1783,8 +1841,9 @@ int check_galore_memory(const meo_galore_hparams* hp, int32_t n, const meo_tenso
     return MEO_OK;
 }
 
-int check_galore_workspace(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, void* ws, size_t bytes) {
-    const int64_t need = ga_layout(hp, n, ts, nullptr);
+int check_galore_workspace(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, bool mx, void* ws,
+                           size_t bytes) {
+    const int64_t need = ga_layout(hp, n, ts, mx, nullptr);
     if (need == 0) return MEO_OK;
     if (!ws) return fail(MEO_EWORKSPACE, "workspace is NULL");
     if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(MEO_EWORKSPACE, "workspace not 256-byte aligned");
@@ -1798,21 +1857,22 @@ int check_galore_workspace(const meo_galore_hparams* hp, int32_t n, const meo_te
     return check_device_range(ws, bytes, dev, "workspace", MEO_EWORKSPACE);
 }
 
-GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, const meo_galore_state* st,
+GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, const GaState* st, bool mx,
                         void* ws, int* rc) {
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess) {
         *rc = fail(MEO_EHIP, "hipGetDevice failed");
         return nullptr;
     }
-    std::vector<uint8_t> key(sizeof(int) * 3 + sizeof(void*) + n * (sizeof(meo_tensor) + sizeof(meo_galore_state)));
+    std::vector<uint8_t> key(sizeof(int) * 3 + sizeof(void*) + n * (sizeof(meo_tensor) + sizeof(GaState)));
     {
         uint8_t* w = key.data();
-        const int hdr[3] = {n, dev, hp->rank * 2 + (hp->proj_type == MEO_GALORE_REVERSE_STD ? 1 : 0)};
+        // hp->rank <= 2^31 - 1: the side and the projectors' form go with the count and device
+        const int hdr[3] = {n, dev * 4 + (hp->proj_type == MEO_GALORE_REVERSE_STD ? 1 : 0) + (mx ? 2 : 0), hp->rank};
         std::memcpy(w, hdr, sizeof hdr); w += sizeof hdr;
         std::memcpy(w, &ws, sizeof ws); w += sizeof ws;
         std::memcpy(w, ts, n * sizeof(meo_tensor)); w += n * sizeof(meo_tensor);
-        std::memcpy(w, st, n * sizeof(meo_galore_state));
+        std::memcpy(w, st, n * sizeof(GaState));
     }
     std::lock_guard<std::mutex> lock(g_mu);
     for (auto it = g_ga_plans.begin(); it != g_ga_plans.end(); ++it) {
@@ -1823,12 +1883,13 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
             return p;
         }
     }
-    *rc = check_galore_memory(hp, n, ts, st, dev);
+    *rc = check_galore_memory(hp, n, ts, st, mx, dev);
     if (*rc) return nullptr;
     std::vector<int64_t> woff, roff;
-    ga_layout(hp, n, ts, &woff, &roff);
+    ga_layout(hp, n, ts, mx, &woff, &roff);
     std::vector<RDesc> rd;
-    std::vector<GDesc> right, left;
+    std::vector<GxDesc> right, left;  // the MX4 fields stay zero for bf16 projectors
+    std::vector<MxMat> quant;
     std::vector<TDesc> flat;
     std::vector<int2> lists[kGaListCount];
     std::vector<int32_t> kr, kl;  // tensor indices of the right and left descriptors
@@ -1837,10 +1898,10 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
         int64_t numel = 0;
         overflow_numel(t, &numel);
         if (numel == 0) continue;
-        const meo_galore_state& s = st[k];
+        const GaState& s = st[k];
         if (ga_projected(t)) {
-            GDesc d;
-            std::memset(&d, 0, sizeof d);
+            GxDesc d;
+            std::memset(static_cast<void*>(&d), 0, sizeof d);
             d.m = static_cast<int32_t>(t.rows);
             d.n = static_cast<int32_t>(t.cols);
             const bool is_left = ga_left(hp, t);
@@ -1850,20 +1911,30 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
             d.g = static_cast<const uint16_t*>(t.grad);
             d.x = t.param;
             d.xbf16 = t.param_dtype == MEO_BF16;
-            d.em = s.exp_avg;
-            d.ev = s.exp_avg_sq;
-            d.u = static_cast<uint16_t*>(s.projector);
-            d.ut = static_cast<uint16_t*>(s.projector_t);
+            d.em = s.em;
+            d.ev = s.ev;
+            d.u = static_cast<uint16_t*>(s.u);
+            d.ut = static_cast<uint16_t*>(s.ut);
+            const bool g4 = t.grad_dtype == MEO_MX4;
             uint8_t* wb = static_cast<uint8_t*>(ws) + woff[k];
             d.nh = reinterpret_cast<uint16_t*>(wb);
             d.nl = reinterpret_cast<uint16_t*>(wb + (static_cast<int64_t>(d.D) * d.r * 2 + 255) / 256 * 256);
             d.vec = aligned16(d.g) && aligned16(d.u) && aligned16(d.ut) && d.n % 8 == 0 && d.d % 8 == 0 &&
                     d.r % 8 == 0;
+            if (mx) {
+                d.uc = static_cast<const uint8_t*>(s.uc);
+                d.us = static_cast<const uint8_t*>(s.us);
+                d.gs = static_cast<const uint8_t*>(s.gs);
+                d.nb = static_cast<int32_t>(ceil_div(d.d, kMxBlock));
+                // the gradient's rows (bf16) and the planes of N
+                d.vec = (g4 || (aligned16(d.g) && d.n % 8 == 0)) && d.r % 8 == 0;
+            }
             d.rvec = aligned16(d.em) && aligned16(d.ev) && d.r % 8 == 0;
             d.wvec = aligned16(d.x) && d.n % 8 == 0;
             d.btj = static_cast<int32_t>(is_left ? ceil_div(d.n, kGaTile * kGaBackRW) : ceil_div(d.n, kGaWide));
             (is_left ? left : right).push_back(d);
             (is_left ? kl : kr).push_back(k);
+            if (g4) continue;  // not refreshed
             // refresh descriptor
             RDesc q;
             std::memset(&q, 0, sizeof q);
@@ -1883,6 +1954,21 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
             q.w = reinterpret_cast<double*>(rb + 2 * sq + sy + ss);
             q.s2 = reinterpret_cast<double*>(rb + 2 * sq + sy + 2 * ss);
             q.w2 = reinterpret_cast<double*>(rb + 2 * sq + sy + 3 * ss);
+            if (mx) {
+                q.u = reinterpret_cast<uint16_t*>(rb + 2 * sq + sy + 4 * ss);
+                q.ut = reinterpret_cast<uint16_t*>(rb + 2 * sq + sy + 4 * ss + align256(static_cast<int64_t>(q.d) * q.r * 2));
+                MxMat w;
+                std::memset(&w, 0, sizeof w);
+                w.data = q.ut;
+                w.codes = static_cast<uint8_t*>(const_cast<void*>(s.uc));
+                w.scales = static_cast<uint8_t*>(const_cast<void*>(s.us));
+                w.rows = q.r;
+                w.cols = w.ld = q.d;
+                w.nb = d.nb;
+                w.bf16 = 1;
+                w.vec = q.d % 8 == 0;
+                quant.push_back(w);
+            }
             const int id = static_cast<int>(rd.size());
             rd.push_back(q);
             auto addr = [&](int list, int64_t count) {
@@ -1900,8 +1986,8 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
             std::memset(&d, 0, sizeof d);
             d.x = t.param;
             d.g = t.grad;
-            d.m = s.exp_avg;
-            d.v = s.exp_avg_sq;
+            d.m = s.em;
+            d.v = s.ev;
             d.numel = numel;
             d.gbf16 = t.grad_dtype == MEO_BF16;
             d.xbf16 = t.param_dtype == MEO_BF16;
@@ -1916,9 +2002,9 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
     // a dtype; its items cover 256 rows of U x up to kUrTiles tiles of N.
     int back_mode[2] = {kBackReg, kBackReg};
     for (int side = 0; side < 2; ++side) {
-        const std::vector<GDesc>& v = side ? left : right;
-        bool direct = true, all_f32 = true, all_bf16 = true;
-        for (const GDesc& d : v) {
+        const std::vector<GxDesc>& v = side ? left : right;
+        bool direct = !mx, all_f32 = true, all_bf16 = true;
+        for (const GxDesc& d : v) {
             direct = direct && d.vec && d.r % kGaKb == 0;
             all_f32 = all_f32 && !d.xbf16;
             all_bf16 = all_bf16 && d.xbf16;
@@ -1927,22 +2013,22 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
     }
     for (int side = 0; side < 2; ++side)
         if (back_mode[side] == kBackUr || back_mode[side] == kBackUrBf16)
-            for (GDesc& d : side ? left : right) d.btj = static_cast<int32_t>(ceil_div(ceil_div(d.D, kGaTile), kUrTiles));
+            for (GxDesc& d : side ? left : right) d.btj = static_cast<int32_t>(ceil_div(ceil_div(d.D, kGaTile), kUrTiles));
     // Right descriptors first, then left; the item tables index that array.
-    std::vector<GDesc> gd(right);
+    std::vector<GxDesc> gd(right);
     gd.insert(gd.end(), left.begin(), left.end());
-    bool proj_direct[2] = {true, true};  // right, left
-    for (const GDesc& d : right) proj_direct[0] = proj_direct[0] && d.vec && d.d % kGaKb == 0;
-    for (const GDesc& d : left) proj_direct[1] = proj_direct[1] && d.vec && d.d % kGaKb == 0;
+    bool proj_direct[2] = {!mx, !mx};  // right, left
+    for (const GxDesc& d : right) proj_direct[0] = proj_direct[0] && d.vec && d.d % kGaKb == 0;
+    for (const GxDesc& d : left) proj_direct[1] = proj_direct[1] && d.vec && d.d % kGaKb == 0;
     for (size_t i = 0; i < gd.size(); ++i) {
-        const GDesc& d = gd[i];
+        const GxDesc& d = gd[i];
         const bool is_left = i >= right.size();
         const int id = static_cast<int>(i);
         const int64_t pt = ceil_div(d.D, proj_direct[is_left] ? kGaPwRows : kGaProjRows);
         // both sides direct: one list (kGaProjR) for the mixed kernel
         const bool one_list = proj_direct[0] && proj_direct[1];
         for (int64_t y = 0; y < pt; ++y)
-            lists[is_left && !one_list ? kGaProjL : kGaProjR].push_back(make_int2(id, static_cast<int>(y)));
+            lists[d.gs ? kGxProjM : is_left && !one_list ? kGaProjL : kGaProjR].push_back(make_int2(id, static_cast<int>(y)));
         std::vector<int2>& L = lists[is_left ? kGaBackL : kGaBackR];
         if (back_mode[is_left] == kBackUr || back_mode[is_left] == kBackUrBf16) {
             // chunks of N outer, bands of U inner: consecutive items share N's rows
@@ -1968,10 +2054,15 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
     // back-projection -2.4%).
     xcd_deal(lists[kGaProjR]);
     xcd_deal(lists[kGaProjL]);
+    xcd_deal(lists[kGxProjM]);
     xcd_deal(lists[kGaBackR]);
     xcd_deal(lists[kGaBackL]);
     size_t offs[kGaListCount];
-    size_t total = (gd.size() * sizeof(GDesc) + 255) / 256 * 256;
+    std::vector<GDesc> plain(mx ? 0 : gd.size());
+    for (size_t i = 0; i < plain.size(); ++i) plain[i] = gd[i];
+    const void* gsrc = mx ? static_cast<const void*>(gd.data()) : plain.data();
+    const size_t gbytes = gd.size() * (mx ? sizeof(GxDesc) : sizeof(GDesc));
+    size_t total = (gbytes + 255) / 256 * 256;
     const size_t foff = total;
     total += (flat.size() * sizeof(TDesc) + 255) / 256 * 256;
     const size_t roffb = total;
@@ -1982,7 +2073,7 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
     }
     total = std::max<size_t>(total, 256);
     std::vector<uint8_t> host(total, 0);
-    if (!gd.empty()) std::memcpy(host.data(), gd.data(), gd.size() * sizeof(GDesc));
+    if (!gd.empty()) std::memcpy(host.data(), gsrc, gbytes);
     if (!flat.empty()) std::memcpy(host.data() + foff, flat.data(), flat.size() * sizeof(TDesc));
     if (!rd.empty()) std::memcpy(host.data() + roffb, rd.data(), rd.size() * sizeof(RDesc));
     for (int l = 0; l < kGaListCount; ++l)
@@ -2003,7 +2094,9 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
         return nullptr;
     }
     uint8_t* base = static_cast<uint8_t*>(p->mem);
-    p->gdesc = reinterpret_cast<const GDesc*>(base);
+    if (mx) p->gxdesc = reinterpret_cast<const GxDesc*>(base);
+    else p->gdesc = reinterpret_cast<const GDesc*>(base);
+    p->quant = std::move(quant);
     p->fdesc = reinterpret_cast<const TDesc*>(base + foff);
     p->rdesc = reinterpret_cast<const RDesc*>(base + roffb);
     for (int l = 0; l < kGaListCount; ++l) {
@@ -2020,50 +2113,17 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
     return p;
 }
 
-}  // namespace
-
-void meo_galore_defaults(meo_galore_hparams* hp) {
-    if (!hp) return;
-    std::memset(hp, 0, sizeof *hp);
-    hp->lr = 1e-3;
-    hp->beta1 = 0.9;
-    hp->beta2 = 0.999;
-    hp->eps = 1e-8;
-    hp->weight_decay = 0.0;
-    hp->rank = 256;
-    hp->update_proj_gap = 200;
-    hp->scale = 0.25;
-    hp->proj_type = MEO_GALORE_STD;
-}
-
-int32_t meo_galore_rank(const meo_galore_hparams* hp, const meo_tensor* t) {
-    if (!hp || !t || hp->rank < 1) return 0;
-    return ga_rank(hp, *t);
-}
-
-size_t meo_galore_workspace_size(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts) {
-    if (!hp || n <= 0 || !ts || hp->rank < 1) return 0;
-    return static_cast<size_t>(ga_layout(hp, n, ts, nullptr));
-}
-
-int meo_galore_validate(const meo_galore_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts,
-                        const meo_galore_state* st) {
-    g_err.clear();
-    const int rc = check_galore_hp(hp);
+// Recomputes the projectors (bf16 ones in place, MX4 ones from the bf16 result in the
+// workspace). Arguments are validated.
+int ga_refresh(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, const std::vector<GaState>& st, bool mx,
+               void* ws, size_t ws_bytes, hipStream_t s) {
+    int rc = check_galore_workspace(hp, n, ts, mx, ws, ws_bytes);
     if (rc) return rc;
-    return check_galore_tensors(hp, step, n, ts, st);
-}
-
-int meo_galore_refresh(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, const meo_galore_state* st,
-                       void* ws, size_t ws_bytes, void* stream) {
-    int rc = meo_galore_validate(hp, 1, n, ts, st);
-    if (rc) return rc;
-    if (n == 0) return MEO_OK;
-    rc = check_galore_workspace(hp, n, ts, ws, ws_bytes);
-    if (rc) return rc;
-    GaPlan* p = get_galore_plan(hp, n, ts, st, ws, &rc);
+    for (int32_t k = 0; k < n; ++k)
+        if (ga_projected(ts[k]) && ts[k].grad_dtype == MEO_MX4)
+            return fail(MEO_EDTYPE, "tensor " + std::to_string(k) + ": a projector refresh needs a bf16 gradient");
+    GaPlan* p = get_galore_plan(hp, n, ts, st.data(), mx, ws, &rc);
     if (!p) return rc;
-    const hipStream_t s = static_cast<hipStream_t>(stream);
     auto tab = [&](int l) { return RTable{p->rdesc, p->items[l]}; };
     auto cnt = [&](int l) { return p->count[l]; };
     if (cnt(kRfOne) == 0) return MEO_OK;
@@ -2086,6 +2146,23 @@ int meo_galore_refresh(const meo_galore_hparams* hp, int32_t n, const meo_tensor
         launch_rf_gemm(tab(kRfG0N), cnt(kRfG0N), 0, src, dst, false, s);
         launch_rf_gemm(tab(kRfG0T), cnt(kRfG0T), 0, src, dst, true, s);
     };
+    // MX4 projectors: the stored values into the workspace's bf16 transpose, from which the
+    // iteration starts, and the refreshed ones back.
+    auto mx_projectors = [&](bool quantize) {
+        for (size_t k = 0; k < p->quant.size(); k += kMxBatch) {
+            MxBatch b;
+            b.n = 0;
+            uint32_t grid = 0;
+            for (; b.n < kMxBatch && k + b.n < p->quant.size(); ++b.n) {
+                b.m[b.n] = p->quant[k + b.n];
+                b.m[b.n].first = grid;
+                grid += static_cast<uint32_t>(ceil_div(b.m[b.n].rows * b.m[b.n].nb, kMxRowBlocks));
+            }
+            if (quantize) launch_mx4_quantize(b, grid, false, s);
+            else launch_mx4_dequantize(b, grid, false, s);
+        }
+    };
+    mx_projectors(false);
     launch_rf_init(tab(kRfInit), cnt(kRfInit), kRbQa, s);
     cholqr2(kRbQa);
     for (int i = 0; i < kRfIters; ++i) {
@@ -2104,24 +2181,21 @@ int meo_galore_refresh(const meo_galore_hparams* hp, int32_t n, const meo_tensor
     launch_rf_jacobi(tab(kRfOne), cnt(kRfOne), s);
     launch_rf_basis(tab(kRfCols), cnt(kRfCols), kRbQa, s);
     launch_rf_store(tab(kRfStore), cnt(kRfStore), s);
+    mx_projectors(true);
     pt.mark(kPassGaRefresh);
     return launch_status("galore refresh launch");
 }
 
-int meo_galore_step(const meo_galore_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts,
-                    const meo_galore_state* st, void* ws, size_t ws_bytes, void* stream) {
-    int rc = meo_galore_validate(hp, step, n, ts, st);
-    if (rc) return rc;
-    if (n == 0) return MEO_OK;
-    rc = check_galore_workspace(hp, n, ts, ws, ws_bytes);
+int ga_step(const meo_galore_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts,
+            const std::vector<GaState>& st, bool mx, void* ws, size_t ws_bytes, hipStream_t s) {
+    int rc = check_galore_workspace(hp, n, ts, mx, ws, ws_bytes);
     if (rc) return rc;
     if ((step - 1) % hp->update_proj_gap == 0) {
-        rc = meo_galore_refresh(hp, n, ts, st, ws, ws_bytes, stream);
+        rc = ga_refresh(hp, n, ts, st, mx, ws, ws_bytes, s);
         if (rc) return rc;
     }
-    GaPlan* p = get_galore_plan(hp, n, ts, st, ws, &rc);
+    GaPlan* p = get_galore_plan(hp, n, ts, st.data(), mx, ws, &rc);
     if (!p) return rc;
-    const hipStream_t s = static_cast<hipStream_t>(stream);
     const double tt = static_cast<double>(step);
     const double bc1 = 1.0 - std::pow(hp->beta1, tt), bc2 = 1.0 - std::pow(hp->beta2, tt);
     GaArgs a{static_cast<float>(hp->beta1), static_cast<float>(hp->beta2), static_cast<float>(1.0 - hp->beta1),
@@ -2129,20 +2203,296 @@ int meo_galore_step(const meo_galore_hparams* hp, int64_t step, int32_t n, const
              static_cast<float>(hp->eps), static_cast<float>(1.0 - hp->lr * hp->weight_decay),
              static_cast<float>(hp->lr * hp->scale)};
     PassTimer pt(s);
-    if (p->proj_direct[0] && p->proj_direct[1]) {
+    if (mx) {
+        launch_gx_project(GxTable{p->gxdesc, p->items[kGaProjR]}, p->count[kGaProjR], a, false, s);
+        launch_gx_project(GxTable{p->gxdesc, p->items[kGaProjL]}, p->count[kGaProjL], a, true, s);
+        launch_gx_project_mx4(GxTable{p->gxdesc, p->items[kGxProjM]}, p->count[kGxProjM], a, s);
+    } else if (p->proj_direct[0] && p->proj_direct[1]) {
         launch_galore_project_mixed(GTable{p->gdesc, p->items[kGaProjR]}, p->count[kGaProjR], p->nright, a, s);
     } else {
         launch_galore_project(GTable{p->gdesc, p->items[kGaProjR]}, p->count[kGaProjR], a, false, p->proj_direct[0], s);
         launch_galore_project(GTable{p->gdesc, p->items[kGaProjL]}, p->count[kGaProjL], a, true, p->proj_direct[1], s);
     }
     pt.mark(kPassGaProject);
-    launch_galore_back(GTable{p->gdesc, p->items[kGaBackR]}, p->count[kGaBackR], a, false, p->back_mode[0], s);
-    launch_galore_back(GTable{p->gdesc, p->items[kGaBackL]}, p->count[kGaBackL], a, true, p->back_mode[1], s);
+    if (mx) {
+        launch_gx_back(GxTable{p->gxdesc, p->items[kGaBackR]}, p->count[kGaBackR], a, false, p->back_mode[0], s);
+        launch_gx_back(GxTable{p->gxdesc, p->items[kGaBackL]}, p->count[kGaBackL], a, true, p->back_mode[1], s);
+    } else {
+        launch_galore_back(GTable{p->gdesc, p->items[kGaBackR]}, p->count[kGaBackR], a, false, p->back_mode[0], s);
+        launch_galore_back(GTable{p->gdesc, p->items[kGaBackL]}, p->count[kGaBackL], a, true, p->back_mode[1], s);
+    }
     pt.mark(kPassGaBack);
     a.coef = static_cast<float>(hp->lr);
     launch_galore_adamw(Table{p->fdesc, p->items[kGaFlat], nullptr}, p->count[kGaFlat], a, s);
     pt.mark(kPassGaAdamw);
     return launch_status("galore step launch");
+}
+
+// ----------------------------------------------------------------------------- MX4
+
+int current_device(int* dev) {
+    if (hipGetDevice(dev) != hipSuccess) {
+        (void)hipGetLastError();
+        return fail(MEO_EHIP, "hipGetDevice failed");
+    }
+    return MEO_OK;
+}
+
+// Bytes of a [rows][ld] array of elements of `size`, rows of `cols`.
+size_t strided_bytes(int64_t rows, int64_t ld, int64_t cols, size_t size) {
+    return (static_cast<size_t>(rows - 1) * static_cast<size_t>(ld) + static_cast<size_t>(cols)) * size;
+}
+
+int check_mx4_values(const std::string& who, const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype,
+                     const char* name) {
+    if (dtype != MEO_F32 && dtype != MEO_BF16) return fail(MEO_EDTYPE, who + "dtype must be MEO_F32 or MEO_BF16");
+    if (ld < cols) return fail(MEO_ESHAPE, who + "leading dimension below the row length");
+    if (ld > kMaxDim) return fail(MEO_ESHAPE, who + "leading dimension exceeds 2^31 - 1");
+    if (rows == 0 || cols == 0) return MEO_OK;
+    if (!p) return fail(MEO_ENULL, who + name + " is NULL");
+    if (reinterpret_cast<uintptr_t>(p) % elem_bytes(dtype)) return fail(MEO_EALIGN, who + name + " misaligned for its dtype");
+    return MEO_OK;
+}
+
+int check_mx4_codes(const std::string& who, const void* codes, const void* scales, const char* name) {
+    if (!codes || !scales) return fail(MEO_ENULL, who + name + "codes or scales is NULL");
+    if (reinterpret_cast<uintptr_t>(codes) % 16) return fail(MEO_EALIGN, who + name + "codes not 16-byte aligned");
+    return MEO_OK;
+}
+
+int check_mx4_ranges(const std::string& who, const void* codes, const void* scales, int64_t rows, int64_t cols, int dev,
+                     const char* name) {
+    const size_t blocks = static_cast<size_t>(rows) * static_cast<size_t>(ceil_div(cols, kMxBlock));
+    int rc = check_device_range(codes, blocks * 16, dev, who + name + "codes", MEO_EMEMORY);
+    if (rc) return rc;
+    return check_device_range(scales, blocks, dev, who + name + "scales", MEO_EMEMORY);
+}
+
+int mx4_convert(int32_t n, const meo_mx4_matrix* ms, bool transposed, bool quantize, hipStream_t s) {
+    g_err.clear();
+    if (n < 0) return fail(MEO_EINVAL, "negative matrix count");
+    if (n == 0) return MEO_OK;
+    if (!ms) return fail(MEO_ENULL, "matrices is NULL");
+    auto grid_of = [&](const meo_mx4_matrix& m) {
+        const int64_t nb = ceil_div(m.cols, kMxBlock);
+        return transposed ? ceil_div(m.rows, kMxColRows) * ceil_div(nb, kMxColBlocks) : ceil_div(m.rows * nb, kMxRowBlocks);
+    };
+    for (int32_t k = 0; k < n; ++k) {
+        const meo_mx4_matrix& m = ms[k];
+        const std::string who = "matrix " + std::to_string(k) + ": ";
+        if (m.rows < 0 || m.cols < 0) return fail(MEO_ESHAPE, who + "negative rows or cols");
+        if (m.rows > kMaxDim || m.cols > kMaxDim) return fail(MEO_ESHAPE, who + "rows or cols exceed 2^31 - 1");
+        int rc = transposed ? check_mx4_values(who, m.data, m.cols, m.rows, m.ld, m.dtype, "data")
+                            : check_mx4_values(who, m.data, m.rows, m.cols, m.ld, m.dtype, "data");
+        if (rc) return rc;
+        if (m.rows == 0 || m.cols == 0) continue;
+        rc = check_mx4_codes(who, m.codes, m.scales, "");
+        if (rc) return rc;
+        if (grid_of(m) > kMaxDim) return fail(MEO_ESHAPE, who + "too many blocks");
+    }
+    int dev = 0;
+    int rc = current_device(&dev);
+    if (rc) return rc;
+    for (int32_t k = 0; k < n; ++k) {
+        const meo_mx4_matrix& m = ms[k];
+        if (m.rows == 0 || m.cols == 0) continue;
+        const std::string who = "matrix " + std::to_string(k) + ": ";
+        const size_t bytes = transposed ? strided_bytes(m.cols, m.ld, m.rows, elem_bytes(m.dtype))
+                                        : strided_bytes(m.rows, m.ld, m.cols, elem_bytes(m.dtype));
+        rc = check_device_range(m.data, bytes, dev, who + "data", MEO_EMEMORY);
+        if (!rc) rc = check_mx4_ranges(who, m.codes, m.scales, m.rows, m.cols, dev, "");
+        if (rc) return rc;
+    }
+    MxBatch b;
+    b.n = 0;
+    int64_t grid = 0;
+    auto flush = [&]() {
+        if (quantize) launch_mx4_quantize(b, static_cast<uint32_t>(grid), transposed, s);
+        else launch_mx4_dequantize(b, static_cast<uint32_t>(grid), transposed, s);
+        b.n = 0;
+        grid = 0;
+    };
+    for (int32_t k = 0; k < n; ++k) {
+        const meo_mx4_matrix& m = ms[k];
+        if (m.rows == 0 || m.cols == 0) continue;
+        const int64_t blocks = grid_of(m);
+        if (b.n == kMxBatch || grid + blocks > kMaxDim) flush();
+        MxMat& w = b.m[b.n++];
+        w.data = m.data;
+        w.codes = static_cast<uint8_t*>(m.codes);
+        w.scales = static_cast<uint8_t*>(m.scales);
+        w.ld = m.ld;
+        w.rows = m.rows;
+        w.cols = m.cols;
+        w.nb = ceil_div(m.cols, kMxBlock);
+        w.first = static_cast<uint32_t>(grid);
+        w.tiles_y = static_cast<uint32_t>(ceil_div(m.rows, kMxColRows));
+        w.bf16 = m.dtype == MEO_BF16;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(m.data);
+        w.vec = transposed ? m.ld % 2 == 0 && a % (2 * elem_bytes(m.dtype)) == 0
+                           : aligned16(m.data) && m.ld % (w.bf16 ? 8 : 4) == 0;
+        grid += blocks;
+    }
+    flush();
+    return launch_status(quantize ? "mx4 quantize launch" : "mx4 dequantize launch");
+}
+
+int check_mx4_products(int32_t n, const meo_mx4_product* ps) {
+    g_err.clear();
+    if (n < 0) return fail(MEO_EINVAL, "negative product count");
+    if (n == 0) return MEO_OK;
+    if (!ps) return fail(MEO_ENULL, "products is NULL");
+    for (int32_t k = 0; k < n; ++k) {
+        const meo_mx4_product& q = ps[k];
+        const std::string who = "product " + std::to_string(k) + ": ";
+        if (q.m < 0 || q.n < 0 || q.k < 0) return fail(MEO_ESHAPE, who + "negative m, n or k");
+        if (q.m > kMaxDim || q.n > kMaxDim || q.k > kMaxDim) return fail(MEO_ESHAPE, who + "m, n or k exceeds 2^31 - 1");
+        int rc = check_mx4_values(who, q.c, q.m, q.n, q.ldc, q.dtype, "c");
+        if (rc) return rc;
+        if (q.m == 0 || q.n == 0) continue;
+        if (ceil_div(q.m, kMxTile) * ceil_div(q.n, kMxTile) > kMaxDim) return fail(MEO_ESHAPE, who + "too many tiles");
+        if (q.k == 0) continue;
+        rc = check_mx4_codes(who, q.a_codes, q.a_scales, "a_");
+        if (!rc) rc = check_mx4_codes(who, q.b_codes, q.b_scales, "b_");
+        if (rc) return rc;
+    }
+    int dev = 0;
+    int rc = current_device(&dev);
+    if (rc) return rc;
+    for (int32_t k = 0; k < n; ++k) {
+        const meo_mx4_product& q = ps[k];
+        if (q.m == 0 || q.n == 0) continue;
+        const std::string who = "product " + std::to_string(k) + ": ";
+        rc = check_device_range(q.c, strided_bytes(q.m, q.ldc, q.n, elem_bytes(q.dtype)), dev, who + "c", MEO_EMEMORY);
+        if (!rc && q.k > 0) rc = check_mx4_ranges(who, q.a_codes, q.a_scales, q.m, q.k, dev, "a_");
+        if (!rc && q.k > 0) rc = check_mx4_ranges(who, q.b_codes, q.b_scales, q.n, q.k, dev, "b_");
+        if (rc) return rc;
+    }
+    return MEO_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+void meo_galore_defaults(meo_galore_hparams* hp) {
+    if (!hp) return;
+    std::memset(hp, 0, sizeof *hp);
+    hp->lr = 1e-3;
+    hp->beta1 = 0.9;
+    hp->beta2 = 0.999;
+    hp->eps = 1e-8;
+    hp->weight_decay = 0.0;
+    hp->rank = 256;
+    hp->update_proj_gap = 200;
+    hp->scale = 0.25;
+    hp->proj_type = MEO_GALORE_STD;
+}
+
+int32_t meo_galore_rank(const meo_galore_hparams* hp, const meo_tensor* t) {
+    if (!hp || !t || hp->rank < 1) return 0;
+    return ga_rank(hp, *t);
+}
+
+size_t meo_galore_workspace_size(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts) {
+    if (!hp || n <= 0 || !ts || hp->rank < 1) return 0;
+    return static_cast<size_t>(ga_layout(hp, n, ts, false, nullptr));
+}
+
+size_t meo_galore_mx4_workspace_size(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts) {
+    if (!hp || n <= 0 || !ts || hp->rank < 1) return 0;
+    return static_cast<size_t>(ga_layout(hp, n, ts, true, nullptr));
+}
+
+int meo_galore_validate(const meo_galore_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts,
+                        const meo_galore_state* st) {
+    g_err.clear();
+    const int rc = check_galore_hp(hp);
+    if (rc) return rc;
+    return check_galore_tensors(hp, step, n, ts, st ? ga_states(n, st).data() : nullptr, false);
+}
+
+int meo_galore_mx4_validate(const meo_galore_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts,
+                            const meo_galore_mx4_state* st) {
+    g_err.clear();
+    const int rc = check_galore_hp(hp);
+    if (rc) return rc;
+    return check_galore_tensors(hp, step, n, ts, st ? ga_states(n, st).data() : nullptr, true);
+}
+
+int meo_galore_refresh(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, const meo_galore_state* st,
+                       void* ws, size_t ws_bytes, void* stream) {
+    const int rc = meo_galore_validate(hp, 1, n, ts, st);
+    if (rc || n == 0) return rc;
+    return ga_refresh(hp, n, ts, ga_states(n, st), false, ws, ws_bytes, static_cast<hipStream_t>(stream));
+}
+
+int meo_galore_mx4_refresh(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts,
+                           const meo_galore_mx4_state* st, void* ws, size_t ws_bytes, void* stream) {
+    const int rc = meo_galore_mx4_validate(hp, 1, n, ts, st);
+    if (rc || n == 0) return rc;
+    return ga_refresh(hp, n, ts, ga_states(n, st), true, ws, ws_bytes, static_cast<hipStream_t>(stream));
+}
+
+int meo_galore_step(const meo_galore_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts,
+                    const meo_galore_state* st, void* ws, size_t ws_bytes, void* stream) {
+    const int rc = meo_galore_validate(hp, step, n, ts, st);
+    if (rc || n == 0) return rc;
+    return ga_step(hp, step, n, ts, ga_states(n, st), false, ws, ws_bytes, static_cast<hipStream_t>(stream));
+}
+
+int meo_galore_mx4_step(const meo_galore_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts,
+                        const meo_galore_mx4_state* st, void* ws, size_t ws_bytes, void* stream) {
+    const int rc = meo_galore_mx4_validate(hp, step, n, ts, st);
+    if (rc || n == 0) return rc;
+    return ga_step(hp, step, n, ts, ga_states(n, st), true, ws, ws_bytes, static_cast<hipStream_t>(stream));
+}
+
+// ----------------------------------------------------------------------------- MX4
+
+int meo_mx4_quantize(int32_t n, const meo_mx4_matrix* ms, int32_t transposed, void* stream) {
+    return mx4_convert(n, ms, transposed != 0, true, static_cast<hipStream_t>(stream));
+}
+
+int meo_mx4_dequantize(int32_t n, const meo_mx4_matrix* ms, int32_t transposed, void* stream) {
+    return mx4_convert(n, ms, transposed != 0, false, static_cast<hipStream_t>(stream));
+}
+
+int meo_mx4_matmul(int32_t n, const meo_mx4_product* ps, void* stream) {
+    int rc = check_mx4_products(n, ps);
+    if (rc || n == 0) return rc;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    MxProdBatch b;
+    b.n = 0;
+    int64_t grid = 0;
+    auto flush = [&]() {
+        launch_mx4_matmul(b, static_cast<uint32_t>(grid), s);
+        b.n = 0;
+        grid = 0;
+    };
+    for (int32_t k = 0; k < n; ++k) {
+        const meo_mx4_product& q = ps[k];
+        if (q.m == 0 || q.n == 0) continue;
+        const int64_t tiles = ceil_div(q.m, kMxTile) * ceil_div(q.n, kMxTile);
+        if (b.n == kMxBatch || grid + tiles > kMaxDim) flush();
+        MxProd& p = b.p[b.n++];
+        p.ac = static_cast<const uint8_t*>(q.a_codes);
+        p.as = static_cast<const uint8_t*>(q.a_scales);
+        p.bc = static_cast<const uint8_t*>(q.b_codes);
+        p.bs = static_cast<const uint8_t*>(q.b_scales);
+        p.c = q.c;
+        p.ldc = q.ldc;
+        p.m = q.m;
+        p.n = q.n;
+        p.nb = ceil_div(q.k, kMxBlock);
+        p.first = static_cast<uint32_t>(grid);
+        p.tn = static_cast<uint32_t>(ceil_div(q.n, kMxTile));
+        p.cbf16 = q.dtype == MEO_BF16;
+        p.vec = aligned16(q.c) && q.ldc % (p.cbf16 ? 8 : 4) == 0;
+        grid += tiles;
+    }
+    flush();
+    return launch_status("mx4 matmul launch");
 }
 
 }  // extern "C"

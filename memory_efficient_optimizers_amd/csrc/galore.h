@@ -40,6 +40,22 @@ struct GTable {
                         // item (padding of the XCD-aligned back-projection list)
 };
 
+// A projected tensor whose projector is held in MX4 (one copy, [r][d], blocks along d);
+// u and ut are unused by its step. The gradient is bf16 (g, gs NULL) or MX4 [D][d] with
+// blocks along d (g: its codes, gs: its scales).
+struct GxDesc : GDesc {
+    const uint8_t* uc;  // projector codes [r][16 nb]
+    const uint8_t* us;  // projector scales [r][nb]
+    const uint8_t* gs;
+    int32_t nb;         // blocks along d
+    int32_t tpi;        // U-register back-projection: 64-row tiles of N per item
+};
+
+struct GxTable {
+    const GxDesc* desc;
+    const int2* items;
+};
+
 struct GaArgs {
     float beta1, beta2, omb1, omb2;  // betas and 1 - betas
     float inv_bc1, inv_bc2;          // 1 / (1 - beta^t)
@@ -65,6 +81,13 @@ enum BackMode { kBackReg = 0, kBackDirect = 1, kBackUr = 2, kBackUrBf16 = 3 };
 constexpr int kUrTiles = 64;  // 64-row tiles of N per item of the U-register back-projection
 void launch_galore_back(const GTable& t, int64_t n, const GaArgs& a, bool left, int mode, hipStream_t s);
 void launch_galore_adamw(const Table& t, int64_t n, const GaArgs& a, hipStream_t s);
+
+// The step's products with an MX4 projector. Projection of a bf16 gradient (`left`) or of
+// an MX4 one (its rows are rows of R on either side); items are tiles of kGxRows rows of R.
+constexpr int kGxRows = 64;
+void launch_gx_project(const GxTable& t, int64_t n, const GaArgs& a, bool left, hipStream_t s);
+void launch_gx_project_mx4(const GxTable& t, int64_t n, const GaArgs& a, hipStream_t s);
+void launch_gx_back(const GxTable& t, int64_t n, const GaArgs& a, bool left, int mode, hipStream_t s);
 
 // ------------------------------------------------------------------ projector refresh
 

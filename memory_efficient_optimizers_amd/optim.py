@@ -33,6 +33,7 @@ from typing import Dict, List, Optional, Tuple
 import torch
 
 from . import _lib
+from .mx4 import MX4Tensor, mx4_dequantize, mx4_quantize
 
 
 def moment_dtype(optimizer: str, shape, requested: Optional[torch.dtype], param_dtype: torch.dtype,
@@ -105,6 +106,10 @@ class _MeoOptimizer(torch.optim.Optimizer):
                 if torch.is_tensor(v) and key != "step":
                     self.state[p][key] = v.to(device=p.device, copy=True).contiguous()
 
+    def _grad(self, p: torch.Tensor):
+        """The gradient the step takes for ``p`` (None: the parameter is skipped)."""
+        return p.grad
+
     def _state_for(self, p: torch.Tensor, group) -> Dict[str, torch.Tensor]:
         raise NotImplementedError
 
@@ -123,9 +128,10 @@ class _MeoOptimizer(torch.optim.Optimizer):
         for group in self.param_groups:
             buckets: Dict[Tuple[torch.device, int], List[torch.Tensor]] = defaultdict(list)
             for p in group["params"]:
-                if p.grad is None:
+                g = self._grad(p)
+                if g is None:
                     continue
-                if p.grad.is_sparse:
+                if isinstance(g, torch.Tensor) and g.is_sparse:
                     raise RuntimeError(f"{type(self).__name__} does not support sparse gradients")
                 st = self.state[p]
                 if len(st) == 0:
@@ -134,7 +140,8 @@ class _MeoOptimizer(torch.optim.Optimizer):
                 st["step"] += 1
                 buckets[(p.device, st["step"])].append(p)
             for (device, step), ps in buckets.items():
-                grads = [p.grad if p.grad.is_contiguous() else p.grad.contiguous() for p in ps]
+                grads = [self._grad(p) for p in ps]
+                grads = [g.contiguous() if isinstance(g, torch.Tensor) else g for g in grads]
                 states = [self.state[p] for p in ps]
                 ws = self._ws(self._wsize(ps, grads), device)
                 with torch.cuda.device(device):
@@ -330,11 +337,20 @@ class GaLoreAdamW(_MeoOptimizer):
     The projection runs on bf16 matrix cores: a projected parameter's gradient is
     read in bfloat16 (converted if it is float32), and its projector is kept in
     bfloat16. States: ``exp_avg`` and ``exp_avg_sq`` float32 ([max(m, n)][r] when
-    projected), ``projector`` [min(m, n)][r] and ``projector_t`` [r][min(m, n)]."""
+    projected), ``projector`` [min(m, n)][r] and ``projector_t`` [r][min(m, n)].
+
+    ``projector_dtype=torch.float4_e2m1fn_x2`` keeps the projector in MX4 instead
+    (``mx4.py``: 4-bit codes, one scale per 32 values), once, as its transpose:
+    ``projector`` (codes) and ``projector_scale``, about an eighth of the two bfloat16
+    copies. ``compress_grad`` then also lets a projected gradient wait for the step in
+    MX4. ``load_state_dict`` converts a projector saved in the other form."""
 
     _kind = "galore"
 
-    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0):
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0,
+                 projector_dtype=torch.bfloat16):
+        if projector_dtype not in (torch.bfloat16, torch.float4_e2m1fn_x2):
+            raise TypeError("projector_dtype must be torch.bfloat16 or torch.float4_e2m1fn_x2")
         if not lr >= 0.0:
             raise ValueError(f"Invalid learning rate: {lr}")
         if not eps >= 0.0:
@@ -344,6 +360,8 @@ class GaLoreAdamW(_MeoOptimizer):
                 raise ValueError(f"Invalid beta parameter at index {i}: {b}")
         defaults = dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay)
         super().__init__(params, defaults, None)
+        self._mx4 = projector_dtype == torch.float4_e2m1fn_x2
+        self._compressed: Dict[torch.Tensor, MX4Tensor] = {}
         for g in self.param_groups:
             if "rank" in g:
                 g.setdefault("update_proj_gap", 200)
@@ -356,8 +374,75 @@ class GaLoreAdamW(_MeoOptimizer):
     def _projected(p: torch.Tensor, group) -> bool:
         return "rank" in group and p.dim() == 2 and p.numel() > 0
 
+    @staticmethod
+    def _right(p: torch.Tensor, group) -> bool:
+        """Whether the projector spans the columns' space (R = G U)."""
+        return (p.shape[0] >= p.shape[1]) == (group["proj_type"] == "std")
+
+    def _grad(self, p):
+        q = self._compressed.get(p)
+        if q is not None and p.grad is not None:
+            raise RuntimeError("a parameter has both a compressed gradient and a new .grad: take the step (or "
+                               "zero_grad) before the next backward pass, or compress only the last one")
+        return p.grad if q is None else q
+
+    def compress_grad(self, p: torch.Tensor) -> None:
+        """Turns ``p.grad`` into MX4 (17/32 byte per value) until the next ``step()``, which
+        projects it from there, and sets ``p.grad`` to None. Made for
+        ``p.register_post_accumulate_grad_hook(opt.compress_grad)``: full gradients of the
+        projected parameters then never exist together. A gradient that the next step
+        needs whole (not projected, or the step refreshes the projector) is left as it
+        is. Each parameter's gradient can be compressed once per step, so gradients that
+        accumulate over several backward passes are compressed after the last."""
+        if not self._mx4:
+            raise RuntimeError("compress_grad needs projector_dtype=torch.float4_e2m1fn_x2")
+        group = next((g for g in self.param_groups if any(p is q for q in g["params"])), None)
+        if group is None:
+            raise ValueError("compress_grad takes one of the optimizer's parameters")
+        if p.grad is None or not self._projected(p, group):
+            return
+        if p in self._compressed:
+            raise RuntimeError("the parameter's gradient is already compressed: gradients that accumulate over "
+                               "several backward passes are compressed after the last one")
+        if p.grad.is_sparse:
+            raise RuntimeError("GaLoreAdamW does not support sparse gradients")
+        step = (self.state[p]["step"] if len(self.state[p]) else 0) + 1
+        if (step - 1) % group["update_proj_gap"] == 0:
+            return
+        self._compressed[p] = mx4_quantize(p.grad, transposed=not self._right(p, group))
+        p.grad = None
+
+    def zero_grad(self, set_to_none: bool = True) -> None:
+        super().zero_grad(set_to_none)
+        self._compressed.clear()
+
+    def step(self, closure=None):
+        """As torch's; gradients that ``compress_grad`` took are used once."""
+        loss = super().step(closure)
+        self._compressed.clear()
+        return loss
+
+    def load_state_dict(self, state_dict) -> None:
+        super().load_state_dict(state_dict)
+        self._compressed.clear()
+        for group in self.param_groups:
+            for p in group["params"]:
+                st = self.state.get(p)
+                if not st or "projector" not in st or self._mx4 == ("projector_scale" in st):
+                    continue
+                if self._mx4:
+                    q = mx4_quantize(st.pop("projector_t"))
+                    st["projector"], st["projector_scale"] = q.codes, q.scales
+                else:
+                    d = p.shape[1] if self._right(p, group) else p.shape[0]
+                    q = MX4Tensor(st["projector"], st.pop("projector_scale"), d)
+                    st["projector_t"] = mx4_dequantize(q, torch.bfloat16)
+                    st["projector"] = mx4_dequantize(q, torch.bfloat16, transposed=True)
+
     def _state_for(self, p, group):
         if self._projected(p, group):
+            if self._mx4:
+                return _lib.galore_mx4_init_state(p, group["rank"], group["proj_type"])
             return _lib.galore_init_state(p, group["rank"], group["proj_type"])
         return {k: torch.zeros(p.shape, dtype=torch.float32, device=p.device) for k in ("exp_avg", "exp_avg_sq")}
 
@@ -368,7 +453,7 @@ class GaLoreAdamW(_MeoOptimizer):
         for p, g, st in zip(params, grads, states):
             if self._projected(p, group):
                 ps.append(p)
-                gs.append(g if g.dtype == torch.bfloat16 else g.to(torch.bfloat16))
+                gs.append(g if isinstance(g, MX4Tensor) or g.dtype == torch.bfloat16 else g.to(torch.bfloat16))
                 ss.append(st)
             else:
                 ps.append(p.view(-1))
@@ -388,5 +473,13 @@ class GaLoreAdamW(_MeoOptimizer):
     def _call(self, group, step, params, grads, states, ws):
         ps, gs, ss = self._lists(group, params, grads, states)
         hp = self._hp(group)
+        if self._mx4:
+            ws = self._ws(_lib.meo_galore_mx4_workspace_size(hp, ps, gs), ps[0].device)
+            _lib.meo_galore_mx4_step(hp, step, ps, gs, ss, ws)
+            for g in gs:  # dropped after the step; made on the backward pass's stream
+                if isinstance(g, MX4Tensor):
+                    g.codes.record_stream(torch.cuda.current_stream())
+                    g.scales.record_stream(torch.cuda.current_stream())
+            return
         ws = self._ws(_lib.meo_galore_workspace_size(hp, ps, gs), ps[0].device)
         _lib.meo_galore_step(hp, step, ps, gs, ss, ws)
