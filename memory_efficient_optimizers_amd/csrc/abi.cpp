@@ -1611,9 +1611,12 @@ int meo_came_shard_apply(const meo_came_hparams* hp, int64_t step, int32_t n, co
 
 namespace {
 
-enum GaList { kGaProjR = 0, kGaProjL, kGaBackR, kGaBackL, kGaFlat, kGxProjM /* MX4 gradients */,
+enum GaList { kGaProjR = 0, kGaProjL, kGaBackR, kGaBackL, kGaFlat,
+              // MX4 projectors: projection by form (GxForm, right then left; MxForm for MX4
+              // gradients), back-projection by parameter dtype (float32 right, left, bf16 ...)
+              kGxProj, kGxProjM = kGxProj + 2 * kGxForms, kGxBack = kGxProjM + kMxForms, kGxEnd = kGxBack + 4,
               // projector refresh
-              kRfInit, kRfG0N, kRfG0T, kRfG1N, kRfG1T, kRfGram, kRfOne, kRfCols, kRfStore, kGaListCount };
+              kRfInit = kGxEnd, kRfG0N, kRfG0T, kRfG1N, kRfG1T, kRfGram, kRfOne, kRfCols, kRfStore, kGaListCount };
 
 struct GaPlan {
     std::vector<uint8_t> key;
@@ -1694,6 +1697,8 @@ bool ga_left(const meo_galore_hparams* hp, const meo_tensor& t) {
 int64_t ga_rows(const meo_galore_hparams* hp, const meo_tensor& t) { return ga_left(hp, t) ? t.cols : t.rows; }   // D
 int64_t ga_basis(const meo_galore_hparams* hp, const meo_tensor& t) { return ga_left(hp, t) ? t.rows : t.cols; }  // d
 
+int32_t gx_pitch(int32_t r) { return (r + 15) / 16 * 16; }  // MX4 projectors: values per row of N's planes
+
 int64_t align256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
 // Workspace, per projected tensor, every array at a 256-byte boundary (offsets in
@@ -1709,7 +1714,7 @@ int64_t ga_layout(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts,
         const int32_t r = ga_rank(hp, ts[k]);
         if (!r) continue;
         if (offs) (*offs)[k] = off;
-        off += 2 * align256(ga_rows(hp, ts[k]) * r * 2);
+        off += 2 * align256(ga_rows(hp, ts[k]) * (mx ? gx_pitch(r) : r) * 2);
     }
     for (int32_t k = 0; k < n; ++k) {
         const int32_t r = ga_rank(hp, ts[k]);
@@ -1785,6 +1790,7 @@ int check_galore_tensors(const meo_galore_hparams* hp, int64_t step, int32_t n, 
             const int32_t r = ga_rank(hp, t);
             if (r > kGaWide) return fail(MEO_EINVAL, who + "effective rank " + std::to_string(r) + " exceeds 256");
             if (mx) {
+                if (ga_basis(hp, t) > kMxMaxK) return fail(MEO_ESHAPE, who + "the projected side exceeds 2^23");
                 if (!s.uc || !s.us) return fail(MEO_ENULL, who + "projector or projector_scale is NULL");
                 if (reinterpret_cast<uintptr_t>(s.uc) % 16)
                     return fail(MEO_EALIGN, who + "MX4 projector codes not 16-byte aligned");
@@ -1857,6 +1863,66 @@ int check_galore_workspace(const meo_galore_hparams* hp, int32_t n, const meo_te
     return check_device_range(ws, bytes, dev, "workspace", MEO_EWORKSPACE);
 }
 
+// Items of a step with MX4 projectors. gd: the descriptors, right-side ones first; sets btj and
+// tpi. Projection forms and the tiles per back-projection item follow the call's total
+// work: the larger tiles share each part of U among more rows but need as many of
+// them as there are CUs.
+constexpr int64_t kCus = 256;
+constexpr int64_t kMxTallTiles = 200;  // 128-row tiles of a call from which its products take them
+constexpr int64_t kGxTallTiles = 512;
+void gx_lists(std::vector<GxDesc>& gd, size_t nright, std::vector<int2>* lists) {
+    auto words = [](const void* p, int32_t nb) { return nb % 4 == 0 && reinterpret_cast<uintptr_t>(p) % 4 == 0; };
+    auto direct = [&](const GxDesc& d) { return d.vec && d.d % 128 == 0 && words(d.us, d.nb); };
+    int64_t tall = 0, tall4 = 0;  // 128-row tiles of the call
+    for (const GxDesc& d : gd) (d.gs ? tall4 : tall) += ceil_div(d.D, 128);
+    for (size_t i = 0; i < gd.size(); ++i) {
+        const GxDesc& d = gd[i];
+        const bool left = i >= nright;
+        int list, rows;
+        if (d.gs) {
+            const int form = !words(d.us, d.nb) || !words(d.gs, d.nb) ? kMxAny
+                             : d.r <= kMxFormCols[kMxNarrow]          ? kMxNarrow
+                             : tall4 >= kMxTallTiles                  ? kMxTall
+                                                                      : kMxWide;
+            list = kGxProjM + form;
+            rows = kMxFormRows[form];
+        } else {
+            const int form = !direct(d) ? kGxAny : tall >= kGxTallTiles ? kGxDirectTall : kGxDirect;
+            list = kGxProj + 2 * form + left;
+            rows = kGxFormRows[form];
+        }
+        for (int64_t y = 0; y < ceil_div(d.D, rows); ++y) lists[list].push_back(make_int2(static_cast<int>(i), static_cast<int>(y)));
+    }
+    for (int side = 0; side < 2; ++side)
+        for (int xb = 0; xb < 2; ++xb) {
+            std::vector<size_t> ids;
+            for (size_t i = 0; i < gd.size(); ++i)
+                if ((i >= nright) == (side == 1) && (gd[i].xbf16 != 0) == (xb == 1)) ids.push_back(i);
+            // Tiles per item: the count with the least time, in tiles, of the rounds that
+            // the items take on the CUs (an item's start, its part of U, is about a tile).
+            int best = 1;
+            int64_t least = INT64_MAX;
+            for (int tpi = 1; tpi <= kUrTiles; ++tpi) {
+                int64_t items = 0;
+                for (size_t i : ids) items += ceil_div(gd[i].d, kGaWide) * ceil_div(ceil_div(gd[i].D, kGaTile), tpi);
+                const int64_t time = ceil_div(items, kCus) * (tpi + 1);
+                if (time < least) {
+                    least = time;
+                    best = tpi;
+                }
+            }
+            for (size_t i : ids) {
+                GxDesc& d = gd[i];
+                d.tpi = best;
+                d.btj = static_cast<int32_t>(ceil_div(ceil_div(d.D, kGaTile), best));
+                // chunks of N outer, bands of U inner: consecutive items share N's rows
+                for (int64_t c = 0; c < d.btj; ++c)
+                    for (int64_t k = 0; k < ceil_div(d.d, kGaWide); ++k)
+                        lists[kGxBack + 2 * xb + side].push_back(make_int2(static_cast<int>(i), static_cast<int>(k * d.btj + c)));
+            }
+        }
+}
+
 GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, const GaState* st, bool mx,
                         void* ws, int* rc) {
     int dev = 0;
@@ -1918,7 +1984,8 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
             const bool g4 = t.grad_dtype == MEO_MX4;
             uint8_t* wb = static_cast<uint8_t*>(ws) + woff[k];
             d.nh = reinterpret_cast<uint16_t*>(wb);
-            d.nl = reinterpret_cast<uint16_t*>(wb + (static_cast<int64_t>(d.D) * d.r * 2 + 255) / 256 * 256);
+            d.rp = gx_pitch(d.r);
+            d.nl = reinterpret_cast<uint16_t*>(wb + align256(static_cast<int64_t>(d.D) * (mx ? d.rp : d.r) * 2));
             d.vec = aligned16(d.g) && aligned16(d.u) && aligned16(d.ut) && d.n % 8 == 0 && d.d % 8 == 0 &&
                     d.r % 8 == 0;
             if (mx) {
@@ -1926,8 +1993,7 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
                 d.us = static_cast<const uint8_t*>(s.us);
                 d.gs = static_cast<const uint8_t*>(s.gs);
                 d.nb = static_cast<int32_t>(ceil_div(d.d, kMxBlock));
-                // the gradient's rows (bf16) and the planes of N
-                d.vec = (g4 || (aligned16(d.g) && d.n % 8 == 0)) && d.r % 8 == 0;
+                d.vec = aligned16(d.g) && d.n % 8 == 0;  // 16-byte rows of a bf16 gradient
             }
             d.rvec = aligned16(d.em) && aligned16(d.ev) && d.r % 8 == 0;
             d.wvec = aligned16(d.x) && d.n % 8 == 0;
@@ -2003,7 +2069,7 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
     int back_mode[2] = {kBackReg, kBackReg};
     for (int side = 0; side < 2; ++side) {
         const std::vector<GxDesc>& v = side ? left : right;
-        bool direct = !mx, all_f32 = true, all_bf16 = true;
+        bool direct = true, all_f32 = true, all_bf16 = true;
         for (const GxDesc& d : v) {
             direct = direct && d.vec && d.r % kGaKb == 0;
             all_f32 = all_f32 && !d.xbf16;
@@ -2017,10 +2083,11 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
     // Right descriptors first, then left; the item tables index that array.
     std::vector<GxDesc> gd(right);
     gd.insert(gd.end(), left.begin(), left.end());
-    bool proj_direct[2] = {!mx, !mx};  // right, left
+    bool proj_direct[2] = {true, true};  // right, left
     for (const GxDesc& d : right) proj_direct[0] = proj_direct[0] && d.vec && d.d % kGaKb == 0;
     for (const GxDesc& d : left) proj_direct[1] = proj_direct[1] && d.vec && d.d % kGaKb == 0;
-    for (size_t i = 0; i < gd.size(); ++i) {
+    if (mx) gx_lists(gd, right.size(), lists);
+    for (size_t i = 0; !mx && i < gd.size(); ++i) {
         const GxDesc& d = gd[i];
         const bool is_left = i >= right.size();
         const int id = static_cast<int>(i);
@@ -2028,7 +2095,7 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
         // both sides direct: one list (kGaProjR) for the mixed kernel
         const bool one_list = proj_direct[0] && proj_direct[1];
         for (int64_t y = 0; y < pt; ++y)
-            lists[d.gs ? kGxProjM : is_left && !one_list ? kGaProjL : kGaProjR].push_back(make_int2(id, static_cast<int>(y)));
+            lists[is_left && !one_list ? kGaProjL : kGaProjR].push_back(make_int2(id, static_cast<int>(y)));
         std::vector<int2>& L = lists[is_left ? kGaBackL : kGaBackR];
         if (back_mode[is_left] == kBackUr || back_mode[is_left] == kBackUrBf16) {
             // chunks of N outer, bands of U inner: consecutive items share N's rows
@@ -2054,7 +2121,6 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
     // back-projection -2.4%).
     xcd_deal(lists[kGaProjR]);
     xcd_deal(lists[kGaProjL]);
-    xcd_deal(lists[kGxProjM]);
     xcd_deal(lists[kGaBackR]);
     xcd_deal(lists[kGaBackL]);
     size_t offs[kGaListCount];
@@ -2204,9 +2270,10 @@ int ga_step(const meo_galore_hparams* hp, int64_t step, int32_t n, const meo_ten
              static_cast<float>(hp->lr * hp->scale)};
     PassTimer pt(s);
     if (mx) {
-        launch_gx_project(GxTable{p->gxdesc, p->items[kGaProjR]}, p->count[kGaProjR], a, false, s);
-        launch_gx_project(GxTable{p->gxdesc, p->items[kGaProjL]}, p->count[kGaProjL], a, true, s);
-        launch_gx_project_mx4(GxTable{p->gxdesc, p->items[kGxProjM]}, p->count[kGxProjM], a, s);
+        for (int l = 0; l < 2 * kGxForms; ++l)
+            launch_gx_project(GxTable{p->gxdesc, p->items[kGxProj + l]}, p->count[kGxProj + l], a, l & 1, l / 2, s);
+        for (int f = 0; f < kMxForms; ++f)
+            launch_gx_project_mx4(GxTable{p->gxdesc, p->items[kGxProjM + f]}, p->count[kGxProjM + f], a, f, s);
     } else if (p->proj_direct[0] && p->proj_direct[1]) {
         launch_galore_project_mixed(GTable{p->gdesc, p->items[kGaProjR]}, p->count[kGaProjR], p->nright, a, s);
     } else {
@@ -2215,8 +2282,8 @@ int ga_step(const meo_galore_hparams* hp, int64_t step, int32_t n, const meo_ten
     }
     pt.mark(kPassGaProject);
     if (mx) {
-        launch_gx_back(GxTable{p->gxdesc, p->items[kGaBackR]}, p->count[kGaBackR], a, false, p->back_mode[0], s);
-        launch_gx_back(GxTable{p->gxdesc, p->items[kGaBackL]}, p->count[kGaBackL], a, true, p->back_mode[1], s);
+        for (int l = 0; l < 4; ++l)
+            launch_gx_back(GxTable{p->gxdesc, p->items[kGxBack + l]}, p->count[kGxBack + l], a, l & 1, l >= 2, s);
     } else {
         launch_galore_back(GTable{p->gdesc, p->items[kGaBackR]}, p->count[kGaBackR], a, false, p->back_mode[0], s);
         launch_galore_back(GTable{p->gdesc, p->items[kGaBackL]}, p->count[kGaBackL], a, true, p->back_mode[1], s);
@@ -2337,6 +2404,15 @@ int mx4_convert(int32_t n, const meo_mx4_matrix* ms, bool transposed, bool quant
     return launch_status(quantize ? "mx4 quantize launch" : "mx4 dequantize launch");
 }
 
+// The tile form of a product (launch_mx4_matmul).
+MxForm mx4_form(const meo_mx4_product& q) {
+    const int64_t nb = ceil_div(q.k, kMxBlock);
+    if (nb == 0 || nb % 4 != 0 || reinterpret_cast<uintptr_t>(q.a_scales) % 4 || reinterpret_cast<uintptr_t>(q.b_scales) % 4)
+        return kMxAny;
+    if (q.n <= kMxFormCols[kMxNarrow]) return kMxNarrow;
+    return ceil_div(q.m, kMxFormRows[kMxTall]) * ceil_div(q.n, kMxFormCols[kMxTall]) >= kMxTallTiles ? kMxTall : kMxWide;
+}
+
 int check_mx4_products(int32_t n, const meo_mx4_product* ps) {
     g_err.clear();
     if (n < 0) return fail(MEO_EINVAL, "negative product count");
@@ -2346,11 +2422,12 @@ int check_mx4_products(int32_t n, const meo_mx4_product* ps) {
         const meo_mx4_product& q = ps[k];
         const std::string who = "product " + std::to_string(k) + ": ";
         if (q.m < 0 || q.n < 0 || q.k < 0) return fail(MEO_ESHAPE, who + "negative m, n or k");
-        if (q.m > kMaxDim || q.n > kMaxDim || q.k > kMaxDim) return fail(MEO_ESHAPE, who + "m, n or k exceeds 2^31 - 1");
+        if (q.m > kMaxDim || q.n > kMaxDim) return fail(MEO_ESHAPE, who + "m or n exceeds 2^31 - 1");
+        if (q.k > kMxMaxK) return fail(MEO_ESHAPE, who + "k exceeds 2^23");
         int rc = check_mx4_values(who, q.c, q.m, q.n, q.ldc, q.dtype, "c");
         if (rc) return rc;
         if (q.m == 0 || q.n == 0) continue;
-        if (ceil_div(q.m, kMxTile) * ceil_div(q.n, kMxTile) > kMaxDim) return fail(MEO_ESHAPE, who + "too many tiles");
+        if (ceil_div(q.m, kMxFormRows[0]) * ceil_div(q.n, kMxFormCols[0]) > kMaxDim) return fail(MEO_ESHAPE, who + "too many tiles");
         if (q.k == 0) continue;
         rc = check_mx4_codes(who, q.a_codes, q.a_scales, "a_");
         if (!rc) rc = check_mx4_codes(who, q.b_codes, q.b_scales, "b_");
@@ -2462,36 +2539,39 @@ int meo_mx4_matmul(int32_t n, const meo_mx4_product* ps, void* stream) {
     int rc = check_mx4_products(n, ps);
     if (rc || n == 0) return rc;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    MxProdBatch b;
-    b.n = 0;
-    int64_t grid = 0;
-    auto flush = [&]() {
-        launch_mx4_matmul(b, static_cast<uint32_t>(grid), s);
+    std::vector<MxForm> form(n);
+    for (int32_t k = 0; k < n; ++k) form[k] = mx4_form(ps[k]);
+    for (int f = 0; f < kMxForms; ++f) {  // each form in launches of its own
+        MxProdBatch b;
         b.n = 0;
-        grid = 0;
-    };
-    for (int32_t k = 0; k < n; ++k) {
-        const meo_mx4_product& q = ps[k];
-        if (q.m == 0 || q.n == 0) continue;
-        const int64_t tiles = ceil_div(q.m, kMxTile) * ceil_div(q.n, kMxTile);
-        if (b.n == kMxBatch || grid + tiles > kMaxDim) flush();
-        MxProd& p = b.p[b.n++];
-        p.ac = static_cast<const uint8_t*>(q.a_codes);
-        p.as = static_cast<const uint8_t*>(q.a_scales);
-        p.bc = static_cast<const uint8_t*>(q.b_codes);
-        p.bs = static_cast<const uint8_t*>(q.b_scales);
-        p.c = q.c;
-        p.ldc = q.ldc;
-        p.m = q.m;
-        p.n = q.n;
-        p.nb = ceil_div(q.k, kMxBlock);
-        p.first = static_cast<uint32_t>(grid);
-        p.tn = static_cast<uint32_t>(ceil_div(q.n, kMxTile));
-        p.cbf16 = q.dtype == MEO_BF16;
-        p.vec = aligned16(q.c) && q.ldc % (p.cbf16 ? 8 : 4) == 0;
-        grid += tiles;
+        int64_t grid = 0;
+        auto flush = [&]() {
+            launch_mx4_matmul(b, static_cast<uint32_t>(grid), static_cast<MxForm>(f), s);
+            b.n = 0;
+            grid = 0;
+        };
+        for (int32_t k = 0; k < n; ++k) {
+            const meo_mx4_product& q = ps[k];
+            if (q.m == 0 || q.n == 0 || form[k] != f) continue;
+            const int64_t tiles = ceil_div(q.m, kMxFormRows[f]) * ceil_div(q.n, kMxFormCols[f]);
+            if (b.n == kMxBatch || grid + tiles > kMaxDim) flush();
+            MxProd& p = b.p[b.n++];
+            p.ac = static_cast<const uint8_t*>(q.a_codes);
+            p.as = static_cast<const uint8_t*>(q.a_scales);
+            p.bc = static_cast<const uint8_t*>(q.b_codes);
+            p.bs = static_cast<const uint8_t*>(q.b_scales);
+            p.c = q.c;
+            p.ldc = q.ldc;
+            p.m = q.m;
+            p.n = q.n;
+            p.nb = ceil_div(q.k, kMxBlock);
+            p.first = static_cast<uint32_t>(grid);
+            p.tn = static_cast<uint32_t>(ceil_div(q.n, kMxFormCols[f]));
+            p.cbf16 = q.dtype == MEO_BF16;
+            grid += tiles;
+        }
+        flush();
     }
-    flush();
     return launch_status("mx4 matmul launch");
 }
 

@@ -42,13 +42,15 @@ struct GTable {
 
 // A projected tensor whose projector is held in MX4 (one copy, [r][d], blocks along d);
 // u and ut are unused by its step. The gradient is bf16 (g, gs NULL) or MX4 [D][d] with
-// blocks along d (g: its codes, gs: its scales).
+// blocks along d (g: its codes, gs: its scales). The planes of N have rows of rp >= r
+// values, zero past r.
 struct GxDesc : GDesc {
     const uint8_t* uc;  // projector codes [r][16 nb]
     const uint8_t* us;  // projector scales [r][nb]
     const uint8_t* gs;
     int32_t nb;         // blocks along d
-    int32_t tpi;        // U-register back-projection: 64-row tiles of N per item
+    int32_t rp;         // r rounded up to the matrix instruction's depth, 16
+    int32_t tpi;        // back-projection: 64-row tiles of N per item
 };
 
 struct GxTable {
@@ -82,12 +84,16 @@ constexpr int kUrTiles = 64;  // 64-row tiles of N per item of the U-register ba
 void launch_galore_back(const GTable& t, int64_t n, const GaArgs& a, bool left, int mode, hipStream_t s);
 void launch_galore_adamw(const Table& t, int64_t n, const GaArgs& a, hipStream_t s);
 
-// The step's products with an MX4 projector. Projection of a bf16 gradient (`left`) or of
-// an MX4 one (its rows are rows of R on either side); items are tiles of kGxRows rows of R.
-constexpr int kGxRows = 64;
-void launch_gx_project(const GxTable& t, int64_t n, const GaArgs& a, bool left, hipStream_t s);
-void launch_gx_project_mx4(const GxTable& t, int64_t n, const GaArgs& a, hipStream_t s);
-void launch_gx_back(const GxTable& t, int64_t n, const GaArgs& a, bool left, int mode, hipStream_t s);
+// Projection with an MX4 projector: tiles of kGxFormRows rows of R. kGxAny: bf16 gradient of
+// any shape and alignment; kGxDirect, kGxDirectTall: d a multiple of 128, rows of the gradient
+// and of the scales aligned. An MX4 gradient takes the product's forms (MxForm).
+enum GxForm { kGxAny = 0, kGxDirect, kGxDirectTall, kGxForms };
+constexpr int kGxFormRows[kGxForms] = {64, 64, 128};
+void launch_gx_project(const GxTable& t, int64_t n, const GaArgs& a, bool left, int form, hipStream_t s);
+void launch_gx_project_mx4(const GxTable& t, int64_t n, const GaArgs& a, int form, hipStream_t s);
+// Back-projection with an MX4 projector: the U-register kernel for any shape, parameters
+// of one dtype; item y = band * btj + chunk, chunks of tpi tiles of N.
+void launch_gx_back(const GxTable& t, int64_t n, const GaArgs& a, bool left, bool xbf16, hipStream_t s);
 
 // ------------------------------------------------------------------ projector refresh
 

@@ -338,9 +338,8 @@ constexpr int kBackN = kGaTile * kGaBackRW;  // rows of N per tile
 // (48 KB: 3 blocks per CU), for lists whose rank is a multiple of kGaKb; otherwise
 // through registers into a padded arena (55 KB) with the next block's loads in
 // flight during the multiply.
-template <bool Left, bool Direct, bool MX>
-__global__ __launch_bounds__(kBackThreads, Direct ? 3 : 1) void k_galore_back(TableOf<MX> t, GaArgs a) {
-    static_assert(!(Direct && MX), "an MX4 projector is decoded on its way through registers");
+template <bool Left, bool Direct>
+__global__ __launch_bounds__(kBackThreads, Direct ? 3 : 1) void k_galore_back(GTable t, GaArgs a) {
     // one arena: N's planes [kBackN][pitch] twice, then U [256][pitch]; reused by
     // the epilogue exchange (4 kGaBackRW x 8.5 KB)
     constexpr int kPitch = Direct ? kDirectPitch : kGaPitch;
@@ -351,7 +350,7 @@ __global__ __launch_bounds__(kBackThreads, Direct ? 3 : 1) void k_galore_back(Ta
     uint16_t* su = arena + 2 * kBackN * kPitch;   // U rows
     const int2 it = t.items[blockIdx.x];
     if (it.x < 0) return;  // an empty item of the XCD-dealt list
-    const DescOf<MX> d = t.desc[it.x];
+    const GDesc d = t.desc[it.x];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int ug = wave & 3, ng = wave >> 2;  // the wave's 64-row groups of U and of N
     const int ti = it.y / d.btj, tj = it.y % d.btj;
@@ -370,12 +369,11 @@ __global__ __launch_bounds__(kBackThreads, Direct ? 3 : 1) void k_galore_back(Ta
             for (int v = 0; v < 16; ++v) acc[ib][jb][v] = 0.0f;
 
     RowStage<kBackN, kBackThreads> ph, pl;
-    typename std::conditional<MX, MxTransStage, RowStage<kGaWide, kBackThreads>>::type pu;
+    RowStage<kGaWide, kBackThreads> pu;
     auto fetch = [&](int k0) {
         ph.load(d.nh, d.D, d.r, n0, k0, vec);
         pl.load(d.nl, d.D, d.r, n0, k0, vec);
-        if constexpr (MX) pu.load(d, u0, k0);
-        else pu.load(d.u, d.d, d.r, u0, k0, vec);
+        pu.load(d.u, d.d, d.r, u0, k0, vec);
     };
     // The wave's part of the parameter tile, as the epilogue reads it (lane: rows
     // (lane >> 3) + 8 q of each 32-row half ib, columns 8 (lane & 7) ..): loaded
@@ -577,7 +575,8 @@ __device__ __forceinline__ int ur_ex(int r, int col) {
     return ((r ^ ((r >> 2) & 1)) << 5) + ((((col >> 2) ^ ((r >> 1) & 1))) << 2) + (col & 3);
 }
 
-__device__ __forceinline__ void ur_stage(const GDesc& d, int64_t n0, uint16_t* buf, int wave, int lane) {
+// pitch: values per row of N's planes, a multiple of 8.
+__device__ __forceinline__ void ur_stage(const GDesc& d, int pitch, int64_t n0, uint16_t* buf, int wave, int lane) {
     // instruction j: rows 2j, 2j + 1 of one plane (plane = j / 32), 32 chunks each
 #pragma unroll
     for (int i = 0; i < kUrNDma; ++i) {
@@ -585,9 +584,9 @@ __device__ __forceinline__ void ur_stage(const GDesc& d, int64_t n0, uint16_t* b
         const int plane = j >> 5, jr = j & 31;
         const int row = 2 * jr + (lane >> 5);       // 0 .. 63
         const int c = (lane & 31) ^ (row & 15);     // global chunk held at position lane & 31
-        const int cc = min(c, d.r / 8 - 1);
+        const int cc = min(c, pitch / 8 - 1);
         const int64_t grow = min(n0 + row, static_cast<int64_t>(d.D) - 1);
-        const uint16_t* src = (plane ? d.nl : d.nh) + grow * d.r + cc * 8;
+        const uint16_t* src = (plane ? d.nl : d.nh) + grow * pitch + cc * 8;
         __builtin_amdgcn_global_load_lds((const MEO_GLOBAL void*)src,
                                          (__attribute__((address_space(3))) void*)(buf + j * 512), 16, 0, 0);
     }
@@ -597,8 +596,8 @@ __device__ __forceinline__ bfv8 ur_frag(const uint16_t* plane, int row, int kk) 
     return *reinterpret_cast<const bfv8*>(plane + row * 256 + ((((kk >> 3) ^ (row & 15))) << 3));
 }
 
-template <bool Left, bool XB>
-__global__ __launch_bounds__(512, 1) void k_galore_back_ur(GTable t, GaArgs a) {
+template <bool Left, bool XB, bool MX>
+__global__ __launch_bounds__(512, 1) void k_galore_back_ur(TableOf<MX> t, GaArgs a) {
     static_assert(kUrNDma == 8, "wait counts below");
     constexpr int kP = XB ? 4 : 8;  // 16-byte parameter loads (and stores) per lane per tile
     __shared__ __attribute__((aligned(16))) uint16_t nb0[2 * kUrN * 256];
@@ -606,20 +605,53 @@ __global__ __launch_bounds__(512, 1) void k_galore_back_ur(GTable t, GaArgs a) {
     __shared__ __attribute__((aligned(16))) float exb[8 * 32 * 32];
     const int2 it = t.items[blockIdx.x];
     if (it.x < 0) return;  // an empty item of the XCD-dealt list
-    const GDesc d = t.desc[it.x];
+    const DescOf<MX> d = t.desc[it.x];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int nc = d.btj;  // chunks of kUrTiles tiles per band
+    int pitch, tpi;  // values per row of N's planes; tiles per item
+    if constexpr (MX) {
+        pitch = d.rp;
+        tpi = d.tpi;
+    } else {
+        pitch = d.r;
+        tpi = kUrTiles;
+    }
+    const int nc = d.btj;  // chunks of tpi tiles per band
     const int band = it.y / nc, chunk = it.y % nc;
     const int64_t u0 = static_cast<int64_t>(band) * kGaWide;
-    const int64_t nt0 = static_cast<int64_t>(chunk) * kUrTiles;
-    const int ntiles = static_cast<int>(min<int64_t>(kUrTiles, (d.D + kUrN - 1) / kUrN - nt0));
-    const int nks = d.r / 16;  // 16-wide contraction sub-steps
+    const int64_t nt0 = static_cast<int64_t>(chunk) * tpi;
+    const int ntiles = static_cast<int>(min<int64_t>(tpi, (d.D + kUrN - 1) / kUrN - nt0));
+    const int nks = pitch / 16;  // 16-wide contraction sub-steps
     using PT = typename std::conditional<XB, uint16_t, float>::type;
     PT* const x = static_cast<PT*>(d.x);
     // U fragments of the wave's 32 rows for the whole rank (64 VGPRs), landed before the
     // pipeline starts so that no wait inside it has to cover them
     bfv8 uf[16];
-    {
+    if constexpr (MX) {
+        // The wave's 32 rows of U are one block of each row of U^T: decoded into LDS as
+        // [r][32] (the stages are free yet) and read back transposed.
+        uint16_t* lu = (wave < 4 ? nb0 : nb1) + (wave & 3) * 8192;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = lane + 64 * j;
+            u32x4 c;
+            uint32_t e;
+            ld_mx_block(d, r, u0 / kMxBlock + wave, c, e);
+            const float sc = mx4_scale(e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st_lds8(lu + r * 32 + i * 8, mx4_to_bf16(c[i], sc));
+        }
+        __syncthreads();
+#pragma unroll
+        for (int ks = 0; ks < 16; ++ks) {
+            // as ld_frag_tr, rows of 32
+            const int g = lane >> 4, e = (lane >> 2) & 3, q = lane & 3;
+            const uint16_t* p = lu + (16 * ks + 8 * (g >> 1) + e) * 32 + 16 * (g & 1) + 4 * q;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p + 4 * 32));
+            const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            uf[ks] = __builtin_bit_cast(bfv8, v);
+        }
+    } else {
         const int64_t row = min(u0 + wave * 32 + (lane & 31), static_cast<int64_t>(d.d) - 1);
 #pragma unroll
         for (int ks = 0; ks < 16; ++ks) {
@@ -630,6 +662,7 @@ __global__ __launch_bounds__(512, 1) void k_galore_back_ur(GTable t, GaArgs a) {
     MEO_WAIT_VM(0);
 #pragma unroll
     for (int ks = 0; ks < 16; ++ks) __asm__ volatile("" : "+v"(uf[ks]));
+    if constexpr (MX) __syncthreads();  // every wave has its fragments: the stages may be filled
     // W cells of the wave: two 32 x 32 blocks (blk: the tile's 32-row halves of N); in
     // block blk, lane holds rows (lane >> 2) + 16 q (q < 2), columns 8 (lane & 3) .. + 7.
     auto cell = [&](int64_t n0, int blk, int q, int64_t& row, int64_t& col) {
@@ -750,6 +783,15 @@ __global__ __launch_bounds__(512, 1) void k_galore_back_ur(GTable t, GaArgs a) {
                 } else {
                     if (row >= d.m || col >= d.n) continue;
                     PT* xp = x + row * d.n + col;
+                    if constexpr (MX) {  // only the edge is element-wise
+                        if (d.wvec && col + 8 <= d.n) {
+                            load_v8(x, row * d.n + col, kVec, true, XB, w);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e] = a.decay * w[e] - a.coef * cq[e];
+                            store_v8(x, row * d.n + col, kVec, true, XB, w);
+                            continue;
+                        }
+                    }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         if (col + e >= d.n) continue;
@@ -786,8 +828,8 @@ __global__ __launch_bounds__(512, 1) void k_galore_back_ur(GTable t, GaArgs a) {
     // the first tile: the next stage's 8 and its kP loads, or no loads where the
     // parameter rows are not 16-byte aligned and load_w issues none).
     const int last = ntiles - 1;
-    ur_stage(d, nt0 * kUrN, nb0, wave, lane);
-    ur_stage(d, (nt0 + min(1, last)) * kUrN, nb1, wave, lane);
+    ur_stage(d, pitch, nt0 * kUrN, nb0, wave, lane);
+    ur_stage(d, pitch, (nt0 + min(1, last)) * kUrN, nb1, wave, lane);
     load_w(nt0 * kUrN);
     if (d.wvec) MEO_WAIT_VM(kP + 8);
     else MEO_WAIT_VM(8);
@@ -800,7 +842,7 @@ __global__ __launch_bounds__(512, 1) void k_galore_back_ur(GTable t, GaArgs a) {
         update((nt0 + i) * kUrN, exact);
         if (i + 1 >= ntiles) break;
         // tile i + 1 in nb1
-        ur_stage(d, (nt0 + min(i + 2, last)) * kUrN, nb0, wave, lane);
+        ur_stage(d, pitch, (nt0 + min(i + 2, last)) * kUrN, nb0, wave, lane);
         load_w((nt0 + i + 1) * kUrN);
         if (exact) MEO_WAIT_VM(2 * kP + 8);
         else MEO_WAIT_VM(0);
@@ -810,7 +852,7 @@ __global__ __launch_bounds__(512, 1) void k_galore_back_ur(GTable t, GaArgs a) {
         __builtin_amdgcn_s_barrier();
         update((nt0 + i + 1) * kUrN, exact);
         if (i + 2 >= ntiles) break;
-        ur_stage(d, (nt0 + min(i + 3, last)) * kUrN, nb1, wave, lane);
+        ur_stage(d, pitch, (nt0 + min(i + 3, last)) * kUrN, nb1, wave, lane);
         load_w((nt0 + i + 2) * kUrN);
         if (exact) MEO_WAIT_VM(2 * kP + 8);
         else MEO_WAIT_VM(0);
@@ -1050,26 +1092,28 @@ void launch_galore_back(const GTable& t, int64_t n, const GaArgs& a, bool left, 
     const bool direct = mode == kBackDirect;
     if (mode == kBackUr || mode == kBackUrBf16) {
         const bool xb = mode == kBackUrBf16;
-        if (left && xb) hipLaunchKernelGGL((k_galore_back_ur<true, true>), grid, dim3(512), 0, s, t, a);
-        else if (left) hipLaunchKernelGGL((k_galore_back_ur<true, false>), grid, dim3(512), 0, s, t, a);
+        if (left && xb) hipLaunchKernelGGL((k_galore_back_ur<true, true, false>), grid, dim3(512), 0, s, t, a);
+        else if (left) hipLaunchKernelGGL((k_galore_back_ur<true, false, false>), grid, dim3(512), 0, s, t, a);
         else if (xb) hipLaunchKernelGGL((k_galore_back_u2<true>), grid, dim3(256), 0, s, t, a);
-        else hipLaunchKernelGGL((k_galore_back_ur<false, false>), grid, dim3(512), 0, s, t, a);
+        else hipLaunchKernelGGL((k_galore_back_ur<false, false, false>), grid, dim3(512), 0, s, t, a);
         return;
     }
     if (left) {
-        if (direct) hipLaunchKernelGGL((k_galore_back<true, true, false>), grid, block, 0, s, t, a);
-        else hipLaunchKernelGGL((k_galore_back<true, false, false>), grid, block, 0, s, t, a);
+        if (direct) hipLaunchKernelGGL((k_galore_back<true, true>), grid, block, 0, s, t, a);
+        else hipLaunchKernelGGL((k_galore_back<true, false>), grid, block, 0, s, t, a);
     } else {
-        if (direct) hipLaunchKernelGGL((k_galore_back<false, true, false>), grid, block, 0, s, t, a);
-        else hipLaunchKernelGGL((k_galore_back<false, false, false>), grid, block, 0, s, t, a);
+        if (direct) hipLaunchKernelGGL((k_galore_back<false, true>), grid, block, 0, s, t, a);
+        else hipLaunchKernelGGL((k_galore_back<false, false>), grid, block, 0, s, t, a);
     }
 }
 
-void launch_gx_back(const GxTable& t, int64_t n, const GaArgs& a, bool left, int mode, hipStream_t s) {
+void launch_gx_back(const GxTable& t, int64_t n, const GaArgs& a, bool left, bool xbf16, hipStream_t s) {
     if (n <= 0) return;
-    const dim3 grid(static_cast<uint32_t>(n)), block(kBackThreads);
-    if (left) hipLaunchKernelGGL((k_galore_back<true, false, true>), grid, block, 0, s, t, a);
-    else hipLaunchKernelGGL((k_galore_back<false, false, true>), grid, block, 0, s, t, a);
+    const dim3 grid(static_cast<uint32_t>(n));
+    if (left && xbf16) hipLaunchKernelGGL((k_galore_back_ur<true, true, true>), grid, dim3(512), 0, s, t, a);
+    else if (left) hipLaunchKernelGGL((k_galore_back_ur<true, false, true>), grid, dim3(512), 0, s, t, a);
+    else if (xbf16) hipLaunchKernelGGL((k_galore_back_ur<false, true, true>), grid, dim3(512), 0, s, t, a);
+    else hipLaunchKernelGGL((k_galore_back_ur<false, false, true>), grid, dim3(512), 0, s, t, a);
 }
 
 // ------------------------------------------------------------------ flat AdamW

@@ -100,15 +100,12 @@ using DescOf = typename std::conditional<MX, GxDesc, GDesc>::type;
 template <bool MX>
 using TableOf = typename std::conditional<MX, GxTable, GTable>::type;
 
-// 32 codes times their scale as bf16 (exact: a code has two significant bits).
-__device__ __forceinline__ void mx4_to_bf16(const u32x4& c, uint32_t e, u32x4* w) {
-    const float s = mx4_scale(e);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float v[8];
-        mx4_unpack8(c[i], s, v);
-        w[i] = pack_bf16x8(v);
-    }
+// 8 codes times their scale as bf16 (exact: a code has two significant bits).
+__device__ __forceinline__ u32x4 mx4_to_bf16(uint32_t q, float scale) {
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 3))};
 }
 
 // One block of the MX4 projector: row `row` of U^T, block kb; zero outside it.
@@ -137,42 +134,10 @@ struct MxRowStage {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int u = threadIdx.x + i * kThreads;
-            u32x4 w[4];
-            mx4_to_bf16(c[i], e[i], w);
+            const float s = mx4_scale(e[i]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) st_lds8(lds + (u >> 1) * kGaPitch + (u & 1) * kMxBlock + 8 * j, w[j]);
-        }
-    }
-};
-
-// Rows [u0, u0 + kGaWide) of U x contraction columns [k0, k0 + kGaKb) of an MX4 projector
-// (u0 a multiple of kMxBlock): its blocks run along U's rows, so each is scattered down a
-// column of the tile.
-struct MxTransStage {
-    static constexpr int kBlocks = kGaWide / kMxBlock;
-    static constexpr int kPer = kGaKb * kBlocks / kThreads;
-    u32x4 c[kPer];
-    uint32_t e[kPer];
-    __device__ __forceinline__ void load(const GxDesc& d, int64_t u0, int64_t k0) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int u = threadIdx.x + i * kThreads;
-            ld_mx_block(d, k0 + u / kBlocks, u0 / kMxBlock + u % kBlocks, c[i], e[i]);
-        }
-    }
-    __device__ __forceinline__ void store(uint16_t* lds) const {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int u = threadIdx.x + i * kThreads;
-            u32x4 w[4];
-            mx4_to_bf16(c[i], e[i], w);
-            uint16_t* p = lds + (u % kBlocks) * kMxBlock * kGaPitch + u / kBlocks;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const uint32_t x = w[j >> 2][j & 3];
-                p[(2 * j) * kGaPitch] = static_cast<uint16_t>(x & 0xffffu);
-                p[(2 * j + 1) * kGaPitch] = static_cast<uint16_t>(x >> 16);
-            }
+            for (int j = 0; j < 4; ++j)
+                st_lds8(lds + (u >> 1) * kGaPitch + (u & 1) * kMxBlock + 8 * j, mx4_to_bf16(c[i][j], s));
         }
     }
 };

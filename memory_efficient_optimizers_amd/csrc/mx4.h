@@ -11,6 +11,7 @@
 namespace meo {
 
 constexpr int kMxBlock = 32;   // values per scale
+constexpr int64_t kMxMaxK = 1 << 23;  // longest contraction of a product (32-bit offsets in a tile)
 constexpr int kMxBatch = 32;   // matrices per launch (their descriptors are kernel arguments)
 
 // One matrix of a quantize or dequantize call.
@@ -53,7 +54,6 @@ struct MxProd {
     uint32_t first;          // the product's first block in the launch
     uint32_t tn;             // tiles along n
     int32_t cbf16;
-    int32_t vec;             // rows of c allow 16-byte accesses
 };
 
 struct MxProdBatch {
@@ -61,9 +61,13 @@ struct MxProdBatch {
     MxProd p[kMxBatch];
 };
 
-constexpr int kMxTile = 64;  // rows and columns of a product tile
+// Tile of a product (rows x columns of C): any operands; at most 128 columns; more; more, and
+// enough rows that 128 at a time fill the GPU.
+enum MxForm { kMxAny = 0, kMxNarrow, kMxWide, kMxTall, kMxForms };
+constexpr int kMxFormRows[kMxForms] = {64, 64, 64, 128};
+constexpr int kMxFormCols[kMxForms] = {128, 128, 256, 256};
 
-void launch_mx4_matmul(const MxProdBatch& b, uint32_t grid, hipStream_t s);
+void launch_mx4_matmul(const MxProdBatch& b, uint32_t grid, MxForm form, hipStream_t s);
 
 // ----------------------------------------------------------------------------- device
 
@@ -73,12 +77,13 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bfv2 __attribute__((ext_vector_type(2)));
 
 // C += A B over 64 values of the contraction. Lane l holds one MX block of each operand
-// (row l & 31, block l >> 5: 16 bytes of codes) and its scale byte in the low byte of sa
-// or sb. The products are exact and the sums fp32.
+// (row l & 31, block l >> 5: 16 bytes of codes) and its scale as byte T of sa and sb. The
+// products are exact and the sums fp32.
+template <int T>
 __device__ __forceinline__ f32x16 mfma_mx4(const u32x4& a, const u32x4& b, const f32x16& c, uint32_t sa, uint32_t sb) {
     const i32x8 x = {static_cast<int>(a.x), static_cast<int>(a.y), static_cast<int>(a.z), static_cast<int>(a.w), 0, 0, 0, 0};
     const i32x8 y = {static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w), 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 0, sa, 0, sb);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, T, sa, T, sb);
 }
 
 // 2^(e - 127) as fp32: e = 0 is a subnormal, e = 255 a NaN.

@@ -8,7 +8,7 @@
 // columns of 32 rows and finds their maxima in registers; the codes of 8 such waves
 // (256 values of each column) are exchanged through LDS so that each row of codes is
 // written 128 bytes at a time.
-#include "mx4.h"
+#include "mx4_tile.h"
 
 namespace meo {
 
@@ -254,48 +254,65 @@ void launch_mx4_dequantize(const MxBatch& b, uint32_t grid, bool transposed, hip
 
 // ----------------------------------------------------------------------------- product
 
-// C = A B^T on the scaled matrix instructions: 4 waves, one 32 x 32 quadrant of a 64 x 64
-// tile each. Blocks past the operands' rows or contraction read as zero codes.
-__global__ __launch_bounds__(256) void k_mx4_matmul(MxProdBatch b) {
+// C = A B^T, stored from the accumulators: 32 consecutive values of two rows per
+// instruction. Tiles (MxForm): 128 rows x 256 columns of 8 waves where that fills the GPU,
+// 64 x 256 otherwise and 64 x 128 of 4 waves for products of at most 128 columns; any
+// nb or alignment that mx4_accumulate does not take goes through 64 x 128 tiles that read every
+// fragment as it lies.
+template <int IB, bool BF>
+__device__ __forceinline__ void mx4_store(const MxProd& p, int64_t i0, int64_t j0, int lane, const f32x16 (&acc)[IB][2]) {
+    const bool whole = i0 + 32 * IB <= p.m && j0 + 64 <= p.n;
+#pragma unroll
+    for (int jb = 0; jb < 2; ++jb) {
+        const int64_t col = j0 + jb * 32 + (lane & 31);
+        if (!whole && col >= p.n) continue;
+#pragma unroll
+        for (int ib = 0; ib < IB; ++ib)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int64_t row = i0 + ib * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+                if (!whole && row >= p.m) continue;
+                if (BF) *gst<uint16_t>(static_cast<uint16_t*>(p.c) + row * p.ldc + col) = static_cast<uint16_t>(bf16_bits(acc[ib][jb][v]));
+                else *gst<float>(static_cast<float*>(p.c) + row * p.ldc + col) = acc[ib][jb][v];
+            }
+    }
+}
+
+template <int IB, int WN, int NW, bool Any>
+__global__ __launch_bounds__(NW * 64) void k_mx4_matmul(MxProdBatch b) {
+    using T = MxTile<IB, WN, NW>;
+    __shared__ __attribute__((aligned(16))) uint8_t stages[Any ? 16 : 3 * T::kStage];
     int i = 0;
     while (i + 1 < b.n && blockIdx.x >= b.p[i + 1].first) ++i;
     const MxProd& p = b.p[i];
     const uint32_t tile = blockIdx.x - p.first;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t i0 = static_cast<int64_t>(tile / p.tn) * kMxTile + (wave >> 1) * 32;
-    const int64_t j0 = static_cast<int64_t>(tile % p.tn) * kMxTile + (wave & 1) * 32;
-    const int64_t ra = i0 + (lane & 31), rb = j0 + (lane & 31);
-    f32x16 acc;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    int64_t i0 = static_cast<int64_t>(uniform(static_cast<int>(tile / p.tn))) * T::kRowsA;
+    int64_t j0 = static_cast<int64_t>(uniform(static_cast<int>(tile % p.tn))) * T::kRowsB;
+    f32x16 acc[IB][2];
 #pragma unroll
-    for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
-    for (int64_t k = 0; k < p.nb; k += 2) {
-        const int64_t kb = k + (lane >> 5);
-        u32x4 ca = {0u, 0u, 0u, 0u}, cb = {0u, 0u, 0u, 0u};
-        uint32_t sa = 127, sb = 127;
-        if (ra < p.m && kb < p.nb) {
-            ca = *gld<u32x4>(p.ac + (ra * p.nb + kb) * 16);
-            sa = *gld<uint8_t>(p.as + ra * p.nb + kb);
-        }
-        if (rb < p.n && kb < p.nb) {
-            cb = *gld<u32x4>(p.bc + (rb * p.nb + kb) * 16);
-            sb = *gld<uint8_t>(p.bs + rb * p.nb + kb);
-        }
-        acc = mfma_mx4(ca, cb, acc, sa, sb);
-    }
-    const int64_t col = j0 + (lane & 31);
-    if (col >= p.n) return;
+    for (int ib = 0; ib < IB; ++ib)
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-        const int64_t row = i0 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-        if (row >= p.m) continue;
-        if (p.cbf16) *gst<uint16_t>(static_cast<uint16_t*>(p.c) + row * p.ldc + col) = static_cast<uint16_t>(bf16_bits(acc[v]));
-        else *gst<float>(static_cast<float*>(p.c) + row * p.ldc + col) = acc[v];
-    }
+        for (int jb = 0; jb < 2; ++jb)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[ib][jb][v] = 0.0f;
+    const MxOperand oa{p.ac, p.as, p.m, static_cast<int32_t>(p.nb)}, ob{p.bc, p.bs, p.n, static_cast<int32_t>(p.nb)};
+    if constexpr (Any) mx4_accumulate_any(oa, ob, i0, j0, acc);
+    else mx4_accumulate<IB, WN, NW>(oa, ob, i0, j0, stages, acc);
+    i0 += (wave / WN) * 32 * IB;
+    j0 += (wave % WN) * 64;
+    if (p.cbf16) mx4_store<IB, true>(p, i0, j0, lane, acc);
+    else mx4_store<IB, false>(p, i0, j0, lane, acc);
 }
 
-void launch_mx4_matmul(const MxProdBatch& b, uint32_t grid, hipStream_t s) {
+void launch_mx4_matmul(const MxProdBatch& b, uint32_t grid, MxForm form, hipStream_t s) {
     if (grid == 0) return;
-    hipLaunchKernelGGL(k_mx4_matmul, dim3(grid), dim3(256), 0, s, b);
+    switch (form) {
+        case kMxAny: hipLaunchKernelGGL((k_mx4_matmul<1, 2, 4, true>), dim3(grid), dim3(256), 0, s, b); break;
+        case kMxNarrow: hipLaunchKernelGGL((k_mx4_matmul<1, 2, 4, false>), dim3(grid), dim3(256), 0, s, b); break;
+        case kMxWide: hipLaunchKernelGGL((k_mx4_matmul<1, 4, 8, false>), dim3(grid), dim3(512), 0, s, b); break;
+        default: hipLaunchKernelGGL((k_mx4_matmul<2, 4, 8, false>), dim3(grid), dim3(512), 0, s, b); break;
+    }
 }
 
 }  // namespace meo
