@@ -1612,9 +1612,9 @@ int meo_came_shard_apply(const meo_came_hparams* hp, int64_t step, int32_t n, co
 namespace {
 
 enum GaList { kGaProjR = 0, kGaProjL, kGaBackR, kGaBackL, kGaFlat,
-              // MX4 projectors: projection by form (GxForm, right then left; MxForm for MX4
-              // gradients), back-projection by parameter dtype (float32 right, left, bf16 ...)
-              kGxProj, kGxProjM = kGxProj + 2 * kGxForms, kGxBack = kGxProjM + kMxForms, kGxEnd = kGxBack + 4,
+              // MX4 projectors: projection by form (GxForm; MxForm for MX4 gradients),
+              // back-projection by parameter dtype (float32, bf16)
+              kGxProj, kGxProjM = kGxProj + kGxForms, kGxBack = kGxProjM + kMxForms, kGxEnd = kGxBack + 2,
               // projector refresh
               kRfInit = kGxEnd, kRfG0N, kRfG0T, kRfG1N, kRfG1T, kRfGram, kRfOne, kRfCols, kRfStore, kGaListCount };
 
@@ -1863,64 +1863,67 @@ int check_galore_workspace(const meo_galore_hparams* hp, int32_t n, const meo_te
     return check_device_range(ws, bytes, dev, "workspace", MEO_EWORKSPACE);
 }
 
-// Items of a step with MX4 projectors. gd: the descriptors, right-side ones first; sets btj and
-// tpi. Projection forms and the tiles per back-projection item follow the call's total
-// work: the larger tiles share each part of U among more rows but need as many of
-// them as there are CUs.
 constexpr int64_t kCus = 256;
-constexpr int64_t kMxTallTiles = 200;  // 128-row tiles of a call from which its products take them
-constexpr int64_t kGxTallTiles = 512;
-void gx_lists(std::vector<GxDesc>& gd, size_t nright, std::vector<int2>* lists) {
+
+// Whether `tall` tiles of 128 rows take less time than `wide` of 64: a tile runs alone on its
+// CU, a tall one about 1.5 times as long.
+bool mx4_tall(int64_t tall, int64_t wide) { return 3 * ceil_div(tall, kCus) < 2 * ceil_div(wide, kCus); }
+
+// Items of a step with MX4 projectors over its descriptors; sets btj and tpi. The products'
+// form and the tiles per back-projection item follow the call's total work.
+void gx_lists(std::vector<GxDesc>& gd, std::vector<int2>* lists) {
     auto words = [](const void* p, int32_t nb) { return nb % 4 == 0 && reinterpret_cast<uintptr_t>(p) % 4 == 0; };
     auto direct = [&](const GxDesc& d) { return d.vec && d.d % 128 == 0 && words(d.us, d.nb); };
-    int64_t tall = 0, tall4 = 0;  // 128-row tiles of the call
-    for (const GxDesc& d : gd) (d.gs ? tall4 : tall) += ceil_div(d.D, 128);
+    int64_t tall = 0, wide = 0;  // tiles of the MX4 gradients' wide products, 128 and 64 rows each
+    for (const GxDesc& d : gd)
+        if (d.gs && words(d.us, d.nb) && words(d.gs, d.nb) && d.r > kMxFormCols[kMxNarrow]) {
+            tall += ceil_div(d.D, kMxFormRows[kMxTall]);
+            wide += ceil_div(d.D, kMxFormRows[kMxWide]);
+        }
     for (size_t i = 0; i < gd.size(); ++i) {
         const GxDesc& d = gd[i];
-        const bool left = i >= nright;
         int list, rows;
         if (d.gs) {
             const int form = !words(d.us, d.nb) || !words(d.gs, d.nb) ? kMxAny
                              : d.r <= kMxFormCols[kMxNarrow]          ? kMxNarrow
-                             : tall4 >= kMxTallTiles                  ? kMxTall
+                             : mx4_tall(tall, wide)                   ? kMxTall
                                                                       : kMxWide;
             list = kGxProjM + form;
             rows = kMxFormRows[form];
         } else {
-            const int form = !direct(d) ? kGxAny : tall >= kGxTallTiles ? kGxDirectTall : kGxDirect;
-            list = kGxProj + 2 * form + left;
+            const int form = direct(d) ? kGxDirect : kGxAny;
+            list = kGxProj + form;
             rows = kGxFormRows[form];
         }
         for (int64_t y = 0; y < ceil_div(d.D, rows); ++y) lists[list].push_back(make_int2(static_cast<int>(i), static_cast<int>(y)));
     }
-    for (int side = 0; side < 2; ++side)
-        for (int xb = 0; xb < 2; ++xb) {
-            std::vector<size_t> ids;
-            for (size_t i = 0; i < gd.size(); ++i)
-                if ((i >= nright) == (side == 1) && (gd[i].xbf16 != 0) == (xb == 1)) ids.push_back(i);
-            // Tiles per item: the count with the least time, in tiles, of the rounds that
-            // the items take on the CUs (an item's start, its part of U, is about a tile).
-            int best = 1;
-            int64_t least = INT64_MAX;
-            for (int tpi = 1; tpi <= kUrTiles; ++tpi) {
-                int64_t items = 0;
-                for (size_t i : ids) items += ceil_div(gd[i].d, kGaWide) * ceil_div(ceil_div(gd[i].D, kGaTile), tpi);
-                const int64_t time = ceil_div(items, kCus) * (tpi + 1);
-                if (time < least) {
-                    least = time;
-                    best = tpi;
-                }
-            }
-            for (size_t i : ids) {
-                GxDesc& d = gd[i];
-                d.tpi = best;
-                d.btj = static_cast<int32_t>(ceil_div(ceil_div(d.D, kGaTile), best));
-                // chunks of N outer, bands of U inner: consecutive items share N's rows
-                for (int64_t c = 0; c < d.btj; ++c)
-                    for (int64_t k = 0; k < ceil_div(d.d, kGaWide); ++k)
-                        lists[kGxBack + 2 * xb + side].push_back(make_int2(static_cast<int>(i), static_cast<int>(k * d.btj + c)));
+    for (int xb = 0; xb < 2; ++xb) {
+        std::vector<size_t> ids;
+        for (size_t i = 0; i < gd.size(); ++i)
+            if ((gd[i].xbf16 != 0) == (xb == 1)) ids.push_back(i);
+        // Tiles per item: the count with the least time, in tiles, of the rounds that the
+        // items take on the CUs (an item's start, its part of U, is about a tile).
+        int best = 1;
+        int64_t least = INT64_MAX;
+        for (int tpi = 1; tpi <= kUrTiles; ++tpi) {
+            int64_t items = 0;
+            for (size_t i : ids) items += ceil_div(gd[i].d, kGaWide) * ceil_div(ceil_div(gd[i].D, kGaTile), tpi);
+            const int64_t time = ceil_div(items, kCus) * (tpi + 1);
+            if (time < least) {
+                least = time;
+                best = tpi;
             }
         }
+        for (size_t i : ids) {
+            GxDesc& d = gd[i];
+            d.tpi = best;
+            d.btj = static_cast<int32_t>(ceil_div(ceil_div(d.D, kGaTile), best));
+            // chunks of N outer, bands of U inner: consecutive items share N's rows
+            for (int64_t c = 0; c < d.btj; ++c)
+                for (int64_t k = 0; k < ceil_div(d.d, kGaWide); ++k)
+                    lists[kGxBack + xb].push_back(make_int2(static_cast<int>(i), static_cast<int>(k * d.btj + c)));
+        }
+    }
 }
 
 GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, const GaState* st, bool mx,
@@ -2086,7 +2089,7 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
     bool proj_direct[2] = {true, true};  // right, left
     for (const GxDesc& d : right) proj_direct[0] = proj_direct[0] && d.vec && d.d % kGaKb == 0;
     for (const GxDesc& d : left) proj_direct[1] = proj_direct[1] && d.vec && d.d % kGaKb == 0;
-    if (mx) gx_lists(gd, right.size(), lists);
+    if (mx) gx_lists(gd, lists);
     for (size_t i = 0; !mx && i < gd.size(); ++i) {
         const GxDesc& d = gd[i];
         const bool is_left = i >= right.size();
@@ -2270,8 +2273,8 @@ int ga_step(const meo_galore_hparams* hp, int64_t step, int32_t n, const meo_ten
              static_cast<float>(hp->lr * hp->scale)};
     PassTimer pt(s);
     if (mx) {
-        for (int l = 0; l < 2 * kGxForms; ++l)
-            launch_gx_project(GxTable{p->gxdesc, p->items[kGxProj + l]}, p->count[kGxProj + l], a, l & 1, l / 2, s);
+        for (int f = 0; f < kGxForms; ++f)
+            launch_gx_project(GxTable{p->gxdesc, p->items[kGxProj + f]}, p->count[kGxProj + f], p->nright, a, f, s);
         for (int f = 0; f < kMxForms; ++f)
             launch_gx_project_mx4(GxTable{p->gxdesc, p->items[kGxProjM + f]}, p->count[kGxProjM + f], a, f, s);
     } else if (p->proj_direct[0] && p->proj_direct[1]) {
@@ -2282,8 +2285,8 @@ int ga_step(const meo_galore_hparams* hp, int64_t step, int32_t n, const meo_ten
     }
     pt.mark(kPassGaProject);
     if (mx) {
-        for (int l = 0; l < 4; ++l)
-            launch_gx_back(GxTable{p->gxdesc, p->items[kGxBack + l]}, p->count[kGxBack + l], a, l & 1, l >= 2, s);
+        for (int xb = 0; xb < 2; ++xb)
+            launch_gx_back(GxTable{p->gxdesc, p->items[kGxBack + xb]}, p->count[kGxBack + xb], p->nright, a, xb == 1, s);
     } else {
         launch_galore_back(GTable{p->gdesc, p->items[kGaBackR]}, p->count[kGaBackR], a, false, p->back_mode[0], s);
         launch_galore_back(GTable{p->gdesc, p->items[kGaBackL]}, p->count[kGaBackL], a, true, p->back_mode[1], s);
@@ -2410,7 +2413,8 @@ MxForm mx4_form(const meo_mx4_product& q) {
     if (nb == 0 || nb % 4 != 0 || reinterpret_cast<uintptr_t>(q.a_scales) % 4 || reinterpret_cast<uintptr_t>(q.b_scales) % 4)
         return kMxAny;
     if (q.n <= kMxFormCols[kMxNarrow]) return kMxNarrow;
-    return ceil_div(q.m, kMxFormRows[kMxTall]) * ceil_div(q.n, kMxFormCols[kMxTall]) >= kMxTallTiles ? kMxTall : kMxWide;
+    const int64_t tn = ceil_div(q.n, kMxFormCols[kMxWide]);
+    return mx4_tall(ceil_div(q.m, kMxFormRows[kMxTall]) * tn, ceil_div(q.m, kMxFormRows[kMxWide]) * tn) ? kMxTall : kMxWide;
 }
 
 int check_mx4_products(int32_t n, const meo_mx4_product* ps) {

@@ -84,16 +84,17 @@ constexpr int kUrTiles = 64;  // 64-row tiles of N per item of the U-register ba
 void launch_galore_back(const GTable& t, int64_t n, const GaArgs& a, bool left, int mode, hipStream_t s);
 void launch_galore_adamw(const Table& t, int64_t n, const GaArgs& a, hipStream_t s);
 
-// Projection with an MX4 projector: tiles of kGxFormRows rows of R. kGxAny: bf16 gradient of
-// any shape and alignment; kGxDirect, kGxDirectTall: d a multiple of 128, rows of the gradient
-// and of the scales aligned. An MX4 gradient takes the product's forms (MxForm).
-enum GxForm { kGxAny = 0, kGxDirect, kGxDirectTall, kGxForms };
-constexpr int kGxFormRows[kGxForms] = {64, 64, 128};
-void launch_gx_project(const GxTable& t, int64_t n, const GaArgs& a, bool left, int form, hipStream_t s);
+// Projection with an MX4 projector: tiles of kGxFormRows rows of R, both sides in one launch
+// (descriptors [0, nright) right-side ones). kGxAny: bf16 gradient of
+// any shape and alignment; kGxDirect: d a multiple of 128, rows of the gradient and of the
+// scales aligned. An MX4 gradient takes the product's forms (MxForm).
+enum GxForm { kGxAny = 0, kGxDirect, kGxForms };
+constexpr int kGxFormRows[kGxForms] = {64, 64};
+void launch_gx_project(const GxTable& t, int64_t n, int nright, const GaArgs& a, int form, hipStream_t s);
 void launch_gx_project_mx4(const GxTable& t, int64_t n, const GaArgs& a, int form, hipStream_t s);
 // Back-projection with an MX4 projector: the U-register kernel for any shape, parameters
 // of one dtype; item y = band * btj + chunk, chunks of tpi tiles of N.
-void launch_gx_back(const GxTable& t, int64_t n, const GaArgs& a, bool left, bool xbf16, hipStream_t s);
+void launch_gx_back(const GxTable& t, int64_t n, int nright, const GaArgs& a, bool xbf16, hipStream_t s);
 
 // ------------------------------------------------------------------ projector refresh
 

@@ -596,16 +596,12 @@ __device__ __forceinline__ bfv8 ur_frag(const uint16_t* plane, int row, int kk) 
     return *reinterpret_cast<const bfv8*>(plane + row * 256 + ((((kk >> 3) ^ (row & 15))) << 3));
 }
 
+// One item; nb0, nb1 and exb are the kernel's LDS.
 template <bool Left, bool XB, bool MX>
-__global__ __launch_bounds__(512, 1) void k_galore_back_ur(TableOf<MX> t, GaArgs a) {
+__device__ __forceinline__ void back_ur_item(const DescOf<MX>& d, int item, const GaArgs& a, uint16_t* nb0, uint16_t* nb1,
+                                             float* exb) {
     static_assert(kUrNDma == 8, "wait counts below");
     constexpr int kP = XB ? 4 : 8;  // 16-byte parameter loads (and stores) per lane per tile
-    __shared__ __attribute__((aligned(16))) uint16_t nb0[2 * kUrN * 256];
-    __shared__ __attribute__((aligned(16))) uint16_t nb1[2 * kUrN * 256];
-    __shared__ __attribute__((aligned(16))) float exb[8 * 32 * 32];
-    const int2 it = t.items[blockIdx.x];
-    if (it.x < 0) return;  // an empty item of the XCD-dealt list
-    const DescOf<MX> d = t.desc[it.x];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int pitch, tpi;  // values per row of N's planes; tiles per item
     if constexpr (MX) {
@@ -616,7 +612,7 @@ __global__ __launch_bounds__(512, 1) void k_galore_back_ur(TableOf<MX> t, GaArgs
         tpi = kUrTiles;
     }
     const int nc = d.btj;  // chunks of tpi tiles per band
-    const int band = it.y / nc, chunk = it.y % nc;
+    const int band = item / nc, chunk = item % nc;
     const int64_t u0 = static_cast<int64_t>(band) * kGaWide;
     const int64_t nt0 = static_cast<int64_t>(chunk) * tpi;
     const int ntiles = static_cast<int>(min<int64_t>(tpi, (d.D + kUrN - 1) / kUrN - nt0));
@@ -860,6 +856,28 @@ __global__ __launch_bounds__(512, 1) void k_galore_back_ur(TableOf<MX> t, GaArgs
     MEO_WAIT_VM(0);
 }
 
+template <bool Left, bool XB>
+__global__ __launch_bounds__(512, 1) void k_galore_back_ur(GTable t, GaArgs a) {
+    __shared__ __attribute__((aligned(16))) uint16_t nb0[2 * kUrN * 256];
+    __shared__ __attribute__((aligned(16))) uint16_t nb1[2 * kUrN * 256];
+    __shared__ __attribute__((aligned(16))) float exb[8 * 32 * 32];
+    const int2 it = t.items[blockIdx.x];
+    if (it.x < 0) return;  // an empty item of the XCD-dealt list
+    back_ur_item<Left, XB, false>(t.desc[it.x], it.y, a, nb0, nb1, exb);
+}
+
+// MX4 projectors: both sides in one launch, descriptors [0, nright) right-side ones.
+template <bool XB>
+__global__ __launch_bounds__(512, 1) void k_gx_back(GxTable t, GaArgs a, int nright) {
+    __shared__ __attribute__((aligned(16))) uint16_t nb0[2 * kUrN * 256];
+    __shared__ __attribute__((aligned(16))) uint16_t nb1[2 * kUrN * 256];
+    __shared__ __attribute__((aligned(16))) float exb[8 * 32 * 32];
+    const int2 it = t.items[blockIdx.x];
+    const GxDesc d = t.desc[it.x];
+    if (it.x < nright) back_ur_item<false, XB, true>(d, it.y, a, nb0, nb1, exb);
+    else back_ur_item<true, XB, true>(d, it.y, a, nb0, nb1, exb);
+}
+
 // m >= n back-projection of bf16 parameters, two blocks per CU. A block of 4 waves
 // holds a 256-row band of U in registers, 64 rows per wave (128 VGPRs), and walks up
 // to kU2Tiles 32-row tiles of N: per tile its two planes are staged (32 KB, two
@@ -1092,10 +1110,10 @@ void launch_galore_back(const GTable& t, int64_t n, const GaArgs& a, bool left, 
     const bool direct = mode == kBackDirect;
     if (mode == kBackUr || mode == kBackUrBf16) {
         const bool xb = mode == kBackUrBf16;
-        if (left && xb) hipLaunchKernelGGL((k_galore_back_ur<true, true, false>), grid, dim3(512), 0, s, t, a);
-        else if (left) hipLaunchKernelGGL((k_galore_back_ur<true, false, false>), grid, dim3(512), 0, s, t, a);
+        if (left && xb) hipLaunchKernelGGL((k_galore_back_ur<true, true>), grid, dim3(512), 0, s, t, a);
+        else if (left) hipLaunchKernelGGL((k_galore_back_ur<true, false>), grid, dim3(512), 0, s, t, a);
         else if (xb) hipLaunchKernelGGL((k_galore_back_u2<true>), grid, dim3(256), 0, s, t, a);
-        else hipLaunchKernelGGL((k_galore_back_ur<false, false, false>), grid, dim3(512), 0, s, t, a);
+        else hipLaunchKernelGGL((k_galore_back_ur<false, false>), grid, dim3(512), 0, s, t, a);
         return;
     }
     if (left) {
@@ -1107,13 +1125,11 @@ void launch_galore_back(const GTable& t, int64_t n, const GaArgs& a, bool left, 
     }
 }
 
-void launch_gx_back(const GxTable& t, int64_t n, const GaArgs& a, bool left, bool xbf16, hipStream_t s) {
+void launch_gx_back(const GxTable& t, int64_t n, int nright, const GaArgs& a, bool xbf16, hipStream_t s) {
     if (n <= 0) return;
     const dim3 grid(static_cast<uint32_t>(n));
-    if (left && xbf16) hipLaunchKernelGGL((k_galore_back_ur<true, true, true>), grid, dim3(512), 0, s, t, a);
-    else if (left) hipLaunchKernelGGL((k_galore_back_ur<true, false, true>), grid, dim3(512), 0, s, t, a);
-    else if (xbf16) hipLaunchKernelGGL((k_galore_back_ur<false, true, true>), grid, dim3(512), 0, s, t, a);
-    else hipLaunchKernelGGL((k_galore_back_ur<false, false, true>), grid, dim3(512), 0, s, t, a);
+    if (xbf16) hipLaunchKernelGGL(k_gx_back<true>, grid, dim3(512), 0, s, t, a, nright);
+    else hipLaunchKernelGGL(k_gx_back<false>, grid, dim3(512), 0, s, t, a, nright);
 }
 
 // ------------------------------------------------------------------ flat AdamW

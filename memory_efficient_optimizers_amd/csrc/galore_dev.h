@@ -94,11 +94,9 @@ struct TransStage {
     }
 };
 
-// Descriptor and table types of a step with a bf16 or an MX4 projector.
+// Descriptor type of a step with a bf16 or an MX4 projector.
 template <bool MX>
 using DescOf = typename std::conditional<MX, GxDesc, GDesc>::type;
-template <bool MX>
-using TableOf = typename std::conditional<MX, GxTable, GTable>::type;
 
 // 8 codes times their scale as bf16 (exact: a code has two significant bits).
 __device__ __forceinline__ u32x4 mx4_to_bf16(uint32_t q, float scale) {

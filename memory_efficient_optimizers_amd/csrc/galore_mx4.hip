@@ -15,14 +15,14 @@ namespace meo {
 
 namespace {
 
-// AdamW on 8 columns of a row of R (galore_adamw8 with N's planes in rows of rp values): the
-// moments up to column r, the planes up to rp, zero past r.
-__device__ __forceinline__ void gx_adamw8(const GxDesc& d, const GaArgs& a, int64_t row, int col, const float* rv) {
-    float m[8], v[8], nh[8], nl[8];
-    const int valid = min(max(d.r - col, 0), 8);
+// AdamW on 8 columns of a row of R: the moments (m, v: as loaded, the `valid` first columns
+// in range) are stored back, N goes to its two planes up to column rp, zero past r. (bf16
+// parameters need the low plane too: with N rounded to bf16 alone, 3% of the entries of
+// a 256 x 200 parameter came out one bf16 step away.)
+__device__ __forceinline__ void gx_adamw8(const GxDesc& d, const GaArgs& a, int64_t row, int col, int valid, float* m,
+                                          float* v, const float* rv) {
+    float nh[8], nl[8];
     const int64_t idx = row * d.r + col;
-    load_f8(d.em + idx, valid, d.rvec, m);
-    load_f8(d.ev + idx, valid, d.rvec, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         m[e] = fmaf(a.beta1, m[e], a.omb1 * rv[e]);
@@ -48,24 +48,37 @@ __device__ __forceinline__ int gx_ex(int r, int col) {
 
 // AdamW on a wave's 32 x 64 piece of R (accumulator blocks a0, a1) at row i0, column c0,
 // through the wave's exchange region lw: lane l ends with rows (l >> 2) + 16 q of a block
-// and its columns 8 (l & 3) .. + 7.
+// and its columns 8 (l & 3) .. + 7. All moments are loaded before the first is used.
 __device__ __forceinline__ void gx_epilogue(const GxDesc& d, const GaArgs& a, const f32x16& a0, const f32x16& a1,
                                             int64_t i0, int c0, float* lw, int lane) {
+    const int c = 8 * (lane & 3);
+    float m[2][2][8], v[2][2][8];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int64_t row = i0 + (lane >> 2) + 16 * q;
+            const int col = c0 + 32 * b + c;
+            const int valid = row < d.D ? min(max(d.r - col, 0), 8) : 0;
+            load_f8(d.em + row * d.r + col, valid, d.rvec, m[b][q]);
+            load_f8(d.ev + row * d.r + col, valid, d.rvec, v[b][q]);
+        }
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
         const f32x16& acc = b ? a1 : a0;
 #pragma unroll
-        for (int v = 0; v < 16; ++v) lw[gx_ex(acc_row(v, lane), acc_col(lane))] = acc[v];
+        for (int w = 0; w < 16; ++w) lw[gx_ex(acc_row(w, lane), acc_col(lane))] = acc[w];
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const int r = (lane >> 2) + 16 * q, c = 8 * (lane & 3);
+            const int r = (lane >> 2) + 16 * q;
             const f32x4 x0 = *reinterpret_cast<const f32x4*>(lw + gx_ex(r, c));
             const f32x4 x1 = *reinterpret_cast<const f32x4*>(lw + gx_ex(r, c + 4));
             const float rv[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
             const int64_t row = i0 + r;
             const int col = c0 + 32 * b + c;
-            if (row < d.D && col < d.rp) gx_adamw8(d, a, row, col, rv);
+            if (row < d.D && col < d.rp)
+                gx_adamw8(d, a, row, col, min(max(d.r - col, 0), 8), m[b][q], v[b][q], rv);
         }
         __builtin_amdgcn_wave_barrier();  // this block's gathers before the next block's spill
     }
@@ -87,18 +100,14 @@ __device__ __forceinline__ void zero_acc(f32x16 (&acc)[IB][2]) {
 
 // Any shape and alignment: the register-staged projection of galore.hip (64 rows of R x all r
 // columns per block, wave w columns 64 w .. 64 w + 63), U^T decoded into LDS.
+constexpr int kGxArena = (kGxFormRows[kGxAny] + kGaWide) * kGaPitch;
 template <bool Left>
-__global__ __launch_bounds__(kThreads, 3) void k_gx_project(GxTable t, GaArgs a) {
+__device__ __forceinline__ void gx_any_tile(const GxDesc& d, int64_t i0, const GaArgs& a, uint16_t* arena) {
     constexpr int kRows = kGxFormRows[kGxAny];
-    __shared__ __attribute__((aligned(16))) uint16_t arena[(kRows + kGaWide) * kGaPitch];
-    static_assert((kRows + kGaWide) * kGaPitch * 2 >= kWaves * kGxEx * 4, "exchange space");
+    static_assert(kGxArena * 2 >= kWaves * kGxEx * 4, "exchange space");
     uint16_t* sa = arena;
     uint16_t* sb = arena + kRows * kGaPitch;
-    const int2 it = t.items[blockIdx.x];
-    if (it.x < 0) return;
-    const GxDesc d = t.desc[it.x];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t i0 = static_cast<int64_t>(it.y) * kRows;
     const bool active = wave * 64 < d.r;
     f32x16 acc[2][2];
     zero_acc(acc);
@@ -139,84 +148,104 @@ __global__ __launch_bounds__(kThreads, 3) void k_gx_project(GxTable t, GaArgs a)
     for (int ib = 0; ib < 2; ++ib) gx_epilogue(d, a, acc[ib][0], acc[ib][1], i0 + ib * 32, wave * 64, lw, lane);
 }
 
-// d a multiple of 128, 16-byte rows of G and whole words of scales. 8 waves on 64 IB rows of R
-// x 256 columns: wave w at rows 32 IB (w / 4), columns 64 (w % 4). One contraction step is
-// 128 long: G's tile (256-byte pieces of its rows; left: 128 rows of 128 IB bytes), the codes of
-// U^T (64 bytes of each of its 256 rows) and their scales (a word each) go by
-// global_load_lds into one of three LDS stages, two steps ahead; the codes are decoded
-// as the fragments are read. Lane half h takes values 64 h .. 64 h + 63 of a step: two whole
-// MX blocks, so a lane's scale changes once per step.
+__global__ __launch_bounds__(kThreads, 3) void k_gx_project(GxTable t, GaArgs a, int nright) {
+    __shared__ __attribute__((aligned(16))) uint16_t arena[kGxArena];
+    const int2 it = t.items[blockIdx.x];
+    const GxDesc d = t.desc[it.x];
+    const int64_t i0 = static_cast<int64_t>(it.y) * kGxFormRows[kGxAny];
+    if (it.x < nright) gx_any_tile<false>(d, i0, a, arena);
+    else gx_any_tile<true>(d, i0, a, arena);
+}
+
+// d a multiple of 128, 16-byte rows of G and whole words of scales. 8 waves on 64 rows of R
+// x 256 columns: wave w at rows 32 (w / 4), columns 64 (w % 4). One contraction step is 128
+// long. Everything goes by global_load_lds, as in mx4_accumulate: waves 0 .. 3 fetch G's
+// tile (256-byte pieces of its rows; left: 128 rows of 128 bytes) into one of five stages,
+// four steps ahead, which keeps the 64 KB in flight that HBM takes per CU; waves 4 .. 7 the
+// codes of U^T of two steps (a whole 128-byte line of each of its 256 rows) and the
+// scales of four (a word per row and step) into one of two buffers each. (All waves
+// fetching all, two steps ahead, each step's codes and scales on their own: 84 us for
+// the four 4096 x 4096 matrices of a layer.) The codes are decoded as the fragments are read.
+// Lane half h takes values 64 h .. 64 h + 63 of a step: two whole MX blocks, so a lane's
+// scale changes once per step.
+constexpr int kGdRows = kGxFormRows[kGxDirect];
 constexpr int kGdStep = 128;
 constexpr int kGdWaves = 8;
+constexpr int kGdDepth = 5;
+constexpr int kGdG = kGdRows * kGdStep * 2;      // bytes of G per stage
+constexpr int kGdCodes = kGaWide * kGdStep;      // bytes of codes of two steps
+constexpr int kGdScales = kGaWide * 4 * 4;       // bytes of scales of four: [word][row]
+constexpr int kGdLds = kGdDepth * kGdG + 2 * kGdCodes + 2 * kGdScales;
 
-template <bool Left, int IB>
-__global__ __launch_bounds__(kGdWaves * 64) void k_gx_project_direct(GxTable t, GaArgs a) {
-    constexpr int kRows = 64 * IB;
-    constexpr int kAg = kRows * kGdStep * 2, kBc = kGaWide * kGdStep / 2;  // bytes of a stage's G and codes
-    constexpr int kStage = kAg + kBc + kGaWide * 4;
-    constexpr int kA = kAg / 1024 / kGdWaves, kB = kBc / 1024 / kGdWaves, kDma = kA + kB + 1;
-    __shared__ __attribute__((aligned(16))) uint8_t stages[3 * kStage];
-    static_assert(3 * kStage >= kGdWaves * kGxEx * 4, "exchange space");
-    const int2 it = t.items[blockIdx.x];
-    if (it.x < 0) return;
-    const GxDesc d = t.desc[it.x];
+template <bool Left>
+__device__ __forceinline__ void gx_direct_tile(const GxDesc& d, int64_t i0, const GaArgs& a, uint8_t* lds) {
+    constexpr int kA = kGdG / 1024 / 4, kB = kGdCodes / 1024 / 4;  // 1 KB transfers per wave of its kind
+    static_assert(kGdWaves == 8 && kGdDepth * kGdG >= kGdWaves * kGxEx * 4, "waves below; exchange space");
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
-    const int64_t i0 = static_cast<int64_t>(it.y) * kRows;
     const int cw = (wave & 3) * 64;   // the wave's first column of R
-    const int rw = (wave >> 2) * 32 * IB;
-    f32x16 acc[IB][2];
+    const int rw = (wave >> 2) * 32;
+    const bool fetch_g = wave < 4;
+    const int fw = wave & 3;
+    f32x16 acc[1][2];
     zero_acc(acc);
 
-    // Transfers. Right: transfer j holds rows 4 j + (l >> 4) of G's tile, 16-byte chunk
-    // (l & 15) ^ (row & 15). Left: rows of 128 IB bytes (64 IB columns of G), chunk
+    // G. Right: transfer j holds rows 4 j + (l >> 4) of the tile, 16-byte chunk
+    // (l & 15) ^ (row & 15). Left: rows 8 j + (l >> 3) of 128 bytes (64 columns of G), chunk
     // c ^ lsw(row & 3), so that the transposed reads of four rows (64 bytes each) meet 64 banks.
-    auto lsw = [](int e) { return IB == 2 ? e << 2 : (e >> 1) << 2; };
+    auto lsw = [](int e) { return (e >> 1) << 2; };
     const uint8_t* const g = reinterpret_cast<const uint8_t*>(d.g);
-    constexpr int kChunks = 8 * IB;                 // left: chunks per row
     int64_t ga[kA];
 #pragma unroll
     for (int i = 0; i < kA; ++i) {
-        const int j = wave + i * kGdWaves;
+        const int j = fw + i * 4;
         if constexpr (Left) {
-            const int p = j * 64 + lane, kr = p / kChunks, c = (p % kChunks) ^ lsw(kr & 3);
-            const int64_t col = min<int64_t>(i0 + c * 8, d.D - 8);
-            ga[i] = (static_cast<int64_t>(kr) * d.D + col) * 2;
+            const int kr = 8 * j + (lane >> 3), c = (lane & 7) ^ lsw(kr & 3);
+            ga[i] = (static_cast<int64_t>(kr) * d.D + min<int64_t>(i0 + c * 8, d.D - 8)) * 2;
         } else {
             const int r = 4 * j + (lane >> 4), c = (lane & 15) ^ (r & 15);
             ga[i] = (min<int64_t>(i0 + r, d.D - 1) * d.d + c * 8) * 2;
         }
     }
     const int64_t gstep = static_cast<int64_t>(kGdStep) * 2 * (Left ? d.D : 1);
-    // codes: transfer j holds rows 16 j + (l >> 2) of U^T, block (l & 3) ^ ((row >> 2) & 3)
-    uint32_t ub[kB];
-#pragma unroll
-    for (int i = 0; i < kB; ++i) {
-        const int r = 16 * (wave + i * kGdWaves) + (lane >> 2);
-        ub[i] = (static_cast<uint32_t>(min(r, d.r - 1)) * d.nb + ((lane & 3) ^ ((r >> 2) & 3))) * 16;
-    }
-    // scales: transfer j holds rows 64 j + l; waves 4 .. 7 repeat those of 0 .. 3
-    const uint32_t us = static_cast<uint32_t>(min(64 * (wave & 3) + lane, d.r - 1)) * d.nb;
     const int steps = d.d / kGdStep;
     auto stage = [&](int k, uint8_t* s) {
-        k = min(k, steps - 1);  // past the end: the last step again, for equal counts
-        const uint8_t* gk = g + k * gstep;
+        const uint8_t* gk = g + min(k, steps - 1) * gstep;  // past the end: the last again, for equal counts
 #pragma unroll
-        for (int i = 0; i < kA; ++i) dma16(gk + ga[i], s + (wave + i * kGdWaves) * 1024);
-#pragma unroll
-        for (int i = 0; i < kB; ++i) dma16(d.uc + (ub[i] + k * 64u), s + kAg + (wave + i * kGdWaves) * 1024);
-        dma4(d.us + (us + k * 4u), s + kAg + kBc + (wave & 3) * 256);
+        for (int i = 0; i < kA; ++i) dma16(gk + ga[i], s + (fw + i * 4) * 1024);
     };
-    const uint32_t base = lds_addr(stages);
-    auto multiply = [&](uint32_t s) {
+    // Codes: transfer j holds rows 8 j + (l >> 3) of U^T, block (l & 7) ^ mx_swz(row).
+    uint32_t ub[kB];
+    const int cblk = (lane & 7) ^ mx_swz(lane >> 3) ^ (fw & 1);
+#pragma unroll
+    for (int i = 0; i < kB; ++i)
+        ub[i] = static_cast<uint32_t>(min(8 * (fw + i * 4) + (lane >> 3), d.r - 1)) * d.nb;
+    uint8_t* const cbuf = lds + kGdDepth * kGdG;
+    auto codes = [&](int pair) {
+        const uint32_t kc = static_cast<uint32_t>(min(8 * pair + cblk, d.nb - 1));
+#pragma unroll
+        for (int i = 0; i < kB; ++i) dma16(d.uc + (ub[i] + kc) * 16, cbuf + (pair & 1) * kGdCodes + (fw + i * 4) * 1024);
+    };
+    // Scales: wave 4 + f fetches the words of rows 64 f + l.
+    const uint32_t us = static_cast<uint32_t>(min(64 * fw + lane, d.r - 1)) * d.nb;
+    uint8_t* const sbuf = cbuf + 2 * kGdCodes;
+    auto scales = [&](int quad) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            dma4(d.us + (us + static_cast<uint32_t>(min(16 * quad + 4 * w, d.nb - 4))),
+                 sbuf + (quad & 1) * kGdScales + w * (kGaWide * 4) + fw * 256);
+    };
+    const uint32_t base = lds_addr(lds);
+    auto multiply = [&](int k, int cur) {
+        const uint32_t s = base + cur * kGdG;
         // the two blocks of the lane's two columns of R, and their scales
-        const int r0 = cw + (lane & 31);
-        const uint32_t pb = s + kAg + r0 * 64, sw = (r0 >> 2) & 3;  // rows 32 on share sw
+        const int r0 = cw + (lane & 31), sw = mx_swz(lane & 31), b0 = 4 * (k & 1) + 2 * h;
+        const uint32_t pb = base + kGdDepth * kGdG + ((k >> 1) & 1) * kGdCodes + r0 * 128;
+        const uint32_t pe = base + kGdDepth * kGdG + 2 * kGdCodes + ((k >> 2) & 1) * kGdScales + (k & 3) * (kGaWide * 4) + r0 * 4;
         u32x4 c[4];
-        lds_read4(pb + (((2 * h) ^ sw) << 4), pb + (((2 * h + 1) ^ sw) << 4), pb + 2048 + (((2 * h) ^ sw) << 4),
-                  pb + 2048 + (((2 * h + 1) ^ sw) << 4), c);
-        uint32_t e[4];
-        lds_read_words(s + kAg + kBc + r0 * 4, s + kAg + kBc + r0 * 4 + 128, s + kAg + kBc + r0 * 4,
-                       s + kAg + kBc + r0 * 4 + 128, e);
+        lds_read4(pb + ((b0 ^ sw) << 4), pb + (((b0 + 1) ^ sw) << 4), pb + 4096 + ((b0 ^ sw) << 4),
+                  pb + 4096 + (((b0 + 1) ^ sw) << 4), c);
+        uint32_t e[2];
+        lds_read_words2(pe, pe + 128, e);
         float sc[2][2];  // [column][block]
 #pragma unroll
         for (int jb = 0; jb < 2; ++jb) {
@@ -225,88 +254,84 @@ __global__ __launch_bounds__(kGdWaves * 64) void k_gx_project_direct(GxTable t, 
             sc[jb][1] = mx4_scale((w >> 8) & 255u);
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {  // two 8-value sub-steps at a time
-            bfv8 fa[2][IB];
+        for (int q = 0; q < 2; ++q) {  // four 8-value sub-steps at a time, one block
+            bfv8 fa[4];
+            if constexpr (Left) {
+                const int gq = lane >> 4, eq = (lane >> 2) & 3;
+                const int col = rw + 16 * (gq & 1) + 4 * (lane & 3);
+                const int kr = 64 * h + 32 * q + eq;
+                const uint32_t p = s + kr * 128 + (((col >> 3) ^ lsw(eq)) << 4) + (col & 7) * 2;
+                u32x2 x[8];
+                lds_read_tr8(p, x);
 #pragma unroll
-            for (int ib = 0; ib < IB; ++ib) {
-                if constexpr (Left) {
-                    const int gq = lane >> 4, eq = (lane >> 2) & 3;
-                    const int col = rw + ib * 32 + 16 * (gq & 1) + 4 * (lane & 3);
-                    const int kr = 64 * h + 16 * q + eq;
-                    const uint32_t p = s + kr * (kChunks * 16) + (((col >> 3) ^ lsw(eq)) << 4) + (col & 7) * 2;
-                    constexpr uint32_t kFour = 4 * kChunks * 16;
-                    u32x2 x0, x1, x2, x3;
-                    __asm__ volatile(
-                        "ds_read_b64_tr_b16 %0, %4\n\t"
-                        "ds_read_b64_tr_b16 %1, %5\n\t"
-                        "ds_read_b64_tr_b16 %2, %6\n\t"
-                        "ds_read_b64_tr_b16 %3, %7\n\t"
-                        "s_waitcnt lgkmcnt(0)"
-                        : "=&v"(x0), "=&v"(x1), "=&v"(x2), "=&v"(x3)
-                        : "v"(p), "v"(p + kFour), "v"(p + 2 * kFour), "v"(p + 3 * kFour));
-                    fa[0][ib] = __builtin_bit_cast(bfv8, u32x4{x0.x, x0.y, x1.x, x1.y});
-                    fa[1][ib] = __builtin_bit_cast(bfv8, u32x4{x2.x, x2.y, x3.x, x3.y});
-                }
-            }
-            if constexpr (!Left) {
-                const int r = rw + (lane & 31);
-                const uint32_t p0 = s + r * 256 + (((8 * h + 2 * q) ^ (r & 15)) << 4);
-                const uint32_t p1 = s + r * 256 + (((8 * h + 2 * q + 1) ^ (r & 15)) << 4);
+                for (int u = 0; u < 4; ++u)
+                    fa[u] = __builtin_bit_cast(bfv8, u32x4{x[2 * u].x, x[2 * u].y, x[2 * u + 1].x, x[2 * u + 1].y});
+            } else {
+                const int r = rw + (lane & 31), b = 8 * h + 4 * q;
+                const uint32_t p = s + r * 256;
                 u32x4 x[4];
-                if constexpr (IB == 2) {
-                    lds_read4(p0, p0 + 8192, p1, p1 + 8192, x);
-                    fa[0][0] = __builtin_bit_cast(bfv8, x[0]);
-                    fa[0][1] = __builtin_bit_cast(bfv8, x[1]);
-                    fa[1][0] = __builtin_bit_cast(bfv8, x[2]);
-                    fa[1][1] = __builtin_bit_cast(bfv8, x[3]);
-                } else {
-                    lds_read2(p0, p1, x);
-                    fa[0][0] = __builtin_bit_cast(bfv8, x[0]);
-                    fa[1][0] = __builtin_bit_cast(bfv8, x[1]);
-                }
+                lds_read4(p + ((b ^ (r & 15)) << 4), p + (((b + 1) ^ (r & 15)) << 4), p + (((b + 2) ^ (r & 15)) << 4),
+                          p + (((b + 3) ^ (r & 15)) << 4), x);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) fa[u] = __builtin_bit_cast(bfv8, x[u]);
             }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int sub = 2 * q + u;  // 8 values: dword sub & 3 of block sub >> 2
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
                 for (int jb = 0; jb < 2; ++jb) {
-                    const bfv8 fb = __builtin_bit_cast(bfv8, mx4_to_bf16(c[2 * jb + (sub >> 2)][sub & 3], sc[jb][sub >> 2]));
-#pragma unroll
-                    for (int ib = 0; ib < IB; ++ib) acc[ib][jb] = mfma32(fa[u][ib], fb, acc[ib][jb]);
+                    const bfv8 fb = __builtin_bit_cast(bfv8, mx4_to_bf16(c[2 * jb + q][u], sc[jb][q]));
+                    acc[0][jb] = mfma32(fa[u], fb, acc[0][jb]);
                 }
-            }
         }
     };
+    // Before step k's barrier a wave that fetches G waits until only steps k + 1 .. k + 3 are
+    // outstanding. One that fetches U^T issued the codes of a pair of steps in the even step
+    // before it and the scales of four steps two steps before them: before an even step it
+    // waits for all, before an odd one for nothing that step k - 1 issued. What a step fills
+    // was last read before its barrier.
     const bool active = cw < d.r;
-    stage(0, stages);
-    stage(1, stages + kStage);
+    if (fetch_g) {
+#pragma unroll
+        for (int k = 0; k < kGdDepth - 1; ++k) stage(k, lds + k * kGdG);
+    } else {
+        scales(0);
+        codes(0);
+    }
     int cur = 0;
     for (int k = 0; k < steps; ++k) {
-        wait_and_sync<kDma>();
-        stage(k + 2, stages + (cur == 0 ? 2 : cur - 1) * kStage);
-        if (active) multiply(base + cur * kStage);
-        cur = cur == 2 ? 0 : cur + 1;
+        if (fetch_g) wait_and_sync<3 * kA>();
+        else if (!(k & 1)) wait_and_sync<0>();
+        else if ((k & 3) == 3) wait_and_sync<kB + 4>();
+        else wait_and_sync<kB>();
+        if (fetch_g) {
+            stage(k + kGdDepth - 1, lds + (cur == 0 ? kGdDepth - 1 : cur - 1) * kGdG);
+        } else if (!(k & 1)) {
+            if ((k & 3) == 2) scales((k >> 2) + 1);
+            codes((k >> 1) + 1);
+        }
+        if (active) multiply(k, cur);
+        cur = cur == kGdDepth - 1 ? 0 : cur + 1;
     }
     wait_and_sync<0>();
     if (!active) return;
-    float* lw = reinterpret_cast<float*>(stages) + wave * kGxEx;
-#pragma unroll
-    for (int ib = 0; ib < IB; ++ib) gx_epilogue(d, a, acc[ib][0], acc[ib][1], i0 + rw + ib * 32, cw, lw, lane);
+    float* lw = reinterpret_cast<float*>(lds) + wave * kGxEx;
+    gx_epilogue(d, a, acc[0][0], acc[0][1], i0 + rw, cw, lw, lane);
 }
 
-void launch_gx_project(const GxTable& t, int64_t n, const GaArgs& a, bool left, int form, hipStream_t s) {
+__global__ __launch_bounds__(kGdWaves * 64) void k_gx_project_direct(GxTable t, GaArgs a, int nright) {
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kGdLds];
+    const int2 it = t.items[blockIdx.x];
+    const GxDesc d = t.desc[it.x];
+    const int64_t i0 = static_cast<int64_t>(it.y) * kGdRows;
+    if (it.x < nright) gx_direct_tile<false>(d, i0, a, lds);
+    else gx_direct_tile<true>(d, i0, a, lds);
+}
+
+void launch_gx_project(const GxTable& t, int64_t n, int nright, const GaArgs& a, int form, hipStream_t s) {
     if (n <= 0) return;
     const dim3 grid(static_cast<uint32_t>(n)), wide(kGdWaves * 64);
-    if (form == kGxAny) {
-        if (left) hipLaunchKernelGGL(k_gx_project<true>, grid, dim3(kThreads), 0, s, t, a);
-        else hipLaunchKernelGGL(k_gx_project<false>, grid, dim3(kThreads), 0, s, t, a);
-    } else if (form == kGxDirect) {
-        if (left) hipLaunchKernelGGL((k_gx_project_direct<true, 1>), grid, wide, 0, s, t, a);
-        else hipLaunchKernelGGL((k_gx_project_direct<false, 1>), grid, wide, 0, s, t, a);
-    } else {
-        if (left) hipLaunchKernelGGL((k_gx_project_direct<true, 2>), grid, wide, 0, s, t, a);
-        else hipLaunchKernelGGL((k_gx_project_direct<false, 2>), grid, wide, 0, s, t, a);
-    }
+    if (form == kGxAny) hipLaunchKernelGGL(k_gx_project, grid, dim3(kThreads), 0, s, t, a, nright);
+    else hipLaunchKernelGGL(k_gx_project_direct, grid, wide, 0, s, t, a, nright);
 }
 
 // ------------------------------------------------------------------ MX4 gradient
@@ -316,20 +341,19 @@ template <int IB, int WN, int NW, bool Any>
 __global__ __launch_bounds__(NW * 64) void k_gx_project_mx4(GxTable t, GaArgs a) {
     using T = MxTile<IB, WN, NW>;
     constexpr int kEx = NW * kGxEx * 4;
-    __shared__ __attribute__((aligned(16))) uint8_t stages[Any ? kEx : 3 * T::kStage];
-    static_assert(3 * T::kStage >= kEx, "exchange space");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[Any ? kEx : T::kLds];
+    static_assert(T::kLds >= kEx, "exchange space");
     const int2 it = t.items[blockIdx.x];
-    if (it.x < 0) return;
     const GxDesc d = t.desc[it.x];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int64_t i0 = static_cast<int64_t>(it.y) * T::kRowsA;
     const MxOperand oa{reinterpret_cast<const uint8_t*>(d.g), d.gs, d.D, d.nb}, ob{d.uc, d.us, d.r, d.nb};
-    float* lw = reinterpret_cast<float*>(stages) + wave * kGxEx;
+    float* lw = reinterpret_cast<float*>(lds) + wave * kGxEx;
     for (int c0 = 0; c0 < d.r; c0 += T::kRowsB) {
         f32x16 acc[IB][2];
         zero_acc(acc);
         if constexpr (Any) mx4_accumulate_any(oa, ob, i0, c0, acc);
-        else mx4_accumulate<IB, WN, NW>(oa, ob, i0, c0, stages, acc);
+        else mx4_accumulate<IB, WN, NW>(oa, ob, i0, c0, lds, acc);
         const int64_t row = i0 + (wave / WN) * 32 * IB;
         const int col = c0 + (wave % WN) * 64;
         if (col < d.r)

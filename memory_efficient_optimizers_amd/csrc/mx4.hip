@@ -95,13 +95,14 @@ __global__ __launch_bounds__(kMxRowThreads) void k_mx4_dequantize_rows(MxBatch b
 
 namespace {
 
-// Two adjacent values of a row of the data, zero where out of range.
-template <bool BF>
+// Two adjacent values of a row of the data: Whole, one aligned access; else the `valid` first
+// of them, zero where out of range.
+template <bool BF, bool Whole>
 __device__ __forceinline__ void load_pair(const MxMat& m, int64_t row, int64_t col, int valid, float& x, float& y) {
     const int64_t i = row * m.ld + col;
     if (BF) {
         const uint16_t* p = static_cast<const uint16_t*>(m.data) + i;
-        if (m.vec && valid == 2) {
+        if constexpr (Whole) {
             const uint32_t w = *gld<uint32_t>(p);
             x = bf16_lo(w);
             y = bf16_hi(w);
@@ -111,7 +112,7 @@ __device__ __forceinline__ void load_pair(const MxMat& m, int64_t row, int64_t c
         }
     } else {
         const float* p = static_cast<const float*>(m.data) + i;
-        if (m.vec && valid == 2) {
+        if constexpr (Whole) {
             const f32x2 w = *gld<f32x2>(p);
             x = w.x;
             y = w.y;
@@ -135,10 +136,15 @@ __device__ __forceinline__ void quantize_cols(const MxMat& m, uint32_t tile, uin
     const int64_t row = r0 + 2 * lane, kb = k0 + wave;
     const int valid = static_cast<int>(min<int64_t>(max<int64_t>(m.rows - row, 0), 2));
     float x[kMxBlock], y[kMxBlock];
+    if (m.vec && r0 + kMxColRows <= m.rows && (k0 + kMxColBlocks) * kMxBlock <= m.cols) {
 #pragma unroll
-    for (int i = 0; i < kMxBlock; ++i) {
-        const int64_t k = kb * kMxBlock + i;
-        load_pair<BF>(m, k, row, k < m.cols ? valid : 0, x[i], y[i]);
+        for (int i = 0; i < kMxBlock; ++i) load_pair<BF, true>(m, kb * kMxBlock + i, row, 2, x[i], y[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kMxBlock; ++i) {
+            const int64_t k = kb * kMxBlock + i;
+            load_pair<BF, false>(m, k, row, k < m.cols ? valid : 0, x[i], y[i]);
+        }
     }
     uint32_t ax = 0, ay = 0;
 #pragma unroll
@@ -281,7 +287,7 @@ __device__ __forceinline__ void mx4_store(const MxProd& p, int64_t i0, int64_t j
 template <int IB, int WN, int NW, bool Any>
 __global__ __launch_bounds__(NW * 64) void k_mx4_matmul(MxProdBatch b) {
     using T = MxTile<IB, WN, NW>;
-    __shared__ __attribute__((aligned(16))) uint8_t stages[Any ? 16 : 3 * T::kStage];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[Any ? 16 : T::kLds];
     int i = 0;
     while (i + 1 < b.n && blockIdx.x >= b.p[i + 1].first) ++i;
     const MxProd& p = b.p[i];
@@ -298,7 +304,7 @@ __global__ __launch_bounds__(NW * 64) void k_mx4_matmul(MxProdBatch b) {
             for (int v = 0; v < 16; ++v) acc[ib][jb][v] = 0.0f;
     const MxOperand oa{p.ac, p.as, p.m, static_cast<int32_t>(p.nb)}, ob{p.bc, p.bs, p.n, static_cast<int32_t>(p.nb)};
     if constexpr (Any) mx4_accumulate_any(oa, ob, i0, j0, acc);
-    else mx4_accumulate<IB, WN, NW>(oa, ob, i0, j0, stages, acc);
+    else mx4_accumulate<IB, WN, NW>(oa, ob, i0, j0, lds, acc);
     i0 += (wave / WN) * 32 * IB;
     j0 += (wave % WN) * 64;
     if (p.cbf16) mx4_store<IB, true>(p, i0, j0, lane, acc);

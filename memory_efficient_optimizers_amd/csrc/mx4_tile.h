@@ -47,17 +47,6 @@ __device__ __forceinline__ void lds_read4(uint32_t a0, uint32_t a1, uint32_t a2,
     v[0] = v0; v[1] = v1; v[2] = v2; v[3] = v3;
 }
 
-__device__ __forceinline__ void lds_read2(uint32_t a0, uint32_t a1, u32x4* v) {
-    u32x4 v0, v1;
-    __asm__ volatile(
-        "ds_read_b128 %0, %2\n\t"
-        "ds_read_b128 %1, %3\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(v0), "=&v"(v1)
-        : "v"(a0), "v"(a1));
-    v[0] = v0; v[1] = v1;
-}
-
 __device__ __forceinline__ void lds_read_words(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t* w) {
     uint32_t w0, w1, w2, w3;
     __asm__ volatile(
@@ -69,6 +58,35 @@ __device__ __forceinline__ void lds_read_words(uint32_t a0, uint32_t a1, uint32_
         : "=&v"(w0), "=&v"(w1), "=&v"(w2), "=&v"(w3)
         : "v"(a0), "v"(a1), "v"(a2), "v"(a3));
     w[0] = w0; w[1] = w1; w[2] = w2; w[3] = w3;
+}
+
+__device__ __forceinline__ void lds_read_words2(uint32_t a0, uint32_t a1, uint32_t* w) {
+    uint32_t w0, w1;
+    __asm__ volatile(
+        "ds_read_b32 %0, %2\n\t"
+        "ds_read_b32 %1, %3\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(w0), "=&v"(w1)
+        : "v"(a0), "v"(a1));
+    w[0] = w0; w[1] = w1;
+}
+
+// Eight transposed 8-byte reads of 16-bit values, 4 rows of 128 bytes apart each.
+__device__ __forceinline__ void lds_read_tr8(uint32_t p, u32x2* v) {
+    u32x2 v0, v1, v2, v3, v4, v5, v6, v7;
+    __asm__ volatile(
+        "ds_read_b64_tr_b16 %0, %8\n\t"
+        "ds_read_b64_tr_b16 %1, %8 offset:512\n\t"
+        "ds_read_b64_tr_b16 %2, %8 offset:1024\n\t"
+        "ds_read_b64_tr_b16 %3, %8 offset:1536\n\t"
+        "ds_read_b64_tr_b16 %4, %8 offset:2048\n\t"
+        "ds_read_b64_tr_b16 %5, %8 offset:2560\n\t"
+        "ds_read_b64_tr_b16 %6, %8 offset:3072\n\t"
+        "ds_read_b64_tr_b16 %7, %8 offset:3584\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v0), "=&v"(v1), "=&v"(v2), "=&v"(v3), "=&v"(v4), "=&v"(v5), "=&v"(v6), "=&v"(v7)
+        : "v"(p));
+    v[0] = v0; v[1] = v1; v[2] = v2; v[3] = v3; v[4] = v4; v[5] = v5; v[6] = v6; v[7] = v7;
 }
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
@@ -90,84 +108,96 @@ __device__ __forceinline__ int mx_swz(int r) { return (r & 7) ^ ((r >> 3) & 1); 
 constexpr int kMxStep = 8;  // MX blocks (256 values) per contraction step
 
 // The tile of a block: NW waves, WN along B's rows (64 each) and NW / WN along A's (32 IB
-// each). acc: the wave's 32 IB x 64 part of C.
+// each). acc: the wave's 32 IB x 64 part of C. LDS: five stages of A (the codes of kMxStep
+// blocks of every row), two of B, two buffers of both operands' scales of two steps (4
+// words, [word][row]).
 template <int IB, int WN, int NW>
 struct MxTile {
     static constexpr int kRowsA = 32 * IB * NW / WN;
     static constexpr int kRowsB = 64 * WN;
-    // one LDS stage: the codes of kMxStep blocks of every row of A, then of B, then the scales
-    static constexpr int kScales = (kRowsA + kRowsB) * 128;
-    static constexpr int kStage = kScales + (kRowsA + kRowsB) * 8;
+    static constexpr int kRows = kRowsA + kRowsB;
+    static constexpr int kDepth = 5;
+    static constexpr int kStageA = kRowsA * 128, kStageB = kRowsB * 128;
+    static constexpr int kScales = 4 * kRows * 4;
+    static constexpr int kLds = kDepth * kStageA + 2 * kStageB + 2 * kScales;
 };
 
 // acc += A B^T over the whole contraction; nb a multiple of 4 and the scales 4-byte aligned.
-// Codes and scales of both operands go by global_load_lds into one of three LDS stages, two
-// steps ahead, so that nothing in the loop waits for a register load. Lane half h takes
-// blocks 4 h .. 4 h + 3 of a step: its codes are 64 contiguous bytes and its scales one
-// word (the order of the contraction is free as long as both operands agree).
+// Codes and scales of both operands go by global_load_lds into LDS, so that nothing in the
+// loop waits for a register load. A wave's transfers land in order, so one that fetched both
+// operands could keep A, which comes from HBM, no further ahead than B, which every block
+// reads from L2 and whose stages are the larger: half of the waves fetch A, four steps
+// ahead (64 KB in flight per CU in the 128-row tile; with 32 KB and one kind of wave the
+// product of a 32000 x 4096 gradient with a rank-256 projector took 33 us), the others B, one
+// step ahead, and the scales of two steps at a time (8 bytes per row and step:
+// fetched singly they cost the L2 as many requests as the codes).
+// Lane half h takes blocks 4 h .. 4 h + 3 of a step: its codes are 64 contiguous bytes and
+// its scales one word (the order of the contraction is free as long as both operands agree).
 // Rows past an operand's end repeat its last one (they reach outputs that are not stored);
 // in a last step of 4 blocks, lane half 1 multiplies zero codes under scales of 1.
 // Offsets within the tile's rows of an operand are 32 bits (kMxMaxK).
 template <int IB, int WN, int NW>
 __device__ __forceinline__ void mx4_accumulate(const MxOperand& a, const MxOperand& b, int64_t i0, int64_t j0,
-                                               uint8_t* stages, f32x16 (&acc)[IB][2]) {
+                                               uint8_t* lds, f32x16 (&acc)[IB][2]) {
     using T = MxTile<IB, WN, NW>;
-    constexpr int kA = T::kRowsA / 8 / NW, kB = T::kRowsB / 8 / NW;  // 1 KB transfers per wave: 8 rows each
-    constexpr int kS = (T::kRowsA / 32 + NW - 1) / NW, kT = (T::kRowsB / 32 + NW - 1) / NW;  // 32 rows' scales each
-    constexpr int kDma = kA + kB + kS + kT;
-    static_assert(kA * 8 * NW == T::kRowsA && kB * 8 * NW == T::kRowsB, "whole transfers");
+    constexpr int kHalf = NW / 2;  // waves of each kind
+    constexpr int kA = T::kRowsA / 8 / kHalf, kB = T::kRowsB / 8 / kHalf;  // 1 KB transfers per wave: 8 rows each
+    constexpr int kGroups = T::kRows / 64;  // of 64 rows, for the scales
+    static_assert(kA * 8 * kHalf == T::kRowsA && kB * 8 * kHalf == T::kRowsB && T::kRowsA % 64 == 0, "whole transfers");
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
+    const bool fetch_a = wave < kHalf;
+    const int fw = fetch_a ? wave : wave - kHalf;  // its number among its kind
     const int nb = a.nb;
-    const uint8_t* const ac = uniform(a.codes + i0 * nb * 16);
-    const uint8_t* const bc = uniform(b.codes + j0 * nb * 16);
-    const uint8_t* const as = uniform(a.scales + i0 * nb);
-    const uint8_t* const bs = uniform(b.scales + j0 * nb);
     const uint32_t ra = uniform(static_cast<int>(min<int64_t>(a.rows - i0, T::kRowsA))) - 1;  // last valid row
     const uint32_t rb = uniform(static_cast<int>(min<int64_t>(b.rows - j0, T::kRowsB))) - 1;
-    // Row offsets (in blocks) of the wave's transfers; wave w's i-th is transfer w + i NW.
-    uint32_t oa[kA], ob[kB], sa[kS], sb[kT];
-    auto row_of = [&](int i) { return static_cast<uint32_t>(8 * (wave + i * NW) + (lane >> 3)); };
-    const int chunk = (lane & 7) ^ mx_swz(lane >> 3);  // rows 8 j + (l >> 3): odd j flips one bit
-    const int odd = wave & 1;                          // NW is even: the parity of j is the wave's
-    const int cblk = chunk ^ odd;
+    uint8_t* const ldsb = lds + T::kDepth * T::kStageA;
+    uint8_t* const ldss = ldsb + 2 * T::kStageB;
+    // The wave's i-th transfer of codes is transfer fw + i kHalf of its operand: 8 rows of 8
+    // chunks. op: row offsets in blocks.
+    constexpr int kMost = kA > kB ? kA : kB;
+    const uint8_t* const cp = uniform(fetch_a ? a.codes + i0 * nb * 16 : b.codes + j0 * nb * 16);
+    uint32_t op[kMost];
+    static_assert(kHalf % 2 == 0, "the swizzle of a transfer's rows follows its wave");
+    const int cblk = (lane & 7) ^ mx_swz(lane >> 3) ^ (fw & 1);  // mx_swz of the row
 #pragma unroll
-    for (int i = 0; i < kA; ++i) oa[i] = min(row_of(i), ra) * static_cast<uint32_t>(nb);
+    for (int i = 0; i < kMost; ++i)
+        op[i] = min<uint32_t>(8 * (fw + i * kHalf) + (lane >> 3), fetch_a ? ra : rb) * static_cast<uint32_t>(nb);
+    auto codes = [&](int k, uint8_t* s, auto count) {
+        const uint32_t kc = static_cast<uint32_t>(min(k * kMxStep + cblk, nb - 1));
 #pragma unroll
-    for (int i = 0; i < kB; ++i) ob[i] = min(row_of(i), rb) * static_cast<uint32_t>(nb);
-    // scales: transfer j holds rows 32 j + (l >> 1), word l & 1; past the last transfer a wave
-    // repeats one, so that every wave has the same number in flight
+        for (int i = 0; i < decltype(count)::value; ++i) dma16(cp + (op[i] + kc) * 16, s + (fw + i * kHalf) * 1024);
+    };
+    using CA = std::integral_constant<int, kA>;
+    using CB = std::integral_constant<int, kB>;
+    // Scales: group g is rows 64 g .. 64 g + 63 of [A; B], one word of every row per transfer.
+    auto scales = [&](int pair) {
+        for (int g = fw; g < kGroups; g += kHalf) {
+            const bool ga = g < T::kRowsA / 64;
+            const uint8_t* p = ga ? a.scales + i0 * nb : b.scales + j0 * nb;
+            const uint32_t o = (ga ? min<uint32_t>(64 * g + lane, ra) : min<uint32_t>(64 * g - T::kRowsA + lane, rb)) *
+                               static_cast<uint32_t>(nb);
+            uint8_t* s = ldss + (pair & 1) * T::kScales + g * 256;
 #pragma unroll
-    for (int i = 0; i < kS; ++i)
-        sa[i] = min<uint32_t>(32 * ((wave + i * NW) % (T::kRowsA / 32)) + (lane >> 1), ra) * static_cast<uint32_t>(nb);
-#pragma unroll
-    for (int i = 0; i < kT; ++i)
-        sb[i] = min<uint32_t>(32 * ((wave + i * NW) % (T::kRowsB / 32)) + (lane >> 1), rb) * static_cast<uint32_t>(nb);
-    auto stage = [&](int k0, uint8_t* s) {
-        const uint32_t kc = static_cast<uint32_t>(min(k0 + cblk, nb - 1));
-        const uint32_t ks = static_cast<uint32_t>(min(k0 + 4 * (lane & 1), nb - 4));
-#pragma unroll
-        for (int i = 0; i < kA; ++i) dma16(ac + (oa[i] + kc) * 16, s + (wave + i * NW) * 1024);
-#pragma unroll
-        for (int i = 0; i < kB; ++i) dma16(bc + (ob[i] + kc) * 16, s + T::kRowsA * 128 + (wave + i * NW) * 1024);
-#pragma unroll
-        for (int i = 0; i < kS; ++i) dma4(as + (sa[i] + ks), s + T::kScales + ((wave + i * NW) % (T::kRowsA / 32)) * 256);
-#pragma unroll
-        for (int i = 0; i < kT; ++i)
-            dma4(bs + (sb[i] + ks), s + T::kScales + T::kRowsA * 8 + ((wave + i * NW) % (T::kRowsB / 32)) * 256);
+            for (int w = 0; w < 4; ++w)
+                dma4(p + (o + static_cast<uint32_t>(min(16 * pair + 4 * w, nb - 4))), s + w * T::kRows * 4);
+        }
     };
     const int wr = (wave / WN) * 32 * IB + (lane & 31), wc = (wave % WN) * 64 + (lane & 31);  // the lane's rows
     const int sw = mx_swz(lane & 31);  // rows 32 apart share it
-    const uint32_t base = lds_addr(stages);
-    auto multiply = [&](int k0, uint32_t s) {
-        const uint32_t pa = s + wr * 128, pb = s + (T::kRowsA + wc) * 128;
-        const uint32_t qa = s + T::kScales + wr * 8 + 4 * h, qb = s + T::kScales + (T::kRowsA + wc) * 8 + 4 * h;
+    const uint32_t base = lds_addr(lds);
+    auto multiply = [&](int k, int cur) {
+        const uint32_t pa = base + cur * T::kStageA + wr * 128;
+        const uint32_t pb = base + T::kDepth * T::kStageA + (k & 1) * T::kStageB + wc * 128;
+        const uint32_t q = base + T::kDepth * T::kStageA + 2 * T::kStageB + ((k >> 1) & 1) * T::kScales +
+                           (2 * (k & 1) + h) * (T::kRows * 4);
+        const uint32_t qa = q + wr * 4, qb = q + (T::kRowsA + wc) * 4;
         auto at = [&](int t) { return static_cast<uint32_t>(((4 * h + t) ^ sw) << 4); };
         uint32_t e[4];  // scales: A's one or two rows, B's two
-        lds_read_words(qa, qa + (IB - 1) * 256, qb, qb + 256, e);
+        lds_read_words(qa, qa + (IB - 1) * 128, qb, qb + 128, e);
         u32x4 cb[2][4];
         lds_read4(pb + at(0), pb + at(1), pb + at(2), pb + at(3), cb[0]);
         lds_read4(pb + 4096 + at(0), pb + 4096 + at(1), pb + 4096 + at(2), pb + 4096 + at(3), cb[1]);
-        if (k0 + kMxStep > nb) {
+        if ((k + 1) * kMxStep > nb) {
 #pragma unroll
             for (int jb = 0; jb < 2; ++jb)
 #pragma unroll
@@ -190,18 +220,31 @@ __device__ __forceinline__ void mx4_accumulate(const MxOperand& a, const MxOpera
             }
         }
     };
-    // Step k: its stage has landed once only the next stage's transfers are outstanding; the
-    // stage that the new transfers fill was read in step k - 1, before the barrier.
+    // Before step k's barrier a wave that fetches A waits until only steps k + 1 .. k + 3 are
+    // outstanding, one that fetches B for all it issued (step k and the pair's scales). The
+    // stages that step k fills, A's of step k + 4 and B's of k + 1, were last read in step
+    // k - 1, the scales' buffer in the pair before. Past the end the last blocks are fetched
+    // again, for equal counts.
     const int steps = (nb + kMxStep - 1) / kMxStep;
-    stage(0, stages);
-    stage(kMxStep, stages + T::kStage);
+    if (fetch_a) {
+#pragma unroll
+        for (int k = 0; k < T::kDepth - 1; ++k) codes(k, lds + k * T::kStageA, CA{});
+    } else {
+        scales(0);
+        codes(0, ldsb, CB{});
+    }
     int cur = 0;
     for (int k = 0; k < steps; ++k) {
-        wait_and_sync<kDma>();
-        const int next = cur == 0 ? 2 : cur - 1;
-        stage((k + 2) * kMxStep, stages + next * T::kStage);
-        multiply(k * kMxStep, base + cur * T::kStage);
-        cur = cur == 2 ? 0 : cur + 1;
+        if (fetch_a) wait_and_sync<3 * kA>();
+        else wait_and_sync<0>();
+        if (fetch_a) {
+            codes(k + T::kDepth - 1, lds + (cur == 0 ? T::kDepth - 1 : cur - 1) * T::kStageA, CA{});
+        } else {
+            if (k & 1) scales((k + 1) >> 1);
+            codes(k + 1, ldsb + ((k + 1) & 1) * T::kStageB, CB{});
+        }
+        multiply(k, cur);
+        cur = cur == T::kDepth - 1 ? 0 : cur + 1;
     }
     wait_and_sync<0>();  // transfers past the end have landed before the stages are reused
 }
