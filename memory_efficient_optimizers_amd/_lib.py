@@ -295,8 +295,8 @@ def _tensors(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], stat
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # torch.cuda.current_stream().cuda_stream without the Stream object (2.6 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -833,9 +833,12 @@ class MX4Tensor:
 
     @classmethod
     def empty(cls, rows: int, cols: int, device) -> "MX4Tensor":
-        blocks = -(-int(cols) // MX4_BLOCK)
-        return cls(torch.empty((rows, 16 * blocks), dtype=torch.uint8, device=device),
-                   torch.empty((rows, blocks), dtype=torch.uint8, device=device), cols)
+        blocks = -(-cols // MX4_BLOCK)
+        q = cls.__new__(cls)  # the fields are right by construction
+        q.codes = torch.empty((rows, 16 * blocks), dtype=torch.uint8, device=device)
+        q.scales = torch.empty((rows, blocks), dtype=torch.uint8, device=device)
+        q.cols = cols
+        return q
 
     @property
     def shape(self):
@@ -846,36 +849,51 @@ class MX4Tensor:
         return self.codes.device
 
 
+def _row_stride(t: torch.Tensor, what: str) -> int:
+    """Elements between the rows of a row-major matrix (rows may be strided)."""
+    n, m = t.shape
+    if t.is_contiguous():
+        return m if m > 0 else 1
+    ld = t.stride(0) if n > 1 else max(m, 1)
+    if t.numel() and ((m > 1 and t.stride(1) != 1) or ld < m):
+        raise ValueError(f"{what} must be row-major (rows may be strided)")
+    return max(ld, m)
+
+
+def _mx4_matrix(v: torch.Tensor, q: MX4Tensor, transposed: bool) -> meo_mx4_matrix:
+    dtype = _DTYPE.get(v.dtype)
+    if dtype is None:
+        raise TypeError("values must be float32 or bfloat16")
+    rows, cols = q.codes.shape[0], q.cols
+    if v.shape != ((cols, rows) if transposed else (rows, cols)):
+        raise ValueError(f"values of shape {tuple(v.shape)} for an MX4 matrix of {rows} x {cols}"
+                         + (", transposed" if transposed else ""))
+    if v.device != q.codes.device:
+        raise ValueError("values and MX4 tensors must be on one device")
+    return meo_mx4_matrix(v.data_ptr(), q.codes.data_ptr(), q.scales.data_ptr(), rows, cols, _row_stride(v, "values"),
+                          dtype, 0)
+
+
 def _mx4_matrices(values: Sequence[torch.Tensor], mx: Sequence[MX4Tensor], transposed: bool):
     if len(values) != len(mx):
         raise ValueError("values and MX4 tensors differ in length")
+    if len(mx) == 1:
+        return ctypes.byref(_mx4_matrix(values[0], mx[0], transposed))
     arr = (meo_mx4_matrix * max(len(mx), 1))()
     for i, (v, q) in enumerate(zip(values, mx)):
-        if v.dtype not in _DTYPE:
-            raise TypeError("values must be float32 or bfloat16")
-        rows, cols = q.shape
-        want = (cols, rows) if transposed else (rows, cols)
-        if tuple(v.shape) != want:
-            raise ValueError(f"values of shape {tuple(v.shape)}, expected {want}")
-        if v.device != q.device:
-            raise ValueError("values and MX4 tensors must be on one device")
-        ld = v.stride(0) if v.shape[0] > 1 else max(v.shape[1], 1)
-        if v.numel() and ((v.shape[1] > 1 and v.stride(1) != 1) or ld < v.shape[1]):
-            raise ValueError("values must be row-major (rows may be strided)")
-        arr[i] = meo_mx4_matrix(v.data_ptr(), q.codes.data_ptr(), q.scales.data_ptr(), rows, cols,
-                                max(ld, v.shape[1]), _DTYPE[v.dtype], 0)
+        arr[i] = _mx4_matrix(v, q, transposed)
     return arr
 
 
 def meo_mx4_quantize(values, mx, transposed: bool = False, stream=None) -> None:
     """Each of ``values`` into the MX4Tensor of ``mx`` beside it."""
-    _check(load().meo_mx4_quantize(len(mx), _mx4_matrices(values, mx, transposed), int(bool(transposed)),
+    _check(load().meo_mx4_quantize(len(mx), _mx4_matrices(values, mx, transposed), 1 if transposed else 0,
                                    _stream(stream)))
 
 
 def meo_mx4_dequantize(values, mx, transposed: bool = False, stream=None) -> None:
     """Writes each of ``values`` from the MX4Tensor of ``mx`` beside it."""
-    _check(load().meo_mx4_dequantize(len(mx), _mx4_matrices(values, mx, transposed), int(bool(transposed)),
+    _check(load().meo_mx4_dequantize(len(mx), _mx4_matrices(values, mx, transposed), 1 if transposed else 0,
                                      _stream(stream)))
 
 
@@ -886,23 +904,22 @@ def meo_mx4_matmul(a, b, c, stream=None) -> None:
     arr = (meo_mx4_product * max(len(c), 1))()
     for i, (x, y, z) in enumerate(zip(a, b, c)):
         (m, k), (n, k2) = x.shape, y.shape
-        if k != k2 or tuple(z.shape) != (m, n):
+        if k != k2 or z.shape != (m, n):
             raise ValueError(f"product of {x.shape} and {y.shape} transposed into {tuple(z.shape)}")
-        if z.dtype not in _DTYPE:
+        dtype = _DTYPE.get(z.dtype)
+        if dtype is None:
             raise TypeError("outputs must be float32 or bfloat16")
         if not x.device == y.device == z.device:
             raise ValueError("operands and output must be on one device")
-        ld = z.stride(0) if m > 1 else max(n, 1)
-        if z.numel() and ((n > 1 and z.stride(1) != 1) or ld < n):
-            raise ValueError("outputs must be row-major (rows may be strided)")
         arr[i] = meo_mx4_product(x.codes.data_ptr(), x.scales.data_ptr(), y.codes.data_ptr(), y.scales.data_ptr(),
-                                 z.data_ptr(), m, n, k, max(ld, n), _DTYPE[z.dtype], 0)
+                                 z.data_ptr(), m, n, k, _row_stride(z, "outputs"), dtype, 0)
     _check(load().meo_mx4_matmul(len(c), arr, _stream(stream)))
 
 
 # ----------------------------------------------------------------------------- GaLore, MX4 projector
 
 GALORE_MX4_KEYS = ["exp_avg", "exp_avg_sq", "projector", "projector_scale"]
+_MOMENTS = ("exp_avg", "exp_avg_sq")
 
 
 def _galore_mx4_args(hp, params, grads, states):
@@ -911,33 +928,42 @@ def _galore_mx4_args(hp, params, grads, states):
         raise ValueError("params, grads and states differ in length")
     tensors = (meo_tensor * max(len(params), 1))()
     arr = (meo_galore_mx4_state * max(len(states), 1))()
+    std, rank = hp.proj_type == MEO_GALORE_STD, hp.rank
     for i, (p, g, st) in enumerate(zip(params, grads, states)):
-        right = p.dim() == 2 and (p.shape[0] >= p.shape[1]) == (hp.proj_type == MEO_GALORE_STD)
+        shape = p.shape
+        projected = len(shape) == 2 and shape[0] > 0 and shape[1] > 0
+        if projected:
+            right = (shape[0] >= shape[1]) == std
+            D, d = shape if right else shape[::-1]
+            r, blocks = min(rank, D, d), -(-d // MX4_BLOCK)
         scale = None
         if isinstance(g, MX4Tensor):
-            if p.dim() != 2:
+            if not projected:
                 raise ValueError("only a 2-D parameter takes an MX4 gradient")
-            want = tuple(p.shape) if right else (p.shape[1], p.shape[0])
-            if g.shape != want:
-                raise ValueError(f"MX4 gradient of shape {g.shape}, expected {want} (blocks along the contraction)")
-            tensors[i] = tensor_struct(p, p)
-            tensors[i].grad, tensors[i].grad_dtype = g.codes.data_ptr(), MEO_MX4
+            if g.shape != (D, d):
+                raise ValueError(f"MX4 gradient of shape {g.shape}, expected {(D, d)} (blocks along the contraction)")
+            t = tensor_struct(p, p)
+            t.grad, t.grad_dtype = g.codes.data_ptr(), MEO_MX4
             scale = g.scales.data_ptr()
         else:
-            tensors[i] = tensor_struct(p, g)
-        shapes = galore_mx4_state_shapes(p.shape, hp.rank, "std" if hp.proj_type == MEO_GALORE_STD else "reverse_std")
+            t = tensor_struct(p, g)
+        tensors[i] = t
+        ptrs = []
         for k in GALORE_MX4_KEYS:
-            t = st.get(k)
-            dt = torch.uint8 if k.startswith("projector") else torch.float32
-            if t is None:
+            s = st.get(k)
+            if s is None:
+                ptrs.append(None)
                 continue
-            if t.dtype != dt:
-                raise TypeError(f"GaLore state {k} must be {dt}")
-            if not t.is_contiguous():
+            moment = k in _MOMENTS
+            if s.dtype != (torch.float32 if moment else torch.uint8):
+                raise TypeError(f"GaLore state {k} must be {'float32' if moment else 'uint8'}")
+            if not s.is_contiguous():
                 raise ValueError(f"GaLore state {k} must be contiguous (row-major)")
-            if k in shapes and tuple(t.shape) != tuple(shapes[k]):
-                raise ValueError(f"GaLore state {k} of shape {tuple(t.shape)}, expected {tuple(shapes[k])}")
-        arr[i] = meo_galore_mx4_state(*[_ptr(st.get(k)) for k in GALORE_MX4_KEYS], scale)
+            want = ((D, r) if moment else (r, 16 * blocks if k == "projector" else blocks)) if projected else shape
+            if s.shape != want and (projected or moment):
+                raise ValueError(f"GaLore state {k} of shape {tuple(s.shape)}, expected {tuple(want)}")
+            ptrs.append(s.data_ptr())
+        arr[i] = meo_galore_mx4_state(*ptrs, scale)
     return tensors, arr
 
 

@@ -46,23 +46,28 @@ __device__ __forceinline__ int gx_ex(int r, int col) {
     return ((r ^ ((r >> 2) & 1)) << 5) + ((((col >> 2) ^ ((r >> 1) & 1))) << 2) + (col & 3);
 }
 
-// AdamW on a wave's 32 x 64 piece of R (accumulator blocks a0, a1) at row i0, column c0,
-// through the wave's exchange region lw: lane l ends with rows (l >> 2) + 16 q of a block
-// and its columns 8 (l & 3) .. + 7. All moments are loaded before the first is used.
-__device__ __forceinline__ void gx_epilogue(const GxDesc& d, const GaArgs& a, const f32x16& a0, const f32x16& a1,
-                                            int64_t i0, int c0, float* lw, int lane) {
-    const int c = 8 * (lane & 3);
+// A wave's 32 x 64 piece of R at row i0, column c0: lane l holds, in block b (32 columns each),
+// rows (l >> 2) + 16 q and columns 8 (l & 3) .. + 7. The moments of all of them:
+struct GxMoments {
     float m[2][2][8], v[2][2][8];
+    __device__ __forceinline__ void load(const GxDesc& d, int64_t i0, int c0, int lane) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int64_t row = i0 + (lane >> 2) + 16 * q;
-            const int col = c0 + 32 * b + c;
-            const int valid = row < d.D ? min(max(d.r - col, 0), 8) : 0;
-            load_f8(d.em + row * d.r + col, valid, d.rvec, m[b][q]);
-            load_f8(d.ev + row * d.r + col, valid, d.rvec, v[b][q]);
-        }
+            for (int q = 0; q < 2; ++q) {
+                const int64_t row = i0 + (lane >> 2) + 16 * q;
+                const int col = c0 + 32 * b + 8 * (lane & 3);
+                const int valid = row < d.D ? min(max(d.r - col, 0), 8) : 0;
+                load_f8(d.em + row * d.r + col, valid, d.rvec, m[b][q]);
+                load_f8(d.ev + row * d.r + col, valid, d.rvec, v[b][q]);
+            }
+    }
+};
+
+// AdamW on that piece (accumulator blocks a0, a1), through the wave's exchange region lw.
+__device__ __forceinline__ void gx_epilogue(const GxDesc& d, const GaArgs& a, const f32x16& a0, const f32x16& a1,
+                                            GxMoments& mv, int64_t i0, int c0, float* lw, int lane) {
+    const int c = 8 * (lane & 3);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
         const f32x16& acc = b ? a1 : a0;
@@ -78,7 +83,7 @@ __device__ __forceinline__ void gx_epilogue(const GxDesc& d, const GaArgs& a, co
             const int64_t row = i0 + r;
             const int col = c0 + 32 * b + c;
             if (row < d.D && col < d.rp)
-                gx_adamw8(d, a, row, col, min(max(d.r - col, 0), 8), m[b][q], v[b][q], rv);
+                gx_adamw8(d, a, row, col, min(max(d.r - col, 0), 8), mv.m[b][q], mv.v[b][q], rv);
         }
         __builtin_amdgcn_wave_barrier();  // this block's gathers before the next block's spill
     }
@@ -145,7 +150,11 @@ __device__ __forceinline__ void gx_any_tile(const GxDesc& d, int64_t i0, const G
     if (!active) return;
     float* lw = reinterpret_cast<float*>(arena) + wave * kGxEx;
 #pragma unroll
-    for (int ib = 0; ib < 2; ++ib) gx_epilogue(d, a, acc[ib][0], acc[ib][1], i0 + ib * 32, wave * 64, lw, lane);
+    for (int ib = 0; ib < 2; ++ib) {
+        GxMoments mv;
+        mv.load(d, i0 + ib * 32, wave * 64, lane);
+        gx_epilogue(d, a, acc[ib][0], acc[ib][1], mv, i0 + ib * 32, wave * 64, lw, lane);
+    }
 }
 
 __global__ __launch_bounds__(kThreads, 3) void k_gx_project(GxTable t, GaArgs a, int nright) {
@@ -241,11 +250,20 @@ __device__ __forceinline__ void gx_direct_tile(const GxDesc& d, int64_t i0, cons
         const int r0 = cw + (lane & 31), sw = mx_swz(lane & 31), b0 = 4 * (k & 1) + 2 * h;
         const uint32_t pb = base + kGdDepth * kGdG + ((k >> 1) & 1) * kGdCodes + r0 * 128;
         const uint32_t pe = base + kGdDepth * kGdG + 2 * kGdCodes + ((k >> 2) & 1) * kGdScales + (k & 3) * (kGaWide * 4) + r0 * 4;
-        u32x4 c[4];
-        lds_read4(pb + ((b0 ^ sw) << 4), pb + (((b0 + 1) ^ sw) << 4), pb + 4096 + ((b0 ^ sw) << 4),
-                  pb + 4096 + (((b0 + 1) ^ sw) << 4), c);
+        const uint32_t q[2] = {pb + ((b0 ^ sw) << 4), pb + (((b0 + 1) ^ sw) << 4)};
+        u32x4 x[8], c[4];  // G's eight fragments; codes, [column][block]
         uint32_t e[2];
-        lds_read_words2(pe, pe + 128, e);
+        if constexpr (Left) {
+            const int gq = lane >> 4, eq = (lane >> 2) & 3;
+            const int col = rw + 16 * (gq & 1) + 4 * (lane & 3);
+            lds_read_tr(s + (64 * h + eq) * 128 + (((col >> 3) ^ lsw(eq)) << 4) + (col & 7) * 2, q, pe, x, c, e);
+        } else {
+            const int r = rw + (lane & 31);
+            uint32_t p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = s + r * 256 + (((8 * h + i) ^ (r & 15)) << 4);
+            lds_read_row(p, q, pe, x, c, e);
+        }
         float sc[2][2];  // [column][block]
 #pragma unroll
         for (int jb = 0; jb < 2; ++jb) {
@@ -254,42 +272,22 @@ __device__ __forceinline__ void gx_direct_tile(const GxDesc& d, int64_t i0, cons
             sc[jb][1] = mx4_scale((w >> 8) & 255u);
         }
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {  // four 8-value sub-steps at a time, one block
-            bfv8 fa[4];
-            if constexpr (Left) {
-                const int gq = lane >> 4, eq = (lane >> 2) & 3;
-                const int col = rw + 16 * (gq & 1) + 4 * (lane & 3);
-                const int kr = 64 * h + 32 * q + eq;
-                const uint32_t p = s + kr * 128 + (((col >> 3) ^ lsw(eq)) << 4) + (col & 7) * 2;
-                u32x2 x[8];
-                lds_read_tr8(p, x);
+        for (int u = 0; u < 8; ++u)  // 8 values: dword u & 3 of block u >> 2
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    fa[u] = __builtin_bit_cast(bfv8, u32x4{x[2 * u].x, x[2 * u].y, x[2 * u + 1].x, x[2 * u + 1].y});
-            } else {
-                const int r = rw + (lane & 31), b = 8 * h + 4 * q;
-                const uint32_t p = s + r * 256;
-                u32x4 x[4];
-                lds_read4(p + ((b ^ (r & 15)) << 4), p + (((b + 1) ^ (r & 15)) << 4), p + (((b + 2) ^ (r & 15)) << 4),
-                          p + (((b + 3) ^ (r & 15)) << 4), x);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) fa[u] = __builtin_bit_cast(bfv8, x[u]);
+            for (int jb = 0; jb < 2; ++jb) {
+                const bfv8 fb = __builtin_bit_cast(bfv8, mx4_to_bf16(c[2 * jb + (u >> 2)][u & 3], sc[jb][u >> 2]));
+                acc[0][jb] = mfma32(__builtin_bit_cast(bfv8, x[u]), fb, acc[0][jb]);
             }
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int jb = 0; jb < 2; ++jb) {
-                    const bfv8 fb = __builtin_bit_cast(bfv8, mx4_to_bf16(c[2 * jb + q][u], sc[jb][q]));
-                    acc[0][jb] = mfma32(fa[u], fb, acc[0][jb]);
-                }
-        }
     };
     // Before step k's barrier a wave that fetches G waits until only steps k + 1 .. k + 3 are
     // outstanding. One that fetches U^T issued the codes of a pair of steps in the even step
     // before it and the scales of four steps two steps before them: before an even step it
     // waits for all, before an odd one for nothing that step k - 1 issued. What a step fills
     // was last read before its barrier.
+    // The moments of the wave's piece of R are loaded before everything else.
     const bool active = cw < d.r;
+    GxMoments mv;
+    if (active) mv.load(d, i0 + rw, cw, lane);
     if (fetch_g) {
 #pragma unroll
         for (int k = 0; k < kGdDepth - 1; ++k) stage(k, lds + k * kGdG);
@@ -315,7 +313,7 @@ __device__ __forceinline__ void gx_direct_tile(const GxDesc& d, int64_t i0, cons
     wait_and_sync<0>();
     if (!active) return;
     float* lw = reinterpret_cast<float*>(lds) + wave * kGxEx;
-    gx_epilogue(d, a, acc[0][0], acc[0][1], i0 + rw, cw, lw, lane);
+    gx_epilogue(d, a, acc[0][0], acc[0][1], mv, i0 + rw, cw, lw, lane);
 }
 
 __global__ __launch_bounds__(kGdWaves * 64) void k_gx_project_direct(GxTable t, GaArgs a, int nright) {
@@ -358,7 +356,11 @@ __global__ __launch_bounds__(NW * 64) void k_gx_project_mx4(GxTable t, GaArgs a)
         const int col = c0 + (wave % WN) * 64;
         if (col < d.r)
 #pragma unroll
-            for (int ib = 0; ib < IB; ++ib) gx_epilogue(d, a, acc[ib][0], acc[ib][1], row + ib * 32, col, lw, lane);
+            for (int ib = 0; ib < IB; ++ib) {
+                GxMoments mv;
+                mv.load(d, row + ib * 32, col, lane);
+                gx_epilogue(d, a, acc[ib][0], acc[ib][1], mv, row + ib * 32, col, lw, lane);
+            }
         if (c0 + T::kRowsB < d.r) __syncthreads();  // the exchange regions are read before the stages are filled
     }
 }

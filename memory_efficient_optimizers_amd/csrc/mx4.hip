@@ -14,7 +14,8 @@ namespace meo {
 
 namespace {
 
-__device__ __forceinline__ const MxMat& mx_find(const MxBatch& b, uint32_t block) {
+template <int N>
+__device__ __forceinline__ const MxMat& mx_find(const MxBatchOf<N>& b, uint32_t block) {
     int i = 0;
     while (i + 1 < b.n && block >= b.m[i + 1].first) ++i;
     return b.m[i];
@@ -57,7 +58,8 @@ __device__ __forceinline__ void quantize_rows(const MxMat& m, uint32_t tile) {
     }
 }
 
-__global__ __launch_bounds__(kMxRowThreads) void k_mx4_quantize_rows(MxBatch b) {
+template <int N>
+__global__ __launch_bounds__(kMxRowThreads) void k_mx4_quantize_rows(MxBatchOf<N> b) {
     const MxMat& m = mx_find(b, blockIdx.x);
     if (m.bf16) quantize_rows<true>(m, blockIdx.x - m.first);
     else quantize_rows<false>(m, blockIdx.x - m.first);
@@ -87,7 +89,8 @@ __device__ __forceinline__ void dequantize_rows(const MxMat& m, uint32_t tile) {
     }
 }
 
-__global__ __launch_bounds__(kMxRowThreads) void k_mx4_dequantize_rows(MxBatch b) {
+template <int N>
+__global__ __launch_bounds__(kMxRowThreads) void k_mx4_dequantize_rows(MxBatchOf<N> b) {
     const MxMat& m = mx_find(b, blockIdx.x);
     if (m.bf16) dequantize_rows<true>(m, blockIdx.x - m.first);
     else dequantize_rows<false>(m, blockIdx.x - m.first);
@@ -176,7 +179,8 @@ __device__ __forceinline__ void quantize_cols(const MxMat& m, uint32_t tile, uin
     }
 }
 
-__global__ __launch_bounds__(kMxColThreads) void k_mx4_quantize_cols(MxBatch b) {
+template <int N>
+__global__ __launch_bounds__(kMxColThreads) void k_mx4_quantize_cols(MxBatchOf<N> b) {
     __shared__ __attribute__((aligned(16))) uint8_t lc[kMxColRows * kMxColPitch];
     __shared__ uint8_t ls[kMxColRows * kMxColBlocks];
     const MxMat& m = mx_find(b, blockIdx.x);
@@ -238,7 +242,8 @@ __device__ __forceinline__ void dequantize_cols(const MxMat& m, uint32_t tile, u
     }
 }
 
-__global__ __launch_bounds__(kMxColThreads) void k_mx4_dequantize_cols(MxBatch b) {
+template <int N>
+__global__ __launch_bounds__(kMxColThreads) void k_mx4_dequantize_cols(MxBatchOf<N> b) {
     __shared__ __attribute__((aligned(16))) uint8_t lc[kMxColRows * kMxColPitch];
     __shared__ uint8_t ls[kMxColRows * kMxColBlocks];
     const MxMat& m = mx_find(b, blockIdx.x);
@@ -246,16 +251,29 @@ __global__ __launch_bounds__(kMxColThreads) void k_mx4_dequantize_cols(MxBatch b
     else dequantize_cols<false>(m, blockIdx.x - m.first, lc, ls);
 }
 
+namespace {
+
+MxBatchOf<1> only(const MxBatch& b) { return MxBatchOf<1>{1, {b.m[0]}}; }
+MxProdBatchOf<1> only(const MxProdBatch& b) { return MxProdBatchOf<1>{1, {b.p[0]}}; }
+
+}  // namespace
+
 void launch_mx4_quantize(const MxBatch& b, uint32_t grid, bool transposed, hipStream_t s) {
     if (grid == 0) return;
-    if (transposed) hipLaunchKernelGGL(k_mx4_quantize_cols, dim3(grid), dim3(kMxColThreads), 0, s, b);
-    else hipLaunchKernelGGL(k_mx4_quantize_rows, dim3(grid), dim3(kMxRowThreads), 0, s, b);
+    const dim3 g(grid), t(transposed ? kMxColThreads : kMxRowThreads);
+    if (b.n == 1 && transposed) hipLaunchKernelGGL(k_mx4_quantize_cols<1>, g, t, 0, s, only(b));
+    else if (b.n == 1) hipLaunchKernelGGL(k_mx4_quantize_rows<1>, g, t, 0, s, only(b));
+    else if (transposed) hipLaunchKernelGGL(k_mx4_quantize_cols<kMxBatch>, g, t, 0, s, b);
+    else hipLaunchKernelGGL(k_mx4_quantize_rows<kMxBatch>, g, t, 0, s, b);
 }
 
 void launch_mx4_dequantize(const MxBatch& b, uint32_t grid, bool transposed, hipStream_t s) {
     if (grid == 0) return;
-    if (transposed) hipLaunchKernelGGL(k_mx4_dequantize_cols, dim3(grid), dim3(kMxColThreads), 0, s, b);
-    else hipLaunchKernelGGL(k_mx4_dequantize_rows, dim3(grid), dim3(kMxRowThreads), 0, s, b);
+    const dim3 g(grid), t(transposed ? kMxColThreads : kMxRowThreads);
+    if (b.n == 1 && transposed) hipLaunchKernelGGL(k_mx4_dequantize_cols<1>, g, t, 0, s, only(b));
+    else if (b.n == 1) hipLaunchKernelGGL(k_mx4_dequantize_rows<1>, g, t, 0, s, only(b));
+    else if (transposed) hipLaunchKernelGGL(k_mx4_dequantize_cols<kMxBatch>, g, t, 0, s, b);
+    else hipLaunchKernelGGL(k_mx4_dequantize_rows<kMxBatch>, g, t, 0, s, b);
 }
 
 // ----------------------------------------------------------------------------- product
@@ -284,8 +302,8 @@ __device__ __forceinline__ void mx4_store(const MxProd& p, int64_t i0, int64_t j
     }
 }
 
-template <int IB, int WN, int NW, bool Any>
-__global__ __launch_bounds__(NW * 64) void k_mx4_matmul(MxProdBatch b) {
+template <int IB, int WN, int NW, bool Any, int N>
+__global__ __launch_bounds__(NW * 64) void k_mx4_matmul(MxProdBatchOf<N> b) {
     using T = MxTile<IB, WN, NW>;
     __shared__ __attribute__((aligned(16))) uint8_t lds[Any ? 16 : T::kLds];
     int i = 0;
@@ -311,13 +329,19 @@ __global__ __launch_bounds__(NW * 64) void k_mx4_matmul(MxProdBatch b) {
     else mx4_store<IB, false>(p, i0, j0, lane, acc);
 }
 
+template <int IB, int WN, int NW, bool Any>
+static void launch_matmul(const MxProdBatch& b, uint32_t grid, hipStream_t s) {
+    if (b.n == 1) hipLaunchKernelGGL((k_mx4_matmul<IB, WN, NW, Any, 1>), dim3(grid), dim3(NW * 64), 0, s, only(b));
+    else hipLaunchKernelGGL((k_mx4_matmul<IB, WN, NW, Any, kMxBatch>), dim3(grid), dim3(NW * 64), 0, s, b);
+}
+
 void launch_mx4_matmul(const MxProdBatch& b, uint32_t grid, MxForm form, hipStream_t s) {
     if (grid == 0) return;
     switch (form) {
-        case kMxAny: hipLaunchKernelGGL((k_mx4_matmul<1, 2, 4, true>), dim3(grid), dim3(256), 0, s, b); break;
-        case kMxNarrow: hipLaunchKernelGGL((k_mx4_matmul<1, 2, 4, false>), dim3(grid), dim3(256), 0, s, b); break;
-        case kMxWide: hipLaunchKernelGGL((k_mx4_matmul<1, 4, 8, false>), dim3(grid), dim3(512), 0, s, b); break;
-        default: hipLaunchKernelGGL((k_mx4_matmul<2, 4, 8, false>), dim3(grid), dim3(512), 0, s, b); break;
+        case kMxAny: launch_matmul<1, 2, 4, true>(b, grid, s); break;
+        case kMxNarrow: launch_matmul<1, 2, 4, false>(b, grid, s); break;
+        case kMxWide: launch_matmul<1, 4, 8, false>(b, grid, s); break;
+        default: launch_matmul<2, 4, 8, false>(b, grid, s); break;
     }
 }
 

@@ -31,62 +31,143 @@ __device__ __forceinline__ void dma4(const uint8_t* src, void* dst) {
     __builtin_amdgcn_global_load_lds((const MEO_GLOBAL void*)src, (__attribute__((address_space(3))) void*)dst, 4, 0, 0);
 }
 
-// Four 16-byte LDS reads that have landed when it returns. In one asm block with their wait:
-// before a plain read the compiler, which cannot tell what a transfer in flight writes, would
-// wait for every transfer. The stage read has landed (the wait and barrier before).
-__device__ __forceinline__ void lds_read4(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, u32x4* v) {
-    u32x4 v0, v1, v2, v3;
-    __asm__ volatile(
-        "ds_read_b128 %0, %4\n\t"
-        "ds_read_b128 %1, %5\n\t"
-        "ds_read_b128 %2, %6\n\t"
-        "ds_read_b128 %3, %7\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(v0), "=&v"(v1), "=&v"(v2), "=&v"(v3)
-        : "v"(a0), "v"(a1), "v"(a2), "v"(a3));
-    v[0] = v0; v[1] = v1; v[2] = v2; v[3] = v3;
+// The LDS reads of a step's fragments are one asm block with their wait: before a plain read
+// the compiler, which cannot tell what a transfer in flight writes, would wait for every
+// transfer. The stages read have landed (the wait and barrier before), and one wait for
+// all reads exposes the LDS latency once per step.
+
+// An MX4 step: four 16-byte chunks (p[t]) of A's row and of the rows 32 on (IB = 2), the
+// same of B's two rows (q[t]), the scale words at ea (and 32 rows on), eb and 32 rows on.
+template <int IB>
+__device__ __forceinline__ void lds_read_mx(const uint32_t* p, const uint32_t* q, uint32_t ea, uint32_t eb, u32x4 (&ca)[2][4],
+                                            u32x4 (&cb)[2][4], uint32_t* e) {
+    u32x4 a0, a1, a2, a3, a4, a5, a6, a7, b0, b1, b2, b3, b4, b5, b6, b7;
+    uint32_t e0, e1, e2, e3;
+    if constexpr (IB == 2) {
+        __asm__ volatile(
+            "ds_read_b32 %16, %28\n\t"
+            "ds_read_b32 %17, %28 offset:128\n\t"
+            "ds_read_b32 %18, %29\n\t"
+            "ds_read_b32 %19, %29 offset:128\n\t"
+            "ds_read_b128 %0, %20\n\t"
+            "ds_read_b128 %8, %24\n\t"
+            "ds_read_b128 %12, %24 offset:4096\n\t"
+            "ds_read_b128 %4, %20 offset:4096\n\t"
+            "ds_read_b128 %1, %21\n\t"
+            "ds_read_b128 %9, %25\n\t"
+            "ds_read_b128 %13, %25 offset:4096\n\t"
+            "ds_read_b128 %5, %21 offset:4096\n\t"
+            "ds_read_b128 %2, %22\n\t"
+            "ds_read_b128 %10, %26\n\t"
+            "ds_read_b128 %14, %26 offset:4096\n\t"
+            "ds_read_b128 %6, %22 offset:4096\n\t"
+            "ds_read_b128 %3, %23\n\t"
+            "ds_read_b128 %11, %27\n\t"
+            "ds_read_b128 %15, %27 offset:4096\n\t"
+            "ds_read_b128 %7, %23 offset:4096\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(a0), "=&v"(a1), "=&v"(a2), "=&v"(a3), "=&v"(a4), "=&v"(a5), "=&v"(a6), "=&v"(a7), "=&v"(b0), "=&v"(b1),
+              "=&v"(b2), "=&v"(b3), "=&v"(b4), "=&v"(b5), "=&v"(b6), "=&v"(b7), "=&v"(e0), "=&v"(e1), "=&v"(e2), "=&v"(e3)
+            : "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "v"(q[0]), "v"(q[1]), "v"(q[2]), "v"(q[3]), "v"(ea), "v"(eb));
+        ca[1][0] = a4; ca[1][1] = a5; ca[1][2] = a6; ca[1][3] = a7;
+    } else {
+        __asm__ volatile(
+            "ds_read_b32 %12, %23\n\t"
+            "ds_read_b32 %13, %24\n\t"
+            "ds_read_b32 %14, %24 offset:128\n\t"
+            "ds_read_b128 %0, %15\n\t"
+            "ds_read_b128 %4, %19\n\t"
+            "ds_read_b128 %8, %19 offset:4096\n\t"
+            "ds_read_b128 %1, %16\n\t"
+            "ds_read_b128 %5, %20\n\t"
+            "ds_read_b128 %9, %20 offset:4096\n\t"
+            "ds_read_b128 %2, %17\n\t"
+            "ds_read_b128 %6, %21\n\t"
+            "ds_read_b128 %10, %21 offset:4096\n\t"
+            "ds_read_b128 %3, %18\n\t"
+            "ds_read_b128 %7, %22\n\t"
+            "ds_read_b128 %11, %22 offset:4096\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(a0), "=&v"(a1), "=&v"(a2), "=&v"(a3), "=&v"(b0), "=&v"(b1), "=&v"(b2), "=&v"(b3), "=&v"(b4), "=&v"(b5),
+              "=&v"(b6), "=&v"(b7), "=&v"(e0), "=&v"(e2), "=&v"(e3)
+            : "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "v"(q[0]), "v"(q[1]), "v"(q[2]), "v"(q[3]), "v"(ea), "v"(eb));
+        e1 = 0;
+    }
+    ca[0][0] = a0; ca[0][1] = a1; ca[0][2] = a2; ca[0][3] = a3;
+    cb[0][0] = b0; cb[0][1] = b1; cb[0][2] = b2; cb[0][3] = b3;
+    cb[1][0] = b4; cb[1][1] = b5; cb[1][2] = b6; cb[1][3] = b7;
+    e[0] = e0; e[1] = e1; e[2] = e2; e[3] = e3;
 }
 
-__device__ __forceinline__ void lds_read_words(uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t* w) {
-    uint32_t w0, w1, w2, w3;
+// A bf16 step: eight 16-byte chunks (p[i]) of G's row, two chunks (q[t]) of a row of codes
+// and of the row 32 on, their scale words (pe).
+__device__ __forceinline__ void lds_read_row(const uint32_t* p, const uint32_t* q, uint32_t pe, u32x4* g, u32x4* c, uint32_t* e) {
+    u32x4 g0, g1, g2, g3, g4, g5, g6, g7, c0, c1, c2, c3;
+    uint32_t e0, e1;
     __asm__ volatile(
-        "ds_read_b32 %0, %4\n\t"
-        "ds_read_b32 %1, %5\n\t"
-        "ds_read_b32 %2, %6\n\t"
-        "ds_read_b32 %3, %7\n\t"
+        "ds_read_b32 %12, %24\n\t"
+        "ds_read_b32 %13, %24 offset:128\n\t"
+        "ds_read_b128 %8, %22\n\t"
+        "ds_read_b128 %10, %22 offset:4096\n\t"
+        "ds_read_b128 %0, %14\n\t"
+        "ds_read_b128 %1, %15\n\t"
+        "ds_read_b128 %2, %16\n\t"
+        "ds_read_b128 %3, %17\n\t"
+        "ds_read_b128 %9, %23\n\t"
+        "ds_read_b128 %11, %23 offset:4096\n\t"
+        "ds_read_b128 %4, %18\n\t"
+        "ds_read_b128 %5, %19\n\t"
+        "ds_read_b128 %6, %20\n\t"
+        "ds_read_b128 %7, %21\n\t"
         "s_waitcnt lgkmcnt(0)"
-        : "=&v"(w0), "=&v"(w1), "=&v"(w2), "=&v"(w3)
-        : "v"(a0), "v"(a1), "v"(a2), "v"(a3));
-    w[0] = w0; w[1] = w1; w[2] = w2; w[3] = w3;
+        : "=&v"(g0), "=&v"(g1), "=&v"(g2), "=&v"(g3), "=&v"(g4), "=&v"(g5), "=&v"(g6), "=&v"(g7), "=&v"(c0), "=&v"(c1),
+          "=&v"(c2), "=&v"(c3), "=&v"(e0), "=&v"(e1)
+        : "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "v"(p[4]), "v"(p[5]), "v"(p[6]), "v"(p[7]), "v"(q[0]), "v"(q[1]), "v"(pe));
+    g[0] = g0; g[1] = g1; g[2] = g2; g[3] = g3; g[4] = g4; g[5] = g5; g[6] = g6; g[7] = g7;
+    c[0] = c0; c[1] = c1; c[2] = c2; c[3] = c3;
+    e[0] = e0; e[1] = e1;
 }
 
-__device__ __forceinline__ void lds_read_words2(uint32_t a0, uint32_t a1, uint32_t* w) {
-    uint32_t w0, w1;
+// The same with G's tile transposed: sixteen transposed 8-byte reads of 16-bit values, 4 rows
+// of 128 bytes apart each, give the eight fragments.
+__device__ __forceinline__ void lds_read_tr(uint32_t p, const uint32_t* q, uint32_t pe, u32x4* g, u32x4* c, uint32_t* e) {
+    u32x2 x0, x1, x2, x3, x4, x5, x6, x7, x8, x9, xa, xb, xc, xd, xe, xf;
+    u32x4 c0, c1, c2, c3;
+    uint32_t e0, e1;
     __asm__ volatile(
-        "ds_read_b32 %0, %2\n\t"
-        "ds_read_b32 %1, %3\n\t"
+        "ds_read_b32 %20, %25\n\t"
+        "ds_read_b32 %21, %25 offset:128\n\t"
+        "ds_read_b128 %16, %23\n\t"
+        "ds_read_b128 %18, %23 offset:4096\n\t"
+        "ds_read_b64_tr_b16 %0, %22\n\t"
+        "ds_read_b64_tr_b16 %1, %22 offset:512\n\t"
+        "ds_read_b64_tr_b16 %2, %22 offset:1024\n\t"
+        "ds_read_b64_tr_b16 %3, %22 offset:1536\n\t"
+        "ds_read_b64_tr_b16 %4, %22 offset:2048\n\t"
+        "ds_read_b64_tr_b16 %5, %22 offset:2560\n\t"
+        "ds_read_b64_tr_b16 %6, %22 offset:3072\n\t"
+        "ds_read_b64_tr_b16 %7, %22 offset:3584\n\t"
+        "ds_read_b128 %17, %24\n\t"
+        "ds_read_b128 %19, %24 offset:4096\n\t"
+        "ds_read_b64_tr_b16 %8, %22 offset:4096\n\t"
+        "ds_read_b64_tr_b16 %9, %22 offset:4608\n\t"
+        "ds_read_b64_tr_b16 %10, %22 offset:5120\n\t"
+        "ds_read_b64_tr_b16 %11, %22 offset:5632\n\t"
+        "ds_read_b64_tr_b16 %12, %22 offset:6144\n\t"
+        "ds_read_b64_tr_b16 %13, %22 offset:6656\n\t"
+        "ds_read_b64_tr_b16 %14, %22 offset:7168\n\t"
+        "ds_read_b64_tr_b16 %15, %22 offset:7680\n\t"
         "s_waitcnt lgkmcnt(0)"
-        : "=&v"(w0), "=&v"(w1)
-        : "v"(a0), "v"(a1));
-    w[0] = w0; w[1] = w1;
-}
-
-// Eight transposed 8-byte reads of 16-bit values, 4 rows of 128 bytes apart each.
-__device__ __forceinline__ void lds_read_tr8(uint32_t p, u32x2* v) {
-    u32x2 v0, v1, v2, v3, v4, v5, v6, v7;
-    __asm__ volatile(
-        "ds_read_b64_tr_b16 %0, %8\n\t"
-        "ds_read_b64_tr_b16 %1, %8 offset:512\n\t"
-        "ds_read_b64_tr_b16 %2, %8 offset:1024\n\t"
-        "ds_read_b64_tr_b16 %3, %8 offset:1536\n\t"
-        "ds_read_b64_tr_b16 %4, %8 offset:2048\n\t"
-        "ds_read_b64_tr_b16 %5, %8 offset:2560\n\t"
-        "ds_read_b64_tr_b16 %6, %8 offset:3072\n\t"
-        "ds_read_b64_tr_b16 %7, %8 offset:3584\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(v0), "=&v"(v1), "=&v"(v2), "=&v"(v3), "=&v"(v4), "=&v"(v5), "=&v"(v6), "=&v"(v7)
-        : "v"(p));
-    v[0] = v0; v[1] = v1; v[2] = v2; v[3] = v3; v[4] = v4; v[5] = v5; v[6] = v6; v[7] = v7;
+        : "=&v"(x0), "=&v"(x1), "=&v"(x2), "=&v"(x3), "=&v"(x4), "=&v"(x5), "=&v"(x6), "=&v"(x7), "=&v"(x8), "=&v"(x9),
+          "=&v"(xa), "=&v"(xb), "=&v"(xc), "=&v"(xd), "=&v"(xe), "=&v"(xf), "=&v"(c0), "=&v"(c1), "=&v"(c2), "=&v"(c3),
+          "=&v"(e0), "=&v"(e1)
+        : "v"(p), "v"(q[0]), "v"(q[1]), "v"(pe));
+    g[0] = u32x4{x0.x, x0.y, x1.x, x1.y}; g[1] = u32x4{x2.x, x2.y, x3.x, x3.y};
+    g[2] = u32x4{x4.x, x4.y, x5.x, x5.y}; g[3] = u32x4{x6.x, x6.y, x7.x, x7.y};
+    g[4] = u32x4{x8.x, x8.y, x9.x, x9.y}; g[5] = u32x4{xa.x, xa.y, xb.x, xb.y};
+    g[6] = u32x4{xc.x, xc.y, xd.x, xd.y}; g[7] = u32x4{xe.x, xe.y, xf.x, xf.y};
+    c[0] = c0; c[1] = c1; c[2] = c2; c[3] = c3;
+    e[0] = e0; e[1] = e1;
 }
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
@@ -191,12 +272,14 @@ __device__ __forceinline__ void mx4_accumulate(const MxOperand& a, const MxOpera
         const uint32_t q = base + T::kDepth * T::kStageA + 2 * T::kStageB + ((k >> 1) & 1) * T::kScales +
                            (2 * (k & 1) + h) * (T::kRows * 4);
         const uint32_t qa = q + wr * 4, qb = q + (T::kRowsA + wc) * 4;
-        auto at = [&](int t) { return static_cast<uint32_t>(((4 * h + t) ^ sw) << 4); };
-        uint32_t e[4];  // scales: A's one or two rows, B's two
-        lds_read_words(qa, qa + (IB - 1) * 128, qb, qb + 128, e);
-        u32x4 cb[2][4];
-        lds_read4(pb + at(0), pb + at(1), pb + at(2), pb + at(3), cb[0]);
-        lds_read4(pb + 4096 + at(0), pb + 4096 + at(1), pb + 4096 + at(2), pb + 4096 + at(3), cb[1]);
+        uint32_t p[4], r[4], e[4];  // e: scales, A's one or two rows, B's two
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            p[t] = pa + (((4 * h + t) ^ sw) << 4);
+            r[t] = pb + (((4 * h + t) ^ sw) << 4);
+        }
+        u32x4 ca[2][4], cb[2][4];
+        lds_read_mx<IB>(p, r, qa, qb, ca, cb, e);
         if ((k + 1) * kMxStep > nb) {
 #pragma unroll
             for (int jb = 0; jb < 2; ++jb)
@@ -209,14 +292,12 @@ __device__ __forceinline__ void mx4_accumulate(const MxOperand& a, const MxOpera
         }
 #pragma unroll
         for (int ib = 0; ib < IB; ++ib) {
-            u32x4 ca[4];
-            lds_read4(pa + ib * 4096 + at(0), pa + ib * 4096 + at(1), pa + ib * 4096 + at(2), pa + ib * 4096 + at(3), ca);
 #pragma unroll
             for (int jb = 0; jb < 2; ++jb) {
-                acc[ib][jb] = mfma_mx4<0>(ca[0], cb[jb][0], acc[ib][jb], e[ib], e[2 + jb]);
-                acc[ib][jb] = mfma_mx4<1>(ca[1], cb[jb][1], acc[ib][jb], e[ib], e[2 + jb]);
-                acc[ib][jb] = mfma_mx4<2>(ca[2], cb[jb][2], acc[ib][jb], e[ib], e[2 + jb]);
-                acc[ib][jb] = mfma_mx4<3>(ca[3], cb[jb][3], acc[ib][jb], e[ib], e[2 + jb]);
+                acc[ib][jb] = mfma_mx4<0>(ca[ib][0], cb[jb][0], acc[ib][jb], e[ib], e[2 + jb]);
+                acc[ib][jb] = mfma_mx4<1>(ca[ib][1], cb[jb][1], acc[ib][jb], e[ib], e[2 + jb]);
+                acc[ib][jb] = mfma_mx4<2>(ca[ib][2], cb[jb][2], acc[ib][jb], e[ib], e[2 + jb]);
+                acc[ib][jb] = mfma_mx4<3>(ca[ib][3], cb[jb][3], acc[ib][jb], e[ib], e[2 + jb]);
             }
         }
     };
