@@ -46,8 +46,10 @@ __device__ __forceinline__ int gx_ex(int r, int col) {
     return ((r ^ ((r >> 2) & 1)) << 5) + ((((col >> 2) ^ ((r >> 1) & 1))) << 2) + (col & 3);
 }
 
-// A wave's 32 x 64 piece of R at row i0, column c0: lane l holds, in block b (32 columns each),
-// rows (l >> 2) + 16 q and columns 8 (l & 3) .. + 7. The moments of all of them:
+// A wave's piece of R at row i0, column c0: two 32 x 32 blocks, the second 32 columns on or
+// (Tall) 32 rows on. Lane l holds, in block b, rows (l >> 2) + 16 q and columns 8 (l & 3) .. + 7.
+// The moments of all of them:
+template <bool Tall>
 struct GxMoments {
     float m[2][2][8], v[2][2][8];
     __device__ __forceinline__ void load(const GxDesc& d, int64_t i0, int c0, int lane) {
@@ -55,8 +57,8 @@ struct GxMoments {
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const int64_t row = i0 + (lane >> 2) + 16 * q;
-                const int col = c0 + 32 * b + 8 * (lane & 3);
+                const int64_t row = i0 + (Tall ? 32 * b : 0) + (lane >> 2) + 16 * q;
+                const int col = c0 + (Tall ? 0 : 32 * b) + 8 * (lane & 3);
                 const int valid = row < d.D ? min(max(d.r - col, 0), 8) : 0;
                 load_f8(d.em + row * d.r + col, valid, d.rvec, m[b][q]);
                 load_f8(d.ev + row * d.r + col, valid, d.rvec, v[b][q]);
@@ -65,8 +67,9 @@ struct GxMoments {
 };
 
 // AdamW on that piece (accumulator blocks a0, a1), through the wave's exchange region lw.
+template <bool Tall>
 __device__ __forceinline__ void gx_epilogue(const GxDesc& d, const GaArgs& a, const f32x16& a0, const f32x16& a1,
-                                            GxMoments& mv, int64_t i0, int c0, float* lw, int lane) {
+                                            GxMoments<Tall>& mv, int64_t i0, int c0, float* lw, int lane) {
     const int c = 8 * (lane & 3);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -80,8 +83,8 @@ __device__ __forceinline__ void gx_epilogue(const GxDesc& d, const GaArgs& a, co
             const f32x4 x0 = *reinterpret_cast<const f32x4*>(lw + gx_ex(r, c));
             const f32x4 x1 = *reinterpret_cast<const f32x4*>(lw + gx_ex(r, c + 4));
             const float rv[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-            const int64_t row = i0 + r;
-            const int col = c0 + 32 * b + c;
+            const int64_t row = i0 + (Tall ? 32 * b : 0) + r;
+            const int col = c0 + (Tall ? 0 : 32 * b) + c;
             if (row < d.D && col < d.rp)
                 gx_adamw8(d, a, row, col, min(max(d.r - col, 0), 8), mv.m[b][q], mv.v[b][q], rv);
         }
@@ -151,7 +154,7 @@ __device__ __forceinline__ void gx_any_tile(const GxDesc& d, int64_t i0, const G
     float* lw = reinterpret_cast<float*>(arena) + wave * kGxEx;
 #pragma unroll
     for (int ib = 0; ib < 2; ++ib) {
-        GxMoments mv;
+        GxMoments<false> mv;
         mv.load(d, i0 + ib * 32, wave * 64, lane);
         gx_epilogue(d, a, acc[ib][0], acc[ib][1], mv, i0 + ib * 32, wave * 64, lw, lane);
     }
@@ -167,8 +170,8 @@ __global__ __launch_bounds__(kThreads, 3) void k_gx_project(GxTable t, GaArgs a,
 }
 
 // d a multiple of 128, 16-byte rows of G and whole words of scales. 8 waves on 64 rows of R
-// x 256 columns: wave w at rows 32 (w / 4), columns 64 (w % 4). One contraction step is 128
-// long. Everything goes by global_load_lds, as in mx4_accumulate: waves 0 .. 3 fetch G's
+// x 256 columns, all rows and columns 32 w .. 32 w + 31 each: a wave's decoded codes then serve
+// two products, and no two waves decode the same. One contraction step is 128 long. Everything goes by global_load_lds, as in mx4_accumulate: waves 0 .. 3 fetch G's
 // tile (256-byte pieces of its rows; left: 128 rows of 128 bytes) into one of five stages,
 // four steps ahead, which keeps the 64 KB in flight that HBM takes per CU; waves 4 .. 7 the
 // codes of U^T of two steps (a whole 128-byte line of each of its 256 rows) and the
@@ -191,12 +194,14 @@ __device__ __forceinline__ void gx_direct_tile(const GxDesc& d, int64_t i0, cons
     constexpr int kA = kGdG / 1024 / 4, kB = kGdCodes / 1024 / 4;  // 1 KB transfers per wave of its kind
     static_assert(kGdWaves == 8 && kGdDepth * kGdG >= kGdWaves * kGxEx * 4, "waves below; exchange space");
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
-    const int cw = (wave & 3) * 64;   // the wave's first column of R
-    const int rw = (wave >> 2) * 32;
+    const int cw = wave * 32;  // the wave's first column of R
     const bool fetch_g = wave < 4;
     const int fw = wave & 3;
-    f32x16 acc[1][2];
-    zero_acc(acc);
+    f32x16 acc[2];
+#pragma unroll
+    for (int ib = 0; ib < 2; ++ib)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[ib][v] = 0.0f;
 
     // G. Right: transfer j holds rows 4 j + (l >> 4) of the tile, 16-byte chunk
     // (l & 15) ^ (row & 15). Left: rows 8 j + (l >> 3) of 128 bytes (64 columns of G), chunk
@@ -246,38 +251,35 @@ __device__ __forceinline__ void gx_direct_tile(const GxDesc& d, int64_t i0, cons
     const uint32_t base = lds_addr(lds);
     auto multiply = [&](int k, int cur) {
         const uint32_t s = base + cur * kGdG;
-        // the two blocks of the lane's two columns of R, and their scales
+        // the two blocks of the lane's column of R, and their scales
         const int r0 = cw + (lane & 31), sw = mx_swz(lane & 31), b0 = 4 * (k & 1) + 2 * h;
         const uint32_t pb = base + kGdDepth * kGdG + ((k >> 1) & 1) * kGdCodes + r0 * 128;
         const uint32_t pe = base + kGdDepth * kGdG + 2 * kGdCodes + ((k >> 2) & 1) * kGdScales + (k & 3) * (kGaWide * 4) + r0 * 4;
         const uint32_t q[2] = {pb + ((b0 ^ sw) << 4), pb + (((b0 + 1) ^ sw) << 4)};
-        u32x4 x[8], c[4];  // G's eight fragments; codes, [column][block]
-        uint32_t e[2];
+        u32x4 x[2][8], c[2];  // G's fragments of two 32-row halves; codes of two blocks
+        uint32_t e;
         if constexpr (Left) {
             const int gq = lane >> 4, eq = (lane >> 2) & 3;
-            const int col = rw + 16 * (gq & 1) + 4 * (lane & 3);
-            lds_read_tr(s + (64 * h + eq) * 128 + (((col >> 3) ^ lsw(eq)) << 4) + (col & 7) * 2, q, pe, x, c, e);
+            const int col = 16 * (gq & 1) + 4 * (lane & 3);
+            const uint32_t p = s + (64 * h + eq) * 128 + (((col >> 3) ^ lsw(eq)) << 4) + (col & 7) * 2;
+            lds_read_codes(q, pe, c, e);
+            lds_read_tr(p, x[0]);
+            lds_read_tr(p ^ 64, x[1]);  // 32 columns on: the other half of the (aligned) 128-byte row
         } else {
-            const int r = rw + (lane & 31);
+            const int r = lane & 31;
             uint32_t p[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) p[i] = s + r * 256 + (((8 * h + i) ^ (r & 15)) << 4);
             lds_read_row(p, q, pe, x, c, e);
         }
-        float sc[2][2];  // [column][block]
+        if (h) e >>= 16;
+        const float sc[2] = {mx4_scale(e & 255u), mx4_scale((e >> 8) & 255u)};
 #pragma unroll
-        for (int jb = 0; jb < 2; ++jb) {
-            const uint32_t w = h ? e[jb] >> 16 : e[jb];
-            sc[jb][0] = mx4_scale(w & 255u);
-            sc[jb][1] = mx4_scale((w >> 8) & 255u);
+        for (int u = 0; u < 8; ++u) {  // 8 values: dword u & 3 of block u >> 2
+            const bfv8 fb = __builtin_bit_cast(bfv8, mx4_to_bf16(c[u >> 2][u & 3], sc[u >> 2]));
+#pragma unroll
+            for (int ib = 0; ib < 2; ++ib) acc[ib] = mfma32(__builtin_bit_cast(bfv8, x[ib][u]), fb, acc[ib]);
         }
-#pragma unroll
-        for (int u = 0; u < 8; ++u)  // 8 values: dword u & 3 of block u >> 2
-#pragma unroll
-            for (int jb = 0; jb < 2; ++jb) {
-                const bfv8 fb = __builtin_bit_cast(bfv8, mx4_to_bf16(c[2 * jb + (u >> 2)][u & 3], sc[jb][u >> 2]));
-                acc[0][jb] = mfma32(__builtin_bit_cast(bfv8, x[u]), fb, acc[0][jb]);
-            }
     };
     // Before step k's barrier a wave that fetches G waits until only steps k + 1 .. k + 3 are
     // outstanding. One that fetches U^T issued the codes of a pair of steps in the even step
@@ -286,8 +288,8 @@ __device__ __forceinline__ void gx_direct_tile(const GxDesc& d, int64_t i0, cons
     // was last read before its barrier.
     // The moments of the wave's piece of R are loaded before everything else.
     const bool active = cw < d.r;
-    GxMoments mv;
-    if (active) mv.load(d, i0 + rw, cw, lane);
+    GxMoments<true> mv;
+    if (active) mv.load(d, i0, cw, lane);
     if (fetch_g) {
 #pragma unroll
         for (int k = 0; k < kGdDepth - 1; ++k) stage(k, lds + k * kGdG);
@@ -313,11 +315,11 @@ __device__ __forceinline__ void gx_direct_tile(const GxDesc& d, int64_t i0, cons
     wait_and_sync<0>();
     if (!active) return;
     float* lw = reinterpret_cast<float*>(lds) + wave * kGxEx;
-    gx_epilogue(d, a, acc[0][0], acc[0][1], mv, i0 + rw, cw, lw, lane);
+    gx_epilogue(d, a, acc[0], acc[1], mv, i0, cw, lw, lane);
 }
 
 __global__ __launch_bounds__(kGdWaves * 64) void k_gx_project_direct(GxTable t, GaArgs a, int nright) {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kGdLds];
+    __shared__ __attribute__((aligned(128))) uint8_t lds[kGdLds];
     const int2 it = t.items[blockIdx.x];
     const GxDesc d = t.desc[it.x];
     const int64_t i0 = static_cast<int64_t>(it.y) * kGdRows;
@@ -357,7 +359,7 @@ __global__ __launch_bounds__(NW * 64) void k_gx_project_mx4(GxTable t, GaArgs a)
         if (col < d.r)
 #pragma unroll
             for (int ib = 0; ib < IB; ++ib) {
-                GxMoments mv;
+                GxMoments<false> mv;
                 mv.load(d, row + ib * 32, col, lane);
                 gx_epilogue(d, a, acc[ib][0], acc[ib][1], mv, row + ib * 32, col, lw, lane);
             }

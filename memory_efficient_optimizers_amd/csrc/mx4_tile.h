@@ -99,75 +99,85 @@ __device__ __forceinline__ void lds_read_mx(const uint32_t* p, const uint32_t* q
     e[0] = e0; e[1] = e1; e[2] = e2; e[3] = e3;
 }
 
-// A bf16 step: eight 16-byte chunks (p[i]) of G's row, two chunks (q[t]) of a row of codes
-// and of the row 32 on, their scale words (pe).
-__device__ __forceinline__ void lds_read_row(const uint32_t* p, const uint32_t* q, uint32_t pe, u32x4* g, u32x4* c, uint32_t* e) {
-    u32x4 g0, g1, g2, g3, g4, g5, g6, g7, c0, c1, c2, c3;
-    uint32_t e0, e1;
+// A bf16 step: eight 16-byte chunks (p[i]) of G's row and of the row 32 on, two chunks (q[t])
+// of a row of codes and their scale word (pe).
+__device__ __forceinline__ void lds_read_row(const uint32_t* p, const uint32_t* q, uint32_t pe, u32x4 (&g)[2][8], u32x4* c,
+                                             uint32_t& e) {
+    u32x4 g0, g1, g2, g3, g4, g5, g6, g7, h0, h1, h2, h3, h4, h5, h6, h7, c0, c1;
+    uint32_t e0;
     __asm__ volatile(
-        "ds_read_b32 %12, %24\n\t"
-        "ds_read_b32 %13, %24 offset:128\n\t"
-        "ds_read_b128 %8, %22\n\t"
-        "ds_read_b128 %10, %22 offset:4096\n\t"
-        "ds_read_b128 %0, %14\n\t"
-        "ds_read_b128 %1, %15\n\t"
-        "ds_read_b128 %2, %16\n\t"
-        "ds_read_b128 %3, %17\n\t"
-        "ds_read_b128 %9, %23\n\t"
-        "ds_read_b128 %11, %23 offset:4096\n\t"
-        "ds_read_b128 %4, %18\n\t"
-        "ds_read_b128 %5, %19\n\t"
-        "ds_read_b128 %6, %20\n\t"
-        "ds_read_b128 %7, %21\n\t"
+        "ds_read_b32 %18, %29\n\t"
+        "ds_read_b128 %16, %27\n\t"
+        "ds_read_b128 %0, %19\n\t"
+        "ds_read_b128 %8, %19 offset:8192\n\t"
+        "ds_read_b128 %1, %20\n\t"
+        "ds_read_b128 %9, %20 offset:8192\n\t"
+        "ds_read_b128 %2, %21\n\t"
+        "ds_read_b128 %10, %21 offset:8192\n\t"
+        "ds_read_b128 %3, %22\n\t"
+        "ds_read_b128 %11, %22 offset:8192\n\t"
+        "ds_read_b128 %17, %28\n\t"
+        "ds_read_b128 %4, %23\n\t"
+        "ds_read_b128 %12, %23 offset:8192\n\t"
+        "ds_read_b128 %5, %24\n\t"
+        "ds_read_b128 %13, %24 offset:8192\n\t"
+        "ds_read_b128 %6, %25\n\t"
+        "ds_read_b128 %14, %25 offset:8192\n\t"
+        "ds_read_b128 %7, %26\n\t"
+        "ds_read_b128 %15, %26 offset:8192\n\t"
         "s_waitcnt lgkmcnt(0)"
-        : "=&v"(g0), "=&v"(g1), "=&v"(g2), "=&v"(g3), "=&v"(g4), "=&v"(g5), "=&v"(g6), "=&v"(g7), "=&v"(c0), "=&v"(c1),
-          "=&v"(c2), "=&v"(c3), "=&v"(e0), "=&v"(e1)
+        : "=&v"(g0), "=&v"(g1), "=&v"(g2), "=&v"(g3), "=&v"(g4), "=&v"(g5), "=&v"(g6), "=&v"(g7), "=&v"(h0), "=&v"(h1),
+          "=&v"(h2), "=&v"(h3), "=&v"(h4), "=&v"(h5), "=&v"(h6), "=&v"(h7), "=&v"(c0), "=&v"(c1), "=&v"(e0)
         : "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "v"(p[4]), "v"(p[5]), "v"(p[6]), "v"(p[7]), "v"(q[0]), "v"(q[1]), "v"(pe));
-    g[0] = g0; g[1] = g1; g[2] = g2; g[3] = g3; g[4] = g4; g[5] = g5; g[6] = g6; g[7] = g7;
-    c[0] = c0; c[1] = c1; c[2] = c2; c[3] = c3;
-    e[0] = e0; e[1] = e1;
+    g[0][0] = g0; g[0][1] = g1; g[0][2] = g2; g[0][3] = g3; g[0][4] = g4; g[0][5] = g5; g[0][6] = g6; g[0][7] = g7;
+    g[1][0] = h0; g[1][1] = h1; g[1][2] = h2; g[1][3] = h3; g[1][4] = h4; g[1][5] = h5; g[1][6] = h6; g[1][7] = h7;
+    c[0] = c0; c[1] = c1;
+    e = e0;
 }
 
-// The same with G's tile transposed: sixteen transposed 8-byte reads of 16-bit values, 4 rows
-// of 128 bytes apart each, give the eight fragments.
-__device__ __forceinline__ void lds_read_tr(uint32_t p, const uint32_t* q, uint32_t pe, u32x4* g, u32x4* c, uint32_t* e) {
-    u32x2 x0, x1, x2, x3, x4, x5, x6, x7, x8, x9, xa, xb, xc, xd, xe, xf;
-    u32x4 c0, c1, c2, c3;
-    uint32_t e0, e1;
+// Two chunks of codes and their scale word; and the eight fragments of 32 rows of G^T from
+// its tile as it lies: sixteen transposed 8-byte reads of 16-bit values, 4 rows of 128
+// bytes apart each.
+__device__ __forceinline__ void lds_read_codes(const uint32_t* q, uint32_t pe, u32x4* c, uint32_t& e) {
+    u32x4 c0, c1;
+    uint32_t e0;
     __asm__ volatile(
-        "ds_read_b32 %20, %25\n\t"
-        "ds_read_b32 %21, %25 offset:128\n\t"
-        "ds_read_b128 %16, %23\n\t"
-        "ds_read_b128 %18, %23 offset:4096\n\t"
-        "ds_read_b64_tr_b16 %0, %22\n\t"
-        "ds_read_b64_tr_b16 %1, %22 offset:512\n\t"
-        "ds_read_b64_tr_b16 %2, %22 offset:1024\n\t"
-        "ds_read_b64_tr_b16 %3, %22 offset:1536\n\t"
-        "ds_read_b64_tr_b16 %4, %22 offset:2048\n\t"
-        "ds_read_b64_tr_b16 %5, %22 offset:2560\n\t"
-        "ds_read_b64_tr_b16 %6, %22 offset:3072\n\t"
-        "ds_read_b64_tr_b16 %7, %22 offset:3584\n\t"
-        "ds_read_b128 %17, %24\n\t"
-        "ds_read_b128 %19, %24 offset:4096\n\t"
-        "ds_read_b64_tr_b16 %8, %22 offset:4096\n\t"
-        "ds_read_b64_tr_b16 %9, %22 offset:4608\n\t"
-        "ds_read_b64_tr_b16 %10, %22 offset:5120\n\t"
-        "ds_read_b64_tr_b16 %11, %22 offset:5632\n\t"
-        "ds_read_b64_tr_b16 %12, %22 offset:6144\n\t"
-        "ds_read_b64_tr_b16 %13, %22 offset:6656\n\t"
-        "ds_read_b64_tr_b16 %14, %22 offset:7168\n\t"
-        "ds_read_b64_tr_b16 %15, %22 offset:7680\n\t"
+        "ds_read_b32 %2, %5\n\t"
+        "ds_read_b128 %0, %3\n\t"
+        "ds_read_b128 %1, %4\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(c0), "=&v"(c1), "=&v"(e0)
+        : "v"(q[0]), "v"(q[1]), "v"(pe));
+    c[0] = c0; c[1] = c1;
+    e = e0;
+}
+__device__ __forceinline__ void lds_read_tr(uint32_t p, u32x4* g) {
+    u32x2 x0, x1, x2, x3, x4, x5, x6, x7, x8, x9, xa, xb, xc, xd, xe, xf;
+    __asm__ volatile(
+        "ds_read_b64_tr_b16 %0, %16\n\t"
+        "ds_read_b64_tr_b16 %1, %16 offset:512\n\t"
+        "ds_read_b64_tr_b16 %2, %16 offset:1024\n\t"
+        "ds_read_b64_tr_b16 %3, %16 offset:1536\n\t"
+        "ds_read_b64_tr_b16 %4, %16 offset:2048\n\t"
+        "ds_read_b64_tr_b16 %5, %16 offset:2560\n\t"
+        "ds_read_b64_tr_b16 %6, %16 offset:3072\n\t"
+        "ds_read_b64_tr_b16 %7, %16 offset:3584\n\t"
+        "ds_read_b64_tr_b16 %8, %16 offset:4096\n\t"
+        "ds_read_b64_tr_b16 %9, %16 offset:4608\n\t"
+        "ds_read_b64_tr_b16 %10, %16 offset:5120\n\t"
+        "ds_read_b64_tr_b16 %11, %16 offset:5632\n\t"
+        "ds_read_b64_tr_b16 %12, %16 offset:6144\n\t"
+        "ds_read_b64_tr_b16 %13, %16 offset:6656\n\t"
+        "ds_read_b64_tr_b16 %14, %16 offset:7168\n\t"
+        "ds_read_b64_tr_b16 %15, %16 offset:7680\n\t"
         "s_waitcnt lgkmcnt(0)"
         : "=&v"(x0), "=&v"(x1), "=&v"(x2), "=&v"(x3), "=&v"(x4), "=&v"(x5), "=&v"(x6), "=&v"(x7), "=&v"(x8), "=&v"(x9),
-          "=&v"(xa), "=&v"(xb), "=&v"(xc), "=&v"(xd), "=&v"(xe), "=&v"(xf), "=&v"(c0), "=&v"(c1), "=&v"(c2), "=&v"(c3),
-          "=&v"(e0), "=&v"(e1)
-        : "v"(p), "v"(q[0]), "v"(q[1]), "v"(pe));
+          "=&v"(xa), "=&v"(xb), "=&v"(xc), "=&v"(xd), "=&v"(xe), "=&v"(xf)
+        : "v"(p));
     g[0] = u32x4{x0.x, x0.y, x1.x, x1.y}; g[1] = u32x4{x2.x, x2.y, x3.x, x3.y};
     g[2] = u32x4{x4.x, x4.y, x5.x, x5.y}; g[3] = u32x4{x6.x, x6.y, x7.x, x7.y};
     g[4] = u32x4{x8.x, x8.y, x9.x, x9.y}; g[5] = u32x4{xa.x, xa.y, xb.x, xb.y};
     g[6] = u32x4{xc.x, xc.y, xd.x, xd.y}; g[7] = u32x4{xe.x, xe.y, xf.x, xf.y};
-    c[0] = c0; c[1] = c1; c[2] = c2; c[3] = c3;
-    e[0] = e0; e[1] = e1;
 }
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
