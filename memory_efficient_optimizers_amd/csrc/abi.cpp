@@ -526,11 +526,12 @@ struct HostPlan {
 // block i runs on XCD i % 8: every tile of a tensor runs on one XCD, whose L2
 // then fetches that tensor's shared operands once. Empty items (x = -1) pad the
 // shorter queues.
-void xcd_deal(std::vector<int2>& items) {
+template <class Same>
+void xcd_deal(std::vector<int2>& items, const Same& same) {
     std::vector<std::pair<size_t, size_t>> runs;
     for (size_t i = 0; i < items.size();) {
         size_t j = i;
-        while (j < items.size() && items[j].x == items[i].x) ++j;
+        while (j < items.size() && same(items[j], items[i])) ++j;
         if (items[i].x >= 0) runs.push_back({i, j});
         i = j;
     }
@@ -553,6 +554,10 @@ void xcd_deal(std::vector<int2>& items) {
     for (size_t r = 0; r < longest; ++r)
         for (int x = 0; x < kXcds; ++x) out.push_back(r < q[x].size() ? q[x][r] : make_int2(-1, -1));
     items.swap(out);
+}
+
+void xcd_deal(std::vector<int2>& items) {
+    xcd_deal(items, [](const int2& a, const int2& b) { return a.x == b.x; });
 }
 
 // Builds the launch tables of a list on the host (no device memory is touched or
@@ -1923,6 +1928,10 @@ void gx_lists(std::vector<GxDesc>& gd, std::vector<int2>* lists) {
                 for (int64_t k = 0; k < ceil_div(d.d, kGaWide); ++k)
                     lists[kGxBack + xb].push_back(make_int2(static_cast<int>(i), static_cast<int>(k * d.btj + c)));
         }
+        // the bands of a chunk on one XCD, whose L2 then fetches the chunk's part of N once
+        xcd_deal(lists[kGxBack + xb], [&](const int2& a, const int2& b) {
+            return a.x == b.x && a.y % gd[a.x].btj == b.y % gd[b.x].btj;
+        });
     }
 }
 

@@ -873,6 +873,7 @@ __global__ __launch_bounds__(512, 1) void k_gx_back(GxTable t, GaArgs a, int nri
     __shared__ __attribute__((aligned(16))) uint16_t nb1[2 * kUrN * 256];
     __shared__ __attribute__((aligned(16))) float exb[8 * 32 * 32];
     const int2 it = t.items[blockIdx.x];
+    if (it.x < 0) return;  // an empty item of the XCD-dealt list
     const GxDesc d = t.desc[it.x];
     if (it.x < nright) back_ur_item<false, XB, true>(d, it.y, a, nb0, nb1, exb);
     else back_ur_item<true, XB, true>(d, it.y, a, nb0, nb1, exb);
