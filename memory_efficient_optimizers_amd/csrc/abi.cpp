@@ -1702,7 +1702,7 @@ bool ga_left(const meo_galore_hparams* hp, const meo_tensor& t) {
 int64_t ga_rows(const meo_galore_hparams* hp, const meo_tensor& t) { return ga_left(hp, t) ? t.cols : t.rows; }   // D
 int64_t ga_basis(const meo_galore_hparams* hp, const meo_tensor& t) { return ga_left(hp, t) ? t.rows : t.cols; }  // d
 
-int32_t gx_pitch(int32_t r) { return (r + 15) / 16 * 16; }  // MX4 projectors: values per row of N's planes
+int32_t gx_pitch(int32_t r) { return (r + 31) / 32 * 32; }  // MX4 projectors: values per row of N's planes
 
 int64_t align256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 

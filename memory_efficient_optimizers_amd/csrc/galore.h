@@ -49,7 +49,7 @@ struct GxDesc : GDesc {
     const uint8_t* us;  // projector scales [r][nb]
     const uint8_t* gs;
     int32_t nb;         // blocks along d
-    int32_t rp;         // r rounded up to the matrix instruction's depth, 16
+    int32_t rp;         // r rounded up to 32: two of the back-projection's sub-steps
     int32_t tpi;        // back-projection: 64-row tiles of N per item
 };
 

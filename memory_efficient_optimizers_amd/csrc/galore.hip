@@ -568,15 +568,7 @@ __global__ __launch_bounds__(kBackThreads, Direct ? 3 : 1) void k_galore_back(GT
 // spends beyond that.
 constexpr int kUrN = kGaTile;           // rows of N per tile
 constexpr int kUrNDma = 2 * kUrN * (kGaWide / 8) / 64 / 8;  // 16-byte transfers per wave per tile: 8
-// A wave's 32 x 32 exchange block in LDS, unpadded: row r at row r ^ ((r >> 2) & 1), its
-// 16-byte chunk c at chunk c ^ ((r >> 1) & 1), so that neither the accumulator spill
-// (rows r and r + 4 at once) nor the 8-column gather (rows 4k .. 4k + 3) hits a bank twice.
-__device__ __forceinline__ int ur_ex(int r, int col) {
-    return ((r ^ ((r >> 2) & 1)) << 5) + ((((col >> 2) ^ ((r >> 1) & 1))) << 2) + (col & 3);
-}
-
-// pitch: values per row of N's planes, a multiple of 8.
-__device__ __forceinline__ void ur_stage(const GDesc& d, int pitch, int64_t n0, uint16_t* buf, int wave, int lane) {
+__device__ __forceinline__ void ur_stage(const GDesc& d, int64_t n0, uint16_t* buf, int wave, int lane) {
     // instruction j: rows 2j, 2j + 1 of one plane (plane = j / 32), 32 chunks each
 #pragma unroll
     for (int i = 0; i < kUrNDma; ++i) {
@@ -584,9 +576,9 @@ __device__ __forceinline__ void ur_stage(const GDesc& d, int pitch, int64_t n0, 
         const int plane = j >> 5, jr = j & 31;
         const int row = 2 * jr + (lane >> 5);       // 0 .. 63
         const int c = (lane & 31) ^ (row & 15);     // global chunk held at position lane & 31
-        const int cc = min(c, pitch / 8 - 1);
+        const int cc = min(c, d.r / 8 - 1);
         const int64_t grow = min(n0 + row, static_cast<int64_t>(d.D) - 1);
-        const uint16_t* src = (plane ? d.nl : d.nh) + grow * pitch + cc * 8;
+        const uint16_t* src = (plane ? d.nl : d.nh) + grow * d.r + cc * 8;
         __builtin_amdgcn_global_load_lds((const MEO_GLOBAL void*)src,
                                          (__attribute__((address_space(3))) void*)(buf + j * 512), 16, 0, 0);
     }
@@ -596,58 +588,29 @@ __device__ __forceinline__ bfv8 ur_frag(const uint16_t* plane, int row, int kk) 
     return *reinterpret_cast<const bfv8*>(plane + row * 256 + ((((kk >> 3) ^ (row & 15))) << 3));
 }
 
-// One item; nb0, nb1 and exb are the kernel's LDS.
-template <bool Left, bool XB, bool MX>
-__device__ __forceinline__ void back_ur_item(const DescOf<MX>& d, int item, const GaArgs& a, uint16_t* nb0, uint16_t* nb1,
-                                             float* exb) {
+template <bool Left, bool XB>
+__global__ __launch_bounds__(512, 1) void k_galore_back_ur(GTable t, GaArgs a) {
     static_assert(kUrNDma == 8, "wait counts below");
     constexpr int kP = XB ? 4 : 8;  // 16-byte parameter loads (and stores) per lane per tile
+    __shared__ __attribute__((aligned(16))) uint16_t nb0[2 * kUrN * 256];
+    __shared__ __attribute__((aligned(16))) uint16_t nb1[2 * kUrN * 256];
+    __shared__ __attribute__((aligned(16))) float exb[8 * 32 * 32];
+    const int2 it = t.items[blockIdx.x];
+    if (it.x < 0) return;  // an empty item of the XCD-dealt list
+    const GDesc d = t.desc[it.x];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int pitch, tpi;  // values per row of N's planes; tiles per item
-    if constexpr (MX) {
-        pitch = d.rp;
-        tpi = d.tpi;
-    } else {
-        pitch = d.r;
-        tpi = kUrTiles;
-    }
-    const int nc = d.btj;  // chunks of tpi tiles per band
-    const int band = item / nc, chunk = item % nc;
+    const int nc = d.btj;  // chunks of kUrTiles tiles per band
+    const int band = it.y / nc, chunk = it.y % nc;
     const int64_t u0 = static_cast<int64_t>(band) * kGaWide;
-    const int64_t nt0 = static_cast<int64_t>(chunk) * tpi;
-    const int ntiles = static_cast<int>(min<int64_t>(tpi, (d.D + kUrN - 1) / kUrN - nt0));
-    const int nks = pitch / 16;  // 16-wide contraction sub-steps
+    const int64_t nt0 = static_cast<int64_t>(chunk) * kUrTiles;
+    const int ntiles = static_cast<int>(min<int64_t>(kUrTiles, (d.D + kUrN - 1) / kUrN - nt0));
+    const int nks = d.r / 16;  // 16-wide contraction sub-steps
     using PT = typename std::conditional<XB, uint16_t, float>::type;
     PT* const x = static_cast<PT*>(d.x);
     // U fragments of the wave's 32 rows for the whole rank (64 VGPRs), landed before the
     // pipeline starts so that no wait inside it has to cover them
     bfv8 uf[16];
-    if constexpr (MX) {
-        // The wave's 32 rows of U are one block of each row of U^T: decoded into LDS as
-        // [r][32] (the stages are free yet) and read back transposed.
-        uint16_t* lu = (wave < 4 ? nb0 : nb1) + (wave & 3) * 8192;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = lane + 64 * j;
-            u32x4 c;
-            uint32_t e;
-            ld_mx_block(d, r, u0 / kMxBlock + wave, c, e);
-            const float sc = mx4_scale(e);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) st_lds8(lu + r * 32 + i * 8, mx4_to_bf16(c[i], sc));
-        }
-        __syncthreads();
-#pragma unroll
-        for (int ks = 0; ks < 16; ++ks) {
-            // as ld_frag_tr, rows of 32
-            const int g = lane >> 4, e = (lane >> 2) & 3, q = lane & 3;
-            const uint16_t* p = lu + (16 * ks + 8 * (g >> 1) + e) * 32 + 16 * (g & 1) + 4 * q;
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p + 4 * 32));
-            const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            uf[ks] = __builtin_bit_cast(bfv8, v);
-        }
-    } else {
+    {
         const int64_t row = min(u0 + wave * 32 + (lane & 31), static_cast<int64_t>(d.d) - 1);
 #pragma unroll
         for (int ks = 0; ks < 16; ++ks) {
@@ -658,7 +621,6 @@ __device__ __forceinline__ void back_ur_item(const DescOf<MX>& d, int item, cons
     MEO_WAIT_VM(0);
 #pragma unroll
     for (int ks = 0; ks < 16; ++ks) __asm__ volatile("" : "+v"(uf[ks]));
-    if constexpr (MX) __syncthreads();  // every wave has its fragments: the stages may be filled
     // W cells of the wave: two 32 x 32 blocks (blk: the tile's 32-row halves of N); in
     // block blk, lane holds rows (lane >> 2) + 16 q (q < 2), columns 8 (lane & 3) .. + 7.
     auto cell = [&](int64_t n0, int blk, int q, int64_t& row, int64_t& col) {
@@ -779,15 +741,6 @@ __device__ __forceinline__ void back_ur_item(const DescOf<MX>& d, int item, cons
                 } else {
                     if (row >= d.m || col >= d.n) continue;
                     PT* xp = x + row * d.n + col;
-                    if constexpr (MX) {  // only the edge is element-wise
-                        if (d.wvec && col + 8 <= d.n) {
-                            load_v8(x, row * d.n + col, kVec, true, XB, w);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) w[e] = a.decay * w[e] - a.coef * cq[e];
-                            store_v8(x, row * d.n + col, kVec, true, XB, w);
-                            continue;
-                        }
-                    }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         if (col + e >= d.n) continue;
@@ -824,8 +777,8 @@ __device__ __forceinline__ void back_ur_item(const DescOf<MX>& d, int item, cons
     // the first tile: the next stage's 8 and its kP loads, or no loads where the
     // parameter rows are not 16-byte aligned and load_w issues none).
     const int last = ntiles - 1;
-    ur_stage(d, pitch, nt0 * kUrN, nb0, wave, lane);
-    ur_stage(d, pitch, (nt0 + min(1, last)) * kUrN, nb1, wave, lane);
+    ur_stage(d, nt0 * kUrN, nb0, wave, lane);
+    ur_stage(d, (nt0 + min(1, last)) * kUrN, nb1, wave, lane);
     load_w(nt0 * kUrN);
     if (d.wvec) MEO_WAIT_VM(kP + 8);
     else MEO_WAIT_VM(8);
@@ -838,7 +791,7 @@ __device__ __forceinline__ void back_ur_item(const DescOf<MX>& d, int item, cons
         update((nt0 + i) * kUrN, exact);
         if (i + 1 >= ntiles) break;
         // tile i + 1 in nb1
-        ur_stage(d, pitch, (nt0 + min(i + 2, last)) * kUrN, nb0, wave, lane);
+        ur_stage(d, (nt0 + min(i + 2, last)) * kUrN, nb0, wave, lane);
         load_w((nt0 + i + 1) * kUrN);
         if (exact) MEO_WAIT_VM(2 * kP + 8);
         else MEO_WAIT_VM(0);
@@ -848,35 +801,12 @@ __device__ __forceinline__ void back_ur_item(const DescOf<MX>& d, int item, cons
         __builtin_amdgcn_s_barrier();
         update((nt0 + i + 1) * kUrN, exact);
         if (i + 2 >= ntiles) break;
-        ur_stage(d, pitch, (nt0 + min(i + 3, last)) * kUrN, nb1, wave, lane);
+        ur_stage(d, (nt0 + min(i + 3, last)) * kUrN, nb1, wave, lane);
         load_w((nt0 + i + 2) * kUrN);
         if (exact) MEO_WAIT_VM(2 * kP + 8);
         else MEO_WAIT_VM(0);
     }
     MEO_WAIT_VM(0);
-}
-
-template <bool Left, bool XB>
-__global__ __launch_bounds__(512, 1) void k_galore_back_ur(GTable t, GaArgs a) {
-    __shared__ __attribute__((aligned(16))) uint16_t nb0[2 * kUrN * 256];
-    __shared__ __attribute__((aligned(16))) uint16_t nb1[2 * kUrN * 256];
-    __shared__ __attribute__((aligned(16))) float exb[8 * 32 * 32];
-    const int2 it = t.items[blockIdx.x];
-    if (it.x < 0) return;  // an empty item of the XCD-dealt list
-    back_ur_item<Left, XB, false>(t.desc[it.x], it.y, a, nb0, nb1, exb);
-}
-
-// MX4 projectors: both sides in one launch, descriptors [0, nright) right-side ones.
-template <bool XB>
-__global__ __launch_bounds__(512, 1) void k_gx_back(GxTable t, GaArgs a, int nright) {
-    __shared__ __attribute__((aligned(16))) uint16_t nb0[2 * kUrN * 256];
-    __shared__ __attribute__((aligned(16))) uint16_t nb1[2 * kUrN * 256];
-    __shared__ __attribute__((aligned(16))) float exb[8 * 32 * 32];
-    const int2 it = t.items[blockIdx.x];
-    if (it.x < 0) return;  // an empty item of the XCD-dealt list
-    const GxDesc d = t.desc[it.x];
-    if (it.x < nright) back_ur_item<false, XB, true>(d, it.y, a, nb0, nb1, exb);
-    else back_ur_item<true, XB, true>(d, it.y, a, nb0, nb1, exb);
 }
 
 // m >= n back-projection of bf16 parameters, two blocks per CU. A block of 4 waves
@@ -1124,13 +1054,6 @@ void launch_galore_back(const GTable& t, int64_t n, const GaArgs& a, bool left, 
         if (direct) hipLaunchKernelGGL((k_galore_back<false, true>), grid, block, 0, s, t, a);
         else hipLaunchKernelGGL((k_galore_back<false, false>), grid, block, 0, s, t, a);
     }
-}
-
-void launch_gx_back(const GxTable& t, int64_t n, int nright, const GaArgs& a, bool xbf16, hipStream_t s) {
-    if (n <= 0) return;
-    const dim3 grid(static_cast<uint32_t>(n));
-    if (xbf16) hipLaunchKernelGGL(k_gx_back<true>, grid, dim3(512), 0, s, t, a, nright);
-    else hipLaunchKernelGGL(k_gx_back<false>, grid, dim3(512), 0, s, t, a, nright);
 }
 
 // ------------------------------------------------------------------ flat AdamW

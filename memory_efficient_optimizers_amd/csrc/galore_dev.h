@@ -94,10 +94,6 @@ struct TransStage {
     }
 };
 
-// Descriptor type of a step with a bf16 or an MX4 projector.
-template <bool MX>
-using DescOf = typename std::conditional<MX, GxDesc, GDesc>::type;
-
 // 8 codes times their scale as bf16 (exact: a code has two significant bits).
 __device__ __forceinline__ u32x4 mx4_to_bf16(uint32_t q, float scale) {
     return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 0)),
@@ -251,6 +247,13 @@ __device__ __forceinline__ void galore_adamw8(const GDesc& d, const GaArgs& a, i
                 *gst<uint16_t>(d.nl + idx + e) = static_cast<uint16_t>(bf16_bits(nl[e]));
             }
     }
+}
+
+// A wave's 32 x 32 exchange block in LDS, unpadded: row r at row r ^ ((r >> 2) & 1), its
+// 16-byte chunk c at chunk c ^ ((r >> 1) & 1), so that neither the accumulator spill
+// (rows r and r + 4 at once) nor the 8-column gather (rows 4k .. 4k + 3) hits a bank twice.
+__device__ __forceinline__ int ur_ex(int r, int col) {
+    return ((r ^ ((r >> 2) & 1)) << 5) + ((((col >> 2) ^ ((r >> 1) & 1))) << 2) + (col & 3);
 }
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));

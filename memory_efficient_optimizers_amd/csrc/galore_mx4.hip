@@ -33,18 +33,12 @@ __device__ __forceinline__ void gx_adamw8(const GxDesc& d, const GaArgs& a, int6
     }
     store_f8(d.em + idx, valid, d.rvec, m);
     store_f8(d.ev + idx, valid, d.rvec, v);
-    const int64_t at = row * d.rp + col;  // the planes are 256-byte aligned, rp a multiple of 16
+    const int64_t at = row * d.rp + col;  // the planes are 256-byte aligned, rp a multiple of 32
     *gst<u32x4>(d.nh + at) = pack_bf16x8(nh);
     *gst<u32x4>(d.nl + at) = pack_bf16x8(nl);
 }
 
 constexpr int kGxEx = 32 * 32;  // floats of a wave's exchange region
-
-// A wave's 32 x 32 exchange block, unpadded (as the back-projection's): conflict-free for
-// the accumulator spill and for the gather of 8 columns of a row.
-__device__ __forceinline__ int gx_ex(int r, int col) {
-    return ((r ^ ((r >> 2) & 1)) << 5) + ((((col >> 2) ^ ((r >> 1) & 1))) << 2) + (col & 3);
-}
 
 // A wave's piece of R at row i0, column c0: two 32 x 32 blocks, the second 32 columns on or
 // (Tall) 32 rows on. Lane l holds, in block b, rows (l >> 2) + 16 q and columns 8 (l & 3) .. + 7.
@@ -75,13 +69,13 @@ __device__ __forceinline__ void gx_epilogue(const GxDesc& d, const GaArgs& a, co
     for (int b = 0; b < 2; ++b) {
         const f32x16& acc = b ? a1 : a0;
 #pragma unroll
-        for (int w = 0; w < 16; ++w) lw[gx_ex(acc_row(w, lane), acc_col(lane))] = acc[w];
+        for (int w = 0; w < 16; ++w) lw[ur_ex(acc_row(w, lane), acc_col(lane))] = acc[w];
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int r = (lane >> 2) + 16 * q;
-            const f32x4 x0 = *reinterpret_cast<const f32x4*>(lw + gx_ex(r, c));
-            const f32x4 x1 = *reinterpret_cast<const f32x4*>(lw + gx_ex(r, c + 4));
+            const f32x4 x0 = *reinterpret_cast<const f32x4*>(lw + ur_ex(r, c));
+            const f32x4 x1 = *reinterpret_cast<const f32x4*>(lw + ur_ex(r, c + 4));
             const float rv[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
             const int64_t row = i0 + (Tall ? 32 * b : 0) + r;
             const int col = c0 + (Tall ? 0 : 32 * b) + c;
@@ -376,6 +370,272 @@ void launch_gx_project_mx4(const GxTable& t, int64_t n, const GaArgs& a, int for
         case kMxWide: hipLaunchKernelGGL((k_gx_project_mx4<1, 4, 8, false>), grid, dim3(512), 0, s, t, a); break;
         default: hipLaunchKernelGGL((k_gx_project_mx4<2, 4, 8, false>), grid, dim3(512), 0, s, t, a); break;
     }
+}
+
+// ------------------------------------------------------------------ back-projection + update
+
+// W <- decay W - coef N U^T (left: U N^T) with U decoded into registers. An item is a band of
+// 256 rows of U and up to tpi tiles of 64 rows of N. 8 waves: wave w holds the fragments of U
+// rows 32 w .. + 31 for the whole rank (64 VGPRs) and multiplies them by each tile of N.
+// N's two planes are staged by global_load_lds into one of two buffers (64 KB each: rows of
+// 256, chunk c of row r at c ^ (r & 15)), the next tile's while the current one is
+// multiplied; the parameter part of a tile is loaded a whole tile ahead. (64 rows of U per wave and
+// 32 of N read half as much LDS, but their 128 VGPRs of U leave no registers to read
+// fragments ahead: 144 instead of 130 us for the MLP matrices of a layer, bf16.)
+constexpr int kGbN = kGaTile;                                 // rows of N per tile
+constexpr int kGbDma = 2 * kGbN * (kGaWide / 8) / 512;        // 16-byte transfers per lane per tile: 8
+
+__device__ __forceinline__ void gb_stage(const GxDesc& d, int64_t n0, uint16_t* buf, int wave, int lane) {
+    // instruction j: rows 2 jr, 2 jr + 1 of plane j / 32 (jr = j % 32), 32 chunks each
+    __asm__ volatile("" : "+v"(lane));
+#pragma unroll
+    for (int i = 0; i < kGbDma; ++i) {
+        const int j = wave + 8 * i;
+        const int plane = j >> 5, jr = j & 31;
+        const int row = 2 * jr + (lane >> 5);
+        const int cc = min((lane & 31) ^ (row & 15), d.rp / 8 - 1);  // global chunk held at position lane & 31
+        const int64_t grow = min(n0 + row, static_cast<int64_t>(d.D) - 1);
+        const uint16_t* src = (plane ? d.nl : d.nh) + grow * d.rp + cc * 8;
+        __builtin_amdgcn_global_load_lds((const MEO_GLOBAL void*)src,
+                                         (__attribute__((address_space(3))) void*)(buf + j * 512), 16, 0, 0);
+    }
+}
+
+template <bool Left, bool XB>
+__device__ __forceinline__ void gb_item(const GxDesc& d, int item, const GaArgs& a, uint16_t* nb0, uint16_t* nb1, float* exb) {
+    static_assert(kGbDma == 8, "wait counts below");
+    constexpr int kP = XB ? 4 : 8;  // 16-byte parameter loads (and stores) per lane per tile
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int nc = d.btj;  // chunks of tpi tiles per band
+    const int band = item / nc, chunk = item % nc;
+    const int64_t u0 = static_cast<int64_t>(band) * kGaWide;
+    const int64_t nt0 = static_cast<int64_t>(chunk) * d.tpi;
+    const int ntiles = static_cast<int>(min<int64_t>(d.tpi, (d.D + kGbN - 1) / kGbN - nt0));
+    const int nks = d.rp / 16;  // 16-wide contraction sub-steps, an even number
+    using PT = typename std::conditional<XB, uint16_t, float>::type;
+    PT* const x = static_cast<PT*>(d.x);
+    // The wave's 32 rows of U are one block of each row of U^T: decoded into LDS as [r][32]
+    // (the stages are free yet) and read back transposed.
+    bfv8 uf[16];
+    {
+        uint16_t* lu = (wave < 4 ? nb0 : nb1) + (wave & 3) * 8192;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = lane + 64 * j;
+            u32x4 c;
+            uint32_t e;
+            ld_mx_block(d, r, u0 / kMxBlock + wave, c, e);
+            const float sc = mx4_scale(e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st_lds8(lu + r * 32 + i * 8, mx4_to_bf16(c[i], sc));
+        }
+        __syncthreads();
+        const int g = lane >> 4, e = (lane >> 2) & 3, q = lane & 3;
+#pragma unroll
+        for (int ks = 0; ks < 16; ++ks) {
+            const uint16_t* p = lu + (16 * ks + 8 * (g >> 1) + e) * 32 + 16 * (g & 1) + 4 * q;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p + 4 * 32));
+            const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            uf[ks] = __builtin_bit_cast(bfv8, v);
+        }
+    }
+    MEO_WAIT_VM(0);
+#pragma unroll
+    for (int ks = 0; ks < 16; ++ks) __asm__ volatile("" : "+v"(uf[ks]));
+    __syncthreads();  // every wave has its fragments: the stages may be filled
+    // W cells of the wave: two 32 x 32 blocks (nb: the tile's 32-row halves of N); in block nb,
+    // lane holds rows (lane >> 2) + 16 q (q < 2), columns 8 (lane & 3) .. + 7.
+    auto cell = [&](int64_t n0, int nb, int q, int64_t& row, int64_t& col) {
+        int ln = lane;
+        __asm__ volatile("" : "+v"(ln));
+        const int r = (ln >> 2) + 16 * q, c = 8 * (ln & 3);
+        if (Left) {  // rows from U, columns from N
+            row = u0 + wave * 32 + r;
+            col = n0 + nb * 32 + c;
+        } else {     // rows from N, columns from U
+            row = n0 + nb * 32 + r;
+            col = u0 + wave * 32 + c;
+        }
+    };
+    u32x4 w0[2][2][2], w1[2][2][2];  // even and odd tiles: [nb][q][16-byte half]
+    // exactly kP loads, rows and columns clamped into the tensor
+    auto load_w = [&](int64_t n0, u32x4 (&wp)[2][2][2]) {
+        if (!d.wvec) return;  // only 16-byte rows use them
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                int64_t row, col;
+                cell(n0, nb, q, row, col);
+                row = min(row, static_cast<int64_t>(d.m) - 1);
+                col = min(col, static_cast<int64_t>(d.n) - 8);
+                const PT* p = x + row * d.n + col;
+                wp[nb][q][0] = *gld<u32x4>(p);
+                if (!XB) wp[nb][q][1] = *gld<u32x4>(p + 4);
+            }
+    };
+    f32x16 acc[2];
+    auto multiply = [&](const uint16_t* buf) {
+        // Fragment reads in asm blocks that wait for their own reads (the compiler cannot tell
+        // which stage an LDS read hits). Two sub-steps per block; the low plane sits 32 KB
+        // after the high one, rows 32 on 16 KB (the same swizzle).
+        static_assert(kGbN * 256 * 2 == 32768, "offsets in the reads below");
+        const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(buf)) + (lane & 31) * 512;
+        const int sw = lane & 15;
+#pragma unroll
+        for (int ks = 0; ks < 16; ks += 2) {
+            if (ks >= nks) break;
+            int swv = sw;
+            __asm__ volatile("" : "+v"(swv));  // computed here, not hoisted and spilled
+            const uint32_t a0 = base + static_cast<uint32_t>(((2 * ks + (lane >> 5)) ^ swv) << 4);
+            const uint32_t a1 = base + static_cast<uint32_t>(((2 * ks + 2 + (lane >> 5)) ^ swv) << 4);
+            u32x4 h0, l0, h1, l1, h2, l2, h3, l3;
+            __asm__ volatile(
+                "ds_read_b128 %0, %8\n\t"
+                "ds_read_b128 %1, %8 offset:32768\n\t"
+                "ds_read_b128 %2, %8 offset:16384\n\t"
+                "ds_read_b128 %3, %8 offset:49152\n\t"
+                "ds_read_b128 %4, %9\n\t"
+                "ds_read_b128 %5, %9 offset:32768\n\t"
+                "ds_read_b128 %6, %9 offset:16384\n\t"
+                "ds_read_b128 %7, %9 offset:49152\n\t"
+                "s_waitcnt lgkmcnt(0)"
+                : "=&v"(h0), "=&v"(l0), "=&v"(h1), "=&v"(l1), "=&v"(h2), "=&v"(l2), "=&v"(h3), "=&v"(l3)
+                : "v"(a0), "v"(a1));
+            // [sub-step][plane][half of N]
+            const u32x4 f[2][2][2] = {{{h0, h1}, {l0, l1}}, {{h2, h3}, {l2, l3}}};
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int pl = 0; pl < 2; ++pl)
+#pragma unroll
+                    for (int nb = 0; nb < 2; ++nb) {
+                        const bfv8 fn = __builtin_bit_cast(bfv8, f[i][pl][nb]);
+                        acc[nb] = Left ? mfma32(uf[ks + i], fn, acc[nb]) : mfma32(fn, uf[ks + i], acc[nb]);
+                    }
+        }
+    };
+    // W <- decay W - coef C for a tile, through the wave's exchange region (one 32 x 32 block
+    // at a time, so that each lane ends with 8 consecutive columns of a row). exact: every
+    // cell inside the tensor and 16-byte rows, exactly kP 16-byte stores; otherwise a
+    // full wait after the stores.
+    auto update = [&](int64_t n0, bool exact, const u32x4 (&wp)[2][2][2]) {
+        int ln = lane;
+        __asm__ volatile("" : "+v"(ln));
+        float* lw = exb + wave * kGxEx;
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
+#pragma unroll
+            for (int v = 0; v < 16; ++v) lw[ur_ex(acc_row(v, ln), acc_col(ln))] = acc[nb][v];
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float cq[8], w[8];
+                {
+                    const int r = (ln >> 2) + 16 * q, c = 8 * (ln & 3);
+                    const f32x4 c0 = *reinterpret_cast<const f32x4*>(lw + ur_ex(r, c));
+                    const f32x4 c1 = *reinterpret_cast<const f32x4*>(lw + ur_ex(r, c + 4));
+                    cq[0] = c0.x; cq[1] = c0.y; cq[2] = c0.z; cq[3] = c0.w;
+                    cq[4] = c1.x; cq[5] = c1.y; cq[6] = c1.z; cq[7] = c1.w;
+                }
+                int64_t row, col;
+                cell(n0, nb, q, row, col);
+                if (exact) {
+                    PT* xp = x + row * d.n + col;
+                    if (XB) {
+                        bf16x8(wp[nb][q][0], w);
+                    } else {
+                        const u32x4 x0 = wp[nb][q][0], x1 = wp[nb][q][1];
+                        w[0] = __uint_as_float(x0.x); w[1] = __uint_as_float(x0.y);
+                        w[2] = __uint_as_float(x0.z); w[3] = __uint_as_float(x0.w);
+                        w[4] = __uint_as_float(x1.x); w[5] = __uint_as_float(x1.y);
+                        w[6] = __uint_as_float(x1.z); w[7] = __uint_as_float(x1.w);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = a.decay * w[e] - a.coef * cq[e];
+                    if (XB) {
+                        *gst<u32x4>(xp) = pack_bf16x8(w);
+                    } else {
+                        *gst<f32x4>(xp) = f32x4{w[0], w[1], w[2], w[3]};
+                        *gst<f32x4>(xp + 4) = f32x4{w[4], w[5], w[6], w[7]};
+                    }
+                } else {
+                    if (row >= d.m || col >= d.n) continue;
+                    const int64_t at = row * d.n + col;
+                    const int valid = static_cast<int>(min<int64_t>(d.n - col, 8));
+                    load_v8(x, at, valid, d.wvec, XB, w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = a.decay * w[e] - a.coef * cq[e];
+                    store_v8(x, at, valid, d.wvec, XB, w);
+                }
+            }
+            __builtin_amdgcn_wave_barrier();  // this block's gathers before the next block's spill
+        }
+        if (!exact) MEO_WAIT_VM(0);
+    };
+    auto zero = [&]() {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[b][v] = 0.0f;
+    };
+    // Exact counts need every tile of the item whole and 16-byte parameter rows.
+    const bool exact = d.wvec && (nt0 + ntiles) * kGbN <= d.D && u0 + kGaWide <= d.d;
+    // Tile i uses buffer i & 1. One barrier a tile: behind it stage i and the tile's parameters
+    // have landed for every wave and every wave has multiplied tile i - 1, so the stage and
+    // the parameters of tile i + 1 are fetched (past the last tile that one again, so counts
+    // stay fixed), with the whole of tile i to land; then a wave multiplies and updates without
+    // waiting for the others. Before the barrier only the update's kP stores may be in flight.
+    const int last = ntiles - 1;
+    gb_stage(d, nt0 * kGbN, nb0, wave, lane);
+    load_w(nt0 * kGbN, w0);
+    MEO_WAIT_VM(0);
+    auto tile = [&](int i, uint16_t* cur, uint16_t* next, u32x4 (&wc)[2][2][2], u32x4 (&wn)[2][2][2]) {
+        __asm__ volatile("s_barrier" ::: "memory");
+        gb_stage(d, (nt0 + min(i + 1, last)) * kGbN, next, wave, lane);
+        load_w((nt0 + min(i + 1, last)) * kGbN, wn);
+        zero();
+        multiply(cur);
+        update((nt0 + i) * kGbN, exact, wc);
+        if (exact) MEO_WAIT_VM(kP);
+        else MEO_WAIT_VM(0);
+        // the compiler's own wait for the loaded parameters goes here, where the order of what is
+        // in flight is plain to it
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                __asm__ volatile("" : "+v"(wn[nb][q][0]));
+                if (!XB) __asm__ volatile("" : "+v"(wn[nb][q][1]));
+            }
+    };
+    tile(0, nb0, nb1, w0, w1);
+    for (int i = 1; i < ntiles; i += 2) {
+        tile(i, nb1, nb0, w1, w0);
+        if (i + 1 >= ntiles) break;
+        tile(i + 1, nb0, nb1, w0, w1);
+    }
+    MEO_WAIT_VM(0);
+}
+
+template <bool XB>
+__global__ __launch_bounds__(512, 1) void k_gx_back(GxTable t, GaArgs a, int nright) {
+    __shared__ __attribute__((aligned(16))) uint16_t nb0[2 * kGbN * 256];
+    __shared__ __attribute__((aligned(16))) uint16_t nb1[2 * kGbN * 256];
+    __shared__ __attribute__((aligned(16))) float exb[8 * kGxEx];
+    const int2 it = t.items[blockIdx.x];
+    if (it.x < 0) return;  // an empty item of the XCD-dealt list
+    const GxDesc d = t.desc[it.x];
+    if (it.x < nright) gb_item<false, XB>(d, it.y, a, nb0, nb1, exb);
+    else gb_item<true, XB>(d, it.y, a, nb0, nb1, exb);
+}
+
+void launch_gx_back(const GxTable& t, int64_t n, int nright, const GaArgs& a, bool xbf16, hipStream_t s) {
+    if (n <= 0) return;
+    const dim3 grid(static_cast<uint32_t>(n));
+    if (xbf16) hipLaunchKernelGGL(k_gx_back<true>, grid, dim3(512), 0, s, t, a, nright);
+    else hipLaunchKernelGGL(k_gx_back<false>, grid, dim3(512), 0, s, t, a, nright);
 }
 
 }  // namespace meo
