@@ -520,7 +520,8 @@ __device__ __forceinline__ void gb_item(const GxDesc& d, int item, const GaArgs&
     // at a time, so that each lane ends with 8 consecutive columns of a row). exact: every
     // cell inside the tensor and 16-byte rows, exactly kP 16-byte stores; otherwise a
     // full wait after the stores.
-    auto update = [&](int64_t n0, bool exact, const u32x4 (&wp)[2][2][2]) {
+    auto update = [&](int64_t n0, auto ec, const u32x4 (&wp)[2][2][2]) {
+        constexpr bool exact = decltype(ec)::value;
         int ln = lane;
         __asm__ volatile("" : "+v"(ln));
         float* lw = exb + wave * kGxEx;
@@ -541,7 +542,7 @@ __device__ __forceinline__ void gb_item(const GxDesc& d, int item, const GaArgs&
                 }
                 int64_t row, col;
                 cell(n0, nb, q, row, col);
-                if (exact) {
+                if constexpr (exact) {
                     PT* xp = x + row * d.n + col;
                     if (XB) {
                         bf16x8(wp[nb][q][0], w);
@@ -572,7 +573,7 @@ __device__ __forceinline__ void gb_item(const GxDesc& d, int item, const GaArgs&
             }
             __builtin_amdgcn_wave_barrier();  // this block's gathers before the next block's spill
         }
-        if (!exact) MEO_WAIT_VM(0);
+        if constexpr (!exact) MEO_WAIT_VM(0);
     };
     auto zero = [&]() {
 #pragma unroll
@@ -582,40 +583,77 @@ __device__ __forceinline__ void gb_item(const GxDesc& d, int item, const GaArgs&
     };
     // Exact counts need every tile of the item whole and 16-byte parameter rows.
     const bool exact = d.wvec && (nt0 + ntiles) * kGbN <= d.D && u0 + kGaWide <= d.d;
-    // Tile i uses buffer i & 1. One barrier a tile: behind it stage i and the tile's parameters
-    // have landed for every wave and every wave has multiplied tile i - 1, so the stage and
-    // the parameters of tile i + 1 are fetched (past the last tile that one again, so counts
-    // stay fixed), with the whole of tile i to land; then a wave multiplies and updates without
-    // waiting for the others. Before the barrier only the update's kP stores may be in flight.
+    // Tile i uses buffer i & 1. One barrier a tile: behind it stage i has landed for every wave and
+    // every wave has multiplied tile i - 1, so the stage for tile i + 1 goes out (past the last
+    // tile that one again, so counts stay fixed). Waves 0 .. 3 then multiply tile i and update
+    // it; waves 4 .. 7 (the others of each SIMD) first update tile i - 1 and then multiply, so
+    // that one's products run beside the other's update (all in one order: 131 us for the
+    // MLP matrices of a layer, bf16). A tile's parameters are loaded a tile before their use.
     const int last = ntiles - 1;
-    gb_stage(d, nt0 * kGbN, nb0, wave, lane);
-    load_w(nt0 * kGbN, w0);
-    MEO_WAIT_VM(0);
-    auto tile = [&](int i, uint16_t* cur, uint16_t* next, u32x4 (&wc)[2][2][2], u32x4 (&wn)[2][2][2]) {
+    auto row0 = [&](int i) { return (nt0 + min(i, last)) * kGbN; };
+    auto sync_and_stage = [&](int i, uint16_t* next) {
         __asm__ volatile("s_barrier" ::: "memory");
-        gb_stage(d, (nt0 + min(i + 1, last)) * kGbN, next, wave, lane);
-        load_w((nt0 + min(i + 1, last)) * kGbN, wn);
-        zero();
-        multiply(cur);
-        update((nt0 + i) * kGbN, exact, wc);
-        if (exact) MEO_WAIT_VM(kP);
-        else MEO_WAIT_VM(0);
-        // the compiler's own wait for the loaded parameters goes here, where the order of what is
-        // in flight is plain to it
+        gb_stage(d, row0(i + 1), next, wave, lane);
+    };
+    // The compiler's own wait for loaded parameters, put where the order of what is in flight is
+    // plain to it.
+    auto landed = [&](u32x4 (&w)[2][2][2]) {
 #pragma unroll
         for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                __asm__ volatile("" : "+v"(wn[nb][q][0]));
-                if (!XB) __asm__ volatile("" : "+v"(wn[nb][q][1]));
+                __asm__ volatile("" : "+v"(w[nb][q][0]));
+                if (!XB) __asm__ volatile("" : "+v"(w[nb][q][1]));
             }
     };
-    tile(0, nb0, nb1, w0, w1);
-    for (int i = 1; i < ntiles; i += 2) {
-        tile(i, nb1, nb0, w1, w0);
-        if (i + 1 >= ntiles) break;
-        tile(i + 1, nb0, nb1, w0, w1);
-    }
+    gb_stage(d, row0(0), nb0, wave, lane);
+    load_w(row0(0), w0);
+    MEO_WAIT_VM(0);
+    auto run = [&](auto ec) {
+        constexpr bool kExact = decltype(ec)::value;
+        if (wave < 4) {
+            // before the barrier only the update's kP stores may be in flight
+            auto tile = [&](int i, uint16_t* cur, uint16_t* next, u32x4 (&wc)[2][2][2], u32x4 (&wn)[2][2][2]) {
+                sync_and_stage(i, next);
+                load_w(row0(i + 1), wn);
+                zero();
+                multiply(cur);
+                update(row0(i), ec, wc);
+                if constexpr (kExact) MEO_WAIT_VM(kP);
+                else MEO_WAIT_VM(0);
+                landed(wn);
+            };
+            tile(0, nb0, nb1, w0, w1);
+            for (int i = 1; i < ntiles; i += 2) {
+                tile(i, nb1, nb0, w1, w0);
+                if (i + 1 >= ntiles) break;
+                tile(i + 1, nb0, nb1, w0, w1);
+            }
+        } else {
+            // before the barrier the update's stores and the loads after them may be in flight
+            auto tile = [&](int i, uint16_t* cur, uint16_t* next, u32x4 (&wc)[2][2][2], u32x4 (&wn)[2][2][2], auto first) {
+                sync_and_stage(i, next);
+                if constexpr (!decltype(first)::value) update(row0(i - 1), ec, wn);
+                load_w(row0(i + 1), wn);
+                zero();
+                multiply(cur);
+                if constexpr (!kExact) MEO_WAIT_VM(0);
+                else if constexpr (decltype(first)::value) MEO_WAIT_VM(kP);
+                else MEO_WAIT_VM(2 * kP);
+                landed(wc);
+            };
+            tile(0, nb0, nb1, w0, w1, std::true_type{});
+            for (int i = 1; i < ntiles; i += 2) {
+                tile(i, nb1, nb0, w1, w0, std::false_type{});
+                if (i + 1 >= ntiles) break;
+                tile(i + 1, nb0, nb1, w0, w1, std::false_type{});
+            }
+            if (last & 1) update(row0(last), ec, w1);
+            else update(row0(last), ec, w0);
+        }
+    };
+    if (exact) run(std::true_type{});
+    else run(std::false_type{});
     MEO_WAIT_VM(0);
 }
 
