@@ -2044,7 +2044,6 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
                 w.cols = w.ld = q.d;
                 w.nb = d.nb;
                 w.bf16 = 1;
-                w.vec = q.d % 8 == 0;
                 quant.push_back(w);
             }
             const int id = static_cast<int>(rd.size());
@@ -2408,8 +2407,7 @@ int mx4_convert(int32_t n, const meo_mx4_matrix* ms, bool transposed, bool quant
         w.tiles_y = static_cast<uint32_t>(ceil_div(m.rows, kMxColRows));
         w.bf16 = m.dtype == MEO_BF16;
         const uintptr_t a = reinterpret_cast<uintptr_t>(m.data);
-        w.vec = transposed ? m.ld % 2 == 0 && a % (2 * elem_bytes(m.dtype)) == 0
-                           : aligned16(m.data) && m.ld % (w.bf16 ? 8 : 4) == 0;
+        w.pairs = m.ld % 2 == 0 && a % (2 * elem_bytes(m.dtype)) == 0;
         grid += blocks;
     }
     flush();

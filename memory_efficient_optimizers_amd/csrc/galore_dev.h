@@ -15,12 +15,14 @@ __device__ __forceinline__ f32x16 mfma32(const bfv8& a, const bfv8& b, const f32
 }
 
 // 8 bf16 (raw bits) of row `row` starting at column `col` of a row-major [rows][cols]
-// array; out-of-range elements read 0.
+// array; out-of-range elements read 0. Any: 16-byte loads at any address (`vec` ignored).
+template <bool Any = false>
 __device__ __forceinline__ u32x4 ld_row8(const uint16_t* p, int64_t rows, int64_t cols, int64_t row,
                                          int64_t col, bool vec) {
     if (row >= rows || col >= cols) return u32x4{0u, 0u, 0u, 0u};
     const uint16_t* q = p + row * cols + col;
-    if (vec && col + 8 <= cols) return *gld<u32x4>(q);
+    if (Any && col + 8 <= cols) return *gld<u32x4_any>(q);
+    if (!Any && vec && col + 8 <= cols) return *gld<u32x4>(q);
     const MEO_GLOBAL uint16_t* s = gld<uint16_t>(q);
     uint32_t w[4];
 #pragma unroll
@@ -44,7 +46,7 @@ __device__ __forceinline__ bfv8 ld_frag(const uint16_t* p) {
 // [rows][cols] bf16 array, zero outside it: loaded into registers first (all of a
 // thread's chunks in flight at once, and the next block's while the current one
 // is multiplied), then written to LDS (row pitch kGaPitch).
-template <int NROWS, int THREADS = kThreads>
+template <int NROWS, int THREADS = kThreads, bool Any = false>
 struct RowStage {
     static constexpr int kPer = NROWS * (kGaKb / 8) / THREADS;
     u32x4 v[kPer];
@@ -53,7 +55,7 @@ struct RowStage {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int c = threadIdx.x + i * THREADS;
-            v[i] = ld_row8(p, rows, cols, r0 + (c >> 3), k0 + (c & 7) * 8, vec);
+            v[i] = ld_row8<Any>(p, rows, cols, r0 + (c >> 3), k0 + (c & 7) * 8, vec);
         }
     }
     __device__ __forceinline__ void store(uint16_t* lds) const {
@@ -67,7 +69,7 @@ struct RowStage {
 
 // The transposed tile A[i][k] = G[k0 + k][i0 + i] (i < kGaTile, k < kGaKb) of the
 // row-major gradient G [K][D]: loaded along G's rows, scattered into LDS.
-template <int IROWS>
+template <int IROWS, bool Any = false>
 struct TransStage {
     static constexpr int kRowChunks = IROWS / 8;  // 16-byte chunks per row of G
     static constexpr int kPer = kGaKb * kRowChunks / kThreads;
@@ -76,7 +78,7 @@ struct TransStage {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int c = threadIdx.x + i * kThreads;
-            v[i] = ld_row8(g, K, D, k0 + c / kRowChunks, i0 + (c % kRowChunks) * 8, vec);
+            v[i] = ld_row8<Any>(g, K, D, k0 + c / kRowChunks, i0 + (c % kRowChunks) * 8, vec);
         }
     }
     __device__ __forceinline__ void store(uint16_t* lds) const {

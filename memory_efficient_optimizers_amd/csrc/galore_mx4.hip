@@ -31,8 +31,8 @@ __device__ __forceinline__ void gx_adamw8(const GxDesc& d, const GaArgs& a, int6
         nh[e] = round_bf16(n);
         nl[e] = n - nh[e];
     }
-    store_f8(d.em + idx, valid, d.rvec, m);
-    store_f8(d.ev + idx, valid, d.rvec, v);
+    store_any8(d.em, idx, valid, false, m);
+    store_any8(d.ev, idx, valid, false, v);
     const int64_t at = row * d.rp + col;  // the planes are 256-byte aligned, rp a multiple of 32
     *gst<u32x4>(d.nh + at) = pack_bf16x8(nh);
     *gst<u32x4>(d.nl + at) = pack_bf16x8(nl);
@@ -54,8 +54,8 @@ struct GxMoments {
                 const int64_t row = i0 + (Tall ? 32 * b : 0) + (lane >> 2) + 16 * q;
                 const int col = c0 + (Tall ? 0 : 32 * b) + 8 * (lane & 3);
                 const int valid = row < d.D ? min(max(d.r - col, 0), 8) : 0;
-                load_f8(d.em + row * d.r + col, valid, d.rvec, m[b][q]);
-                load_f8(d.ev + row * d.r + col, valid, d.rvec, v[b][q]);
+                load_any8(d.em, row * d.r + col, valid, false, m[b][q]);
+                load_any8(d.ev, row * d.r + col, valid, false, v[b][q]);
             }
     }
 };
@@ -100,7 +100,7 @@ __device__ __forceinline__ void zero_acc(f32x16 (&acc)[IB][2]) {
 
 // ------------------------------------------------------------------ bf16 gradient
 
-// Any shape and alignment: the register-staged projection of galore.hip (64 rows of R x all r
+// Any shape and alignment (16-byte loads at any address): the register-staged projection of galore.hip (64 rows of R x all r
 // columns per block, wave w columns 64 w .. 64 w + 63), U^T decoded into LDS.
 constexpr int kGxArena = (kGxFormRows[kGxAny] + kGaWide) * kGaPitch;
 template <bool Left>
@@ -113,11 +113,11 @@ __device__ __forceinline__ void gx_any_tile(const GxDesc& d, int64_t i0, const G
     const bool active = wave * 64 < d.r;
     f32x16 acc[2][2];
     zero_acc(acc);
-    typename std::conditional<Left, TransStage<kRows>, RowStage<kRows>>::type pa;
+    typename std::conditional<Left, TransStage<kRows, true>, RowStage<kRows, kThreads, true>>::type pa;
     MxRowStage pb;
     auto fetch = [&](int64_t k0) {
-        if constexpr (Left) pa.load(d.g, d.d, d.D, i0, k0, d.vec);
-        else pa.load(d.g, d.D, d.d, i0, k0, d.vec);
+        if constexpr (Left) pa.load(d.g, d.d, d.D, i0, k0, true);
+        else pa.load(d.g, d.D, d.d, i0, k0, true);
         pb.load(d, k0);
     };
     fetch(0);
@@ -461,7 +461,7 @@ __device__ __forceinline__ void gb_item(const GxDesc& d, int item, const GaArgs&
     u32x4 w0[2][2][2], w1[2][2][2];  // even and odd tiles: [nb][q][16-byte half]
     // exactly kP loads, rows and columns clamped into the tensor
     auto load_w = [&](int64_t n0, u32x4 (&wp)[2][2][2]) {
-        if (!d.wvec) return;  // only 16-byte rows use them
+        if (d.n < 8) return;
 #pragma unroll
         for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
@@ -471,8 +471,8 @@ __device__ __forceinline__ void gb_item(const GxDesc& d, int item, const GaArgs&
                 row = min(row, static_cast<int64_t>(d.m) - 1);
                 col = min(col, static_cast<int64_t>(d.n) - 8);
                 const PT* p = x + row * d.n + col;
-                wp[nb][q][0] = *gld<u32x4>(p);
-                if (!XB) wp[nb][q][1] = *gld<u32x4>(p + 4);
+                wp[nb][q][0] = *gld<u32x4_any>(p);
+                if (!XB) wp[nb][q][1] = *gld<u32x4_any>(p + 4);
             }
     };
     f32x16 acc[2];
@@ -518,8 +518,7 @@ __device__ __forceinline__ void gb_item(const GxDesc& d, int item, const GaArgs&
     };
     // W <- decay W - coef C for a tile, through the wave's exchange region (one 32 x 32 block
     // at a time, so that each lane ends with 8 consecutive columns of a row). exact: every
-    // cell inside the tensor and 16-byte rows, exactly kP 16-byte stores; otherwise a
-    // full wait after the stores.
+    // cell inside the tensor, exactly kP 16-byte stores; otherwise a full wait after them.
     auto update = [&](int64_t n0, auto ec, const u32x4 (&wp)[2][2][2]) {
         constexpr bool exact = decltype(ec)::value;
         int ln = lane;
@@ -556,19 +555,19 @@ __device__ __forceinline__ void gb_item(const GxDesc& d, int item, const GaArgs&
 #pragma unroll
                     for (int e = 0; e < 8; ++e) w[e] = a.decay * w[e] - a.coef * cq[e];
                     if (XB) {
-                        *gst<u32x4>(xp) = pack_bf16x8(w);
+                        *gst<u32x4_any>(xp) = pack_bf16x8(w);
                     } else {
-                        *gst<f32x4>(xp) = f32x4{w[0], w[1], w[2], w[3]};
-                        *gst<f32x4>(xp + 4) = f32x4{w[4], w[5], w[6], w[7]};
+                        *gst<f32x4_any>(xp) = f32x4{w[0], w[1], w[2], w[3]};
+                        *gst<f32x4_any>(xp + 4) = f32x4{w[4], w[5], w[6], w[7]};
                     }
                 } else {
                     if (row >= d.m || col >= d.n) continue;
                     const int64_t at = row * d.n + col;
                     const int valid = static_cast<int>(min<int64_t>(d.n - col, 8));
-                    load_v8(x, at, valid, d.wvec, XB, w);
+                    load_any8(x, at, valid, XB, w);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) w[e] = a.decay * w[e] - a.coef * cq[e];
-                    store_v8(x, at, valid, d.wvec, XB, w);
+                    store_any8(x, at, valid, XB, w);
                 }
             }
             __builtin_amdgcn_wave_barrier();  // this block's gathers before the next block's spill
@@ -581,8 +580,8 @@ __device__ __forceinline__ void gb_item(const GxDesc& d, int item, const GaArgs&
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[b][v] = 0.0f;
     };
-    // Exact counts need every tile of the item whole and 16-byte parameter rows.
-    const bool exact = d.wvec && (nt0 + ntiles) * kGbN <= d.D && u0 + kGaWide <= d.d;
+    // Exact counts need every tile of the item whole.
+    const bool exact = d.n >= 8 && (nt0 + ntiles) * kGbN <= d.D && u0 + kGaWide <= d.d;
     // Tile i uses buffer i & 1. One barrier a tile: behind it stage i has landed for every wave and
     // every wave has multiplied tile i - 1, so the stage for tile i + 1 goes out (past the last
     // tile that one again, so counts stay fixed). Waves 0 .. 3 then multiply tile i and update

@@ -26,7 +26,7 @@ struct MxMat {
     uint32_t first;      // the matrix's first block in the launch
     uint32_t tiles_y;    // transposed: tiles along rows
     int32_t bf16;        // values are bf16 (else fp32)
-    int32_t vec;         // plain: rows of values allow 16-byte accesses; transposed: pairs
+    int32_t pairs;       // transposed: adjacent values of even columns allow one access
 };
 
 template <int N>
@@ -89,6 +89,57 @@ __device__ __forceinline__ f32x16 mfma_mx4(const u32x4& a, const u32x4& b, const
     const i32x8 x = {static_cast<int>(a.x), static_cast<int>(a.y), static_cast<int>(a.z), static_cast<int>(a.w), 0, 0, 0, 0};
     const i32x8 y = {static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w), 0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, T, sa, T, sb);
+}
+
+// 16-byte accesses at any element's address (the GPU's unaligned access mode): rows of any
+// length and views of any offset move as whole ones do.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
+// 8 values of an fp32 or bf16 array at element i, widened to fp32; the first `valid` of them are
+// in range, the rest read 0. And the same stored, bf16 rounded to nearest even.
+__device__ __forceinline__ void load_any8(const void* p, int64_t i, int valid, bool bf16, float* f) {
+    if (bf16) {
+        const uint16_t* q = static_cast<const uint16_t*>(p) + i;
+        if (valid == kVec) {
+            bf16x8(*gld<u32x4_any>(q), f);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) f[e] = e < valid ? __uint_as_float(static_cast<uint32_t>(*gld<uint16_t>(q + e)) << 16) : 0.0f;
+        }
+    } else {
+        const float* q = static_cast<const float*>(p) + i;
+        if (valid == kVec) {
+            const f32x4 a = *gld<f32x4_any>(q), b = *gld<f32x4_any>(q + 4);
+            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+            f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) f[e] = e < valid ? *gld<float>(q + e) : 0.0f;
+        }
+    }
+}
+__device__ __forceinline__ void store_any8(void* p, int64_t i, int valid, bool bf16, const float* f) {
+    if (bf16) {
+        uint16_t* q = static_cast<uint16_t*>(p) + i;
+        if (valid == kVec) {
+            *gst<u32x4_any>(q) = pack_bf16x8(f);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e)
+                if (e < valid) *gst<uint16_t>(q + e) = static_cast<uint16_t>(bf16_bits(f[e]));
+        }
+    } else {
+        float* q = static_cast<float*>(p) + i;
+        if (valid == kVec) {
+            *gst<f32x4_any>(q) = f32x4{f[0], f[1], f[2], f[3]};
+            *gst<f32x4_any>(q + 4) = f32x4{f[4], f[5], f[6], f[7]};
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e)
+                if (e < valid) *gst<float>(q + e) = f[e];
+        }
+    }
 }
 
 // 2^(e - 127) as fp32: e = 0 is a subnormal, e = 255 a NaN.

@@ -41,7 +41,7 @@ __device__ __forceinline__ void quantize_rows(const MxMat& m, uint32_t tile) {
         const bool in = q < total;
         const int64_t row = in ? q / m.nb : 0, col = (in ? q - row * m.nb : 0) * kMxBlock + sub * kVec;
         const int valid = in ? static_cast<int>(min<int64_t>(max<int64_t>(m.cols - col, 0), kVec)) : 0;
-        load_v8(m.data, row * m.ld + col, valid, m.vec, BF, v[k]);
+        load_any8(m.data, row * m.ld + col, valid, BF, v[k]);
     }
 #pragma unroll
     for (int k = 0; k < kMxRowIters; ++k) {
@@ -85,7 +85,7 @@ __device__ __forceinline__ void dequantize_rows(const MxMat& m, uint32_t tile) {
         const int valid = static_cast<int>(min<int64_t>(max<int64_t>(m.cols - col, 0), kVec));
         float v[kVec];
         mx4_unpack8(c[k], mx4_scale(s[k]), v);
-        store_v8(const_cast<void*>(m.data), row * m.ld + col, valid, m.vec, BF, v);
+        store_any8(const_cast<void*>(m.data), row * m.ld + col, valid, BF, v);
     }
 }
 
@@ -139,7 +139,7 @@ __device__ __forceinline__ void quantize_cols(const MxMat& m, uint32_t tile, uin
     const int64_t row = r0 + 2 * lane, kb = k0 + wave;
     const int valid = static_cast<int>(min<int64_t>(max<int64_t>(m.rows - row, 0), 2));
     float x[kMxBlock], y[kMxBlock];
-    if (m.vec && r0 + kMxColRows <= m.rows && (k0 + kMxColBlocks) * kMxBlock <= m.cols) {
+    if (m.pairs && r0 + kMxColRows <= m.rows && (k0 + kMxColBlocks) * kMxBlock <= m.cols) {
 #pragma unroll
         for (int i = 0; i < kMxBlock; ++i) load_pair<BF, true>(m, kb * kMxBlock + i, row, 2, x[i], y[i]);
     } else {
@@ -223,7 +223,7 @@ __device__ __forceinline__ void dequantize_cols(const MxMat& m, uint32_t tile, u
             const int64_t at = k * m.ld + row;
             if (BF) {
                 uint16_t* p = static_cast<uint16_t*>(const_cast<void*>(m.data)) + at;
-                if (m.vec && valid == 2) {
+                if (m.pairs && valid == 2) {
                     *gst<uint32_t>(p) = bf16_bits(x[e]) | (bf16_bits(y[e]) << 16);
                 } else {
                     *gst<uint16_t>(p) = static_cast<uint16_t>(bf16_bits(x[e]));
@@ -231,7 +231,7 @@ __device__ __forceinline__ void dequantize_cols(const MxMat& m, uint32_t tile, u
                 }
             } else {
                 float* p = static_cast<float*>(const_cast<void*>(m.data)) + at;
-                if (m.vec && valid == 2) {
+                if (m.pairs && valid == 2) {
                     *gst<f32x2>(p) = f32x2{x[e], y[e]};
                 } else {
                     *gst<float>(p) = x[e];
