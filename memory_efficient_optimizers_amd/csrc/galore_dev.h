@@ -46,7 +46,7 @@ __device__ __forceinline__ bfv8 ld_frag(const uint16_t* p) {
 // [rows][cols] bf16 array, zero outside it: loaded into registers first (all of a
 // thread's chunks in flight at once, and the next block's while the current one
 // is multiplied), then written to LDS (row pitch kGaPitch).
-template <int NROWS, int THREADS = kThreads, bool Any = false>
+template <int NROWS, int THREADS = kThreads>
 struct RowStage {
     static constexpr int kPer = NROWS * (kGaKb / 8) / THREADS;
     u32x4 v[kPer];
@@ -55,7 +55,7 @@ struct RowStage {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int c = threadIdx.x + i * THREADS;
-            v[i] = ld_row8<Any>(p, rows, cols, r0 + (c >> 3), k0 + (c & 7) * 8, vec);
+            v[i] = ld_row8(p, rows, cols, r0 + (c >> 3), k0 + (c & 7) * 8, vec);
         }
     }
     __device__ __forceinline__ void store(uint16_t* lds) const {
@@ -69,7 +69,7 @@ struct RowStage {
 
 // The transposed tile A[i][k] = G[k0 + k][i0 + i] (i < kGaTile, k < kGaKb) of the
 // row-major gradient G [K][D]: loaded along G's rows, scattered into LDS.
-template <int IROWS, bool Any = false>
+template <int IROWS>
 struct TransStage {
     static constexpr int kRowChunks = IROWS / 8;  // 16-byte chunks per row of G
     static constexpr int kPer = kGaKb * kRowChunks / kThreads;
@@ -78,7 +78,7 @@ struct TransStage {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int c = threadIdx.x + i * kThreads;
-            v[i] = ld_row8<Any>(g, K, D, k0 + c / kRowChunks, i0 + (c % kRowChunks) * 8, vec);
+            v[i] = ld_row8(g, K, D, k0 + c / kRowChunks, i0 + (c % kRowChunks) * 8, vec);
         }
     }
     __device__ __forceinline__ void store(uint16_t* lds) const {
@@ -112,31 +112,6 @@ __device__ __forceinline__ void ld_mx_block(const GxDesc& d, int64_t row, int64_
     c = *gld<u32x4>(d.uc + (row * d.nb + kb) * 16);
     e = *gld<uint8_t>(d.us + row * d.nb + kb);
 }
-
-// All rows (up to kGaWide) of U^T x contraction columns [k0, k0 + kGaKb) of an MX4
-// projector, decoded to bf16 on the way into LDS (the layout of RowStage).
-struct MxRowStage {
-    static constexpr int kPer = kGaWide * (kGaKb / kMxBlock) / kThreads;
-    u32x4 c[kPer];
-    uint32_t e[kPer];
-    __device__ __forceinline__ void load(const GxDesc& d, int64_t k0) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int u = threadIdx.x + i * kThreads;
-            ld_mx_block(d, u >> 1, k0 / kMxBlock + (u & 1), c[i], e[i]);
-        }
-    }
-    __device__ __forceinline__ void store(uint16_t* lds) const {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int u = threadIdx.x + i * kThreads;
-            const float s = mx4_scale(e[i]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                st_lds8(lds + (u >> 1) * kGaPitch + (u & 1) * kMxBlock + 8 * j, mx4_to_bf16(c[i][j], s));
-        }
-    }
-};
 
 // Accumulator element v of a 32x32 block held by `lane`: row and column in the block.
 __device__ __forceinline__ int acc_row(int v, int lane) { return 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3); }

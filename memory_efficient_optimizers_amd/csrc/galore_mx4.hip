@@ -100,78 +100,18 @@ __device__ __forceinline__ void zero_acc(f32x16 (&acc)[IB][2]) {
 
 // ------------------------------------------------------------------ bf16 gradient
 
-// Any shape and alignment (16-byte loads at any address): the register-staged projection of galore.hip (64 rows of R x all r
-// columns per block, wave w columns 64 w .. 64 w + 63), U^T decoded into LDS.
-constexpr int kGxArena = (kGxFormRows[kGxAny] + kGaWide) * kGaPitch;
-template <bool Left>
-__device__ __forceinline__ void gx_any_tile(const GxDesc& d, int64_t i0, const GaArgs& a, uint16_t* arena) {
-    constexpr int kRows = kGxFormRows[kGxAny];
-    static_assert(kGxArena * 2 >= kWaves * kGxEx * 4, "exchange space");
-    uint16_t* sa = arena;
-    uint16_t* sb = arena + kRows * kGaPitch;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const bool active = wave * 64 < d.r;
-    f32x16 acc[2][2];
-    zero_acc(acc);
-    typename std::conditional<Left, TransStage<kRows, true>, RowStage<kRows, kThreads, true>>::type pa;
-    MxRowStage pb;
-    auto fetch = [&](int64_t k0) {
-        if constexpr (Left) pa.load(d.g, d.d, d.D, i0, k0, true);
-        else pa.load(d.g, d.D, d.d, i0, k0, true);
-        pb.load(d, k0);
-    };
-    fetch(0);
-    for (int64_t k0 = 0; k0 < d.d; k0 += kGaKb) {
-        pa.store(sa);
-        pb.store(sb);
-        __syncthreads();
-        if (k0 + kGaKb < d.d) fetch(k0 + kGaKb);
-        if (active) {
-#pragma unroll
-            for (int ks = 0; ks < kGaKb; ks += 16) {
-                const int kk = ks + 8 * (lane >> 5);
-                bfv8 fa[2], fb[2];
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    fa[b] = ld_frag(sa + (b * 32 + (lane & 31)) * kGaPitch + kk);
-                    fb[b] = ld_frag(sb + (wave * 64 + b * 32 + (lane & 31)) * kGaPitch + kk);
-                }
-#pragma unroll
-                for (int ib = 0; ib < 2; ++ib)
-#pragma unroll
-                    for (int jb = 0; jb < 2; ++jb) acc[ib][jb] = mfma32(fa[ib], fb[jb], acc[ib][jb]);
-            }
-        }
-        __syncthreads();
-    }
-    if (!active) return;
-    float* lw = reinterpret_cast<float*>(arena) + wave * kGxEx;
-#pragma unroll
-    for (int ib = 0; ib < 2; ++ib) {
-        GxMoments<false> mv;
-        mv.load(d, i0 + ib * 32, wave * 64, lane);
-        gx_epilogue(d, a, acc[ib][0], acc[ib][1], mv, i0 + ib * 32, wave * 64, lw, lane);
-    }
-}
-
-__global__ __launch_bounds__(kThreads, 3) void k_gx_project(GxTable t, GaArgs a, int nright) {
-    __shared__ __attribute__((aligned(16))) uint16_t arena[kGxArena];
-    const int2 it = t.items[blockIdx.x];
-    const GxDesc d = t.desc[it.x];
-    const int64_t i0 = static_cast<int64_t>(it.y) * kGxFormRows[kGxAny];
-    if (it.x < nright) gx_any_tile<false>(d, i0, a, arena);
-    else gx_any_tile<true>(d, i0, a, arena);
-}
-
-// d a multiple of 128, 16-byte rows of G and whole words of scales. 8 waves on 64 rows of R
-// x 256 columns, all rows and columns 32 w .. 32 w + 31 each: a wave's decoded codes then serve
-// two products, and no two waves decode the same. One contraction step is 128 long. Everything goes by global_load_lds, as in mx4_accumulate: waves 0 .. 3 fetch G's
-// tile (256-byte pieces of its rows; left: 128 rows of 128 bytes) into one of five stages,
-// four steps ahead, which keeps the 64 KB in flight that HBM takes per CU; waves 4 .. 7 the
-// codes of U^T of two steps (a whole 128-byte line of each of its 256 rows) and the
-// scales of four (a word per row and step) into one of two buffers each. (All waves
-// fetching all, two steps ahead, each step's codes and scales on their own: 84 us for
-// the four 4096 x 4096 matrices of a layer.) The codes are decoded as the fragments are read.
+// 8 waves on 64 rows of R x 256 columns, all rows and columns 32 w .. 32 w + 31 each: a wave's
+// decoded codes then serve two products, and no two waves decode the same. One contraction
+// step is 128 long. Waves 0 .. 3 fetch G's tile (256-byte pieces of its rows; left: 128 rows
+// of 128 bytes) into one of five LDS stages, waves 4 .. 7 the codes of U^T of two steps (a
+// whole 128-byte line of each of its 256 rows) and the scales of four (a word per row and
+// step) into one of two buffers each; the codes are decoded as the fragments are read.
+// kGxDirect (d a multiple of 128, 16-byte rows of G, whole words of scales): everything by
+// global_load_lds, as in mx4_accumulate, G four steps ahead, which keeps the 64 KB in flight
+// that HBM takes per CU. kGxAny: G through registers two steps ahead, with 16-byte loads
+// at any address and zeros past its end; the scales through registers too; codes as there
+// (they are always aligned). (All waves fetching all, each step's codes and scales on
+// their own: 84 instead of 76 us for the four 4096 x 4096 matrices of a layer.)
 // Lane half h takes values 64 h .. 64 h + 63 of a step: two whole MX blocks, so a lane's
 // scale changes once per step.
 constexpr int kGdRows = kGxFormRows[kGxDirect];
@@ -183,8 +123,8 @@ constexpr int kGdCodes = kGaWide * kGdStep;      // bytes of codes of two steps
 constexpr int kGdScales = kGaWide * 4 * 4;       // bytes of scales of four: [word][row]
 constexpr int kGdLds = kGdDepth * kGdG + 2 * kGdCodes + 2 * kGdScales;
 
-template <bool Left>
-__device__ __forceinline__ void gx_direct_tile(const GxDesc& d, int64_t i0, const GaArgs& a, uint8_t* lds) {
+template <bool Left, bool Any>
+__device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArgs& a, uint8_t* lds) {
     constexpr int kA = kGdG / 1024 / 4, kB = kGdCodes / 1024 / 4;  // 1 KB transfers per wave of its kind
     static_assert(kGdWaves == 8 && kGdDepth * kGdG >= kGdWaves * kGxEx * 4, "waves below; exchange space");
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
@@ -215,11 +155,29 @@ __device__ __forceinline__ void gx_direct_tile(const GxDesc& d, int64_t i0, cons
         }
     }
     const int64_t gstep = static_cast<int64_t>(kGdStep) * 2 * (Left ? d.D : 1);
-    const int steps = d.d / kGdStep;
+    const int steps = (d.d + kGdStep - 1) / kGdStep;
     auto stage = [&](int k, uint8_t* s) {
         const uint8_t* gk = g + min(k, steps - 1) * gstep;  // past the end: the last again, for equal counts
 #pragma unroll
         for (int i = 0; i < kA; ++i) dma16(gk + ga[i], s + (fw + i * 4) * 1024);
+    };
+    // The same tile through registers: the thread's four chunks of a step, and their places.
+    auto load_g = [&](int k, u32x4 (&v)[kA]) {
+#pragma unroll
+        for (int i = 0; i < kA; ++i) {
+            const int j = fw + i * 4;
+            if constexpr (Left) v[i] = ld_row8<true>(d.g, d.d, d.D, static_cast<int64_t>(k) * kGdStep + 8 * j + (lane >> 3), i0 + (lane & 7) * 8, true);
+            else v[i] = ld_row8<true>(d.g, d.D, d.d, i0 + 4 * j + (lane >> 4), static_cast<int64_t>(k) * kGdStep + (lane & 15) * 8, true);
+        }
+    };
+    auto store_g = [&](const u32x4 (&v)[kA], uint8_t* s) {
+#pragma unroll
+        for (int i = 0; i < kA; ++i) {
+            const int j = fw + i * 4;
+            const int r = Left ? 8 * j + (lane >> 3) : 4 * j + (lane >> 4);
+            const int at = Left ? r * 128 + (((lane & 7) ^ lsw(r & 3)) << 4) : r * 256 + (((lane & 15) ^ (r & 15)) << 4);
+            *reinterpret_cast<u32x4*>(s + at) = v[i];
+        }
     };
     // Codes: transfer j holds rows 8 j + (l >> 3) of U^T, block (l & 7) ^ mx_swz(row).
     uint32_t ub[kB];
@@ -238,9 +196,12 @@ __device__ __forceinline__ void gx_direct_tile(const GxDesc& d, int64_t i0, cons
     uint8_t* const sbuf = cbuf + 2 * kGdCodes;
     auto scales = [&](int quad) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-            dma4(d.us + (us + static_cast<uint32_t>(min(16 * quad + 4 * w, d.nb - 4))),
-                 sbuf + (quad & 1) * kGdScales + w * (kGaWide * 4) + fw * 256);
+        for (int w = 0; w < 4; ++w) {
+            const int kb = 16 * quad + 4 * w;
+            uint8_t* s = sbuf + (quad & 1) * kGdScales + w * (kGaWide * 4) + fw * 256;
+            if constexpr (Any) *reinterpret_cast<uint32_t*>(s + lane * 4) = mx_scales4(d.us + us, kb, d.nb);
+            else dma4(d.us + (us + static_cast<uint32_t>(min(kb, d.nb - 4))), s);
+        }
     };
     const uint32_t base = lds_addr(lds);
     auto multiply = [&](int k, int cur) {
@@ -267,7 +228,12 @@ __device__ __forceinline__ void gx_direct_tile(const GxDesc& d, int64_t i0, cons
             lds_read_row(p, q, pe, x, c, e);
         }
         if (h) e >>= 16;
-        const float sc[2] = {mx4_scale(e & 255u), mx4_scale((e >> 8) & 255u)};
+        float sc[2] = {mx4_scale(e & 255u), mx4_scale((e >> 8) & 255u)};
+        if constexpr (Any) {  // past the end G is zero; codes and scales are whatever is there
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                if (4 * k + 2 * h + t >= d.nb) sc[t] = 1.0f;
+        }
 #pragma unroll
         for (int u = 0; u < 8; ++u) {  // 8 values: dword u & 3 of block u >> 2
             const bfv8 fb = __builtin_bit_cast(bfv8, mx4_to_bf16(c[u >> 2][u & 3], sc[u >> 2]));
@@ -276,35 +242,61 @@ __device__ __forceinline__ void gx_direct_tile(const GxDesc& d, int64_t i0, cons
         }
     };
     // Before step k's barrier a wave that fetches G waits until only steps k + 1 .. k + 3 are
-    // outstanding. One that fetches U^T issued the codes of a pair of steps in the even step
-    // before it and the scales of four steps two steps before them: before an even step it
-    // waits for all, before an odd one for nothing that step k - 1 issued. What a step fills
-    // was last read before its barrier.
+    // outstanding (Any: has stored step k). One that fetches U^T issued the codes of a pair of
+    // steps in the even step before it and the scales of four steps two steps before them:
+    // before an even step it waits for all, before an odd one for nothing that step k - 1
+    // issued. What a step fills was last read before its barrier.
     // The moments of the wave's piece of R are loaded before everything else.
     const bool active = cw < d.r;
     GxMoments<true> mv;
     if (active) mv.load(d, i0, cw, lane);
-    if (fetch_g) {
-#pragma unroll
-        for (int k = 0; k < kGdDepth - 1; ++k) stage(k, lds + k * kGdG);
-    } else {
+    auto next_u = [&](int k) {  // waves 4 .. 7, even steps
+        if ((k & 3) == 2) scales((k >> 2) + 1);
+        codes((k >> 1) + 1);
+    };
+    if (!fetch_g) {
         scales(0);
         codes(0);
     }
     int cur = 0;
-    for (int k = 0; k < steps; ++k) {
-        if (fetch_g) wait_and_sync<3 * kA>();
-        else if (!(k & 1)) wait_and_sync<0>();
-        else if ((k & 3) == 3) wait_and_sync<kB + 4>();
-        else wait_and_sync<kB>();
+    if constexpr (Any) {
+        u32x4 ve[kA], vo[kA];  // even and odd steps
         if (fetch_g) {
-            stage(k + kGdDepth - 1, lds + (cur == 0 ? kGdDepth - 1 : cur - 1) * kGdG);
-        } else if (!(k & 1)) {
-            if ((k & 3) == 2) scales((k >> 2) + 1);
-            codes((k >> 1) + 1);
+            load_g(0, ve);
+            load_g(1, vo);
+            store_g(ve, lds);
+            load_g(2, ve);
         }
-        if (active) multiply(k, cur);
-        cur = cur == kGdDepth - 1 ? 0 : cur + 1;
+        auto step = [&](int k, u32x4 (&v)[kA]) {
+            wait_lds_and_sync(!fetch_g && !(k & 1));
+            if (fetch_g) {
+                store_g(v, lds + (cur == kGdDepth - 1 ? 0 : cur + 1) * kGdG);
+                load_g(k + 3, v);
+            } else if (!(k & 1)) {
+                next_u(k);
+            }
+            if (active) multiply(k, cur);
+            cur = cur == kGdDepth - 1 ? 0 : cur + 1;
+        };
+        for (int k = 0; k < steps; k += 2) {
+            step(k, vo);
+            if (k + 1 < steps) step(k + 1, ve);
+        }
+    } else {
+        if (fetch_g) {
+#pragma unroll
+            for (int k = 0; k < kGdDepth - 1; ++k) stage(k, lds + k * kGdG);
+        }
+        for (int k = 0; k < steps; ++k) {
+            if (fetch_g) wait_and_sync<3 * kA>();
+            else if (!(k & 1)) wait_and_sync<0>();
+            else if ((k & 3) == 3) wait_and_sync<kB + 4>();
+            else wait_and_sync<kB>();
+            if (fetch_g) stage(k + kGdDepth - 1, lds + (cur == 0 ? kGdDepth - 1 : cur - 1) * kGdG);
+            else if (!(k & 1)) next_u(k);
+            if (active) multiply(k, cur);
+            cur = cur == kGdDepth - 1 ? 0 : cur + 1;
+        }
     }
     wait_and_sync<0>();
     if (!active) return;
@@ -312,20 +304,21 @@ __device__ __forceinline__ void gx_direct_tile(const GxDesc& d, int64_t i0, cons
     gx_epilogue(d, a, acc[0], acc[1], mv, i0, cw, lw, lane);
 }
 
-__global__ __launch_bounds__(kGdWaves * 64) void k_gx_project_direct(GxTable t, GaArgs a, int nright) {
+template <bool Any>
+__global__ __launch_bounds__(kGdWaves * 64) void k_gx_project(GxTable t, GaArgs a, int nright) {
     __shared__ __attribute__((aligned(128))) uint8_t lds[kGdLds];
     const int2 it = t.items[blockIdx.x];
     const GxDesc d = t.desc[it.x];
     const int64_t i0 = static_cast<int64_t>(it.y) * kGdRows;
-    if (it.x < nright) gx_direct_tile<false>(d, i0, a, lds);
-    else gx_direct_tile<true>(d, i0, a, lds);
+    if (it.x < nright) gx_tile<false, Any>(d, i0, a, lds);
+    else gx_tile<true, Any>(d, i0, a, lds);
 }
 
 void launch_gx_project(const GxTable& t, int64_t n, int nright, const GaArgs& a, int form, hipStream_t s) {
     if (n <= 0) return;
-    const dim3 grid(static_cast<uint32_t>(n)), wide(kGdWaves * 64);
-    if (form == kGxAny) hipLaunchKernelGGL(k_gx_project, grid, dim3(kThreads), 0, s, t, a, nright);
-    else hipLaunchKernelGGL(k_gx_project_direct, grid, wide, 0, s, t, a, nright);
+    const dim3 grid(static_cast<uint32_t>(n)), block(kGdWaves * 64);
+    if (form == kGxAny) hipLaunchKernelGGL(k_gx_project<true>, grid, block, 0, s, t, a, nright);
+    else hipLaunchKernelGGL(k_gx_project<false>, grid, block, 0, s, t, a, nright);
 }
 
 // ------------------------------------------------------------------ MX4 gradient

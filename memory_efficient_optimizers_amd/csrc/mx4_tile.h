@@ -184,6 +184,27 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));  // the low half of a generic LDS address
 }
 
+// The same where only the wave's own accesses to LDS, and (all) everything it issued, have to be
+// over.
+__device__ __forceinline__ void wait_lds_and_sync(bool all) {
+    if (all) __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    else __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+typedef uint32_t u32_any __attribute__((aligned(1)));
+
+// The scale bytes of blocks kb .. kb + 3 of a row of nb blocks; 0 past its end. Inside the row.
+__device__ __forceinline__ uint32_t mx_scales4(const uint8_t* row, int kb, int nb) {
+    if (kb >= nb) return 0;
+    if (nb >= 4) {
+        const int at = min(kb, nb - 4);
+        return *gld<u32_any>(row + at) >> (8 * (kb - at));
+    }
+    uint32_t w = 0;
+    for (int t = 0; t < nb; ++t) w |= static_cast<uint32_t>(*gld<uint8_t>(row + t)) << (8 * t);  // kb is 0
+    return w;
+}
+
 // A pointer that is the same in every lane, in scalar registers.
 __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
     const uint64_t v = reinterpret_cast<uint64_t>(p);
