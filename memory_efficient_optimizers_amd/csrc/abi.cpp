@@ -1871,17 +1871,18 @@ int check_galore_workspace(const meo_galore_hparams* hp, int32_t n, const meo_te
 constexpr int64_t kCus = 256;
 
 // Whether `tall` tiles of 128 rows take less time than `wide` of 64: a tile runs alone on its
-// CU, a tall one about 1.5 times as long.
-bool mx4_tall(int64_t tall, int64_t wide) { return 3 * ceil_div(tall, kCus) < 2 * ceil_div(wide, kCus); }
+// CU, a tall one 4/3 as long (rank 256, k = 4096: 32000 rows 33 and 47 us, 16384 rows 28 and
+// 25, 40000 rows 62 and 72).
+bool mx4_tall(int64_t tall, int64_t wide) { return 4 * ceil_div(tall, kCus) < 3 * ceil_div(wide, kCus); }
 
 // Items of a step with MX4 projectors over its descriptors; sets btj and tpi. The products'
 // form and the tiles per back-projection item follow the call's total work.
 void gx_lists(std::vector<GxDesc>& gd, std::vector<int2>* lists) {
-    auto words = [](const void* p, int32_t nb) { return nb % 4 == 0 && reinterpret_cast<uintptr_t>(p) % 4 == 0; };
-    auto direct = [&](const GxDesc& d) { return d.vec && d.d % 128 == 0 && words(d.us, d.nb); };
+    // (d a multiple of 128: whole words of scales)
+    auto direct = [](const GxDesc& d) { return d.vec && d.d % 128 == 0 && reinterpret_cast<uintptr_t>(d.us) % 4 == 0; };
     int64_t tall = 0, wide = 0;  // tiles of the MX4 gradients' wide products, 128 and 64 rows each
     for (const GxDesc& d : gd)
-        if (d.gs && words(d.us, d.nb) && words(d.gs, d.nb) && d.r > kMxFormCols[kMxNarrow]) {
+        if (d.gs && d.r > kMxFormCols[kMxNarrow]) {
             tall += ceil_div(d.D, kMxFormRows[kMxTall]);
             wide += ceil_div(d.D, kMxFormRows[kMxWide]);
         }
@@ -1889,10 +1890,7 @@ void gx_lists(std::vector<GxDesc>& gd, std::vector<int2>* lists) {
         const GxDesc& d = gd[i];
         int list, rows;
         if (d.gs) {
-            const int form = !words(d.us, d.nb) || !words(d.gs, d.nb) ? kMxAny
-                             : d.r <= kMxFormCols[kMxNarrow]          ? kMxNarrow
-                             : mx4_tall(tall, wide)                   ? kMxTall
-                                                                      : kMxWide;
+            const int form = d.r <= kMxFormCols[kMxNarrow] ? kMxNarrow : mx4_tall(tall, wide) ? kMxTall : kMxWide;
             list = kGxProjM + form;
             rows = kMxFormRows[form];
         } else {
@@ -2003,7 +2001,7 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
             if (mx) {
                 d.uc = static_cast<const uint8_t*>(s.uc);
                 d.us = static_cast<const uint8_t*>(s.us);
-                d.gs = static_cast<const uint8_t*>(s.gs);
+                d.gs = g4 ? static_cast<const uint8_t*>(s.gs) : nullptr;
                 d.nb = static_cast<int32_t>(ceil_div(d.d, kMxBlock));
                 d.vec = aligned16(d.g) && d.n % 8 == 0;  // 16-byte rows of a bf16 gradient
             }
@@ -2416,9 +2414,6 @@ int mx4_convert(int32_t n, const meo_mx4_matrix* ms, bool transposed, bool quant
 
 // The tile form of a product (launch_mx4_matmul).
 MxForm mx4_form(const meo_mx4_product& q) {
-    const int64_t nb = ceil_div(q.k, kMxBlock);
-    if (nb == 0 || nb % 4 != 0 || reinterpret_cast<uintptr_t>(q.a_scales) % 4 || reinterpret_cast<uintptr_t>(q.b_scales) % 4)
-        return kMxAny;
     if (q.n <= kMxFormCols[kMxNarrow]) return kMxNarrow;
     const int64_t tn = ceil_div(q.n, kMxFormCols[kMxWide]);
     return mx4_tall(ceil_div(q.m, kMxFormRows[kMxTall]) * tn, ceil_div(q.m, kMxFormRows[kMxWide]) * tn) ? kMxTall : kMxWide;

@@ -194,14 +194,21 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
     // Scales: wave 4 + f fetches the words of rows 64 f + l.
     const uint32_t us = static_cast<uint32_t>(min(64 * fw + lane, d.r - 1)) * d.nb;
     uint8_t* const sbuf = cbuf + 2 * kGdCodes;
+    uint32_t sw4[4];  // Any: of the quad that is stored next
     auto scales = [&](int quad) {
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             const int kb = 16 * quad + 4 * w;
-            uint8_t* s = sbuf + (quad & 1) * kGdScales + w * (kGaWide * 4) + fw * 256;
-            if constexpr (Any) *reinterpret_cast<uint32_t*>(s + lane * 4) = mx_scales4(d.us + us, kb, d.nb);
-            else dma4(d.us + (us + static_cast<uint32_t>(min(kb, d.nb - 4))), s);
+            if constexpr (Any) sw4[w] = mx_scales_load(d.us + us, kb, d.nb);
+            else dma4(d.us + (us + static_cast<uint32_t>(min(kb, d.nb - 4))),
+                      sbuf + (quad & 1) * kGdScales + w * (kGaWide * 4) + fw * 256);
         }
+    };
+    auto store_scales = [&](int quad) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            *reinterpret_cast<uint32_t*>(sbuf + (quad & 1) * kGdScales + w * (kGaWide * 4) + fw * 256 + lane * 4) =
+                mx_scales_take(sw4[w], 16 * quad + 4 * w, d.nb);
     };
     const uint32_t base = lds_addr(lds);
     auto multiply = [&](int k, int cur) {
@@ -251,11 +258,17 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
     GxMoments<true> mv;
     if (active) mv.load(d, i0, cw, lane);
     auto next_u = [&](int k) {  // waves 4 .. 7, even steps
-        if ((k & 3) == 2) scales((k >> 2) + 1);
+        if constexpr (Any) {  // loaded two steps before they are stored
+            if (k & 2) store_scales((k >> 2) + 1);
+            else if (d.nb >= 4) scales((k >> 2) + 1);
+        } else {
+            if (k & 2) scales((k >> 2) + 1);
+        }
         codes((k >> 1) + 1);
     };
     if (!fetch_g) {
         scales(0);
+        if constexpr (Any) store_scales(0);
         codes(0);
     }
     int cur = 0;
@@ -267,20 +280,26 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
             store_g(ve, lds);
             load_g(2, ve);
         }
-        auto step = [&](int k, u32x4 (&v)[kA]) {
-            wait_lds_and_sync(!fetch_g && !(k & 1));
-            if (fetch_g) {
+        // (two loops, as in mx4_accumulate)
+        if (fetch_g) {
+            auto step = [&](int k, u32x4 (&v)[kA]) {
+                wait_lds_and_sync(false);
                 store_g(v, lds + (cur == kGdDepth - 1 ? 0 : cur + 1) * kGdG);
                 load_g(k + 3, v);
-            } else if (!(k & 1)) {
-                next_u(k);
+                if (active) multiply(k, cur);
+                cur = cur == kGdDepth - 1 ? 0 : cur + 1;
+            };
+            for (int k = 0; k < steps; k += 2) {
+                step(k, vo);
+                if (k + 1 < steps) step(k + 1, ve);
             }
-            if (active) multiply(k, cur);
-            cur = cur == kGdDepth - 1 ? 0 : cur + 1;
-        };
-        for (int k = 0; k < steps; k += 2) {
-            step(k, vo);
-            if (k + 1 < steps) step(k + 1, ve);
+        } else {
+            for (int k = 0; k < steps; ++k) {
+                wait_lds_and_sync(!(k & 1));
+                if (!(k & 1)) next_u(k);
+                if (active) multiply(k, cur);
+                cur = cur == kGdDepth - 1 ? 0 : cur + 1;
+            }
         }
     } else {
         if (fetch_g) {
@@ -324,11 +343,11 @@ void launch_gx_project(const GxTable& t, int64_t n, int nright, const GaArgs& a,
 // ------------------------------------------------------------------ MX4 gradient
 
 // The product of mx4_tile.h, one column tile (r <= 256), with AdamW on R.
-template <int IB, int WN, int NW, bool Any>
+template <int IB, int WN, int NW>
 __global__ __launch_bounds__(NW * 64) void k_gx_project_mx4(GxTable t, GaArgs a) {
     using T = MxTile<IB, WN, NW>;
     constexpr int kEx = NW * kGxEx * 4;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[Any ? kEx : T::kLds];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[T::kLds];
     static_assert(T::kLds >= kEx, "exchange space");
     const int2 it = t.items[blockIdx.x];
     const GxDesc d = t.desc[it.x];
@@ -339,8 +358,7 @@ __global__ __launch_bounds__(NW * 64) void k_gx_project_mx4(GxTable t, GaArgs a)
     for (int c0 = 0; c0 < d.r; c0 += T::kRowsB) {
         f32x16 acc[IB][2];
         zero_acc(acc);
-        if constexpr (Any) mx4_accumulate_any(oa, ob, i0, c0, acc);
-        else mx4_accumulate<IB, WN, NW>(oa, ob, i0, c0, lds, acc);
+        mx4_accumulate<IB, WN, NW>(oa, ob, i0, c0, lds, acc);
         const int64_t row = i0 + (wave / WN) * 32 * IB;
         const int col = c0 + (wave % WN) * 64;
         if (col < d.r)
@@ -358,10 +376,9 @@ void launch_gx_project_mx4(const GxTable& t, int64_t n, const GaArgs& a, int for
     if (n <= 0) return;
     const dim3 grid(static_cast<uint32_t>(n));
     switch (form) {
-        case kMxAny: hipLaunchKernelGGL((k_gx_project_mx4<1, 2, 4, true>), grid, dim3(256), 0, s, t, a); break;
-        case kMxNarrow: hipLaunchKernelGGL((k_gx_project_mx4<1, 2, 4, false>), grid, dim3(256), 0, s, t, a); break;
-        case kMxWide: hipLaunchKernelGGL((k_gx_project_mx4<1, 4, 8, false>), grid, dim3(512), 0, s, t, a); break;
-        default: hipLaunchKernelGGL((k_gx_project_mx4<2, 4, 8, false>), grid, dim3(512), 0, s, t, a); break;
+        case kMxNarrow: hipLaunchKernelGGL((k_gx_project_mx4<1, 2, 4>), grid, dim3(256), 0, s, t, a); break;
+        case kMxWide: hipLaunchKernelGGL((k_gx_project_mx4<1, 4, 8>), grid, dim3(512), 0, s, t, a); break;
+        default: hipLaunchKernelGGL((k_gx_project_mx4<2, 4, 8>), grid, dim3(512), 0, s, t, a); break;
     }
 }
 

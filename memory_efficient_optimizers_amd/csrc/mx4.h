@@ -66,11 +66,11 @@ struct MxProdBatchOf {
 };
 using MxProdBatch = MxProdBatchOf<kMxBatch>;
 
-// Tile of a product (rows x columns of C): any operands; at most 128 columns; more; more, and
-// enough rows that 128 at a time fill the GPU.
-enum MxForm { kMxAny = 0, kMxNarrow, kMxWide, kMxTall, kMxForms };
-constexpr int kMxFormRows[kMxForms] = {64, 64, 64, 128};
-constexpr int kMxFormCols[kMxForms] = {128, 128, 256, 256};
+// Tile of a product (rows x columns of C): for at most 128 columns; more; more, and enough
+// rows that 128 at a time fill the GPU.
+enum MxForm { kMxNarrow = 0, kMxWide, kMxTall, kMxForms };
+constexpr int kMxFormRows[kMxForms] = {64, 64, 128};
+constexpr int kMxFormCols[kMxForms] = {128, 256, 256};
 
 void launch_mx4_matmul(const MxProdBatch& b, uint32_t grid, MxForm form, hipStream_t s);
 

@@ -280,9 +280,7 @@ void launch_mx4_dequantize(const MxBatch& b, uint32_t grid, bool transposed, hip
 
 // C = A B^T, stored from the accumulators: 32 consecutive values of two rows per
 // instruction. Tiles (MxForm): 128 rows x 256 columns of 8 waves where that fills the GPU,
-// 64 x 256 otherwise and 64 x 128 of 4 waves for products of at most 128 columns; any
-// nb or alignment that mx4_accumulate does not take goes through 64 x 128 tiles that read every
-// fragment as it lies.
+// 64 x 256 otherwise and 64 x 128 of 4 waves for products of at most 128 columns.
 template <int IB, bool BF>
 __device__ __forceinline__ void mx4_store(const MxProd& p, int64_t i0, int64_t j0, int lane, const f32x16 (&acc)[IB][2]) {
     const bool whole = i0 + 32 * IB <= p.m && j0 + 64 <= p.n;
@@ -302,10 +300,10 @@ __device__ __forceinline__ void mx4_store(const MxProd& p, int64_t i0, int64_t j
     }
 }
 
-template <int IB, int WN, int NW, bool Any, int N>
+template <int IB, int WN, int NW, int N>
 __global__ __launch_bounds__(NW * 64) void k_mx4_matmul(MxProdBatchOf<N> b) {
     using T = MxTile<IB, WN, NW>;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[Any ? 16 : T::kLds];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[T::kLds];
     int i = 0;
     while (i + 1 < b.n && blockIdx.x >= b.p[i + 1].first) ++i;
     const MxProd& p = b.p[i];
@@ -321,27 +319,25 @@ __global__ __launch_bounds__(NW * 64) void k_mx4_matmul(MxProdBatchOf<N> b) {
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[ib][jb][v] = 0.0f;
     const MxOperand oa{p.ac, p.as, p.m, static_cast<int32_t>(p.nb)}, ob{p.bc, p.bs, p.n, static_cast<int32_t>(p.nb)};
-    if constexpr (Any) mx4_accumulate_any(oa, ob, i0, j0, acc);
-    else mx4_accumulate<IB, WN, NW>(oa, ob, i0, j0, lds, acc);
+    mx4_accumulate<IB, WN, NW>(oa, ob, i0, j0, lds, acc);
     i0 += (wave / WN) * 32 * IB;
     j0 += (wave % WN) * 64;
     if (p.cbf16) mx4_store<IB, true>(p, i0, j0, lane, acc);
     else mx4_store<IB, false>(p, i0, j0, lane, acc);
 }
 
-template <int IB, int WN, int NW, bool Any>
+template <int IB, int WN, int NW>
 static void launch_matmul(const MxProdBatch& b, uint32_t grid, hipStream_t s) {
-    if (b.n == 1) hipLaunchKernelGGL((k_mx4_matmul<IB, WN, NW, Any, 1>), dim3(grid), dim3(NW * 64), 0, s, only(b));
-    else hipLaunchKernelGGL((k_mx4_matmul<IB, WN, NW, Any, kMxBatch>), dim3(grid), dim3(NW * 64), 0, s, b);
+    if (b.n == 1) hipLaunchKernelGGL((k_mx4_matmul<IB, WN, NW, 1>), dim3(grid), dim3(NW * 64), 0, s, only(b));
+    else hipLaunchKernelGGL((k_mx4_matmul<IB, WN, NW, kMxBatch>), dim3(grid), dim3(NW * 64), 0, s, b);
 }
 
 void launch_mx4_matmul(const MxProdBatch& b, uint32_t grid, MxForm form, hipStream_t s) {
     if (grid == 0) return;
     switch (form) {
-        case kMxAny: launch_matmul<1, 2, 4, true>(b, grid, s); break;
-        case kMxNarrow: launch_matmul<1, 2, 4, false>(b, grid, s); break;
-        case kMxWide: launch_matmul<1, 4, 8, false>(b, grid, s); break;
-        default: launch_matmul<2, 4, 8, false>(b, grid, s); break;
+        case kMxNarrow: launch_matmul<1, 2, 4>(b, grid, s); break;
+        case kMxWide: launch_matmul<1, 4, 8>(b, grid, s); break;
+        default: launch_matmul<2, 4, 8>(b, grid, s); break;
     }
 }
 

@@ -193,16 +193,17 @@ __device__ __forceinline__ void wait_lds_and_sync(bool all) {
 
 typedef uint32_t u32_any __attribute__((aligned(1)));
 
-// The scale bytes of blocks kb .. kb + 3 of a row of nb blocks; 0 past its end. Inside the row.
-__device__ __forceinline__ uint32_t mx_scales4(const uint8_t* row, int kb, int nb) {
-    if (kb >= nb) return 0;
-    if (nb >= 4) {
-        const int at = min(kb, nb - 4);
-        return *gld<u32_any>(row + at) >> (8 * (kb - at));
-    }
+// The scale bytes of blocks kb .. kb + 3 (kb a multiple of 4) of a row of nb blocks: a load
+// inside the row and, once it has landed, its part of them, 0 past the row's end.
+__device__ __forceinline__ uint32_t mx_scales_load(const uint8_t* row, int kb, int nb) {
+    if (nb >= 4) return *gld<u32_any>(row + min(kb, nb - 4));
     uint32_t w = 0;
-    for (int t = 0; t < nb; ++t) w |= static_cast<uint32_t>(*gld<uint8_t>(row + t)) << (8 * t);  // kb is 0
+    for (int t = 0; t < nb; ++t) w |= static_cast<uint32_t>(*gld<uint8_t>(row + t)) << (8 * t);
     return w;
+}
+__device__ __forceinline__ uint32_t mx_scales_take(uint32_t w, int kb, int nb) {
+    const int past = nb >= 4 ? max(kb - (nb - 4), 0) : kb;
+    return past >= 4 ? 0u : w >> (8 * past);
 }
 
 // A pointer that is the same in every lane, in scalar registers.
@@ -234,19 +235,20 @@ struct MxTile {
     static constexpr int kLds = kDepth * kStageA + 2 * kStageB + 2 * kScales;
 };
 
-// acc += A B^T over the whole contraction; nb a multiple of 4 and the scales 4-byte aligned.
-// Codes and scales of both operands go by global_load_lds into LDS, so that nothing in the
-// loop waits for a register load. A wave's transfers land in order, so one that fetched both
-// operands could keep A, which comes from HBM, no further ahead than B, which every block
-// reads from L2 and whose stages are the larger: half of the waves fetch A, four steps
-// ahead (64 KB in flight per CU in the 128-row tile; with 32 KB and one kind of wave the
-// product of a 32000 x 4096 gradient with a rank-256 projector took 33 us), the others B, one
-// step ahead, and the scales of two steps at a time (8 bytes per row and step:
-// fetched singly they cost the L2 as many requests as the codes).
+// acc += A B^T over the whole contraction. Codes (16-byte aligned) go by global_load_lds into
+// LDS, so that nothing in the loop waits for their loads. A wave's transfers land in order, so
+// one that fetched both operands could keep A, which comes from HBM, no further ahead than
+// B, which every block reads from L2 and whose stages are the larger: half of the waves fetch
+// A, four steps ahead (64 KB in flight per CU in the 128-row tile; with 32 KB and one kind
+// of wave the product of a 32000 x 4096 gradient with a rank-256 projector took 33 us), the
+// others B, one step ahead, and the scales of two steps at a time (8 bytes per row and
+// step: fetched singly they cost the L2 as many requests as the codes). Rows of scales have
+// any length and alignment, so these go through registers, loaded in the pair's even step
+// and stored in its odd one, by waves that wait for their transfers at each barrier anyway.
 // Lane half h takes blocks 4 h .. 4 h + 3 of a step: its codes are 64 contiguous bytes and
 // its scales one word (the order of the contraction is free as long as both operands agree).
 // Rows past an operand's end repeat its last one (they reach outputs that are not stored);
-// in a last step of 4 blocks, lane half 1 multiplies zero codes under scales of 1.
+// past the contraction's end lanes multiply zero codes under scales of 1.
 // Offsets within the tile's rows of an operand are 32 bits (kMxMaxK).
 template <int IB, int WN, int NW>
 __device__ __forceinline__ void mx4_accumulate(const MxOperand& a, const MxOperand& b, int64_t i0, int64_t j0,
@@ -260,6 +262,7 @@ __device__ __forceinline__ void mx4_accumulate(const MxOperand& a, const MxOpera
     const bool fetch_a = wave < kHalf;
     const int fw = fetch_a ? wave : wave - kHalf;  // its number among its kind
     const int nb = a.nb;
+    if (nb == 0) return;
     const uint32_t ra = uniform(static_cast<int>(min<int64_t>(a.rows - i0, T::kRowsA))) - 1;  // last valid row
     const uint32_t rb = uniform(static_cast<int>(min<int64_t>(b.rows - j0, T::kRowsB))) - 1;
     uint8_t* const ldsb = lds + T::kDepth * T::kStageA;
@@ -281,17 +284,30 @@ __device__ __forceinline__ void mx4_accumulate(const MxOperand& a, const MxOpera
     };
     using CA = std::integral_constant<int, kA>;
     using CB = std::integral_constant<int, kB>;
-    // Scales: group g is rows 64 g .. 64 g + 63 of [A; B], one word of every row per transfer.
-    auto scales = [&](int pair) {
-        for (int g = fw; g < kGroups; g += kHalf) {
-            const bool ga = g < T::kRowsA / 64;
-            const uint8_t* p = ga ? a.scales + i0 * nb : b.scales + j0 * nb;
-            const uint32_t o = (ga ? min<uint32_t>(64 * g + lane, ra) : min<uint32_t>(64 * g - T::kRowsA + lane, rb)) *
-                               static_cast<uint32_t>(nb);
-            uint8_t* s = ldss + (pair & 1) * T::kScales + g * 256;
+    // Scales: group g is rows 64 g .. 64 g + 63 of [A; B], a word of four blocks per row and w.
+    constexpr int kG = (kGroups + kHalf - 1) / kHalf;
+    uint32_t sw4[kG][4];
+    auto load_scales = [&](int pair) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-                dma4(p + (o + static_cast<uint32_t>(min(16 * pair + 4 * w, nb - 4))), s + w * T::kRows * 4);
+        for (int i = 0; i < kG; ++i) {
+            const int g = fw + i * kHalf;
+            if (g >= kGroups) break;
+            const bool ga = g < T::kRowsA / 64;
+            const uint8_t* p = (ga ? a.scales + i0 * nb : b.scales + j0 * nb) +
+                               (ga ? min<uint32_t>(64 * g + lane, ra) : min<uint32_t>(64 * g - T::kRowsA + lane, rb)) *
+                                   static_cast<uint32_t>(nb);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) sw4[i][w] = mx_scales_load(p, 16 * pair + 4 * w, nb);
+        }
+    };
+    auto store_scales = [&](int pair) {
+#pragma unroll
+        for (int i = 0; i < kG; ++i) {
+            const int g = fw + i * kHalf;
+            if (g >= kGroups) break;
+            uint8_t* s = ldss + (pair & 1) * T::kScales + g * 256 + lane * 4;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) *reinterpret_cast<uint32_t*>(s + w * T::kRows * 4) = mx_scales_take(sw4[i][w], 16 * pair + 4 * w, nb);
         }
     };
     const int wr = (wave / WN) * 32 * IB + (lane & 31), wc = (wave % WN) * 64 + (lane & 31);  // the lane's rows
@@ -312,14 +328,15 @@ __device__ __forceinline__ void mx4_accumulate(const MxOperand& a, const MxOpera
         u32x4 ca[2][4], cb[2][4];
         lds_read_mx<IB>(p, r, qa, qb, ca, cb, e);
         if ((k + 1) * kMxStep > nb) {
+            const int valid = nb - k * kMxStep - 4 * h;  // of the lane's blocks
 #pragma unroll
             for (int jb = 0; jb < 2; ++jb)
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
-                    if (h) cb[jb][t] = u32x4{0u, 0u, 0u, 0u};
+                    if (t >= valid) cb[jb][t] = u32x4{0u, 0u, 0u, 0u};
+            const uint32_t past = valid >= 4 ? 0u : valid <= 0 ? ~0u : ~0u << (8 * valid);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (h) e[i] = 0x7f7f7f7fu;
+            for (int i = 0; i < 4; ++i) e[i] = (e[i] & ~past) | (0x7f7f7f7fu & past);
         }
 #pragma unroll
         for (int ib = 0; ib < IB; ++ib) {
@@ -333,72 +350,39 @@ __device__ __forceinline__ void mx4_accumulate(const MxOperand& a, const MxOpera
         }
     };
     // Before step k's barrier a wave that fetches A waits until only steps k + 1 .. k + 3 are
-    // outstanding, one that fetches B for all it issued (step k and the pair's scales). The
-    // stages that step k fills, A's of step k + 4 and B's of k + 1, were last read in step
-    // k - 1, the scales' buffer in the pair before. Past the end the last blocks are fetched
+    // outstanding, one that fetches B for all it issued. The stages that step k fills, A's of
+    // step k + 4 and B's of k + 1, were last read in step k - 1, the scales' buffer in the
+    // pair before. Past the end the last blocks are fetched
     // again, for equal counts.
     const int steps = (nb + kMxStep - 1) / kMxStep;
     if (fetch_a) {
 #pragma unroll
         for (int k = 0; k < T::kDepth - 1; ++k) codes(k, lds + k * T::kStageA, CA{});
     } else {
-        scales(0);
+        load_scales(0);
+        store_scales(0);
         codes(0, ldsb, CB{});
     }
+    // (Two loops: in one, the compiler lets the waves that fetch A wait for the others' registers.)
     int cur = 0;
-    for (int k = 0; k < steps; ++k) {
-        if (fetch_a) wait_and_sync<3 * kA>();
-        else wait_and_sync<0>();
-        if (fetch_a) {
+    if (fetch_a) {
+        for (int k = 0; k < steps; ++k) {
+            wait_and_sync<3 * kA>();
             codes(k + T::kDepth - 1, lds + (cur == 0 ? T::kDepth - 1 : cur - 1) * T::kStageA, CA{});
-        } else {
-            if (k & 1) scales((k + 1) >> 1);
-            codes(k + 1, ldsb + ((k + 1) & 1) * T::kStageB, CB{});
+            multiply(k, cur);
+            cur = cur == T::kDepth - 1 ? 0 : cur + 1;
         }
-        multiply(k, cur);
-        cur = cur == T::kDepth - 1 ? 0 : cur + 1;
+    } else {
+        for (int k = 0; k < steps; ++k) {
+            wait_and_sync<0>();
+            if (k & 1) store_scales((k + 1) >> 1);
+            else if (nb >= 4) load_scales((k >> 1) + 1);
+            codes(k + 1, ldsb + ((k + 1) & 1) * T::kStageB, CB{});
+            multiply(k, cur);
+            cur = cur == T::kDepth - 1 ? 0 : cur + 1;
+        }
     }
     wait_and_sync<0>();  // transfers past the end have landed before the stages are reused
-}
-
-// The same product for any nb and alignment, every fragment read as it lies: 4 waves, 2 along
-// each side, 32 x 64 each. A lane's block past the contraction's end is zero codes.
-__device__ __forceinline__ void mx4_accumulate_any(const MxOperand& a, const MxOperand& b, int64_t i0, int64_t j0,
-                                                   f32x16 (&acc)[1][2]) {
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
-    const int nb = a.nb;
-    const int64_t ra = min<int64_t>(i0 + (wave >> 1) * 32 + (lane & 31), a.rows - 1) * nb;
-    int64_t rb[2];
-#pragma unroll
-    for (int jb = 0; jb < 2; ++jb) rb[jb] = min<int64_t>(j0 + (wave & 1) * 64 + jb * 32 + (lane & 31), b.rows - 1) * nb;
-    for (int k = 0; k < nb; k += 4) {
-        u32x4 ca[2], cb[2][2];
-        uint32_t ea[2], eb[2][2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int kb = k + 2 * t + h;
-            const bool in = kb < nb;
-            ca[t] = u32x4{0u, 0u, 0u, 0u};
-            ea[t] = 127;
-            if (in) {
-                ca[t] = *gld<u32x4>(a.codes + (ra + kb) * 16);
-                ea[t] = *gld<uint8_t>(a.scales + ra + kb);
-            }
-#pragma unroll
-            for (int jb = 0; jb < 2; ++jb) {
-                cb[t][jb] = u32x4{0u, 0u, 0u, 0u};
-                eb[t][jb] = 127;
-                if (in) {
-                    cb[t][jb] = *gld<u32x4>(b.codes + (rb[jb] + kb) * 16);
-                    eb[t][jb] = *gld<uint8_t>(b.scales + rb[jb] + kb);
-                }
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int jb = 0; jb < 2; ++jb) acc[0][jb] = mfma_mx4<0>(ca[t], cb[t][jb], acc[0][jb], ea[t], eb[t][jb]);
-    }
 }
 
 }  // namespace meo
