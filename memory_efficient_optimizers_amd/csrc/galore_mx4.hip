@@ -211,14 +211,15 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
                 mx_scales_take(sw4[w], 16 * quad + 4 * w, d.nb);
     };
     const uint32_t base = lds_addr(lds);
-    auto multiply = [&](int k, int cur) {
+    u32x4 x[2][8], c[2];  // a step's fragments: G's of two 32-row halves; codes of two blocks
+    float sc[2];          // and their scales
+    auto read = [&](int k, int cur) {
         const uint32_t s = base + cur * kGdG;
         // the two blocks of the lane's column of R, and their scales
         const int r0 = cw + (lane & 31), sw = mx_swz(lane & 31), b0 = 4 * (k & 1) + 2 * h;
         const uint32_t pb = base + kGdDepth * kGdG + ((k >> 1) & 1) * kGdCodes + r0 * 128;
         const uint32_t pe = base + kGdDepth * kGdG + 2 * kGdCodes + ((k >> 2) & 1) * kGdScales + (k & 3) * (kGaWide * 4) + r0 * 4;
         const uint32_t q[2] = {pb + ((b0 ^ sw) << 4), pb + (((b0 + 1) ^ sw) << 4)};
-        u32x4 x[2][8], c[2];  // G's fragments of two 32-row halves; codes of two blocks
         uint32_t e;
         if constexpr (Left) {
             const int gq = lane >> 4, eq = (lane >> 2) & 3;
@@ -235,12 +236,15 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
             lds_read_row(p, q, pe, x, c, e);
         }
         if (h) e >>= 16;
-        float sc[2] = {mx4_scale(e & 255u), mx4_scale((e >> 8) & 255u)};
+        sc[0] = mx4_scale(e & 255u);
+        sc[1] = mx4_scale((e >> 8) & 255u);
         if constexpr (Any) {  // past the end G is zero; codes and scales are whatever is there
 #pragma unroll
             for (int t = 0; t < 2; ++t)
                 if (4 * k + 2 * h + t >= d.nb) sc[t] = 1.0f;
         }
+    };
+    auto multiply = [&]() {
 #pragma unroll
         for (int u = 0; u < 8; ++u) {  // 8 values: dword u & 3 of block u >> 2
             const bfv8 fb = __builtin_bit_cast(bfv8, mx4_to_bf16(c[u >> 2][u & 3], sc[u >> 2]));
@@ -271,7 +275,28 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
         if constexpr (Any) store_scales(0);
         codes(0);
     }
+    // kGxDirect: the waves that fetch U^T multiply a step's fragments behind the next barrier, before
+    // they read that step's: their products run beside the LDS reads of the others (each SIMD
+    // has one of either kind): 74 us for the four 4096 x 4096 matrices, 78 without. (Any:
+    // 97 and 90 us for 1951 x 3810 and 3750 x 4266, so there every wave multiplies at once.)
     int cur = 0;
+    auto first_half = [&](int k) {  // waves 0 .. 3
+        if (active) {
+            read(k, cur);
+            multiply();
+        }
+        cur = cur == kGdDepth - 1 ? 0 : cur + 1;
+    };
+    auto second_half = [&](int k) {  // waves 4 .. 7
+        if (active) {
+            if (!Any && k) multiply();
+#pragma unroll
+            for (int ib = 0; ib < 2; ++ib) __asm__ volatile("" : "+v"(acc[ib]));  // before the reads
+            read(k, cur);
+            if (Any) multiply();
+        }
+        cur = cur == kGdDepth - 1 ? 0 : cur + 1;
+    };
     if constexpr (Any) {
         u32x4 ve[kA], vo[kA];  // even and odd steps
         if (fetch_g) {
@@ -286,8 +311,7 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
                 wait_lds_and_sync(false);
                 store_g(v, lds + (cur == kGdDepth - 1 ? 0 : cur + 1) * kGdG);
                 load_g(k + 3, v);
-                if (active) multiply(k, cur);
-                cur = cur == kGdDepth - 1 ? 0 : cur + 1;
+                first_half(k);
             };
             for (int k = 0; k < steps; k += 2) {
                 step(k, vo);
@@ -297,8 +321,7 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
             for (int k = 0; k < steps; ++k) {
                 wait_lds_and_sync(!(k & 1));
                 if (!(k & 1)) next_u(k);
-                if (active) multiply(k, cur);
-                cur = cur == kGdDepth - 1 ? 0 : cur + 1;
+                second_half(k);
             }
         }
     } else {
@@ -306,17 +329,23 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
 #pragma unroll
             for (int k = 0; k < kGdDepth - 1; ++k) stage(k, lds + k * kGdG);
         }
-        for (int k = 0; k < steps; ++k) {
-            if (fetch_g) wait_and_sync<3 * kA>();
-            else if (!(k & 1)) wait_and_sync<0>();
-            else if ((k & 3) == 3) wait_and_sync<kB + 4>();
-            else wait_and_sync<kB>();
-            if (fetch_g) stage(k + kGdDepth - 1, lds + (cur == 0 ? kGdDepth - 1 : cur - 1) * kGdG);
-            else if (!(k & 1)) next_u(k);
-            if (active) multiply(k, cur);
-            cur = cur == kGdDepth - 1 ? 0 : cur + 1;
+        if (fetch_g) {
+            for (int k = 0; k < steps; ++k) {
+                wait_and_sync<3 * kA>();
+                stage(k + kGdDepth - 1, lds + (cur == 0 ? kGdDepth - 1 : cur - 1) * kGdG);
+                first_half(k);
+            }
+        } else {
+            for (int k = 0; k < steps; ++k) {
+                if (!(k & 1)) wait_and_sync<0>();
+                else if ((k & 3) == 3) wait_and_sync<kB + 4>();
+                else wait_and_sync<kB>();
+                if (!(k & 1)) next_u(k);
+                second_half(k);
+            }
         }
     }
+    if (!Any && !fetch_g && active) multiply();
     wait_and_sync<0>();
     if (!active) return;
     float* lw = reinterpret_cast<float*>(lds) + wave * kGxEx;
@@ -342,7 +371,10 @@ void launch_gx_project(const GxTable& t, int64_t n, int nright, const GaArgs& a,
 
 // ------------------------------------------------------------------ MX4 gradient
 
-// The product of mx4_tile.h, one column tile (r <= 256), with AdamW on R.
+// The product of mx4_tile.h, one column tile (r <= 256), with AdamW on R: 63 us for 11008 x 4096
+// and 4096 x 11008 at rank 256 (128-row tiles; 77 with 64), whose bytes take 33 at the rate of
+// a copy: 172 tiles on 256 CUs, each first multiplying, then streaming its moments. (Their first
+// half loaded before the product: 69 us, its registers spill.)
 template <int IB, int WN, int NW>
 __global__ __launch_bounds__(NW * 64) void k_gx_project_mx4(GxTable t, GaArgs a) {
     using T = MxTile<IB, WN, NW>;
