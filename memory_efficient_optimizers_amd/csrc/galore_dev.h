@@ -15,14 +15,12 @@ __device__ __forceinline__ f32x16 mfma32(const bfv8& a, const bfv8& b, const f32
 }
 
 // 8 bf16 (raw bits) of row `row` starting at column `col` of a row-major [rows][cols]
-// array; out-of-range elements read 0. Any: 16-byte loads at any address (`vec` ignored).
-template <bool Any = false>
+// array; out-of-range elements read 0.
 __device__ __forceinline__ u32x4 ld_row8(const uint16_t* p, int64_t rows, int64_t cols, int64_t row,
                                          int64_t col, bool vec) {
     if (row >= rows || col >= cols) return u32x4{0u, 0u, 0u, 0u};
     const uint16_t* q = p + row * cols + col;
-    if (Any && col + 8 <= cols) return *gld<u32x4_any>(q);
-    if (!Any && vec && col + 8 <= cols) return *gld<u32x4>(q);
+    if (vec && col + 8 <= cols) return *gld<u32x4>(q);
     const MEO_GLOBAL uint16_t* s = gld<uint16_t>(q);
     uint32_t w[4];
 #pragma unroll

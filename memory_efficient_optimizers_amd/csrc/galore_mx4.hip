@@ -123,6 +123,23 @@ constexpr int kGdCodes = kGaWide * kGdStep;      // bytes of codes of two steps
 constexpr int kGdScales = kGaWide * 4 * 4;       // bytes of scales of four: [word][row]
 constexpr int kGdLds = kGdDepth * kGdG + 2 * kGdCodes + 2 * kGdScales;
 
+// Values `from` on of 8 bf16 values, the `valid` first of them, zeros behind.
+__device__ __forceinline__ u32x4 row_part(const u32x4& v, int from, int valid) {
+    uint64_t lo = static_cast<uint64_t>(v.y) << 32 | v.x, hi = static_cast<uint64_t>(v.w) << 32 | v.z;
+    if (from >= 4) {
+        lo = hi;
+        hi = 0;
+        from -= 4;
+    }
+    if (from > 0) {
+        lo = lo >> (16 * from) | hi << (64 - 16 * from);
+        hi >>= 16 * from;
+    }
+    lo = valid >= 4 ? lo : valid <= 0 ? 0 : lo & (~0ull >> (64 - 16 * valid));
+    hi = valid >= 8 ? hi : valid <= 4 ? 0 : hi & (~0ull >> (128 - 16 * valid));
+    return u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
+}
+
 template <bool Left, bool Any>
 __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArgs& a, uint8_t* lds) {
     constexpr int kA = kGdG / 1024 / 4, kB = kGdCodes / 1024 / 4;  // 1 KB transfers per wave of its kind
@@ -161,18 +178,51 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
 #pragma unroll
         for (int i = 0; i < kA; ++i) dma16(gk + ga[i], s + (fw + i * 4) * 1024);
     };
-    // The same tile through registers: the thread's four chunks of a step, and their places.
+    // The same tile through registers: the thread's four chunks of a step, and their places. Every
+    // load is 16 bytes inside the tensor, without a branch (with the rest of a row read value
+    // by value behind one, each load waited for the others: 59 instead of 31 us for 2048 x 5461 at rank 16): chunk
+    // places past the last are moved back to it. What a step's last tile then holds wrongly
+    // (values of a later row, or moved back) is put right when it is stored.
+    const int64_t last = static_cast<int64_t>(d.m) * d.n - 8;
+    auto place = [&](int k, int i, int64_t& at, int& valid) {
+        const int j = fw + i * 4;
+        if constexpr (Left) {  // (columns past D reach rows of R that are not stored)
+            const int64_t kr = static_cast<int64_t>(k) * kGdStep + 8 * j + (lane >> 3);
+            at = min<int64_t>(kr, d.d - 1) * d.D + min<int64_t>(i0 + (lane & 7) * 8, d.D - 1);
+            valid = kr < d.d ? 8 : 0;
+        } else {
+            const int kc = k * kGdStep + (lane & 15) * 8;
+            at = min<int64_t>(i0 + 4 * j + (lane >> 4), d.D - 1) * d.d + min(kc, d.d - 1);
+            valid = min(max(d.d - kc, 0), 8);
+        }
+    };
     auto load_g = [&](int k, u32x4 (&v)[kA]) {
 #pragma unroll
         for (int i = 0; i < kA; ++i) {
-            const int j = fw + i * 4;
-            if constexpr (Left) v[i] = ld_row8<true>(d.g, d.d, d.D, static_cast<int64_t>(k) * kGdStep + 8 * j + (lane >> 3), i0 + (lane & 7) * 8, true);
-            else v[i] = ld_row8<true>(d.g, d.D, d.d, i0 + 4 * j + (lane >> 4), static_cast<int64_t>(k) * kGdStep + (lane & 15) * 8, true);
+            int64_t at;
+            int valid;
+            place(k, i, at, valid);
+            if (last >= 0) {
+                v[i] = *gld<u32x4_any>(d.g + min(at, last));
+            } else {  // fewer than 8 values in all
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = at + e < last + 8 ? *gld<uint16_t>(d.g + at + e) : 0u;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[i][e] = w[2 * e] | w[2 * e + 1] << 16;
+            }
         }
     };
-    auto store_g = [&](const u32x4 (&v)[kA], uint8_t* s) {
+    auto store_g = [&](int k, u32x4 (&v)[kA], uint8_t* s) {
+        const bool edge = (k + 1) * kGdStep > d.d || (Left && i0 + kGdRows > d.D);
 #pragma unroll
         for (int i = 0; i < kA; ++i) {
+            if (edge) {
+                int64_t at;
+                int valid;
+                place(k, i, at, valid);
+                v[i] = row_part(v[i], last >= 0 ? static_cast<int>(max<int64_t>(at - last, 0)) : 0, valid);
+            }
             const int j = fw + i * 4;
             const int r = Left ? 8 * j + (lane >> 3) : 4 * j + (lane >> 4);
             const int at = Left ? r * 128 + (((lane & 7) ^ lsw(r & 3)) << 4) : r * 256 + (((lane & 15) ^ (r & 15)) << 4);
@@ -302,14 +352,14 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
         if (fetch_g) {
             load_g(0, ve);
             load_g(1, vo);
-            store_g(ve, lds);
+            store_g(0, ve, lds);
             load_g(2, ve);
         }
         // (two loops, as in mx4_accumulate)
         if (fetch_g) {
             auto step = [&](int k, u32x4 (&v)[kA]) {
                 wait_lds_and_sync(false);
-                store_g(v, lds + (cur == kGdDepth - 1 ? 0 : cur + 1) * kGdG);
+                store_g(k + 1, v, lds + (cur == kGdDepth - 1 ? 0 : cur + 1) * kGdG);
                 load_g(k + 3, v);
                 first_half(k);
             };
