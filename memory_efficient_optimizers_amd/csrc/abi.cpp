@@ -1619,7 +1619,7 @@ namespace {
 enum GaList { kGaProjR = 0, kGaProjL, kGaBackR, kGaBackL, kGaFlat,
               // MX4 projectors: projection by form (GxForm; MxForm for MX4 gradients),
               // back-projection by parameter dtype (float32, bf16)
-              kGxProj, kGxProjM = kGxProj + kGxForms, kGxBack = kGxProjM + kMxForms, kGxEnd = kGxBack + 2,
+              kGxProj, kGxProjM = kGxProj + kGxForms, kGxJoin = kGxProjM + kMxForms, kGxBack, kGxEnd = kGxBack + 2,
               // projector refresh
               kRfInit = kGxEnd, kRfG0N, kRfG0T, kRfG1N, kRfG1T, kRfGram, kRfOne, kRfCols, kRfStore, kGaListCount };
 
@@ -1706,20 +1706,48 @@ int32_t gx_pitch(int32_t r) { return (r + 31) / 32 * 32; }  // MX4 projectors: v
 
 int64_t align256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
+constexpr int64_t kCus = 256;
+
+// MX4 projectors: steps of the contraction per part of a projection (a multiple of 4), 0 where it
+// stays whole. Where the tiles of all R leave CUs idle, the contraction is split into as many
+// parts as fill them; the parts' sum is a launch of its own (4 to 10 us), taken as kGxJoinSteps
+// steps of 1 to 1.5 us. Whole, and in parts with their sum: 4096 x 4096 at rank 256 49 and 32
+// us, at 64 29 and 20; 1951 x 3810 with 3750 x 4266 at 177 60 and 48; 1536 x 1536 at 64 16 and
+// 12; below that the two are even.
+constexpr int64_t kGxJoinSteps = 4;
+int64_t gx_split(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts) {
+    int64_t most = 0;
+    for (int32_t k = 0; k < n; ++k)
+        if (ga_rank(hp, ts[k])) most = std::max(most, ceil_div(ga_basis(hp, ts[k]), kGxStep));
+    for (int64_t per = 4; per + kGxJoinSteps < most; per += 4) {
+        int64_t items = 0;
+        for (int32_t k = 0; k < n && items <= kCus; ++k)
+            if (ga_rank(hp, ts[k]))
+                items += ceil_div(ga_rows(hp, ts[k]), kGxFormRows[kGxAny]) * ceil_div(ceil_div(ga_basis(hp, ts[k]), kGxStep), per);
+        if (items <= kCus) return per;
+    }
+    return 0;
+}
+
+int64_t gx_parts(int64_t d, int64_t per) { return per ? ceil_div(ceil_div(d, kGxStep), per) : 1; }
+
 // Workspace, per projected tensor, every array at a 256-byte boundary (offsets in
-// bytes): the step's two bf16 planes of N, [D][r] each; then, for the projector
+// bytes): the step's two bf16 planes of N, [D][r] each (mx: MX4 projectors: rows of rp
+// values, and then the parts of a split projection, fp32 [ks][D][rp]); then, for the projector
 // refresh, two fp32 [r][d] iterates, one fp32 [r][D] product, four fp64 [r][r]
-// matrices and (mx: MX4 projectors) the refreshed projector in bf16, [d][r] and [r][d].
+// matrices and (mx) the refreshed projector in bf16, [d][r] and [r][d].
 int64_t ga_layout(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, bool mx, std::vector<int64_t>* offs,
                   std::vector<int64_t>* roffs = nullptr) {
     int64_t off = 0;
     if (offs) offs->assign(n, -1);
     if (roffs) roffs->assign(n, -1);
+    const int64_t per = mx ? gx_split(hp, n, ts) : 0;
     for (int32_t k = 0; k < n; ++k) {
         const int32_t r = ga_rank(hp, ts[k]);
         if (!r) continue;
         if (offs) (*offs)[k] = off;
         off += 2 * align256(ga_rows(hp, ts[k]) * (mx ? gx_pitch(r) : r) * 2);
+        if (per) off += align256(gx_parts(ga_basis(hp, ts[k]), per) * ga_rows(hp, ts[k]) * gx_pitch(r) * 4);
     }
     for (int32_t k = 0; k < n; ++k) {
         const int32_t r = ga_rank(hp, ts[k]);
@@ -1868,8 +1896,6 @@ int check_galore_workspace(const meo_galore_hparams* hp, int32_t n, const meo_te
     return check_device_range(ws, bytes, dev, "workspace", MEO_EWORKSPACE);
 }
 
-constexpr int64_t kCus = 256;
-
 // Whether `tall` tiles of 128 rows take less time than `wide` of 64: a tile runs alone on its
 // CU, a tall one 4/3 as long (rank 256, k = 4096: 32000 rows 33 and 47 us, 16384 rows 28 and
 // 25, 40000 rows 62 and 72).
@@ -1880,6 +1906,10 @@ bool mx4_tall(int64_t tall, int64_t wide) { return 4 * ceil_div(tall, kCus) < 3 
 void gx_lists(std::vector<GxDesc>& gd, std::vector<int2>* lists) {
     // (d a multiple of 128: whole words of scales)
     auto direct = [](const GxDesc& d) { return d.vec && d.d % 128 == 0 && reinterpret_cast<uintptr_t>(d.us) % 4 == 0; };
+    // One form for all of a list, whose tiles then run side by side: 2048 x 5461 and 5461 x 2048 at rank
+    // 16 in launches of their own 31 and 19 us, together 32.
+    bool all_direct = true;
+    for (const GxDesc& d : gd) all_direct = all_direct && (d.gs || direct(d));
     int64_t tall = 0, wide = 0;  // tiles of the MX4 gradients' wide products, 128 and 64 rows each
     for (const GxDesc& d : gd)
         if (d.gs && d.r > kMxFormCols[kMxNarrow]) {
@@ -1894,11 +1924,14 @@ void gx_lists(std::vector<GxDesc>& gd, std::vector<int2>* lists) {
             list = kGxProjM + form;
             rows = kMxFormRows[form];
         } else {
-            const int form = direct(d) ? kGxDirect : kGxAny;
+            const int form = all_direct ? kGxDirect : kGxAny;
             list = kGxProj + form;
             rows = kGxFormRows[form];
         }
-        for (int64_t y = 0; y < ceil_div(d.D, rows); ++y) lists[list].push_back(make_int2(static_cast<int>(i), static_cast<int>(y)));
+        for (int64_t y = 0; y < ceil_div(d.D, rows) * d.ks; ++y) lists[list].push_back(make_int2(static_cast<int>(i), static_cast<int>(y)));
+        if (d.ks > 1)
+            for (int64_t y = 0; y < ceil_div(static_cast<int64_t>(d.D) * (d.rp / 8), kGxJoinChunks); ++y)
+                lists[kGxJoin].push_back(make_int2(static_cast<int>(i), static_cast<int>(y)));
     }
     for (int xb = 0; xb < 2; ++xb) {
         std::vector<size_t> ids;
@@ -1963,6 +1996,7 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
     if (*rc) return nullptr;
     std::vector<int64_t> woff, roff;
     ga_layout(hp, n, ts, mx, &woff, &roff);
+    const int64_t per = mx ? gx_split(hp, n, ts) : 0;
     std::vector<RDesc> rd;
     std::vector<GxDesc> right, left;  // the MX4 fields stay zero for bf16 projectors
     std::vector<MxMat> quant;
@@ -2004,6 +2038,9 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
                 d.gs = g4 ? static_cast<const uint8_t*>(s.gs) : nullptr;
                 d.nb = static_cast<int32_t>(ceil_div(d.d, kMxBlock));
                 d.vec = aligned16(d.g) && d.n % 8 == 0;  // 16-byte rows of a bf16 gradient
+                d.ks = g4 ? 1 : static_cast<int32_t>(gx_parts(d.d, per));
+                d.kper = d.ks > 1 ? static_cast<int32_t>(per) : (d.d + kGxStep - 1) / kGxStep;
+                d.part = reinterpret_cast<float*>(wb + 2 * align256(static_cast<int64_t>(d.D) * d.rp * 2));
             }
             d.rvec = aligned16(d.em) && aligned16(d.ev) && d.r % 8 == 0;
             d.wvec = aligned16(d.x) && d.n % 8 == 0;
@@ -2283,6 +2320,7 @@ int ga_step(const meo_galore_hparams* hp, int64_t step, int32_t n, const meo_ten
             launch_gx_project(GxTable{p->gxdesc, p->items[kGxProj + f]}, p->count[kGxProj + f], p->nright, a, f, s);
         for (int f = 0; f < kMxForms; ++f)
             launch_gx_project_mx4(GxTable{p->gxdesc, p->items[kGxProjM + f]}, p->count[kGxProjM + f], a, f, s);
+        launch_gx_join(GxTable{p->gxdesc, p->items[kGxJoin]}, p->count[kGxJoin], a, s);
     } else if (p->proj_direct[0] && p->proj_direct[1]) {
         launch_galore_project_mixed(GTable{p->gdesc, p->items[kGaProjR]}, p->count[kGaProjR], p->nright, a, s);
     } else {

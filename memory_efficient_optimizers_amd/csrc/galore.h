@@ -51,6 +51,8 @@ struct GxDesc : GDesc {
     int32_t nb;         // blocks along d
     int32_t rp;         // r rounded up to 32: two of the back-projection's sub-steps
     int32_t tpi;        // back-projection: 64-row tiles of N per item
+    float* part;        // split contraction (ks > 1): R's parts, [ks][D][rp]
+    int32_t ks, kper;   // parts, and steps of kGxStep in each but the last
 };
 
 struct GxTable {
@@ -90,7 +92,12 @@ void launch_galore_adamw(const Table& t, int64_t n, const GaArgs& a, hipStream_t
 // scales aligned. An MX4 gradient takes the product's forms (MxForm).
 enum GxForm { kGxAny = 0, kGxDirect, kGxForms };
 constexpr int kGxFormRows[kGxForms] = {64, 64};
+constexpr int kGxStep = 128;  // contraction step
+// Items of a tensor with ks parts: y = tile * ks + part; its R is summed by launch_gx_join (items
+// of kGxJoinChunks times 8 columns of a row), whose epilogue is then the projection's.
+constexpr int kGxJoinChunks = 256;
 void launch_gx_project(const GxTable& t, int64_t n, int nright, const GaArgs& a, int form, hipStream_t s);
+void launch_gx_join(const GxTable& t, int64_t n, const GaArgs& a, hipStream_t s);
 void launch_gx_project_mx4(const GxTable& t, int64_t n, const GaArgs& a, int form, hipStream_t s);
 // Back-projection with an MX4 projector: the U-register kernel for any shape, parameters
 // of one dtype; item y = band * btj + chunk, chunks of tpi tiles of N.

@@ -115,7 +115,7 @@ __device__ __forceinline__ void zero_acc(f32x16 (&acc)[IB][2]) {
 // Lane half h takes values 64 h .. 64 h + 63 of a step: two whole MX blocks, so a lane's
 // scale changes once per step.
 constexpr int kGdRows = kGxFormRows[kGxDirect];
-constexpr int kGdStep = 128;
+constexpr int kGdStep = kGxStep;
 constexpr int kGdWaves = 8;
 constexpr int kGdDepth = 5;
 constexpr int kGdG = kGdRows * kGdStep * 2;      // bytes of G per stage
@@ -141,7 +141,7 @@ __device__ __forceinline__ u32x4 row_part(const u32x4& v, int from, int valid) {
 }
 
 template <bool Left, bool Any>
-__device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArgs& a, uint8_t* lds) {
+__device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, int part, const GaArgs& a, uint8_t* lds) {
     constexpr int kA = kGdG / 1024 / 4, kB = kGdCodes / 1024 / 4;  // 1 KB transfers per wave of its kind
     static_assert(kGdWaves == 8 && kGdDepth * kGdG >= kGdWaves * kGxEx * 4, "waves below; exchange space");
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
@@ -173,6 +173,7 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
     }
     const int64_t gstep = static_cast<int64_t>(kGdStep) * 2 * (Left ? d.D : 1);
     const int steps = (d.d + kGdStep - 1) / kGdStep;
+    const int k0 = part * d.kper, k1 = min(k0 + d.kper, steps);  // k0 a multiple of 4
     auto stage = [&](int k, uint8_t* s) {
         const uint8_t* gk = g + min(k, steps - 1) * gstep;  // past the end: the last again, for equal counts
 #pragma unroll
@@ -310,7 +311,7 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
     // The moments of the wave's piece of R are loaded before everything else.
     const bool active = cw < d.r;
     GxMoments<true> mv;
-    if (active) mv.load(d, i0, cw, lane);
+    if (active && d.ks == 1) mv.load(d, i0, cw, lane);
     auto next_u = [&](int k) {  // waves 4 .. 7, even steps
         if constexpr (Any) {  // loaded two steps before they are stored
             if (k & 2) store_scales((k >> 2) + 1);
@@ -321,9 +322,9 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
         codes((k >> 1) + 1);
     };
     if (!fetch_g) {
-        scales(0);
-        if constexpr (Any) store_scales(0);
-        codes(0);
+        scales(k0 >> 2);
+        if constexpr (Any) store_scales(k0 >> 2);
+        codes(k0 >> 1);
     }
     // kGxDirect: the waves that fetch U^T multiply a step's fragments behind the next barrier, before
     // they read that step's: their products run beside the LDS reads of the others (each SIMD
@@ -339,7 +340,7 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
     };
     auto second_half = [&](int k) {  // waves 4 .. 7
         if (active) {
-            if (!Any && k) multiply();
+            if (!Any && k > k0) multiply();
 #pragma unroll
             for (int ib = 0; ib < 2; ++ib) __asm__ volatile("" : "+v"(acc[ib]));  // before the reads
             read(k, cur);
@@ -350,10 +351,10 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
     if constexpr (Any) {
         u32x4 ve[kA], vo[kA];  // even and odd steps
         if (fetch_g) {
-            load_g(0, ve);
-            load_g(1, vo);
-            store_g(0, ve, lds);
-            load_g(2, ve);
+            load_g(k0, ve);
+            load_g(k0 + 1, vo);
+            store_g(k0, ve, lds);
+            load_g(k0 + 2, ve);
         }
         // (two loops, as in mx4_accumulate)
         if (fetch_g) {
@@ -363,12 +364,12 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
                 load_g(k + 3, v);
                 first_half(k);
             };
-            for (int k = 0; k < steps; k += 2) {
+            for (int k = k0; k < k1; k += 2) {
                 step(k, vo);
-                if (k + 1 < steps) step(k + 1, ve);
+                if (k + 1 < k1) step(k + 1, ve);
             }
         } else {
-            for (int k = 0; k < steps; ++k) {
+            for (int k = k0; k < k1; ++k) {
                 wait_lds_and_sync(!(k & 1));
                 if (!(k & 1)) next_u(k);
                 second_half(k);
@@ -377,16 +378,16 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
     } else {
         if (fetch_g) {
 #pragma unroll
-            for (int k = 0; k < kGdDepth - 1; ++k) stage(k, lds + k * kGdG);
+            for (int k = 0; k < kGdDepth - 1; ++k) stage(k0 + k, lds + k * kGdG);
         }
         if (fetch_g) {
-            for (int k = 0; k < steps; ++k) {
+            for (int k = k0; k < k1; ++k) {
                 wait_and_sync<3 * kA>();
                 stage(k + kGdDepth - 1, lds + (cur == 0 ? kGdDepth - 1 : cur - 1) * kGdG);
                 first_half(k);
             }
         } else {
-            for (int k = 0; k < steps; ++k) {
+            for (int k = k0; k < k1; ++k) {
                 if (!(k & 1)) wait_and_sync<0>();
                 else if ((k & 3) == 3) wait_and_sync<kB + 4>();
                 else wait_and_sync<kB>();
@@ -398,6 +399,16 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, const GaArg
     if (!Any && !fetch_g && active) multiply();
     wait_and_sync<0>();
     if (!active) return;
+    if (d.ks > 1) {
+#pragma unroll
+        for (int ib = 0; ib < 2; ++ib)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int64_t row = i0 + ib * 32 + acc_row(v, lane);
+                if (row < d.D) *gst<float>(d.part + (part * static_cast<int64_t>(d.D) + row) * d.rp + cw + acc_col(lane)) = acc[ib][v];
+            }
+        return;
+    }
     float* lw = reinterpret_cast<float*>(lds) + wave * kGxEx;
     gx_epilogue(d, a, acc[0], acc[1], mv, i0, cw, lw, lane);
 }
@@ -407,9 +418,10 @@ __global__ __launch_bounds__(kGdWaves * 64) void k_gx_project(GxTable t, GaArgs 
     __shared__ __attribute__((aligned(128))) uint8_t lds[kGdLds];
     const int2 it = t.items[blockIdx.x];
     const GxDesc d = t.desc[it.x];
-    const int64_t i0 = static_cast<int64_t>(it.y) * kGdRows;
-    if (it.x < nright) gx_tile<false, Any>(d, i0, a, lds);
-    else gx_tile<true, Any>(d, i0, a, lds);
+    const int64_t i0 = static_cast<int64_t>(it.y / d.ks) * kGdRows;
+    const int part = it.y % d.ks;
+    if (it.x < nright) gx_tile<false, Any>(d, i0, part, a, lds);
+    else gx_tile<true, Any>(d, i0, part, a, lds);
 }
 
 void launch_gx_project(const GxTable& t, int64_t n, int nright, const GaArgs& a, int form, hipStream_t s) {
@@ -417,6 +429,33 @@ void launch_gx_project(const GxTable& t, int64_t n, int nright, const GaArgs& a,
     const dim3 grid(static_cast<uint32_t>(n)), block(kGdWaves * 64);
     if (form == kGxAny) hipLaunchKernelGGL(k_gx_project<true>, grid, block, 0, s, t, a, nright);
     else hipLaunchKernelGGL(k_gx_project<false>, grid, block, 0, s, t, a, nright);
+}
+
+// R of a split contraction: its parts summed in order, then AdamW; a thread has 8 columns of a row.
+__global__ __launch_bounds__(kGxJoinChunks) void k_gx_join(GxTable t, GaArgs a) {
+    const int2 it = t.items[blockIdx.x];
+    const GxDesc d = t.desc[it.x];
+    const int chunks = d.rp / 8;
+    const int64_t c = static_cast<int64_t>(it.y) * kGxJoinChunks + threadIdx.x;
+    const int64_t row = c / chunks;
+    if (row >= d.D) return;
+    const int col = 8 * static_cast<int>(c - row * chunks);
+    const int valid = min(max(d.r - col, 0), 8);
+    float m[8], v[8], r[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    load_any8(d.em, row * d.r + col, valid, false, m);
+    load_any8(d.ev, row * d.r + col, valid, false, v);
+    for (int s = 0; s < d.ks; ++s) {
+        float x[8];
+        load_any8(d.part, (s * static_cast<int64_t>(d.D) + row) * d.rp + col, 8, false, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] += x[e];
+    }
+    gx_adamw8(d, a, row, col, valid, m, v, r);
+}
+
+void launch_gx_join(const GxTable& t, int64_t n, const GaArgs& a, hipStream_t s) {
+    if (n <= 0) return;
+    hipLaunchKernelGGL(k_gx_join, dim3(static_cast<uint32_t>(n)), dim3(kGxJoinChunks), 0, s, t, a);
 }
 
 // ------------------------------------------------------------------ MX4 gradient

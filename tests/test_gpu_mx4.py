@@ -370,6 +370,75 @@ def test_step_mixed_list(grad):
     run_step([(192, 64), (0, 5), (64, 500), (777,), (3, 5, 7), (1,), (8, 8), (256, 512), (512, 256)], 64, seed=3, grad=grad)
 
 
+REVERSE = dict(proj_type="reverse_std")
+
+
+@pytest.mark.parametrize("pdt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shapes,rank", [
+    ([(70, 1801)], 33), ([(1801, 70)], 33), ([(64, 2048)], 64), ([(2048, 64)], 16), ([(9, 1537)], 9), ([(1543, 1)], 1),
+    ([(300, 1792)], 177), ([(1600, 200)], 200), ([(70, 1801), (2048, 64), (96, 400), (33,), (40, 24)], 48)])
+def test_step_split_contraction(shapes, rank, pdt):
+    """Few rows of R and a long contraction, which then goes in parts: 13 steps of 128 and more,
+    last parts of one step, last steps of one value, lists where only some are long."""
+    run_step(shapes, rank, param_dtype=pdt, hp=REVERSE)
+
+
+def test_step_split_contraction_beside_mx4_gradients():
+    run_step([(1700, 1664)], 8)
+    run_step([(70, 1801), (1801, 70)], 33, grad="mx4", hp=REVERSE)
+    h = _lib.galore_hparams(lr=0.05, rank=33, proj_type="reverse_std")
+    p, g, s, _ = galore_case([(70, 1801), (1801, 70)], 33, 5, proj_type="reverse_std")
+    p2, g2, s2, _ = galore_case([(70, 1801), (1801, 70)], 33, 5, proj_type="reverse_std", grad="mx4")
+    both = [p[0].clone(), p2[1].clone()], [g[0], g2[1]], [{k: v.clone() for k, v in x.items()} for x in (s[0], s2[1])]
+    ws = _lib.workspace(_lib.meo_galore_mx4_workspace_size(h, p, g), DEV)
+    _lib.meo_galore_mx4_step(h, 5, p, g, s, ws)
+    _lib.meo_galore_mx4_step(h, 5, p2, g2, s2, ws)
+    _lib.meo_galore_mx4_step(h, 5, *both, ws)
+    assert torch.equal(both[0][0], p[0]) and torch.equal(both[0][1], p2[1])
+
+
+@pytest.mark.parametrize("shape,proj_type", [((2, 3), "std"), ((1, 7), "std"), ((7, 1), "std"), ((3, 2), "reverse_std"),
+                                             ((1, 8), "std"), ((2, 5), "reverse_std"), ((3, 3), "std")])
+def test_step_tensors_of_a_few_values(shape, proj_type):
+    run_step([shape], 2, hp=dict(proj_type=proj_type))
+    run_step([shape], 1, hp=dict(proj_type=proj_type), grad="mx4")
+
+
+@pytest.mark.parametrize("offset", [0, 1, 3])
+@pytest.mark.parametrize("proj_type", ["std", "reverse_std"])
+def test_projection_reads_the_gradient_only(offset, proj_type):
+    """Rows of a length that is no multiple of 8, NaN right before and behind the gradient: loads
+    that are moved back into it or run over a row's end contribute nothing."""
+    for shape in [(130, 137), (137, 130), (65, 129), (129, 65), (64, 121)]:
+        h = _lib.galore_hparams(lr=0.05, rank=24, proj_type=proj_type)
+        p, g, s, _ = galore_case([shape], 24, 9, proj_type=proj_type)
+        p2, g2, s2, _ = galore_case([shape], 24, 9, proj_type=proj_type)
+        band = torch.full((g2[0].numel() + 32,), float("nan"), dtype=torch.bfloat16, device=DEV)
+        view = band[8 + offset:8 + offset + g2[0].numel()].view(shape)
+        view.copy_(g2[0])
+        ws = _lib.workspace(_lib.meo_galore_mx4_workspace_size(h, p, g), DEV)
+        _lib.meo_galore_mx4_step(h, 5, p, g, s, ws)
+        _lib.meo_galore_mx4_step(h, 5, p2, [view], s2, ws)
+        for a, b in ((p[0], p2[0]), (s[0]["exp_avg"], s2[0]["exp_avg"]), (s[0]["exp_avg_sq"], s2[0]["exp_avg_sq"])):
+            assert torch.equal(a, b), shape
+
+
+def test_grad_scale_beside_a_bf16_gradient_is_ignored():
+    shapes, rank = [(192, 128)], 32
+    h = _lib.galore_hparams(lr=0.05, rank=rank)
+    p, g, s, _ = galore_case(shapes, rank, 3)
+    p2, g2, s2, _ = galore_case(shapes, rank, 3)
+    ws = _lib.workspace(_lib.meo_galore_mx4_workspace_size(h, p, g), DEV)
+    _lib.meo_galore_mx4_step(h, 5, p, g, s, ws)
+    tensors, arr = _lib._galore_mx4_args(h, p2, g2, s2)
+    scale = torch.full((192, 4), 127, dtype=torch.uint8, device=DEV)
+    arr[0].grad_scale = scale.data_ptr()
+    import ctypes
+    assert _lib.load().meo_galore_mx4_step(ctypes.byref(h), 5, 1, tensors, arr, ws.data_ptr(), ws.numel(),
+                                           torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(p[0], p2[0]) and torch.equal(s[0]["exp_avg"], s2[0]["exp_avg"])
+
+
 @pytest.mark.parametrize("grad", ["bf16", "mx4"])
 def test_step_llama_sized(grad):
     run_step([(1024, 4096), (4096, 1024)], 256, seed=4, grad=grad)
@@ -434,11 +503,12 @@ def test_offset_parameter_views(pdt, offset):
     assert bool((buf[:offset] == 3).all()) and bool((buf[at:] == 3).all())
 
 
-def test_step_leaves_other_memory_alone():
+@pytest.mark.parametrize("shapes,rank,proj_type", [([(257, 130), (130, 300)], 40, "std"),
+                                                   ([(70, 1801), (1793, 65)], 33, "reverse_std")])
+def test_step_leaves_other_memory_alone(shapes, rank, proj_type):
     """Guard bands round every array the step writes."""
-    shapes, rank = [(257, 130), (130, 300)], 40
-    h = _lib.galore_hparams(lr=0.05, rank=rank)
-    p, g, s, _ = galore_case(shapes, rank, 43)
+    h = _lib.galore_hparams(lr=0.05, rank=rank, proj_type=proj_type)
+    p, g, s, _ = galore_case(shapes, rank, 43, proj_type=proj_type)
     def guarded(t):
         b = torch.full((t.numel() + 128,), 7.0, dtype=t.dtype, device=DEV)
         v = b[64:64 + t.numel()].view(t.shape)
