@@ -11,6 +11,10 @@
  *   meo_came_step       CAME: Adafactor's factored statistic plus a factored
  *                       confidence statistic of the update's instability.
  *   meo_lamb_step       LAMB: Adam moments with a per-tensor trust ratio.
+ *   meo_galore_step     GaLore: AdamW on gradients projected to a low rank;
+ *                       meo_galore_mx4_step the same with 4-bit projectors.
+ *
+ * and meo_mx4_* convert and multiply the 4-bit matrices that the last one uses.
  *
  * Source of the method: the Colossal-AI distributed-optimizers page
  * ("Colossal-AI 分布式优化器全解析", blog.gitcode.com): section "Step 3" (Adafactor
@@ -542,8 +546,10 @@ int     meo_galore_refresh(const meo_galore_hparams* hp, int32_t n, const meo_te
  * The calls take no workspace and allocate nothing; descriptors travel as kernel
  * arguments, 32 matrices per launch, so the calls can be captured into a graph and run
  * concurrently on any streams. Matrices without elements are skipped. Errors as for the
- * steps: MEO_ESHAPE for negative sizes, sizes past 2^31 - 1 or a leading dimension below
- * the row length, MEO_EALIGN for codes that are not 16-byte aligned.
+ * steps: MEO_ESHAPE for negative sizes, sizes past 2^31 - 1 (k: 2^23), a leading dimension
+ * below the row length or a matrix of more than 2^23 - 1 tiles (256 blocks; transposed
+ * 128 rows x 8 blocks; of a product 64 x 128 outputs), MEO_EALIGN for codes that are
+ * not 16-byte aligned.
  */
 typedef struct meo_mx4_matrix {
     void*   data;       /* values; read by quantize, written by dequantize      */
@@ -583,7 +589,8 @@ int meo_mx4_matmul(int32_t n, const meo_mx4_product* products, void* stream);
  *     itself; left side: G^T, i.e. G quantized with `transposed`), 16-byte aligned, and
  *     `grad_scale` its scales. R = G U is then the product of the two MX4 matrices.
  *     A call that refreshes the projectors needs bf16 gradients (MEO_EDTYPE).
- * Tensors that are not 2-D take AdamW as in meo_galore_step (projector pointers NULL).
+ * d may be at most 2^23 (MEO_ESHAPE). grad_scale is read beside an MX4 gradient only. Tensors
+ * that are not 2-D take AdamW as in meo_galore_step (projector pointers NULL).
  */
 typedef struct meo_galore_mx4_state {
     float*      exp_avg;         /* [D][r] projected, [numel] otherwise               */

@@ -1842,6 +1842,8 @@ int check_galore_tensors(const meo_galore_hparams* hp, int64_t step, int32_t n, 
     }
     for (int64_t b : blocks)
         if (b > 0x7fffffffLL) return fail(MEO_ESHAPE, "the tensor list needs more than 2^31 blocks in one pass");
+    if (mx && blocks[kGaProjR] > kMxMaxGrid)
+        return fail(MEO_ESHAPE, "the tensor list has too many tiles for one launch");
     return MEO_OK;
 }
 
@@ -2402,7 +2404,7 @@ int mx4_convert(int32_t n, const meo_mx4_matrix* ms, bool transposed, bool quant
         if (m.rows == 0 || m.cols == 0) continue;
         rc = check_mx4_codes(who, m.codes, m.scales, "");
         if (rc) return rc;
-        if (grid_of(m) > kMaxDim) return fail(MEO_ESHAPE, who + "too many blocks");
+        if (grid_of(m) > kMxMaxGrid) return fail(MEO_ESHAPE, who + "too many tiles for one launch");
     }
     int dev = 0;
     int rc = current_device(&dev);
@@ -2430,7 +2432,7 @@ int mx4_convert(int32_t n, const meo_mx4_matrix* ms, bool transposed, bool quant
         const meo_mx4_matrix& m = ms[k];
         if (m.rows == 0 || m.cols == 0) continue;
         const int64_t blocks = grid_of(m);
-        if (b.n == kMxBatch || grid + blocks > kMaxDim) flush();
+        if (b.n == kMxBatch || grid + blocks > kMxMaxGrid) flush();
         MxMat& w = b.m[b.n++];
         w.data = m.data;
         w.codes = static_cast<uint8_t*>(m.codes);
@@ -2471,7 +2473,8 @@ int check_mx4_products(int32_t n, const meo_mx4_product* ps) {
         int rc = check_mx4_values(who, q.c, q.m, q.n, q.ldc, q.dtype, "c");
         if (rc) return rc;
         if (q.m == 0 || q.n == 0) continue;
-        if (ceil_div(q.m, kMxFormRows[0]) * ceil_div(q.n, kMxFormCols[0]) > kMaxDim) return fail(MEO_ESHAPE, who + "too many tiles");
+        if (ceil_div(q.m, kMxFormRows[kMxNarrow]) * ceil_div(q.n, kMxFormCols[kMxNarrow]) > kMxMaxGrid)
+            return fail(MEO_ESHAPE, who + "too many tiles for one launch");
         if (q.k == 0) continue;
         rc = check_mx4_codes(who, q.a_codes, q.a_scales, "a_");
         if (!rc) rc = check_mx4_codes(who, q.b_codes, q.b_scales, "b_");
@@ -2598,7 +2601,7 @@ int meo_mx4_matmul(int32_t n, const meo_mx4_product* ps, void* stream) {
             const meo_mx4_product& q = ps[k];
             if (q.m == 0 || q.n == 0 || form[k] != f) continue;
             const int64_t tiles = ceil_div(q.m, kMxFormRows[f]) * ceil_div(q.n, kMxFormCols[f]);
-            if (b.n == kMxBatch || grid + tiles > kMaxDim) flush();
+            if (b.n == kMxBatch || grid + tiles > kMxMaxGrid) flush();
             MxProd& p = b.p[b.n++];
             p.ac = static_cast<const uint8_t*>(q.a_codes);
             p.as = static_cast<const uint8_t*>(q.a_scales);

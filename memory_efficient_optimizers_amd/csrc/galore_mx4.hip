@@ -111,7 +111,10 @@ __device__ __forceinline__ void zero_acc(f32x16 (&acc)[IB][2]) {
 // that HBM takes per CU. kGxAny: G through registers two steps ahead, with 16-byte loads
 // at any address and zeros past its end; the scales through registers too; codes as there
 // (they are always aligned). (All waves fetching all, each step's codes and scales on
-// their own: 84 instead of 76 us for the four 4096 x 4096 matrices of a layer.)
+// their own: 8 us more for the four 4096 x 4096 matrices of a layer.)
+// Those take 73 us at rank 256, of which their bytes need 45 at the rate of a copy: about 11 go
+// into the start and the first stages, 16 into the epilogue's moments and N at the end of
+// the tiles, which all run at once.
 // Lane half h takes values 64 h .. 64 h + 63 of a step: two whole MX blocks, so a lane's
 // scale changes once per step.
 constexpr int kGdRows = kGxFormRows[kGxDirect];
@@ -513,6 +516,9 @@ void launch_gx_project_mx4(const GxTable& t, int64_t n, const GaArgs& a, int for
 // multiplied; the parameter part of a tile is loaded a whole tile ahead. (64 rows of U per wave and
 // 32 of N read half as much LDS, but their 128 VGPRs of U leave no registers to read
 // fragments ahead: 144 instead of 130 us for the MLP matrices of a layer, bf16.)
+// At rank 256 four 4096 x 4096 fp32 matrices take 120 us (a copy of their bytes 114) and 11008 x
+// 4096 and 4096 x 11008 in bf16 125 (75; as many for the products at the rate of a large
+// one: reads of W, products and stores of a tile overlap only in part).
 constexpr int kGbN = kGaTile;                                 // rows of N per tile
 constexpr int kGbDma = 2 * kGbN * (kGaWide / 8) / 512;        // 16-byte transfers per lane per tile: 8
 

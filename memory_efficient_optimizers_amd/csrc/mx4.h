@@ -12,6 +12,7 @@ namespace meo {
 
 constexpr int kMxBlock = 32;   // values per scale
 constexpr int64_t kMxMaxK = 1 << 23;  // longest contraction of a product (32-bit offsets in a tile)
+constexpr int64_t kMxMaxGrid = (1 << 23) - 1;  // blocks per launch: at most 512 threads each, below 2^32 in all
 constexpr int kMxBatch = 32;   // matrices per launch (their descriptors are kernel arguments; one
                                // alone goes by itself: 2.7 us a launch, 4.0 us with all 32)
 

@@ -7,7 +7,9 @@
 // ("transposed") a wave holds one MX block of 128 columns: a lane reads two adjacent
 // columns of 32 rows and finds their maxima in registers; the codes of 8 such waves
 // (256 values of each column) are exchanged through LDS so that each row of codes is
-// written 128 bytes at a time.
+// written 128 bytes at a time. Both are bound by HBM: along the rows 26 us for 30522 x 1024
+// fp32 values (5.4 TB/s) and 44 us back for 11008 x 4096 (4.6); down the columns of 4096 x
+// 11008 bf16 values 25 us and 23 us back (4.6 and 4.9).
 #include "mx4_tile.h"
 
 namespace meo {
@@ -280,7 +282,9 @@ void launch_mx4_dequantize(const MxBatch& b, uint32_t grid, bool transposed, hip
 
 // C = A B^T, stored from the accumulators: 32 consecutive values of two rows per
 // instruction. Tiles (MxForm): 128 rows x 256 columns of 8 waves where that fills the GPU,
-// 64 x 256 otherwise and 64 x 128 of 4 waves for products of at most 128 columns.
+// 64 x 256 otherwise and 64 x 128 of 4 waves for products of at most 128 columns (32000 x 128 x
+// 4096: 25 us, in 256-column tiles 29). 32000 x 256 x 4096 with fp32 outputs takes 33 us, 3.1
+// TB/s: its 250 tiles run at once, and all write their part of C's 33 MB at the end.
 template <int IB, bool BF>
 __device__ __forceinline__ void mx4_store(const MxProd& p, int64_t i0, int64_t j0, int lane, const f32x16 (&acc)[IB][2]) {
     const bool whole = i0 + 32 * IB <= p.m && j0 + 64 <= p.n;

@@ -239,12 +239,14 @@ struct MxTile {
 // LDS, so that nothing in the loop waits for their loads. A wave's transfers land in order, so
 // one that fetched both operands could keep A, which comes from HBM, no further ahead than
 // B, which every block reads from L2 and whose stages are the larger: half of the waves fetch
-// A, four steps ahead (64 KB in flight per CU in the 128-row tile; with 32 KB and one kind
-// of wave the product of a 32000 x 4096 gradient with a rank-256 projector took 33 us), the
-// others B, one step ahead, and the scales of two steps at a time (8 bytes per row and
-// step: fetched singly they cost the L2 as many requests as the codes). Rows of scales have
+// A, four steps ahead (64 KB in flight per CU in the 128-row tile), the others B, one step
+// ahead, and the scales of two steps at a time (8 bytes per row and step: fetched singly
+// they cost the L2 as many requests as the codes). Rows of scales have
 // any length and alignment, so these go through registers, loaded in the pair's even step
-// and stored in its odd one, by waves that wait for their transfers at each barrier anyway.
+// and stored in its odd one, by waves that wait for their transfers at each barrier anyway
+// (whole words by global_load_lds are no faster, and fragments of other rows read from global
+// memory took 181 instead of 33 us for 32000 x 256 x 4096). Products put off behind the next barrier,
+// beside the others' LDS reads, gave nothing here: 34 us.
 // Lane half h takes blocks 4 h .. 4 h + 3 of a step: its codes are 64 contiguous bytes and
 // its scales one word (the order of the contraction is free as long as both operands agree).
 // Rows past an operand's end repeat its last one (they reach outputs that are not stored);

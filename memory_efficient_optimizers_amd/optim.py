@@ -393,7 +393,9 @@ class GaLoreAdamW(_MeoOptimizer):
         projected parameters then never exist together. A gradient that the next step
         needs whole (not projected, or the step refreshes the projector) is left as it
         is. Each parameter's gradient can be compressed once per step, so gradients that
-        accumulate over several backward passes are compressed after the last."""
+        accumulate over several backward passes are compressed after the last. What reads
+        ``p.grad`` between the backward pass and the step (gradient clipping, a loss scaler)
+        does not see a compressed one, and ``state_dict`` does not hold it."""
         if not self._mx4:
             raise RuntimeError("compress_grad needs projector_dtype=torch.float4_e2m1fn_x2")
         group = next((g for g in self.param_groups if any(p is q for q in g["params"])), None)

@@ -68,6 +68,7 @@ def _mat(**kw):
     (dict(rows=-1), "MEO_ESHAPE"), (dict(cols=-1), "MEO_ESHAPE"), (dict(rows=2 ** 31), "MEO_ESHAPE"),
     (dict(cols=2 ** 31, ld=2 ** 31), "MEO_ESHAPE"), (dict(ld=63), "MEO_ESHAPE"), (dict(ld=2 ** 31), "MEO_ESHAPE"),
     (dict(rows=2 ** 31 - 1, cols=2 ** 31 - 1, ld=2 ** 31 - 1), "MEO_ESHAPE"),  # more blocks than a launch holds
+    (dict(rows=2 ** 31 - 1, cols=32), "MEO_ESHAPE"),  # one block more than a launch holds
     (dict(dtype=_lib.MEO_I8), "MEO_EDTYPE"), (dict(dtype=_lib.MEO_MX4), "MEO_EDTYPE"),
     (dict(data=None), "MEO_ENULL"), (dict(codes=None), "MEO_ENULL"), (dict(scales=None), "MEO_ENULL"),
     (dict(data=P + 2), "MEO_EALIGN"), (dict(data=P + 1, dtype=_lib.MEO_BF16), "MEO_EALIGN"),
@@ -100,7 +101,7 @@ def test_matrix_list_arguments():
 
 @pytest.mark.parametrize("kw,code", [
     (dict(m=-1), "MEO_ESHAPE"), (dict(n=-1), "MEO_ESHAPE"), (dict(k=-1), "MEO_ESHAPE"), (dict(k=2 ** 31), "MEO_ESHAPE"),
-    (dict(ldc=7), "MEO_ESHAPE"), (dict(m=2 ** 31 - 1, n=2 ** 31 - 1, ldc=2 ** 31 - 1), "MEO_ESHAPE"),
+    (dict(k=2 ** 23 + 1), "MEO_ESHAPE"), (dict(m=2 ** 31 - 1, n=1, ldc=1), "MEO_ESHAPE"), (dict(ldc=7), "MEO_ESHAPE"), (dict(m=2 ** 31 - 1, n=2 ** 31 - 1, ldc=2 ** 31 - 1), "MEO_ESHAPE"),
     (dict(dtype=_lib.MEO_I8), "MEO_EDTYPE"), (dict(c=None), "MEO_ENULL"), (dict(a_codes=None), "MEO_ENULL"),
     (dict(b_scales=None), "MEO_ENULL"), (dict(c=P + 2), "MEO_EALIGN"), (dict(a_codes=P + 4), "MEO_EALIGN"),
     (dict(b_codes=P + 8), "MEO_EALIGN"),
@@ -160,6 +161,15 @@ def test_galore_validate_needs_the_gradient_scales():
     tensors[0].ndim = 3  # not projected: no MX4 gradient
     tensors[0].grad = P
     assert _lib.load().meo_galore_mx4_validate(hp, 2, 1, tensors, arr) == _lib.MEO_EDTYPE
+
+
+@pytest.mark.parametrize("rows,cols", [(2 ** 24, 2 ** 23 + 1), (2 ** 29, 4), (4, 2 ** 29)])
+def test_galore_validate_refuses_sizes_past_a_launch(rows, cols):
+    hp = _lib.galore_hparams(rank=8)
+    p, g, st = _galore()
+    tensors, arr = _lib._galore_mx4_args(hp, [p], [g], [st])
+    tensors[0].rows, tensors[0].cols = rows, cols
+    assert _lib.load().meo_galore_mx4_validate(hp, 2, 1, tensors, arr) == _lib.MEO_ESHAPE
 
 
 def test_bf16_projector_step_refuses_an_mx4_gradient():
