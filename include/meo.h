@@ -547,9 +547,10 @@ int     meo_galore_refresh(const meo_galore_hparams* hp, int32_t n, const meo_te
  * arguments, 32 matrices per launch, so the calls can be captured into a graph and run
  * concurrently on any streams. Matrices without elements are skipped. Errors as for the
  * steps: MEO_ESHAPE for negative sizes, sizes past 2^31 - 1 (k: 2^23), a leading dimension
- * below the row length or a matrix of more than 2^23 - 1 tiles (256 blocks; transposed
- * 128 rows x 8 blocks; of a product 64 x 128 outputs), MEO_EALIGN for codes that are
- * not 16-byte aligned.
+ * below the row length or a matrix of more tiles than a launch holds (2^24 - 1 of 256
+ * blocks; transposed 2^23 - 1 of 128 rows x 8 blocks; of a product 2^24 - 1 of 64 x 128
+ * outputs for n <= 128, else 2^23 - 1 of 64 x 256), MEO_EALIGN for codes that are not
+ * 16-byte aligned.
  */
 typedef struct meo_mx4_matrix {
     void*   data;       /* values; read by quantize, written by dequantize      */

@@ -1842,7 +1842,7 @@ int check_galore_tensors(const meo_galore_hparams* hp, int64_t step, int32_t n, 
     }
     for (int64_t b : blocks)
         if (b > 0x7fffffffLL) return fail(MEO_ESHAPE, "the tensor list needs more than 2^31 blocks in one pass");
-    if (mx && blocks[kGaProjR] > kMxMaxGrid)
+    if (mx && blocks[kGaProjR] > mx_max_grid(512))
         return fail(MEO_ESHAPE, "the tensor list has too many tiles for one launch");
     return MEO_OK;
 }
@@ -2393,6 +2393,7 @@ int mx4_convert(int32_t n, const meo_mx4_matrix* ms, bool transposed, bool quant
         const int64_t nb = ceil_div(m.cols, kMxBlock);
         return transposed ? ceil_div(m.rows, kMxColRows) * ceil_div(nb, kMxColBlocks) : ceil_div(m.rows * nb, kMxRowBlocks);
     };
+    const int64_t most = mx_max_grid(transposed ? kMxColThreads : kMxRowThreads);
     for (int32_t k = 0; k < n; ++k) {
         const meo_mx4_matrix& m = ms[k];
         const std::string who = "matrix " + std::to_string(k) + ": ";
@@ -2404,7 +2405,7 @@ int mx4_convert(int32_t n, const meo_mx4_matrix* ms, bool transposed, bool quant
         if (m.rows == 0 || m.cols == 0) continue;
         rc = check_mx4_codes(who, m.codes, m.scales, "");
         if (rc) return rc;
-        if (grid_of(m) > kMxMaxGrid) return fail(MEO_ESHAPE, who + "too many tiles for one launch");
+        if (grid_of(m) > most) return fail(MEO_ESHAPE, who + "too many tiles for one launch");
     }
     int dev = 0;
     int rc = current_device(&dev);
@@ -2432,7 +2433,7 @@ int mx4_convert(int32_t n, const meo_mx4_matrix* ms, bool transposed, bool quant
         const meo_mx4_matrix& m = ms[k];
         if (m.rows == 0 || m.cols == 0) continue;
         const int64_t blocks = grid_of(m);
-        if (b.n == kMxBatch || grid + blocks > kMxMaxGrid) flush();
+        if (b.n == kMxBatch || grid + blocks > most) flush();
         MxMat& w = b.m[b.n++];
         w.data = m.data;
         w.codes = static_cast<uint8_t*>(m.codes);
@@ -2473,7 +2474,8 @@ int check_mx4_products(int32_t n, const meo_mx4_product* ps) {
         int rc = check_mx4_values(who, q.c, q.m, q.n, q.ldc, q.dtype, "c");
         if (rc) return rc;
         if (q.m == 0 || q.n == 0) continue;
-        if (ceil_div(q.m, kMxFormRows[kMxNarrow]) * ceil_div(q.n, kMxFormCols[kMxNarrow]) > kMxMaxGrid)
+        const MxForm f = mx4_form(q);
+        if (ceil_div(q.m, kMxFormRows[f]) * ceil_div(q.n, kMxFormCols[f]) > mx_max_grid(kMxFormThreads[f]))
             return fail(MEO_ESHAPE, who + "too many tiles for one launch");
         if (q.k == 0) continue;
         rc = check_mx4_codes(who, q.a_codes, q.a_scales, "a_");
@@ -2601,7 +2603,7 @@ int meo_mx4_matmul(int32_t n, const meo_mx4_product* ps, void* stream) {
             const meo_mx4_product& q = ps[k];
             if (q.m == 0 || q.n == 0 || form[k] != f) continue;
             const int64_t tiles = ceil_div(q.m, kMxFormRows[f]) * ceil_div(q.n, kMxFormCols[f]);
-            if (b.n == kMxBatch || grid + tiles > kMxMaxGrid) flush();
+            if (b.n == kMxBatch || grid + tiles > mx_max_grid(kMxFormThreads[f])) flush();
             MxProd& p = b.p[b.n++];
             p.ac = static_cast<const uint8_t*>(q.a_codes);
             p.as = static_cast<const uint8_t*>(q.a_scales);

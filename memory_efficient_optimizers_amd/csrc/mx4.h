@@ -11,8 +11,8 @@
 namespace meo {
 
 constexpr int kMxBlock = 32;   // values per scale
+constexpr int64_t mx_max_grid(int threads) { return 0xffffffffLL / threads; }  // a launch has fewer than 2^32 threads
 constexpr int64_t kMxMaxK = 1 << 23;  // longest contraction of a product (32-bit offsets in a tile)
-constexpr int64_t kMxMaxGrid = (1 << 23) - 1;  // blocks per launch: at most 512 threads each, below 2^32 in all
 constexpr int kMxBatch = 32;   // matrices per launch (their descriptors are kernel arguments; one
                                // alone goes by itself: 2.7 us a launch, 4.0 us with all 32)
 
@@ -72,6 +72,7 @@ using MxProdBatch = MxProdBatchOf<kMxBatch>;
 enum MxForm { kMxNarrow = 0, kMxWide, kMxTall, kMxForms };
 constexpr int kMxFormRows[kMxForms] = {64, 64, 128};
 constexpr int kMxFormCols[kMxForms] = {128, 256, 256};
+constexpr int kMxFormThreads[kMxForms] = {256, 512, 512};
 
 void launch_mx4_matmul(const MxProdBatch& b, uint32_t grid, MxForm form, hipStream_t s);
 

@@ -68,7 +68,7 @@ def _mat(**kw):
     (dict(rows=-1), "MEO_ESHAPE"), (dict(cols=-1), "MEO_ESHAPE"), (dict(rows=2 ** 31), "MEO_ESHAPE"),
     (dict(cols=2 ** 31, ld=2 ** 31), "MEO_ESHAPE"), (dict(ld=63), "MEO_ESHAPE"), (dict(ld=2 ** 31), "MEO_ESHAPE"),
     (dict(rows=2 ** 31 - 1, cols=2 ** 31 - 1, ld=2 ** 31 - 1), "MEO_ESHAPE"),  # more blocks than a launch holds
-    (dict(rows=2 ** 31 - 1, cols=32), "MEO_ESHAPE"),  # one block more than a launch holds
+    (dict(rows=2 ** 31 - 1, cols=64), "MEO_ESHAPE"),  # one tile more than a launch holds
     (dict(dtype=_lib.MEO_I8), "MEO_EDTYPE"), (dict(dtype=_lib.MEO_MX4), "MEO_EDTYPE"),
     (dict(data=None), "MEO_ENULL"), (dict(codes=None), "MEO_ENULL"), (dict(scales=None), "MEO_ENULL"),
     (dict(data=P + 2), "MEO_EALIGN"), (dict(data=P + 1, dtype=_lib.MEO_BF16), "MEO_EALIGN"),
