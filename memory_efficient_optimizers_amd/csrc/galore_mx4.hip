@@ -463,7 +463,7 @@ void launch_gx_join(const GxTable& t, int64_t n, const GaArgs& a, hipStream_t s)
 
 // ------------------------------------------------------------------ MX4 gradient
 
-// The product of mx4_tile.h, one column tile (r <= 256), with AdamW on R: 63 us for 11008 x 4096
+// The product of mx4_tile.h, whose column tile holds all of R's columns (MxForm), with AdamW on R: 63 us for 11008 x 4096
 // and 4096 x 11008 at rank 256 (128-row tiles; 77 with 64), whose bytes take 33 at the rate of
 // a copy: 172 tiles on 256 CUs, each first multiplying, then streaming its moments. (Their first
 // half loaded before the product: 69 us, its registers spill.)
@@ -479,20 +479,17 @@ __global__ __launch_bounds__(NW * 64) void k_gx_project_mx4(GxTable t, GaArgs a)
     const int64_t i0 = static_cast<int64_t>(it.y) * T::kRowsA;
     const MxOperand oa{reinterpret_cast<const uint8_t*>(d.g), d.gs, d.D, d.nb}, ob{d.uc, d.us, d.r, d.nb};
     float* lw = reinterpret_cast<float*>(lds) + wave * kGxEx;
-    for (int c0 = 0; c0 < d.r; c0 += T::kRowsB) {
-        f32x16 acc[IB][2];
-        zero_acc(acc);
-        mx4_accumulate<IB, WN, NW>(oa, ob, i0, c0, lds, acc);
-        const int64_t row = i0 + (wave / WN) * 32 * IB;
-        const int col = c0 + (wave % WN) * 64;
-        if (col < d.r)
+    f32x16 acc[IB][2];
+    zero_acc(acc);
+    mx4_accumulate<IB, WN, NW>(oa, ob, i0, 0, lds, acc);
+    const int64_t row = i0 + (wave / WN) * 32 * IB;
+    const int col = (wave % WN) * 64;
+    if (col >= d.r) return;
 #pragma unroll
-            for (int ib = 0; ib < IB; ++ib) {
-                GxMoments<false> mv;
-                mv.load(d, row + ib * 32, col, lane);
-                gx_epilogue(d, a, acc[ib][0], acc[ib][1], mv, row + ib * 32, col, lw, lane);
-            }
-        if (c0 + T::kRowsB < d.r) __syncthreads();  // the exchange regions are read before the stages are filled
+    for (int ib = 0; ib < IB; ++ib) {
+        GxMoments<false> mv;
+        mv.load(d, row + ib * 32, col, lane);
+        gx_epilogue(d, a, acc[ib][0], acc[ib][1], mv, row + ib * 32, col, lw, lane);
     }
 }
 

@@ -81,7 +81,6 @@ void launch_mx4_matmul(const MxProdBatch& b, uint32_t grid, MxForm form, hipStre
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bfv2 __attribute__((ext_vector_type(2)));
 
 // C += A B over 64 values of the contraction. Lane l holds one MX block of each operand
 // (row l & 31, block l >> 5: 16 bytes of codes) and its scale as byte T of sa and sb. The

@@ -644,13 +644,14 @@ def test_concurrent_streams():
         assert torch.equal(c, mx4_matmul(mx4_quantize(side[6]), q))
 
 
-def test_captured_and_replayed():
+@pytest.mark.parametrize("shapes,proj_type", [([(256, 512), (512, 256)], "std"), ([(70, 1801), (1801, 70)], "reverse_std")])
+def test_captured_and_replayed(shapes, proj_type):
     """A graph of quantize, product, dequantize and a GaLore step, replayed between eager
     work; every replay equals the eager calls. (The step's launch table is made by an eager
     call before the capture.)"""
-    h = _lib.galore_hparams(lr=0.05, rank=64)
-    p, g, s, _ = galore_case([(256, 512), (512, 256)], 64, 61)
-    pe, ge, se, _ = galore_case([(256, 512), (512, 256)], 64, 61)
+    h = _lib.galore_hparams(lr=0.05, rank=64, proj_type=proj_type)
+    p, g, s, _ = galore_case(shapes, 64, 61, proj_type=proj_type)
+    pe, ge, se, _ = galore_case(shapes, 64, 61, proj_type=proj_type)
     ws = _lib.workspace(_lib.meo_galore_mx4_workspace_size(h, p, g), DEV)
     we = _lib.workspace(_lib.meo_galore_mx4_workspace_size(h, p, g), DEV)
     x = spread((300, 320), 62)
