@@ -365,6 +365,12 @@ def test_step_weight_decay_and_late_step():
     run_step([(260, 130), (130, 260)], 48, t=187, hp=dict(weight_decay=0.1, lr=0.02, betas=(0.8, 0.95)))
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-38, 1e-14, 1e-6])
+@pytest.mark.parametrize("grad", ["bf16", "mx4"])
+def test_step_with_any_eps(eps, grad):
+    run_step([(192, 64), (64, 500), (33,)], 32, hp=dict(eps=eps), grad=grad)
+
+
 @pytest.mark.parametrize("grad", ["bf16", "mx4"])
 def test_step_mixed_list(grad):
     run_step([(192, 64), (0, 5), (64, 500), (777,), (3, 5, 7), (1,), (8, 8), (256, 512), (512, 256)], 64, seed=3, grad=grad)
