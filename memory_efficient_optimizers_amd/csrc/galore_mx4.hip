@@ -478,10 +478,10 @@ void launch_gx_join(const GxTable& t, int64_t n, const GaArgs& a, hipStream_t s)
 
 // ------------------------------------------------------------------ MX4 gradient
 
-// The product of mx4_tile.h, whose column tile holds all of R's columns (MxForm), with AdamW on R: 63 us for 11008 x 4096
-// and 4096 x 11008 at rank 256 (128-row tiles; 77 with 64), whose bytes take 33 at the rate of
-// a copy: 172 tiles on 256 CUs, each first multiplying, then streaming its moments. (Their first
-// half loaded before the product: 69 us, its registers spill.)
+// The product of mx4_tile.h, whose column tile holds all of R's columns (MxForm), with AdamW on R:
+// 61 us for 11008 x 4096 and 4096 x 11008 at rank 256 (128-row tiles; 77 with 64), whose bytes
+// take 33 at the rate of a copy: 172 tiles on 256 CUs, each first multiplying, then streaming
+// its moments. (Their first half loaded before the product: 63 us.)
 template <int IB, int WN, int NW>
 __global__ __launch_bounds__(NW * 64) void k_gx_project_mx4(GxTable t, GaArgs a) {
     using T = MxTile<IB, WN, NW>;

@@ -160,7 +160,7 @@ __device__ __forceinline__ void lds_read_tr(uint32_t p, u32x4* g) {
         "ds_read_b64_tr_b16 %3, %16 offset:1536\n\t"
         "ds_read_b64_tr_b16 %4, %16 offset:2048\n\t"
         "ds_read_b64_tr_b16 %5, %16 offset:2560\n\t"
-        "ds_read_b64_tr_b16 %6, %16 offset:3072\n\t"
+        "ds_read_b64_tr_b16 %6, %16 offset:0xc00\n\t"
         "ds_read_b64_tr_b16 %7, %16 offset:3584\n\t"
         "ds_read_b64_tr_b16 %8, %16 offset:4096\n\t"
         "ds_read_b64_tr_b16 %9, %16 offset:4608\n\t"
