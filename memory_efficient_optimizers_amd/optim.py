@@ -420,7 +420,13 @@ class GaLoreAdamW(_MeoOptimizer):
 
     def step(self, closure=None):
         """As torch's; gradients that ``compress_grad`` took are used once."""
-        loss = super().step(closure)
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for p in self._compressed:
+            self._grad(p)  # refused before any parameter's step is counted
+        super().step()
         self._compressed.clear()
         return loss
 

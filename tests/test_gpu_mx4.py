@@ -778,6 +778,74 @@ def test_compressed_gradients_do_not_accumulate():
     assert opt.state[w]["step"] == 2
 
 
+def test_refused_step_counts_for_no_parameter():
+    m, groups = _model(4)
+    opt = GaLoreAdamW(groups, lr=0.02, projector_dtype=MX4)
+    _backward(m, 1)
+    opt.step()
+    opt.zero_grad()
+    _backward(m, 2)
+    opt.compress_grad(m[2].weight)
+    _backward(m, 3)
+    before = [p.detach().clone() for p in m.parameters()]
+    with pytest.raises(RuntimeError):
+        opt.step()
+    assert all(opt.state[p]["step"] == 1 for p in m.parameters())
+    assert all(torch.equal(a, p.detach()) for a, p in zip(before, m.parameters()))
+
+
+def test_step_with_a_closure():
+    runs = []
+    for closure in (False, True):
+        m, groups = _model(5)
+        opt = GaLoreAdamW(groups, lr=0.02, projector_dtype=MX4)
+        for p in (m[0].weight, m[2].weight):
+            p.register_post_accumulate_grad_hook(opt.compress_grad)
+        for t in (1, 2, 3):
+            def backward():
+                opt.zero_grad()
+                _backward(m, t)
+                return t
+            if closure:
+                assert opt.step(backward) == t
+            else:
+                backward()
+                assert opt.step() is None
+        runs.append([p.detach().clone() for p in m.parameters()])
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
+@pytest.mark.parametrize("proj_type", ["std", "reverse_std"])
+def test_compress_grad_takes_both_sides(proj_type):
+    """Wide and tall matrices of two groups with ranks of their own; a float32 gradient that is a
+    transposed view."""
+    torch.manual_seed(6)
+    ps = [torch.nn.Parameter(0.02 * torch.randn(s, device=DEV)) for s in ((48, 130), (130, 48), (97, 33))]
+    opt = GaLoreAdamW([dict(params=ps[:2], rank=16, proj_type=proj_type), dict(params=ps[2:], rank=9, proj_type=proj_type)],
+                      lr=0.02, projector_dtype=MX4)
+    ws = [p.detach().clone() for p in ps]
+    sts = [_lib.galore_mx4_init_state(w, r, proj_type) for w, r in zip(ws, (16, 16, 9))]
+    for t in (1, 2, 3):
+        gs = []
+        for i, p in enumerate(ps):
+            g = torch.randn(p.shape[::-1], generator=torch.Generator().manual_seed(10 * t + i)).to(DEV).t()
+            p.grad = g
+            opt.compress_grad(p)
+            right = ga.galore_side(tuple(p.shape), proj_type) == "right"
+            gs.append(g.bfloat16().contiguous() if t == 1 else mx4_quantize(g.contiguous(), transposed=not right))
+            assert (p.grad is None) == (t > 1)
+        opt.step()
+        for sl, r in ((slice(0, 2), 16), (slice(2, 3), 9)):
+            h = _lib.galore_hparams(lr=0.02, rank=r, proj_type=proj_type)
+            wsp = _lib.workspace(_lib.meo_galore_mx4_workspace_size(h, ws[sl], gs[sl]), DEV)
+            _lib.meo_galore_mx4_step(h, t, ws[sl], gs[sl], sts[sl], wsp)
+        for p in ps:
+            p.grad = None
+    torch.cuda.synchronize()
+    for w, st, p in zip(ws, sts, ps):
+        assert torch.equal(w, p.detach()) and all(torch.equal(st[k], opt.state[p][k]) for k in st)
+
+
 def test_state_dict_resumes_bitwise():
     m, groups = _model(4)
     opt = GaLoreAdamW(groups, lr=0.02, projector_dtype=MX4)
