@@ -58,6 +58,9 @@
  *   (hipFree, which waits for the device). Calls over a cached list allocate
  *   nothing. meo_release_plans() frees the cache. meo_adafactor_step_noalloc
  *   never allocates.
+ * - Graph capture: a call over a cached list (one that ran before, with the same
+ *   pointers) can be captured; its tables are then kept until
+ *   meo_release_plans(), after which graphs that hold it must not be replayed.
  */
 #ifndef MEO_H
 #define MEO_H
@@ -651,7 +654,8 @@ int meo_lamb_scalar_offsets(int32_t n, const meo_tensor* tensors, int64_t* offse
  * stays valid until the next call on the same thread. */
 const char* meo_last_error(void);
 
-/* Frees the cached launch tables. Waits for the device first. */
+/* Frees the cached launch tables, those of captured calls too (their graphs must not be
+ * replayed afterwards). Waits for the device first. */
 void meo_release_plans(void);
 
 /* MEO_VERSION of the built library. */

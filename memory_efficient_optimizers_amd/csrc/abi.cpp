@@ -13,6 +13,7 @@
 #include <cstdint>
 #include <cstring>
 #include <list>
+#include <memory>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -423,10 +424,73 @@ int scalar_offsets(int op, int32_t n, const meo_tensor* ts, int64_t* out) {
 enum List { kListRc0 = 0, kListRc1, kListTiled, kListAll, kListFin1, kListFin2, kListShard, kListFold, kListEmpty,
             kListConfRows, kListConf, kListEmpty2, kListXnorm, kListCameApply, kListCount };
 
-struct Plan {
+// The device memory of a cached list's tables. Every call that uses them holds a reference, so
+// that a list evicted (or released) by another thread meanwhile is freed when the call has
+// enqueued its kernels; freeing waits for the device, and so for those.
+struct Tables {
     std::vector<uint8_t> key;
     int device = 0;
-    void* mem = nullptr;  // [n TDesc][item tables]
+    void* mem = nullptr;
+    bool captured = false;  // a graph replays kernels that read them: not evicted
+
+    Tables() = default;
+    Tables(const Tables&) = delete;
+    Tables& operator=(const Tables&) = delete;
+    ~Tables() {
+        if (!mem) return;
+        int cur = 0;
+        (void)hipGetDevice(&cur);
+        if (cur != device) (void)hipSetDevice(device);
+        (void)hipFree(mem);
+        if (cur != device) (void)hipSetDevice(cur);
+    }
+};
+
+template <class P>
+using Cache = std::list<std::shared_ptr<P>>;  // most recently used first, under g_mu
+
+bool capturing(hipStream_t s) {
+    hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(s, &st) != hipSuccess) {  // (the null stream while another one captures)
+        (void)hipGetLastError();
+        return false;
+    }
+    return st != hipStreamCaptureStatusNone;
+}
+
+// The cached tables of a list, now the most recently used, marked if stream s captures; else null.
+template <class P>
+std::shared_ptr<P> cache_find(Cache<P>& cache, const std::vector<uint8_t>& key, hipStream_t s) {
+    for (auto it = cache.begin(); it != cache.end(); ++it) {
+        if ((*it)->key != key) continue;
+        cache.splice(cache.begin(), cache, it);
+        if (!cache.front()->captured) cache.front()->captured = capturing(s);
+        return cache.front();
+    }
+    return nullptr;
+}
+
+// Uploads new tables; false with an error set.
+bool cache_upload(Tables* p, const void* bytes, size_t size) {
+    if (hipMalloc(&p->mem, size) == hipSuccess && hipMemcpy(p->mem, bytes, size, hipMemcpyHostToDevice) == hipSuccess) return true;
+    (void)hipGetLastError();
+    fail(MEO_EHIP, "could not allocate or upload the launch table");
+    return false;
+}
+
+// Adds tables; past `most` lists that no graph holds, the least recently used of them go.
+template <class P>
+void cache_add(Cache<P>& cache, const std::shared_ptr<P>& p, hipStream_t s, size_t most) {
+    p->captured = capturing(s);
+    cache.push_front(p);
+    size_t n = 0;
+    for (auto it = cache.begin(); it != cache.end();) {
+        if (!(*it)->captured && ++n > most) it = cache.erase(it);
+        else ++it;
+    }
+}
+
+struct Plan : Tables {  // mem: [n TDesc][item tables]
     int32_t n = 0;
     int32_t storage = kStoreF32;  // Storage class of the list's parameters and first moments
     const TDesc* desc = nullptr;
@@ -435,19 +499,9 @@ struct Plan {
 };
 
 std::mutex g_mu;
-std::list<Plan*> g_plans;  // most recently used first
-// Cached lists per kind (whole-tensor / row-sharded steps, GaLore). Evicting one frees
-// its device memory, which waits for the device.
-constexpr size_t kMaxPlans = 64;
-
-void free_plan(Plan* p) {
-    int cur = 0;
-    (void)hipGetDevice(&cur);
-    if (cur != p->device) (void)hipSetDevice(p->device);
-    (void)hipFree(p->mem);  // waits for work still using it
-    if (cur != p->device) (void)hipSetDevice(cur);
-    delete p;
-}
+using PlanRef = std::shared_ptr<Plan>;
+Cache<Plan>& g_plans = *new Cache<Plan>;  // (not destroyed: the HIP runtime may be gone at exit)
+constexpr size_t kMaxPlans = 64;  // cached lists per kind (whole-tensor / row-sharded steps, GaLore)
 
 // One parameter type for the whole list, and one first-moment type among the
 // tensors that keep a moment: fp32/fp32, bf16/bf16, fp32/int8 or bf16/int8;
@@ -696,8 +750,8 @@ void bind_plan(const HostPlan& h, void* dev_bytes, Plan* p) {
 // Builds (or finds) the device-resident launch tables for this list (allocated
 // once per distinct list and cached). Returns nullptr with g_err set on a failure.
 // `shards` (row-sharded steps; else null): the whole tensors' sizes, part of the key.
-Plan* get_plan(int op, int32_t n, const meo_tensor* ts, const StatePtrs* sp, int has_m, int* rc,
-               const meo_shard* shards = nullptr) {
+PlanRef get_plan(int op, int32_t n, const meo_tensor* ts, const StatePtrs* sp, int has_m, hipStream_t s, int* rc,
+                 const meo_shard* shards = nullptr) {
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess) {
         *rc = fail(MEO_EHIP, "hipGetDevice failed");
@@ -705,33 +759,19 @@ Plan* get_plan(int op, int32_t n, const meo_tensor* ts, const StatePtrs* sp, int
     }
     std::vector<uint8_t> key = plan_key(op, n, ts, sp, has_m, dev, shards);
     std::lock_guard<std::mutex> lock(g_mu);
-    for (auto it = g_plans.begin(); it != g_plans.end(); ++it) {
-        if ((*it)->key == key) {
-            Plan* p = *it;
-            g_plans.erase(it);
-            g_plans.push_front(p);
-            return p;
-        }
-    }
+    if (PlanRef p = cache_find(g_plans, key, s)) return p;
     HostPlan h;
     *rc = build_host_plan(op, n, ts, sp, has_m, dev, shards, &h);
     if (*rc) return nullptr;
-    Plan* p = new Plan;
+    PlanRef p = std::make_shared<Plan>();
     p->key = std::move(key);
     p->device = dev;
-    if (hipMalloc(&p->mem, h.bytes.size()) != hipSuccess ||
-        hipMemcpy(p->mem, h.bytes.data(), h.bytes.size(), hipMemcpyHostToDevice) != hipSuccess) {
-        if (p->mem) (void)hipFree(p->mem);
-        delete p;
-        *rc = fail(MEO_EHIP, "could not allocate or upload the launch table");
+    if (!cache_upload(p.get(), h.bytes.data(), h.bytes.size())) {
+        *rc = MEO_EHIP;
         return nullptr;
     }
-    bind_plan(h, p->mem, p);
-    g_plans.push_front(p);
-    while (g_plans.size() > kMaxPlans) {
-        free_plan(g_plans.back());
-        g_plans.pop_back();
-    }
+    bind_plan(h, p->mem, p.get());
+    cache_add(g_plans, p, s, kMaxPlans);
     return p;
 }
 
@@ -858,7 +898,6 @@ int meo_profile_collect(double* total_ms, int64_t* launches) {
 
 void meo_release_plans(void) {
     std::lock_guard<std::mutex> lock(g_mu);
-    for (Plan* p : g_plans) free_plan(p);
     g_plans.clear();
     release_galore_plans();
 }
@@ -943,10 +982,11 @@ int adafactor_step(const meo_adafactor_hparams* hp, int64_t step, int32_t n, con
     rc = check_workspace(kOpAdafactor, n, ts, ws, ws_bytes);
     if (rc) return rc;
     const std::vector<StatePtrs> sp = state_ptrs(kOpAdafactor, n, st);
-    Plan* p = get_plan(kOpAdafactor, n, ts, sp.data(), hp->has_beta1, &rc);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const PlanRef p = get_plan(kOpAdafactor, n, ts, sp.data(), hp->has_beta1, s, &rc);
     if (!p) return rc;
     if (p->n == 0) return MEO_OK;
-    return adafactor_passes(hp, step, carry, *p, static_cast<float*>(ws), static_cast<hipStream_t>(stream));
+    return adafactor_passes(hp, step, carry, *p, static_cast<float*>(ws), s);
 }
 
 // The passes of one Adafactor step over a list whose launch tables are `p` and
@@ -1149,10 +1189,10 @@ int meo_came_step(const meo_came_hparams* hp, int64_t step, int32_t n, const meo
     rc = check_workspace(kOpCame, n, ts, ws, ws_bytes);
     if (rc) return rc;
     const std::vector<StatePtrs> sp = state_ptrs(kOpCame, n, st);
-    Plan* p = get_plan(kOpCame, n, ts, sp.data(), 1, &rc);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const PlanRef p = get_plan(kOpCame, n, ts, sp.data(), 1, s, &rc);
     if (!p) return rc;
     if (p->n == 0) return MEO_OK;
-    const hipStream_t s = static_cast<hipStream_t>(stream);
     float* w = static_cast<float*>(ws);
     auto tab = [&](int l) { return Table{p->desc, p->items[l], w}; };
     const StatsArgs sa{static_cast<float>(hp->eps1), static_cast<float>(hp->beta2),
@@ -1239,10 +1279,10 @@ int meo_lamb_step(const meo_lamb_hparams* hp, int64_t step, int32_t n, const meo
     rc = check_workspace(kOpLamb, n, ts, ws, ws_bytes);
     if (rc) return rc;
     const std::vector<StatePtrs> sp = state_ptrs(kOpLamb, n, st);
-    Plan* p = get_plan(kOpLamb, n, ts, sp.data(), 1, &rc);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const PlanRef p = get_plan(kOpLamb, n, ts, sp.data(), 1, s, &rc);
     if (!p) return rc;
     if (p->n == 0) return MEO_OK;
-    const hipStream_t s = static_cast<hipStream_t>(stream);
     float* w = static_cast<float*>(ws);
     const Table t{p->desc, p->items[kListAll], w};
     const int64_t tiles = p->count[kListAll];
@@ -1312,13 +1352,13 @@ int check_shards(int op, int32_t n, const meo_tensor* ts, const meo_shard* sh, c
 }
 
 struct AfShard {
-    Plan* p = nullptr;
+    PlanRef p;
     double rho = 0.0, b2 = 0.0;
 };
 
 int af_shard_prepare(const meo_adafactor_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts,
                      const meo_shard* sh, const meo_adafactor_state* st, const void* partials, void* ws,
-                     size_t ws_bytes, AfShard* out, bool carry = false) {
+                     size_t ws_bytes, void* stream, AfShard* out, bool carry = false) {
     int rc = meo_adafactor_validate(hp, step, n, ts, st);
     if (rc) return rc;
     if (carry && hp->scale_parameter) {
@@ -1331,7 +1371,7 @@ int af_shard_prepare(const meo_adafactor_hparams* hp, int64_t step, int32_t n, c
     rc = check_workspace(kOpAdafactor, n, ts, ws, ws_bytes);
     if (rc) return rc;
     const std::vector<StatePtrs> sp = state_ptrs(kOpAdafactor, n, st);
-    out->p = get_plan(kOpAdafactor, n, ts, sp.data(), hp->has_beta1, &rc, sh);
+    out->p = get_plan(kOpAdafactor, n, ts, sp.data(), hp->has_beta1, static_cast<hipStream_t>(stream), &rc, sh);
     if (!out->p) return rc;
     const double tt = static_cast<double>(step);
     out->rho = hp->relative_step ? std::fmin(hp->warmup_init ? 1e-6 * tt : 1e-2, 1.0 / std::sqrt(tt)) : hp->lr;
@@ -1351,7 +1391,7 @@ LambArgs lamb_args(const meo_lamb_hparams* hp, int64_t step) {
 
 int lamb_shard_prepare(const meo_lamb_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts,
                        const meo_shard* sh, const meo_lamb_state* st, const void* partials, void* ws,
-                       size_t ws_bytes, Plan** out) {
+                       size_t ws_bytes, void* stream, PlanRef* out) {
     int rc = meo_lamb_validate(hp, step, n, ts, st);
     if (rc) return rc;
     if (n == 0) return MEO_OK;
@@ -1360,7 +1400,7 @@ int lamb_shard_prepare(const meo_lamb_hparams* hp, int64_t step, int32_t n, cons
     rc = check_workspace(kOpLamb, n, ts, ws, ws_bytes);
     if (rc) return rc;
     const std::vector<StatePtrs> sp = state_ptrs(kOpLamb, n, st);
-    *out = get_plan(kOpLamb, n, ts, sp.data(), 1, &rc, sh);
+    *out = get_plan(kOpLamb, n, ts, sp.data(), 1, static_cast<hipStream_t>(stream), &rc, sh);
     return *out ? MEO_OK : rc;
 }
 
@@ -1382,9 +1422,9 @@ static int af_shard_stats(const meo_adafactor_hparams* hp, int64_t step, int32_t
                    const meo_shard* sh, const meo_adafactor_state* st, float* partials, int carry, void* ws,
                    size_t ws_bytes, void* stream) {
     AfShard a;
-    int rc = af_shard_prepare(hp, step, n, ts, sh, st, partials, ws, ws_bytes, &a, carry >= 0);
+    int rc = af_shard_prepare(hp, step, n, ts, sh, st, partials, ws, ws_bytes, stream, &a, carry >= 0);
     if (rc || n == 0) return rc;
-    Plan* p = a.p;
+    const PlanRef p = a.p;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     launch_zero_records(p->items[kListEmpty], p->count[kListEmpty], partials, s);
     if (p->n == 0) return launch_status("adafactor shard statistics launch");
@@ -1429,10 +1469,10 @@ static int af_shard_apply(const meo_adafactor_hparams* hp, int64_t step, int32_t
                    const meo_shard* sh, const meo_adafactor_state* st, const float* partials, bool carry, void* ws,
                    size_t ws_bytes, void* stream) {
     AfShard a;
-    int rc = af_shard_prepare(hp, step, n, ts, sh, st, partials, ws, ws_bytes, &a, carry);
+    int rc = af_shard_prepare(hp, step, n, ts, sh, st, partials, ws, ws_bytes, stream, &a, carry);
     carry = carry && hp->scale_parameter;
     if (rc || n == 0 || a.p->n == 0) return rc;
-    Plan* p = a.p;
+    const PlanRef p = a.p;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     float* w = static_cast<float*>(ws);
     auto tab = [&](int l) { return Table{p->desc, p->items[l], w}; };
@@ -1468,8 +1508,8 @@ int meo_adafactor_shard_apply_carry(const meo_adafactor_hparams* hp, int64_t ste
 int meo_lamb_shard_stats(const meo_lamb_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts,
                          const meo_shard* sh, const meo_lamb_state* st, float* partials, void* ws, size_t ws_bytes,
                          void* stream) {
-    Plan* p = nullptr;
-    int rc = lamb_shard_prepare(hp, step, n, ts, sh, st, partials, ws, ws_bytes, &p);
+    PlanRef p;
+    int rc = lamb_shard_prepare(hp, step, n, ts, sh, st, partials, ws, ws_bytes, stream, &p);
     if (rc || n == 0) return rc;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     launch_zero_records(p->items[kListEmpty], p->count[kListEmpty], partials, s);
@@ -1486,8 +1526,8 @@ int meo_lamb_shard_stats(const meo_lamb_hparams* hp, int64_t step, int32_t n, co
 int meo_lamb_shard_apply(const meo_lamb_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts,
                          const meo_shard* sh, const meo_lamb_state* st, const float* partials, void* ws,
                          size_t ws_bytes, void* stream) {
-    Plan* p = nullptr;
-    int rc = lamb_shard_prepare(hp, step, n, ts, sh, st, partials, ws, ws_bytes, &p);
+    PlanRef p;
+    int rc = lamb_shard_prepare(hp, step, n, ts, sh, st, partials, ws, ws_bytes, stream, &p);
     if (rc || n == 0 || p->n == 0) return rc;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     float* w = static_cast<float*>(ws);
@@ -1505,7 +1545,7 @@ namespace {
 
 int came_shard_prepare(const meo_came_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts,
                        const meo_shard* sh, const meo_came_state* st, const void* partials, bool with_partials,
-                       const void* conf, bool with_conf, void* ws, size_t ws_bytes, Plan** out) {
+                       const void* conf, bool with_conf, void* ws, size_t ws_bytes, void* stream, PlanRef* out) {
     int rc = meo_came_validate(hp, step, n, ts, st);
     if (rc) return rc;
     if (n == 0) return MEO_OK;
@@ -1518,7 +1558,7 @@ int came_shard_prepare(const meo_came_hparams* hp, int64_t step, int32_t n, cons
     rc = check_workspace(kOpCame, n, ts, ws, ws_bytes);
     if (rc) return rc;
     const std::vector<StatePtrs> sp = state_ptrs(kOpCame, n, st);
-    *out = get_plan(kOpCame, n, ts, sp.data(), 1, &rc, sh);
+    *out = get_plan(kOpCame, n, ts, sp.data(), 1, static_cast<hipStream_t>(stream), &rc, sh);
     return *out ? MEO_OK : rc;
 }
 
@@ -1537,8 +1577,8 @@ size_t meo_came_confidence_size(int32_t n, const meo_tensor* ts) {
 int meo_came_shard_stats(const meo_came_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts,
                          const meo_shard* sh, const meo_came_state* st, float* partials, void* ws, size_t ws_bytes,
                          void* stream) {
-    Plan* p = nullptr;
-    int rc = came_shard_prepare(hp, step, n, ts, sh, st, partials, true, nullptr, false, ws, ws_bytes, &p);
+    PlanRef p;
+    int rc = came_shard_prepare(hp, step, n, ts, sh, st, partials, true, nullptr, false, ws, ws_bytes, stream, &p);
     if (rc || n == 0) return rc;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     launch_zero_records(p->items[kListEmpty], p->count[kListEmpty], partials, s);
@@ -1564,8 +1604,8 @@ int meo_came_shard_stats(const meo_came_hparams* hp, int64_t step, int32_t n, co
 int meo_came_shard_moment(const meo_came_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts,
                           const meo_shard* sh, const meo_came_state* st, const float* partials, float* conf,
                           void* ws, size_t ws_bytes, void* stream) {
-    Plan* p = nullptr;
-    int rc = came_shard_prepare(hp, step, n, ts, sh, st, partials, true, conf, true, ws, ws_bytes, &p);
+    PlanRef p;
+    int rc = came_shard_prepare(hp, step, n, ts, sh, st, partials, true, conf, true, ws, ws_bytes, stream, &p);
     if (rc || n == 0) return rc;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     launch_zero_records(p->items[kListEmpty2], p->count[kListEmpty2], conf, s);
@@ -1593,8 +1633,8 @@ int meo_came_shard_moment(const meo_came_hparams* hp, int64_t step, int32_t n, c
 int meo_came_shard_apply(const meo_came_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts,
                          const meo_shard* sh, const meo_came_state* st, const float* conf, void* ws,
                          size_t ws_bytes, void* stream) {
-    Plan* p = nullptr;
-    int rc = came_shard_prepare(hp, step, n, ts, sh, st, nullptr, false, conf, true, ws, ws_bytes, &p);
+    PlanRef p;
+    int rc = came_shard_prepare(hp, step, n, ts, sh, st, nullptr, false, conf, true, ws, ws_bytes, stream, &p);
     if (rc || n == 0 || p->n == 0) return rc;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     float* w = static_cast<float*>(ws);
@@ -1623,10 +1663,7 @@ enum GaList { kGaProjR = 0, kGaProjL, kGaBackR, kGaBackL, kGaFlat,
               // projector refresh
               kRfInit = kGxEnd, kRfG0N, kRfG0T, kRfG1N, kRfG1T, kRfGram, kRfOne, kRfCols, kRfStore, kGaListCount };
 
-struct GaPlan {
-    std::vector<uint8_t> key;
-    int device = 0;
-    void* mem = nullptr;  // [GDesc right..., left...][TDesc flat...][RDesc...][item tables]
+struct GaPlan : Tables {  // mem: [GDesc right..., left...][TDesc flat...][RDesc...][item tables]
     const GDesc* gdesc = nullptr;
     const GxDesc* gxdesc = nullptr;   // in gdesc's place when the projectors are MX4
     std::vector<MxMat> quant;         // MX4: the refreshed projectors' quantization
@@ -1638,17 +1675,10 @@ struct GaPlan {
     bool proj_direct[2] = {false, false};  // projection staged by global_load_lds (right, left)
     int nright = 0;  // right-side descriptors, first in gdesc
 };
-std::list<GaPlan*> g_ga_plans;  // most recently used first, under g_mu
+using GaPlanRef = std::shared_ptr<GaPlan>;
+Cache<GaPlan>& g_ga_plans = *new Cache<GaPlan>;
 
 void release_galore_plans() {  // caller holds g_mu
-    for (GaPlan* p : g_ga_plans) {
-        int cur = 0;
-        (void)hipGetDevice(&cur);
-        if (cur != p->device) (void)hipSetDevice(p->device);
-        (void)hipFree(p->mem);
-        if (cur != p->device) (void)hipSetDevice(cur);
-        delete p;
-    }
     g_ga_plans.clear();
 }
 
@@ -1968,8 +1998,8 @@ void gx_lists(std::vector<GxDesc>& gd, std::vector<int2>* lists) {
     }
 }
 
-GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, const GaState* st, bool mx,
-                        void* ws, int* rc) {
+GaPlanRef get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, const GaState* st, bool mx,
+                          void* ws, hipStream_t s, int* rc) {
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess) {
         *rc = fail(MEO_EHIP, "hipGetDevice failed");
@@ -1986,14 +2016,7 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
         std::memcpy(w, st, n * sizeof(GaState));
     }
     std::lock_guard<std::mutex> lock(g_mu);
-    for (auto it = g_ga_plans.begin(); it != g_ga_plans.end(); ++it) {
-        if ((*it)->key == key) {
-            GaPlan* p = *it;
-            g_ga_plans.erase(it);
-            g_ga_plans.push_front(p);
-            return p;
-        }
-    }
+    if (GaPlanRef p = cache_find(g_ga_plans, key, s)) return p;
     *rc = check_galore_memory(hp, n, ts, st, mx, dev);
     if (*rc) return nullptr;
     std::vector<int64_t> woff, roff;
@@ -2192,7 +2215,7 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
     if (!rd.empty()) std::memcpy(host.data() + roffb, rd.data(), rd.size() * sizeof(RDesc));
     for (int l = 0; l < kGaListCount; ++l)
         if (!lists[l].empty()) std::memcpy(host.data() + offs[l], lists[l].data(), lists[l].size() * sizeof(int2));
-    GaPlan* p = new GaPlan;
+    GaPlanRef p = std::make_shared<GaPlan>();
     p->key = std::move(key);
     p->device = dev;
     p->back_mode[0] = back_mode[0];
@@ -2200,11 +2223,8 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
     p->proj_direct[0] = proj_direct[0];
     p->proj_direct[1] = proj_direct[1];
     p->nright = static_cast<int>(right.size());
-    if (hipMalloc(&p->mem, host.size()) != hipSuccess ||
-        hipMemcpy(p->mem, host.data(), host.size(), hipMemcpyHostToDevice) != hipSuccess) {
-        if (p->mem) (void)hipFree(p->mem);
-        delete p;
-        *rc = fail(MEO_EHIP, "could not allocate or upload the launch table");
+    if (!cache_upload(p.get(), host.data(), host.size())) {
+        *rc = MEO_EHIP;
         return nullptr;
     }
     uint8_t* base = static_cast<uint8_t*>(p->mem);
@@ -2217,13 +2237,7 @@ GaPlan* get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tenso
         p->items[l] = reinterpret_cast<const int2*>(base + offs[l]);
         p->count[l] = static_cast<int64_t>(lists[l].size());
     }
-    g_ga_plans.push_front(p);
-    while (g_ga_plans.size() > kMaxPlans) {
-        GaPlan* q = g_ga_plans.back();
-        g_ga_plans.pop_back();
-        (void)hipFree(q->mem);
-        delete q;
-    }
+    cache_add(g_ga_plans, p, s, kMaxPlans);
     return p;
 }
 
@@ -2236,7 +2250,7 @@ int ga_refresh(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, co
     for (int32_t k = 0; k < n; ++k)
         if (ga_projected(ts[k]) && ts[k].grad_dtype == MEO_MX4)
             return fail(MEO_EDTYPE, "tensor " + std::to_string(k) + ": a projector refresh needs a bf16 gradient");
-    GaPlan* p = get_galore_plan(hp, n, ts, st.data(), mx, ws, &rc);
+    const GaPlanRef p = get_galore_plan(hp, n, ts, st.data(), mx, ws, s, &rc);
     if (!p) return rc;
     auto tab = [&](int l) { return RTable{p->rdesc, p->items[l]}; };
     auto cnt = [&](int l) { return p->count[l]; };
@@ -2308,7 +2322,7 @@ int ga_step(const meo_galore_hparams* hp, int64_t step, int32_t n, const meo_ten
         rc = ga_refresh(hp, n, ts, st, mx, ws, ws_bytes, s);
         if (rc) return rc;
     }
-    GaPlan* p = get_galore_plan(hp, n, ts, st.data(), mx, ws, &rc);
+    const GaPlanRef p = get_galore_plan(hp, n, ts, st.data(), mx, ws, s, &rc);
     if (!p) return rc;
     const double tt = static_cast<double>(step);
     const double bc1 = 1.0 - std::pow(hp->beta1, tt), bc2 = 1.0 - std::pow(hp->beta2, tt);
