@@ -72,7 +72,7 @@
 extern "C" {
 #endif
 
-#define MEO_VERSION 9
+#define MEO_VERSION 10
 
 /* Return codes. */
 #define MEO_OK          0
@@ -613,6 +613,25 @@ int    meo_galore_mx4_step(const meo_galore_hparams* hp, int64_t step, int32_t n
 int    meo_galore_mx4_refresh(const meo_galore_hparams* hp, int32_t n, const meo_tensor* tensors,
                               const meo_galore_mx4_state* states, void* workspace, size_t workspace_bytes,
                               void* stream);
+
+/*
+ * For tests and diagnostics: the kernel forms that the sizes, types and addresses of a call
+ * choose. Host only; no pointer is followed. meo_galore_mx4_forms writes one record per
+ * tensor of a meo_galore_mx4_step (zeros for one that is not projected; errors as
+ * meo_galore_mx4_validate, and MEO_ENULL for NULL forms with n > 0), meo_mx4_matmul_rows
+ * returns the rows of a product's tiles (0 for an empty product).
+ */
+typedef struct meo_galore_mx4_form {
+    int32_t rows;        /* rows of R per projection tile                                 */
+    int32_t aligned;     /* the gradient goes straight into LDS (always so for MX4)        */
+    int32_t parts;       /* parts of the contraction whose sums are added up in order       */
+    int32_t split;       /* each part is computed by blocks of its own                       */
+    int32_t back_tiles;  /* 64-row tiles of N per block of the back-projection                */
+} meo_galore_mx4_form;
+
+int     meo_galore_mx4_forms(const meo_galore_hparams* hp, int32_t n, const meo_tensor* tensors,
+                             const meo_galore_mx4_state* states, meo_galore_mx4_form* forms);
+int32_t meo_mx4_matmul_rows(int64_t m, int64_t n);
 
 /* ------------------------------------------------------- per-tensor scalars */
 

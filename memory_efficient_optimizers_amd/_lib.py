@@ -47,6 +47,7 @@ EXPORTS = [
     "meo_adafactor_step_noalloc",
     "meo_mx4_quantize", "meo_mx4_dequantize", "meo_mx4_matmul",
     "meo_galore_mx4_workspace_size", "meo_galore_mx4_validate", "meo_galore_mx4_step", "meo_galore_mx4_refresh",
+    "meo_galore_mx4_forms", "meo_mx4_matmul_rows",
 ]
 MEO_NOALLOC_SCRATCH_BYTES = 64 << 20
 MEO_NUM_PASSES = 17
@@ -133,6 +134,10 @@ class meo_mx4_product(ctypes.Structure):
 class meo_galore_mx4_state(ctypes.Structure):
     _fields_ = [("exp_avg", c_void_p), ("exp_avg_sq", c_void_p), ("projector", c_void_p),
                 ("projector_scale", c_void_p), ("grad_scale", c_void_p)]
+
+
+class meo_galore_mx4_form(ctypes.Structure):
+    _fields_ = [(k, c_int32) for k in ("rows", "aligned", "parts", "split", "back_tiles")]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -231,6 +236,10 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.meo_galore_mx4_step.restype = ctypes.c_int
     lib.meo_galore_mx4_refresh.argtypes = [GH, c_int32, T, GX, c_void_p, c_size_t, c_void_p]
     lib.meo_galore_mx4_refresh.restype = ctypes.c_int
+    lib.meo_galore_mx4_forms.argtypes = [GH, c_int32, T, GX, ctypes.POINTER(meo_galore_mx4_form)]
+    lib.meo_galore_mx4_forms.restype = ctypes.c_int
+    lib.meo_mx4_matmul_rows.argtypes = [c_int64, c_int64]
+    lib.meo_mx4_matmul_rows.restype = c_int32
     for name, arr in (("meo_mx4_quantize", MM), ("meo_mx4_dequantize", MM)):
         getattr(lib, name).argtypes = [c_int32, arr, c_int32, c_void_p]
         getattr(lib, name).restype = ctypes.c_int
@@ -989,6 +998,19 @@ def meo_galore_mx4_refresh(hp, params, grads, states, workspace=None, stream=Non
     ws, nb = _ws(workspace)
     tensors, arr = _galore_mx4_args(hp, params, grads, states)
     _check(load().meo_galore_mx4_refresh(ctypes.byref(hp), len(params), tensors, arr, ws, nb, _stream(stream)))
+
+
+def meo_galore_mx4_forms(hp, params, grads, states) -> List[meo_galore_mx4_form]:
+    """The kernel forms of a meo_galore_mx4_step, one record per tensor (host only)."""
+    tensors, arr = _galore_mx4_args(hp, params, grads, states)
+    forms = (meo_galore_mx4_form * max(len(params), 1))()
+    _check(load().meo_galore_mx4_forms(ctypes.byref(hp), len(params), tensors, arr, forms))
+    return list(forms)[:len(params)]
+
+
+def meo_mx4_matmul_rows(m: int, n: int) -> int:
+    """Rows of the tiles of an MX4 product with m x n outputs (host only)."""
+    return int(load().meo_mx4_matmul_rows(m, n))
 
 
 def galore_mx4_state_shapes(shape, rank: int, proj_type: str = "std") -> Dict[str, tuple]:

@@ -1933,7 +1933,10 @@ int check_galore_workspace(const meo_galore_hparams* hp, int32_t n, const meo_te
 // 25, 40000 rows 62 and 72).
 bool mx4_tall(int64_t tall, int64_t wide) { return 4 * ceil_div(tall, kCus) < 3 * ceil_div(wide, kCus); }
 
-// Items of a step with MX4 projectors over its descriptors; sets btj and tpi. The products'
+// Rows of R per projection tile.
+int64_t gx_rows(const GxDesc& d) { return d.gs ? kMxFormRows[d.form] : kGxFormRows[d.form]; }
+
+// Items of a step with MX4 projectors over its descriptors; sets form, btj and tpi. The products'
 // form and the tiles per back-projection item follow the call's total work.
 void gx_lists(std::vector<GxDesc>& gd, std::vector<int2>* lists) {
     // (d a multiple of 128: whole words of scales)
@@ -1949,17 +1952,16 @@ void gx_lists(std::vector<GxDesc>& gd, std::vector<int2>* lists) {
             wide += ceil_div(d.D, kMxFormRows[kMxWide]);
         }
     for (size_t i = 0; i < gd.size(); ++i) {
-        const GxDesc& d = gd[i];
-        int list, rows;
+        GxDesc& d = gd[i];
+        int list;
         if (d.gs) {
-            const int form = d.r <= kMxFormCols[kMxNarrow] ? kMxNarrow : mx4_tall(tall, wide) ? kMxTall : kMxWide;
-            list = kGxProjM + form;
-            rows = kMxFormRows[form];
+            d.form = d.r <= kMxFormCols[kMxNarrow] ? kMxNarrow : mx4_tall(tall, wide) ? kMxTall : kMxWide;
+            list = kGxProjM + d.form;
         } else {
-            const int form = all_direct ? kGxDirect : kGxAny;
-            list = kGxProj + form;
-            rows = kGxFormRows[form];
+            d.form = all_direct ? kGxDirect : kGxAny;
+            list = kGxProj + d.form;
         }
+        const int64_t rows = gx_rows(d);
         for (int64_t y = 0; y < ceil_div(d.D, rows) * d.ks; ++y) lists[list].push_back(make_int2(static_cast<int>(i), static_cast<int>(y)));
         if (d.ks > 1)
             for (int64_t y = 0; y < ceil_div(static_cast<int64_t>(d.D) * (d.rp / 8), kGxJoinChunks); ++y)
@@ -1996,6 +1998,40 @@ void gx_lists(std::vector<GxDesc>& gd, std::vector<int2>* lists) {
             return a.x == b.x && a.y % gd[a.x].btj == b.y % gd[b.x].btj;
         });
     }
+}
+
+// The descriptor of a projected tensor without its workspace; per as gx_split gives it.
+GxDesc ga_desc(const meo_galore_hparams* hp, const meo_tensor& t, const GaState& s, bool mx, int64_t per) {
+    GxDesc d;
+    std::memset(static_cast<void*>(&d), 0, sizeof d);
+    d.m = static_cast<int32_t>(t.rows);
+    d.n = static_cast<int32_t>(t.cols);
+    d.D = static_cast<int32_t>(ga_rows(hp, t));
+    d.d = static_cast<int32_t>(ga_basis(hp, t));
+    d.r = ga_rank(hp, t);
+    d.g = static_cast<const uint16_t*>(t.grad);
+    d.x = t.param;
+    d.xbf16 = t.param_dtype == MEO_BF16;
+    d.em = s.em;
+    d.ev = s.ev;
+    d.u = static_cast<uint16_t*>(s.u);
+    d.ut = static_cast<uint16_t*>(s.ut);
+    const bool g4 = t.grad_dtype == MEO_MX4;
+    d.rp = gx_pitch(d.r);
+    d.vec = aligned16(d.g) && aligned16(d.u) && aligned16(d.ut) && d.n % 8 == 0 && d.d % 8 == 0 && d.r % 8 == 0;
+    if (mx) {
+        d.uc = static_cast<const uint8_t*>(s.uc);
+        d.us = static_cast<const uint8_t*>(s.us);
+        d.gs = g4 ? static_cast<const uint8_t*>(s.gs) : nullptr;
+        d.nb = static_cast<int32_t>(ceil_div(d.d, kMxBlock));
+        d.vec = aligned16(d.g) && d.n % 8 == 0;  // 16-byte rows of a bf16 gradient
+        d.ks = g4 ? 1 : static_cast<int32_t>(gx_parts(d.d, per));
+        d.kper = d.ks > 1 ? static_cast<int32_t>(per) : (d.d + kGxStep - 1) / kGxStep;
+    }
+    d.rvec = aligned16(d.em) && aligned16(d.ev) && d.r % 8 == 0;
+    d.wvec = aligned16(d.x) && d.n % 8 == 0;
+    d.btj = static_cast<int32_t>(ga_left(hp, t) ? ceil_div(d.n, kGaTile * kGaBackRW) : ceil_div(d.n, kGaWide));
+    return d;
 }
 
 GaPlanRef get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, const GaState* st, bool mx,
@@ -2035,41 +2071,13 @@ GaPlanRef get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_ten
         if (numel == 0) continue;
         const GaState& s = st[k];
         if (ga_projected(t)) {
-            GxDesc d;
-            std::memset(static_cast<void*>(&d), 0, sizeof d);
-            d.m = static_cast<int32_t>(t.rows);
-            d.n = static_cast<int32_t>(t.cols);
-            const bool is_left = ga_left(hp, t);
-            d.D = static_cast<int32_t>(ga_rows(hp, t));
-            d.d = static_cast<int32_t>(ga_basis(hp, t));
-            d.r = ga_rank(hp, t);
-            d.g = static_cast<const uint16_t*>(t.grad);
-            d.x = t.param;
-            d.xbf16 = t.param_dtype == MEO_BF16;
-            d.em = s.em;
-            d.ev = s.ev;
-            d.u = static_cast<uint16_t*>(s.u);
-            d.ut = static_cast<uint16_t*>(s.ut);
-            const bool g4 = t.grad_dtype == MEO_MX4;
+            GxDesc d = ga_desc(hp, t, s, mx, per);
+            const bool g4 = t.grad_dtype == MEO_MX4, is_left = ga_left(hp, t);
             uint8_t* wb = static_cast<uint8_t*>(ws) + woff[k];
+            const int64_t plane = align256(static_cast<int64_t>(d.D) * (mx ? d.rp : d.r) * 2);
             d.nh = reinterpret_cast<uint16_t*>(wb);
-            d.rp = gx_pitch(d.r);
-            d.nl = reinterpret_cast<uint16_t*>(wb + align256(static_cast<int64_t>(d.D) * (mx ? d.rp : d.r) * 2));
-            d.vec = aligned16(d.g) && aligned16(d.u) && aligned16(d.ut) && d.n % 8 == 0 && d.d % 8 == 0 &&
-                    d.r % 8 == 0;
-            if (mx) {
-                d.uc = static_cast<const uint8_t*>(s.uc);
-                d.us = static_cast<const uint8_t*>(s.us);
-                d.gs = g4 ? static_cast<const uint8_t*>(s.gs) : nullptr;
-                d.nb = static_cast<int32_t>(ceil_div(d.d, kMxBlock));
-                d.vec = aligned16(d.g) && d.n % 8 == 0;  // 16-byte rows of a bf16 gradient
-                d.ks = g4 ? 1 : static_cast<int32_t>(gx_parts(d.d, per));
-                d.kper = d.ks > 1 ? static_cast<int32_t>(per) : (d.d + kGxStep - 1) / kGxStep;
-                d.part = reinterpret_cast<float*>(wb + 2 * align256(static_cast<int64_t>(d.D) * d.rp * 2));
-            }
-            d.rvec = aligned16(d.em) && aligned16(d.ev) && d.r % 8 == 0;
-            d.wvec = aligned16(d.x) && d.n % 8 == 0;
-            d.btj = static_cast<int32_t>(is_left ? ceil_div(d.n, kGaTile * kGaBackRW) : ceil_div(d.n, kGaWide));
+            d.nl = reinterpret_cast<uint16_t*>(wb + plane);
+            if (mx) d.part = reinterpret_cast<float*>(wb + 2 * plane);
             (is_left ? left : right).push_back(d);
             (is_left ? kl : kr).push_back(k);
             if (g4) continue;  // not refreshed
@@ -2558,6 +2566,40 @@ int meo_galore_mx4_validate(const meo_galore_hparams* hp, int64_t step, int32_t 
     const int rc = check_galore_hp(hp);
     if (rc) return rc;
     return check_galore_tensors(hp, step, n, ts, st ? ga_states(n, st).data() : nullptr, true);
+}
+
+int meo_galore_mx4_forms(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, const meo_galore_mx4_state* st,
+                         meo_galore_mx4_form* forms) {
+    const int rc = meo_galore_mx4_validate(hp, 1, n, ts, st);
+    if (rc || n == 0) return rc;
+    if (!forms) return fail(MEO_ENULL, "forms is NULL");
+    const std::vector<GaState> states = ga_states(n, st);
+    const int64_t per = gx_split(hp, n, ts);
+    std::vector<GxDesc> gd;
+    for (int32_t k = 0; k < n; ++k)
+        if (ga_projected(ts[k])) gd.push_back(ga_desc(hp, ts[k], states[k], true, per));
+    std::vector<int2> lists[kGaListCount];
+    gx_lists(gd, lists);
+    size_t i = 0;
+    for (int32_t k = 0; k < n; ++k) {
+        std::memset(&forms[k], 0, sizeof forms[k]);
+        if (!ga_projected(ts[k])) continue;
+        const GxDesc& d = gd[i++];
+        forms[k].rows = static_cast<int32_t>(gx_rows(d));
+        forms[k].aligned = d.gs || d.form == kGxDirect;
+        forms[k].parts = d.ks;
+        forms[k].split = d.ks > 1;
+        forms[k].back_tiles = d.tpi;
+    }
+    return MEO_OK;
+}
+
+int32_t meo_mx4_matmul_rows(int64_t m, int64_t n) {
+    meo_mx4_product q;
+    std::memset(&q, 0, sizeof q);
+    q.m = m;
+    q.n = n;
+    return m > 0 && n > 0 ? kMxFormRows[mx4_form(q)] : 0;
 }
 
 int meo_galore_refresh(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, const meo_galore_state* st,

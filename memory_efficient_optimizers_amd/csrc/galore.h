@@ -50,6 +50,7 @@ struct GxDesc : GDesc {
     const uint8_t* gs;
     int32_t nb;         // blocks along d
     int32_t rp;         // r rounded up to 32: two of the back-projection's sub-steps
+    int32_t form;       // projection: GxForm; of an MX4 gradient MxForm
     int32_t tpi;        // back-projection: 64-row tiles of N per item
     float* part;        // split contraction (ks > 1): R's parts, [ks][D][rp]
     int32_t ks, kper;   // parts, and steps of kGxStep in each but the last

@@ -256,3 +256,48 @@ def test_optimizer_refusals():
         opt.compress_grad(torch.nn.Parameter(torch.zeros(2, 2)))
     opt.compress_grad(p)  # the first step refreshes the projector: the gradient stays
     assert p.grad is not None
+
+
+# ------------------------------------------------------------------------------ kernel forms
+
+def _forms(shapes, rank, grad="bf16", proj_type="std"):
+    hp = _lib.galore_hparams(rank=rank, proj_type=proj_type)
+    params, grads, states = [], [], []
+    for s in shapes:
+        p = torch.empty(s, device="meta")
+        params.append(p)
+        right = (s[0] >= s[1]) == (proj_type == "std") if len(s) == 2 else True
+        n, m = s if right and len(s) == 2 else s[::-1] if len(s) == 2 else (0, 0)
+        mx = grad == "mx4" and len(s) == 2
+        grads.append(MX4Tensor.empty(n, m, "meta") if mx else torch.empty(s, dtype=torch.bfloat16, device="meta"))
+        states.append(_lib.galore_mx4_init_state(p, rank, proj_type) if len(s) == 2 else
+                      {k: torch.zeros(s, device="meta") for k in ("exp_avg", "exp_avg_sq")})
+    tensors, arr = _lib._galore_mx4_args(hp, params, grads, states)
+    for t, a in zip(tensors, arr):  # validation inspects pointers and follows none
+        t.param = t.grad = a.exp_avg = a.exp_avg_sq = P
+        if a.projector is not None or t.ndim == 2:
+            a.projector = a.projector_scale = a.grad_scale = P
+    out = (_lib.meo_galore_mx4_form * len(shapes))()
+    _lib._check(_lib.load().meo_galore_mx4_forms(hp, len(shapes), tensors, arr, out))
+    return out
+
+
+def test_forms_of_a_step():
+    f = _forms([(4096, 4096)], 64)[0]
+    assert (f.rows, f.aligned, f.parts, f.split) == (64, 1, 4, 1) and f.back_tiles >= 1
+    f = _forms([(4096, 4097), (777,)], 64)
+    assert (f[0].rows, f[0].aligned) == (64, 0) and not any(getattr(f[1], k) for k, _ in f[1]._fields_)
+    assert _forms([(11008, 4096), (4096, 11008)], 256, grad="mx4")[0].rows == 128
+    assert _forms([(11008, 4096)], 256, grad="mx4")[0].rows == 64
+    with pytest.raises(MeoError):
+        _forms([(600, 520)], 512)
+    hp = _lib.galore_hparams(rank=8)
+    p, g, st = _galore()
+    tensors, arr = _lib._galore_mx4_args(hp, [p], [g], [st])
+    assert _lib.load().meo_galore_mx4_forms(hp, 1, tensors, arr, None) == _lib.MEO_ENULL
+    assert len(_lib.meo_galore_mx4_forms(hp, [p], [g], [st])) == 1
+
+
+def test_rows_of_a_product():
+    assert [_lib.meo_mx4_matmul_rows(*s) for s in ((0, 5), (5, 0), (1, 1), (40000, 128), (32000, 256), (16384, 256))] == \
+        [0, 0, 64, 64, 128, 64]
