@@ -625,7 +625,7 @@ typedef struct meo_galore_mx4_form {
     int32_t rows;        /* rows of R per projection tile                                 */
     int32_t aligned;     /* the gradient goes straight into LDS (always so for MX4)        */
     int32_t parts;       /* parts of the contraction whose sums are added up in order       */
-    int32_t split;       /* each part is computed by blocks of its own                       */
+    int32_t item_parts;  /* of them per block: fewer than parts where the sum is a launch of its own */
     int32_t back_tiles;  /* 64-row tiles of N per block of the back-projection                */
 } meo_galore_mx4_form;
 

@@ -137,7 +137,7 @@ class meo_galore_mx4_state(ctypes.Structure):
 
 
 class meo_galore_mx4_form(ctypes.Structure):
-    _fields_ = [(k, c_int32) for k in ("rows", "aligned", "parts", "split", "back_tiles")]
+    _fields_ = [(k, c_int32) for k in ("rows", "aligned", "parts", "item_parts", "back_tiles")]
 
 
 _lib: Optional[ctypes.CDLL] = None

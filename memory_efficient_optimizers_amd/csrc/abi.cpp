@@ -450,8 +450,9 @@ template <class P>
 using Cache = std::list<std::shared_ptr<P>>;  // most recently used first, under g_mu
 
 bool capturing(hipStream_t s) {
+    if (!s) return false;  // the null stream cannot be
     hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
-    if (hipStreamIsCapturing(s, &st) != hipSuccess) {  // (the null stream while another one captures)
+    if (hipStreamIsCapturing(s, &st) != hipSuccess) {
         (void)hipGetLastError();
         return false;
     }
@@ -1738,28 +1739,84 @@ int64_t align256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
 constexpr int64_t kCus = 256;
 
-// MX4 projectors: steps of the contraction per part of a projection (a multiple of 4), 0 where it
-// stays whole. Where the tiles of all R leave CUs idle, the contraction is split into as many
-// parts as fill them; the parts' sum is a launch of its own (4 to 10 us), taken as kGxJoinSteps
-// steps of 1 to 1.5 us. Whole, and in parts with their sum: 4096 x 4096 at rank 256 49 and 32
-// us, at 64 29 and 20; 1951 x 3810 with 3750 x 4266 at 177 60 and 48; 1536 x 1536 at 64 16 and
-// 12; below that the two are even.
+// MX4 projectors: the contraction of a projection is summed in parts of gx_per steps each (a
+// multiple of 4; 0: in one), whose sums are added up in order. The parts follow from the
+// tensor alone, so its results do not depend on the list; how many of them an item takes
+// (gx_span) does. They are as many as fill the CUs that the tiles of R leave idle when the tensor
+// is stepped alone. Whole, and in parts with their sum: 4096 x 4096 at rank 256 49 and 32 us, at
+// 64 29 and 20; 1536 x 1536 at 64 16 and 12; below kGxJoinSteps more than a part the two are even.
 constexpr int64_t kGxJoinSteps = 4;
-int64_t gx_split(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts) {
-    int64_t most = 0;
-    for (int32_t k = 0; k < n; ++k)
-        if (ga_rank(hp, ts[k])) most = std::max(most, ceil_div(ga_basis(hp, ts[k]), kGxStep));
-    for (int64_t per = 4; per + kGxJoinSteps < most; per += 4) {
-        int64_t items = 0;
-        for (int32_t k = 0; k < n && items <= kCus; ++k)
-            if (ga_rank(hp, ts[k]))
-                items += ceil_div(ga_rows(hp, ts[k]), kGxFormRows[kGxAny]) * ceil_div(ceil_div(ga_basis(hp, ts[k]), kGxStep), per);
-        if (items <= kCus) return per;
-    }
+int64_t gx_per(const meo_galore_hparams* hp, const meo_tensor& t) {
+    const int64_t tiles = ceil_div(ga_rows(hp, t), kGxFormRows[kGxAny]), steps = ceil_div(ga_basis(hp, t), kGxStep);
+    for (int64_t per = 4; per + kGxJoinSteps < steps; per += 4)
+        if (tiles * ceil_div(steps, per) <= kCus) return per;
     return 0;
 }
 
-int64_t gx_parts(int64_t d, int64_t per) { return per ? ceil_div(ceil_div(d, kGxStep), per) : 1; }
+int64_t gx_parts(const meo_galore_hparams* hp, const meo_tensor& t) {
+    const int64_t per = gx_per(hp, t);
+    return per ? ceil_div(ceil_div(ga_basis(hp, t), kGxStep), per) : 1;
+}
+
+// Steps that an item of a list's projections takes, in whole parts, at most; 0: every item takes
+// all parts of its rows, which needs no sums in memory. The span with the least time by a model
+// in us: a step takes 0.55 to 1.28 by the rank, 0.7 more where gradients go through registers, half
+// as much again when every CU has an item, an item's fill two steps; items run all at once, or their
+// average load and half of the longest; sums cost a launch and their traffic. Whole, in spans of
+// 16, 8 and 4 steps (* chosen): four 2048 x 2048 at rank 128 *50, -, 55, 63; one 4096 x 4096 at 64
+// 54, -, *45; two 74, *71, 75; 1951 x 3810 and 3750 x 4266 at 177 119, *109, 116, 114; two 1601 x
+// 2001 at 32 48, -, 44, *38; three 512 x 8192 on the longer side at 128 80, 57, *50, 53. The
+// gradients' types do not count: a step with MX4 gradients, which are not split, has the same
+// workspace.
+int64_t gx_span(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts) {
+    struct Tensor {
+        int64_t tiles, steps, per, rp;
+    };
+    std::vector<Tensor> v;
+    int64_t tiles = 0, longest = 0, rp = 0;
+    bool aligned = true;
+    for (int32_t k = 0; k < n; ++k) {
+        if (!ga_rank(hp, ts[k])) continue;
+        v.push_back({ceil_div(ga_rows(hp, ts[k]), kGxFormRows[kGxAny]), ceil_div(ga_basis(hp, ts[k]), kGxStep), gx_per(hp, ts[k]),
+                     gx_pitch(ga_rank(hp, ts[k]))});
+        tiles += v.back().tiles;
+        rp = std::max(rp, v.back().rp);
+        if (v.back().per) longest = std::max(longest, v.back().steps);
+        aligned = aligned && ts[k].cols % 8 == 0 && ga_basis(hp, ts[k]) % kGxStep == 0;
+    }
+    if (tiles > kCus) return 0;  // items enough
+    const double step = (aligned ? 0.55 : 1.25) + 0.73 * static_cast<double>(rp) / kGaWide;
+    int64_t best = 0;
+    double least = 0.0;
+    for (int64_t span = 0; span < longest; span += 4) {
+        int64_t items = 0, sum = 0, most = 0, bytes = 0;
+        auto add = [&](int64_t count, int64_t steps) {
+            items += count;
+            sum += count * (steps + 2);
+            if (count > 0) most = std::max(most, steps + 2);
+        };
+        for (const Tensor& t : v) {
+            const int64_t per = t.per ? t.per : t.steps, len = span ? std::max(span / per, int64_t{1}) * per : t.steps;
+            add(t.tiles * (t.steps / len), len);
+            add(t.steps % len ? t.tiles : 0, t.steps % len);
+            if (len < t.steps) bytes += t.tiles * ceil_div(t.steps, per) * kGxFormRows[kGxAny] * t.rp * 8;
+        }
+        const double load = items <= kCus ? static_cast<double>(most) : static_cast<double>(sum) / kCus + 0.5 * static_cast<double>(most);
+        const double time = load * step * (1.0 + 0.5 * static_cast<double>(std::min(items, kCus)) / kCus) +
+                            (bytes ? 5.0 + static_cast<double>(bytes) / 4.5e6 : 0.0);
+        if (span == 0 || time < least) {
+            least = time;
+            best = span;
+        }
+    }
+    return best;
+}
+
+// Parts per item.
+int64_t gx_item_parts(const meo_galore_hparams* hp, const meo_tensor& t, int64_t span) {
+    const int64_t per = gx_per(hp, t), parts = gx_parts(hp, t);
+    return span && per ? std::min(std::max(span / per, int64_t{1}), parts) : parts;
+}
 
 // Workspace, per projected tensor, every array at a 256-byte boundary (offsets in
 // bytes): the step's two bf16 planes of N, [D][r] each (mx: MX4 projectors: rows of rp
@@ -1771,13 +1828,14 @@ int64_t ga_layout(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts,
     int64_t off = 0;
     if (offs) offs->assign(n, -1);
     if (roffs) roffs->assign(n, -1);
-    const int64_t per = mx ? gx_split(hp, n, ts) : 0;
+    const int64_t span = mx ? gx_span(hp, n, ts) : 0;
     for (int32_t k = 0; k < n; ++k) {
         const int32_t r = ga_rank(hp, ts[k]);
         if (!r) continue;
         if (offs) (*offs)[k] = off;
         off += 2 * align256(ga_rows(hp, ts[k]) * (mx ? gx_pitch(r) : r) * 2);
-        if (per) off += align256(gx_parts(ga_basis(hp, ts[k]), per) * ga_rows(hp, ts[k]) * gx_pitch(r) * 4);
+        if (mx && gx_item_parts(hp, ts[k], span) < gx_parts(hp, ts[k]))
+            off += align256(gx_parts(hp, ts[k]) * ga_rows(hp, ts[k]) * gx_pitch(r) * 4);
     }
     for (int32_t k = 0; k < n; ++k) {
         const int32_t r = ga_rank(hp, ts[k]);
@@ -1962,8 +2020,8 @@ void gx_lists(std::vector<GxDesc>& gd, std::vector<int2>* lists) {
             list = kGxProj + d.form;
         }
         const int64_t rows = gx_rows(d);
-        for (int64_t y = 0; y < ceil_div(d.D, rows) * d.ks; ++y) lists[list].push_back(make_int2(static_cast<int>(i), static_cast<int>(y)));
-        if (d.ks > 1)
+        for (int64_t y = 0; y < ceil_div(d.D, rows) * d.kitems; ++y) lists[list].push_back(make_int2(static_cast<int>(i), static_cast<int>(y)));
+        if (d.kitems > 1)
             for (int64_t y = 0; y < ceil_div(static_cast<int64_t>(d.D) * (d.rp / 8), kGxJoinChunks); ++y)
                 lists[kGxJoin].push_back(make_int2(static_cast<int>(i), static_cast<int>(y)));
     }
@@ -2000,8 +2058,8 @@ void gx_lists(std::vector<GxDesc>& gd, std::vector<int2>* lists) {
     }
 }
 
-// The descriptor of a projected tensor without its workspace; per as gx_split gives it.
-GxDesc ga_desc(const meo_galore_hparams* hp, const meo_tensor& t, const GaState& s, bool mx, int64_t per) {
+// The descriptor of a projected tensor without its workspace; span as gx_span gives it.
+GxDesc ga_desc(const meo_galore_hparams* hp, const meo_tensor& t, const GaState& s, bool mx, int64_t span) {
     GxDesc d;
     std::memset(static_cast<void*>(&d), 0, sizeof d);
     d.m = static_cast<int32_t>(t.rows);
@@ -2025,8 +2083,10 @@ GxDesc ga_desc(const meo_galore_hparams* hp, const meo_tensor& t, const GaState&
         d.gs = g4 ? static_cast<const uint8_t*>(s.gs) : nullptr;
         d.nb = static_cast<int32_t>(ceil_div(d.d, kMxBlock));
         d.vec = aligned16(d.g) && d.n % 8 == 0;  // 16-byte rows of a bf16 gradient
-        d.ks = g4 ? 1 : static_cast<int32_t>(gx_parts(d.d, per));
-        d.kper = d.ks > 1 ? static_cast<int32_t>(per) : (d.d + kGxStep - 1) / kGxStep;
+        d.ks = g4 ? 1 : static_cast<int32_t>(gx_parts(hp, t));
+        d.kper = d.ks > 1 ? static_cast<int32_t>(gx_per(hp, t)) : (d.d + kGxStep - 1) / kGxStep;
+        d.kitem = g4 ? 1 : static_cast<int32_t>(gx_item_parts(hp, t, span));
+        d.kitems = (d.ks + d.kitem - 1) / d.kitem;
     }
     d.rvec = aligned16(d.em) && aligned16(d.ev) && d.r % 8 == 0;
     d.wvec = aligned16(d.x) && d.n % 8 == 0;
@@ -2057,7 +2117,7 @@ GaPlanRef get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_ten
     if (*rc) return nullptr;
     std::vector<int64_t> woff, roff;
     ga_layout(hp, n, ts, mx, &woff, &roff);
-    const int64_t per = mx ? gx_split(hp, n, ts) : 0;
+    const int64_t span = mx ? gx_span(hp, n, ts) : 0;
     std::vector<RDesc> rd;
     std::vector<GxDesc> right, left;  // the MX4 fields stay zero for bf16 projectors
     std::vector<MxMat> quant;
@@ -2071,7 +2131,7 @@ GaPlanRef get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_ten
         if (numel == 0) continue;
         const GaState& s = st[k];
         if (ga_projected(t)) {
-            GxDesc d = ga_desc(hp, t, s, mx, per);
+            GxDesc d = ga_desc(hp, t, s, mx, span);
             const bool g4 = t.grad_dtype == MEO_MX4, is_left = ga_left(hp, t);
             uint8_t* wb = static_cast<uint8_t*>(ws) + woff[k];
             const int64_t plane = align256(static_cast<int64_t>(d.D) * (mx ? d.rp : d.r) * 2);
@@ -2574,10 +2634,10 @@ int meo_galore_mx4_forms(const meo_galore_hparams* hp, int32_t n, const meo_tens
     if (rc || n == 0) return rc;
     if (!forms) return fail(MEO_ENULL, "forms is NULL");
     const std::vector<GaState> states = ga_states(n, st);
-    const int64_t per = gx_split(hp, n, ts);
+    const int64_t span = gx_span(hp, n, ts);
     std::vector<GxDesc> gd;
     for (int32_t k = 0; k < n; ++k)
-        if (ga_projected(ts[k])) gd.push_back(ga_desc(hp, ts[k], states[k], true, per));
+        if (ga_projected(ts[k])) gd.push_back(ga_desc(hp, ts[k], states[k], true, span));
     std::vector<int2> lists[kGaListCount];
     gx_lists(gd, lists);
     size_t i = 0;
@@ -2588,7 +2648,7 @@ int meo_galore_mx4_forms(const meo_galore_hparams* hp, int32_t n, const meo_tens
         forms[k].rows = static_cast<int32_t>(gx_rows(d));
         forms[k].aligned = d.gs || d.form == kGxDirect;
         forms[k].parts = d.ks;
-        forms[k].split = d.ks > 1;
+        forms[k].item_parts = d.kitem;
         forms[k].back_tiles = d.tpi;
     }
     return MEO_OK;

@@ -52,8 +52,9 @@ struct GxDesc : GDesc {
     int32_t rp;         // r rounded up to 32: two of the back-projection's sub-steps
     int32_t form;       // projection: GxForm; of an MX4 gradient MxForm
     int32_t tpi;        // back-projection: 64-row tiles of N per item
-    float* part;        // split contraction (ks > 1): R's parts, [ks][D][rp]
-    int32_t ks, kper;   // parts, and steps of kGxStep in each but the last
+    float* part;        // kitems > 1: the sums of R's parts, [ks][D][rp]
+    int32_t ks, kper;   // parts of the contraction, and steps of kGxStep in each but the last
+    int32_t kitem, kitems;  // parts per item, items per tile
 };
 
 struct GxTable {
@@ -95,8 +96,9 @@ void launch_galore_adamw(const Table& t, int64_t n, const GaArgs& a, hipStream_t
 enum GxForm { kGxAny = 0, kGxDirect, kGxForms };
 constexpr int kGxFormRows[kGxForms] = {64, 64};
 constexpr int kGxStep = 128;  // contraction step
-// Items of a tensor with ks parts: y = tile * ks + part; its R is summed by launch_gx_join (items
-// of kGxJoinChunks times 8 columns of a row), whose epilogue is then the projection's.
+// Items of a tensor: y = tile * kitems + item, of kitem of its ks parts each. Where there are several
+// to a tile, R is summed by launch_gx_join (items of kGxJoinChunks times 8 columns of a row), whose
+// epilogue is then the projection's.
 constexpr int kGxJoinChunks = 256;
 void launch_gx_project(const GxTable& t, int64_t n, int nright, const GaArgs& a, int form, hipStream_t s);
 void launch_gx_join(const GxTable& t, int64_t n, const GaArgs& a, hipStream_t s);

@@ -158,7 +158,12 @@ __device__ __forceinline__ u32x4 row_part(const u32x4& v, int from, int valid) {
     return u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
 }
 
-template <bool Left, bool Any>
+// The contraction's parts (GxDesc::ks) from `part` on, kitem of them. kWhole: it has one. kFold: all
+// of them are here, and their sums are added up as k_gx_join does. kStore: each one's sum is stored
+// for k_gx_join. (A form each: moments and sums of parts are in registers at once in kFold's alone.
+// In kStore an item's sums are not added up first: Any then spills.)
+enum GxParts { kWhole, kFold, kStore };
+template <bool Left, bool Any, GxParts Parts>
 __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, int part, const GaArgs& a, uint8_t* lds) {
     constexpr int kA = kGdG / 1024 / 4, kB = kGdCodes / 1024 / 4;  // 1 KB transfers per wave of its kind
     static_assert(kGdWaves == 8 && kGdDepth * kGdG >= kGdWaves * kGxEx * 4, "waves below; exchange space");
@@ -171,6 +176,7 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, int part, c
     for (int ib = 0; ib < 2; ++ib)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[ib][v] = 0.0f;
+    f32x16 sum[2] = {acc[0], acc[1]};  // kFold
 
     // G. Right: transfer j holds rows 4 j + (l >> 4) of the tile, 16-byte chunk
     // (l & 15) ^ (row & 15). Left: rows 8 j + (l >> 3) of 128 bytes (64 columns of G), chunk
@@ -191,7 +197,7 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, int part, c
     }
     const int64_t gstep = static_cast<int64_t>(kGdStep) * 2 * (Left ? d.D : 1);
     const int steps = (d.d + kGdStep - 1) / kGdStep;
-    const int k0 = part * d.kper, k1 = min(k0 + d.kper, steps);  // k0 a multiple of 4
+    const int k0 = part * d.kper, k1 = min(k0 + d.kitem * d.kper, steps);  // k0 a multiple of 4
     auto stage = [&](int k, uint8_t* s) {
         const uint8_t* gk = g + min(k, steps - 1) * gstep;  // past the end: the last again, for equal counts
 #pragma unroll
@@ -326,10 +332,12 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, int part, c
     // steps in the even step before it and the scales of four steps two steps before them:
     // before an even step it waits for all, before an odd one for nothing that step k - 1
     // issued. What a step fills was last read before its barrier.
-    // The moments of the wave's piece of R are loaded before everything else.
+    // The moments of the wave's piece of R are loaded before everything else (Any with kFold: after
+    // the products, for want of registers).
     const bool active = cw < d.r;
+    constexpr bool kEarly = Parts == kWhole || (!Any && Parts == kFold);
     GxMoments<true> mv;
-    if (active && d.ks == 1) mv.load(d, i0, cw, lane);
+    if (kEarly && active) mv.load(d, i0, cw, lane);
     auto next_u = [&](int k) {  // waves 4 .. 7, even steps
         if constexpr (Any) {  // loaded two steps before they are stored
             if (k & 2) store_scales((k >> 2) + 1);
@@ -349,20 +357,52 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, int part, c
     // has one of either kind): 74 us for the four 4096 x 4096 matrices, 78 without. (Any:
     // 97 and 90 us for 1951 x 3810 and 3750 x 4266, so there every wave multiplies at once.)
     int cur = 0;
+    auto store_part = [&]() {
+        int ln = lane;
+        __asm__ volatile("" : "+v"(ln));  // addresses are computed here: before the loop they cost 1 us
+        float* const p = d.part + (part * static_cast<int64_t>(d.D) + i0) * d.rp + cw;
+        const int rows = static_cast<int>(min<int64_t>(d.D - i0, kGdRows));
+#pragma unroll
+        for (int ib = 0; ib < 2; ++ib)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int r = ib * 32 + acc_row(v, ln);
+                if (r < rows) *gst<float>(p + r * d.rp + acc_col(ln)) = acc[ib][v];
+            }
+        ++part;
+    };
+    int part_end = k0 + d.kper;
+    auto end_part = [&](int done) {  // the steps before `done` are in acc; the last part's end is below
+        if (Parts == kWhole || done != part_end || done == k1) return;
+        part_end += d.kper;
+        if (Parts == kStore) store_part();
+#pragma unroll
+        for (int ib = 0; ib < 2; ++ib)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                if (Parts == kFold) sum[ib][v] += acc[ib][v];
+                acc[ib][v] = 0.0f;
+            }
+    };
     auto first_half = [&](int k) {  // waves 0 .. 3
         if (active) {
             read(k, cur);
             multiply();
+            end_part(k + 1);
         }
         cur = cur == kGdDepth - 1 ? 0 : cur + 1;
     };
     auto second_half = [&](int k) {  // waves 4 .. 7
         if (active) {
             if (!Any && k > k0) multiply();
+            if (!Any) end_part(k);
 #pragma unroll
             for (int ib = 0; ib < 2; ++ib) __asm__ volatile("" : "+v"(acc[ib]));  // before the reads
             read(k, cur);
-            if (Any) multiply();
+            if (Any) {
+                multiply();
+                end_part(k + 1);
+            }
         }
         cur = cur == kGdDepth - 1 ? 0 : cur + 1;
     };
@@ -417,16 +457,16 @@ __device__ __forceinline__ void gx_tile(const GxDesc& d, int64_t i0, int part, c
     if (!Any && !fetch_g && active) multiply();
     wait_and_sync<0>();
     if (!active) return;
-    if (d.ks > 1) {
+    if constexpr (Parts == kFold) {
 #pragma unroll
         for (int ib = 0; ib < 2; ++ib)
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const int64_t row = i0 + ib * 32 + acc_row(v, lane);
-                if (row < d.D) *gst<float>(d.part + (part * static_cast<int64_t>(d.D) + row) * d.rp + cw + acc_col(lane)) = acc[ib][v];
-            }
+            for (int v = 0; v < 16; ++v) acc[ib][v] = sum[ib][v] + acc[ib][v];
+    } else if constexpr (Parts == kStore) {
+        store_part();
         return;
     }
+    if (!kEarly) mv.load(d, i0, cw, lane);
     float* lw = reinterpret_cast<float*>(lds) + wave * kGxEx;
     gx_epilogue(d, a, acc[0], acc[1], mv, i0, cw, lw, lane);
 }
@@ -436,10 +476,16 @@ __global__ __launch_bounds__(kGdWaves * 64) void k_gx_project(GxTable t, GaArgs 
     __shared__ __attribute__((aligned(128))) uint8_t lds[kGdLds];
     const int2 it = t.items[blockIdx.x];
     const GxDesc d = t.desc[it.x];
-    const int64_t i0 = static_cast<int64_t>(it.y / d.ks) * kGdRows;
-    const int part = it.y % d.ks;
-    if (it.x < nright) gx_tile<false, Any>(d, i0, part, a, lds);
-    else gx_tile<true, Any>(d, i0, part, a, lds);
+    const int64_t i0 = static_cast<int64_t>(it.y / d.kitems) * kGdRows;
+    const int part = it.y % d.kitems * d.kitem;
+    auto tile = [&](auto parts) {
+        constexpr GxParts kParts = decltype(parts)::value;
+        if (it.x < nright) gx_tile<false, Any, kParts>(d, i0, part, a, lds);
+        else gx_tile<true, Any, kParts>(d, i0, part, a, lds);
+    };
+    if (d.ks == 1) tile(std::integral_constant<GxParts, kWhole>{});
+    else if (d.kitems == 1) tile(std::integral_constant<GxParts, kFold>{});
+    else tile(std::integral_constant<GxParts, kStore>{});
 }
 
 void launch_gx_project(const GxTable& t, int64_t n, int nright, const GaArgs& a, int form, hipStream_t s) {
@@ -449,7 +495,7 @@ void launch_gx_project(const GxTable& t, int64_t n, int nright, const GaArgs& a,
     else hipLaunchKernelGGL(k_gx_project<false>, grid, block, 0, s, t, a, nright);
 }
 
-// R of a split contraction: its parts summed in order, then AdamW; a thread has 8 columns of a row.
+// R of a split contraction: its parts' sums added up in order, then AdamW; a thread has 8 columns of a row.
 __global__ __launch_bounds__(kGxJoinChunks) void k_gx_join(GxTable t, GaArgs a) {
     const int2 it = t.items[blockIdx.x];
     const GxDesc d = t.desc[it.x];

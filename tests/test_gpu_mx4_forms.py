@@ -68,7 +68,7 @@ def test_projection_of_an_mx4_gradient_in_128_row_tiles(shape, rank):
 def test_projection_of_a_long_contraction_in_one_piece(shape, aligned):
     """16 steps of 128 and more."""
     f = forms([shape], 64)[0]
-    assert (f.aligned, f.split, f.rows) == (aligned, 0, 64)
+    assert (f.aligned, f.parts, f.rows) == (aligned, 1, 64)
     run_step([shape], 64)
 
 

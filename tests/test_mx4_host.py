@@ -284,7 +284,7 @@ def _forms(shapes, rank, grad="bf16", proj_type="std"):
 
 def test_forms_of_a_step():
     f = _forms([(4096, 4096)], 64)[0]
-    assert (f.rows, f.aligned, f.parts, f.split) == (64, 1, 4, 1) and f.back_tiles >= 1
+    assert (f.rows, f.aligned, f.parts, f.item_parts) == (64, 1, 4, 1) and f.back_tiles >= 1
     f = _forms([(4096, 4097), (777,)], 64)
     assert (f[0].rows, f[0].aligned) == (64, 0) and not any(getattr(f[1], k) for k, _ in f[1]._fields_)
     assert _forms([(11008, 4096), (4096, 11008)], 256, grad="mx4")[0].rows == 128
@@ -301,3 +301,17 @@ def test_forms_of_a_step():
 def test_rows_of_a_product():
     assert [_lib.meo_mx4_matmul_rows(*s) for s in ((0, 5), (5, 0), (1, 1), (40000, 128), (32000, 256), (16384, 256))] == \
         [0, 0, 64, 64, 128, 64]
+
+
+def test_parts_of_a_contraction_follow_from_the_tensor_alone():
+    """Whatever else is in the list; how many of them a block takes may not."""
+    tensors = [(4096, 4096), (1700, 1680), (1951, 3810), (3750, 4266), (300, 72), (70, 9000)]
+    for proj_type in ("std", "reverse_std"):
+        alone = [_forms([s], 64, proj_type=proj_type)[0] for s in tensors]
+        for rest in ([(64, 64)], [(32400, 8)], [(4096, 4096)] * 3, tensors):
+            for i, s in enumerate(tensors):
+                f = _forms([s] + rest, 64, proj_type=proj_type)[0]
+                assert f.parts == alone[i].parts
+    assert [f.parts for f in (_forms([s], 64)[0] for s in tensors)] == [4, 4, 4, 3, 1, 1]
+    assert [f.item_parts for f in (_forms([s], 64)[0] for s in tensors)] == [1] * 6
+    assert [_forms([s] * 4, 64)[0].item_parts for s in tensors] == [4, 4, 4, 3, 1, 1]
