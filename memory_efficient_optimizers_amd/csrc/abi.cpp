@@ -1820,9 +1820,11 @@ int64_t gx_item_parts(const meo_galore_hparams* hp, const meo_tensor& t, int64_t
 
 // Workspace, per projected tensor, every array at a 256-byte boundary (offsets in
 // bytes): the step's two bf16 planes of N, [D][r] each (mx: MX4 projectors: rows of rp
-// values, and then the parts of a split projection, fp32 [ks][D][rp]); then, for the projector
-// refresh, two fp32 [r][d] iterates, one fp32 [r][D] product, four fp64 [r][r]
-// matrices and (mx) the refreshed projector in bf16, [d][r] and [r][d].
+// values, and then the sums of a projection's parts where they are stored, fp32 [ks][D][rp]);
+// then, for the projector refresh, two fp32 [r][d] iterates, one fp32 [r][D] product and four
+// fp64 [r][r] matrices. mx: the refresh's arrays lie where the step's do, since a due step has
+// quantized its projectors before it projects, and their bf16 form, [d][r] and [r][d], lies on
+// the two iterates, which are not in use before the first product and after the last.
 int64_t ga_layout(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts, bool mx, std::vector<int64_t>* offs,
                   std::vector<int64_t>* roffs = nullptr) {
     int64_t off = 0;
@@ -1837,6 +1839,8 @@ int64_t ga_layout(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts,
         if (mx && gx_item_parts(hp, ts[k], span) < gx_parts(hp, ts[k]))
             off += align256(gx_parts(hp, ts[k]) * ga_rows(hp, ts[k]) * gx_pitch(r) * 4);
     }
+    const int64_t step = off;
+    if (mx) off = 0;
     for (int32_t k = 0; k < n; ++k) {
         const int32_t r = ga_rank(hp, ts[k]);
         if (!r) continue;
@@ -1844,9 +1848,9 @@ int64_t ga_layout(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts,
         const int64_t d = ga_basis(hp, ts[k]), D = ga_rows(hp, ts[k]);
         // the product buffer [r][D] later holds the basis [r][d] too
         off += 2 * align256(static_cast<int64_t>(r) * d * 4) + align256(static_cast<int64_t>(r) * std::max(D, d) * 4) +
-               4 * align256(static_cast<int64_t>(r) * r * 8) + (mx ? 2 * align256(d * r * 2) : 0);
+               4 * align256(static_cast<int64_t>(r) * r * 8);
     }
-    return off;
+    return std::max(off, step);
 }
 
 int check_galore_hp(const meo_galore_hparams* hp) {
@@ -2161,8 +2165,8 @@ GaPlanRef get_galore_plan(const meo_galore_hparams* hp, int32_t n, const meo_ten
             q.s2 = reinterpret_cast<double*>(rb + 2 * sq + sy + 2 * ss);
             q.w2 = reinterpret_cast<double*>(rb + 2 * sq + sy + 3 * ss);
             if (mx) {
-                q.u = reinterpret_cast<uint16_t*>(rb + 2 * sq + sy + 4 * ss);
-                q.ut = reinterpret_cast<uint16_t*>(rb + 2 * sq + sy + 4 * ss + align256(static_cast<int64_t>(q.d) * q.r * 2));
+                q.u = reinterpret_cast<uint16_t*>(q.qa);   // written from yt by the last kernel
+                q.ut = reinterpret_cast<uint16_t*>(q.qb);  // and read by the first, which writes qa
                 MxMat w;
                 std::memset(&w, 0, sizeof w);
                 w.data = q.ut;

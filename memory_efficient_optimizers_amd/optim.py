@@ -342,7 +342,8 @@ class GaLoreAdamW(_MeoOptimizer):
     ``projector_dtype=torch.float4_e2m1fn_x2`` keeps the projector in MX4 instead
     (``mx4.py``: 4-bit codes, one scale per 32 values), once, as its transpose:
     ``projector`` (codes) and ``projector_scale``, about an eighth of the two bfloat16
-    copies. ``compress_grad`` then also lets a projected gradient wait for the step in
+    copies (with the workspace, 4.2 instead of 6.7 GB over a Llama-7B list at rank 256).
+    ``compress_grad`` then also lets a projected gradient wait for the step in
     MX4. ``load_state_dict`` converts a projector saved in the other form."""
 
     _kind = "galore"

@@ -315,3 +315,42 @@ def test_parts_of_a_contraction_follow_from_the_tensor_alone():
     assert [f.parts for f in (_forms([s], 64)[0] for s in tensors)] == [4, 4, 4, 3, 1, 1]
     assert [f.item_parts for f in (_forms([s], 64)[0] for s in tensors)] == [1] * 6
     assert [_forms([s] * 4, 64)[0].item_parts for s in tensors] == [4, 4, 4, 3, 1, 1]
+
+
+# ------------------------------------------------------------------------------ memory
+
+def _memory(shapes, rank, proj_type="std"):
+    """Bytes of projectors and workspace, bf16 and MX4."""
+    hp = _lib.galore_hparams(rank=rank, proj_type=proj_type)
+    ps = [torch.empty(s, device="meta") for s in shapes]
+    tensors = _lib._tensors(ps, ps)
+    for t in tensors:
+        t.param = t.grad = P
+    out = []
+    for shapes_of, size, ws in ((_lib.galore_state_shapes, 2, _lib.load().meo_galore_workspace_size),
+                                (_lib.galore_mx4_state_shapes, 1, _lib.load().meo_galore_mx4_workspace_size)):
+        state = sum(size * math.prod(v) for s in shapes for k, v in shapes_of(s, rank, proj_type).items() if k.startswith("proj"))
+        out.append((state, ws(hp, len(ps), tensors)))
+    return out
+
+
+LLAMA_LAYER = [(4096, 4096)] * 4 + [(11008, 4096)] * 2 + [(4096, 11008)]
+
+
+@pytest.mark.parametrize("shapes,rank,proj_type", [
+    (LLAMA_LAYER * 32 + [(32000, 4096)] * 2, 256, "std"), (LLAMA_LAYER, 256, "std"), (LLAMA_LAYER, 64, "std"),
+    (LLAMA_LAYER, 100, "reverse_std"), ([(4096, 4096)], 256, "std"), ([(1024, 4096)], 128, "std"),
+    ([(1024, 1024)] * 96, 32, "std"), ([(256, 512), (200, 96)], 64, "std"), ([(64, 160), (160, 48)], 16, "std")])
+def test_mx4_projectors_take_less_memory(shapes, rank, proj_type):
+    """With the workspace that the optimizer keeps: the refresh's scratch and the step's."""
+    (state, ws), (state4, ws4) = _memory(shapes, rank, proj_type)
+    assert state4 + ws4 < state + ws and state4 < state / 3
+    if sum(s[0] * s[1] for s in shapes) > 10 ** 8:
+        assert ws4 < ws and state4 < state / 7
+
+
+@pytest.mark.parametrize("shape,rank", [((4096, 4096), 64), ((8192, 1700), 64), ((2048, 2048), 32), ((2048, 2048), 250)])
+def test_memory_of_one_tensor_in_parts(shape, rank):
+    """Stepped alone, a tensor's projection stores the sums of its parts: at most a fifth more then."""
+    (state, ws), (state4, ws4) = _memory([shape], rank)
+    assert state4 + ws4 < 1.2 * (state + ws)
