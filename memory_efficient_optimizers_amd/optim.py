@@ -110,6 +110,9 @@ class _MeoOptimizer(torch.optim.Optimizer):
         """The gradient the step takes for ``p`` (None: the parameter is skipped)."""
         return p.grad
 
+    def _taken(self, p: torch.Tensor) -> None:
+        """After the library has taken ``p``'s step."""
+
     def _state_for(self, p: torch.Tensor, group) -> Dict[str, torch.Tensor]:
         raise NotImplementedError
 
@@ -126,7 +129,8 @@ class _MeoOptimizer(torch.optim.Optimizer):
             with torch.enable_grad():
                 loss = closure()
         for group in self.param_groups:
-            buckets: Dict[Tuple[torch.device, int], List[torch.Tensor]] = defaultdict(list)
+            buckets: Dict[Tuple[torch.device, int], List[tuple]] = defaultdict(list)
+            steps: Dict[torch.Tensor, int] = {}  # of parameters seen (one listed twice takes two)
             for p in group["params"]:
                 g = self._grad(p)
                 if g is None:
@@ -135,17 +139,21 @@ class _MeoOptimizer(torch.optim.Optimizer):
                     raise RuntimeError(f"{type(self).__name__} does not support sparse gradients")
                 st = self.state[p]
                 if len(st) == 0:
+                    new = self._state_for(p, group)
                     st["step"] = 0
-                    st.update(self._state_for(p, group))
-                st["step"] += 1
-                buckets[(p.device, st["step"])].append(p)
-            for (device, step), ps in buckets.items():
-                grads = [self._grad(p) for p in ps]
-                grads = [g.contiguous() if isinstance(g, torch.Tensor) else g for g in grads]
+                    st.update(new)
+                steps[p] = steps.get(p, st["step"]) + 1
+                buckets[(p.device, steps[p])].append((p, g))
+            for (device, step), items in buckets.items():
+                ps = [p for p, _ in items]
+                grads = [g.contiguous() if isinstance(g, torch.Tensor) else g for _, g in items]
                 states = [self.state[p] for p in ps]
                 ws = self._ws(self._wsize(ps, grads), device)
                 with torch.cuda.device(device):
                     self._call(group, step, ps, grads, states, ws)
+                    for p, st in zip(ps, states):  # a refused call counts for none
+                        st["step"] = step
+                        self._taken(p)
                     if self._check_finite:
                         # read before the next call reuses the workspace (one
                         # synchronisation per call)
@@ -387,6 +395,9 @@ class GaLoreAdamW(_MeoOptimizer):
                                "zero_grad) before the next backward pass, or compress only the last one")
         return p.grad if q is None else q
 
+    def _taken(self, p):
+        self._compressed.pop(p, None)
+
     def compress_grad(self, p: torch.Tensor) -> None:
         """Turns ``p.grad`` into MX4 (17/32 byte per value) until the next ``step()``, which
         projects it from there, and sets ``p.grad`` to None. Made for
@@ -420,7 +431,8 @@ class GaLoreAdamW(_MeoOptimizer):
         self._compressed.clear()
 
     def step(self, closure=None):
-        """As torch's; gradients that ``compress_grad`` took are used once."""
+        """As torch's; a gradient that ``compress_grad`` took is used once: by the step that the
+        library takes, not by one it refuses."""
         loss = None
         if closure is not None:
             with torch.enable_grad():
@@ -428,7 +440,6 @@ class GaLoreAdamW(_MeoOptimizer):
         for p in self._compressed:
             self._grad(p)  # refused before any parameter's step is counted
         super().step()
-        self._compressed.clear()
         return loss
 
     def load_state_dict(self, state_dict) -> None:
