@@ -407,7 +407,10 @@ class GaLoreAdamW(_MeoOptimizer):
         is. Each parameter's gradient can be compressed once per step, so gradients that
         accumulate over several backward passes are compressed after the last. What reads
         ``p.grad`` between the backward pass and the step (gradient clipping, a loss scaler)
-        does not see a compressed one, and ``state_dict`` does not hold it."""
+        does not see a compressed one, and ``state_dict`` does not hold it. Only this
+        optimizer's ``zero_grad`` discards it: after ``model.zero_grad()`` or ``p.grad = None``,
+        to skip a batch for example, it would still be the next step's, and the hook refuses
+        the next backward pass."""
         if not self._mx4:
             raise RuntimeError("compress_grad needs projector_dtype=torch.float4_e2m1fn_x2")
         group = next((g for g in self.param_groups if any(p is q for q in g["params"])), None)

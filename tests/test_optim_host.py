@@ -98,3 +98,25 @@ def test_compressed_gradients_are_used_by_the_step_that_is_taken(host, monkeypat
     assert [(s, ps, gs) for s, ps, gs in calls[2:]] == [(2, [a], [made[0]]), (2, [b], [made[1]])]
     opt.step()
     assert len(calls) == 4
+
+
+def test_only_the_optimizer_discards_compressed_gradients(host, monkeypatch):
+    calls, _ = host
+    monkeypatch.setattr(optim, "mx4_quantize", lambda x, transposed=False: MX4Tensor.empty(*x.shape, "cpu"))
+    m = torch.nn.Linear(8, 8, bias=False)
+    opt = GaLoreAdamW([dict(params=[m.weight], rank=4)], projector_dtype=MX4)
+    m.weight.register_post_accumulate_grad_hook(opt.compress_grad)
+    backward = lambda: m(torch.ones(2, 8)).sum().backward()  # noqa: E731
+    backward()
+    opt.step()  # refreshes: took the whole gradient
+    m.zero_grad()
+    backward()
+    m.zero_grad()
+    with pytest.raises(RuntimeError, match="already compressed"):
+        backward()
+    opt.zero_grad()
+    opt.step()
+    assert len(calls) == 1  # discarded: nothing to step
+    backward()
+    opt.step()
+    assert opt.state[m.weight]["step"] == 2 and isinstance(calls[1][2][0], MX4Tensor)
