@@ -304,8 +304,11 @@ def _tensors(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], stat
 
 
 def _stream(stream) -> int:
-    if stream is None:  # torch.cuda.current_stream().cuda_stream without the Stream object (2.6 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:  # not part of torch's public interface
+            return torch.cuda.current_stream().cuda_stream
+        return raw(torch.cuda.current_device())  # without the Stream object (2.6 us a call)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)

@@ -358,7 +358,8 @@ class GaLoreAdamW(_MeoOptimizer):
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0,
                  projector_dtype=torch.bfloat16):
-        if projector_dtype not in (torch.bfloat16, torch.float4_e2m1fn_x2):
+        mx4 = getattr(torch, "float4_e2m1fn_x2", None)  # (a torch without the type has bfloat16 projectors)
+        if projector_dtype is None or projector_dtype not in (torch.bfloat16, mx4):
             raise TypeError("projector_dtype must be torch.bfloat16 or torch.float4_e2m1fn_x2")
         if not lr >= 0.0:
             raise ValueError(f"Invalid learning rate: {lr}")
@@ -369,7 +370,7 @@ class GaLoreAdamW(_MeoOptimizer):
                 raise ValueError(f"Invalid beta parameter at index {i}: {b}")
         defaults = dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay)
         super().__init__(params, defaults, None)
-        self._mx4 = projector_dtype == torch.float4_e2m1fn_x2
+        self._mx4 = projector_dtype == mx4
         self._compressed: Dict[torch.Tensor, MX4Tensor] = {}
         for g in self.param_groups:
             if "rank" in g:

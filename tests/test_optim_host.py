@@ -5,8 +5,7 @@ import contextlib
 import pytest
 import torch
 
-from memory_efficient_optimizers_amd import CAME, Adafactor, GaLoreAdamW, Lamb, MX4Tensor
-from memory_efficient_optimizers_amd import optim
+from memory_efficient_optimizers_amd import CAME, Adafactor, GaLoreAdamW, Lamb, MX4Tensor, _lib, optim
 
 MX4 = torch.float4_e2m1fn_x2
 
@@ -120,3 +119,23 @@ def test_only_the_optimizer_discards_compressed_gradients(host, monkeypatch):
     backward()
     opt.step()
     assert opt.state[m.weight]["step"] == 2 and isinstance(calls[1][2][0], MX4Tensor)
+
+
+def test_a_torch_without_the_4_bit_type_keeps_bf16_projectors(monkeypatch):
+    monkeypatch.delattr(torch, "float4_e2m1fn_x2")
+    p = torch.nn.Parameter(torch.zeros(8, 8))
+    GaLoreAdamW([dict(params=[p], rank=4)])
+    for dt in (None, torch.float16):
+        with pytest.raises(TypeError):
+            GaLoreAdamW([dict(params=[p], rank=4)], projector_dtype=dt)
+
+
+def test_the_current_stream_without_torchs_private_call(monkeypatch):
+    class Stream:
+        cuda_stream = 77
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 88 + d, raising=False)
+    assert _lib._stream(None) == 88
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    assert _lib._stream(None) == 77
