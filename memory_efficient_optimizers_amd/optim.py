@@ -372,6 +372,7 @@ class GaLoreAdamW(_MeoOptimizer):
         super().__init__(params, defaults, None)
         self._mx4 = projector_dtype == mx4
         self._compressed: Dict[torch.Tensor, MX4Tensor] = {}
+        self._places: Dict[torch.Tensor, Tuple[int, int]] = {}
         for g in self.param_groups:
             if "rank" in g:
                 g.setdefault("update_proj_gap", 200)
@@ -399,6 +400,17 @@ class GaLoreAdamW(_MeoOptimizer):
     def _taken(self, p):
         self._compressed.pop(p, None)
 
+    def _group_of(self, p: torch.Tensor):
+        """The parameter group that holds ``p``, or None; found again if the groups were changed."""
+        for again in (False, True):
+            if again:
+                self._places = {q: (i, j) for i, g in enumerate(self.param_groups) for j, q in enumerate(g["params"])}
+            i, j = self._places.get(p, (0, -1))
+            if 0 <= j and i < len(self.param_groups) and j < len(self.param_groups[i]["params"]) and \
+                    self.param_groups[i]["params"][j] is p:
+                return self.param_groups[i]
+        return None
+
     def compress_grad(self, p: torch.Tensor) -> None:
         """Turns ``p.grad`` into MX4 (17/32 byte per value) until the next ``step()``, which
         projects it from there, and sets ``p.grad`` to None. Made for
@@ -414,7 +426,7 @@ class GaLoreAdamW(_MeoOptimizer):
         the next backward pass."""
         if not self._mx4:
             raise RuntimeError("compress_grad needs projector_dtype=torch.float4_e2m1fn_x2")
-        group = next((g for g in self.param_groups if any(p is q for q in g["params"])), None)
+        group = self._group_of(p)
         if group is None:
             raise ValueError("compress_grad takes one of the optimizer's parameters")
         if p.grad is None or not self._projected(p, group):

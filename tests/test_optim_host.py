@@ -139,3 +139,35 @@ def test_the_current_stream_without_torchs_private_call(monkeypatch):
     assert _lib._stream(None) == 88
     monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
     assert _lib._stream(None) == 77
+
+
+def test_compress_grad_finds_a_group_without_searching_them_all(host, monkeypatch):
+    """One pass over the parameters serves all of them; changed groups are found again."""
+    class Counted(list):
+        passes = 0
+
+        def __iter__(self):
+            Counted.passes += 1
+            return super().__iter__()
+
+    monkeypatch.setattr(optim, "mx4_quantize", lambda x, transposed=False: MX4Tensor.empty(*x.shape, "cpu"))
+    ps = _params(50)
+    opt = GaLoreAdamW([dict(params=ps[:25], rank=4), dict(params=ps[25:], rank=4)], projector_dtype=MX4)
+    opt.step()
+    for g in opt.param_groups:
+        g["params"] = Counted(g["params"])
+    for p in ps:
+        p.grad = torch.ones(8, 8)
+        opt.compress_grad(p)
+    assert len(opt._compressed) == 50 and Counted.passes <= 2
+    opt.zero_grad()
+    (q,) = _params(1)
+    with pytest.raises(ValueError):
+        opt.compress_grad(q)
+    opt.add_param_group(dict(params=[q], rank=4, update_proj_gap=1, scale=0.25, proj_type="std"))
+    ps[3].grad = torch.ones(8, 8)
+    opt.param_groups[0]["params"].remove(ps[3])
+    opt.param_groups[2]["params"].append(ps[3])
+    opt.compress_grad(q)
+    opt.compress_grad(ps[3])
+    assert q.grad is not None and ps[3].grad is not None  # a gap of 1: every step is due
