@@ -166,7 +166,7 @@ def test_compress_grad_finds_a_group_without_searching_them_all(host, monkeypatc
         opt.compress_grad(q)
     opt.add_param_group(dict(params=[q], rank=4, update_proj_gap=1, scale=0.25, proj_type="std"))
     ps[3].grad = torch.ones(8, 8)
-    opt.param_groups[0]["params"].remove(ps[3])
+    del opt.param_groups[0]["params"][3]
     opt.param_groups[2]["params"].append(ps[3])
     opt.compress_grad(q)
     opt.compress_grad(ps[3])
