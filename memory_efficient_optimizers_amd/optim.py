@@ -440,6 +440,8 @@ class GaLoreAdamW(_MeoOptimizer):
         if (step - 1) % group["update_proj_gap"] == 0:
             return
         self._compressed[p] = mx4_quantize(p.grad, transposed=not self._right(p, group))
+        if p.grad.is_cuda:  # dropped while this stream, perhaps not the one it was made on, reads it
+            p.grad.record_stream(torch.cuda.current_stream(p.grad.device))
         p.grad = None
 
     def zero_grad(self, set_to_none: bool = True) -> None:
