@@ -1748,9 +1748,9 @@ constexpr int64_t kCus = 256;
 constexpr int64_t kGxJoinSteps = 4;
 int64_t gx_per(const meo_galore_hparams* hp, const meo_tensor& t) {
     const int64_t tiles = ceil_div(ga_rows(hp, t), kGxFormRows[kGxAny]), steps = ceil_div(ga_basis(hp, t), kGxStep);
-    for (int64_t per = 4; per + kGxJoinSteps < steps; per += 4)
-        if (tiles * ceil_div(steps, per) <= kCus) return per;
-    return 0;
+    if (2 * tiles > kCus) return 0;
+    const int64_t per = ceil_div(ceil_div(steps, kCus / tiles), 4) * 4;
+    return per + kGxJoinSteps < steps ? per : 0;
 }
 
 int64_t gx_parts(const meo_galore_hparams* hp, const meo_tensor& t) {
@@ -1788,7 +1788,8 @@ int64_t gx_span(const meo_galore_hparams* hp, int32_t n, const meo_tensor* ts) {
     const double step = (aligned ? 0.55 : 1.25) + 0.73 * static_cast<double>(rp) / kGaWide;
     int64_t best = 0;
     double least = 0.0;
-    for (int64_t span = 0; span < longest; span += 4) {
+    const int64_t by = ceil_div(longest, 256) * 4;  // at most 64 spans
+    for (int64_t span = 0; span < longest; span += by) {
         int64_t items = 0, sum = 0, most = 0, bytes = 0;
         auto add = [&](int64_t count, int64_t steps) {
             items += count;
