@@ -21,6 +21,7 @@
 #include "meo.h"
 #include "internal.h"
 #include "galore.h"
+#include "galore_mx4.h"
 #include "mx4.h"
 
 using namespace meo;

@@ -2,13 +2,13 @@
 // staging, the epilogue exchange and AdamW on a piece of the low-rank gradient.
 #pragma once
 #include "galore.h"
-#include "mx4.h"
 
 #include <type_traits>
 
 namespace meo {
 
 typedef __bf16 bfv8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ f32x16 mfma32(const bfv8& a, const bfv8& b, const f32x16& c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -93,23 +93,6 @@ struct TransStage {
         }
     }
 };
-
-// 8 codes times their scale as bf16 (exact: a code has two significant bits).
-__device__ __forceinline__ u32x4 mx4_to_bf16(uint32_t q, float scale) {
-    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 0)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 1)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 2)),
-                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 3))};
-}
-
-// One block of the MX4 projector: row `row` of U^T, block kb; zero outside it.
-__device__ __forceinline__ void ld_mx_block(const GxDesc& d, int64_t row, int64_t kb, u32x4& c, uint32_t& e) {
-    c = u32x4{0u, 0u, 0u, 0u};
-    e = 127;
-    if (row >= d.r || kb >= d.nb) return;
-    c = *gld<u32x4>(d.uc + (row * d.nb + kb) * 16);
-    e = *gld<uint8_t>(d.us + row * d.nb + kb);
-}
 
 // Accumulator element v of a 32x32 block held by `lane`: row and column in the block.
 __device__ __forceinline__ int acc_row(int v, int lane) { return 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3); }

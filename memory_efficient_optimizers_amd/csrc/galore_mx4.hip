@@ -9,11 +9,29 @@
 // products are those of the values that the codes stand for. A gradient in MX4 is
 // multiplied in its own form on the scaled matrix instructions.
 #include "galore_dev.h"
+#include "galore_mx4.h"
 #include "mx4_tile.h"
 
 namespace meo {
 
 namespace {
+
+// 8 codes times their scale as bf16 (exact: a code has two significant bits).
+__device__ __forceinline__ u32x4 mx4_to_bf16(uint32_t q, float scale) {
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 3))};
+}
+
+// One block of the MX4 projector: row `row` of U^T, block kb; zero outside it.
+__device__ __forceinline__ void ld_mx_block(const GxDesc& d, int64_t row, int64_t kb, u32x4& c, uint32_t& e) {
+    c = u32x4{0u, 0u, 0u, 0u};
+    e = 127;
+    if (row >= d.r || kb >= d.nb) return;
+    c = *gld<u32x4>(d.uc + (row * d.nb + kb) * 16);
+    e = *gld<uint8_t>(d.us + row * d.nb + kb);
+}
 
 // AdamW on 8 columns of a row of R: the moments (m, v: as loaded, the `valid` first columns
 // in range) are stored back, N goes to its two planes up to column rp, zero past r. (bf16

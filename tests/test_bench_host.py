@@ -2,6 +2,9 @@
 roofline lines divide by, the latter against closed forms written from the Llama-7B
 architecture (vocabulary 32000, hidden 4096, MLP 11008, 32 layers), not from
 bench.py's own accounting."""
+import glob
+import hashlib
+import json
 import os
 import subprocess
 import sys
@@ -76,3 +79,15 @@ def test_galore_bytes():
         assert b["galore_back"] == 2 * xb * P2 + 4 * r * sum_big + 2 * r * d * 226 == back
         assert b["flops_back"] == 2 * b["flops_project"] == 4 * r * P2
         assert b["galore_adamw"] == (2 + 2 * xb + 16) * P1
+
+
+@pytest.mark.parametrize("path", sorted(glob.glob(os.path.join(ROOT, "profiles", "*_traffic.json"))), ids=os.path.basename)
+def test_traffic_records_belong_to_the_committed_sources(path):
+    """The bench reports a counter record only while the kernels' sources are those it was taken on."""
+    with open(path) as f:
+        rec = json.load(f)
+    h = hashlib.sha256()
+    for src in rec["sources"]:
+        with open(os.path.join(ROOT, src), "rb") as f:
+            h.update(f.read())
+    assert h.hexdigest() == rec["sources_sha256"]
