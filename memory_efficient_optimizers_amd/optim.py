@@ -369,17 +369,20 @@ class GaLoreAdamW(_MeoOptimizer):
             if not 0.0 <= b < 1.0:
                 raise ValueError(f"Invalid beta parameter at index {i}: {b}")
         defaults = dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay)
-        super().__init__(params, defaults, None)
+        super().__init__(params, defaults, None)  # (adds the groups)
         self._mx4 = projector_dtype == mx4
         self._compressed: Dict[torch.Tensor, MX4Tensor] = {}
         self._places: Dict[torch.Tensor, Tuple[int, int]] = {}
-        for g in self.param_groups:
-            if "rank" in g:
-                g.setdefault("update_proj_gap", 200)
-                g.setdefault("scale", 0.25)
-                g.setdefault("proj_type", "std")
-                if g["proj_type"] not in ("std", "reverse_std"):
-                    raise ValueError("proj_type must be 'std' or 'reverse_std'")
+
+    def add_param_group(self, param_group) -> None:
+        """As torch's; a group with a ``rank`` gets the projection's other fields."""
+        if "rank" in param_group:
+            param_group.setdefault("update_proj_gap", 200)
+            param_group.setdefault("scale", 0.25)
+            param_group.setdefault("proj_type", "std")
+            if param_group["proj_type"] not in ("std", "reverse_std"):
+                raise ValueError("proj_type must be 'std' or 'reverse_std'")
+        super().add_param_group(param_group)
 
     @staticmethod
     def _projected(p: torch.Tensor, group) -> bool:

@@ -171,3 +171,19 @@ def test_compress_grad_finds_a_group_without_searching_them_all(host, monkeypatc
     opt.compress_grad(q)
     opt.compress_grad(ps[3])
     assert q.grad is not None and ps[3].grad is not None  # a gap of 1: every step is due
+
+
+def test_a_group_added_later_gets_the_projections_defaults(host, monkeypatch):
+    monkeypatch.setattr(optim, "mx4_quantize", lambda x, transposed=False: MX4Tensor.empty(*x.shape, "cpu"))
+    a, b = _params(2)
+    opt = GaLoreAdamW([dict(params=[a], rank=4)], projector_dtype=MX4)
+    with pytest.raises(ValueError):
+        opt.add_param_group(dict(params=[b], rank=4, proj_type="both"))
+    opt.add_param_group(dict(params=[b], rank=4))
+    fields = {k: v for k, v in opt.param_groups[0].items() if k != "params"}
+    assert {k: v for k, v in opt.param_groups[1].items() if k != "params"} == fields
+    assert (fields["update_proj_gap"], fields["scale"], fields["proj_type"]) == (200, 0.25, "std")
+    opt.step()
+    b.grad = torch.ones(8, 8)
+    opt.compress_grad(b)
+    assert b.grad is None
