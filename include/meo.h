@@ -13,6 +13,8 @@
  *   meo_lamb_step       LAMB: Adam moments with a per-tensor trust ratio.
  *   meo_galore_step     GaLore: AdamW on gradients projected to a low rank;
  *                       meo_galore_mx4_step the same with 4-bit projectors.
+ *   meo_muon_step       Muon: the momentum of each matrix, orthogonalized by
+ *                       Newton-Schulz steps (meo_orthogonalize does that alone).
  *
  * and meo_mx4_* convert and multiply the 4-bit matrices that the last one uses.
  *
@@ -72,7 +74,7 @@
 extern "C" {
 #endif
 
-#define MEO_VERSION 10
+#define MEO_VERSION 11
 
 /* Return codes. */
 #define MEO_OK          0
@@ -633,6 +635,109 @@ int     meo_galore_mx4_forms(const meo_galore_hparams* hp, int32_t n, const meo_
                              const meo_galore_mx4_state* states, meo_galore_mx4_form* forms);
 int32_t meo_mx4_matmul_rows(int64_t m, int64_t n);
 
+/* ---------------------------------------------------------------------- Muon */
+
+/*
+ * Orthogonalization of matrices by Newton-Schulz steps, as the Muon optimizer does with its
+ * momentum. A tensor [batch][rows][cols] is `batch` independent matrices. With U one of them,
+ * or its transpose if rows > cols (so that U has m <= n rows),
+ *     X_0 = U / max(|U|, eps)                     (|U| the Frobenius norm)
+ *     A = X_k X_k^T,  X_{k+1} = a X_k + (b A + c A^2) X_k      for each step's (a, b, c),
+ * and the result is the last X (transposed back). Singular values go through the odd
+ * polynomials a s + b s^3 + c s^5; with the defaults they end between 0.68 and 1.14 unless they
+ * were below about 1e-3 of the norm, and singular vectors stay. A zero matrix gives zeros (with
+ * eps = 0 too); one that holds a NaN or an infinity gives NaN throughout.
+ *
+ * Precision. Products are fp16 with float32 sums; the iterate itself is held in 22 bits and the
+ * diagonals of A and of b A + c A^2 in float32. The result is within about 1e-3 (relative, in
+ * the Frobenius norm) of the exact polynomial's, for matrices of any conditioning; a bfloat16
+ * result is rounded once, to nearest even. Values are held times powers of two; a result whose
+ * entries are below about 2^-24 of those of a matrix with orthonormal rows (eps far above |U|)
+ * loses them.
+ *
+ * Hyperparameters: eps, the steps (1 to MEO_NS_MAX_STEPS) and the coefficients of each. Defaults
+ * (meo_orthogonalize_defaults): eps 1e-7, 5 steps of (3.4445, -4.7750, 2.0315), the values Muon
+ * was published with. MEO_EINVAL for non-finite values, negative eps, steps out of range, and
+ * for coefficients under which a singular value of at most 1 could grow past 8, or
+ * |b s^2 + c s^4| past 100, in any step (the range that the fp16 operands have).
+ */
+#define MEO_NS_MAX_STEPS 16
+typedef struct meo_orthogonalize_hparams {
+    double  eps;
+    int32_t steps;
+    int32_t reserved; /* 0 */
+    double  coefficients[MEO_NS_MAX_STEPS][3];
+} meo_orthogonalize_hparams;
+
+/* One tensor of meo_orthogonalize. Rows of x (of out) are ldx (ldo) elements apart and its
+ * matrices rows * ldx (rows * ldo); elements between rows are neither read nor written. `out`
+ * may be x itself if both are bf16 and ldo = ldx; it must not overlap anything else of the call. */
+typedef struct meo_ns_matrices {
+    const void* x;       /* [batch][rows][ldx], read only               */
+    void*       out;     /* bf16 [batch][rows][ldo]                     */
+    int64_t     batch, rows, cols;
+    int64_t     ldx, ldo;
+    int32_t     dtype;   /* of x: MEO_F32 or MEO_BF16                   */
+    int32_t     reserved; /* 0 */
+} meo_ns_matrices;
+
+/* The result of a matrix does not depend on the rest of its list, bit for bit. The calls
+ * allocate nothing and keep nothing: descriptors travel as kernel arguments, so that a call can
+ * be captured into a graph. The workspace holds part of the list at a time (6 bytes per value
+ * and 4 per value of A, of about 2^26 values or the largest matrix); lists are worked off in
+ * that order. Errors as for the steps; MEO_ESHAPE also for a side past 2^22, a matrix past
+ * 2^35 values (both after rounding up to 64) or a leading dimension below the row length. */
+void   meo_orthogonalize_defaults(meo_orthogonalize_hparams* hp);
+size_t meo_orthogonalize_workspace_size(const meo_orthogonalize_hparams* hp, int32_t n, const meo_ns_matrices* matrices);
+int    meo_orthogonalize_validate(const meo_orthogonalize_hparams* hp, int32_t n, const meo_ns_matrices* matrices);
+int    meo_orthogonalize(const meo_orthogonalize_hparams* hp, int32_t n, const meo_ns_matrices* matrices,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Muon. Per tensor of two or more dims (its matrices independent, as everywhere in this file):
+ *     exp_avg <- momentum exp_avg + (1 - momentum) grad
+ *     U = (1 - momentum) grad + momentum exp_avg with nesterov, else exp_avg
+ *     O = orthogonalized U (above)
+ *     param <- param (1 - lr weight_decay) - lr s O
+ * with s = sqrt(max(1, rows / cols)) (MEO_MUON_ORIGINAL) or 0.2 sqrt(max(rows, cols))
+ * (MEO_MUON_MATCH_RMS_ADAMW: updates of the size that AdamW's have, so that its lr and weight
+ * decay can be kept). Tensors with fewer dims are refused (MEO_ESHAPE): AdamW is for those
+ * (meo_galore_step takes them).
+ *
+ * Storage: param and grad fp32 or bf16; exp_avg in the tensor's state_dtype, fp32, bf16 or 8-bit
+ * as for the other steps (groups of 128 values in row-major order, which may cross rows; with
+ * batch > 1 rows * cols must be a multiple of 128, MEO_ESHAPE otherwise; the scale is max|m|
+ * times the float32 1/127, which may differ from the quotient in its last bit). The step uses the
+ * stored exp_avg. It starts at zero. The arithmetic outside the products is float32.
+ *
+ * Defaults (meo_muon_defaults): lr 1e-3, momentum 0.95, nesterov, weight_decay 0.1,
+ * MEO_MUON_ORIGINAL and meo_orthogonalize_defaults. Errors (MEO_EINVAL): lr < 0, momentum outside
+ * [0, 1), an unknown adjust_lr, non-finite values, and those of the orthogonalization. `step`
+ * must be >= 1 and is not used. Workspace, graph capture and limits as for meo_orthogonalize.
+ */
+#define MEO_MUON_ORIGINAL         0
+#define MEO_MUON_MATCH_RMS_ADAMW  1
+typedef struct meo_muon_hparams {
+    double  lr;
+    double  momentum;
+    double  weight_decay;
+    int32_t nesterov;
+    int32_t adjust_lr;  /* MEO_MUON_ORIGINAL or MEO_MUON_MATCH_RMS_ADAMW */
+    meo_orthogonalize_hparams ns;
+} meo_muon_hparams;
+
+typedef struct meo_muon_state {
+    void*  exp_avg;       /* state_dtype [numel] */
+    float* exp_avg_scale; /* [ceil(numel / 128)]; iff exp_avg is MEO_I8 */
+} meo_muon_state;
+
+void   meo_muon_defaults(meo_muon_hparams* hp);
+size_t meo_muon_workspace_size(const meo_muon_hparams* hp, int32_t n, const meo_tensor* tensors);
+int    meo_muon_validate(const meo_muon_hparams* hp, int64_t step, int32_t n, const meo_tensor* tensors,
+                         const meo_muon_state* states);
+int    meo_muon_step(const meo_muon_hparams* hp, int64_t step, int32_t n, const meo_tensor* tensors,
+                     const meo_muon_state* states, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------- per-tensor scalars */
 
 /*
@@ -691,7 +796,7 @@ int meo_version(void);
  * launches[id] (both arrays of MEO_NUM_PASSES entries, caller-owned host
  * memory, zeroed by the caller), and forgets the events. Returns MEO_OK or
  * MEO_EHIP. Not for use under graph capture. */
-#define MEO_NUM_PASSES 17
+#define MEO_NUM_PASSES 22
 int         meo_profile_enable(int on);
 const char* meo_pass_name(int id);
 int         meo_profile_collect(double* total_ms, int64_t* launches);

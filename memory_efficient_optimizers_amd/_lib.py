@@ -48,9 +48,12 @@ EXPORTS = [
     "meo_mx4_quantize", "meo_mx4_dequantize", "meo_mx4_matmul",
     "meo_galore_mx4_workspace_size", "meo_galore_mx4_validate", "meo_galore_mx4_step", "meo_galore_mx4_refresh",
     "meo_galore_mx4_forms", "meo_mx4_matmul_rows",
+    "meo_orthogonalize_defaults", "meo_orthogonalize_workspace_size", "meo_orthogonalize_validate", "meo_orthogonalize",
+    "meo_muon_defaults", "meo_muon_workspace_size", "meo_muon_validate", "meo_muon_step",
 ]
 MEO_NOALLOC_SCRATCH_BYTES = 64 << 20
-MEO_NUM_PASSES = 17
+MEO_NUM_PASSES = 22
+MEO_NS_MAX_STEPS = 16
 
 
 class MeoError(RuntimeError):
@@ -138,6 +141,29 @@ class meo_galore_mx4_state(ctypes.Structure):
 
 class meo_galore_mx4_form(ctypes.Structure):
     _fields_ = [(k, c_int32) for k in ("rows", "aligned", "parts", "item_parts", "back_tiles")]
+
+
+class meo_orthogonalize_hparams(ctypes.Structure):
+    _fields_ = [("eps", c_double), ("steps", c_int32), ("reserved", c_int32),
+                ("coefficients", (c_double * 3) * MEO_NS_MAX_STEPS)]
+
+
+class meo_ns_matrices(ctypes.Structure):
+    _fields_ = [("x", c_void_p), ("out", c_void_p), ("batch", c_int64), ("rows", c_int64), ("cols", c_int64),
+                ("ldx", c_int64), ("ldo", c_int64), ("dtype", c_int32), ("reserved", c_int32)]
+
+
+MEO_MUON_ORIGINAL, MEO_MUON_MATCH_RMS_ADAMW = 0, 1
+_ADJUST_LR = {"original": MEO_MUON_ORIGINAL, "match_rms_adamw": MEO_MUON_MATCH_RMS_ADAMW}
+
+
+class meo_muon_hparams(ctypes.Structure):
+    _fields_ = [("lr", c_double), ("momentum", c_double), ("weight_decay", c_double), ("nesterov", c_int32),
+                ("adjust_lr", c_int32), ("ns", meo_orthogonalize_hparams)]
+
+
+class meo_muon_state(ctypes.Structure):
+    _fields_ = [("exp_avg", c_void_p), ("exp_avg_scale", c_void_p)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -245,6 +271,17 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         getattr(lib, name).restype = ctypes.c_int
     lib.meo_mx4_matmul.argtypes = [c_int32, MP, c_void_p]
     lib.meo_mx4_matmul.restype = ctypes.c_int
+    OH, OM, UH, US = (ctypes.POINTER(c) for c in (meo_orthogonalize_hparams, meo_ns_matrices, meo_muon_hparams,
+                                                  meo_muon_state))
+    for name, args, res in (("orthogonalize_defaults", [OH], None),
+                            ("orthogonalize_workspace_size", [OH, c_int32, OM], c_size_t),
+                            ("orthogonalize_validate", [OH, c_int32, OM], ctypes.c_int),
+                            ("orthogonalize", [OH, c_int32, OM, c_void_p, c_size_t, c_void_p], ctypes.c_int),
+                            ("muon_defaults", [UH], None), ("muon_workspace_size", [UH, c_int32, T], c_size_t),
+                            ("muon_validate", [UH, c_int64, c_int32, T, US], ctypes.c_int),
+                            ("muon_step", [UH, c_int64, c_int32, T, US, c_void_p, c_size_t, c_void_p], ctypes.c_int)):
+        getattr(lib, f"meo_{name}").argtypes = args
+        getattr(lib, f"meo_{name}").restype = res
     _lib = lib
     return lib
 
@@ -1033,6 +1070,124 @@ def galore_mx4_init_state(param: torch.Tensor, rank: int, proj_type: str = "std"
             for k, s in galore_mx4_state_shapes(param.shape, rank, proj_type).items()}
 
 
+# ----------------------------------------------------------------------------- Muon
+
+MUON_KEYS = ["exp_avg", "exp_avg_scale"]
+NS_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize_hparams(steps: int = 5, coefficients=NS_COEFFICIENTS, eps: float = 1e-7) -> meo_orthogonalize_hparams:
+    """``coefficients``: one (a, b, c) for every step, or a sequence with one for each."""
+    hp = meo_orthogonalize_hparams(float(eps), int(steps), 0)
+    rows = list(coefficients)
+    if len(rows) == 3 and not any(hasattr(v, "__len__") for v in rows):
+        rows = [rows] * MEO_NS_MAX_STEPS
+    elif len(rows) != steps or any(len(r) != 3 for r in rows):
+        raise ValueError("coefficients are one (a, b, c), or one for each step")
+    for k, r in enumerate(rows[:MEO_NS_MAX_STEPS]):
+        hp.coefficients[k][:] = [float(v) for v in r]
+    return hp
+
+
+def muon_hparams(lr=1e-3, momentum=0.95, weight_decay=0.1, nesterov=True, adjust_lr="original", ns_steps=5,
+                 ns_coefficients=NS_COEFFICIENTS, eps=1e-7) -> meo_muon_hparams:
+    if adjust_lr not in _ADJUST_LR:
+        raise ValueError("adjust_lr must be 'original' or 'match_rms_adamw'")
+    return meo_muon_hparams(float(lr), float(momentum), float(weight_decay), int(bool(nesterov)), _ADJUST_LR[adjust_lr],
+                            orthogonalize_hparams(ns_steps, ns_coefficients, eps))
+
+
+def meo_orthogonalize_defaults() -> meo_orthogonalize_hparams:
+    hp = meo_orthogonalize_hparams()
+    load().meo_orthogonalize_defaults(ctypes.byref(hp))
+    return hp
+
+
+def meo_muon_defaults() -> meo_muon_hparams:
+    hp = meo_muon_hparams()
+    load().meo_muon_defaults(ctypes.byref(hp))
+    return hp
+
+
+def _ns_row_stride(t: torch.Tensor, what: str) -> int:
+    """Elements between rows of [..., rows, cols] matrices whose leading dims follow each other
+    without gaps (rows may be strided)."""
+    if t.is_contiguous():
+        return max(t.shape[-1], 1)
+    rows, cols = t.shape[-2:]
+    ld = t.stride(-2) if rows > 1 else cols
+    if rows == 1:  # one row per matrix: the distance between matrices
+        for n, s in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+            if n > 1:
+                ld = s
+                break
+    span, ok = rows * ld, ld >= cols and (cols == 1 or t.stride(-1) == 1)
+    for n, s in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        ok = ok and (n == 1 or s == span)
+        span *= n
+    if t.numel() and not ok:
+        raise ValueError(f"{what} must be row-major matrices (rows may be strided, matrices follow each other)")
+    return max(ld, 1)
+
+
+def _ns_matrices(xs, outs):
+    if len(xs) != len(outs):
+        raise ValueError("xs and outs differ in length")
+    arr = (meo_ns_matrices * max(len(xs), 1))()
+    for i, (x, o) in enumerate(zip(xs, outs)):
+        if x.dim() < 2:
+            raise ValueError("matrices have two or more dims")
+        if x.dtype not in _DTYPE:
+            raise TypeError("matrices must be float32 or bfloat16")
+        if o.dtype != torch.bfloat16:
+            raise TypeError("orthogonalized matrices are bfloat16")
+        if o.shape != x.shape or o.device != x.device:
+            raise ValueError(f"out of shape {tuple(o.shape)} on {o.device}, expected {tuple(x.shape)} on {x.device}")
+        arr[i] = meo_ns_matrices(x.data_ptr(), o.data_ptr(), math.prod(x.shape[:-2]), x.shape[-2], x.shape[-1],
+                                 _ns_row_stride(x, "x"), _ns_row_stride(o, "out"), _DTYPE[x.dtype], 0)
+    return arr
+
+
+def meo_orthogonalize_workspace_size(hp, xs, outs) -> int:
+    return int(load().meo_orthogonalize_workspace_size(ctypes.byref(hp), len(xs), _ns_matrices(xs, outs)))
+
+
+def meo_orthogonalize_validate(hp, xs, outs) -> None:
+    _check(load().meo_orthogonalize_validate(ctypes.byref(hp), len(xs), _ns_matrices(xs, outs)))
+
+
+def meo_orthogonalize(hp, xs, outs, workspace=None, stream=None) -> None:
+    """Each of ``xs`` (leading dims: a batch of matrices), orthogonalized, into the bfloat16
+    tensor of ``outs`` beside it."""
+    ws, nb = _ws(workspace)
+    _check(load().meo_orthogonalize(ctypes.byref(hp), len(xs), _ns_matrices(xs, outs), ws, nb, _stream(stream)))
+
+
+def meo_muon_workspace_size(hp, params, grads, states=None) -> int:
+    return int(load().meo_muon_workspace_size(ctypes.byref(hp), len(params), _tensors(params, grads, states)))
+
+
+def meo_muon_validate(hp, step, params, grads, states) -> None:
+    _check(load().meo_muon_validate(ctypes.byref(hp), step, len(params), _tensors(params, grads, states),
+                                    _muon_states(params, states)))
+
+
+def _muon_states(params, states):
+    for p, st in zip(params, states):
+        m, s = st["exp_avg"], st.get("exp_avg_scale")
+        if m.shape != p.shape:
+            raise ValueError(f"exp_avg of shape {tuple(m.shape)} for a parameter of {tuple(p.shape)}")
+        if m.dtype == torch.int8 and (s is None or s.numel() != -(-m.numel() // I8_GROUP)):
+            raise ValueError("an 8-bit exp_avg needs exp_avg_scale, one value per 128 of its own")
+    return _states(meo_muon_state, MUON_KEYS, states)
+
+
+def meo_muon_step(hp, step, params, grads, states, workspace=None, stream=None) -> None:
+    ws, nb = _ws(workspace)
+    _check(load().meo_muon_step(ctypes.byref(hp), step, len(params), _tensors(params, grads, states),
+                                _muon_states(params, states), ws, nb, _stream(stream)))
+
+
 # ----------------------------------------------------------------------------- state allocation
 
 def state_shapes(optimizer: str, shape, *, beta1: bool = True, i8: bool = False) -> Dict[str, tuple]:
@@ -1043,8 +1198,10 @@ def state_shapes(optimizer: str, shape, *, beta1: bool = True, i8: bool = False)
     for d in shape:
         n *= d
     groups = ((n + I8_GROUP - 1) // I8_GROUP,)
-    if optimizer == "lamb":
-        st = {"exp_avg": shape, "exp_avg_sq": shape}
+    if optimizer in ("lamb", "muon"):
+        st = {"exp_avg": shape}
+        if optimizer == "lamb":
+            st["exp_avg_sq"] = shape
         if i8:
             st["exp_avg_scale"] = groups
         return st

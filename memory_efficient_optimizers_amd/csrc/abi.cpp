@@ -22,6 +22,7 @@
 #include "internal.h"
 #include "galore.h"
 #include "galore_mx4.h"
+#include "muon.h"
 #include "mx4.h"
 
 using namespace meo;
@@ -803,12 +804,14 @@ std::vector<StatePtrs> state_ptrs(int op, int32_t n, const void* states) {
 
 enum Pass { kPassStats = 0, kPassFinalize, kPassRms, kPassScalars, kPassAfApply, kPassCameMom,
             kPassCameApply, kPassLambMoments, kPassLambApply, kPassStatsWide, kPassStatsTiled,
-            kPassGaProject, kPassGaBack, kPassGaAdamw, kPassGaRefresh, kPassXnorm, kPassSumsqFold, kPassCount };
+            kPassGaProject, kPassGaBack, kPassGaAdamw, kPassGaRefresh, kPassXnorm, kPassSumsqFold,
+            kPassMuMomentum, kPassMuScatter, kPassMuGram, kPassMuPoly, kPassMuApply, kPassCount };
 static_assert(kPassCount == MEO_NUM_PASSES, "pass table");
 const char* const kPassNames[kPassCount] = {"stats", "finalize", "rms", "scalars", "adafactor_apply",
                                             "came_mom", "came_apply", "lamb_moments", "lamb_apply",
                                             "stats_wide", "stats_tiled", "galore_project", "galore_back",
-                                            "galore_adamw", "galore_refresh", "xnorm", "sumsq_fold"};
+                                            "galore_adamw", "galore_refresh", "xnorm", "sumsq_fold",
+                                            "muon_momentum", "muon_scatter", "ns_gram", "ns_poly", "ns_apply"};
 
 struct ProfRec { int pass; hipEvent_t a, b; };
 std::mutex g_prof_mu;
@@ -2744,6 +2747,474 @@ int meo_mx4_matmul(int32_t n, const meo_mx4_product* ps, void* stream) {
         flush();
     }
     return launch_status("mx4 matmul launch");
+}
+
+}  // extern "C"
+
+// ----------------------------------------------------------------------------- Muon
+
+namespace {
+
+// One tensor of an orthogonalization or a Muon step.
+struct MuIn {
+    const void* g = nullptr;  // gradient, or the matrices
+    void* m = nullptr;        // momentum; null: orthogonalization
+    float* ms = nullptr;
+    void* x = nullptr;        // parameter, or the result
+    int64_t batch = 0, rows = 0, cols = 0, ldg = 0, ldx = 0;
+    int16_t gbf16 = 0, xbf16 = 1, mkind = 0;
+    float coef = 0.0f;
+    bool empty() const { return batch == 0 || rows == 0 || cols == 0; }
+    int64_t mp() const { return ceil_div(std::min(rows, cols), kMuPad) * kMuPad; }
+    int64_t np() const { return ceil_div(std::max(rows, cols), kMuPad) * kMuPad; }
+};
+
+constexpr int64_t kMuMaxValues = int64_t{1} << 35;
+constexpr int64_t kMuChunkValues = int64_t{1} << 26;  // padded values of the matrices worked on together
+
+// Parts of the contraction of A = X X^T, of `steps` steps of 64 values each: as many as bring
+// the tiles of a matrix with few rows and a long axis to the CUs. They follow from the matrix
+// alone, so that its result does not depend on the list.
+void mu_gram_parts(int64_t mp, int64_t np, int64_t* parts, int64_t* steps) {
+    const int64_t nt = mp / kMuPad, tiles = nt * (nt + 1) / 2, all = np / 64;
+    *steps = all;
+    if (all >= 16 && 2 * tiles <= kCus) *steps = std::max<int64_t>(ceil_div(all * tiles, kCus), 4);
+    *parts = ceil_div(all, *steps);
+}
+
+// Matrices of a tensor worked on together with others.
+struct MuItem {
+    int32_t k;
+    int64_t b0, count;
+    int64_t off, norm;  // of their workspace and sums of squares
+};
+struct MuChunk {
+    std::vector<MuItem> items;
+    int64_t bytes = 0;
+};
+
+int64_t mu_norm_tiles(const MuIn& t) { return ceil_div(t.rows * t.cols, kMuPart); }
+int64_t mu_norm_span(const MuIn& t) { return ceil_div(mu_norm_tiles(t), kMuMaxParts); }
+int64_t mu_norm_parts(const MuIn& t) { return ceil_div(mu_norm_tiles(t), mu_norm_span(t)); }
+
+int64_t mu_stride(const MuIn& t) {
+    int64_t parts, steps;
+    mu_gram_parts(t.mp(), t.np(), &parts, &steps);
+    return align256(MuPlace(t.mp(), t.np(), parts).total);
+}
+
+// The list in chunks, in order; returns the workspace's bytes.
+int64_t mu_chunks(const std::vector<MuIn>& ts, std::vector<MuChunk>* out) {
+    int64_t most = 0, values = 0;
+    MuChunk c;
+    auto close = [&]() {
+        most = std::max(most, c.bytes);
+        if (out && !c.items.empty()) out->push_back(c);
+        c = MuChunk();
+        values = 0;
+    };
+    for (size_t k = 0; k < ts.size(); ++k) {
+        const MuIn& t = ts[k];
+        if (t.empty()) continue;
+        const int64_t size = t.mp() * t.np(), stride = mu_stride(t), parts = mu_norm_parts(t);
+        for (int64_t b = 0; b < t.batch;) {
+            if (!c.items.empty() && (values + size > kMuChunkValues || c.items.size() == kMuBatch)) close();
+            const int64_t count = std::min(t.batch - b, std::max<int64_t>((kMuChunkValues - values) / size, 1));
+            MuItem i{static_cast<int32_t>(k), b, count, c.bytes, 0};
+            i.norm = i.off + count * stride;
+            c.bytes = i.norm + align256(count * parts * 8);
+            c.items.push_back(i);
+            values += count * size;
+            b += count;
+        }
+    }
+    close();
+    return most;
+}
+
+// The tile form of a pass: the one whose tiles, dealt to the CUs, are done first. A CU holds one
+// large tile, two medium or four small ones at a time; kMuFormCost is what a CU's load takes.
+constexpr int kMuFormLoad[kMuForms] = {4, 2, 1};
+constexpr double kMuFormCost[kMuForms] = {0.45, 0.60, 1.0};
+
+template <class Tiles>
+int mu_form(const std::vector<MuIn>& ts, const MuChunk& c, Tiles tiles) {
+    int best = kMuSmall;
+    double cost = 0.0;
+    for (int f = 0; f < kMuForms; ++f) {
+        int64_t n = 0;
+        for (const MuItem& i : c.items) n += i.count * tiles(ts[i.k], kMuFormTile[f]);
+        const double w = static_cast<double>(ceil_div(n, kCus * kMuFormLoad[f])) * kMuFormCost[f];
+        if (f == 0 || w <= cost) {
+            best = f;
+            cost = w;
+        }
+    }
+    return best;
+}
+
+int check_ns_hp(const meo_orthogonalize_hparams* hp) {
+    if (!hp) return fail(MEO_ENULL, "hparams is NULL");
+    if (!(finite(hp->eps) && hp->eps >= 0.0)) return fail(MEO_EINVAL, "Invalid epsilon value");
+    if (hp->steps < 1 || hp->steps > MEO_NS_MAX_STEPS)
+        return fail(MEO_EINVAL, "steps must be 1 to " + std::to_string(MEO_NS_MAX_STEPS));
+    double top = 1.0;  // the largest singular value there can be
+    for (int k = 0; k < hp->steps; ++k) {
+        const double a = hp->coefficients[k][0], b = hp->coefficients[k][1], c = hp->coefficients[k][2];
+        if (!finite(a) || !finite(b) || !finite(c)) return fail(MEO_EINVAL, "non-finite coefficient");
+        const double s2 = top * top;
+        double poly = std::abs(b * s2 + c * s2 * s2), next = std::abs(top * (a + b * s2 + c * s2 * s2));
+        const double turn = c != 0.0 ? -b / (2.0 * c) : -1.0;  // of b x + c x^2
+        if (turn > 0.0 && turn < s2) poly = std::max(poly, std::abs(b * turn + c * turn * turn));
+        // of a s + b s^3 + c s^5: a + 3 b x + 5 c x^2 = 0, x = s^2
+        double x[2] = {-1.0, -1.0};
+        const double disc = 9.0 * b * b - 20.0 * a * c;
+        if (c != 0.0 && disc >= 0.0) {
+            x[0] = (-3.0 * b + std::sqrt(disc)) / (10.0 * c);
+            x[1] = (-3.0 * b - std::sqrt(disc)) / (10.0 * c);
+        } else if (c == 0.0 && b != 0.0) {
+            x[0] = -a / (3.0 * b);
+        }
+        for (double v : x)
+            if (v > 0.0 && v < s2) next = std::max(next, std::abs(std::sqrt(v) * (a + b * v + c * v * v)));
+        if (!(next <= 8.0) || !(poly <= 100.0))
+            return fail(MEO_EINVAL, "coefficients of step " + std::to_string(k) + " let singular values grow too large");
+        top = next;
+    }
+    return MEO_OK;
+}
+
+int check_mu_shape(const std::string& who, int64_t rows, int64_t cols) {
+    const int64_t m = ceil_div(std::min(rows, cols), kMuPad) * kMuPad, n = ceil_div(std::max(rows, cols), kMuPad) * kMuPad;
+    if (n > kMuMaxSide) return fail(MEO_ESHAPE, who + "rows or cols exceed 2^22");
+    if (m * n > kMuMaxValues) return fail(MEO_ESHAPE, who + "a matrix exceeds 2^35 values");
+    return MEO_OK;
+}
+
+int check_mu_workspace(int64_t need, void* ws, size_t bytes, int dev) {
+    if (need == 0) return MEO_OK;
+    if (!ws) return fail(MEO_EWORKSPACE, "workspace is NULL");
+    if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(MEO_EWORKSPACE, "workspace not 256-byte aligned");
+    if (bytes < static_cast<size_t>(need))
+        return fail(MEO_EWORKSPACE, "workspace too small: need " + std::to_string(need) + " bytes");
+    return check_device_range(ws, bytes, dev, "workspace", MEO_EWORKSPACE);
+}
+
+// The passes over a validated list. update: Muon's parameters (else results).
+int mu_run(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, MuStepArgs a, float decay, bool update, void* ws,
+           size_t ws_bytes, int dev, hipStream_t s) {
+    std::vector<MuChunk> chunks;
+    const int rc = check_mu_workspace(mu_chunks(ts, &chunks), ws, ws_bytes, dev);
+    if (rc) return rc;
+    a.eps = hp.eps;
+    PassTimer pt(s);
+    for (const MuChunk& c : chunks) {
+        MuLast last;
+        std::memset(&last, 0, sizeof last);
+        last.decay = decay;
+        last.update = update;
+        MuTensors& t = last.t;
+        MuMatrices all;
+        std::memset(&all, 0, sizeof all);
+        t.n = all.n = static_cast<int32_t>(c.items.size());
+        bool split = false;
+        for (int i = 0; i < t.n; ++i) {
+            const MuItem& it = c.items[i];
+            const MuIn& in = ts[it.k];
+            const int64_t size = in.rows * in.cols;
+            MuTensor& d = t.d[i];
+            MuMatrix& m = all.d[i];
+            d.g = static_cast<const uint8_t*>(in.g) + it.b0 * in.rows * in.ldg * (in.gbf16 ? 2 : 4);
+            d.x = static_cast<uint8_t*>(in.x) + it.b0 * in.rows * in.ldx * (in.xbf16 ? 2 : 4);
+            if (in.m) {
+                d.m = static_cast<uint8_t*>(in.m) + it.b0 * size * (in.mkind == 2 ? 1 : in.mkind == 1 ? 2 : 4);
+                if (in.mkind == 2) d.ms = in.ms + it.b0 * size / kI8Group;  // (several matrices: whole groups)
+            }
+            d.ws = m.ws = static_cast<uint8_t*>(ws) + it.off;
+            d.norm = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + it.norm);
+            d.ldg = in.ldg;
+            d.ldx = in.ldx;
+            d.stride = m.stride = mu_stride(in);
+            d.rows = static_cast<int32_t>(in.rows);
+            d.cols = static_cast<int32_t>(in.cols);
+            d.batch = m.batch = static_cast<int32_t>(it.count);
+            d.mp = m.mp = static_cast<int32_t>(in.mp());
+            d.np = m.np = static_cast<int32_t>(in.np());
+            d.parts = static_cast<int32_t>(mu_norm_parts(in));
+            d.tiles_per_part = static_cast<int32_t>(mu_norm_span(in));
+            // about the square root of the longer side: entries of a matrix with orthonormal
+            // rows are then about 1
+            d.lift = std::min(12, static_cast<int>(std::lround(0.5 * std::log2(static_cast<double>(std::max(in.rows, in.cols))))));
+            m.lift = static_cast<float>(std::ldexp(1.0, d.lift));
+            d.coef = in.coef;
+            d.gbf16 = in.gbf16;
+            d.xbf16 = in.xbf16;
+            d.mkind = in.mkind;
+            d.tall = in.rows > in.cols;
+            int64_t parts, steps;
+            mu_gram_parts(m.mp, m.np, &parts, &steps);
+            m.parts = static_cast<int32_t>(parts);
+            m.steps = static_cast<int32_t>(steps);
+            split = split || parts > 1;
+        }
+        auto count = [&](auto& l, auto blocks) {
+            uint32_t n = 0;
+            for (int i = 0; i < l.n; ++i) {
+                l.first[i] = n;
+                n += static_cast<uint32_t>(blocks(l.d[i]));
+            }
+            l.first[l.n] = n;
+        };
+        auto square = [](int64_t side, int64_t tile) { const int64_t q = ceil_div(side, tile); return q * (q + 1) / 2; };
+        const int fg = mu_form(ts, c, [&](const MuIn& q, int64_t tile) {
+            int64_t parts, steps;
+            mu_gram_parts(q.mp(), q.np(), &parts, &steps);
+            return square(q.mp(), tile) * parts;
+        });
+        const int fp = mu_form(ts, c, [&](const MuIn& q, int64_t tile) { return square(q.mp(), tile); });
+        const int fa = mu_form(ts, c, [&](const MuIn& q, int64_t tile) { return ceil_div(q.mp(), tile) * ceil_div(q.np(), tile); });
+        MuMatrices gram = all, join = all, poly = all, apply = all;
+        count(gram, [&](const MuMatrix& m) { return m.batch * square(m.mp, kMuFormTile[fg]) * m.parts; });
+        count(join, [&](const MuMatrix& m) { return m.parts > 1 ? m.batch * (int64_t{m.mp} / 4 * m.mp / kMuThreads) : 0; });
+        count(poly, [&](const MuMatrix& m) { return m.batch * square(m.mp, kMuFormTile[fp]); });
+        count(apply, [&](const MuMatrix& m) { return m.batch * ceil_div(m.mp, kMuFormTile[fa]) * ceil_div(m.np, kMuFormTile[fa]); });
+        count(t, [&](const MuTensor& d) { return int64_t{d.batch} * d.parts; });
+        launch_mu_momentum(t, a, s);
+        pt.mark(kPassMuMomentum);
+        count(t, [&](const MuTensor& d) { return d.batch * (int64_t{d.mp} / kMuTile) * (d.np / kMuTile); });
+        launch_mu_scatter(t, a, s);
+        pt.mark(kPassMuScatter);
+        for (int k = 0; k < hp.steps; ++k) {
+            const MuPoly p{static_cast<float>(hp.coefficients[k][0]), static_cast<float>(hp.coefficients[k][1]),
+                           static_cast<float>(hp.coefficients[k][2])};
+            launch_mu_gram(gram, fg, k & 1, s);
+            if (split) launch_mu_join(join, s);
+            pt.mark(kPassMuGram);
+            launch_mu_poly(poly, fp, p, s);
+            pt.mark(kPassMuPoly);
+            launch_mu_apply(apply, fa, k & 1, k + 1 == hp.steps ? &last : nullptr, s);
+            pt.mark(kPassMuApply);
+        }
+    }
+    return launch_status("newton-schulz launch");
+}
+
+std::vector<MuIn> mu_list(int32_t n, const meo_ns_matrices* ms) {
+    std::vector<MuIn> out(ms && n > 0 ? n : 0);
+    for (size_t k = 0; k < out.size(); ++k) {
+        MuIn& t = out[k];
+        t.g = ms[k].x;
+        t.x = ms[k].out;
+        t.batch = ms[k].batch;
+        t.rows = ms[k].rows;
+        t.cols = ms[k].cols;
+        t.ldg = ms[k].ldx;
+        t.ldx = ms[k].ldo;
+        t.gbf16 = ms[k].dtype == MEO_BF16;
+    }
+    return out;
+}
+
+std::vector<MuIn> mu_list(const meo_muon_hparams* hp, int32_t n, const meo_tensor* ts, const meo_muon_state* st) {
+    std::vector<MuIn> out(ts && n > 0 ? n : 0);
+    for (size_t k = 0; k < out.size(); ++k) {
+        MuIn& t = out[k];
+        t.g = ts[k].grad;
+        t.x = ts[k].param;
+        t.batch = ts[k].batch;
+        t.rows = ts[k].rows;
+        t.cols = t.ldg = t.ldx = ts[k].cols;
+        t.gbf16 = ts[k].grad_dtype == MEO_BF16;
+        t.xbf16 = ts[k].param_dtype == MEO_BF16;
+        t.mkind = ts[k].state_dtype == MEO_I8 ? 2 : ts[k].state_dtype == MEO_BF16 ? 1 : 0;
+        if (st) {
+            t.m = st[k].exp_avg;
+            t.ms = st[k].exp_avg_scale;
+        }
+        if (t.empty()) continue;
+        const double r = static_cast<double>(t.rows), c = static_cast<double>(t.cols);
+        const double s = hp->adjust_lr == MEO_MUON_ORIGINAL ? std::sqrt(std::max(1.0, r / c)) : 0.2 * std::sqrt(std::max(r, c));
+        t.coef = static_cast<float>(hp->lr * s);
+    }
+    return out;
+}
+
+int check_ns_matrices(int32_t n, const meo_ns_matrices* ms) {
+    if (n < 0) return fail(MEO_EINVAL, "negative matrix count");
+    if (n == 0) return MEO_OK;
+    if (!ms) return fail(MEO_ENULL, "matrices is NULL");
+    for (int32_t k = 0; k < n; ++k) {
+        const meo_ns_matrices& m = ms[k];
+        const std::string who = "matrix " + std::to_string(k) + ": ";
+        if (m.batch < 0 || m.rows < 0 || m.cols < 0) return fail(MEO_ESHAPE, who + "negative batch, rows or cols");
+        if (m.dtype != MEO_F32 && m.dtype != MEO_BF16) return fail(MEO_EDTYPE, who + "dtype must be MEO_F32 or MEO_BF16");
+        if (m.ldx < m.cols || m.ldo < m.cols) return fail(MEO_ESHAPE, who + "leading dimension below the row length");
+        if (m.batch == 0 || m.rows == 0 || m.cols == 0) continue;
+        if (m.batch > kMaxDim || m.rows > kMaxDim || m.ldx > kMaxDim || m.ldo > kMaxDim)
+            return fail(MEO_ESHAPE, who + "batch, rows or a leading dimension exceeds 2^31 - 1");
+        const int rc = check_mu_shape(who, m.rows, m.cols);
+        if (rc) return rc;
+        if (static_cast<__int128>(m.batch) * m.rows * std::max(m.ldx, m.ldo) > (static_cast<__int128>(1) << 60))
+            return fail(MEO_ESHAPE, who + "too many elements");
+        if (!m.x) return fail(MEO_ENULL, who + "x is NULL");
+        if (!m.out) return fail(MEO_ENULL, who + "out is NULL");
+        if (reinterpret_cast<uintptr_t>(m.x) % elem_bytes(m.dtype)) return fail(MEO_EALIGN, who + "x misaligned for its dtype");
+        if (reinterpret_cast<uintptr_t>(m.out) % 2) return fail(MEO_EALIGN, who + "out misaligned");
+    }
+    return MEO_OK;
+}
+
+int check_muon_tensors(int64_t step, int32_t n, const meo_tensor* ts, const meo_muon_state* st) {
+    if (step < 1) return fail(MEO_EINVAL, "step must be >= 1 (1-based index of the step being taken)");
+    if (n < 0) return fail(MEO_EINVAL, "negative tensor count");
+    if (n == 0) return MEO_OK;
+    if (!ts) return fail(MEO_ENULL, "tensors is NULL");
+    if (!st) return fail(MEO_ENULL, "states is NULL");
+    for (int32_t k = 0; k < n; ++k) {
+        const meo_tensor& t = ts[k];
+        const std::string who = "tensor " + std::to_string(k) + ": ";
+        if (t.batch < 0 || t.rows < 0 || t.cols < 0 || t.ndim < 0)
+            return fail(MEO_ESHAPE, who + "negative batch, rows, cols or ndim");
+        int64_t numel;
+        if (overflow_numel(t, &numel)) return fail(MEO_ESHAPE, who + "too many elements");
+        if (t.param_dtype != MEO_F32 && t.param_dtype != MEO_BF16)
+            return fail(MEO_EDTYPE, who + "param_dtype must be MEO_F32 or MEO_BF16");
+        if (t.grad_dtype != MEO_F32 && t.grad_dtype != MEO_BF16)
+            return fail(MEO_EDTYPE, who + "grad_dtype must be MEO_F32 or MEO_BF16");
+        if (t.state_dtype != MEO_F32 && t.state_dtype != MEO_BF16 && t.state_dtype != MEO_I8)
+            return fail(MEO_EDTYPE, who + "state_dtype must be MEO_F32, MEO_BF16 or MEO_I8");
+        if (numel == 0) continue;
+        if (t.ndim < 2) return fail(MEO_ESHAPE, who + "Muon takes tensors of two or more dims");
+        if (t.ndim == 2 && t.batch != 1) return fail(MEO_ESHAPE, who + "a 2-D tensor has batch 1");
+        if (t.batch > kMaxDim) return fail(MEO_ESHAPE, who + "batch exceeds 2^31 - 1");
+        const int rc = check_mu_shape(who, t.rows, t.cols);
+        if (rc) return rc;
+        if (!t.param) return fail(MEO_ENULL, who + "param is NULL");
+        if (!t.grad) return fail(MEO_ENULL, who + "grad is NULL");
+        if (reinterpret_cast<uintptr_t>(t.param) % elem_bytes(t.param_dtype))
+            return fail(MEO_EALIGN, who + "param misaligned for its dtype");
+        if (reinterpret_cast<uintptr_t>(t.grad) % elem_bytes(t.grad_dtype))
+            return fail(MEO_EALIGN, who + "grad misaligned for its dtype");
+        if (!st[k].exp_avg) return fail(MEO_ENULL, who + "exp_avg is NULL");
+        if (reinterpret_cast<uintptr_t>(st[k].exp_avg) % elem_bytes(t.state_dtype))
+            return fail(MEO_EALIGN, who + "exp_avg misaligned");
+        if (t.state_dtype == MEO_I8) {
+            if (!st[k].exp_avg_scale) return fail(MEO_ENULL, who + "exp_avg_scale is NULL (8-bit momentum)");
+            if (reinterpret_cast<uintptr_t>(st[k].exp_avg_scale) % 4) return fail(MEO_EALIGN, who + "exp_avg_scale misaligned");
+            if (t.batch > 1 && t.rows * t.cols % kI8Group != 0)
+                return fail(MEO_ESHAPE, who + "an 8-bit momentum of several matrices needs rows * cols % 128 == 0");
+        }
+    }
+    return MEO_OK;
+}
+
+int check_muon_hp(const meo_muon_hparams* hp) {
+    if (!hp) return fail(MEO_ENULL, "hparams is NULL");
+    if (!(finite(hp->lr) && hp->lr >= 0.0)) return fail(MEO_EINVAL, "Invalid learning rate");
+    if (!(hp->momentum >= 0.0 && hp->momentum < 1.0)) return fail(MEO_EINVAL, "Invalid momentum value");
+    if (!finite(hp->weight_decay)) return fail(MEO_EINVAL, "weight_decay must be finite");
+    if (hp->adjust_lr != MEO_MUON_ORIGINAL && hp->adjust_lr != MEO_MUON_MATCH_RMS_ADAMW)
+        return fail(MEO_EINVAL, "adjust_lr must be MEO_MUON_ORIGINAL or MEO_MUON_MATCH_RMS_ADAMW");
+    return check_ns_hp(&hp->ns);
+}
+
+}  // namespace
+
+extern "C" {
+
+void meo_orthogonalize_defaults(meo_orthogonalize_hparams* hp) {
+    if (!hp) return;
+    std::memset(hp, 0, sizeof *hp);
+    hp->eps = 1e-7;
+    hp->steps = 5;
+    for (auto& c : hp->coefficients) {
+        c[0] = 3.4445;
+        c[1] = -4.7750;
+        c[2] = 2.0315;
+    }
+}
+
+int meo_orthogonalize_validate(const meo_orthogonalize_hparams* hp, int32_t n, const meo_ns_matrices* ms) {
+    g_err.clear();
+    const int rc = check_ns_hp(hp);
+    return rc ? rc : check_ns_matrices(n, ms);
+}
+
+size_t meo_orthogonalize_workspace_size(const meo_orthogonalize_hparams* hp, int32_t n, const meo_ns_matrices* ms) {
+    if (!hp || n <= 0 || !ms) return 0;
+    for (int32_t k = 0; k < n; ++k)  // (what the call refuses)
+        if (ms[k].batch < 0 || ms[k].rows < 0 || ms[k].cols < 0 || check_mu_shape("", ms[k].rows, ms[k].cols)) return 0;
+    return static_cast<size_t>(mu_chunks(mu_list(n, ms), nullptr));
+}
+
+int meo_orthogonalize(const meo_orthogonalize_hparams* hp, int32_t n, const meo_ns_matrices* ms, void* ws, size_t ws_bytes,
+                      void* stream) {
+    int rc = meo_orthogonalize_validate(hp, n, ms);
+    if (rc || n == 0) return rc;
+    int dev = 0;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    for (int32_t k = 0; k < n; ++k) {
+        const meo_ns_matrices& m = ms[k];
+        if (m.batch == 0 || m.rows == 0 || m.cols == 0) continue;
+        const std::string who = "matrix " + std::to_string(k) + ": ";
+        rc = check_device_range(m.x, strided_bytes(m.batch * m.rows, m.ldx, m.cols, elem_bytes(m.dtype)), dev, who + "x", MEO_EMEMORY);
+        if (!rc) rc = check_device_range(m.out, strided_bytes(m.batch * m.rows, m.ldo, m.cols, 2), dev, who + "out", MEO_EMEMORY);
+        if (rc) return rc;
+    }
+    return mu_run(*hp, mu_list(n, ms), MuStepArgs{0.0f, 1.0f, 0, 0.0}, 1.0f, false, ws, ws_bytes, dev,
+                  static_cast<hipStream_t>(stream));
+}
+
+void meo_muon_defaults(meo_muon_hparams* hp) {
+    if (!hp) return;
+    std::memset(hp, 0, sizeof *hp);
+    hp->lr = 1e-3;
+    hp->momentum = 0.95;
+    hp->weight_decay = 0.1;
+    hp->nesterov = 1;
+    hp->adjust_lr = MEO_MUON_ORIGINAL;
+    meo_orthogonalize_defaults(&hp->ns);
+}
+
+int meo_muon_validate(const meo_muon_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts, const meo_muon_state* st) {
+    g_err.clear();
+    const int rc = check_muon_hp(hp);
+    return rc ? rc : check_muon_tensors(step, n, ts, st);
+}
+
+size_t meo_muon_workspace_size(const meo_muon_hparams* hp, int32_t n, const meo_tensor* ts) {
+    if (!hp || n <= 0 || !ts) return 0;
+    for (int32_t k = 0; k < n; ++k)
+        if (ts[k].batch < 0 || ts[k].rows < 0 || ts[k].cols < 0 || check_mu_shape("", ts[k].rows, ts[k].cols)) return 0;
+    return static_cast<size_t>(mu_chunks(mu_list(hp, n, ts, nullptr), nullptr));
+}
+
+int meo_muon_step(const meo_muon_hparams* hp, int64_t step, int32_t n, const meo_tensor* ts, const meo_muon_state* st, void* ws,
+                  size_t ws_bytes, void* stream) {
+    int rc = meo_muon_validate(hp, step, n, ts, st);
+    if (rc || n == 0) return rc;
+    int dev = 0;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    for (int32_t k = 0; k < n; ++k) {
+        const meo_tensor& t = ts[k];
+        int64_t numel = 0;
+        overflow_numel(t, &numel);
+        if (numel == 0) continue;
+        const std::string who = "tensor " + std::to_string(k) + ": ";
+        const size_t ne = static_cast<size_t>(numel);
+        rc = check_device_range(t.param, ne * elem_bytes(t.param_dtype), dev, who + "param", MEO_EMEMORY);
+        if (!rc) rc = check_device_range(t.grad, ne * elem_bytes(t.grad_dtype), dev, who + "grad", MEO_EMEMORY);
+        if (!rc) rc = check_device_range(st[k].exp_avg, ne * elem_bytes(t.state_dtype), dev, who + "exp_avg", MEO_EMEMORY);
+        if (!rc && t.state_dtype == MEO_I8)
+            rc = check_device_range(st[k].exp_avg_scale, static_cast<size_t>(ceil_div(numel, kI8Group)) * 4, dev, who + "exp_avg_scale",
+                                    MEO_EMEMORY);
+        if (rc) return rc;
+    }
+    const MuStepArgs a{static_cast<float>(hp->momentum), static_cast<float>(1.0 - hp->momentum), hp->nesterov != 0, 0.0};
+    return mu_run(hp->ns, mu_list(hp, n, ts, st), a, static_cast<float>(1.0 - hp->lr * hp->weight_decay), true, ws, ws_bytes, dev,
+                  static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,108 @@
+// Orthogonalization by Newton-Schulz steps and the Muon step: descriptors and launchers
+// shared by muon.hip and the C ABI.
+#pragma once
+#include "internal.h"
+
+namespace meo {
+
+constexpr int kMuPad = 64;         // both sides of a matrix in the workspace are multiples of it
+constexpr int kMuBatch = 16;       // tensors per launch (their descriptors are kernel arguments)
+constexpr int kMuThreads = 256;    // momentum and scatter passes
+constexpr int kMuTile = 64;        // scatter pass: square tiles of the matrix in the workspace
+constexpr int64_t kMuPart = 8192;  // values per part of the momentum pass
+constexpr int64_t kMuMaxParts = 1024;
+constexpr int64_t kMuMaxSide = 1 << 22;  // longer side of a matrix (32-bit offsets in a tile)
+
+// What the passes over the caller's tensors need of one of them ([batch] matrices).
+struct MuTensor {
+    const void* g;    // gradient, or the matrices to orthogonalize
+    void* m;          // momentum (null: orthogonalize)
+    float* ms;        // scales of an 8-bit momentum
+    void* x;          // parameter, or the result
+    uint8_t* ws;      // workspace of the first matrix
+    double* norm;     // [batch][parts] sums of squares
+    int64_t ldg, ldx; // elements between rows of g and x
+    int64_t stride;   // bytes of workspace per matrix
+    int32_t rows, cols, batch;
+    int32_t mp, np;   // padded shorter and longer side
+    int32_t parts, tiles_per_part;  // of the momentum pass: kMuPart values per tile
+    int32_t lift;     // the workspace holds values times 2^lift
+    float coef;       // Muon: lr times the scale of the matrix' shape
+    int16_t gbf16, xbf16, mkind;  // mkind: Storage of m (0 fp32, 1 bf16, 2 int8)
+    int16_t tall;     // rows > cols: the workspace holds the transpose
+};
+
+// What a product needs of one tensor.
+struct MuMatrix {
+    uint8_t* ws;
+    int64_t stride;
+    int32_t mp, np, batch;
+    int32_t parts, steps;  // A = X X^T: parts of the contraction, steps of 64 in each
+    float lift;            // 2^lift
+};
+
+template <class T>
+struct MuList {
+    int32_t n;
+    uint32_t first[kMuBatch + 1];  // blocks before each tensor; [n]: all
+    T d[kMuBatch];
+};
+using MuTensors = MuList<MuTensor>;
+using MuMatrices = MuList<MuMatrix>;
+
+// Values between rows of a matrix in the workspace, its columns a multiple of 64: an odd
+// multiple, so that the same columns of consecutive rows lie in different channels of the L2
+// (rows of 8192 bytes put all of a tile's 128-byte pieces into one).
+__host__ __device__ constexpr int64_t mu_ld(int64_t cols) { return (cols / 64 | 1) * 64; }
+
+// A matrix in the workspace (offsets in bytes): two buffers of X's high parts and one of the
+// low parts ([mp][np] fp16), off-diagonal A and B ([mp][mp] fp16), the diagonal of A and
+// the row factors a + B_ii ([mp] fp32), partial sums of A.
+struct MuPlace {
+    int64_t x, lo, a, b, d, q, part, total;
+    __host__ __device__ MuPlace(int64_t mp, int64_t np, int64_t parts) {
+        const int64_t s = mp * mu_ld(mp) * 2;
+        x = mp * mu_ld(np) * 2;
+        lo = 2 * x;
+        a = 3 * x;
+        b = a + s;
+        d = b + s;
+        q = d + mp * 4;
+        part = (q + mp * 4 + 255) / 256 * 256;
+        total = part + (parts > 1 ? parts * mp * mp * 4 : 0);
+    }
+    __host__ __device__ int64_t hi(int buffer) const { return buffer ? x : 0; }
+};
+
+struct MuStepArgs {   // momentum pass and scatter
+    float beta, omb;  // momentum weight and 1 - it
+    int32_t nesterov;
+    double eps;
+};
+
+struct MuPoly {       // X <- a X + (b A + c A^2) X
+    float a, b, c;
+};
+
+// Square tiles of a product.
+enum MuForm { kMuSmall = 0, kMuMedium, kMuLarge, kMuForms };
+constexpr int kMuFormTile[kMuForms] = {64, 128, 256};
+constexpr int kMuFormThreads[kMuForms] = {256, 256, 256};
+
+struct MuLast {       // the last step's results go to the caller's tensors
+    MuTensors t;
+    float decay;      // 1 - lr wd
+    int32_t update;   // a parameter's update (else bf16 results)
+};
+
+void launch_mu_momentum(const MuTensors& t, const MuStepArgs& a, hipStream_t s);
+void launch_mu_scatter(const MuTensors& t, const MuStepArgs& a, hipStream_t s);
+// A's off-diagonal part and diagonal from X (buffer src); with parts, their sums and the join.
+void launch_mu_gram(const MuMatrices& m, int form, int src, hipStream_t s);
+void launch_mu_join(const MuMatrices& m, hipStream_t s);
+// B = b A + c A^2 off the diagonal, a + B_ii on it.
+void launch_mu_poly(const MuMatrices& m, int form, const MuPoly& p, hipStream_t s);
+// X' = (a + B_ii) X + B X, into the other buffer or, `last` given, the caller's tensors.
+void launch_mu_apply(const MuMatrices& m, int form, int src, const MuLast* last, hipStream_t s);
+
+}  // namespace meo

@@ -1,0 +1,809 @@
+// Orthogonalization of matrices by Newton-Schulz steps, and the Muon step around it.
+//
+// With X0 = U / max(|U|, eps) (Frobenius norm; the shorter side as rows, m <= n), each step is
+//     A = X X^T,   X <- a X + (b A + c A^2) X.
+// The products run on fp16 matrix cores with fp32 sums. What is rounded to fp16 (relative 2^-12,
+// bf16 would be 2^-9 at the same rate) and why that is enough:
+//   * X as an operand. The linear term, which alone carries the small singular values, takes X
+//     as the sum of two fp16 parts (hi + lo, 22 bits): with hi alone a matrix of rank 8 plus 1%
+//     noise came out 3.7e-2 off, so 9e-4.
+//   * A and B = b A + c A^2 off their diagonals. The diagonals, which near the end are most of
+//     A, are held in fp32 (d, and q = a + B_ii) and enter by row: (A^2)_ij = (O^2)_ij +
+//     O_ij (d_i + d_j) off the diagonal, with O the rest of A. That halves the error of
+//     well-conditioned matrices (1.2e-3 to 6e-4).
+// Values are held times powers of two, so that entries of ordinary size are normal fp16
+// numbers: X times 2^lift, about the square root of its longer side, O and B times 2^8.
+#include "muon.h"
+#include "mx4_tile.h"
+
+namespace meo {
+
+namespace {
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+
+struct MuNone {};
+struct MuNoLoad {
+    __device__ MuNone operator()(int, int) const { return {}; }
+};
+
+constexpr float kMuLift = 256.0f;        // of O and B
+constexpr float kMuUnlift = 1.0f / 256;
+
+__device__ __forceinline__ f32x16 mfma_f16(const u32x4& a, const u32x4& b, const f32x16& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
+}
+
+// The tensor of block `id`, whose blocks the list counts in order.
+template <class L>
+__device__ __forceinline__ int mu_find(const L& l, uint32_t id) {
+    int i = 0;
+    while (i + 1 < l.n && id >= l.first[i + 1]) ++i;
+    return i;
+}
+
+// ----------------------------------------------------------------------------- the caller's tensors
+
+// 8 values of matrix b of the gradient (or input) from element i of its rows on, the first
+// `valid` of them.
+__device__ __forceinline__ void mu_load_g(const MuTensor& t, int b, int64_t i, int valid, float* f) {
+    const int64_t at = static_cast<int64_t>(b) * t.rows * t.ldg;
+    if (t.ldg == t.cols) {
+        load_any8(t.g, at + i, valid, t.gbf16, f);
+        return;
+    }
+    const int64_t r = i / t.cols;
+    const int c = static_cast<int>(i - r * t.cols);
+    if (c + kVec <= t.cols) {
+        load_any8(t.g, at + r * t.ldg + c, valid, t.gbf16, f);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+        f[e] = 0.0f;
+        if (e >= valid) continue;
+        const int64_t re = (i + e) / t.cols, j = at + re * t.ldg + (i + e - re * t.cols);
+        f[e] = t.gbf16 ? __uint_as_float(static_cast<uint32_t>(*gld<uint16_t>(static_cast<const uint16_t*>(t.g) + j)) << 16)
+                       : *gld<float>(static_cast<const float*>(t.g) + j);
+    }
+}
+
+// 8 values of the momentum at element i of the whole tensor.
+__device__ __forceinline__ void mu_load_m(const MuTensor& t, int64_t i, int valid, float* f) {
+    if (t.mkind != 2) {
+        load_any8(t.m, i, valid, t.mkind == 1, f);
+        return;
+    }
+    const int8_t* p = static_cast<const int8_t*>(t.m) + i;
+    typedef u32x2 u32x2_any __attribute__((aligned(1)));
+    u32x2 w = {0u, 0u};
+    if (valid == kVec) {
+        w = *gld<u32x2_any>(p);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+            if (e < valid) w[e >> 2] |= static_cast<uint32_t>(*gld<uint8_t>(p + e)) << (8 * (e & 3));
+    }
+    const float s0 = valid > 0 ? *gld<float>(t.ms + (i >> 7)) : 0.0f;
+    const float s1 = valid > 0 ? *gld<float>(t.ms + ((i + valid - 1) >> 7)) : 0.0f;  // 8 values touch two groups at most
+#pragma unroll
+    for (int e = 0; e < kVec; ++e)
+        f[e] = static_cast<float>(static_cast<int8_t>(w[e >> 2] >> (8 * (e & 3)))) * (((i + e) >> 7) == (i >> 7) ? s0 : s1);
+}
+
+// The direction from the gradient and the stored momentum.
+__device__ __forceinline__ void mu_direction(const MuStepArgs& a, const float* g, const float* m, float* u) {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) u[e] = a.nesterov ? g[e] * a.omb + m[e] * a.beta : m[e];
+}
+
+// The momentum's update and the sum of squares of the direction, in fp64 (the squares of any
+// fp32 value neither vanish nor overflow). One block per part of a matrix; parts are joined by
+// every block of the next pass, in order.
+__global__ __launch_bounds__(kMuThreads) void k_mu_momentum(MuTensors l, MuStepArgs a) {
+    __shared__ double sums[kMuThreads / 64];
+    const int k = mu_find(l, blockIdx.x);
+    const MuTensor& t = l.d[k];
+    const uint32_t item = blockIdx.x - l.first[k];
+    const int b = static_cast<int>(item / t.parts), part = static_cast<int>(item % t.parts);
+    const int64_t size = static_cast<int64_t>(t.rows) * t.cols, base = b * size;
+    const int64_t i0 = part * t.tiles_per_part * kMuPart, i1 = min(size, i0 + t.tiles_per_part * kMuPart);
+    double sum = 0.0;
+    for (int64_t i = i0 + threadIdx.x * kVec; i - threadIdx.x * kVec < i1; i += kMuThreads * kVec) {
+        const int valid = clamp_valid(i1 - i);
+        float g[kVec], u[kVec];
+        if (valid > 0) mu_load_g(t, b, i, valid, g);
+        else
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) g[e] = 0.0f;
+        if (t.m) {
+            float m[kVec];
+            mu_load_m(t, base + i, valid, m);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) m[e] = m[e] * a.beta + g[e] * a.omb;
+            if (t.mkind == 2) {
+                uint32_t lo, hi;
+                float scale = group_max8(m) * (1.0f / 127.0f);
+                quant_by_scale8(m, lo, hi, scale);
+                store_i8x8(t.m, t.ms, base + i, valid, (reinterpret_cast<uintptr_t>(t.m) & 7) == 0, lo, hi, scale);
+            } else if (valid > 0) {
+                if (t.mkind == 1)
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) m[e] = round_bf16(m[e]);
+                store_any8(t.m, base + i, valid, t.mkind == 1, m);
+            }
+            mu_direction(a, g, m, u);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) u[e] = g[e];
+        }
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) sum += static_cast<double>(u[e]) * static_cast<double>(u[e]);
+    }
+    const double s = block_sum_d(sum, sums);
+    if (threadIdx.x == 0) *gst<double>(t.norm + item) = s;
+}
+
+// 2^lift / max(norm, eps) of matrix b; a norm that is not finite gives NaN, one of zero (with
+// eps zero) 0.
+__device__ __forceinline__ double mu_factor(const MuTensor& t, int b, double eps, double* sums) {
+    const double* p = t.norm + static_cast<int64_t>(b) * t.parts;
+    double s = 0.0;
+    for (int i = threadIdx.x; i < t.parts; i += kMuThreads) s += *gld<double>(p + i);
+    s = block_sum_d(s, sums);
+    if (threadIdx.x == 0) {
+        const double norm = sqrt(s), top = norm > eps ? norm : eps;
+        sums[kMuThreads / 64] = !(norm <= 1.7976931348623157e308) ? __builtin_nan("") : top > 0.0 ? ldexp(1.0, t.lift) / top : 0.0;
+    }
+    __syncthreads();
+    return sums[kMuThreads / 64];
+}
+
+__device__ __forceinline__ void mu_split(float v, uint32_t& hi, uint32_t& lo) {
+    const _Float16 h = static_cast<_Float16>(v);
+    const _Float16 r = static_cast<_Float16>(v - static_cast<float>(h));
+    hi = __builtin_bit_cast(uint16_t, h);
+    lo = __builtin_bit_cast(uint16_t, r);
+}
+
+// The directions, scaled, into the workspace: a square tile of the padded matrix per block,
+// zeros outside the matrix. A tall matrix is transposed on the way, through LDS.
+__global__ __launch_bounds__(kMuThreads) void k_mu_scatter(MuTensors l, MuStepArgs a) {
+    __shared__ double sums[kMuThreads / 64 + 1];
+    __shared__ float tile[kMuTile][kMuTile + 1];
+    const int k = mu_find(l, blockIdx.x);
+    const MuTensor& t = l.d[k];
+    const uint32_t item = blockIdx.x - l.first[k];
+    const uint32_t tn = t.np / kMuTile, per = tn * (t.mp / kMuTile);
+    const int b = static_cast<int>(item / per);
+    const int r0 = static_cast<int>(item % per / tn) * kMuTile, c0 = static_cast<int>(item % per % tn) * kMuTile;
+    const double f = mu_factor(t, b, a.eps, sums);
+    const MuPlace at(t.mp, t.np, 1);
+    uint8_t* const w = t.ws + b * t.stride;
+    const int64_t size = static_cast<int64_t>(t.rows) * t.cols;
+    const int s0 = t.tall ? c0 : r0, z0 = t.tall ? r0 : c0;  // the source's first row and column
+    const int q = threadIdx.x & 7;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const int r = (threadIdx.x >> 3) + 32 * p, row = s0 + r, col = z0 + q * kVec;
+        const int valid = row < t.rows ? clamp_valid(static_cast<int64_t>(t.cols) - col) : 0;
+        float u[kVec];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) u[e] = 0.0f;
+        if (valid > 0) {
+            const int64_t i = static_cast<int64_t>(row) * t.cols + col;
+            float g[kVec], m[kVec];
+            // (a row's piece, so that row and column need no division)
+            load_any8(t.g, (static_cast<int64_t>(b) * t.rows + row) * t.ldg + col, valid, t.gbf16, g);
+            if (t.m) {
+                mu_load_m(t, b * size + i, valid, m);
+                mu_direction(a, g, m, u);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) u[e] = g[e];
+            }
+        }
+        if (!t.tall) {
+            uint32_t h[kVec], o[kVec];
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) mu_split(e < valid ? static_cast<float>(u[e] * f) : 0.0f, h[e], o[e]);
+            const int64_t i = (static_cast<int64_t>(r0 + r) * mu_ld(t.np) + c0 + q * kVec) * 2;
+            *gst<u32x4>(w + at.hi(0) + i) = u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+            *gst<u32x4>(w + at.lo + i) = u32x4{o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16};
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) tile[r][q * kVec + e] = e < valid ? static_cast<float>(u[e] * f) : 0.0f;
+        }
+    }
+    if (!t.tall) return;
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const int r = (threadIdx.x >> 3) + 32 * p;
+        uint32_t h[kVec], o[kVec];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) mu_split(tile[q * kVec + e][r], h[e], o[e]);
+        const int64_t i = (static_cast<int64_t>(r0 + r) * mu_ld(t.np) + c0 + q * kVec) * 2;
+        *gst<u32x4>(w + at.hi(0) + i) = u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+        *gst<u32x4>(w + at.lo + i) = u32x4{o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16};
+    }
+}
+
+// ----------------------------------------------------------------------------- products
+
+// A T x T tile of a product of NW waves, WM along P's rows and NW / WM along Q's: 32 MB x 32 NB
+// values each. LDS: a ring of kDepth stages of 32 values of the contraction of both operands.
+// What bounds the products is the way from L2 to LDS: with two stages of 64 values (64 KB in
+// flight per CU) a step took 1.16 us without any multiplication, and 0.85 us is what its
+// multiplications take; with five of 32 there are 128 KB in flight.
+template <int T, int WM, int NW>
+struct MuTileOf {
+    static constexpr int kT = T, kWM = WM, kWN = NW / WM, kNW = NW;
+    static constexpr int MB = T / 32 / WM, NB = T / 32 / (NW / WM);
+    static constexpr int kDepth = 5;
+    static constexpr int kOperand = T * 64;  // bytes of one operand's stage
+    static constexpr int kStage = 2 * kOperand;
+    static constexpr int kLds = kDepth * kStage;
+};
+template <int F> struct MuTiles;
+template <> struct MuTiles<kMuSmall> : MuTileOf<64, 2, 4> {};
+template <> struct MuTiles<kMuMedium> : MuTileOf<128, 2, 4> {};
+template <> struct MuTiles<kMuLarge> : MuTileOf<256, 2, 4> {};
+
+// Position of 16-byte chunk c of row r of a tile read transposed: the 8 rows that a read
+// touches 64 bytes of then lie on different banks (rows 8 apart share them, twice is what
+// 512 bytes take).
+template <int T>
+__device__ __forceinline__ int mu_swz_tr(int r) { return T >= 128 ? 4 * (r & 3) : 4 * ((r >> 1) & 1); }
+
+// 16 bytes per lane from base + offset into LDS, lane l at dst + 16 l. In asm, because before
+// every LDS read the compiler would wait for all of its own transfers (it cannot tell what they
+// write); it writes no vector registers, mu_arrive waits for it, and nothing else here uses m0.
+__device__ __forceinline__ void mu_fetch16(const uint8_t* base, uint32_t offset, uint32_t dst) {
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(offset), "s"(base));
+}
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x2 mu_lds_tr(uint32_t a) {  // 4 rows of a column (16-bit values)
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4*)static_cast<uintptr_t>(a)));
+}
+__device__ __forceinline__ u32x4 mu_lds(uint32_t a) {
+    return *(const __attribute__((address_space(3))) u32x4*)static_cast<uintptr_t>(a);
+}
+
+// acc += the tile's product over `steps` steps of 32 values: P's rows i0 .. with lines of ldp
+// values (TR: P is [contraction][columns], columns i0 ..), Q's rows j0 ... Rows past the
+// operands' end (columns, TR) repeat the last ones; they reach values that are not stored.
+// A step's operands go straight into their stage, four steps ahead. The fragments of 16 values
+// of the contraction are read while the ones before are multiplied; the barrier of a step comes
+// before its last multiplication, when its stage has been read and the next one has landed: so
+// one wave per SIMD (a large tile) keeps its matrix core busy. Past the end the last step is
+// fetched again, for equal counts of transfers.
+template <class M, bool TR>
+__device__ __forceinline__ void mu_accumulate(const uint16_t* P, int ldp, int rows_p, const uint16_t* Q, int ldq, int rows_q,
+                                              int i0, int j0, int k0, int steps, uint8_t* lds, f32x16 (&acc)[M::MB][M::NB]) {
+    constexpr int T = M::kT, NW = M::kNW, kRB = T * 2, kCount = T / 16 / NW, kAll = 2 * kCount;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
+    const uint32_t base = uniform(static_cast<int>(lds_addr(lds)));
+    // transfers: 1 KB each, kCount of either operand per wave. Chunk c of row r (64 bytes) lies
+    // at position c ^ (r >> 2 & 3): 16 rows read at one chunk then touch every bank once.
+    uint32_t op[kCount], oq[kCount];
+    const uint32_t chunk = ((lane & 3) ^ ((lane >> 4) & 3)) * 16;
+    const uint8_t* cp;
+    const uint8_t* cq = uniform(reinterpret_cast<const uint8_t*>(Q) + (static_cast<int64_t>(j0) * ldq + k0) * 2);
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+        const int r = 16 * (wave + i * NW) + (lane >> 2);
+        oq[i] = static_cast<uint32_t>(min(r, rows_q - 1 - j0)) * static_cast<uint32_t>(ldq) * 2u + chunk;
+    }
+    if constexpr (TR) {
+        constexpr int kLine = kRB / 16, kRows = 64 / kLine;  // lanes per row, rows per transfer
+        cp = uniform(reinterpret_cast<const uint8_t*>(P) + (static_cast<int64_t>(k0) * ldp + i0) * 2);
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) {
+            const int r = kRows * (wave + i * NW) + lane / kLine;
+            const int c = (lane % kLine) ^ mu_swz_tr<T>(r);
+            op[i] = static_cast<uint32_t>(r) * static_cast<uint32_t>(ldp) * 2u + min(c * 8, rows_p - 8 - i0) * 2u;
+        }
+    } else {
+        cp = uniform(reinterpret_cast<const uint8_t*>(P) + (static_cast<int64_t>(i0) * ldp + k0) * 2);
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) {
+            const int r = 16 * (wave + i * NW) + (lane >> 2);
+            op[i] = static_cast<uint32_t>(min(r, rows_p - 1 - i0)) * static_cast<uint32_t>(ldp) * 2u + chunk;
+        }
+    }
+    const int64_t step_p = TR ? static_cast<int64_t>(ldp) * 64 : 64;
+    auto fetch_p = [&](int k, uint32_t stage, int i) {
+        mu_fetch16(cp + min(k, steps - 1) * step_p, op[i], base + stage + (wave + i * NW) * 1024);
+    };
+    auto fetch_q = [&](int k, uint32_t stage, int i) {
+        mu_fetch16(cq + static_cast<int64_t>(min(k, steps - 1)) * 64, oq[i], base + stage + M::kOperand + (wave + i * NW) * 1024);
+    };
+    // fragments: the lane's addresses in the first stage
+    const int wm = wave / M::kWN, wn = wave % M::kWN;
+    uint32_t pa[4], qa[2];
+    const int sw = (lane >> 2) & 3;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        qa[s] = base + M::kOperand + (wn * 32 * M::NB + (lane & 31)) * 64 + (((2 * s + h) ^ sw) << 4);
+        if constexpr (!TR) pa[s] = base + (wm * 32 * M::MB + (lane & 31)) * 64 + (((2 * s + h) ^ sw) << 4);
+    }
+    if constexpr (TR) {
+        const int gq = lane >> 4, eq = (lane >> 2) & 3;
+#pragma unroll
+        for (int i = 0; i < M::MB; ++i) {
+            const int col = wm * 32 * M::MB + 32 * i + 16 * (gq & 1) + 4 * (lane & 3);
+            pa[i] = base + (8 * h + eq) * kRB + (((col >> 3) ^ mu_swz_tr<T>(eq)) << 4) + (col & 7) * 2;
+        }
+    }
+    struct Frags {
+        u32x4 p[M::MB], q[M::NB];
+    };
+    auto read_q = [&](Frags& f, uint32_t stage, int s, int j) { f.q[j] = mu_lds(qa[s] + stage + j * 2048); };
+    auto read_p = [&](Frags& f, uint32_t stage, int s, int i) {
+        if constexpr (TR) {
+            const u32x2 a = mu_lds_tr(pa[i] + stage + 16 * s * kRB), b = mu_lds_tr(pa[i] + stage + (16 * s + 4) * kRB);
+            f.p[i] = u32x4{a.x, a.y, b.x, b.y};
+        } else {
+            f.p[i] = mu_lds(pa[s] + stage + i * 2048);
+        }
+    };
+    // Half a step: the products of `now`, a row of them at a time, between them the reads of
+    // `next` (all of Q's fragments first, which its first row needs) and, after each row, a
+    // transfer: in a burst after the barrier they held up the products behind them (a wave
+    // issues in order; 256 x 256 tiles, 64 values: 1.20 us in bursts).
+    auto half = [&](const Frags& now, Frags& next, uint32_t stage, int s, auto fetch) {
+        constexpr int kReads = M::NB + M::MB;
+#pragma unroll
+        for (int i = 0; i < M::MB; ++i) {
+#pragma unroll
+            for (int e = i * kReads / M::MB; e < (i + 1) * kReads / M::MB; ++e)
+                if (e < M::NB) read_q(next, stage, s, e);
+                else read_p(next, stage, s, e - M::NB);
+#pragma unroll
+            for (int j = 0; j < M::NB; ++j) acc[i][j] = mfma_f16(now.p[i], now.q[j], acc[i][j]);
+#pragma unroll
+            for (int j = 0; j < M::NB; ++j) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
+                __builtin_amdgcn_sched_group_barrier(0x100, TR ? 2 : 1, 0);  // LDS reads
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            fetch(i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    static_assert(kCount == M::MB, "a transfer of either operand per row of products");
+    Frags f, g;
+#pragma unroll
+    for (int k = 0; k < M::kDepth; ++k) {
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) fetch_p(k, k * M::kStage, i);
+        if (k == M::kDepth - 1) break;
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) fetch_q(k, k * M::kStage, i);
+    }
+    wait_and_sync<(M::kDepth - 2) * kAll + kCount>();
+#pragma unroll
+    for (int j = 0; j < M::NB; ++j) read_q(f, 0, 0, j);
+#pragma unroll
+    for (int i = 0; i < M::MB; ++i) read_p(f, 0, 0, i);
+    uint32_t stage = 0, before = (M::kDepth - 1) * M::kStage;  // of this step and the one before
+    for (int k = 0; k < steps; ++k) {
+        half(f, g, stage, 1, [&](int i) { fetch_q(k + M::kDepth - 1, before, i); });
+        wait_and_sync<(M::kDepth - 2) * kAll>();
+        before = stage;
+        stage = stage == (M::kDepth - 1) * M::kStage ? 0 : stage + M::kStage;
+        // (past the last step: read of no use, in bounds)
+        half(g, f, stage, 0, [&](int i) { fetch_p(k + M::kDepth, before, i); });
+    }
+    wait_and_sync<0>();  // transfers past the end have landed before the stages are reused
+}
+
+// Blocks go round-robin to the 8 XCDs: consecutive tiles on one XCD.
+__device__ __forceinline__ uint32_t mu_swizzle(uint32_t id, uint32_t n) {
+    constexpr uint32_t kX = 8;
+    const uint32_t x = id % kX, q = n / kX, r = n % kX;
+    return x * q + min(x, r) + id / kX;
+}
+
+constexpr int kMuGroup = 4;  // tile rows that consecutive tiles share columns of
+
+// Tile t of the upper triangle (i <= j) of n x n tiles, kMuGroup rows at a time, by columns.
+__device__ __forceinline__ void mu_triangle(uint32_t t, int n, int& i, int& j) {
+    int r = 0;
+    while (true) {
+        const int rows = min(kMuGroup, n - r);
+        const uint32_t count = rows * (rows + 1) / 2 + rows * (n - r - rows);
+        if (t < count) {
+            j = r;
+            while (true) {
+                const uint32_t c = min(rows, j - r + 1);
+                if (t < c) break;
+                t -= c;
+                ++j;
+            }
+            i = r + t;
+            return;
+        }
+        t -= count;
+        r += kMuGroup;
+    }
+}
+
+// 8 consecutive values as fp16, and back.
+__device__ __forceinline__ u32x4 mu_pack(const float* v) {
+    half8 h;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = static_cast<_Float16>(v[e]);
+    return __builtin_bit_cast(u32x4, h);
+}
+__device__ __forceinline__ void mu_unpack(u32x4 w, float* v) {
+    const half8 h = __builtin_bit_cast(half8, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(h[e]);
+}
+
+template <class M>
+__device__ __forceinline__ void mu_zero(f32x16 (&acc)[M::MB][M::NB]) {
+#pragma unroll
+    for (int i = 0; i < M::MB; ++i)
+#pragma unroll
+        for (int j = 0; j < M::NB; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+}
+
+// The wave's part of a tile, through LDS, so that a lane has 8 consecutive rows i of a column j:
+// f(i, j, values, load(i, j)), the loads a batch ahead. Mirror: f's values go back into LDS and
+// from there, turned round, to g(j, i, values): 8 consecutive columns of row i. (Stored from the
+// accumulators, an access of the wave touched 16 bytes of each of 32 lines.) The wave's share of
+// LDS holds up to 64 of its rows at a time, as [j][i] in chunks of 4 values, placed so that
+// neither the accumulators' columns nor the rows that the mirror reads share banks.
+template <class M, bool Mirror, class Load, class Fn, class Gn>
+__device__ __forceinline__ void mu_pieces(const f32x16 (&acc)[M::MB][M::NB], int i0, int j0, uint8_t* lds, Load load, Fn f, Gn g) {
+    constexpr int IP = M::MB >= 2 ? 2 : 1, kI = 32 * IP, kJ = 32 * M::NB, kChunks = kI / 4;
+    constexpr int kLanes = kI / 8, kCols = 64 / kLanes, kBatch = M::MB >= 4 ? 4 : 2;  // lanes per column, columns at a time
+    static_assert(M::kNW * kI * kJ * 4 <= M::kLds && kJ % (kBatch * kCols) == 0, "the waves' shares fit the stages");
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int wm = wave / M::kWN, wn = wave % M::kWN;
+    float* const share = reinterpret_cast<float*>(lds) + wave * kI * kJ;
+    auto at = [&](int i, int j) { return share + j * kI + (((i >> 2) ^ (j ^ j >> 3)) & (kChunks - 1)) * 4 + (i & 3); };
+    const int jb = j0 + wn * kJ, q = (lane % kLanes) * 8, r = lane / kLanes;
+#pragma unroll
+    for (int ip = 0; ip < M::MB / IP; ++ip) {
+        const int ib = i0 + (wm * M::MB + ip * IP) * 32;
+        using Loaded = decltype(load(0, 0));
+        Loaded next[kBatch];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) next[e] = load(ib + q, jb + e * kCols + r);
+#pragma unroll
+        for (int j = 0; j < M::NB; ++j)
+#pragma unroll
+            for (int ii = 0; ii < IP; ++ii)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const f32x16& c = acc[ip * IP + ii][j];
+                    *reinterpret_cast<f32x4*>(at(32 * ii + 8 * v + 4 * (lane >> 5), 32 * j + (lane & 31))) =
+                        f32x4{c[4 * v], c[4 * v + 1], c[4 * v + 2], c[4 * v + 3]};
+                }
+#pragma unroll 1
+        for (int c = 0; c < kJ; c += kBatch * kCols) {
+            Loaded now[kBatch];
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) now[e] = next[e];
+            if (c + kBatch * kCols < kJ)
+#pragma unroll
+                for (int e = 0; e < kBatch; ++e) next[e] = load(ib + q, jb + c + (kBatch + e) * kCols + r);
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+                const int j = c + e * kCols + r;
+                f32x4* const pa = reinterpret_cast<f32x4*>(at(q, j));
+                f32x4* const pb = reinterpret_cast<f32x4*>(at(q + 4, j));
+                const f32x4 a = *pa, b = *pb;
+                float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                f(ib + q, jb + j, v, now[e]);
+                if constexpr (Mirror) {
+                    *pa = f32x4{v[0], v[1], v[2], v[3]};
+                    *pb = f32x4{v[4], v[5], v[6], v[7]};
+                }
+            }
+        }
+        if constexpr (Mirror) {
+            constexpr int kRowLanes = kJ / 8, kRows = 64 / kRowLanes;
+#pragma unroll kBatch
+            for (int i = lane / kRowLanes; i < kI; i += kRows) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = *at(i, (lane % kRowLanes) * 8 + e);
+                g(jb + (lane % kRowLanes) * 8, ib + i, v);
+            }
+        }
+    }
+}
+
+// A = X X^T: tiles of the upper triangle, stored both ways round (sums over k in the same
+// order, so A is symmetric to the bit), 2^8 times; the diagonal in fp32. A contraction in parts
+// leaves each part's fp32 sums for k_mu_join.
+template <int F>
+__global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_gram(MuMatrices l, int src) {
+    using M = MuTiles<F>;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[M::kLds];
+    const uint32_t id = mu_swizzle(blockIdx.x, l.first[l.n]);
+    const int k = mu_find(l, id);
+    const MuMatrix& m = l.d[k];
+    const int nt = (m.mp + M::kT - 1) / M::kT;
+    const uint32_t per = nt * (nt + 1) / 2;
+    uint32_t t = id - l.first[k];
+    const uint32_t b = t / (per * m.parts);
+    t -= b * (per * m.parts);
+    const int part = static_cast<int>(t / per);
+    int ti, tj;
+    mu_triangle(t % per, nt, ti, tj);
+    ti = uniform(ti);
+    tj = uniform(tj);
+    const MuPlace at(m.mp, m.np, m.parts);
+    uint8_t* const w = m.ws + b * m.stride;
+    const uint16_t* x = reinterpret_cast<const uint16_t*>(w + at.hi(src));
+    const int k0 = part * m.steps * 64, steps = min(m.steps, m.np / 64 - part * m.steps);
+    f32x16 acc[M::MB][M::NB];
+    mu_zero<M>(acc);
+    mu_accumulate<M, false>(x, mu_ld(m.np), m.mp, x, mu_ld(m.np), m.mp, ti * M::kT, tj * M::kT, k0, 2 * steps, lds, acc);
+    const int i0 = ti * M::kT, j0 = tj * M::kT;
+    if (m.parts > 1) {
+        float* const o = reinterpret_cast<float*>(w + at.part) + static_cast<int64_t>(part) * m.mp * m.mp;
+        mu_pieces<M, false>(acc, i0, j0, lds, MuNoLoad{}, [&](int i, int j, float* v, MuNone) {
+            if (i >= m.mp || j >= m.mp) return;
+            float* const p = o + static_cast<int64_t>(j) * m.mp + i;
+            *gst<f32x4>(p) = f32x4{v[0], v[1], v[2], v[3]};
+            *gst<f32x4>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+        }, MuNone{});
+        return;
+    }
+    uint16_t* const o = reinterpret_cast<uint16_t*>(w + at.a);
+    float* const d = reinterpret_cast<float*>(w + at.d);
+    const float un = 1.0f / (m.lift * m.lift);  // powers of two: exact
+    const int ld = mu_ld(m.mp);
+    auto store = [&](int i, int j, const float* v) {
+        if (i < m.mp && j < m.mp) *gst<u32x4>(o + static_cast<int64_t>(j) * ld + i) = mu_pack(v);
+    };
+    mu_pieces<M, true>(acc, i0, j0, lds, MuNoLoad{}, [&](int i, int j, float* v, MuNone) {
+        const bool in = j < m.mp;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            v[e] *= un;
+            if (i + e == j && in) stf(d + j, v[e]);
+            v[e] = i + e == j ? 0.0f : v[e] * kMuLift;
+        }
+        store(i, j, v);
+    }, store);
+}
+
+// The sums of A's parts, in order: 4 rows of a column j per thread (of the upper triangle).
+__global__ __launch_bounds__(kMuThreads) void k_mu_join(MuMatrices l) {
+    const int k = mu_find(l, blockIdx.x);
+    const MuMatrix& m = l.d[k];
+    const uint32_t per = static_cast<uint32_t>(m.mp / 4) * m.mp / kMuThreads;  // blocks per matrix (mp is a multiple of 64)
+    const uint32_t item = blockIdx.x - l.first[k], b = item / per;
+    const int64_t q = static_cast<int64_t>(item % per) * kMuThreads + threadIdx.x;
+    const int j = static_cast<int>(q / (m.mp / 4)), i = static_cast<int>(q % (m.mp / 4)) * 4;
+    if (i > j) return;
+    const MuPlace at(m.mp, m.np, m.parts);
+    uint8_t* const w = m.ws + b * m.stride;
+    const float* p = reinterpret_cast<const float*>(w + at.part) + static_cast<int64_t>(j) * m.mp + i;
+    f32x4 s = *gld<f32x4>(p);
+    for (int e = 1; e < m.parts; ++e) s += *gld<f32x4>(p + static_cast<int64_t>(e) * m.mp * m.mp);
+    const float un = 1.0f / (m.lift * m.lift);
+    float v[4] = {s.x * un, s.y * un, s.z * un, s.w * un};
+    float* const d = reinterpret_cast<float*>(w + at.d);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (i + e == j) stf(d + j, v[e]);
+        v[e] *= kMuLift;
+    }
+    uint16_t* const o = reinterpret_cast<uint16_t*>(w + at.a);
+    const int ld = mu_ld(m.mp);
+    // (rows past the diagonal belong to the other half: their values were not summed there)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (i + e > j) break;
+        const uint16_t c = i + e == j ? 0 : __builtin_bit_cast(uint16_t, static_cast<_Float16>(v[e]));
+        *gst<uint16_t>(o + static_cast<int64_t>(j) * ld + i + e) = c;
+        *gst<uint16_t>(o + static_cast<int64_t>(i + e) * ld + j) = c;
+    }
+}
+
+// B = b A + c A^2 from A's off-diagonal part O and its diagonal d, 2^8 times off the diagonal,
+// q = a + B_ii on it.
+template <int F>
+__global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_poly(MuMatrices l, MuPoly p) {
+    using M = MuTiles<F>;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[M::kLds];
+    const uint32_t id = mu_swizzle(blockIdx.x, l.first[l.n]);
+    const int k = mu_find(l, id);
+    const MuMatrix& m = l.d[k];
+    const int nt = (m.mp + M::kT - 1) / M::kT;
+    const uint32_t per = nt * (nt + 1) / 2;
+    const uint32_t t = id - l.first[k], b = t / per;
+    int ti, tj;
+    mu_triangle(t % per, nt, ti, tj);
+    ti = uniform(ti);
+    tj = uniform(tj);
+    const MuPlace at(m.mp, m.np, m.parts);
+    uint8_t* const w = m.ws + b * m.stride;
+    const uint16_t* o = reinterpret_cast<const uint16_t*>(w + at.a);
+    const int ld = mu_ld(m.mp);
+    f32x16 acc[M::MB][M::NB];
+    mu_zero<M>(acc);
+    mu_accumulate<M, false>(o, ld, m.mp, o, ld, m.mp, ti * M::kT, tj * M::kT, 0, m.mp / 32, lds, acc);
+    uint16_t* const out = reinterpret_cast<uint16_t*>(w + at.b);
+    const float* const d = reinterpret_cast<const float*>(w + at.d);
+    float* const q = reinterpret_cast<float*>(w + at.q);
+    auto store = [&](int i, int j, const float* v) {
+        if (i < m.mp && j < m.mp) *gst<u32x4>(out + static_cast<int64_t>(j) * ld + i) = mu_pack(v);
+    };
+    struct Operands {
+        u32x4 o;
+        f32x4 d0, d1;
+        float dj;
+    };
+    mu_pieces<M, true>(acc, ti * M::kT, tj * M::kT, lds, [&](int i, int j) {
+        i = min(i, m.mp - 8);
+        j = min(j, m.mp - 1);
+        return Operands{*gld<u32x4>(o + static_cast<int64_t>(j) * ld + i), *gld<f32x4>(d + i), *gld<f32x4>(d + i + 4), ldf(d + j)};
+    }, [&](int i, int j, float* v, const Operands& z) {
+        if (i >= m.mp || j >= m.mp) return;
+        float x[8];
+        mu_unpack(z.o, x);
+        const float di[8] = {z.d0.x, z.d0.y, z.d0.z, z.d0.w, z.d1.x, z.d1.y, z.d1.z, z.d1.w}, dj = z.dj;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float sq = v[e] * (kMuUnlift * kMuUnlift), a = x[e] * kMuUnlift;
+            if (i + e == j) stf(q + j, p.a + fmaf(p.b, dj, p.c * fmaf(dj, dj, sq)));
+            v[e] = i + e == j ? 0.0f : kMuLift * fmaf(p.b, a, p.c * fmaf(a, di[e] + dj, sq));
+        }
+        store(i, j, v);
+    }, store);
+}
+
+// X' = q X + B X: X^T's tile (rows: X's columns) times B (symmetric: its rows), so that a lane's
+// four values are consecutive in a row of X'. Into the other buffer, and the low part in place;
+// the last step's into the caller's tensors.
+
+// 8 values of the result in a row, from element i on, the first `valid` of them: the
+// parameter's update or the rounded values.
+__device__ __forceinline__ void mu_finish8(const MuTensor& t, const MuLast& z, int64_t i, int valid, float* v) {
+    if (z.update) {
+        float x[8];
+        load_any8(t.x, i, valid, t.xbf16, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = x[e] * z.decay - t.coef * v[e];
+    }
+    store_any8(t.x, i, valid, t.xbf16, v);
+}
+
+template <int F, class Last>
+__global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_apply(MuMatrices l, int src, Last z) {
+    using M = MuTiles<F>;
+    constexpr bool kLast = std::is_same<Last, MuLast>::value;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[M::kLds];
+    const uint32_t id = mu_swizzle(blockIdx.x, l.first[l.n]);
+    const int k = mu_find(l, id);
+    const MuMatrix& m = l.d[k];
+    const uint32_t tm = (m.mp + M::kT - 1) / M::kT, tn = (m.np + M::kT - 1) / M::kT, per = tm * tn;
+    uint32_t t = id - l.first[k];
+    const uint32_t b = t / per;
+    t -= b * per;
+    // kMuGroup rows of X' at a time, by columns
+    const uint32_t g = t / (kMuGroup * tn), rows = min<uint32_t>(kMuGroup, tm - g * kMuGroup);
+    t -= g * kMuGroup * tn;
+    const int ti = uniform(static_cast<int>(t / rows)), tj = uniform(static_cast<int>(g * kMuGroup + t % rows));
+    const MuPlace at(m.mp, m.np, m.parts);
+    uint8_t* const w = m.ws + b * m.stride;
+    const uint16_t* const x = reinterpret_cast<const uint16_t*>(w + at.hi(src));
+    uint16_t* const lo = reinterpret_cast<uint16_t*>(w + at.lo);
+    const int ld = mu_ld(m.np);
+    f32x16 acc[M::MB][M::NB];
+    mu_zero<M>(acc);
+    mu_accumulate<M, true>(x, ld, m.np, reinterpret_cast<const uint16_t*>(w + at.b), mu_ld(m.mp), m.mp, ti * M::kT, tj * M::kT, 0,
+                           m.mp / 32, lds, acc);
+    const float* const q = reinterpret_cast<const float*>(w + at.q);
+    uint16_t* const hi = reinterpret_cast<uint16_t*>(w + at.hi(src ^ 1));
+    const float un = 1.0f / m.lift;
+    struct Operands {
+        u32x4 hi, lo;
+        float q;
+    };
+    auto load = [&](int i, int j) {
+        i = min(i, m.np - 8);
+        j = min(j, m.mp - 1);
+        const int64_t p = static_cast<int64_t>(j) * ld + i;
+        return Operands{*gld<u32x4>(x + p), *gld<u32x4>(lo + p), ldf(q + j)};
+    };
+    auto result = [&](const Operands& z, float* v) {  // 8 columns of X'
+        float xh[8], xl[8];
+        mu_unpack(z.hi, xh);
+        mu_unpack(z.lo, xl);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(z.q, xh[e] + xl[e], v[e] * kMuUnlift);
+    };
+    if constexpr (kLast) {
+        const MuTensor& c = z.t.d[k];
+        const int64_t base = b * (static_cast<int64_t>(c.rows) * c.ldx);
+        if (c.tall) {  // row j of X' is column j of the caller's matrix
+            mu_pieces<M, true>(acc, ti * M::kT, tj * M::kT, lds, load, [&](int, int, float* v, const Operands& o) {
+                result(o, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= un;
+            }, [&](int j, int i, float* v) {
+                const int valid = i < c.rows ? clamp_valid(static_cast<int64_t>(c.cols) - j) : 0;
+                if (valid > 0) mu_finish8(c, z, base + i * c.ldx + j, valid, v);
+            });
+        } else {
+            mu_pieces<M, false>(acc, ti * M::kT, tj * M::kT, lds, load, [&](int i, int j, float* v, const Operands& o) {
+                const int valid = j < c.rows ? clamp_valid(static_cast<int64_t>(c.cols) - i) : 0;
+                if (valid == 0) return;
+                result(o, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= un;
+                mu_finish8(c, z, base + j * c.ldx + i, valid, v);
+            }, MuNone{});
+        }
+    } else {
+        mu_pieces<M, false>(acc, ti * M::kT, tj * M::kT, lds, load, [&](int i, int j, float* v, const Operands& o) {
+            if (i >= m.np || j >= m.mp) return;
+            const int64_t p = static_cast<int64_t>(j) * ld + i;
+            result(o, v);
+            const u32x4 h = mu_pack(v);
+            float r[8];
+            mu_unpack(h, r);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[e] = v[e] - r[e];
+            *gst<u32x4>(hi + p) = h;
+            *gst<u32x4>(lo + p) = mu_pack(r);
+        }, MuNone{});
+    }
+}
+
+}  // namespace
+
+void launch_mu_momentum(const MuTensors& t, const MuStepArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL(k_mu_momentum, dim3(t.first[t.n]), dim3(kMuThreads), 0, s, t, a);
+}
+
+void launch_mu_scatter(const MuTensors& t, const MuStepArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL(k_mu_scatter, dim3(t.first[t.n]), dim3(kMuThreads), 0, s, t, a);
+}
+
+void launch_mu_gram(const MuMatrices& m, int form, int src, hipStream_t s) {
+    const dim3 g(m.first[m.n]), t(kMuFormThreads[form]);
+    if (form == kMuLarge) hipLaunchKernelGGL(k_mu_gram<kMuLarge>, g, t, 0, s, m, src);
+    else if (form == kMuMedium) hipLaunchKernelGGL(k_mu_gram<kMuMedium>, g, t, 0, s, m, src);
+    else hipLaunchKernelGGL(k_mu_gram<kMuSmall>, g, t, 0, s, m, src);
+}
+
+void launch_mu_join(const MuMatrices& m, hipStream_t s) {
+    hipLaunchKernelGGL(k_mu_join, dim3(m.first[m.n]), dim3(kMuThreads), 0, s, m);
+}
+
+void launch_mu_poly(const MuMatrices& m, int form, const MuPoly& p, hipStream_t s) {
+    const dim3 g(m.first[m.n]), t(kMuFormThreads[form]);
+    if (form == kMuLarge) hipLaunchKernelGGL(k_mu_poly<kMuLarge>, g, t, 0, s, m, p);
+    else if (form == kMuMedium) hipLaunchKernelGGL(k_mu_poly<kMuMedium>, g, t, 0, s, m, p);
+    else hipLaunchKernelGGL(k_mu_poly<kMuSmall>, g, t, 0, s, m, p);
+}
+
+template <class Last>
+static void launch_apply(const MuMatrices& m, int form, int src, const Last& z, hipStream_t s) {
+    const dim3 g(m.first[m.n]), t(kMuFormThreads[form]);
+    if (form == kMuLarge) hipLaunchKernelGGL((k_mu_apply<kMuLarge, Last>), g, t, 0, s, m, src, z);
+    else if (form == kMuMedium) hipLaunchKernelGGL((k_mu_apply<kMuMedium, Last>), g, t, 0, s, m, src, z);
+    else hipLaunchKernelGGL((k_mu_apply<kMuSmall, Last>), g, t, 0, s, m, src, z);
+}
+
+void launch_mu_apply(const MuMatrices& m, int form, int src, const MuLast* last, hipStream_t s) {
+    if (last) launch_apply(m, form, src, *last, s);
+    else launch_apply(m, form, src, MuNone{}, s);
+}
+
+}  // namespace meo

@@ -19,10 +19,10 @@ from ._lib import MX4Tensor
 __all__ = ["MX4Tensor", "mx4_quantize", "mx4_dequantize", "mx4_matmul"]
 
 
-def _call(device: torch.device, fn, *args) -> None:
+def _call(device: torch.device, fn, *args, what: str = "MX4 operators need tensors") -> None:
     """fn on the current stream of `device`, made current for the call if it is not."""
     if device.type != "cuda":
-        raise ValueError("MX4 operators need tensors on a GPU")
+        raise ValueError(f"{what} on a GPU")
     if device.index == torch.cuda.current_device():
         fn(*args)
     else:

@@ -1,4 +1,4 @@
-"""torch.optim front ends over the C ABI: Adafactor, CAME, Lamb and GaLoreAdamW.
+"""torch.optim front ends over the C ABI: Adafactor, CAME, Lamb, GaLoreAdamW and Muon.
 
 Each class owns its state tensors (on the parameter's device, named as on the
 Colossal-AI distributed-optimizers page: ``step``, ``exp_avg``,
@@ -42,7 +42,8 @@ def moment_dtype(optimizer: str, shape, requested: Optional[torch.dtype], param_
     (bfloat16 -> bfloat16, else float32). int8 applies to tensors of at least
     ``min_8bit_size`` elements (the GaLore section's 8-bit optimizer default: smaller
     ones stay 32-bit) whose rows hold whole groups of 128 when the statistics are
-    factored (Adafactor and CAME with ndim >= 2); other tensors get float32."""
+    factored (Adafactor and CAME with ndim >= 2), and for Muon whose matrices hold whole
+    groups when there are several; other tensors get float32."""
     if requested is None:
         return torch.bfloat16 if param_dtype == torch.bfloat16 else torch.float32
     if requested != torch.int8:
@@ -51,8 +52,10 @@ def moment_dtype(optimizer: str, shape, requested: Optional[torch.dtype], param_
     n = 1
     for d in shape:
         n *= d
-    factored = optimizer != "lamb" and len(shape) >= 2
+    factored = optimizer not in ("lamb", "muon") and len(shape) >= 2
     if n < min_8bit_size or (factored and shape[-1] % _lib.I8_GROUP != 0):
+        return torch.float32
+    if optimizer == "muon" and len(shape) > 2 and n != shape[-2] * shape[-1] and shape[-2] * shape[-1] % _lib.I8_GROUP:
         return torch.float32
     return torch.int8
 
@@ -524,3 +527,89 @@ class GaLoreAdamW(_MeoOptimizer):
             return
         ws = self._ws(_lib.meo_galore_workspace_size(hp, ps, gs), ps[0].device)
         _lib.meo_galore_step(hp, step, ps, gs, ss, ws)
+
+
+class Muon(_MeoOptimizer):
+    """Muon: each matrix steps along its momentum, orthogonalized by Newton-Schulz steps
+    (``orthogonalize``; the arithmetic and its precision are described in meo.h):
+
+        exp_avg <- momentum exp_avg + (1 - momentum) grad
+        u = (1 - momentum) grad + momentum exp_avg with nesterov, else exp_avg
+        p <- p (1 - lr weight_decay) - lr s orthogonalize(u)
+
+    with s = sqrt(max(1, rows / cols)) for ``adjust_lr="original"`` and 0.2 sqrt(max(rows, cols))
+    for ``"match_rms_adamw"`` (updates of AdamW's size: its lr and weight decay can be kept). A
+    parameter with more than two dims is a batch of matrices (its last two dims); a
+    convolution's weight is viewed as a matrix by the caller. ``ns_coefficients``: one (a, b, c)
+    for all ``ns_steps``, or one for each.
+
+    Muon is for hidden matrices. A parameter group with ``muon=False`` (embeddings, the output
+    layer) and parameters with fewer than two dims take AdamW with the group's lr,
+    weight_decay, ``betas`` and ``adamw_eps``, float32 states ``exp_avg`` and ``exp_avg_sq``.
+
+    ``state_dtype``: element type of Muon's ``exp_avg`` (None: that of the parameter;
+    torch.int8: 8-bit where ``moment_dtype`` allows, with ``min_8bit_size``)."""
+
+    _kind = "muon"
+
+    def __init__(self, params, lr=1e-3, momentum=0.95, weight_decay=0.1, nesterov=True, adjust_lr="original",
+                 ns_steps=5, ns_coefficients=_lib.NS_COEFFICIENTS, eps=1e-7, betas=(0.9, 0.999), adamw_eps=1e-8,
+                 state_dtype=None, min_8bit_size=4096):
+        defaults = dict(lr=lr, momentum=momentum, weight_decay=weight_decay, nesterov=nesterov, adjust_lr=adjust_lr,
+                        ns_steps=ns_steps, ns_coefficients=ns_coefficients, eps=eps, betas=betas,
+                        adamw_eps=adamw_eps, muon=True)
+        super().__init__(params, defaults, state_dtype, min_8bit_size)
+
+    def add_param_group(self, param_group) -> None:
+        """As torch's, with the group's hyperparameters checked."""
+        g = {**self.defaults, **param_group}
+        if not g["lr"] >= 0.0:
+            raise ValueError(f"Invalid learning rate: {g['lr']}")
+        if not 0.0 <= g["momentum"] < 1.0:
+            raise ValueError(f"Invalid momentum value: {g['momentum']}")
+        for name in ("eps", "adamw_eps"):
+            if not g[name] >= 0.0:
+                raise ValueError(f"Invalid epsilon value: {g[name]}")
+        for i, b in enumerate(g["betas"]):
+            if not 0.0 <= b < 1.0:
+                raise ValueError(f"Invalid beta parameter at index {i}: {b}")
+        if not 1 <= g["ns_steps"] <= _lib.MEO_NS_MAX_STEPS:
+            raise ValueError(f"ns_steps must be 1 to {_lib.MEO_NS_MAX_STEPS}")
+        self._muon_hp(g)  # the rest
+        super().add_param_group(param_group)
+
+    @staticmethod
+    def _muon_hp(group):
+        return _lib.muon_hparams(**{k: group[k] for k in ("lr", "momentum", "weight_decay", "nesterov", "adjust_lr",
+                                                          "ns_steps", "ns_coefficients", "eps")})
+
+    @staticmethod
+    def _matrix(p: torch.Tensor, group) -> bool:
+        return bool(group["muon"]) and p.dim() >= 2
+
+    def _state_for(self, p, group):
+        if self._matrix(p, group):
+            return _lib.init_state("muon", p, state_dtype=self._moment_dtype(p))
+        return {k: torch.zeros(p.shape, dtype=torch.float32, device=p.device) for k in ("exp_avg", "exp_avg_sq")}
+
+    def _wsize(self, params, grads):
+        return 0  # computed in _call, where the group is known
+
+    def _call(self, group, step, params, grads, states, ws):
+        muon = [self._matrix(p, group) for p in params]
+        hp = self._muon_hp(group)
+        flat = _lib.galore_hparams(lr=group["lr"], betas=group["betas"], eps=group["adamw_eps"],
+                                   weight_decay=group["weight_decay"])
+        mats = [[v for v, m in zip(vs, muon) if m] for vs in (params, grads, states)]
+        # the others as flat views, which GaLore's step takes AdamW on
+        rest = [[p.view(-1) for p, m in zip(params, muon) if not m],
+                [g.reshape(-1) for g, m in zip(grads, muon) if not m],
+                [{k: st[k].view(-1) for k in ("exp_avg", "exp_avg_sq")} for st, m in zip(states, muon) if not m]]
+        # both calls are checked before either is made: a step that is refused changes nothing
+        _lib.meo_muon_validate(hp, step, *mats)
+        _lib.meo_galore_validate(flat, step, *rest)
+        if mats[0]:
+            ws = self._ws(_lib.meo_muon_workspace_size(hp, *mats), mats[0][0].device)
+            _lib.meo_muon_step(hp, step, *mats, ws)
+        if rest[0]:
+            _lib.meo_galore_step(flat, step, *rest)
