@@ -650,8 +650,8 @@ int32_t meo_mx4_matmul_rows(int64_t m, int64_t n);
  *
  * Precision. Products are fp16 with float32 sums; the iterate itself is held in 22 bits and the
  * diagonals of A and of b A + c A^2 in float32. The result is within about 1e-3 (relative, in
- * the Frobenius norm) of the exact polynomial's, for matrices of any conditioning; a bfloat16
- * result is rounded once, to nearest even. Values are held times powers of two; a result whose
+ * the Frobenius norm; 2e-3 for the smallest matrices) of the exact polynomial's, at any
+ * conditioning; a bfloat16 result is rounded once, to nearest even. Values are held times powers of two; a result whose
  * entries are below about 2^-24 of those of a matrix with orthonormal rows (eps far above |U|)
  * loses them.
  *

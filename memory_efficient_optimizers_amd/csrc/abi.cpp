@@ -2917,7 +2917,6 @@ int mu_run(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, MuS
         MuMatrices all;
         std::memset(&all, 0, sizeof all);
         t.n = all.n = static_cast<int32_t>(c.items.size());
-        bool split = false;
         for (int i = 0; i < t.n; ++i) {
             const MuItem& it = c.items[i];
             const MuIn& in = ts[it.k];
@@ -2955,26 +2954,25 @@ int mu_run(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, MuS
             mu_gram_parts(m.mp, m.np, &parts, &steps);
             m.parts = static_cast<int32_t>(parts);
             m.steps = static_cast<int32_t>(steps);
-            split = split || parts > 1;
         }
         auto count = [&](auto& l, auto blocks) {
-            uint32_t n = 0;
-            for (int i = 0; i < l.n; ++i) {
-                l.first[i] = n;
-                n += static_cast<uint32_t>(blocks(l.d[i]));
+            l.blocks = 0;
+            for (int i = 0; i < kMuBatch; ++i) {
+                l.first[i] = i < l.n ? l.blocks : 0xffffffffu;
+                if (i < l.n) l.blocks += static_cast<uint32_t>(blocks(l.d[i]));
             }
-            l.first[l.n] = n;
         };
         auto square = [](int64_t side, int64_t tile) { const int64_t q = ceil_div(side, tile); return q * (q + 1) / 2; };
         const int fg = mu_form(ts, c, [&](const MuIn& q, int64_t tile) {
             int64_t parts, steps;
             mu_gram_parts(q.mp(), q.np(), &parts, &steps);
-            return square(q.mp(), tile) * parts;
+            return parts > 1 ? 0 : square(q.mp(), tile);
         });
         const int fp = mu_form(ts, c, [&](const MuIn& q, int64_t tile) { return square(q.mp(), tile); });
         const int fa = mu_form(ts, c, [&](const MuIn& q, int64_t tile) { return ceil_div(q.mp(), tile) * ceil_div(q.np(), tile); });
-        MuMatrices gram = all, join = all, poly = all, apply = all;
-        count(gram, [&](const MuMatrix& m) { return m.batch * square(m.mp, kMuFormTile[fg]) * m.parts; });
+        MuMatrices gram = all, parts = all, join = all, poly = all, apply = all;
+        count(gram, [&](const MuMatrix& m) { return m.parts > 1 ? 0 : m.batch * square(m.mp, kMuFormTile[fg]); });
+        count(parts, [&](const MuMatrix& m) { return m.parts > 1 ? m.batch * square(m.mp, kMuFormTile[kMuSmall]) * m.parts : 0; });
         count(join, [&](const MuMatrix& m) { return m.parts > 1 ? m.batch * (int64_t{m.mp} / 4 * m.mp / kMuThreads) : 0; });
         count(poly, [&](const MuMatrix& m) { return m.batch * square(m.mp, kMuFormTile[fp]); });
         count(apply, [&](const MuMatrix& m) { return m.batch * ceil_div(m.mp, kMuFormTile[fa]) * ceil_div(m.np, kMuFormTile[fa]); });
@@ -2988,11 +2986,12 @@ int mu_run(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, MuS
             const MuPoly p{static_cast<float>(hp.coefficients[k][0]), static_cast<float>(hp.coefficients[k][1]),
                            static_cast<float>(hp.coefficients[k][2])};
             launch_mu_gram(gram, fg, k & 1, s);
-            if (split) launch_mu_join(join, s);
+            launch_mu_gram(parts, kMuSmall, k & 1, s);
+            launch_mu_join(join, s);
             pt.mark(kPassMuGram);
             launch_mu_poly(poly, fp, p, s);
             pt.mark(kPassMuPoly);
-            launch_mu_apply(apply, fa, k & 1, k + 1 == hp.steps ? &last : nullptr, s);
+            launch_mu_apply(apply, fa, k & 1, p.a, k + 1 == hp.steps ? &last : nullptr, s);
             pt.mark(kPassMuApply);
         }
     }

@@ -361,7 +361,7 @@ __device__ __forceinline__ float dpp(float v) {
     return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, false));
 }
 
-__device__ __forceinline__ float group_max8(const float* m) {
+__device__ __forceinline__ void quant_i8x8(float* m, uint32_t& lo, uint32_t& hi, float& scale) {
     float a = 0.0f;
 #pragma unroll
     for (int e = 0; e < kVec; ++e) a = max_nan(a, fabsf(m[e]));
@@ -370,10 +370,8 @@ __device__ __forceinline__ float group_max8(const float* m) {
     a = max_nan(a, dpp<0xb1>(a));   // quad_perm [1, 0, 3, 2]
     a = max_nan(a, dpp<0x4e>(a));   // quad_perm [2, 3, 0, 1]
     a = max_nan(a, dpp<0x141>(a));  // row_half_mirror
-    return max_nan(a, dpp<0x140>(a));  // row_mirror
-}
-
-__device__ __forceinline__ void quant_by_scale8(float* m, uint32_t& lo, uint32_t& hi, float& scale) {
+    a = max_nan(a, dpp<0x140>(a));  // row_mirror
+    scale = a / 127.0f;
     const bool ok = scale > 0.0f && scale <= 3.402823466e38f;  // finite and nonzero
     if (!(scale <= 3.402823466e38f)) scale = __builtin_nanf("");
     lo = 0u;
@@ -386,11 +384,6 @@ __device__ __forceinline__ void quant_by_scale8(float* m, uint32_t& lo, uint32_t
         if (e < 4) lo |= byte << (8 * e); else hi |= byte << (8 * (e - 4));
         m[e] = q * scale;  // a zero scale reads back 0, a NaN one NaN
     }
-}
-
-__device__ __forceinline__ void quant_i8x8(float* m, uint32_t& lo, uint32_t& hi, float& scale) {
-    scale = group_max8(m) / 127.0f;
-    quant_by_scale8(m, lo, hi, scale);
 }
 
 // Stores the codes of quant_i8x8 at element i (the `valid` first of 8) and, from

@@ -41,14 +41,19 @@ struct MuMatrix {
     float lift;            // 2^lift
 };
 
-template <class T>
-struct MuList {
+// The blocks of a launch, by tensor: those before tensor i > 0 in first[i] (past the last one
+// nothing is reached: 2^32 - 1), all in `blocks`. N = 1: one tensor alone (kernels are compiled for
+// it too, see mu_find).
+template <class T, int N>
+struct MuListOf {
     int32_t n;
-    uint32_t first[kMuBatch + 1];  // blocks before each tensor; [n]: all
-    T d[kMuBatch];
+    uint32_t blocks;
+    uint32_t first[N];
+    T d[N];
+    MuListOf<T, 1> only() const { return MuListOf<T, 1>{1, blocks, {0}, {d[0]}}; }
 };
-using MuTensors = MuList<MuTensor>;
-using MuMatrices = MuList<MuMatrix>;
+using MuTensors = MuListOf<MuTensor, kMuBatch>;
+using MuMatrices = MuListOf<MuMatrix, kMuBatch>;
 
 // Values between rows of a matrix in the workspace, its columns a multiple of 64: an odd
 // multiple, so that the same columns of consecutive rows lie in different channels of the L2
@@ -89,20 +94,23 @@ enum MuForm { kMuSmall = 0, kMuMedium, kMuLarge, kMuForms };
 constexpr int kMuFormTile[kMuForms] = {64, 128, 256};
 constexpr int kMuFormThreads[kMuForms] = {256, 256, 256};
 
-struct MuLast {       // the last step's results go to the caller's tensors
-    MuTensors t;
+template <int N>
+struct MuLastOf {     // the last step's results go to the caller's tensors
+    MuListOf<MuTensor, N> t;
     float decay;      // 1 - lr wd
     int32_t update;   // a parameter's update (else bf16 results)
 };
+using MuLast = MuLastOf<kMuBatch>;
 
 void launch_mu_momentum(const MuTensors& t, const MuStepArgs& a, hipStream_t s);
 void launch_mu_scatter(const MuTensors& t, const MuStepArgs& a, hipStream_t s);
-// A's off-diagonal part and diagonal from X (buffer src); with parts, their sums and the join.
+// A's off-diagonal part and diagonal from X (buffer src); with parts (kMuSmall only), their sums
+// and the join.
 void launch_mu_gram(const MuMatrices& m, int form, int src, hipStream_t s);
 void launch_mu_join(const MuMatrices& m, hipStream_t s);
 // B = b A + c A^2 off the diagonal, a + B_ii on it.
 void launch_mu_poly(const MuMatrices& m, int form, const MuPoly& p, hipStream_t s);
-// X' = (a + B_ii) X + B X, into the other buffer or, `last` given, the caller's tensors.
-void launch_mu_apply(const MuMatrices& m, int form, int src, const MuLast* last, hipStream_t s);
+// X' = a X + B X, into the other buffer or, `last` given, the caller's tensors. linear: a.
+void launch_mu_apply(const MuMatrices& m, int form, int src, float linear, const MuLast* last, hipStream_t s);
 
 }  // namespace meo

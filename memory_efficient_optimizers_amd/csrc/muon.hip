@@ -6,7 +6,11 @@
 // bf16 would be 2^-9 at the same rate) and why that is enough:
 //   * X as an operand. The linear term, which alone carries the small singular values, takes X
 //     as the sum of two fp16 parts (hi + lo, 22 bits): with hi alone a matrix of rank 8 plus 1%
-//     noise came out 3.7e-2 off, so 9e-4.
+//     noise came out 3.7e-2 off, so 4e-4. B takes hi only; the diagonal of B takes lo as well
+//     as far as the row's norm is that of a finished matrix (B_ii min(1, d_i^2)). Where singular
+//     values are all near 1 that is most of what B lo is (gaussian 256 x 256: 9.6e-4 off, without
+//     it 1.3e-3); where few are, it would add a noise of full rank (16 x 16, rank 1 plus 1e-4 noise:
+//     1.5e-2 with B_ii lo whole, 1.7e-3 so).
 //   * A and B = b A + c A^2 off their diagonals. The diagonals, which near the end are most of
 //     A, are held in fp32 (d, and q = a + B_ii) and enter by row: (A^2)_ij = (O^2)_ij +
 //     O_ij (d_i + d_j) off the diagonal, with O the rest of A. That halves the error of
@@ -23,9 +27,6 @@ namespace {
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 
 struct MuNone {};
-struct MuNoLoad {
-    __device__ MuNone operator()(int, int) const { return {}; }
-};
 
 constexpr float kMuLift = 256.0f;        // of O and B
 constexpr float kMuUnlift = 1.0f / 256;
@@ -34,12 +35,19 @@ __device__ __forceinline__ f32x16 mfma_f16(const u32x4& a, const u32x4& b, const
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
 }
 
-// The tensor of block `id`, whose blocks the list counts in order.
-template <class L>
-__device__ __forceinline__ int mu_find(const L& l, uint32_t id) {
-    int i = 0;
-    while (i + 1 < l.n && id >= l.first[i + 1]) ++i;
-    return i;
+// The tensor of block `id`. Kernel arguments are a microsecond away, so all counts are read at
+// once, and a tensor alone (N = 1) needs none.
+template <class T, int N>
+__device__ __forceinline__ int mu_find(const MuListOf<T, N>& l, uint32_t id) {
+    int k = 0;
+#pragma unroll
+    for (int i = 1; i < N; ++i) k += id >= l.first[i];
+    return k;
+}
+// Its number among the tensor's blocks.
+template <class T, int N>
+__device__ __forceinline__ uint32_t mu_item(const MuListOf<T, N>& l, int k, uint32_t id) {
+    return N == 1 ? id : id - l.first[k];
 }
 
 // ----------------------------------------------------------------------------- the caller's tensors
@@ -91,6 +99,28 @@ __device__ __forceinline__ void mu_load_m(const MuTensor& t, int64_t i, int vali
         f[e] = static_cast<float>(static_cast<int8_t>(w[e >> 2] >> (8 * (e & 3)))) * (((i + e) >> 7) == (i >> 7) ? s0 : s1);
 }
 
+// As quant_i8x8, with the scale as max|m| times 1/127: no division before the codes' own.
+__device__ __forceinline__ void mu_quantize8(float* m, uint32_t& lo, uint32_t& hi, float& scale) {
+    float a = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) a = max_nan(a, fabsf(m[e]));
+    a = max_nan(a, dpp<0xb1>(a));   // over the 16 lanes of a group: swap neighbours,
+    a = max_nan(a, dpp<0x4e>(a));   // swap pairs,
+    a = max_nan(a, dpp<0x141>(a));  // mirror halves,
+    a = max_nan(a, dpp<0x140>(a));  // mirror the row
+    scale = a * (1.0f / 127.0f);
+    const bool ok = scale > 0.0f && scale <= 3.402823466e38f;  // finite and nonzero
+    if (!(scale <= 3.402823466e38f)) scale = __builtin_nanf("");
+    lo = hi = 0u;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+        const float q = fminf(fmaxf(ok ? rintf(m[e] / scale) : 0.0f, -128.0f), 127.0f);
+        const uint32_t byte = static_cast<uint32_t>(static_cast<int32_t>(q)) & 0xffu;
+        if (e < 4) lo |= byte << (8 * e); else hi |= byte << (8 * (e - 4));
+        m[e] = q * scale;
+    }
+}
+
 // The direction from the gradient and the stored momentum.
 __device__ __forceinline__ void mu_direction(const MuStepArgs& a, const float* g, const float* m, float* u) {
 #pragma unroll
@@ -100,11 +130,12 @@ __device__ __forceinline__ void mu_direction(const MuStepArgs& a, const float* g
 // The momentum's update and the sum of squares of the direction, in fp64 (the squares of any
 // fp32 value neither vanish nor overflow). One block per part of a matrix; parts are joined by
 // every block of the next pass, in order.
-__global__ __launch_bounds__(kMuThreads) void k_mu_momentum(MuTensors l, MuStepArgs a) {
+template <int N>
+__global__ __launch_bounds__(kMuThreads) void k_mu_momentum(MuListOf<MuTensor, N> l, MuStepArgs a) {
     __shared__ double sums[kMuThreads / 64];
     const int k = mu_find(l, blockIdx.x);
     const MuTensor& t = l.d[k];
-    const uint32_t item = blockIdx.x - l.first[k];
+    const uint32_t item = mu_item(l, k, blockIdx.x);
     const int b = static_cast<int>(item / t.parts), part = static_cast<int>(item % t.parts);
     const int64_t size = static_cast<int64_t>(t.rows) * t.cols, base = b * size;
     const int64_t i0 = part * t.tiles_per_part * kMuPart, i1 = min(size, i0 + t.tiles_per_part * kMuPart);
@@ -123,8 +154,8 @@ __global__ __launch_bounds__(kMuThreads) void k_mu_momentum(MuTensors l, MuStepA
             for (int e = 0; e < kVec; ++e) m[e] = m[e] * a.beta + g[e] * a.omb;
             if (t.mkind == 2) {
                 uint32_t lo, hi;
-                float scale = group_max8(m) * (1.0f / 127.0f);
-                quant_by_scale8(m, lo, hi, scale);
+                float scale;
+                mu_quantize8(m, lo, hi, scale);
                 store_i8x8(t.m, t.ms, base + i, valid, (reinterpret_cast<uintptr_t>(t.m) & 7) == 0, lo, hi, scale);
             } else if (valid > 0) {
                 if (t.mkind == 1)
@@ -168,12 +199,13 @@ __device__ __forceinline__ void mu_split(float v, uint32_t& hi, uint32_t& lo) {
 
 // The directions, scaled, into the workspace: a square tile of the padded matrix per block,
 // zeros outside the matrix. A tall matrix is transposed on the way, through LDS.
-__global__ __launch_bounds__(kMuThreads) void k_mu_scatter(MuTensors l, MuStepArgs a) {
+template <int N>
+__global__ __launch_bounds__(kMuThreads) void k_mu_scatter(MuListOf<MuTensor, N> l, MuStepArgs a) {
     __shared__ double sums[kMuThreads / 64 + 1];
     __shared__ float tile[kMuTile][kMuTile + 1];
     const int k = mu_find(l, blockIdx.x);
     const MuTensor& t = l.d[k];
-    const uint32_t item = blockIdx.x - l.first[k];
+    const uint32_t item = mu_item(l, k, blockIdx.x);
     const uint32_t tn = t.np / kMuTile, per = tn * (t.mp / kMuTile);
     const int b = static_cast<int>(item / per);
     const int r0 = static_cast<int>(item % per / tn) * kMuTile, c0 = static_cast<int>(item % per % tn) * kMuTile;
@@ -285,6 +317,8 @@ __device__ __forceinline__ void mu_accumulate(const uint16_t* P, int ldp, int ro
     constexpr int T = M::kT, NW = M::kNW, kRB = T * 2, kCount = T / 16 / NW, kAll = 2 * kCount;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
     const uint32_t base = uniform(static_cast<int>(lds_addr(lds)));
+    steps = uniform(steps);  // (the transfers' addresses and counts stay in scalar registers)
+    ldp = uniform(ldp);
     // transfers: 1 KB each, kCount of either operand per wave. Chunk c of row r (64 bytes) lies
     // at position c ^ (r >> 2 & 3): 16 rows read at one chunk then touch every bank once.
     uint32_t op[kCount], oq[kCount];
@@ -314,11 +348,15 @@ __device__ __forceinline__ void mu_accumulate(const uint16_t* P, int ldp, int ro
         }
     }
     const int64_t step_p = TR ? static_cast<int64_t>(ldp) * 64 : 64;
-    auto fetch_p = [&](int k, uint32_t stage, int i) {
-        mu_fetch16(cp + min(k, steps - 1) * step_p, op[i], base + stage + (wave + i * NW) * 1024);
+    // The i-th transfer of an operand's next step.
+    int next_p = 1, next_q = 1;
+    auto fetch_p = [&](uint32_t stage, int i) {
+        mu_fetch16(cp, op[i], base + stage + (wave + i * NW) * 1024);
+        if (i == kCount - 1) cp += next_p++ < steps ? step_p : 0;
     };
-    auto fetch_q = [&](int k, uint32_t stage, int i) {
-        mu_fetch16(cq + static_cast<int64_t>(min(k, steps - 1)) * 64, oq[i], base + stage + M::kOperand + (wave + i * NW) * 1024);
+    auto fetch_q = [&](uint32_t stage, int i) {
+        mu_fetch16(cq, oq[i], base + stage + M::kOperand + (wave + i * NW) * 1024);
+        if (i == kCount - 1) cq += next_q++ < steps ? 64 : 0;
     };
     // fragments: the lane's addresses in the first stage
     const int wm = wave / M::kWN, wn = wave % M::kWN;
@@ -378,10 +416,10 @@ __device__ __forceinline__ void mu_accumulate(const uint16_t* P, int ldp, int ro
 #pragma unroll
     for (int k = 0; k < M::kDepth; ++k) {
 #pragma unroll
-        for (int i = 0; i < kCount; ++i) fetch_p(k, k * M::kStage, i);
+        for (int i = 0; i < kCount; ++i) fetch_p(k * M::kStage, i);
         if (k == M::kDepth - 1) break;
 #pragma unroll
-        for (int i = 0; i < kCount; ++i) fetch_q(k, k * M::kStage, i);
+        for (int i = 0; i < kCount; ++i) fetch_q(k * M::kStage, i);
     }
     wait_and_sync<(M::kDepth - 2) * kAll + kCount>();
 #pragma unroll
@@ -390,12 +428,12 @@ __device__ __forceinline__ void mu_accumulate(const uint16_t* P, int ldp, int ro
     for (int i = 0; i < M::MB; ++i) read_p(f, 0, 0, i);
     uint32_t stage = 0, before = (M::kDepth - 1) * M::kStage;  // of this step and the one before
     for (int k = 0; k < steps; ++k) {
-        half(f, g, stage, 1, [&](int i) { fetch_q(k + M::kDepth - 1, before, i); });
+        half(f, g, stage, 1, [&](int i) { fetch_q(before, i); });
         wait_and_sync<(M::kDepth - 2) * kAll>();
         before = stage;
         stage = stage == (M::kDepth - 1) * M::kStage ? 0 : stage + M::kStage;
         // (past the last step: read of no use, in bounds)
-        half(g, f, stage, 0, [&](int i) { fetch_p(k + M::kDepth, before, i); });
+        half(g, f, stage, 0, [&](int i) { fetch_p(before, i); });
     }
     wait_and_sync<0>();  // transfers past the end have landed before the stages are reused
 }
@@ -431,17 +469,17 @@ __device__ __forceinline__ void mu_triangle(uint32_t t, int n, int& i, int& j) {
     }
 }
 
-// 8 consecutive values as fp16, and back.
-__device__ __forceinline__ u32x4 mu_pack(const float* v) {
-    half8 h;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = static_cast<_Float16>(v[e]);
-    return __builtin_bit_cast(u32x4, h);
+// Four consecutive values as fp16, and one of such a word pair. The values are rounded to fp32
+// first: an instruction that multiplies, adds and rounds to fp16 at once, which the compiler takes
+// in some variants of a kernel and not in others, made results depend on the tile form.
+__device__ __forceinline__ u32x2 mu_pack4(float a, float b, float c, float d) {
+    typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+    __asm__("" : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
+    return __builtin_bit_cast(u32x2, half4{static_cast<_Float16>(a), static_cast<_Float16>(b), static_cast<_Float16>(c),
+                                           static_cast<_Float16>(d)});
 }
-__device__ __forceinline__ void mu_unpack(u32x4 w, float* v) {
-    const half8 h = __builtin_bit_cast(half8, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(h[e]);
+__device__ __forceinline__ float mu_half(const u32x2& w, int e) {
+    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)))));
 }
 
 template <class M>
@@ -454,87 +492,116 @@ __device__ __forceinline__ void mu_zero(f32x16 (&acc)[M::MB][M::NB]) {
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 }
 
-// The wave's part of a tile, through LDS, so that a lane has 8 consecutive rows i of a column j:
-// f(i, j, values, load(i, j)), the loads a batch ahead. Mirror: f's values go back into LDS and
-// from there, turned round, to g(j, i, values): 8 consecutive columns of row i. (Stored from the
-// accumulators, an access of the wave touched 16 bytes of each of 32 lines.) The wave's share of
-// LDS holds up to 64 of its rows at a time, as [j][i] in chunks of 4 values, placed so that
-// neither the accumulators' columns nor the rows that the mirror reads share banks.
-template <class M, bool Mirror, class Load, class Fn, class Gn>
-__device__ __forceinline__ void mu_pieces(const f32x16 (&acc)[M::MB][M::NB], int i0, int j0, uint8_t* lds, Load load, Fn f, Gn g) {
-    constexpr int IP = M::MB >= 2 ? 2 : 1, kI = 32 * IP, kJ = 32 * M::NB, kChunks = kI / 4;
-    constexpr int kLanes = kI / 8, kCols = 64 / kLanes, kBatch = M::MB >= 4 ? 4 : 2;  // lanes per column, columns at a time
-    static_assert(M::kNW * kI * kJ * 4 <= M::kLds && kJ % (kBatch * kCols) == 0, "the waves' shares fit the stages");
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int wm = wave / M::kWN, wn = wave % M::kWN;
-    float* const share = reinterpret_cast<float*>(lds) + wave * kI * kJ;
-    auto at = [&](int i, int j) { return share + j * kI + (((i >> 2) ^ (j ^ j >> 3)) & (kChunks - 1)) * 4 + (i & 3); };
-    const int jb = j0 + wn * kJ, q = (lane % kLanes) * 8, r = lane / kLanes;
+// What follows the contraction works on the wave's part of the tile in rounds of 32 columns j, in
+// the wave's own share of LDS, without barriers: fp16 values [32 j][kI i], where an accumulator
+// finds its four rows i of a column as 8 bytes, a row of memory goes by 16 bytes per lane
+// and, turned round, a transposed read has 8 columns of a row i. (One wave per SIMD issues an
+// instruction in 4 cycles, so this is kept to a few per value: with fp32 values through LDS
+// and a comparison each, it took 20 us of a 4096 x 4096 product's 104.)
+template <class M>
+struct MuRound {
+    static constexpr int kI = 32 * M::MB;
+    static constexpr int kLanes = kI / 8, kRows = 64 / kLanes, kIters = 32 / kRows;  // 16 bytes per lane
+    static constexpr int kBytes = 32 * kI * 2;
+    typedef __attribute__((address_space(3))) u32x2 L2;
+    typedef __attribute__((address_space(3))) u32x4 L4;
+    typedef __attribute__((address_space(3))) f32x4 F4;
+    uint32_t base;  // of the wave's share
+    int lane, ib, jb, j, h;  // first row and column of the wave's part; the lane's accumulator column and half
+
+    __device__ MuRound(uint8_t* lds, int i0, int j0, int share) {
+        const int wave = uniform(threadIdx.x >> 6);
+        lane = threadIdx.x & 63;
+        base = uniform(static_cast<int>(lds_addr(lds))) + wave * share;
+        ib = i0 + wave / M::kWN * kI;
+        jb = j0 + wave % M::kWN * 32 * M::NB;
+        j = lane & 31;
+        h = lane >> 5;
+    }
+    // Bytes of chunk c (4 values) of column j: columns that an access touches at one chunk lie on
+    // different banks; columns 16 apart in the two halves of 16 bytes.
+    __device__ static uint32_t at(int j, int c) {
+        constexpr int kPer = 128 / kI;  // columns per 256 bytes
+        return j * (kI * 2) + ((c ^ 2 * (j / kPer & (kI / 8 - 1)) ^ (j >> 4 & 1)) << 3);
+    }
+    __device__ u32x2 get(int array, int ii, int v) const {
+        return *(const L2*)static_cast<uintptr_t>(base + array * kBytes + at(j, 8 * ii + 2 * v + h));
+    }
+    __device__ void put(int array, int ii, int v, u32x2 w) const {
+        *(L2*)static_cast<uintptr_t>(base + array * kBytes + at(j, 8 * ii + 2 * v + h)) = w;
+    }
+    // The lane's 16 bytes of memory rows: column row(e), rows col() .. col() + 7.
+    __device__ int row(int e) const { return e * kRows + lane / kLanes; }
+    __device__ int col() const { return lane % kLanes * 8; }
+    __device__ uint32_t line(int array, int e) const {  // (the 16 bytes; their halves are swapped from column 16 on)
+        return base + array * kBytes + (at(row(e), 2 * (lane % kLanes)) & ~8u);
+    }
+    __device__ u32x4 get_line(int array, int e) const {
+        const u32x4 w = *(const L4*)static_cast<uintptr_t>(line(array, e));
+        return e * kRows < 16 ? w : u32x4{w.z, w.w, w.x, w.y};
+    }
+    __device__ void put_line(int array, int e, u32x4 w) const {
+        *(L4*)static_cast<uintptr_t>(line(array, e)) = e * kRows < 16 ? w : u32x4{w.z, w.w, w.x, w.y};
+    }
+    // 8 columns, from turned_col() on, of row turned_row(t), t < kI / 16.
+    __device__ int turned_row(int t) const { return 16 * t + (lane & 15); }
+    __device__ int turned_col() const { return lane >> 4 << 3; }
+    __device__ u32x4 get_turned(int t) const {
+        const int r = (lane >> 4) * 8 + (lane >> 2 & 3), c = 4 * t + (lane & 3);
+        const u32x2 a = mu_lds_tr(base + at(r, c)), b = mu_lds_tr(base + at(r + 4, c));
+        return u32x4{a.x, a.y, b.x, b.y};
+    }
+    // fp32 values in chunks of 4, [32 j][kI i], at an offset of the share.
+    __device__ uint32_t at32(int j, int c) const { return j * (kI * 4) + ((c ^ (j & (kI / 4 - 1))) << 4); }
+    __device__ void put32(uint32_t offset, int ii, int v, f32x4 w) const {
+        *(F4*)static_cast<uintptr_t>(base + offset + at32(j, 8 * ii + 2 * v + h)) = w;
+    }
+    __device__ f32x4 get32(uint32_t offset, int j, int c) const {
+        return *(const F4*)static_cast<uintptr_t>(base + offset + at32(j, c));
+    }
+    __device__ float get32_value(uint32_t offset, int j, int i) const {
+        return *(const __attribute__((address_space(3))) float*)static_cast<uintptr_t>(base + offset + at32(j, i >> 2) + (i & 3) * 4);
+    }
+};
+
+// Element (row, col) of the rows from `row0` on, of a matrix with ld values between rows: the rows'
+// start is the same in every lane, the rest an offset of 32 bits (a tile's rows).
+__device__ __forceinline__ uint16_t* mu_element(uint16_t* s, int64_t ld, int row0, int row, int col) {
+    uint8_t* const base = const_cast<uint8_t*>(uniform(reinterpret_cast<const uint8_t*>(s + row0 * ld)));
+    return reinterpret_cast<uint16_t*>(base + ((row - row0) * static_cast<uint32_t>(ld) + col) * 2u);
+}
+
+// A finished round of a symmetric product: columns j0 .. and, turned round, rows j0 ...
+template <class M>
+__device__ __forceinline__ void mu_store_sym(const MuRound<M>& r, uint16_t* s, int ld, int mp, int j0) {
+    using R = MuRound<M>;
 #pragma unroll
-    for (int ip = 0; ip < M::MB / IP; ++ip) {
-        const int ib = i0 + (wm * M::MB + ip * IP) * 32;
-        using Loaded = decltype(load(0, 0));
-        Loaded next[kBatch];
+    for (int e = 0; e < R::kIters; ++e) {
+        const int i = r.ib + r.col(), j = j0 + r.row(e);
+        const u32x4 w = r.get_line(0, e);
+        if (i < mp && j < mp) *gst<u32x4>(mu_element(s, ld, j0, j, i)) = w;
+    }
 #pragma unroll
-        for (int e = 0; e < kBatch; ++e) next[e] = load(ib + q, jb + e * kCols + r);
-#pragma unroll
-        for (int j = 0; j < M::NB; ++j)
-#pragma unroll
-            for (int ii = 0; ii < IP; ++ii)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const f32x16& c = acc[ip * IP + ii][j];
-                    *reinterpret_cast<f32x4*>(at(32 * ii + 8 * v + 4 * (lane >> 5), 32 * j + (lane & 31))) =
-                        f32x4{c[4 * v], c[4 * v + 1], c[4 * v + 2], c[4 * v + 3]};
-                }
-#pragma unroll 1
-        for (int c = 0; c < kJ; c += kBatch * kCols) {
-            Loaded now[kBatch];
-#pragma unroll
-            for (int e = 0; e < kBatch; ++e) now[e] = next[e];
-            if (c + kBatch * kCols < kJ)
-#pragma unroll
-                for (int e = 0; e < kBatch; ++e) next[e] = load(ib + q, jb + c + (kBatch + e) * kCols + r);
-#pragma unroll
-            for (int e = 0; e < kBatch; ++e) {
-                const int j = c + e * kCols + r;
-                f32x4* const pa = reinterpret_cast<f32x4*>(at(q, j));
-                f32x4* const pb = reinterpret_cast<f32x4*>(at(q + 4, j));
-                const f32x4 a = *pa, b = *pb;
-                float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                f(ib + q, jb + j, v, now[e]);
-                if constexpr (Mirror) {
-                    *pa = f32x4{v[0], v[1], v[2], v[3]};
-                    *pb = f32x4{v[4], v[5], v[6], v[7]};
-                }
-            }
-        }
-        if constexpr (Mirror) {
-            constexpr int kRowLanes = kJ / 8, kRows = 64 / kRowLanes;
-#pragma unroll kBatch
-            for (int i = lane / kRowLanes; i < kI; i += kRows) {
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = *at(i, (lane % kRowLanes) * 8 + e);
-                g(jb + (lane % kRowLanes) * 8, ib + i, v);
-            }
-        }
+    for (int t = 0; t < R::kI / 16; ++t) {
+        const int i = r.ib + r.turned_row(t), j = j0 + r.turned_col();
+        const u32x4 w = r.get_turned(t);
+        if (i < mp && j < mp) *gst<u32x4>(mu_element(s, ld, r.ib, i, j)) = w;
     }
 }
 
 // A = X X^T: tiles of the upper triangle, stored both ways round (sums over k in the same
 // order, so A is symmetric to the bit), 2^8 times; the diagonal in fp32. A contraction in parts
-// leaves each part's fp32 sums for k_mu_join.
-template <int F>
-__global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_gram(MuMatrices l, int src) {
+// (small tiles only) leaves each part's fp32 sums for k_mu_join.
+template <int F, int N>
+__global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_gram(MuListOf<MuMatrix, N> l, int src) {
     using M = MuTiles<F>;
     __shared__ __attribute__((aligned(16))) uint8_t lds[M::kLds];
-    const uint32_t id = mu_swizzle(blockIdx.x, l.first[l.n]);
+    const uint32_t id = mu_swizzle(blockIdx.x, l.blocks);
     const int k = mu_find(l, id);
     const MuMatrix& m = l.d[k];
     const int nt = (m.mp + M::kT - 1) / M::kT;
     const uint32_t per = nt * (nt + 1) / 2;
-    uint32_t t = id - l.first[k];
+    uint32_t t = mu_item(l, k, id);
     const uint32_t b = t / (per * m.parts);
     t -= b * (per * m.parts);
     const int part = static_cast<int>(t / per);
@@ -549,42 +616,59 @@ __global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_gram(MuMatrices l, int
     f32x16 acc[M::MB][M::NB];
     mu_zero<M>(acc);
     mu_accumulate<M, false>(x, mu_ld(m.np), m.mp, x, mu_ld(m.np), m.mp, ti * M::kT, tj * M::kT, k0, 2 * steps, lds, acc);
-    const int i0 = ti * M::kT, j0 = tj * M::kT;
-    if (m.parts > 1) {
+    if (F == kMuSmall && m.parts > 1) {
+        const MuRound<M> r(lds, ti * M::kT, tj * M::kT, 0);
         float* const o = reinterpret_cast<float*>(w + at.part) + static_cast<int64_t>(part) * m.mp * m.mp;
-        mu_pieces<M, false>(acc, i0, j0, lds, MuNoLoad{}, [&](int i, int j, float* v, MuNone) {
-            if (i >= m.mp || j >= m.mp) return;
-            float* const p = o + static_cast<int64_t>(j) * m.mp + i;
-            *gst<f32x4>(p) = f32x4{v[0], v[1], v[2], v[3]};
-            *gst<f32x4>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
-        }, MuNone{});
+#pragma unroll
+        for (int jj = 0; jj < M::NB; ++jj)
+#pragma unroll
+            for (int ii = 0; ii < M::MB; ++ii)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int i = r.ib + 32 * ii + 8 * v + 4 * r.h, j = r.jb + 32 * jj + r.j;
+                    const f32x16& c = acc[ii][jj];
+                    if (i < m.mp && j < m.mp)
+                        *gst<f32x4>(o + static_cast<int64_t>(j) * m.mp + i) = f32x4{c[4 * v], c[4 * v + 1], c[4 * v + 2], c[4 * v + 3]};
+                }
         return;
     }
+    const MuRound<M> r(lds, ti * M::kT, tj * M::kT, MuRound<M>::kBytes);
     uint16_t* const o = reinterpret_cast<uint16_t*>(w + at.a);
     float* const d = reinterpret_cast<float*>(w + at.d);
-    const float un = 1.0f / (m.lift * m.lift);  // powers of two: exact
-    const int ld = mu_ld(m.mp);
-    auto store = [&](int i, int j, const float* v) {
-        if (i < m.mp && j < m.mp) *gst<u32x4>(o + static_cast<int64_t>(j) * ld + i) = mu_pack(v);
-    };
-    mu_pieces<M, true>(acc, i0, j0, lds, MuNoLoad{}, [&](int i, int j, float* v, MuNone) {
-        const bool in = j < m.mp;
+    const float un = 1.0f / (m.lift * m.lift), scale = kMuLift * un;  // powers of two: exact
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            v[e] *= un;
-            if (i + e == j && in) stf(d + j, v[e]);
-            v[e] = i + e == j ? 0.0f : v[e] * kMuLift;
+    for (int jj = 0; jj < M::NB; ++jj) {
+        const int j0 = r.jb + 32 * jj;
+        __builtin_amdgcn_sched_barrier(0);  // (one round's accumulators in registers at a time)
+#pragma unroll
+        for (int ii = 0; ii < M::MB; ++ii) {
+            const f32x16& c = acc[ii][jj];
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                r.put(0, ii, v, mu_pack4(c[4 * v] * scale, c[4 * v + 1] * scale, c[4 * v + 2] * scale, c[4 * v + 3] * scale));
+            if (r.ib + 32 * ii == j0) {  // the diagonal: the lane whose row is its column
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (8 * v + 4 * r.h + e == r.j) {
+                            if (j0 + r.j < m.mp) stf(d + j0 + r.j, c[4 * v + e] * un);
+                            r.put(0, ii, v, mu_pack4(e == 0 ? 0.0f : c[4 * v] * scale, e == 1 ? 0.0f : c[4 * v + 1] * scale,
+                                                     e == 2 ? 0.0f : c[4 * v + 2] * scale, e == 3 ? 0.0f : c[4 * v + 3] * scale));
+                        }
+            }
         }
-        store(i, j, v);
-    }, store);
+        mu_store_sym(r, o, mu_ld(m.mp), m.mp, j0);
+    }
 }
 
 // The sums of A's parts, in order: 4 rows of a column j per thread (of the upper triangle).
-__global__ __launch_bounds__(kMuThreads) void k_mu_join(MuMatrices l) {
+template <int N>
+__global__ __launch_bounds__(kMuThreads) void k_mu_join(MuListOf<MuMatrix, N> l) {
     const int k = mu_find(l, blockIdx.x);
     const MuMatrix& m = l.d[k];
     const uint32_t per = static_cast<uint32_t>(m.mp / 4) * m.mp / kMuThreads;  // blocks per matrix (mp is a multiple of 64)
-    const uint32_t item = blockIdx.x - l.first[k], b = item / per;
+    const uint32_t item = mu_item(l, k, blockIdx.x), b = item / per;
     const int64_t q = static_cast<int64_t>(item % per) * kMuThreads + threadIdx.x;
     const int j = static_cast<int>(q / (m.mp / 4)), i = static_cast<int>(q % (m.mp / 4)) * 4;
     if (i > j) return;
@@ -615,16 +699,16 @@ __global__ __launch_bounds__(kMuThreads) void k_mu_join(MuMatrices l) {
 
 // B = b A + c A^2 from A's off-diagonal part O and its diagonal d, 2^8 times off the diagonal,
 // q = a + B_ii on it.
-template <int F>
-__global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_poly(MuMatrices l, MuPoly p) {
+template <int F, int N>
+__global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_poly(MuListOf<MuMatrix, N> l, MuPoly p) {
     using M = MuTiles<F>;
     __shared__ __attribute__((aligned(16))) uint8_t lds[M::kLds];
-    const uint32_t id = mu_swizzle(blockIdx.x, l.first[l.n]);
+    const uint32_t id = mu_swizzle(blockIdx.x, l.blocks);
     const int k = mu_find(l, id);
     const MuMatrix& m = l.d[k];
     const int nt = (m.mp + M::kT - 1) / M::kT;
     const uint32_t per = nt * (nt + 1) / 2;
-    const uint32_t t = id - l.first[k], b = t / per;
+    const uint32_t t = mu_item(l, k, id), b = t / per;
     int ti, tj;
     mu_triangle(t % per, nt, ti, tj);
     ti = uniform(ti);
@@ -639,59 +723,83 @@ __global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_poly(MuMatrices l, MuP
     uint16_t* const out = reinterpret_cast<uint16_t*>(w + at.b);
     const float* const d = reinterpret_cast<const float*>(w + at.d);
     float* const q = reinterpret_cast<float*>(w + at.q);
-    auto store = [&](int i, int j, const float* v) {
-        if (i < m.mp && j < m.mp) *gst<u32x4>(out + static_cast<int64_t>(j) * ld + i) = mu_pack(v);
-    };
-    struct Operands {
-        u32x4 o;
-        f32x4 d0, d1;
-        float dj;
-    };
-    mu_pieces<M, true>(acc, ti * M::kT, tj * M::kT, lds, [&](int i, int j) {
-        i = min(i, m.mp - 8);
-        j = min(j, m.mp - 1);
-        return Operands{*gld<u32x4>(o + static_cast<int64_t>(j) * ld + i), *gld<f32x4>(d + i), *gld<f32x4>(d + i + 4), ldf(d + j)};
-    }, [&](int i, int j, float* v, const Operands& z) {
-        if (i >= m.mp || j >= m.mp) return;
-        float x[8];
-        mu_unpack(z.o, x);
-        const float di[8] = {z.d0.x, z.d0.y, z.d0.z, z.d0.w, z.d1.x, z.d1.y, z.d1.z, z.d1.w}, dj = z.dj;
+    using R = MuRound<M>;
+    const R r(lds, ti * M::kT, tj * M::kT, R::kBytes + R::kI * 4);
+    auto load = [&](int j0, u32x4* f) {  // O's round
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float sq = v[e] * (kMuUnlift * kMuUnlift), a = x[e] * kMuUnlift;
-            if (i + e == j) stf(q + j, p.a + fmaf(p.b, dj, p.c * fmaf(dj, dj, sq)));
-            v[e] = i + e == j ? 0.0f : kMuLift * fmaf(p.b, a, p.c * fmaf(a, di[e] + dj, sq));
+        for (int e = 0; e < R::kIters; ++e)
+            f[e] = *gld<u32x4>(mu_element(const_cast<uint16_t*>(o), ld, tj * M::kT, min(j0 + r.row(e), m.mp - 1), min(r.ib + r.col(), m.mp - 8)));
+    };
+    u32x4 next[R::kIters];
+    load(r.jb, next);
+    // d_i of the wave's rows, in LDS
+    const uint32_t di = r.base + R::kBytes;
+    for (int i = r.lane; i < R::kI; i += 64)
+        *(__attribute__((address_space(3))) float*)static_cast<uintptr_t>(di + i * 4) = ldf(d + min(r.ib + i, m.mp - 1));
+    const float cs = p.c * kMuUnlift;
+#pragma unroll
+    for (int jj = 0; jj < M::NB; ++jj) {
+        const int j0 = r.jb + 32 * jj;
+        __builtin_amdgcn_sched_barrier(0);  // (one round's accumulators in registers at a time)
+#pragma unroll
+        for (int e = 0; e < R::kIters; ++e) r.put_line(0, e, next[e]);
+        if (jj + 1 < M::NB) load(j0 + 32, next);
+        const float dj = ldf(d + min(j0 + r.j, m.mp - 1));
+#pragma unroll
+        for (int ii = 0; ii < M::MB; ++ii) {
+            const f32x16& c = acc[ii][jj];
+            const bool diagonal = r.ib + 32 * ii == j0;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                // b A + c (O^2 + O (d_i + d_j)) = O (b + c (d_i + d_j)) + c O^2, the same bits for (j, i): a
+                // tile on the diagonal forms and stores both
+                const u32x2 x = r.get(0, ii, v);
+                const f32x4 dd = *(const typename R::F4*)static_cast<uintptr_t>(di + (32 * ii + 8 * v + 4 * r.h) * 4);
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = fmaf(mu_half(x, e), fmaf(p.c, dd[e] + dj, p.b), c[4 * v + e] * cs);
+                if (diagonal) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (8 * v + 4 * r.h + e == r.j) {
+                            const float sq = c[4 * v + e] * (kMuUnlift * kMuUnlift);
+                            if (j0 + r.j < m.mp) stf(q + j0 + r.j, p.a + fmaf(p.b, dj, p.c * fmaf(dj, dj, sq)));
+                            y[e] = 0.0f;
+                        }
+                }
+                r.put(0, ii, v, mu_pack4(y[0], y[1], y[2], y[3]));
+            }
         }
-        store(i, j, v);
-    }, store);
+        mu_store_sym(r, out, ld, m.mp, j0);
+    }
 }
 
-// X' = q X + B X: X^T's tile (rows: X's columns) times B (symmetric: its rows), so that a lane's
-// four values are consecutive in a row of X'. Into the other buffer, and the low part in place;
+// X' = q hi + t lo + B hi (t = a + B_ii min(1, d_i^2)): X^T's tile (rows: X's columns) times B (symmetric: its rows), so that a
+// lane's four values are consecutive in a row of X'. Into the other buffer, and the low part in place;
 // the last step's into the caller's tensors.
 
 // 8 values of the result in a row, from element i on, the first `valid` of them: the
 // parameter's update or the rounded values.
-__device__ __forceinline__ void mu_finish8(const MuTensor& t, const MuLast& z, int64_t i, int valid, float* v) {
-    if (z.update) {
+__device__ __forceinline__ void mu_finish8(const MuTensor& t, bool update, float decay, int64_t i, int valid, float* v) {
+    if (update) {
         float x[8];
         load_any8(t.x, i, valid, t.xbf16, x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = x[e] * z.decay - t.coef * v[e];
+        for (int e = 0; e < 8; ++e) v[e] = x[e] * decay - t.coef * v[e];
     }
     store_any8(t.x, i, valid, t.xbf16, v);
 }
 
-template <int F, class Last>
-__global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_apply(MuMatrices l, int src, Last z) {
+template <int F, int N, class Last>
+__global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_apply(MuListOf<MuMatrix, N> l, int src, float linear, Last z) {
     using M = MuTiles<F>;
-    constexpr bool kLast = std::is_same<Last, MuLast>::value;
+    constexpr bool kLast = !std::is_same<Last, MuNone>::value;
     __shared__ __attribute__((aligned(16))) uint8_t lds[M::kLds];
-    const uint32_t id = mu_swizzle(blockIdx.x, l.first[l.n]);
+    const uint32_t id = mu_swizzle(blockIdx.x, l.blocks);
     const int k = mu_find(l, id);
     const MuMatrix& m = l.d[k];
     const uint32_t tm = (m.mp + M::kT - 1) / M::kT, tn = (m.np + M::kT - 1) / M::kT, per = tm * tn;
-    uint32_t t = id - l.first[k];
+    uint32_t t = mu_item(l, k, id);
     const uint32_t b = t / per;
     t -= b * per;
     // kMuGroup rows of X' at a time, by columns
@@ -709,101 +817,158 @@ __global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_apply(MuMatrices l, in
                            m.mp / 32, lds, acc);
     const float* const q = reinterpret_cast<const float*>(w + at.q);
     uint16_t* const hi = reinterpret_cast<uint16_t*>(w + at.hi(src ^ 1));
-    const float un = 1.0f / m.lift;
-    struct Operands {
-        u32x4 hi, lo;
-        float q;
-    };
-    auto load = [&](int i, int j) {
-        i = min(i, m.np - 8);
-        j = min(j, m.mp - 1);
-        const int64_t p = static_cast<int64_t>(j) * ld + i;
-        return Operands{*gld<u32x4>(x + p), *gld<u32x4>(lo + p), ldf(q + j)};
-    };
-    auto result = [&](const Operands& z, float* v) {  // 8 columns of X'
-        float xh[8], xl[8];
-        mu_unpack(z.hi, xh);
-        mu_unpack(z.lo, xl);
+    using R = MuRound<M>;
+    constexpr uint32_t kPlanes = 2 * R::kBytes;  // X's two parts, then (last) the result
+    const R r(lds, ti * M::kT, tj * M::kT, kLast ? 2 * kPlanes : kPlanes);
+    static_assert(M::kNW * 2 * kPlanes <= M::kLds, "the waves' shares fit the stages");
+    auto load = [&](int j0, u32x4* f) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fmaf(z.q, xh[e] + xl[e], v[e] * kMuUnlift);
-    };
-    if constexpr (kLast) {
-        const MuTensor& c = z.t.d[k];
-        const int64_t base = b * (static_cast<int64_t>(c.rows) * c.ldx);
-        if (c.tall) {  // row j of X' is column j of the caller's matrix
-            mu_pieces<M, true>(acc, ti * M::kT, tj * M::kT, lds, load, [&](int, int, float* v, const Operands& o) {
-                result(o, v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= un;
-            }, [&](int j, int i, float* v) {
-                const int valid = i < c.rows ? clamp_valid(static_cast<int64_t>(c.cols) - j) : 0;
-                if (valid > 0) mu_finish8(c, z, base + i * c.ldx + j, valid, v);
-            });
-        } else {
-            mu_pieces<M, false>(acc, ti * M::kT, tj * M::kT, lds, load, [&](int i, int j, float* v, const Operands& o) {
-                const int valid = j < c.rows ? clamp_valid(static_cast<int64_t>(c.cols) - i) : 0;
-                if (valid == 0) return;
-                result(o, v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= un;
-                mu_finish8(c, z, base + j * c.ldx + i, valid, v);
-            }, MuNone{});
+        for (int e = 0; e < R::kIters; ++e) {
+            const int j = min(j0 + r.row(e), m.mp - 1), i = min(r.ib + r.col(), m.np - 8);
+            f[2 * e] = *gld<u32x4>(mu_element(const_cast<uint16_t*>(x), ld, tj * M::kT, j, i));
+            f[2 * e + 1] = *gld<u32x4>(mu_element(lo, ld, tj * M::kT, j, i));
         }
-    } else {
-        mu_pieces<M, false>(acc, ti * M::kT, tj * M::kT, lds, load, [&](int i, int j, float* v, const Operands& o) {
-            if (i >= m.np || j >= m.mp) return;
-            const int64_t p = static_cast<int64_t>(j) * ld + i;
-            result(o, v);
-            const u32x4 h = mu_pack(v);
-            float r[8];
-            mu_unpack(h, r);
+    };
+    u32x4 next[2 * R::kIters];
+    load(r.jb, next);
+    const float un = 1.0f / m.lift * kMuUnlift;
+    const float* const d = reinterpret_cast<const float*>(w + at.d);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[e] = v[e] - r[e];
-            *gst<u32x4>(hi + p) = h;
-            *gst<u32x4>(lo + p) = mu_pack(r);
-        }, MuNone{});
+    for (int jj = 0; jj < M::NB; ++jj) {
+        const int j0 = r.jb + 32 * jj;
+        __builtin_amdgcn_sched_barrier(0);  // (one round's accumulators in registers at a time)
+#pragma unroll
+        for (int e = 0; e < R::kIters; ++e) {
+            r.put_line(0, e, next[2 * e]);
+            r.put_line(1, e, next[2 * e + 1]);
+        }
+        if (jj + 1 < M::NB) load(j0 + 32, next);
+        const float dj = ldf(d + min(j0 + r.j, m.mp - 1)), qj = ldf(q + min(j0 + r.j, m.mp - 1)) * kMuLift;
+        const float al = linear * kMuLift, tl = fmaf(qj - al, fminf(dj * dj, 1.0f), al);
+#pragma unroll
+        for (int ii = 0; ii < M::MB; ++ii) {
+            const f32x16& c = acc[ii][jj];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const u32x2 xh = r.get(0, ii, v), xl = r.get(1, ii, v);
+                float y[4];  // 2^8 X'
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = fmaf(tl, mu_half(xl, e), fmaf(qj, mu_half(xh, e), c[4 * v + e]));
+                if constexpr (kLast) {
+                    r.put32(kPlanes, ii, v, f32x4{y[0] * un, y[1] * un, y[2] * un, y[3] * un});
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] *= kMuUnlift;
+                    const u32x2 n = mu_pack4(y[0], y[1], y[2], y[3]);
+                    r.put(0, ii, v, n);
+                    r.put(1, ii, v, mu_pack4(y[0] - mu_half(n, 0), y[1] - mu_half(n, 1), y[2] - mu_half(n, 2), y[3] - mu_half(n, 3)));
+                }
+            }
+        }
+        if constexpr (!kLast) {
+#pragma unroll
+            for (int e = 0; e < R::kIters; ++e) {
+                const int i = r.ib + r.col(), j = j0 + r.row(e);
+                const u32x4 a = r.get_line(0, e), b = r.get_line(1, e);
+                if (i < m.np && j < m.mp) {
+                    *gst<u32x4>(mu_element(hi, ld, tj * M::kT, j, i)) = a;
+                    *gst<u32x4>(mu_element(lo, ld, tj * M::kT, j, i)) = b;
+                }
+            }
+        } else {
+            const MuTensor& t = z.t.d[k];
+            const int64_t first = b * (static_cast<int64_t>(t.rows) * t.ldx);
+            if (t.tall) {  // row j of X' is column j of the caller's matrix: 8 of them of its row i
+#pragma unroll 2
+                for (int e = 0; e < R::kI / 16; ++e) {
+                    const int i = r.ib + 16 * e + (r.lane >> 2), j = j0 + (r.lane & 3) * 8;
+                    const int valid = i < t.rows ? clamp_valid(static_cast<int64_t>(t.cols) - j) : 0;
+                    float v[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) v[u] = r.get32_value(kPlanes, (r.lane & 3) * 8 + u, 16 * e + (r.lane >> 2));
+                    if (valid > 0) mu_finish8(t, z.update, z.decay, first + i * t.ldx + j, valid, v);
+                }
+            } else {
+#pragma unroll 2
+                for (int e = 0; e < R::kIters; ++e) {
+                    const int i = r.ib + r.col(), j = j0 + r.row(e);
+                    const int valid = j < t.rows ? clamp_valid(static_cast<int64_t>(t.cols) - i) : 0;
+                    const f32x4 a = r.get32(kPlanes, r.row(e), r.col() / 4), c = r.get32(kPlanes, r.row(e), r.col() / 4 + 1);
+                    float v[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+                    if (valid > 0) mu_finish8(t, z.update, z.decay, first + j * t.ldx + i, valid, v);
+                }
+            }
+        }
     }
 }
 
 }  // namespace
 
+// f(list, form) with one tensor alone by itself.
+template <class List, class Fn>
+static void with_list(const List& l, Fn f) {
+    if (l.n == 1) f(l.only(), std::integral_constant<int, 1>{});
+    else f(l, std::integral_constant<int, kMuBatch>{});
+}
+template <class Fn>
+static void with_form(int form, Fn f) {
+    if (form == kMuLarge) f(std::integral_constant<int, kMuLarge>{});
+    else if (form == kMuMedium) f(std::integral_constant<int, kMuMedium>{});
+    else f(std::integral_constant<int, kMuSmall>{});
+}
+
 void launch_mu_momentum(const MuTensors& t, const MuStepArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(k_mu_momentum, dim3(t.first[t.n]), dim3(kMuThreads), 0, s, t, a);
+    with_list(t, [&](const auto& l, auto n) {
+        hipLaunchKernelGGL(k_mu_momentum<decltype(n)::value>, dim3(t.blocks), dim3(kMuThreads), 0, s, l, a);
+    });
 }
 
 void launch_mu_scatter(const MuTensors& t, const MuStepArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(k_mu_scatter, dim3(t.first[t.n]), dim3(kMuThreads), 0, s, t, a);
+    with_list(t, [&](const auto& l, auto n) {
+        hipLaunchKernelGGL(k_mu_scatter<decltype(n)::value>, dim3(t.blocks), dim3(kMuThreads), 0, s, l, a);
+    });
 }
 
 void launch_mu_gram(const MuMatrices& m, int form, int src, hipStream_t s) {
-    const dim3 g(m.first[m.n]), t(kMuFormThreads[form]);
-    if (form == kMuLarge) hipLaunchKernelGGL(k_mu_gram<kMuLarge>, g, t, 0, s, m, src);
-    else if (form == kMuMedium) hipLaunchKernelGGL(k_mu_gram<kMuMedium>, g, t, 0, s, m, src);
-    else hipLaunchKernelGGL(k_mu_gram<kMuSmall>, g, t, 0, s, m, src);
+    if (m.blocks == 0) return;
+    with_list(m, [&](const auto& l, auto n) {
+        with_form(form, [&](auto f) {
+            hipLaunchKernelGGL((k_mu_gram<decltype(f)::value, decltype(n)::value>), dim3(m.blocks), dim3(kMuFormThreads[form]), 0, s, l, src);
+        });
+    });
 }
 
 void launch_mu_join(const MuMatrices& m, hipStream_t s) {
-    hipLaunchKernelGGL(k_mu_join, dim3(m.first[m.n]), dim3(kMuThreads), 0, s, m);
+    if (m.blocks == 0) return;
+    with_list(m, [&](const auto& l, auto n) {
+        hipLaunchKernelGGL(k_mu_join<decltype(n)::value>, dim3(m.blocks), dim3(kMuThreads), 0, s, l);
+    });
 }
 
 void launch_mu_poly(const MuMatrices& m, int form, const MuPoly& p, hipStream_t s) {
-    const dim3 g(m.first[m.n]), t(kMuFormThreads[form]);
-    if (form == kMuLarge) hipLaunchKernelGGL(k_mu_poly<kMuLarge>, g, t, 0, s, m, p);
-    else if (form == kMuMedium) hipLaunchKernelGGL(k_mu_poly<kMuMedium>, g, t, 0, s, m, p);
-    else hipLaunchKernelGGL(k_mu_poly<kMuSmall>, g, t, 0, s, m, p);
+    with_list(m, [&](const auto& l, auto n) {
+        with_form(form, [&](auto f) {
+            hipLaunchKernelGGL((k_mu_poly<decltype(f)::value, decltype(n)::value>), dim3(m.blocks), dim3(kMuFormThreads[form]), 0, s, l, p);
+        });
+    });
 }
 
-template <class Last>
-static void launch_apply(const MuMatrices& m, int form, int src, const Last& z, hipStream_t s) {
-    const dim3 g(m.first[m.n]), t(kMuFormThreads[form]);
-    if (form == kMuLarge) hipLaunchKernelGGL((k_mu_apply<kMuLarge, Last>), g, t, 0, s, m, src, z);
-    else if (form == kMuMedium) hipLaunchKernelGGL((k_mu_apply<kMuMedium, Last>), g, t, 0, s, m, src, z);
-    else hipLaunchKernelGGL((k_mu_apply<kMuSmall, Last>), g, t, 0, s, m, src, z);
-}
-
-void launch_mu_apply(const MuMatrices& m, int form, int src, const MuLast* last, hipStream_t s) {
-    if (last) launch_apply(m, form, src, *last, s);
-    else launch_apply(m, form, src, MuNone{}, s);
+void launch_mu_apply(const MuMatrices& m, int form, int src, float linear, const MuLast* last, hipStream_t s) {
+    with_list(m, [&](const auto& l, auto n) {
+        constexpr int N = decltype(n)::value;
+        with_form(form, [&](auto f) {
+            constexpr int F = decltype(f)::value;
+            const dim3 g(m.blocks), t(kMuFormThreads[F]);
+            if (!last) {
+                hipLaunchKernelGGL((k_mu_apply<F, N, MuNone>), g, t, 0, s, l, src, linear, MuNone{});
+            } else if constexpr (N == 1) {
+                const MuLastOf<1> z{last->t.only(), last->decay, last->update};
+                hipLaunchKernelGGL((k_mu_apply<F, N, MuLastOf<1>>), g, t, 0, s, l, src, linear, z);
+            } else {
+                hipLaunchKernelGGL((k_mu_apply<F, N, MuLast>), g, t, 0, s, l, src, linear, *last);
+            }
+        });
+    });
 }
 
 }  // namespace meo

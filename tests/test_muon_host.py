@@ -1,0 +1,264 @@
+"""Muon's operators on the host (no GPU): the oracle against closed forms, the refusals of the
+entry points and front ends, which all come before any device work, and the layout rules."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from memory_efficient_optimizers_amd import MeoError, Muon, _lib, moment_dtype, orthogonalize
+from oracle import muon as om
+
+P = 0x7F0000001000  # a pointer value that validation inspects and never follows
+
+
+# ------------------------------------------------------------------------------ oracle
+
+def test_singular_values_go_through_the_polynomial():
+    rng = np.random.default_rng(0)
+    u, _ = np.linalg.qr(rng.standard_normal((6, 6)))
+    v, _ = np.linalg.qr(rng.standard_normal((9, 6)))
+    s = np.array([3.0, 1.0, 0.5, 0.1, 1e-2, 0.0])
+    want = s / np.linalg.norm(s)
+    for a, b, c in [om.COEFFICIENTS] * 5:
+        want = a * want + b * want ** 3 + c * want ** 5
+    for x in (u @ np.diag(s) @ v.T, (u @ np.diag(s) @ v.T).T):
+        got = om.newton_schulz(x)
+        exp = u @ np.diag(want) @ v.T
+        assert np.allclose(got, exp if x.shape == (6, 9) else exp.T, atol=1e-12)
+
+
+def test_one_by_one_zero_and_eps():
+    s = 1.0
+    for _ in range(5):
+        s = 3.4445 * s - 4.7750 * s ** 3 + 2.0315 * s ** 5
+    assert om.newton_schulz(np.array([[-7.0]]))[0, 0] == pytest.approx(-s, rel=1e-12)
+    assert (om.newton_schulz(np.zeros((2, 3))) == 0).all() and (om.newton_schulz(np.zeros((2, 3)), eps=0.0) == 0).all()
+    assert om.newton_schulz(np.array([[1e-9]]), steps=1, eps=1e-7)[0, 0] == pytest.approx(3.4445e-2, rel=1e-3)
+
+
+@pytest.mark.parametrize("shape,kind", [((40, 70), "noise"), ((64, 64), "decades"), ((48, 130), "low"), ((90, 30), "noise"),
+                                        ((16, 16), "one"), ((48, 130), "one")])
+def test_the_roundings_cost_little_at_any_conditioning(shape, kind):
+    """meo.h's precision: 4e-3 of the result at most, for matrices of any conditioning.
+
+    A rounding to fp16 is 2^-11 of the value at most, 2.1e-4 in the root mean square (a step's
+    third root, over the significands). Where singular values are about 1 a step adds that times
+    |b s^2 + c s^4| <= 2.8 (B times X's rounding), the rounding of A times |b + 2 c s^2| <= 2.5 (A
+    off its diagonal is at most half of A), and of B, half of 2.8: 6e-4, 3e-4 and 3e-4, in
+    quadrature 8e-4. Five steps, were they all to add up, are 4e-3; small singular values go
+    by the linear term, which takes 22 bits of X."""
+    rng = np.random.default_rng(1)
+    x = rng.standard_normal(shape)
+    if kind == "decades":
+        u, s, v = np.linalg.svd(x, full_matrices=False)
+        x = u @ np.diag(np.logspace(0, -5, len(s))) @ v
+    if kind == "low":
+        x = rng.standard_normal((shape[0], 4)) @ rng.standard_normal((4, shape[1])) + 1e-2 * x
+    if kind == "one":
+        x = rng.standard_normal((shape[0], 1)) @ rng.standard_normal((1, shape[1])) + 1e-4 * x
+    want = om.newton_schulz(x)
+    assert np.linalg.norm(om.rounded_newton_schulz(x) - want) <= 4e-3 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("shape", [(1, 1), (5, 9), (33, 20), (64, 100)])
+def test_bound_of_one_step_holds_for_the_roundings(shape):
+    x = np.random.default_rng(2).standard_normal(shape)
+    assert np.all(np.abs(om.rounded_newton_schulz(x, 1) - om.newton_schulz(x, 1)) <= om.bound_of_one_step(x))
+
+
+def test_quantizer():
+    m = np.zeros(300, np.float32)
+    m[:4] = [1.27, -0.635, 0.005, 0.0149]
+    m[128] = np.inf
+    codes, scale = om.quantize(m)
+    assert list(codes[:4]) == [127, -64, 0, 1] and codes[128] == 0 and np.isnan(scale[1]) and scale[2] == 0
+    assert scale.shape == (3,) and np.isnan(om.dequantize(codes, scale)[128:256]).all()
+
+
+# ------------------------------------------------------------------------------ hyperparameters
+
+def test_defaults():
+    h, u = _lib.meo_orthogonalize_defaults(), _lib.meo_muon_defaults()
+    assert (h.eps, h.steps) == (1e-7, 5) and all(tuple(r) == om.COEFFICIENTS for r in h.coefficients)
+    assert (u.lr, u.momentum, u.weight_decay, u.nesterov, u.adjust_lr) == (1e-3, 0.95, 0.1, 1, _lib.MEO_MUON_ORIGINAL)
+    assert (u.ns.eps, u.ns.steps) == (1e-7, 5)
+    assert bytes(_lib.orthogonalize_hparams()) == bytes(h) and bytes(_lib.muon_hparams()) == bytes(u)
+
+
+@pytest.mark.parametrize("kw,why", [
+    (dict(steps=0), "steps"), (dict(steps=17), "steps"), (dict(eps=-1e-9), "epsilon"), (dict(eps=math.nan), "epsilon"),
+    (dict(eps=math.inf), "epsilon"), (dict(coefficients=(math.nan, 0, 0)), "non-finite"),
+    (dict(coefficients=(3.0, math.inf, 0)), "non-finite"),
+    (dict(coefficients=(8.5, 0, 0), steps=1), "too large"),         # 8.5 s
+    (dict(coefficients=(2.0, 0.0, 0.0), steps=4), "too large"),     # 2^4
+    (dict(coefficients=(1.0, -101.0, 100.0), steps=1), "too large"),  # s(1 - 101/2.02 ..) within
+    (dict(coefficients=(0.0, 0.0, 101.0), steps=1), "too large"),
+])
+def test_hyperparameter_refusals(kw, why):
+    with pytest.raises(MeoError, match=why) as e:
+        _lib.meo_orthogonalize_validate(_lib.orthogonalize_hparams(**kw), [], [])
+    assert e.value.code == _lib.MEO_EINVAL
+    with pytest.raises(MeoError, match=why):
+        hp = _lib.muon_hparams(ns_steps=kw.get("steps", 5), eps=kw.get("eps", 1e-7),
+                               ns_coefficients=kw.get("coefficients", om.COEFFICIENTS))
+        _lib.meo_muon_validate(hp, 1, [], [], [])
+
+
+@pytest.mark.parametrize("coefficients,steps", [
+    ((2.0, -1.5, 0.5), 10), ((1.5, -0.5, 0.0), 16), ((2.0, 0.0, 0.0), 3), (om.COEFFICIENTS, 16),
+    ([(8.2, -22.9, 16.46), (4.0, -2.9, 0.5), (3.9, -2.8, 0.5), (3.3, -2.4, 0.5)], 4)])
+def test_coefficients_in_use_elsewhere_are_taken(coefficients, steps):
+    _lib.meo_orthogonalize_validate(_lib.orthogonalize_hparams(steps, coefficients), [], [])
+
+
+def test_coefficient_shapes():
+    for bad in ([(1, 2, 3)] * 4, [(1, 2)] * 5, (1, 2)):
+        with pytest.raises((ValueError, TypeError)):
+            _lib.orthogonalize_hparams(5, bad)
+    assert [list(r) for r in _lib.orthogonalize_hparams(2, [(1, 2, 3), (4, 5, 6)]).coefficients][:2] == [[1, 2, 3], [4, 5, 6]]
+
+
+@pytest.mark.parametrize("kw,why", [
+    (dict(lr=-1.0), "learning rate"), (dict(lr=math.nan), "learning rate"), (dict(momentum=1.0), "momentum"),
+    (dict(momentum=-0.1), "momentum"), (dict(momentum=math.nan), "momentum"), (dict(weight_decay=math.inf), "weight_decay")])
+def test_muon_hyperparameter_refusals(kw, why):
+    with pytest.raises(MeoError, match=why):
+        _lib.meo_muon_validate(_lib.muon_hparams(**kw), 1, [], [], [])
+
+
+# ------------------------------------------------------------------------------ C entry points
+
+def _mat(**kw):
+    a = dict(x=P, out=P, batch=1, rows=4, cols=6, ldx=6, ldo=6, dtype=_lib.MEO_F32)
+    a.update(kw)
+    return _lib.meo_ns_matrices(*a.values(), 0)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1), "MEO_ESHAPE"), (dict(cols=-1), "MEO_ESHAPE"), (dict(batch=-1), "MEO_ESHAPE"),
+    (dict(ldx=5), "MEO_ESHAPE"), (dict(ldo=5), "MEO_ESHAPE"), (dict(ldx=2 ** 31), "MEO_ESHAPE"),
+    (dict(rows=2 ** 22 + 1), "MEO_ESHAPE"), (dict(cols=2 ** 22 + 1, ldx=2 ** 23, ldo=2 ** 23), "MEO_ESHAPE"),
+    (dict(rows=2 ** 20, cols=2 ** 16, ldx=2 ** 16, ldo=2 ** 16), "MEO_ESHAPE"),
+    (dict(batch=2 ** 31), "MEO_ESHAPE"), (dict(batch=2 ** 31 - 1, rows=2 ** 22, ldx=2 ** 20, ldo=2 ** 20), "MEO_ESHAPE"),
+    (dict(dtype=_lib.MEO_I8), "MEO_EDTYPE"), (dict(x=None), "MEO_ENULL"), (dict(out=None), "MEO_ENULL"),
+    (dict(x=P + 2), "MEO_EALIGN"), (dict(x=P + 1, dtype=_lib.MEO_BF16), "MEO_EALIGN"), (dict(out=P + 1), "MEO_EALIGN"),
+])
+def test_matrix_refusals(kw, code):
+    hp = _lib.orthogonalize_hparams()
+    arr = (_lib.meo_ns_matrices * 2)(_mat(rows=0, x=None, out=None), _mat(**kw))
+    rc = _lib.load().meo_orthogonalize(hp, 2, arr, None, 0, None)
+    assert _lib.ERROR_NAMES.get(rc) == code, (rc, _lib.meo_last_error())
+    assert _lib.meo_last_error().startswith("matrix 1: ")
+
+
+def test_list_arguments():
+    lib, hp, u = _lib.load(), _lib.orthogonalize_hparams(), _lib.muon_hparams()
+    assert lib.meo_orthogonalize(hp, 0, None, None, 0, None) == _lib.MEO_OK
+    assert lib.meo_orthogonalize(hp, -1, None, None, 0, None) == _lib.MEO_EINVAL
+    assert lib.meo_orthogonalize(hp, 1, None, None, 0, None) == _lib.MEO_ENULL
+    assert lib.meo_orthogonalize(None, 0, None, None, 0, None) == _lib.MEO_ENULL
+    assert lib.meo_muon_step(u, 1, 0, None, None, None, 0, None) == _lib.MEO_OK
+    assert lib.meo_muon_step(u, 0, 0, None, None, None, 0, None) == _lib.MEO_EINVAL
+    assert lib.meo_muon_step(u, 1, -1, None, None, None, 0, None) == _lib.MEO_EINVAL
+    assert lib.meo_muon_step(u, 1, 1, None, None, None, 0, None) == _lib.MEO_ENULL
+    assert lib.meo_muon_step(None, 1, 0, None, None, None, 0, None) == _lib.MEO_ENULL
+
+
+def _muon(**kw):
+    t = dict(param=P, grad=P, batch=1, rows=64, cols=48, ndim=2, param_dtype=_lib.MEO_F32, grad_dtype=_lib.MEO_F32,
+             state_dtype=_lib.MEO_F32)
+    st = dict(exp_avg=P, exp_avg_scale=None)
+    t.update({k: v for k, v in kw.items() if k in t})
+    st.update({k: v for k, v in kw.items() if k in st})
+    rc = _lib.load().meo_muon_validate(_lib.muon_hparams(), 1, 1, _lib.meo_tensor(*t.values()), _lib.meo_muon_state(*st.values()))
+    return _lib.ERROR_NAMES.get(rc, rc)
+
+
+I8 = dict(state_dtype=_lib.MEO_I8, exp_avg_scale=P)
+
+
+@pytest.mark.parametrize("kw,want", [
+    ({}, 0), (I8, 0), (dict(batch=3, ndim=3, **I8), 0), (dict(rows=0, param=None, exp_avg=None, ndim=1), 0),
+    (dict(ndim=1, rows=1), "MEO_ESHAPE"), (dict(ndim=0, rows=1, cols=1), "MEO_ESHAPE"), (dict(batch=2), "MEO_ESHAPE"),
+    (dict(rows=-1), "MEO_ESHAPE"), (dict(rows=2 ** 22 + 1), "MEO_ESHAPE"), (dict(rows=2 ** 40, cols=2 ** 40), "MEO_ESHAPE"),
+    (dict(batch=3, ndim=3, rows=5, **I8), "MEO_ESHAPE"), (dict(state_dtype=_lib.MEO_I8), "MEO_ENULL"),
+    (dict(state_dtype=_lib.MEO_I8, exp_avg_scale=P + 2), "MEO_EALIGN"), (dict(param_dtype=_lib.MEO_I8), "MEO_EDTYPE"),
+    (dict(grad_dtype=_lib.MEO_MX4), "MEO_EDTYPE"), (dict(state_dtype=_lib.MEO_MX4), "MEO_EDTYPE"), (dict(param=None), "MEO_ENULL"),
+    (dict(grad=None), "MEO_ENULL"), (dict(exp_avg=None), "MEO_ENULL"), (dict(param=P + 2), "MEO_EALIGN"),
+    (dict(grad=P + 2), "MEO_EALIGN"), (dict(exp_avg=P + 2), "MEO_EALIGN"), (dict(exp_avg=P + 1, state_dtype=_lib.MEO_BF16), "MEO_EALIGN"),
+])
+def test_tensor_refusals(kw, want):
+    assert _muon(**kw) == want, _lib.meo_last_error()
+
+
+def test_workspace_grows_to_a_bound():
+    """Lists are worked on in parts of about 2^26 values."""
+    hp = _lib.muon_hparams()
+    size = lambda n, r, c: _lib.load().meo_muon_workspace_size(  # noqa: E731
+        hp, n, (_lib.meo_tensor * n)(*[_lib.meo_tensor(P, P, 1, r, c, 2, 0, 0, 0)] * n))
+    one = size(1, 4096, 4096)
+    assert 6 * 4096 ** 2 + 4 * 4096 ** 2 <= one <= 1.05 * (10 * 4096 ** 2)
+    assert size(4, 4096, 4096) == 4 * one == size(40, 4096, 4096)
+    assert size(0, 4096, 4096) == 0 and size(2, 0, 5) == 0 and size(1, 2 ** 23, 4) == 0
+    assert size(3, 32000, 4096) == size(1, 32000, 4096)  # larger than a part: one at a time
+
+
+# ------------------------------------------------------------------------------ front ends
+
+def test_orthogonalize_refusals():
+    x = torch.zeros(4, 6)
+    for bad, err in ((x, ValueError), (x[0], ValueError), (x.double(), TypeError), ([x, x[0]], ValueError)):
+        with pytest.raises(err):
+            orthogonalize(bad)
+    with pytest.raises(ValueError, match="out of shape"):
+        orthogonalize(x, out=torch.zeros(6, 4, dtype=torch.bfloat16))
+    with pytest.raises(TypeError, match="bfloat16"):
+        orthogonalize(x, out=torch.zeros(4, 6))
+    with pytest.raises(ValueError, match="differ in length"):
+        orthogonalize([x], out=[])
+    assert orthogonalize([]) == []
+    with pytest.raises(MeoError):
+        orthogonalize([], steps=0)
+
+
+def test_row_strides():
+    f = lambda t: _lib._ns_row_stride(t, "t")  # noqa: E731
+    x = torch.zeros(4, 6, 10)
+    assert f(x) == 10 and f(x[0, :, :7]) == 10 and f(x[:, :, :7]) == 10 and f(x[0, 2:3, :7]) >= 7
+    assert f(x[:, :1, :]) == 60 and f(torch.zeros(0, 5)) == 5 and f(torch.zeros(5, 0)) == 1
+    for bad in (x.mT, x[:, ::2, ::2], x[:, :3], x[0].t(), x[::2]):
+        with pytest.raises(ValueError):
+            f(bad)
+
+
+@pytest.mark.parametrize("kw", [dict(lr=-1), dict(momentum=1.0), dict(eps=-1), dict(adamw_eps=-1), dict(betas=(1.0, 0.9)),
+                                dict(ns_steps=0), dict(ns_steps=17), dict(adjust_lr="rms"), dict(ns_coefficients=(1, 2))])
+def test_muon_front_end_refusals(kw):
+    p = torch.nn.Parameter(torch.zeros(4, 4))
+    with pytest.raises((ValueError, TypeError)):
+        Muon([p], **kw)
+    opt = Muon([p])
+    with pytest.raises((ValueError, TypeError)):
+        opt.add_param_group(dict(params=[torch.nn.Parameter(torch.zeros(2, 2))], **kw))
+    with pytest.raises(TypeError):
+        Muon([p], state_dtype=torch.float16)
+
+
+def test_momentum_dtype():
+    f = lambda shape, **kw: moment_dtype("muon", shape, torch.int8, torch.float32, **kw)  # noqa: E731
+    assert f((64, 64)) == torch.int8 and f((100, 77)) == torch.int8  # groups may cross rows
+    assert f((63, 64)) == torch.float32  # fewer than 4096 values
+    assert f((8, 64, 64)) == torch.int8 and f((8, 65, 63)) == torch.float32 and f((1, 65, 64)) == torch.int8
+    assert moment_dtype("muon", (4, 4), None, torch.bfloat16) == torch.bfloat16
+
+
+def test_muon_state_checks():
+    p, g = torch.zeros(64, 64), torch.zeros(64, 64)
+    hp = _lib.muon_hparams()
+    for st in (dict(exp_avg=torch.zeros(64, 63)), dict(exp_avg=torch.zeros(64, 64, dtype=torch.int8)),
+               dict(exp_avg=torch.zeros(64, 64, dtype=torch.int8), exp_avg_scale=torch.zeros(31))):
+        with pytest.raises(ValueError):
+            _lib.meo_muon_step(hp, 1, [p], [g], [st])
+    with pytest.raises(TypeError):
+        _lib.meo_muon_step(hp, 1, [p], [g], [dict(exp_avg=torch.zeros(64, 64, dtype=torch.float16))])
