@@ -2834,8 +2834,8 @@ int64_t mu_chunks(const std::vector<MuIn>& ts, std::vector<MuChunk>* out) {
 
 // The tile form of a pass: the one whose tiles, dealt to the CUs, are done first. A CU holds one
 // large tile, two medium or four small ones at a time; kMuFormCost is what a CU's load takes.
-constexpr int kMuFormLoad[kMuForms] = {4, 2, 1};
-constexpr double kMuFormCost[kMuForms] = {0.45, 0.60, 1.0};
+constexpr int kMuFormLoad[kMuForms] = {4, 2, 1, 1};
+constexpr double kMuFormCost[kMuForms] = {0.45, 0.60, 0.6, 1.0};
 
 template <class Tiles>
 int mu_form(const std::vector<MuIn>& ts, const MuChunk& c, Tiles tiles) {

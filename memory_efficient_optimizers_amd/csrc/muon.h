@@ -55,10 +55,11 @@ struct MuListOf {
 using MuTensors = MuListOf<MuTensor, kMuBatch>;
 using MuMatrices = MuListOf<MuMatrix, kMuBatch>;
 
-// Values between rows of a matrix in the workspace, its columns a multiple of 64: an odd
-// multiple, so that the same columns of consecutive rows lie in different channels of the L2
-// (rows of 8192 bytes put all of a tile's 128-byte pieces into one).
-__host__ __device__ constexpr int64_t mu_ld(int64_t cols) { return (cols / 64 | 1) * 64; }
+// Matrices in the workspace lie in blocks of 64 rows x 32 columns, 4 KB each, the blocks of a row of
+// blocks one after the other: what a tile takes of 32 values of the contraction is then whole
+// kilobytes, along rows and down columns. (Row-major, a transfer touched 16 rows, each in a page of
+// its own where they are long.) Elements before row r (a multiple of 32) of column 0:
+__host__ __device__ constexpr int64_t mu_rows(int64_t r, int64_t cols) { return (r / 64 * (cols / 32) * 64 + r % 64) * 32; }
 
 // A matrix in the workspace (offsets in bytes): two buffers of X's high parts and one of the
 // low parts ([mp][np] fp16), off-diagonal A and B ([mp][mp] fp16), the diagonal of A and
@@ -66,8 +67,8 @@ __host__ __device__ constexpr int64_t mu_ld(int64_t cols) { return (cols / 64 | 
 struct MuPlace {
     int64_t x, lo, a, b, d, q, part, total;
     __host__ __device__ MuPlace(int64_t mp, int64_t np, int64_t parts) {
-        const int64_t s = mp * mu_ld(mp) * 2;
-        x = mp * mu_ld(np) * 2;
+        const int64_t s = mp * mp * 2;
+        x = mp * np * 2;
         lo = 2 * x;
         a = 3 * x;
         b = a + s;
@@ -90,9 +91,9 @@ struct MuPoly {       // X <- a X + (b A + c A^2) X
 };
 
 // Square tiles of a product.
-enum MuForm { kMuSmall = 0, kMuMedium, kMuLarge, kMuForms };
-constexpr int kMuFormTile[kMuForms] = {64, 128, 256};
-constexpr int kMuFormThreads[kMuForms] = {256, 256, 256};
+enum MuForm { kMuSmall = 0, kMuMedium, kMuThreeQuarters, kMuLarge, kMuForms };
+constexpr int kMuFormTile[kMuForms] = {64, 128, 192, 256};
+constexpr int kMuTileThreads = 256;
 
 template <int N>
 struct MuLastOf {     // the last step's results go to the caller's tensors

@@ -50,6 +50,11 @@ __device__ __forceinline__ uint32_t mu_item(const MuListOf<T, N>& l, int k, uint
     return N == 1 ? id : id - l.first[k];
 }
 
+// Element (r, c) of a matrix of `cols` columns in the workspace.
+__device__ __forceinline__ int64_t mu_at(int r, int c, int cols) {
+    return (static_cast<int64_t>(r >> 6) * (cols >> 5) + (c >> 5)) * 2048 + (r & 63) * 32 + (c & 31);
+}
+
 // ----------------------------------------------------------------------------- the caller's tensors
 
 // 8 values of matrix b of the gradient (or input) from element i of its rows on, the first
@@ -239,7 +244,7 @@ __global__ __launch_bounds__(kMuThreads) void k_mu_scatter(MuListOf<MuTensor, N>
             uint32_t h[kVec], o[kVec];
 #pragma unroll
             for (int e = 0; e < kVec; ++e) mu_split(e < valid ? static_cast<float>(u[e] * f) : 0.0f, h[e], o[e]);
-            const int64_t i = (static_cast<int64_t>(r0 + r) * mu_ld(t.np) + c0 + q * kVec) * 2;
+            const int64_t i = mu_at(r0 + r, c0 + q * kVec, t.np) * 2;
             *gst<u32x4>(w + at.hi(0) + i) = u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
             *gst<u32x4>(w + at.lo + i) = u32x4{o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16};
         } else {
@@ -255,7 +260,7 @@ __global__ __launch_bounds__(kMuThreads) void k_mu_scatter(MuListOf<MuTensor, N>
         uint32_t h[kVec], o[kVec];
 #pragma unroll
         for (int e = 0; e < kVec; ++e) mu_split(tile[q * kVec + e][r], h[e], o[e]);
-        const int64_t i = (static_cast<int64_t>(r0 + r) * mu_ld(t.np) + c0 + q * kVec) * 2;
+        const int64_t i = mu_at(r0 + r, c0 + q * kVec, t.np) * 2;
         *gst<u32x4>(w + at.hi(0) + i) = u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
         *gst<u32x4>(w + at.lo + i) = u32x4{o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16};
     }
@@ -272,21 +277,17 @@ template <int T, int WM, int NW>
 struct MuTileOf {
     static constexpr int kT = T, kWM = WM, kWN = NW / WM, kNW = NW;
     static constexpr int MB = T / 32 / WM, NB = T / 32 / (NW / WM);
-    static constexpr int kDepth = 5;
+    static constexpr int kDepth = T == 192 ? 6 : 5;
     static constexpr int kOperand = T * 64;  // bytes of one operand's stage
     static constexpr int kStage = 2 * kOperand;
     static constexpr int kLds = kDepth * kStage;
+    static constexpr int kBlocks = T >= 192 ? 1 : T == 128 ? 2 : 4;  // per CU
 };
 template <int F> struct MuTiles;
 template <> struct MuTiles<kMuSmall> : MuTileOf<64, 2, 4> {};
 template <> struct MuTiles<kMuMedium> : MuTileOf<128, 2, 4> {};
+template <> struct MuTiles<kMuThreeQuarters> : MuTileOf<192, 2, 4> {};
 template <> struct MuTiles<kMuLarge> : MuTileOf<256, 2, 4> {};
-
-// Position of 16-byte chunk c of row r of a tile read transposed: the 8 rows that a read
-// touches 64 bytes of then lie on different banks (rows 8 apart share them, twice is what
-// 512 bytes take).
-template <int T>
-__device__ __forceinline__ int mu_swz_tr(int r) { return T >= 128 ? 4 * (r & 3) : 4 * ((r >> 1) & 1); }
 
 // 16 bytes per lane from base + offset into LDS, lane l at dst + 16 l. In asm, because before
 // every LDS read the compiler would wait for all of its own transfers (it cannot tell what they
@@ -303,85 +304,75 @@ __device__ __forceinline__ u32x4 mu_lds(uint32_t a) {
     return *(const __attribute__((address_space(3))) u32x4*)static_cast<uintptr_t>(a);
 }
 
-// acc += the tile's product over `steps` steps of 32 values: P's rows i0 .. with lines of ldp
-// values (TR: P is [contraction][columns], columns i0 ..), Q's rows j0 ... Rows past the
-// operands' end (columns, TR) repeat the last ones; they reach values that are not stored.
+// acc += the tile's product over `steps` steps of 32 values, from step k0 on: P's rows i0 .. (TR:
+// its columns, the contraction runs down its rows), Q's rows j0 .., matrices of cols_p and cols_q
+// columns. Blocks past the operands' end (rows_p and rows_q: columns_p, TR) repeat the last ones;
+// they reach values that are not stored.
 // A step's operands go straight into their stage, four steps ahead. The fragments of 16 values
 // of the contraction are read while the ones before are multiplied; the barrier of a step comes
 // before its last multiplication, when its stage has been read and the next one has landed: so
 // one wave per SIMD (a large tile) keeps its matrix core busy. Past the end the last step is
 // fetched again, for equal counts of transfers.
 template <class M, bool TR>
-__device__ __forceinline__ void mu_accumulate(const uint16_t* P, int ldp, int rows_p, const uint16_t* Q, int ldq, int rows_q,
+__device__ __forceinline__ void mu_accumulate(const uint16_t* P, int cols_p, int rows_p, const uint16_t* Q, int cols_q, int rows_q,
                                               int i0, int j0, int k0, int steps, uint8_t* lds, f32x16 (&acc)[M::MB][M::NB]) {
-    constexpr int T = M::kT, NW = M::kNW, kRB = T * 2, kCount = T / 16 / NW, kAll = 2 * kCount;
+    constexpr int T = M::kT, NW = M::kNW, kCount = T / 16 / NW, kAll = 2 * kCount;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), h = lane >> 5;
     const uint32_t base = uniform(static_cast<int>(lds_addr(lds)));
     steps = uniform(steps);  // (the transfers' addresses and counts stay in scalar registers)
-    ldp = uniform(ldp);
-    // transfers: 1 KB each, kCount of either operand per wave. Chunk c of row r (64 bytes) lies
-    // at position c ^ (r >> 2 & 3): 16 rows read at one chunk then touch every bank once.
+    cols_p = uniform(cols_p);
+    // Transfers: 1 KB each, 16 rows of a block, kCount of either operand per wave. In LDS a row's
+    // chunk c (16 bytes) lies at position c ^ (row >> 2 & 3): 16 rows read at one chunk then touch
+    // every bank once. TR: as they come; a transposed read's 8 rows of 64 bytes do so too.
     uint32_t op[kCount], oq[kCount];
     const uint32_t chunk = ((lane & 3) ^ ((lane >> 4) & 3)) * 16;
-    const uint8_t* cp;
-    const uint8_t* cq = uniform(reinterpret_cast<const uint8_t*>(Q) + (static_cast<int64_t>(j0) * ldq + k0) * 2);
+    const uint8_t* cp = uniform(reinterpret_cast<const uint8_t*>(P) +
+                                (TR ? static_cast<int64_t>(k0 >> 1) * cols_p * 128 + (k0 & 1) * 2048 + static_cast<int64_t>(i0) * 128
+                                    : static_cast<int64_t>(i0) * cols_p * 2 + static_cast<int64_t>(k0) * 4096));
+    const uint8_t* cq = uniform(reinterpret_cast<const uint8_t*>(Q) + static_cast<int64_t>(j0) * cols_q * 2 + static_cast<int64_t>(k0) * 4096);
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
-        const int r = 16 * (wave + i * NW) + (lane >> 2);
-        oq[i] = static_cast<uint32_t>(min(r, rows_q - 1 - j0)) * static_cast<uint32_t>(ldq) * 2u + chunk;
+        const int t = wave + i * NW;  // 16 rows t of the tile; TR: half t & 1 of a block's 32 rows
+        oq[i] = static_cast<uint32_t>(min(t >> 2, (rows_q - j0) / 64 - 1)) * static_cast<uint32_t>(cols_q) * 128u +
+                (16 * (t & 3) + (lane >> 2)) * 64u + chunk;
+        op[i] = TR ? static_cast<uint32_t>(min(t >> 1, (rows_p - i0) / 32 - 1)) * 4096u + (t & 1) * 1024u + lane * 16u
+                   : static_cast<uint32_t>(min(t >> 2, (rows_p - i0) / 64 - 1)) * static_cast<uint32_t>(cols_p) * 128u +
+                         (16 * (t & 3) + (lane >> 2)) * 64u + chunk;
     }
-    if constexpr (TR) {
-        constexpr int kLine = kRB / 16, kRows = 64 / kLine;  // lanes per row, rows per transfer
-        cp = uniform(reinterpret_cast<const uint8_t*>(P) + (static_cast<int64_t>(k0) * ldp + i0) * 2);
-#pragma unroll
-        for (int i = 0; i < kCount; ++i) {
-            const int r = kRows * (wave + i * NW) + lane / kLine;
-            const int c = (lane % kLine) ^ mu_swz_tr<T>(r);
-            op[i] = static_cast<uint32_t>(r) * static_cast<uint32_t>(ldp) * 2u + min(c * 8, rows_p - 8 - i0) * 2u;
-        }
-    } else {
-        cp = uniform(reinterpret_cast<const uint8_t*>(P) + (static_cast<int64_t>(i0) * ldp + k0) * 2);
-#pragma unroll
-        for (int i = 0; i < kCount; ++i) {
-            const int r = 16 * (wave + i * NW) + (lane >> 2);
-            op[i] = static_cast<uint32_t>(min(r, rows_p - 1 - i0)) * static_cast<uint32_t>(ldp) * 2u + chunk;
-        }
-    }
-    const int64_t step_p = TR ? static_cast<int64_t>(ldp) * 64 : 64;
+    // from one step of P to the next: TR: the other half of a row of blocks, or the next row
+    const int64_t step_p = TR ? static_cast<int64_t>(cols_p) * 128 - 2048 : 4096;
     // The i-th transfer of an operand's next step.
     int next_p = 1, next_q = 1;
     auto fetch_p = [&](uint32_t stage, int i) {
         mu_fetch16(cp, op[i], base + stage + (wave + i * NW) * 1024);
-        if (i == kCount - 1) cp += next_p++ < steps ? step_p : 0;
+        if (i == kCount - 1) {
+            cp += next_p >= steps ? 0 : TR && (next_p + k0) % 2 != 0 ? 2048 : step_p;
+            ++next_p;
+        }
     };
     auto fetch_q = [&](uint32_t stage, int i) {
         mu_fetch16(cq, oq[i], base + stage + M::kOperand + (wave + i * NW) * 1024);
-        if (i == kCount - 1) cq += next_q++ < steps ? 64 : 0;
+        if (i == kCount - 1) cq += next_q++ < steps ? 4096 : 0;
     };
     // fragments: the lane's addresses in the first stage
     const int wm = wave / M::kWN, wn = wave % M::kWN;
-    uint32_t pa[4], qa[2];
+    uint32_t pa[2], qa[2];
     const int sw = (lane >> 2) & 3;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         qa[s] = base + M::kOperand + (wn * 32 * M::NB + (lane & 31)) * 64 + (((2 * s + h) ^ sw) << 4);
-        if constexpr (!TR) pa[s] = base + (wm * 32 * M::MB + (lane & 31)) * 64 + (((2 * s + h) ^ sw) << 4);
+        pa[s] = base + (wm * 32 * M::MB + (lane & 31)) * 64 + (((2 * s + h) ^ sw) << 4);
     }
-    if constexpr (TR) {
-        const int gq = lane >> 4, eq = (lane >> 2) & 3;
-#pragma unroll
-        for (int i = 0; i < M::MB; ++i) {
-            const int col = wm * 32 * M::MB + 32 * i + 16 * (gq & 1) + 4 * (lane & 3);
-            pa[i] = base + (8 * h + eq) * kRB + (((col >> 3) ^ mu_swz_tr<T>(eq)) << 4) + (col & 7) * 2;
-        }
-    }
+    // TR: 16 lanes read 4 rows of 16 columns; columns 16 on in the next 16 lanes, rows 8 on in the other half
+    const uint32_t pt = base + wm * M::MB * 2048 + (8 * h + ((lane >> 2) & 3)) * 64 + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
     struct Frags {
         u32x4 p[M::MB], q[M::NB];
     };
     auto read_q = [&](Frags& f, uint32_t stage, int s, int j) { f.q[j] = mu_lds(qa[s] + stage + j * 2048); };
     auto read_p = [&](Frags& f, uint32_t stage, int s, int i) {
         if constexpr (TR) {
-            const u32x2 a = mu_lds_tr(pa[i] + stage + 16 * s * kRB), b = mu_lds_tr(pa[i] + stage + (16 * s + 4) * kRB);
+            const uint32_t a0 = pt + stage + i * 2048 + s * 1024;
+            const u32x2 a = mu_lds_tr(a0), b = mu_lds_tr(a0 + 256);
             f.p[i] = u32x4{a.x, a.y, b.x, b.y};
         } else {
             f.p[i] = mu_lds(pa[s] + stage + i * 2048);
@@ -501,8 +492,9 @@ __device__ __forceinline__ void mu_zero(f32x16 (&acc)[M::MB][M::NB]) {
 template <class M>
 struct MuRound {
     static constexpr int kI = 32 * M::MB;
-    static constexpr int kLanes = kI / 8, kRows = 64 / kLanes, kIters = 32 / kRows;  // 16 bytes per lane
-    static constexpr int kBytes = 32 * kI * 2;
+    static constexpr int kP = M::MB == 3 ? 128 : kI;  // values from column to column in LDS: a power of two
+    static constexpr int kIters = kI / 16;  // 1 KB accesses to memory per round: 16 columns of a block each
+    static constexpr int kBytes = 32 * kP * 2;
     typedef __attribute__((address_space(3))) u32x2 L2;
     typedef __attribute__((address_space(3))) u32x4 L4;
     typedef __attribute__((address_space(3))) f32x4 F4;
@@ -521,8 +513,8 @@ struct MuRound {
     // Bytes of chunk c (4 values) of column j: columns that an access touches at one chunk lie on
     // different banks; columns 16 apart in the two halves of 16 bytes.
     __device__ static uint32_t at(int j, int c) {
-        constexpr int kPer = 128 / kI;  // columns per 256 bytes
-        return j * (kI * 2) + ((c ^ 2 * (j / kPer & (kI / 8 - 1)) ^ (j >> 4 & 1)) << 3);
+        constexpr int kPer = 128 / kP;  // columns per 256 bytes
+        return j * (kP * 2) + ((c ^ 2 * (j / kPer & (kP / 8 - 1)) ^ (j >> 4 & 1)) << 3);
     }
     __device__ u32x2 get(int array, int ii, int v) const {
         return *(const L2*)static_cast<uintptr_t>(base + array * kBytes + at(j, 8 * ii + 2 * v + h));
@@ -530,19 +522,26 @@ struct MuRound {
     __device__ void put(int array, int ii, int v, u32x2 w) const {
         *(L2*)static_cast<uintptr_t>(base + array * kBytes + at(j, 8 * ii + 2 * v + h)) = w;
     }
-    // The lane's 16 bytes of memory rows: column row(e), rows col() .. col() + 7.
-    __device__ int row(int e) const { return e * kRows + lane / kLanes; }
-    __device__ int col() const { return lane % kLanes * 8; }
-    __device__ uint32_t line(int array, int e) const {  // (the 16 bytes; their halves are swapped from column 16 on)
-        return base + array * kBytes + (at(row(e), 2 * (lane % kLanes)) & ~8u);
+    // The lane's 16 bytes of access e: column row(e) (a row of memory), rows col(e) .. + 7.
+    __device__ int row(int e) const { return 16 * (e & 1) + (lane >> 2); }
+    __device__ int col(int e) const { return 32 * (e >> 1) + (lane & 3) * 8; }
+    __device__ uint32_t line(int array, int e) const {  // (their halves are swapped from column 16 on)
+        return base + array * kBytes + (at(row(e), col(e) / 4) & ~8u);
     }
     __device__ u32x4 get_line(int array, int e) const {
         const u32x4 w = *(const L4*)static_cast<uintptr_t>(line(array, e));
-        return e * kRows < 16 ? w : u32x4{w.z, w.w, w.x, w.y};
+        return e & 1 ? u32x4{w.z, w.w, w.x, w.y} : w;
     }
     __device__ void put_line(int array, int e, u32x4 w) const {
-        *(L4*)static_cast<uintptr_t>(line(array, e)) = e * kRows < 16 ? w : u32x4{w.z, w.w, w.x, w.y};
+        *(L4*)static_cast<uintptr_t>(line(array, e)) = e & 1 ? u32x4{w.z, w.w, w.x, w.y} : w;
     }
+    // Where they are in a matrix of `cols` columns in the workspace, of the round from column j0 on:
+    // a kilobyte, and whether the matrix has it.
+    __device__ uint16_t* place(uint16_t* s, int cols, int j0, int e) const {
+        const int64_t at = mu_rows(j0 + 16 * (e & 1), cols) + static_cast<int64_t>(ib + 32 * (e >> 1)) * 64;
+        return const_cast<uint16_t*>(reinterpret_cast<const uint16_t*>(uniform(reinterpret_cast<const uint8_t*>(s + at)))) + lane * 8;
+    }
+    __device__ bool has(int rows, int cols, int j0, int e) const { return j0 < rows && ib + 32 * (e >> 1) < cols; }
     // 8 columns, from turned_col() on, of row turned_row(t), t < kI / 16.
     __device__ int turned_row(int t) const { return 16 * t + (lane & 15); }
     __device__ int turned_col() const { return lane >> 4 << 3; }
@@ -551,8 +550,8 @@ struct MuRound {
         const u32x2 a = mu_lds_tr(base + at(r, c)), b = mu_lds_tr(base + at(r + 4, c));
         return u32x4{a.x, a.y, b.x, b.y};
     }
-    // fp32 values in chunks of 4, [32 j][kI i], at an offset of the share.
-    __device__ uint32_t at32(int j, int c) const { return j * (kI * 4) + ((c ^ (j & (kI / 4 - 1))) << 4); }
+    // fp32 values in chunks of 4, [32 j][kP i], at an offset of the share.
+    __device__ uint32_t at32(int j, int c) const { return j * (kP * 4) + ((c ^ (j & (kP / 4 - 1))) << 4); }
     __device__ void put32(uint32_t offset, int ii, int v, f32x4 w) const {
         *(F4*)static_cast<uintptr_t>(base + offset + at32(j, 8 * ii + 2 * v + h)) = w;
     }
@@ -564,28 +563,20 @@ struct MuRound {
     }
 };
 
-// Element (row, col) of the rows from `row0` on, of a matrix with ld values between rows: the rows'
-// start is the same in every lane, the rest an offset of 32 bits (a tile's rows).
-__device__ __forceinline__ uint16_t* mu_element(uint16_t* s, int64_t ld, int row0, int row, int col) {
-    uint8_t* const base = const_cast<uint8_t*>(uniform(reinterpret_cast<const uint8_t*>(s + row0 * ld)));
-    return reinterpret_cast<uint16_t*>(base + ((row - row0) * static_cast<uint32_t>(ld) + col) * 2u);
-}
-
-// A finished round of a symmetric product: columns j0 .. and, turned round, rows j0 ...
+// A finished round of a symmetric product of mp rows: columns j0 .. and, turned round, rows j0 ...
 template <class M>
-__device__ __forceinline__ void mu_store_sym(const MuRound<M>& r, uint16_t* s, int ld, int mp, int j0) {
+__device__ __forceinline__ void mu_store_sym(const MuRound<M>& r, uint16_t* s, int mp, int j0) {
     using R = MuRound<M>;
 #pragma unroll
-    for (int e = 0; e < R::kIters; ++e) {
-        const int i = r.ib + r.col(), j = j0 + r.row(e);
-        const u32x4 w = r.get_line(0, e);
-        if (i < mp && j < mp) *gst<u32x4>(mu_element(s, ld, j0, j, i)) = w;
-    }
+    for (int e = 0; e < R::kIters; ++e)
+        if (r.has(mp, mp, j0, e)) *gst<u32x4>(r.place(s, mp, j0, e)) = r.get_line(0, e);
 #pragma unroll
     for (int t = 0; t < R::kI / 16; ++t) {
-        const int i = r.ib + r.turned_row(t), j = j0 + r.turned_col();
-        const u32x4 w = r.get_turned(t);
-        if (i < mp && j < mp) *gst<u32x4>(mu_element(s, ld, r.ib, i, j)) = w;
+        const int i = r.ib + 16 * t;
+        if (i >= mp || j0 >= mp) continue;
+        const int64_t at = mu_rows(i, mp) + static_cast<int64_t>(j0) * 64;  // 16 rows of a block: a kilobyte
+        uint8_t* const p = const_cast<uint8_t*>(uniform(reinterpret_cast<const uint8_t*>(s + at)));
+        *gst<u32x4>(p + (r.lane & 15) * 64 + (r.lane >> 4) * 16) = r.get_turned(t);
     }
 }
 
@@ -593,7 +584,7 @@ __device__ __forceinline__ void mu_store_sym(const MuRound<M>& r, uint16_t* s, i
 // order, so A is symmetric to the bit), 2^8 times; the diagonal in fp32. A contraction in parts
 // (small tiles only) leaves each part's fp32 sums for k_mu_join.
 template <int F, int N>
-__global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_gram(MuListOf<MuMatrix, N> l, int src) {
+__global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_gram(MuListOf<MuMatrix, N> l, int src) {
     using M = MuTiles<F>;
     __shared__ __attribute__((aligned(16))) uint8_t lds[M::kLds];
     const uint32_t id = mu_swizzle(blockIdx.x, l.blocks);
@@ -612,10 +603,10 @@ __global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_gram(MuListOf<MuMatrix
     const MuPlace at(m.mp, m.np, m.parts);
     uint8_t* const w = m.ws + b * m.stride;
     const uint16_t* x = reinterpret_cast<const uint16_t*>(w + at.hi(src));
-    const int k0 = part * m.steps * 64, steps = min(m.steps, m.np / 64 - part * m.steps);
+    const int k0 = part * m.steps * 2, steps = min(m.steps, m.np / 64 - part * m.steps);
     f32x16 acc[M::MB][M::NB];
     mu_zero<M>(acc);
-    mu_accumulate<M, false>(x, mu_ld(m.np), m.mp, x, mu_ld(m.np), m.mp, ti * M::kT, tj * M::kT, k0, 2 * steps, lds, acc);
+    mu_accumulate<M, false>(x, m.np, m.mp, x, m.np, m.mp, ti * M::kT, tj * M::kT, k0, 2 * steps, lds, acc);
     if (F == kMuSmall && m.parts > 1) {
         const MuRound<M> r(lds, ti * M::kT, tj * M::kT, 0);
         float* const o = reinterpret_cast<float*>(w + at.part) + static_cast<int64_t>(part) * m.mp * m.mp;
@@ -658,7 +649,7 @@ __global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_gram(MuListOf<MuMatrix
                         }
             }
         }
-        mu_store_sym(r, o, mu_ld(m.mp), m.mp, j0);
+        mu_store_sym(r, o, m.mp, j0);
     }
 }
 
@@ -686,21 +677,20 @@ __global__ __launch_bounds__(kMuThreads) void k_mu_join(MuListOf<MuMatrix, N> l)
         v[e] *= kMuLift;
     }
     uint16_t* const o = reinterpret_cast<uint16_t*>(w + at.a);
-    const int ld = mu_ld(m.mp);
     // (rows past the diagonal belong to the other half: their values were not summed there)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         if (i + e > j) break;
         const uint16_t c = i + e == j ? 0 : __builtin_bit_cast(uint16_t, static_cast<_Float16>(v[e]));
-        *gst<uint16_t>(o + static_cast<int64_t>(j) * ld + i + e) = c;
-        *gst<uint16_t>(o + static_cast<int64_t>(i + e) * ld + j) = c;
+        *gst<uint16_t>(o + mu_at(j, i + e, m.mp)) = c;
+        *gst<uint16_t>(o + mu_at(i + e, j, m.mp)) = c;
     }
 }
 
 // B = b A + c A^2 from A's off-diagonal part O and its diagonal d, 2^8 times off the diagonal,
 // q = a + B_ii on it.
 template <int F, int N>
-__global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_poly(MuListOf<MuMatrix, N> l, MuPoly p) {
+__global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_poly(MuListOf<MuMatrix, N> l, MuPoly p) {
     using M = MuTiles<F>;
     __shared__ __attribute__((aligned(16))) uint8_t lds[M::kLds];
     const uint32_t id = mu_swizzle(blockIdx.x, l.blocks);
@@ -716,10 +706,9 @@ __global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_poly(MuListOf<MuMatrix
     const MuPlace at(m.mp, m.np, m.parts);
     uint8_t* const w = m.ws + b * m.stride;
     const uint16_t* o = reinterpret_cast<const uint16_t*>(w + at.a);
-    const int ld = mu_ld(m.mp);
     f32x16 acc[M::MB][M::NB];
     mu_zero<M>(acc);
-    mu_accumulate<M, false>(o, ld, m.mp, o, ld, m.mp, ti * M::kT, tj * M::kT, 0, m.mp / 32, lds, acc);
+    mu_accumulate<M, false>(o, m.mp, m.mp, o, m.mp, m.mp, ti * M::kT, tj * M::kT, 0, m.mp / 32, lds, acc);
     uint16_t* const out = reinterpret_cast<uint16_t*>(w + at.b);
     const float* const d = reinterpret_cast<const float*>(w + at.d);
     float* const q = reinterpret_cast<float*>(w + at.q);
@@ -728,7 +717,7 @@ __global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_poly(MuListOf<MuMatrix
     auto load = [&](int j0, u32x4* f) {  // O's round
 #pragma unroll
         for (int e = 0; e < R::kIters; ++e)
-            f[e] = *gld<u32x4>(mu_element(const_cast<uint16_t*>(o), ld, tj * M::kT, min(j0 + r.row(e), m.mp - 1), min(r.ib + r.col(), m.mp - 8)));
+            if (r.has(m.mp, m.mp, j0, e)) f[e] = *gld<u32x4>(r.place(const_cast<uint16_t*>(o), m.mp, j0, e));
     };
     u32x4 next[R::kIters];
     load(r.jb, next);
@@ -770,7 +759,7 @@ __global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_poly(MuListOf<MuMatrix
                 r.put(0, ii, v, mu_pack4(y[0], y[1], y[2], y[3]));
             }
         }
-        mu_store_sym(r, out, ld, m.mp, j0);
+        mu_store_sym(r, out, m.mp, j0);
     }
 }
 
@@ -791,7 +780,7 @@ __device__ __forceinline__ void mu_finish8(const MuTensor& t, bool update, float
 }
 
 template <int F, int N, class Last>
-__global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_apply(MuListOf<MuMatrix, N> l, int src, float linear, Last z) {
+__global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_apply(MuListOf<MuMatrix, N> l, int src, float linear, Last z) {
     using M = MuTiles<F>;
     constexpr bool kLast = !std::is_same<Last, MuNone>::value;
     __shared__ __attribute__((aligned(16))) uint8_t lds[M::kLds];
@@ -810,10 +799,9 @@ __global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_apply(MuListOf<MuMatri
     uint8_t* const w = m.ws + b * m.stride;
     const uint16_t* const x = reinterpret_cast<const uint16_t*>(w + at.hi(src));
     uint16_t* const lo = reinterpret_cast<uint16_t*>(w + at.lo);
-    const int ld = mu_ld(m.np);
     f32x16 acc[M::MB][M::NB];
     mu_zero<M>(acc);
-    mu_accumulate<M, true>(x, ld, m.np, reinterpret_cast<const uint16_t*>(w + at.b), mu_ld(m.mp), m.mp, ti * M::kT, tj * M::kT, 0,
+    mu_accumulate<M, true>(x, m.np, m.np, reinterpret_cast<const uint16_t*>(w + at.b), m.mp, m.mp, ti * M::kT, tj * M::kT, 0,
                            m.mp / 32, lds, acc);
     const float* const q = reinterpret_cast<const float*>(w + at.q);
     uint16_t* const hi = reinterpret_cast<uint16_t*>(w + at.hi(src ^ 1));
@@ -824,9 +812,9 @@ __global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_apply(MuListOf<MuMatri
     auto load = [&](int j0, u32x4* f) {
 #pragma unroll
         for (int e = 0; e < R::kIters; ++e) {
-            const int j = min(j0 + r.row(e), m.mp - 1), i = min(r.ib + r.col(), m.np - 8);
-            f[2 * e] = *gld<u32x4>(mu_element(const_cast<uint16_t*>(x), ld, tj * M::kT, j, i));
-            f[2 * e + 1] = *gld<u32x4>(mu_element(lo, ld, tj * M::kT, j, i));
+            if (!r.has(m.mp, m.np, j0, e)) continue;
+            f[2 * e] = *gld<u32x4>(r.place(const_cast<uint16_t*>(x), m.np, j0, e));
+            f[2 * e + 1] = *gld<u32x4>(r.place(lo, m.np, j0, e));
         }
     };
     u32x4 next[2 * R::kIters];
@@ -868,12 +856,9 @@ __global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_apply(MuListOf<MuMatri
         if constexpr (!kLast) {
 #pragma unroll
             for (int e = 0; e < R::kIters; ++e) {
-                const int i = r.ib + r.col(), j = j0 + r.row(e);
-                const u32x4 a = r.get_line(0, e), b = r.get_line(1, e);
-                if (i < m.np && j < m.mp) {
-                    *gst<u32x4>(mu_element(hi, ld, tj * M::kT, j, i)) = a;
-                    *gst<u32x4>(mu_element(lo, ld, tj * M::kT, j, i)) = b;
-                }
+                if (!r.has(m.mp, m.np, j0, e)) continue;
+                *gst<u32x4>(r.place(hi, m.np, j0, e)) = r.get_line(0, e);
+                *gst<u32x4>(r.place(lo, m.np, j0, e)) = r.get_line(1, e);
             }
         } else {
             const MuTensor& t = z.t.d[k];
@@ -890,10 +875,10 @@ __global__ __launch_bounds__(kMuFormThreads[F]) void k_mu_apply(MuListOf<MuMatri
                 }
             } else {
 #pragma unroll 2
-                for (int e = 0; e < R::kIters; ++e) {
-                    const int i = r.ib + r.col(), j = j0 + r.row(e);
+                for (int e = r.lane; e < 32 * R::kI / 8; e += 64) {  // 8 values of a row j each
+                    const int row = e / (R::kI / 8), col = e % (R::kI / 8) * 8, i = r.ib + col, j = j0 + row;
                     const int valid = j < t.rows ? clamp_valid(static_cast<int64_t>(t.cols) - i) : 0;
-                    const f32x4 a = r.get32(kPlanes, r.row(e), r.col() / 4), c = r.get32(kPlanes, r.row(e), r.col() / 4 + 1);
+                    const f32x4 a = r.get32(kPlanes, row, col / 4), c = r.get32(kPlanes, row, col / 4 + 1);
                     float v[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
                     if (valid > 0) mu_finish8(t, z.update, z.decay, first + j * t.ldx + i, valid, v);
                 }
@@ -913,6 +898,7 @@ static void with_list(const List& l, Fn f) {
 template <class Fn>
 static void with_form(int form, Fn f) {
     if (form == kMuLarge) f(std::integral_constant<int, kMuLarge>{});
+    else if (form == kMuThreeQuarters) f(std::integral_constant<int, kMuThreeQuarters>{});
     else if (form == kMuMedium) f(std::integral_constant<int, kMuMedium>{});
     else f(std::integral_constant<int, kMuSmall>{});
 }
@@ -933,7 +919,7 @@ void launch_mu_gram(const MuMatrices& m, int form, int src, hipStream_t s) {
     if (m.blocks == 0) return;
     with_list(m, [&](const auto& l, auto n) {
         with_form(form, [&](auto f) {
-            hipLaunchKernelGGL((k_mu_gram<decltype(f)::value, decltype(n)::value>), dim3(m.blocks), dim3(kMuFormThreads[form]), 0, s, l, src);
+            hipLaunchKernelGGL((k_mu_gram<decltype(f)::value, decltype(n)::value>), dim3(m.blocks), dim3(kMuTileThreads), 0, s, l, src);
         });
     });
 }
@@ -948,7 +934,7 @@ void launch_mu_join(const MuMatrices& m, hipStream_t s) {
 void launch_mu_poly(const MuMatrices& m, int form, const MuPoly& p, hipStream_t s) {
     with_list(m, [&](const auto& l, auto n) {
         with_form(form, [&](auto f) {
-            hipLaunchKernelGGL((k_mu_poly<decltype(f)::value, decltype(n)::value>), dim3(m.blocks), dim3(kMuFormThreads[form]), 0, s, l, p);
+            hipLaunchKernelGGL((k_mu_poly<decltype(f)::value, decltype(n)::value>), dim3(m.blocks), dim3(kMuTileThreads), 0, s, l, p);
         });
     });
 }
@@ -958,7 +944,7 @@ void launch_mu_apply(const MuMatrices& m, int form, int src, float linear, const
         constexpr int N = decltype(n)::value;
         with_form(form, [&](auto f) {
             constexpr int F = decltype(f)::value;
-            const dim3 g(m.blocks), t(kMuFormThreads[F]);
+            const dim3 g(m.blocks), t(kMuTileThreads);
             if (!last) {
                 hipLaunchKernelGGL((k_mu_apply<F, N, MuNone>), g, t, 0, s, l, src, linear, MuNone{});
             } else if constexpr (N == 1) {
