@@ -2832,20 +2832,33 @@ int64_t mu_chunks(const std::vector<MuIn>& ts, std::vector<MuChunk>* out) {
     return most;
 }
 
-// The tile form of a pass: the one whose tiles, dealt to the CUs, are done first. A CU holds one
-// large tile, two medium or four small ones at a time; kMuFormCost is what a CU's load takes.
-constexpr int kMuFormLoad[kMuForms] = {4, 2, 1, 1};
-constexpr double kMuFormCost[kMuForms] = {0.45, 0.60, 0.6, 1.0};
+// The tile form of a pass: the one whose tiles, dealt to the CUs, are done first. A tile takes
+// kMuTileStart (kMuApplyStart where it also moves X) and kMuTileStep per 64 values of the
+// contraction, in microseconds, beside the others that a CU holds. Fitted to (measured, model):
+// A of 4096 x 4096 in 64-, 128-, 192- and 256-tiles 108 (116), 92 (97), 74 (67), 90 (94); of four of
+// them 430, 268, 261, 283 (426, 290, 268, 282); of 1024 x 1024 8, 12, 20, 28; X' of 4096 x 4096 205,
+// 144, 148, 134 and of four 1024 x 1024 20, 18, 27, 41. No form changes a result.
+constexpr double kMuTileStart[kMuForms] = {2, 4, 17, 20};
+constexpr double kMuApplyStart[kMuForms] = {2, 7, 24, 57};
+constexpr double kMuTileStep[kMuForms] = {0.17, 0.44, 0.78, 1.15};
 
+// tiles(tensor, side): its matrices' tiles and the steps of each.
 template <class Tiles>
-int mu_form(const std::vector<MuIn>& ts, const MuChunk& c, Tiles tiles) {
+int mu_form(const std::vector<MuIn>& ts, const MuChunk& c, const double* start, Tiles tiles) {
     int best = kMuSmall;
     double cost = 0.0;
     for (int f = 0; f < kMuForms; ++f) {
         int64_t n = 0;
-        for (const MuItem& i : c.items) n += i.count * tiles(ts[i.k], kMuFormTile[f]);
-        const double w = static_cast<double>(ceil_div(n, kCus * kMuFormLoad[f])) * kMuFormCost[f];
-        if (f == 0 || w <= cost) {
+        double all = 0.0;
+        for (const MuItem& i : c.items) {
+            int64_t count = 0, steps = 0;
+            tiles(ts[i.k], kMuFormTile[f], &count, &steps);
+            n += i.count * count;
+            all += static_cast<double>(i.count * count) * (start[f] + kMuTileStep[f] * static_cast<double>(steps));
+        }
+        if (n == 0) return kMuSmall;
+        const double w = all / static_cast<double>(n) * static_cast<double>(ceil_div(n, kCus));
+        if (f == 0 || w < cost) {
             best = f;
             cost = w;
         }
@@ -2963,13 +2976,19 @@ int mu_run(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, MuS
             }
         };
         auto square = [](int64_t side, int64_t tile) { const int64_t q = ceil_div(side, tile); return q * (q + 1) / 2; };
-        const int fg = mu_form(ts, c, [&](const MuIn& q, int64_t tile) {
-            int64_t parts, steps;
-            mu_gram_parts(q.mp(), q.np(), &parts, &steps);
-            return parts > 1 ? 0 : square(q.mp(), tile);
+        const int fg = mu_form(ts, c, kMuTileStart, [&](const MuIn& q, int64_t tile, int64_t* n, int64_t* steps) {
+            int64_t parts;
+            mu_gram_parts(q.mp(), q.np(), &parts, steps);
+            *n = parts > 1 ? 0 : square(q.mp(), tile);
         });
-        const int fp = mu_form(ts, c, [&](const MuIn& q, int64_t tile) { return square(q.mp(), tile); });
-        const int fa = mu_form(ts, c, [&](const MuIn& q, int64_t tile) { return ceil_div(q.mp(), tile) * ceil_div(q.np(), tile); });
+        const int fp = mu_form(ts, c, kMuTileStart, [&](const MuIn& q, int64_t tile, int64_t* n, int64_t* steps) {
+            *n = square(q.mp(), tile);
+            *steps = q.mp() / 64;
+        });
+        const int fa = mu_form(ts, c, kMuApplyStart, [&](const MuIn& q, int64_t tile, int64_t* n, int64_t* steps) {
+            *n = ceil_div(q.mp(), tile) * ceil_div(q.np(), tile);
+            *steps = q.mp() / 64;
+        });
         MuMatrices gram = all, parts = all, join = all, poly = all, apply = all;
         count(gram, [&](const MuMatrix& m) { return m.parts > 1 ? 0 : m.batch * square(m.mp, kMuFormTile[fg]); });
         count(parts, [&](const MuMatrix& m) { return m.parts > 1 ? m.batch * square(m.mp, kMuFormTile[kMuSmall]) * m.parts : 0; });
