@@ -805,13 +805,13 @@ std::vector<StatePtrs> state_ptrs(int op, int32_t n, const void* states) {
 enum Pass { kPassStats = 0, kPassFinalize, kPassRms, kPassScalars, kPassAfApply, kPassCameMom,
             kPassCameApply, kPassLambMoments, kPassLambApply, kPassStatsWide, kPassStatsTiled,
             kPassGaProject, kPassGaBack, kPassGaAdamw, kPassGaRefresh, kPassXnorm, kPassSumsqFold,
-            kPassMuMomentum, kPassMuScatter, kPassMuGram, kPassMuPoly, kPassMuApply, kPassCount };
+            kPassMuMomentum, kPassMuScatter, kPassMuGram, kPassMuPoly, kPassMuApply, kPassMuWhole, kPassCount };
 static_assert(kPassCount == MEO_NUM_PASSES, "pass table");
 const char* const kPassNames[kPassCount] = {"stats", "finalize", "rms", "scalars", "adafactor_apply",
                                             "came_mom", "came_apply", "lamb_moments", "lamb_apply",
                                             "stats_wide", "stats_tiled", "galore_project", "galore_back",
                                             "galore_adamw", "galore_refresh", "xnorm", "sumsq_fold",
-                                            "muon_momentum", "muon_scatter", "ns_gram", "ns_poly", "ns_apply"};
+                                            "muon_momentum", "muon_scatter", "ns_gram", "ns_poly", "ns_apply", "ns_whole"};
 
 struct ProfRec { int pass; hipEvent_t a, b; };
 std::mutex g_prof_mu;
@@ -2767,6 +2767,15 @@ struct MuIn {
     bool empty() const { return batch == 0 || rows == 0 || cols == 0; }
     int64_t mp() const { return ceil_div(std::min(rows, cols), kMuPad) * kMuPad; }
     int64_t np() const { return ceil_div(std::max(rows, cols), kMuPad) * kMuPad; }
+    int few() const { return mu_few(std::min(rows, cols), std::max(rows, cols)); }
+    // The power of two that values are held times: about the square root of the longer side, so that
+    // entries of a matrix with orthonormal rows are about 1.
+    int lift() const { return std::min(12, static_cast<int>(std::lround(0.5 * std::log2(static_cast<double>(std::max(rows, cols)))))); }
+    const void* g_at(int64_t b) const { return static_cast<const uint8_t*>(g) + b * rows * ldg * (gbf16 ? 2 : 4); }
+    void* x_at(int64_t b) const { return static_cast<uint8_t*>(x) + b * rows * ldx * (xbf16 ? 2 : 4); }
+    void* m_at(int64_t b) const { return m ? static_cast<uint8_t*>(m) + b * rows * cols * (mkind == 2 ? 1 : mkind == 1 ? 2 : 4) : nullptr; }
+    // (several matrices: whole groups)
+    float* ms_at(int64_t b) const { return m && mkind == 2 ? ms + b * rows * cols / kI8Group : nullptr; }
 };
 
 constexpr int64_t kMuMaxValues = int64_t{1} << 35;
@@ -2803,7 +2812,8 @@ int64_t mu_stride(const MuIn& t) {
     return align256(MuPlace(t.mp(), t.np(), parts).total);
 }
 
-// The list in chunks, in order; returns the workspace's bytes.
+// The list's larger matrices in chunks, in order; returns the workspace's bytes (some for every list
+// with anything in it, so that what a caller has to bring does not turn on a matrix' size).
 int64_t mu_chunks(const std::vector<MuIn>& ts, std::vector<MuChunk>* out) {
     int64_t most = 0, values = 0;
     MuChunk c;
@@ -2816,6 +2826,8 @@ int64_t mu_chunks(const std::vector<MuIn>& ts, std::vector<MuChunk>* out) {
     for (size_t k = 0; k < ts.size(); ++k) {
         const MuIn& t = ts[k];
         if (t.empty()) continue;
+        most = std::max<int64_t>(most, 256);
+        if (t.few()) continue;
         const int64_t size = t.mp() * t.np(), stride = mu_stride(t), parts = mu_norm_parts(t);
         for (int64_t b = 0; b < t.batch;) {
             if (!c.items.empty() && (values + size > kMuChunkValues || c.items.size() == kMuBatch)) close();
@@ -2913,6 +2925,63 @@ int check_mu_workspace(int64_t need, void* ws, size_t bytes, int dev) {
     return check_device_range(ws, bytes, dev, "workspace", MEO_EWORKSPACE);
 }
 
+// The small matrices, a block each: lists of up to kMuFewBatch tensors of a kind.
+constexpr int64_t kMuFewBlocks = 1 << 22;  // of a launch
+
+void mu_run_few(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, const MuStepArgs& step, float decay, bool update,
+                PassTimer& pt, hipStream_t s) {
+    MuFewArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.step = step;
+    a.decay = decay;
+    a.update = update;
+    a.steps = hp.steps;
+    for (int k = 0; k < hp.steps; ++k)
+        a.poly[k] = MuPoly{static_cast<float>(hp.coefficients[k][0]), static_cast<float>(hp.coefficients[k][1]),
+                           static_cast<float>(hp.coefficients[k][2])};
+    for (int rows : {16, 32, 64}) {
+        MuFewTensors l;
+        auto start = [&]() {
+            std::memset(&l, 0, sizeof l);
+            std::fill(std::begin(l.first), std::end(l.first), 0xffffffffu);
+        };
+        auto flush = [&]() {
+            if (l.n) {
+                launch_mu_few(l, rows, a, s);
+                pt.mark(kPassMuWhole);
+            }
+            start();
+        };
+        start();
+        for (const MuIn& t : ts) {
+            if (t.empty() || t.few() != rows) continue;
+            for (int64_t b = 0; b < t.batch;) {
+                if (l.n == kMuFewBatch || l.blocks == kMuFewBlocks) flush();
+                const int64_t count = std::min<int64_t>(t.batch - b, kMuFewBlocks - l.blocks);
+                l.first[l.n] = l.blocks;
+                MuFewTensor& d = l.d[l.n++];
+                d.g = t.g_at(b);
+                d.m = t.m_at(b);
+                d.ms = t.ms_at(b);
+                d.x = t.x_at(b);
+                d.ldg = static_cast<int32_t>(t.ldg);
+                d.ldx = static_cast<int32_t>(t.ldx);
+                d.rows = static_cast<int32_t>(t.rows);
+                d.cols = static_cast<int32_t>(t.cols);
+                d.batch = static_cast<int32_t>(count);
+                d.coef = t.coef;
+                d.gbf16 = t.gbf16;
+                d.xbf16 = t.xbf16;
+                d.mkind = t.mkind;
+                d.lift = static_cast<int16_t>(t.lift());
+                l.blocks += static_cast<uint32_t>(count);
+                b += count;
+            }
+        }
+        flush();
+    }
+}
+
 // The passes over a validated list. update: Muon's parameters (else results).
 int mu_run(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, MuStepArgs a, float decay, bool update, void* ws,
            size_t ws_bytes, int dev, hipStream_t s) {
@@ -2921,6 +2990,7 @@ int mu_run(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, MuS
     if (rc) return rc;
     a.eps = hp.eps;
     PassTimer pt(s);
+    mu_run_few(hp, ts, a, decay, update, pt, s);
     for (const MuChunk& c : chunks) {
         MuLast last;
         std::memset(&last, 0, sizeof last);
@@ -2933,15 +3003,12 @@ int mu_run(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, MuS
         for (int i = 0; i < t.n; ++i) {
             const MuItem& it = c.items[i];
             const MuIn& in = ts[it.k];
-            const int64_t size = in.rows * in.cols;
             MuTensor& d = t.d[i];
             MuMatrix& m = all.d[i];
-            d.g = static_cast<const uint8_t*>(in.g) + it.b0 * in.rows * in.ldg * (in.gbf16 ? 2 : 4);
-            d.x = static_cast<uint8_t*>(in.x) + it.b0 * in.rows * in.ldx * (in.xbf16 ? 2 : 4);
-            if (in.m) {
-                d.m = static_cast<uint8_t*>(in.m) + it.b0 * size * (in.mkind == 2 ? 1 : in.mkind == 1 ? 2 : 4);
-                if (in.mkind == 2) d.ms = in.ms + it.b0 * size / kI8Group;  // (several matrices: whole groups)
-            }
+            d.g = in.g_at(it.b0);
+            d.x = in.x_at(it.b0);
+            d.m = in.m_at(it.b0);
+            d.ms = in.ms_at(it.b0);
             d.ws = m.ws = static_cast<uint8_t*>(ws) + it.off;
             d.norm = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + it.norm);
             d.ldg = in.ldg;
@@ -2954,9 +3021,7 @@ int mu_run(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, MuS
             d.np = m.np = static_cast<int32_t>(in.np());
             d.parts = static_cast<int32_t>(mu_norm_parts(in));
             d.tiles_per_part = static_cast<int32_t>(mu_norm_span(in));
-            // about the square root of the longer side: entries of a matrix with orthonormal
-            // rows are then about 1
-            d.lift = std::min(12, static_cast<int>(std::lround(0.5 * std::log2(static_cast<double>(std::max(in.rows, in.cols))))));
+            d.lift = in.lift();
             m.lift = static_cast<float>(std::ldexp(1.0, d.lift));
             d.coef = in.coef;
             d.gbf16 = in.gbf16;

@@ -103,6 +103,39 @@ struct MuLastOf {     // the last step's results go to the caller's tensors
 };
 using MuLast = MuLastOf<kMuBatch>;
 
+// ---- matrices worked on by one block each, all steps in one launch
+
+// The rows that a matrix of shorter side `m` and longer side `n` takes (16, 32 or 64, the longer side
+// in blocks of 32); 0: it is not one of these. From the matrix alone: its result does not depend on
+// the list.
+__host__ __device__ constexpr int mu_few(int64_t m, int64_t n) {
+    const int64_t p = (n + 31) / 32 * 32;
+    return m <= 16 && p <= 4096 ? 16 : m <= 32 && p <= 2048 ? 32 : m <= 64 && p <= 768 ? 64 : 0;
+}
+constexpr int kMuFewBatch = 48;     // tensors per launch
+constexpr int kMuFewThreads = 512;
+
+struct MuFewTensor {  // fields as MuTensor's
+    const void* g;
+    void* m;
+    float* ms;
+    void* x;
+    int32_t ldg, ldx, rows, cols, batch;
+    float coef;
+    int16_t gbf16, xbf16, mkind, lift;
+};
+using MuFewTensors = MuListOf<MuFewTensor, kMuFewBatch>;
+
+struct MuFewArgs {
+    MuStepArgs step;
+    float decay;
+    int32_t update, steps;
+    MuPoly poly[16];
+};
+
+// rows: 16, 32 or 64, the same for all.
+void launch_mu_few(const MuFewTensors& t, int rows, const MuFewArgs& a, hipStream_t s);
+
 void launch_mu_momentum(const MuTensors& t, const MuStepArgs& a, hipStream_t s);
 void launch_mu_scatter(const MuTensors& t, const MuStepArgs& a, hipStream_t s);
 // A's off-diagonal part and diagonal from X (buffer src); with parts (kMuSmall only), their sums

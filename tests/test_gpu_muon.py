@@ -432,11 +432,12 @@ def test_memory_refusals():
 def test_profile_names_the_passes():
     _lib.meo_profile_enable(True)
     try:
-        orthogonalize(matrix((64, 64), 92))
+        orthogonalize([matrix((96, 128), 92), matrix((64, 64), 92), matrix((20, 10), 92)])
         got = _lib.meo_profile_collect()
     finally:
         _lib.meo_profile_enable(False)
     assert got["ns_gram"]["launches"] == got["ns_apply"]["launches"] == 5 and got["muon_scatter"]["launches"] == 1
+    assert got["ns_whole"]["launches"] == 2  # (of 16 and of 64 rows)
 
 
 # ------------------------------------------------------------------------------ Muon (front end)
