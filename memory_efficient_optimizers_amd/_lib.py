@@ -52,7 +52,7 @@ EXPORTS = [
     "meo_muon_defaults", "meo_muon_workspace_size", "meo_muon_validate", "meo_muon_step",
 ]
 MEO_NOALLOC_SCRATCH_BYTES = 64 << 20
-MEO_NUM_PASSES = 23
+MEO_NUM_PASSES = 24
 MEO_NS_MAX_STEPS = 16
 
 

@@ -805,13 +805,13 @@ std::vector<StatePtrs> state_ptrs(int op, int32_t n, const void* states) {
 enum Pass { kPassStats = 0, kPassFinalize, kPassRms, kPassScalars, kPassAfApply, kPassCameMom,
             kPassCameApply, kPassLambMoments, kPassLambApply, kPassStatsWide, kPassStatsTiled,
             kPassGaProject, kPassGaBack, kPassGaAdamw, kPassGaRefresh, kPassXnorm, kPassSumsqFold,
-            kPassMuMomentum, kPassMuScatter, kPassMuGram, kPassMuPoly, kPassMuApply, kPassMuWhole, kPassCount };
+            kPassMuMomentum, kPassMuScatter, kPassMuGram, kPassMuPoly, kPassMuApply, kPassMuWhole, kPassMuStrips, kPassCount };
 static_assert(kPassCount == MEO_NUM_PASSES, "pass table");
 const char* const kPassNames[kPassCount] = {"stats", "finalize", "rms", "scalars", "adafactor_apply",
                                             "came_mom", "came_apply", "lamb_moments", "lamb_apply",
                                             "stats_wide", "stats_tiled", "galore_project", "galore_back",
                                             "galore_adamw", "galore_refresh", "xnorm", "sumsq_fold",
-                                            "muon_momentum", "muon_scatter", "ns_gram", "ns_poly", "ns_apply", "ns_whole"};
+                                            "muon_momentum", "muon_scatter", "ns_gram", "ns_poly", "ns_apply", "ns_whole", "ns_strips"};
 
 struct ProfRec { int pass; hipEvent_t a, b; };
 std::mutex g_prof_mu;
@@ -2765,9 +2765,10 @@ struct MuIn {
     int16_t gbf16 = 0, xbf16 = 1, mkind = 0;
     float coef = 0.0f;
     bool empty() const { return batch == 0 || rows == 0 || cols == 0; }
-    int64_t mp() const { return ceil_div(std::min(rows, cols), kMuPad) * kMuPad; }
-    int64_t np() const { return ceil_div(std::max(rows, cols), kMuPad) * kMuPad; }
     int few() const { return mu_few(std::min(rows, cols), std::max(rows, cols)); }
+    int64_t mp() const { return few() ? few() : ceil_div(std::min(rows, cols), kMuPad) * kMuPad; }
+    int64_t np() const { return ceil_div(std::max(rows, cols), few() ? kMuStrip : kMuPad) * (few() ? kMuStrip : kMuPad); }
+    bool whole() const { return few() && np() == kMuStrip; }  // all steps in one launch
     // The power of two that values are held times: about the square root of the longer side, so that
     // entries of a matrix with orthonormal rows are about 1.
     int lift() const { return std::min(12, static_cast<int>(std::lround(0.5 * std::log2(static_cast<double>(std::max(rows, cols)))))); }
@@ -2798,6 +2799,7 @@ struct MuItem {
     int64_t off, norm;  // of their workspace and sums of squares
 };
 struct MuChunk {
+    int rows = 0;  // of matrices in strips; 0: in tiles
     std::vector<MuItem> items;
     int64_t bytes = 0;
 };
@@ -2807,40 +2809,45 @@ int64_t mu_norm_span(const MuIn& t) { return ceil_div(mu_norm_tiles(t), kMuMaxPa
 int64_t mu_norm_parts(const MuIn& t) { return ceil_div(mu_norm_tiles(t), mu_norm_span(t)); }
 
 int64_t mu_stride(const MuIn& t) {
+    if (t.few()) return align256(MuStripPlace(t.mp(), t.np()).total);
     int64_t parts, steps;
     mu_gram_parts(t.mp(), t.np(), &parts, &steps);
     return align256(MuPlace(t.mp(), t.np(), parts).total);
 }
 
-// The list's larger matrices in chunks, in order; returns the workspace's bytes (some for every list
-// with anything in it, so that what a caller has to bring does not turn on a matrix' size).
+// The list's matrices that take more than a launch in chunks, kind by kind and in order; returns the
+// workspace's bytes (some for every list with anything in it, so that what a caller has to bring
+// does not turn on a matrix' size).
 int64_t mu_chunks(const std::vector<MuIn>& ts, std::vector<MuChunk>* out) {
     int64_t most = 0, values = 0;
     MuChunk c;
     auto close = [&]() {
         most = std::max(most, c.bytes);
         if (out && !c.items.empty()) out->push_back(c);
-        c = MuChunk();
-        values = 0;
+        c.items.clear();
+        c.bytes = values = 0;
     };
-    for (size_t k = 0; k < ts.size(); ++k) {
-        const MuIn& t = ts[k];
-        if (t.empty()) continue;
-        most = std::max<int64_t>(most, 256);
-        if (t.few()) continue;
-        const int64_t size = t.mp() * t.np(), stride = mu_stride(t), parts = mu_norm_parts(t);
-        for (int64_t b = 0; b < t.batch;) {
-            if (!c.items.empty() && (values + size > kMuChunkValues || c.items.size() == kMuBatch)) close();
-            const int64_t count = std::min(t.batch - b, std::max<int64_t>((kMuChunkValues - values) / size, 1));
-            MuItem i{static_cast<int32_t>(k), b, count, c.bytes, 0};
-            i.norm = i.off + count * stride;
-            c.bytes = i.norm + align256(count * parts * 8);
-            c.items.push_back(i);
-            values += count * size;
-            b += count;
+    for (int rows : {0, 16, 32, 64}) {
+        c.rows = rows;
+        for (size_t k = 0; k < ts.size(); ++k) {
+            const MuIn& t = ts[k];
+            if (t.empty()) continue;
+            most = std::max<int64_t>(most, 256);
+            if (t.few() != rows || t.whole()) continue;
+            const int64_t size = t.mp() * t.np(), stride = mu_stride(t), parts = mu_norm_parts(t);
+            for (int64_t b = 0; b < t.batch;) {
+                if (!c.items.empty() && (values + size > kMuChunkValues || c.items.size() == kMuBatch)) close();
+                const int64_t count = std::min(t.batch - b, std::max<int64_t>((kMuChunkValues - values) / size, 1));
+                MuItem i{static_cast<int32_t>(k), b, count, c.bytes, 0};
+                i.norm = i.off + count * stride;
+                c.bytes = i.norm + align256(count * parts * 8);
+                c.items.push_back(i);
+                values += count * size;
+                b += count;
+            }
         }
+        close();
     }
-    close();
     return most;
 }
 
@@ -2925,7 +2932,7 @@ int check_mu_workspace(int64_t need, void* ws, size_t bytes, int dev) {
     return check_device_range(ws, bytes, dev, "workspace", MEO_EWORKSPACE);
 }
 
-// The small matrices, a block each: lists of up to kMuFewBatch tensors of a kind.
+// Matrices of one strip, a block each: lists of up to kMuFewBatch tensors of a kind.
 constexpr int64_t kMuFewBlocks = 1 << 22;  // of a launch
 
 void mu_run_few(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, const MuStepArgs& step, float decay, bool update,
@@ -2954,7 +2961,7 @@ void mu_run_few(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts
         };
         start();
         for (const MuIn& t : ts) {
-            if (t.empty() || t.few() != rows) continue;
+            if (t.empty() || t.few() != rows || !t.whole()) continue;
             for (int64_t b = 0; b < t.batch;) {
                 if (l.n == kMuFewBatch || l.blocks == kMuFewBlocks) flush();
                 const int64_t count = std::min<int64_t>(t.batch - b, kMuFewBlocks - l.blocks);
@@ -3028,6 +3035,7 @@ int mu_run(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, MuS
             d.xbf16 = in.xbf16;
             d.mkind = in.mkind;
             d.tall = in.rows > in.cols;
+            if (c.rows) continue;
             int64_t parts, steps;
             mu_gram_parts(m.mp, m.np, &parts, &steps);
             m.parts = static_cast<int32_t>(parts);
@@ -3040,6 +3048,23 @@ int mu_run(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, MuS
                 if (i < l.n) l.blocks += static_cast<uint32_t>(blocks(l.d[i]));
             }
         };
+        count(t, [&](const MuTensor& d) { return int64_t{d.batch} * d.parts; });
+        launch_mu_momentum(t, a, s);
+        pt.mark(kPassMuMomentum);
+        auto poly_of = [&](int k) {
+            return MuPoly{static_cast<float>(hp.coefficients[k][0]), static_cast<float>(hp.coefficients[k][1]),
+                          static_cast<float>(hp.coefficients[k][2])};
+        };
+        if (c.rows) {
+            count(t, [&](const MuTensor& d) { return int64_t{d.batch} * (d.np / kMuStrip); });
+            launch_mu_strip_start(t, c.rows, a, s);
+            pt.mark(kPassMuScatter);
+            for (int k = 0; k < hp.steps; ++k) {
+                launch_mu_strip_step(t, c.rows, poly_of(k), k & 1, k + 1 == hp.steps, update, decay, s);
+                pt.mark(kPassMuStrips);
+            }
+            continue;
+        }
         auto square = [](int64_t side, int64_t tile) { const int64_t q = ceil_div(side, tile); return q * (q + 1) / 2; };
         const int fg = mu_form(ts, c, kMuTileStart, [&](const MuIn& q, int64_t tile, int64_t* n, int64_t* steps) {
             int64_t parts;
@@ -3060,15 +3085,11 @@ int mu_run(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, MuS
         count(join, [&](const MuMatrix& m) { return m.parts > 1 ? m.batch * (int64_t{m.mp} / 4 * m.mp / kMuThreads) : 0; });
         count(poly, [&](const MuMatrix& m) { return m.batch * square(m.mp, kMuFormTile[fp]); });
         count(apply, [&](const MuMatrix& m) { return m.batch * ceil_div(m.mp, kMuFormTile[fa]) * ceil_div(m.np, kMuFormTile[fa]); });
-        count(t, [&](const MuTensor& d) { return int64_t{d.batch} * d.parts; });
-        launch_mu_momentum(t, a, s);
-        pt.mark(kPassMuMomentum);
         count(t, [&](const MuTensor& d) { return d.batch * (int64_t{d.mp} / kMuTile) * (d.np / kMuTile); });
         launch_mu_scatter(t, a, s);
         pt.mark(kPassMuScatter);
         for (int k = 0; k < hp.steps; ++k) {
-            const MuPoly p{static_cast<float>(hp.coefficients[k][0]), static_cast<float>(hp.coefficients[k][1]),
-                           static_cast<float>(hp.coefficients[k][2])};
+            const MuPoly p = poly_of(k);
             launch_mu_gram(gram, fg, k & 1, s);
             launch_mu_gram(parts, kMuSmall, k & 1, s);
             launch_mu_join(join, s);

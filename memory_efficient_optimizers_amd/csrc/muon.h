@@ -103,15 +103,26 @@ struct MuLastOf {     // the last step's results go to the caller's tensors
 };
 using MuLast = MuLastOf<kMuBatch>;
 
-// ---- matrices worked on by one block each, all steps in one launch
+// ---- matrices with few rows
 
-// The rows that a matrix of shorter side `m` and longer side `n` takes (16, 32 or 64, the longer side
-// in blocks of 32); 0: it is not one of these. From the matrix alone: its result does not depend on
-// the list.
+// A matrix whose shorter side is at most 64 takes 16, 32 or 64 rows, and its longer side strips of
+// kMuStrip columns, one to a thread block: of one strip, all steps are one launch; of up to 64 (32 of
+// 64 rows), a launch each. The rows; 0: the matrix is worked on in tiles. From the matrix
+// alone: its result does not depend on the list.
+constexpr int kMuStrip = 512;
 __host__ __device__ constexpr int mu_few(int64_t m, int64_t n) {
-    const int64_t p = (n + 31) / 32 * 32;
-    return m <= 16 && p <= 4096 ? 16 : m <= 32 && p <= 2048 ? 32 : m <= 64 && p <= 768 ? 64 : 0;
+    return m <= 16 && n <= 64 * kMuStrip ? 16 : m <= 32 && n <= 64 * kMuStrip ? 32 : m <= 64 && n <= 32 * kMuStrip ? 64 : 0;
 }
+// The workspace of one in strips (np: whole strips): the iterate's high and low parts, and two buffers
+// of the strips' parts of A.
+struct MuStripPlace {
+    int64_t lo, part, total;
+    __host__ __device__ MuStripPlace(int64_t rows, int64_t np) {
+        lo = rows * np * 2;
+        part = 2 * lo;
+        total = part + 2 * (np / kMuStrip) * rows * rows * 4;
+    }
+};
 constexpr int kMuFewBatch = 48;     // tensors per launch
 constexpr int kMuFewThreads = 512;
 
@@ -133,8 +144,11 @@ struct MuFewArgs {
     MuPoly poly[16];
 };
 
-// rows: 16, 32 or 64, the same for all.
+// rows: 16, 32 or 64, the same for all. Of one strip; of several (after the momentum pass: X0 and its
+// A, then the steps; src: the buffer of A's parts).
 void launch_mu_few(const MuFewTensors& t, int rows, const MuFewArgs& a, hipStream_t s);
+void launch_mu_strip_start(const MuTensors& t, int rows, const MuStepArgs& a, hipStream_t s);
+void launch_mu_strip_step(const MuTensors& t, int rows, const MuPoly& p, int src, bool last, bool update, float decay, hipStream_t s);
 
 void launch_mu_momentum(const MuTensors& t, const MuStepArgs& a, hipStream_t s);
 void launch_mu_scatter(const MuTensors& t, const MuStepArgs& a, hipStream_t s);

@@ -1,16 +1,18 @@
-// Orthogonalization and the Muon step of matrices with few values, one block each, all steps in
-// one launch: the mathematics and roundings of muon.hip (there each pass over such a matrix is a
-// launch of 3 to 5 us, 15 and more in all).
+// Orthogonalization and the Muon step of matrices with few rows (a shorter side of at most 64): the
+// mathematics and roundings of muon.hip, where each pass over such a matrix is a launch of 3 to
+// 5 us, 17 and more of them.
 //
-// The iterate stays on the CU: its high parts in LDS, its low parts in the registers of the lanes
-// that form them. The longer side goes by blocks of 32 columns; a wave's blocks are its own: the step
-// X' = a X + B X needs nothing else of X. A = X X^T is summed over them through LDS.
-// Every wave then forms B for itself: in an accumulator of a symmetric matrix a lane holds four
-// consecutive rows of a column, which are four consecutive values of the contraction of that
-// column as an operand, so A, A^2 and B go from product to product in registers.
+// The longer side goes by blocks of 32 columns, 16 of them (a strip) to a thread block, of which a
+// wave has two: the step X' = a X + B X needs nothing else of X. A = X X^T is summed over the waves
+// through LDS, over strips through the workspace. Every wave then forms B for itself: in an accumulator
+// of a symmetric matrix a lane holds four consecutive rows of a column, which are four
+// consecutive values of the contraction of that column as an operand, so A, A^2 and B go from
+// product to product in registers. A matrix of one strip is one launch, with the iterate in LDS (high
+// parts) and registers (low parts); one of more strips is a launch per step and two before them.
 //
-// What bounds it: latencies (barriers, LDS, dependent products) and, for the largest, one CU's way
-// to memory.
+// What bounds it: latencies (launches, barriers, LDS, dependent products). The work per value is
+// some 8 vector instructions a step, 2 us for 16 x 4096 on one CU: that many in one block took 59 us
+// (4096 x 16: 87).
 #include "muon_device.h"
 
 namespace meo {
@@ -18,33 +20,60 @@ namespace meo {
 namespace {
 
 typedef _Float16 half4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) u32x2 L2;
 typedef __attribute__((address_space(3))) u32x4 L4;
 typedef __attribute__((address_space(3))) f32x4 F4;
+typedef __attribute__((address_space(3))) double D1;
+typedef __attribute__((address_space(3))) uint16_t H1;
 
 constexpr int kMuFewWaves = kMuFewThreads / 64;
+static_assert(kMuStrip == 2 * 32 * kMuFewWaves, "two blocks per wave");
 
 // An LDS access of a wave to what its other lanes wrote is not moved over this.
 __device__ __forceinline__ void mu_order() { __asm__ volatile("" ::: "memory"); }
 
-// A matrix of R rows. Accumulators: tiles of T x T, where a lane holds rows 8 v + 4 h + 0 .. 3 of its
-// column, v < V.
+// f(p) with p a constant, for registers that a loop indexes: a branch each. (An array indexed at run
+// time became a selection over all of it; a loop written out in full, code that is read from memory
+// once per launch.)
+template <int N, class Fn>
+__device__ __forceinline__ void mu_case(int p, Fn f) {
+    if constexpr (N > 0) {
+        if (p == N - 1) {
+            f(std::integral_constant<int, N - 1>{});
+            __asm__ volatile("; %0" ::"n"(N));  // (branches that end alike would be merged)
+        } else {
+            mu_case<N - 1>(p, f);
+        }
+    }
+}
+
+// X in LDS: blocks of 32 columns, R rows of 64 bytes in each, chunk c (16 bytes) of row r at position
+// c ^ (r >> 2 & 3): rows read at one chunk touch every bank alike. The bytes of 4 values, chunk c8 >> 1:
+__device__ __forceinline__ uint32_t mu_few_at(int r, int c8) {
+    return r * 64 + (((c8 >> 1) ^ ((r >> 2) & 3)) << 4) + (c8 & 1) * 8;
+}
+
+// The products of a strip of R rows at LDS address x. Accumulators: tiles of T x T, where a lane holds
+// rows 8 v + 4 h + 0 .. 3 of its column, v < V. A block of 32 columns: SB parts of NT tiles.
 template <int R>
 struct MuFew {
     static constexpr int T = R == 16 ? 16 : 32, NT = R / T, V = T == 16 ? 1 : 4, SB = 32 / T;
-    static constexpr int kValues = R == 64 ? 49152 : 65536;
-    static constexpr int kBlocks = kValues / R / 32 / kMuFewWaves;  // of 32 columns per wave, at most
-    static constexpr int kLow = SB * NT * V * 2;  // registers of a block's low parts
-    static constexpr int kX = kValues * 2;  // bytes of X
+    static constexpr int kBytes = R * kMuStrip * 2;  // of one part of the strip
     // A's parts: by wave; R = 64: by pairs of waves, which have a column of tiles each.
     static constexpr int kParts = R == 64 ? kMuFewWaves / 2 : kMuFewWaves;
-    static constexpr int kPart = R * R * 4;
-    static constexpr int kLds = kX + kParts * kPart * (R == 16 ? 2 : 1);
-    typedef uint32_t Low __attribute__((ext_vector_type(R == 16 ? 16 : R == 32 ? 8 : 4)));
-    static_assert(kBlocks <= static_cast<int>(sizeof(Low) / 4), "a wave's blocks");
+    static constexpr int kPart = R * R * 4, kSums = kParts * kPart;
     struct Acc { f32x4 v[V]; };
     struct Op { u32x2 v[V]; };  // T values of the contraction
+    typedef u32x2 Block[SB][NT][V];  // of the iterate, as accumulators have it
+
+    uint32_t x, sums;
+    int lane, wave, col, h;
+    __device__ MuFew(uint32_t x_, uint32_t sums_) : x(x_), sums(sums_) {
+        lane = threadIdx.x & 63;
+        wave = uniform(threadIdx.x >> 6);
+        col = lane & (T - 1);
+        h = lane / T;
+    }
 
     static __device__ __forceinline__ void mul(Acc& c, const Op& a, const Op& b) {
         if constexpr (T == 16) {
@@ -62,12 +91,178 @@ struct MuFew {
 #pragma unroll
         for (int v = 0; v < V; ++v) c.v[v] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
+    // The n-th block of the wave, and where an accumulator's four values are in it.
+    __device__ int block(int n) const { return n * kMuFewWaves + wave; }
+    __device__ uint32_t place(int blk, int sb, int it, int v) const {
+        return x + blk * (R * 64) + mu_few_at(it * T + col, T == 16 ? 4 * sb + h : 2 * v + h);
+    }
+    // f(sb, it, v) over a block.
+    template <class Fn>
+    static __device__ __forceinline__ void each(Fn f) {
+#pragma unroll
+        for (int sb = 0; sb < SB; ++sb)
+#pragma unroll
+            for (int it = 0; it < NT; ++it)
+#pragma unroll
+                for (int v = 0; v < V; ++v) f(sb, it, v);
+    }
+
+    // The wave's part of X X^T, of nb blocks, to `sums`. (R = 64: of blocks that two waves have.)
+    __device__ __forceinline__ void gram(int nb) const {
+        const int part = R == 64 ? wave >> 1 : wave, tj = R == 64 ? wave & 1 : 0;
+        Acc g[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) zero(g[i]);
+        for (int blk = part; blk < nb; blk += kParts) {
+            const uint32_t o = x + blk * (R * 64);
+            if constexpr (T == 16) {
+                const half8 w = __builtin_bit_cast(half8, mu_lds(o + mu_few_at(col, 2 * h)));
+                g[0].v[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, w, g[0].v[0], 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    u32x4 w[NT];
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) w[i] = mu_lds(o + mu_few_at(i * T + col, 4 * c + 2 * h));
+                    const u32x4 z = NT == 1 || tj == 0 ? w[0] : w[NT - 1];
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) g[i] = __builtin_bit_cast(Acc, mfma_f16(w[i], z, __builtin_bit_cast(f32x16, g[i])));
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                *(F4*)static_cast<uintptr_t>(sums + part * kPart + (((tj * NT + i) * V + v) * 64 + lane) * 16) = g[i].v[v];
+    }
+    // 16 bytes of the parts' sum, in order: chunks [column of tiles][row][v][lane].
+    __device__ __forceinline__ f32x4 joined(int chunk) const {
+        f32x4 w = *(const F4*)static_cast<uintptr_t>(sums + chunk * 16);
+#pragma unroll
+        for (int e = 1; e < kParts; ++e) w += *(const F4*)static_cast<uintptr_t>(sums + e * kPart + chunk * 16);
+        return w;
+    }
+
+    // From X X^T (times 4^lift, at `sums`): the wave's B, 2^8 times off the diagonal, as operands, and
+    // of its lanes' columns q = a + B_ii and t = a + B_ii min(1, d_i^2), 2^8 times.
+    Op B[NT][NT];  // [column][row]
+    float q[NT], tl[NT];
+    __device__ __forceinline__ void poly(const MuPoly& p, float un) {
+        const int holder = col + T * ((col >> 2) & (64 / T - 1));  // the lane with the diagonal of column `col`
+        Op O[NT][NT];
+        float d[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            float own = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    f32x4 w = *(const F4*)static_cast<uintptr_t>(sums + (((j * NT + i) * V + v) * 64 + lane) * 16) * un;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (i == j && 8 * v + 4 * h + e == col) {
+                            own = w[e];
+                            w[e] = 0.0f;
+                        }
+                    w *= kMuLift;
+                    O[j][i].v[v] = mu_pack4(w.x, w.y, w.z, w.w);
+                }
+            d[j] = __shfl(own, holder, 64);
+        }
+        const float cs = p.c * kMuUnlift;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            f32x4 di[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) di[v][e] = __shfl(d[i], 8 * v + 4 * h + e, 64);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                Acc sq;
+                zero(sq);
+#pragma unroll
+                for (int z = 0; z < NT; ++z) mul(sq, O[i][z], O[j][z]);
+                float own = 0.0f;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        y[e] = fmaf(mu_half(O[j][i].v[v], e), fmaf(p.c, di[v][e] + d[j], p.b), sq.v[v][e] * cs);
+                        if (i == j && 8 * v + 4 * h + e == col) {
+                            own = p.a + fmaf(p.b, d[j], p.c * fmaf(d[j], d[j], sq.v[v][e] * (kMuUnlift * kMuUnlift)));
+                            y[e] = 0.0f;
+                        }
+                    }
+                    B[j][i].v[v] = mu_pack4(y[0], y[1], y[2], y[3]);
+                }
+                if (i == j) {
+                    const float al = p.a * kMuLift;
+                    q[j] = __shfl(own, holder, 64) * kMuLift;
+                    tl[j] = fmaf(q[j] - al, fminf(d[j] * d[j], 1.0f), al);
+                }
+            }
+        }
+    }
+
+    // X' of a block from its high parts in LDS and the low ones `lo`: f(sb, it, v, four values, 2^8 times).
+    template <class Fn>
+    __device__ __forceinline__ void apply(int blk, const Block& lo, Fn f) const {
+        mu_order();
+#pragma unroll
+        for (int sb = 0; sb < SB; ++sb) {
+            Op xt[NT];  // X^T's part: 4 rows of X of the lane's column each
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    xt[i].v[v] = mu_lds_tr(x + blk * (R * 64) + mu_few_at(i * T + 8 * v + 4 * h + ((lane >> 2) & 3),
+                                                                        T == 16 ? 4 * sb + (lane & 3) : ((lane >> 4) & 1) * 4 + (lane & 3)));
+            mu_order();
+#pragma unroll
+            for (int it = 0; it < NT; ++it) {
+                Acc c;
+                zero(c);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) mul(c, xt[i], B[it][i]);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const u32x2 xh = *(const L2*)static_cast<uintptr_t>(place(blk, sb, it, v)), xl = lo[sb][it][v];
+                    f32x4 y;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = fmaf(tl[it], mu_half(xl, e), fmaf(q[it], mu_half(xh, e), c.v[v][e]));
+                    f(sb, it, v, y);
+                }
+            }
+        }
+    }
+    // As an iterate's high parts (also into LDS) and low parts.
+    __device__ __forceinline__ u32x2 split(int blk, int sb, int it, int v, f32x4 y, u32x2& lo) const {
+        y *= kMuUnlift;
+        const u32x2 w = mu_pack4(y.x, y.y, y.z, y.w);
+        *(L2*)static_cast<uintptr_t>(place(blk, sb, it, v)) = w;
+        lo = mu_pack4(y.x - mu_half(w, 0), y.y - mu_half(w, 1), y.z - mu_half(w, 2), y.w - mu_half(w, 3));
+        return w;
+    }
+    // The first column, in a block, of four values.
+    __device__ int column(int sb, int v) const { return (T == 16 ? 16 * sb : 0) + 8 * v + 4 * h; }
 };
 
-// X in LDS: blocks of 32 columns, R rows of 64 bytes in each, chunk c (16 bytes) of row r at position
-// c ^ (r >> 2 & 3): rows read at one chunk touch every bank alike. The bytes of 4 values, chunk c8 >> 1:
-__device__ __forceinline__ uint32_t mu_few_at(int r, int c8) {
-    return r * 64 + (((c8 >> 1) ^ ((r >> 2) & 3)) << 4) + (c8 & 1) * 8;
+__device__ __forceinline__ void mu_few_clear(uint32_t at, uint32_t bytes) {
+    for (uint32_t o = threadIdx.x * 16; o < bytes; o += kMuFewThreads * 16) *(L4*)static_cast<uintptr_t>(at + o) = u32x4{0u, 0u, 0u, 0u};
+}
+// The sum over the block, in order; `at`: 8 bytes of LDS per wave.
+__device__ __forceinline__ double mu_few_sum(double s, uint32_t at) {
+    s = wave_sum(s);
+    if ((threadIdx.x & 63) == 0) *(D1*)static_cast<uintptr_t>(at + (threadIdx.x >> 6) * 8) = s;
+    __syncthreads();
+    s = 0.0;
+#pragma unroll
+    for (int w = 0; w < kMuFewWaves; ++w) s += *(const D1*)static_cast<uintptr_t>(at + w * 8);
+    return s;
 }
 
 // Four values of a row of X' (element (i, j), ..., (i, j + 3)) into the caller's tensor.
@@ -110,13 +305,12 @@ __device__ __forceinline__ void mu_few_store(const MuTensor& t, bool update, flo
     }
 }
 
+// A matrix of one strip per block, all steps.
 template <int R, int N>
 __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_few(MuListOf<MuFewTensor, N> l, MuFewArgs a) {
     using M = MuFew<R>;
-    constexpr int T = M::T, NT = M::NT, V = M::V, SB = M::SB;
-    using Acc = typename M::Acc;
-    using Op = typename M::Op;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[M::kLds];
+    constexpr int kTurn = kMuFewThreads * kVec, kTurns = R * kMuStrip / kTurn;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[M::kBytes + M::kSums];
     const int k = mu_find(l, blockIdx.x);
     const int b = static_cast<int>(mu_item(l, k, blockIdx.x));
     const MuFewTensor& s = l.d[k];
@@ -129,16 +323,13 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_few(MuListOf<MuFewTenso
     t.tall = s.rows > s.cols;
     const int size = t.rows * t.cols;
     const int nb = uniform((max(t.rows, t.cols) + 31) / 32);
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const uint32_t x0 = uniform(static_cast<int>(lds_addr(lds))), s0 = x0 + M::kX;
+    const uint32_t x0 = uniform(static_cast<int>(lds_addr(lds)));
+    M m(x0, x0 + M::kBytes);
 
     // the directions and their squares' sum
-    for (uint32_t o = threadIdx.x * 16; o < static_cast<uint32_t>(nb) * R * 64; o += kMuFewThreads * 16)
-        *(L4*)static_cast<uintptr_t>(x0 + o) = u32x4{0u, 0u, 0u, 0u};
-    constexpr int kTurn = kMuFewThreads * kVec;
-    static_assert(M::kValues <= 16 * kTurn, "a thread's values");
+    mu_few_clear(x0, nb * R * 64);
     const int turns = uniform((size + kTurn - 1) / kTurn);
-    u32x16 u[kVec];  // [e][turn]; turns and blocks are indexed at run time, which keeps the code short
+    float u[kTurns][kVec];
     double sum = 0.0;
 #pragma unroll 1
     for (int p = 0; p < turns; ++p) {
@@ -146,30 +337,29 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_few(MuListOf<MuFewTenso
         float w[kVec];
         mu_take8(t, a.step, b, static_cast<int64_t>(b) * size, i, clamp_valid(static_cast<int64_t>(size) - i), w);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            sum += static_cast<double>(w[e]) * static_cast<double>(w[e]);
-            u[e][p] = __float_as_uint(w[e]);
-        }
-    }
-    sum = wave_sum(sum);
-    typedef __attribute__((address_space(3))) double D1;
-    if (lane == 0) *(D1*)static_cast<uintptr_t>(s0 + wave * 8) = sum;
-    __syncthreads();
-    sum = 0.0;
+        for (int e = 0; e < kVec; ++e) sum += static_cast<double>(w[e]) * static_cast<double>(w[e]);
+        mu_case<kTurns>(p, [&](auto q) {
 #pragma unroll
-    for (int w = 0; w < kMuFewWaves; ++w) sum += *(const D1*)static_cast<uintptr_t>(s0 + w * 8);
-    const double f = mu_factor_of(sum, a.step.eps, s.lift);
+            for (int e = 0; e < kVec; ++e) u[q][e] = w[e];
+        });
+    }
+    const double f = mu_factor_of(mu_few_sum(sum, m.sums), a.step.eps, s.lift);
 
     // X0 in two parts: the low ones through LDS to the lanes that keep them, then the high ones
     auto scatter = [&](bool low) {
 #pragma unroll 1
         for (int p = 0; p < turns; ++p) {
             const int i = p * kTurn + threadIdx.x * kVec;
+            float z[kVec];
+            mu_case<kTurns>(p, [&](auto q) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) z[e] = u[q][e];
+            });
             uint32_t w[kVec];
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
                 uint32_t hi, lo;
-                mu_split(static_cast<float>(__uint_as_float(u[e][p]) * f), hi, lo);
+                mu_split(static_cast<float>(z[e] * f), hi, lo);
                 w[e] = low ? lo : hi;
             }
             if (i >= size) continue;
@@ -183,8 +373,7 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_few(MuListOf<MuFewTenso
             for (int e = 0; e < kVec; ++e) {
                 const int r = t.tall ? col : row, c = t.tall ? row : col;
                 if (i + e < size)
-                    *(__attribute__((address_space(3))) uint16_t*)static_cast<uintptr_t>(
-                        x0 + (c >> 5) * (R * 64) + mu_few_at(r, (c & 31) >> 2) + (c & 3) * 2) = static_cast<uint16_t>(w[e]);
+                    *(H1*)static_cast<uintptr_t>(x0 + (c >> 5) * (R * 64) + mu_few_at(r, (c & 31) >> 2) + (c & 3) * 2) = static_cast<uint16_t>(w[e]);
                 if (++col == t.cols) {
                     col = 0;
                     ++row;
@@ -194,210 +383,228 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_few(MuListOf<MuFewTenso
     };
     scatter(true);
     __syncthreads();
-    const int col = lane & (T - 1), h = lane / T;
-    // of an accumulator's (or its low part's) four values v in block `blk`, part sb, tile it
-    auto place = [&](int blk, int sb, int it, int v) {
-        return x0 + blk * (R * 64) + mu_few_at(it * T + col, T == 16 ? 4 * sb + h : 2 * v + h);
-    };
-    const int mine = uniform((nb - wave + kMuFewWaves - 1) / kMuFewWaves);  // (nb < wave: 0)
-    typename M::Low low[M::kLow];  // [..][block]
-#pragma unroll 1
-    for (int n = 0; n < mine; ++n)
+    typename M::Block low[2];
 #pragma unroll
-        for (int sb = 0; sb < SB; ++sb)
-#pragma unroll
-            for (int it = 0; it < NT; ++it)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const u32x2 w = *(const L2*)static_cast<uintptr_t>(place(n * kMuFewWaves + wave, sb, it, v));
-                    const int e = ((sb * NT + it) * V + v) * 2;
-                    low[e][n] = w.x;
-                    low[e + 1][n] = w.y;
-                }
+    for (int n = 0; n < 2; ++n)
+        if (m.block(n) < nb) M::each([&](int sb, int it, int v) { low[n][sb][it][v] = *(const L2*)static_cast<uintptr_t>(m.place(m.block(n), sb, it, v)); });
     __syncthreads();
     scatter(false);
     __syncthreads();
 
     const float lift = ldexpf(1.0f, s.lift), un = 1.0f / (lift * lift), out = 1.0f / lift * kMuUnlift;
     const int64_t first = static_cast<int64_t>(b) * t.rows * t.ldx;
-    const int part = R == 64 ? wave >> 1 : wave;
 #pragma unroll 1
     for (int step = 0; step < a.steps; ++step) {
-        const MuPoly p = a.poly[step];
-        // A over the wave's blocks
-        const uint32_t sp = s0 + (R == 16 ? (step & 1) * M::kParts * M::kPart : 0);
-        {
-            Acc g[NT];
-#pragma unroll
-            for (int i = 0; i < NT; ++i) M::zero(g[i]);
-            for (int blk = part; blk < nb; blk += M::kParts) {
-                const uint32_t o = x0 + blk * (R * 64);
-                if constexpr (T == 16) {
-                    const half8 w = __builtin_bit_cast(half8, mu_lds(o + mu_few_at(col, 2 * h)));
-                    g[0].v[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, w, g[0].v[0], 0, 0, 0);
-                } else {
-                    const int tj = R == 64 ? wave & 1 : 0;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        u32x4 w[NT];
-#pragma unroll
-                        for (int i = 0; i < NT; ++i) w[i] = mu_lds(o + mu_few_at(i * T + col, 4 * c + 2 * h));
-                        const u32x4 z = NT == 1 || tj == 0 ? w[0] : w[NT - 1];
-#pragma unroll
-                        for (int i = 0; i < NT; ++i) g[i] = __builtin_bit_cast(Acc, mfma_f16(w[i], z, __builtin_bit_cast(f32x16, g[i])));
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    *(F4*)static_cast<uintptr_t>(sp + part * M::kPart + ((((R == 64 ? wave & 1 : 0) * NT + i) * V + v) * 64 + lane) * 16) = g[i].v[v];
-        }
+        m.gram(nb);
         __syncthreads();
-        // the parts' sums, in order: [column of tiles][row][v][lane]
-        auto joined = [&](int chunk) {
-            f32x4 w = *(const F4*)static_cast<uintptr_t>(sp + chunk * 16);
+        for (int c = threadIdx.x; c < M::kPart / 16; c += kMuFewThreads) *(F4*)static_cast<uintptr_t>(m.sums + c * 16) = m.joined(c);
+        __syncthreads();
+        m.poly(a.poly[step], un);
+        if (step + 1 < a.steps) {
 #pragma unroll
-            for (int e = 1; e < M::kParts; ++e) w += *(const F4*)static_cast<uintptr_t>(sp + e * M::kPart + chunk * 16);
-            return w;
-        };
-        Acc A[NT][NT];  // [column][row]
-        if constexpr (R == 16) {
-            A[0][0].v[0] = joined(lane);
+            for (int n = 0; n < 2; ++n) {
+                const int blk = m.block(n);
+                if (blk < nb) m.apply(blk, low[n], [&](int sb, int it, int v, const f32x4& y) { m.split(blk, sb, it, v, y, low[n][sb][it][v]); });
+            }
         } else {
-            for (int c = threadIdx.x; c < M::kPart / 16; c += kMuFewThreads) {
-                const f32x4 w = joined(c);
-                *(F4*)static_cast<uintptr_t>(sp + c * 16) = w;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) A[j][i].v[v] = *(const F4*)static_cast<uintptr_t>(sp + (((j * NT + i) * V + v) * 64 + lane) * 16);
-        }
-        // O 2^8 times and the diagonal d of the lane's columns
-        const int holder = col + T * ((col >> 2) & (64 / T - 1));  // the lane with the diagonal of column `col`
-        Op O[NT][NT], B[NT][NT];
-        float d[NT], q[NT], tl[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            float own = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    f32x4 w = A[j][i].v[v] * un;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (i == j && 8 * v + 4 * h + e == col) {
-                            own = w[e];
-                            w[e] = 0.0f;
-                        }
-                    w *= kMuLift;
-                    O[j][i].v[v] = mu_pack4(w.x, w.y, w.z, w.w);
-                }
-            d[j] = __shfl(own, holder, 64);
-        }
-        // B 2^8 times off the diagonal, q = a + B_ii
-        const float cs = p.c * kMuUnlift;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            f32x4 di[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) di[v][e] = __shfl(d[i], 8 * v + 4 * h + e, 64);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                Acc sq;
-                M::zero(sq);
-#pragma unroll
-                for (int z = 0; z < NT; ++z) M::mul(sq, O[i][z], O[j][z]);
-                float own = 0.0f;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float y[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        y[e] = fmaf(mu_half(O[j][i].v[v], e), fmaf(p.c, di[v][e] + d[j], p.b), sq.v[v][e] * cs);
-                        if (i == j && 8 * v + 4 * h + e == col) {
-                            own = p.a + fmaf(p.b, d[j], p.c * fmaf(d[j], d[j], sq.v[v][e] * (kMuUnlift * kMuUnlift)));
-                            y[e] = 0.0f;
-                        }
-                    }
-                    B[j][i].v[v] = mu_pack4(y[0], y[1], y[2], y[3]);
-                }
-                if (i == j) {
-                    const float al = p.a * kMuLift;
-                    q[j] = __shfl(own, holder, 64) * kMuLift;
-                    tl[j] = fmaf(q[j] - al, fminf(d[j] * d[j], 1.0f), al);
-                }
-            }
-        }
-        // X' of the wave's blocks
-        const bool last = step + 1 == a.steps;
 #pragma unroll 1
-        for (int n = 0; n < mine; ++n) {
-            const int blk = n * kMuFewWaves + wave;
-            mu_order();
-#pragma unroll
-            for (int sb = 0; sb < SB; ++sb) {
-                Op x[NT];  // X^T's part: 4 rows of X of the lane's column each
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        x[i].v[v] = mu_lds_tr(x0 + blk * (R * 64) + mu_few_at(i * T + 8 * v + 4 * h + ((lane >> 2) & 3),
-                                                                           T == 16 ? 4 * sb + (lane & 3) : ((lane >> 4) & 1) * 4 + (lane & 3)));
-                mu_order();
-#pragma unroll
-                for (int it = 0; it < NT; ++it) {
-                    Acc c;
-                    M::zero(c);
-#pragma unroll
-                    for (int i = 0; i < NT; ++i) M::mul(c, x[i], B[it][i]);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const uint32_t at = place(blk, sb, it, v);
-                        const int reg = ((sb * NT + it) * V + v) * 2;
-                        const u32x2 xh = *(const L2*)static_cast<uintptr_t>(at), xl = {low[reg][n], low[reg + 1][n]};
-                        f32x4 y;  // 2^8 X'
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) y[e] = fmaf(tl[it], mu_half(xl, e), fmaf(q[it], mu_half(xh, e), c.v[v][e]));
-                        if (last) {
-                            mu_few_store(t, a.update, a.decay, first, it * T + col, 32 * blk + 16 * (T == 16 ? sb : 0) + 8 * v + 4 * h, y * out);
-                        } else {
-                            y *= kMuUnlift;
-                            const u32x2 w = mu_pack4(y.x, y.y, y.z, y.w);
-                            *(L2*)static_cast<uintptr_t>(at) = w;
-                            const u32x2 z = mu_pack4(y.x - mu_half(w, 0), y.y - mu_half(w, 1), y.z - mu_half(w, 2), y.w - mu_half(w, 3));
-                            low[reg][n] = z.x;
-                            low[reg + 1][n] = z.y;
-                        }
-                    }
-                }
+            for (int n = 0; n < 2; ++n) {
+                const int blk = m.block(n);
+                if (blk >= nb) continue;
+                typename M::Block lo;
+                mu_case<2>(n, [&](auto z) { M::each([&](int sb, int it, int v) { lo[sb][it][v] = low[z][sb][it][v]; }); });
+                m.apply(blk, lo, [&](int sb, int it, int v, const f32x4& y) {
+                    mu_few_store(t, a.update, a.decay, first, it * M::T + m.col, 32 * blk + m.column(sb, v), y * out);
+                });
             }
         }
         mu_order();
-        if (R != 16) __syncthreads();  // (A's sums have been read; R = 64: X' is read by two waves)
+        __syncthreads();  // A's sums have been read; R = 64: X' is read by two waves
     }
+}
+
+// Strips: X0 of one, into the workspace as accumulators have it, and its part of A.
+template <int R, int N>
+__global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_start(MuListOf<MuTensor, N> l, MuStepArgs a) {
+    using M = MuFew<R>;
+    constexpr int kLow = M::kBytes > M::kSums ? M::kBytes : M::kSums;  // the low parts, then A's sums
+    __shared__ __attribute__((aligned(16))) uint8_t lds[M::kBytes + kLow];
+    const int k = mu_find(l, blockIdx.x);
+    const MuTensor& t = l.d[k];
+    const uint32_t item = mu_item(l, k, blockIdx.x);
+    const int strips = t.np / kMuStrip, b = uniform(static_cast<int>(item / strips)), strip = uniform(static_cast<int>(item % strips));
+    const uint32_t x0 = uniform(static_cast<int>(lds_addr(lds))), y0 = x0 + M::kBytes;
+    M m(x0, y0);
+    double sum = 0.0;
+    const double* p = t.norm + static_cast<int64_t>(b) * t.parts;
+    for (int i = threadIdx.x; i < t.parts; i += kMuFewThreads) sum += *gld<double>(p + i);
+    const double f = mu_factor_of(mu_few_sum(sum, y0), a.eps, t.lift);
+    __syncthreads();
+    mu_few_clear(x0, 2 * M::kBytes);
+    __syncthreads();
+    const int c0 = strip * kMuStrip, per = t.tall ? (t.cols + kVec - 1) / kVec : kMuStrip / kVec;  // 8 values each of a row
+    const int rows = t.tall ? min(kMuStrip, t.rows - c0) : t.rows;
+#pragma unroll 2
+    for (int e0 = threadIdx.x; e0 < rows * per; e0 += kMuFewThreads) {
+        const int r = e0 / per, c = e0 % per * kVec;
+        const int row = t.tall ? c0 + r : r, col = t.tall ? c : c0 + c;
+        const int valid = clamp_valid(static_cast<int64_t>(t.cols) - col);
+        if (valid <= 0) continue;
+        float u[kVec], g[kVec], w[kVec];
+        const int64_t i = (static_cast<int64_t>(b) * t.rows + row);
+        load_any8(t.g, i * t.ldg + col, valid, t.gbf16, g);
+        if (t.m) {
+            mu_load_m(t, i * t.cols + col, valid, w);
+            mu_direction(a, g, w, u);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) u[e] = g[e];
+        }
+        uint32_t hi[kVec], lo[kVec];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) mu_split(e < valid ? static_cast<float>(u[e] * f) : 0.0f, hi[e], lo[e]);
+        if (!t.tall) {
+            const uint32_t at = (c >> 5) * (R * 64) + mu_few_at(r, (c & 31) >> 2);
+            *(L4*)static_cast<uintptr_t>(x0 + at) = u32x4{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16};
+            *(L4*)static_cast<uintptr_t>(y0 + at) = u32x4{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16};
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                if (e >= valid) break;
+                const uint32_t at = (r >> 5) * (R * 64) + mu_few_at(c + e, (r & 31) >> 2) + (r & 3) * 2;
+                *(H1*)static_cast<uintptr_t>(x0 + at) = static_cast<uint16_t>(hi[e]);
+                *(H1*)static_cast<uintptr_t>(y0 + at) = static_cast<uint16_t>(lo[e]);
+            }
+        }
+    }
+    __syncthreads();
+    const MuStripPlace at(t.mp, t.np);
+    uint8_t* const ws = t.ws + b * t.stride;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        const int blk = m.block(n);
+        uint8_t* const w = ws + strip * M::kBytes + blk * (R * 64) + m.lane * 8;
+        M::each([&](int sb, int it, int v) {
+            const int64_t o = ((sb * M::NT + it) * M::V + v) * 512;
+            const uint32_t z = m.place(blk, sb, it, v);
+            *gst<u32x2>(w + o) = *(const L2*)static_cast<uintptr_t>(z);
+            *gst<u32x2>(w + at.lo + o) = *(const L2*)static_cast<uintptr_t>(z + M::kBytes);
+        });
+    }
+    __syncthreads();
+    m.gram(kMuStrip / 32);
+    __syncthreads();
+    float* const o = reinterpret_cast<float*>(ws + at.part) + static_cast<int64_t>(strip) * R * R;
+    for (int c = threadIdx.x; c < M::kPart / 16; c += kMuFewThreads) *gst<f32x4>(o + c * 4) = m.joined(c);
+}
+
+// One step of a strip: A from all strips' parts (buffer src), X', its part of the next A; the last
+// step's X' goes to the caller's tensors.
+template <int R, int N>
+__global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_step(MuListOf<MuTensor, N> l, MuPoly poly, int src, int last, int update,
+                                                                    float decay) {
+    using M = MuFew<R>;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[M::kBytes + M::kSums];
+    const int k = mu_find(l, blockIdx.x);
+    const MuTensor& t = l.d[k];
+    const uint32_t item = mu_item(l, k, blockIdx.x);
+    const int strips = t.np / kMuStrip, b = uniform(static_cast<int>(item / strips)), strip = uniform(static_cast<int>(item % strips));
+    const uint32_t x0 = uniform(static_cast<int>(lds_addr(lds)));
+    M m(x0, x0 + M::kBytes);
+    const MuStripPlace at(t.mp, t.np);
+    uint8_t* const ws = t.ws + b * t.stride;
+    uint8_t* const w = ws + strip * M::kBytes + m.lane * 8;
+    typename M::Block high[2], low[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+        M::each([&](int sb, int it, int v) {
+            const int64_t o = m.block(n) * (R * 64) + ((sb * M::NT + it) * M::V + v) * 512;
+            high[n][sb][it][v] = *gld<u32x2>(w + o);
+            low[n][sb][it][v] = *gld<u32x2>(w + at.lo + o);
+        });
+    // the parts' sums, in order of groups of parts
+    constexpr int kChunks = M::kPart / 16, kGroups = kChunks < kMuFewThreads ? kMuFewThreads / kChunks : 1;
+    const float* const parts = reinterpret_cast<const float*>(ws + at.part) + static_cast<int64_t>(src) * strips * R * R;
+    const int group = threadIdx.x / kChunks;  // (one group: 0 .. 0)
+#pragma unroll
+    for (int c = threadIdx.x % kChunks; c < kChunks; c += kMuFewThreads) {
+        f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+        for (int e = group; e < strips; e += kGroups) s += *gld<f32x4>(parts + static_cast<int64_t>(e) * R * R + c * 4);
+        *(F4*)static_cast<uintptr_t>(m.sums + group * M::kPart + c * 16) = s;
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+        M::each([&](int sb, int it, int v) { *(L2*)static_cast<uintptr_t>(m.place(m.block(n), sb, it, v)) = high[n][sb][it][v]; });
+    __syncthreads();
+    if (kGroups > 1) {
+        if (threadIdx.x < kChunks) {
+            f32x4 s = *(const F4*)static_cast<uintptr_t>(m.sums + threadIdx.x * 16);
+#pragma unroll
+            for (int e = 1; e < kGroups; ++e) s += *(const F4*)static_cast<uintptr_t>(m.sums + e * M::kPart + threadIdx.x * 16);
+            *(F4*)static_cast<uintptr_t>(m.sums + threadIdx.x * 16) = s;
+        }
+        __syncthreads();
+    }
+    const float lift = ldexpf(1.0f, t.lift);
+    m.poly(poly, 1.0f / (lift * lift));
+    if (last) {
+        const int64_t first = static_cast<int64_t>(b) * t.rows * t.ldx;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+            m.apply(m.block(n), low[n], [&](int sb, int it, int v, const f32x4& y) {
+                mu_few_store(t, update, decay, first, it * M::T + m.col, strip * kMuStrip + 32 * m.block(n) + m.column(sb, v),
+                             y * (1.0f / lift * kMuUnlift));
+            });
+        return;
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+        m.apply(m.block(n), low[n], [&](int sb, int it, int v, const f32x4& y) {
+            const int64_t o = m.block(n) * (R * 64) + ((sb * M::NT + it) * M::V + v) * 512;
+            u32x2 lo;
+            *gst<u32x2>(w + o) = m.split(m.block(n), sb, it, v, y, lo);
+            *gst<u32x2>(w + at.lo + o) = lo;
+        });
+    mu_order();
+    __syncthreads();  // A's sums have been read; R = 64: X' is read by two waves
+    m.gram(kMuStrip / 32);
+    __syncthreads();
+    float* const o = reinterpret_cast<float*>(ws + at.part) + static_cast<int64_t>((src ^ 1) * strips + strip) * R * R;
+    for (int c = threadIdx.x; c < M::kPart / 16; c += kMuFewThreads) *gst<f32x4>(o + c * 4) = m.joined(c);
+}
+
+template <class Fn>
+void with_rows(int rows, Fn f) {
+    if (rows == 16) f(std::integral_constant<int, 16>{});
+    else if (rows == 32) f(std::integral_constant<int, 32>{});
+    else f(std::integral_constant<int, 64>{});
 }
 
 }  // namespace
 
 void launch_mu_few(const MuFewTensors& t, int rows, const MuFewArgs& a, hipStream_t s) {
-    const dim3 g(t.blocks), n(kMuFewThreads);
-    auto go = [&](auto r) {
-        constexpr int R = decltype(r)::value;
-        if (t.n == 1) hipLaunchKernelGGL((k_mu_few<R, 1>), g, n, 0, s, t.only(), a);
-        else hipLaunchKernelGGL((k_mu_few<R, kMuFewBatch>), g, n, 0, s, t, a);
-    };
-    if (rows == 16) go(std::integral_constant<int, 16>{});
-    else if (rows == 32) go(std::integral_constant<int, 32>{});
-    else go(std::integral_constant<int, 64>{});
+    with_rows(rows, [&](auto r) {
+        const dim3 g(t.blocks), n(kMuFewThreads);
+        if (t.n == 1) hipLaunchKernelGGL((k_mu_few<decltype(r)::value, 1>), g, n, 0, s, t.only(), a);
+        else hipLaunchKernelGGL((k_mu_few<decltype(r)::value, kMuFewBatch>), g, n, 0, s, t, a);
+    });
+}
+
+void launch_mu_strip_start(const MuTensors& t, int rows, const MuStepArgs& a, hipStream_t s) {
+    with_rows(rows, [&](auto r) {
+        const dim3 g(t.blocks), n(kMuFewThreads);
+        if (t.n == 1) hipLaunchKernelGGL((k_mu_strip_start<decltype(r)::value, 1>), g, n, 0, s, t.only(), a);
+        else hipLaunchKernelGGL((k_mu_strip_start<decltype(r)::value, kMuBatch>), g, n, 0, s, t, a);
+    });
+}
+
+void launch_mu_strip_step(const MuTensors& t, int rows, const MuPoly& p, int src, bool last, bool update, float decay, hipStream_t s) {
+    with_rows(rows, [&](auto r) {
+        const dim3 g(t.blocks), n(kMuFewThreads);
+        if (t.n == 1) hipLaunchKernelGGL((k_mu_strip_step<decltype(r)::value, 1>), g, n, 0, s, t.only(), p, src, last, update, decay);
+        else hipLaunchKernelGGL((k_mu_strip_step<decltype(r)::value, kMuBatch>), g, n, 0, s, t, p, src, last, update, decay);
+    });
 }
 
 }  // namespace meo
