@@ -1076,9 +1076,17 @@ MUON_KEYS = ["exp_avg", "exp_avg_scale"]
 NS_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 
 
+_NS_DEFAULT = meo_orthogonalize_hparams()
+for _row in _NS_DEFAULT.coefficients:
+    _row[:] = NS_COEFFICIENTS
+
+
 def orthogonalize_hparams(steps: int = 5, coefficients=NS_COEFFICIENTS, eps: float = 1e-7) -> meo_orthogonalize_hparams:
     """``coefficients``: one (a, b, c) for every step, or a sequence with one for each."""
-    hp = meo_orthogonalize_hparams(float(eps), int(steps), 0)
+    hp = meo_orthogonalize_hparams.from_buffer_copy(_NS_DEFAULT)
+    hp.eps, hp.steps = float(eps), int(steps)
+    if coefficients is NS_COEFFICIENTS:
+        return hp
     rows = list(coefficients)
     if len(rows) == 3 and not any(hasattr(v, "__len__") for v in rows):
         rows = [rows] * MEO_NS_MAX_STEPS
@@ -1131,6 +1139,9 @@ def _ns_row_stride(t: torch.Tensor, what: str) -> int:
 
 
 def _ns_matrices(xs, outs):
+    """The descriptors; they can stand for the tensors in the calls below."""
+    if isinstance(xs, ctypes.Array):
+        return xs
     if len(xs) != len(outs):
         raise ValueError("xs and outs differ in length")
     arr = (meo_ns_matrices * max(len(xs), 1))()
@@ -1141,10 +1152,11 @@ def _ns_matrices(xs, outs):
             raise TypeError("matrices must be float32 or bfloat16")
         if o.dtype != torch.bfloat16:
             raise TypeError("orthogonalized matrices are bfloat16")
-        if o.shape != x.shape or o.device != x.device:
-            raise ValueError(f"out of shape {tuple(o.shape)} on {o.device}, expected {tuple(x.shape)} on {x.device}")
-        arr[i] = meo_ns_matrices(x.data_ptr(), o.data_ptr(), math.prod(x.shape[:-2]), x.shape[-2], x.shape[-1],
-                                 _ns_row_stride(x, "x"), _ns_row_stride(o, "out"), _DTYPE[x.dtype], 0)
+        shape = x.shape
+        if o.shape != shape or o.device != x.device:
+            raise ValueError(f"out of shape {tuple(o.shape)} on {o.device}, expected {tuple(shape)} on {x.device}")
+        arr[i] = (x.data_ptr(), o.data_ptr(), math.prod(shape[:-2]), shape[-2], shape[-1],
+                  _ns_row_stride(x, "x"), _ns_row_stride(o, "out"), _DTYPE[x.dtype], 0)
     return arr
 
 

@@ -50,9 +50,13 @@ def orthogonalize(x: Union[torch.Tensor, Sequence[torch.Tensor]], steps: int = 5
     for t, o in zip(xs, outs):
         if t.dim() < 2:
             raise ValueError("orthogonalize takes matrices (two or more dims)")
-        t = t.detach()
+        if t.requires_grad:
+            t = t.detach()
         # the transpose's result is the result's transpose: either orientation is worked on as it lies
-        if o is None:
+        if o is None and t.is_contiguous():
+            v, o = t, torch.empty_like(t, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
+            d = o
+        elif o is None:
             flip = not _row_major(t) and _row_major(t.mT)
             v = t.mT if flip else t
             v = v if flip or _row_major(v) else v.contiguous()
@@ -68,7 +72,8 @@ def orthogonalize(x: Union[torch.Tensor, Sequence[torch.Tensor]], steps: int = 5
         src.append(v)
         dst.append(d)
         res.append(o)
-    size = _lib.meo_orthogonalize_workspace_size(hp, src, dst)
-    _call(xs[0].device, lambda: _lib.meo_orthogonalize(hp, src, dst, _lib.workspace(size, xs[0].device)),
+    arr = _lib._ns_matrices(src, dst)
+    size = _lib.meo_orthogonalize_workspace_size(hp, arr, dst)
+    _call(xs[0].device, lambda: _lib.meo_orthogonalize(hp, arr, dst, _lib.workspace(size, xs[0].device)),
           what="orthogonalize needs matrices")
     return res[0] if single else res
