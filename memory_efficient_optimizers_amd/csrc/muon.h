@@ -9,7 +9,7 @@ constexpr int kMuPad = 64;         // both sides of a matrix in the workspace ar
 constexpr int kMuBatch = 16;       // tensors per launch (their descriptors are kernel arguments)
 constexpr int kMuThreads = 256;    // momentum and scatter passes
 constexpr int kMuTile = 64;        // scatter pass: square tiles of the matrix in the workspace
-constexpr int64_t kMuPart = 8192;  // values per part of the momentum pass
+constexpr int64_t kMuPart = 2048;  // values per part of the momentum pass, up to kMuMaxParts of them
 constexpr int64_t kMuMaxParts = 1024;
 constexpr int64_t kMuMaxSide = 1 << 22;  // longer side of a matrix (32-bit offsets in a tile)
 

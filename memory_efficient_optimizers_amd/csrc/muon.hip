@@ -291,7 +291,8 @@ __device__ __forceinline__ void mu_accumulate(const uint16_t* P, int cols_p, int
     wait_and_sync<0>();  // transfers past the end have landed before the stages are reused
 }
 
-// Blocks go round-robin to the 8 XCDs: consecutive tiles on one XCD.
+// Blocks go round-robin to the 8 XCDs: consecutive tiles of a tensor on one XCD. (Of the whole list,
+// some XCDs had all tiles of the tensors with a long contraction.)
 __device__ __forceinline__ uint32_t mu_swizzle(uint32_t id, uint32_t n) {
     constexpr uint32_t kX = 8;
     const uint32_t x = id % kX, q = n / kX, r = n % kX;
@@ -436,12 +437,11 @@ template <int F, int N>
 __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_gram(MuListOf<MuMatrix, N> l, int src) {
     using M = MuTiles<F>;
     __shared__ __attribute__((aligned(16))) uint8_t lds[M::kLds];
-    const uint32_t id = mu_swizzle(blockIdx.x, l.blocks);
-    const int k = mu_find(l, id);
+    const int k = mu_find(l, blockIdx.x);
     const MuMatrix& m = l.d[k];
     const int nt = (m.mp + M::kT - 1) / M::kT;
     const uint32_t per = nt * (nt + 1) / 2;
-    uint32_t t = mu_item(l, k, id);
+    uint32_t t = mu_swizzle(mu_item(l, k, blockIdx.x), per * m.parts * m.batch);
     const uint32_t b = t / (per * m.parts);
     t -= b * (per * m.parts);
     const int part = static_cast<int>(t / per);
@@ -542,12 +542,11 @@ template <int F, int N>
 __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_poly(MuListOf<MuMatrix, N> l, MuPoly p) {
     using M = MuTiles<F>;
     __shared__ __attribute__((aligned(16))) uint8_t lds[M::kLds];
-    const uint32_t id = mu_swizzle(blockIdx.x, l.blocks);
-    const int k = mu_find(l, id);
+    const int k = mu_find(l, blockIdx.x);
     const MuMatrix& m = l.d[k];
     const int nt = (m.mp + M::kT - 1) / M::kT;
     const uint32_t per = nt * (nt + 1) / 2;
-    const uint32_t t = mu_item(l, k, id), b = t / per;
+    const uint32_t t = mu_swizzle(mu_item(l, k, blockIdx.x), per * m.batch), b = t / per;
     int ti, tj;
     mu_triangle(t % per, nt, ti, tj);
     ti = uniform(ti);
@@ -555,9 +554,6 @@ __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_poly
     const MuPlace at(m.mp, m.np, m.parts);
     uint8_t* const w = m.ws + b * m.stride;
     const uint16_t* o = reinterpret_cast<const uint16_t*>(w + at.a);
-    f32x16 acc[M::MB][M::NB];
-    mu_zero<M>(acc);
-    mu_accumulate<M, false>(o, m.mp, m.mp, o, m.mp, m.mp, ti * M::kT, tj * M::kT, 0, m.mp / 32, lds, acc);
     uint16_t* const out = reinterpret_cast<uint16_t*>(w + at.b);
     const float* const d = reinterpret_cast<const float*>(w + at.d);
     float* const q = reinterpret_cast<float*>(w + at.q);
@@ -569,7 +565,11 @@ __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_poly
             if (r.has(m.mp, m.mp, j0, e)) f[e] = *gld<u32x4>(r.place(const_cast<uint16_t*>(o), m.mp, j0, e));
     };
     u32x4 next[R::kIters];
-    load(r.jb, next);
+    if (M::kT < 256) load(r.jb, next);  // (the first round's before the product, which hides it; large: no registers)
+    f32x16 acc[M::MB][M::NB];
+    mu_zero<M>(acc);
+    mu_accumulate<M, false>(o, m.mp, m.mp, o, m.mp, m.mp, ti * M::kT, tj * M::kT, 0, m.mp / 32, lds, acc);
+    if (M::kT == 256) load(r.jb, next);
     // d_i of the wave's rows, in LDS
     const uint32_t di = r.base + R::kBytes;
     for (int i = r.lane; i < R::kI; i += 64)
@@ -633,11 +633,10 @@ __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_appl
     using M = MuTiles<F>;
     constexpr bool kLast = !std::is_same<Last, MuNone>::value;
     __shared__ __attribute__((aligned(16))) uint8_t lds[M::kLds];
-    const uint32_t id = mu_swizzle(blockIdx.x, l.blocks);
-    const int k = mu_find(l, id);
+    const int k = mu_find(l, blockIdx.x);
     const MuMatrix& m = l.d[k];
     const uint32_t tm = (m.mp + M::kT - 1) / M::kT, tn = (m.np + M::kT - 1) / M::kT, per = tm * tn;
-    uint32_t t = mu_item(l, k, id);
+    uint32_t t = mu_swizzle(mu_item(l, k, blockIdx.x), per * m.batch);
     const uint32_t b = t / per;
     t -= b * per;
     // kMuGroup rows of X' at a time, by columns
@@ -648,10 +647,6 @@ __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_appl
     uint8_t* const w = m.ws + b * m.stride;
     const uint16_t* const x = reinterpret_cast<const uint16_t*>(w + at.hi(src));
     uint16_t* const lo = reinterpret_cast<uint16_t*>(w + at.lo);
-    f32x16 acc[M::MB][M::NB];
-    mu_zero<M>(acc);
-    mu_accumulate<M, true>(x, m.np, m.np, reinterpret_cast<const uint16_t*>(w + at.b), m.mp, m.mp, ti * M::kT, tj * M::kT, 0,
-                           m.mp / 32, lds, acc);
     const float* const q = reinterpret_cast<const float*>(w + at.q);
     uint16_t* const hi = reinterpret_cast<uint16_t*>(w + at.hi(src ^ 1));
     using R = MuRound<M>;
@@ -667,7 +662,12 @@ __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_appl
         }
     };
     u32x4 next[2 * R::kIters];
-    load(r.jb, next);
+    if (M::kT < 256) load(r.jb, next);  // (the first round's before the product, which hides it; large: no registers)
+    f32x16 acc[M::MB][M::NB];
+    mu_zero<M>(acc);
+    mu_accumulate<M, true>(x, m.np, m.np, reinterpret_cast<const uint16_t*>(w + at.b), m.mp, m.mp, ti * M::kT, tj * M::kT, 0,
+                           m.mp / 32, lds, acc);
+    if (M::kT == 256) load(r.jb, next);
     const float un = 1.0f / m.lift * kMuUnlift;
     const float* const d = reinterpret_cast<const float*>(w + at.d);
 #pragma unroll
