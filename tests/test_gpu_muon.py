@@ -239,6 +239,104 @@ def test_several_parts_of_a_list():
         assert torch.equal(ys[1][b], orthogonalize(xs[1][b]))
 
 
+# ------------------------------------------------------------------------------ few rows
+
+# One strip of 512 columns and up to 64 (32 of 64 rows) of them, either way round, and what lies beside.
+FEW = [(1, 512), (513, 1), (15, 511), (16, 512), (513, 16), (17, 700), (32, 512), (32, 1025), (512, 33), (1025, 33), (64, 512), (64, 513),
+       (63, 5000), (2000, 32), (5, 12000)]
+ENDS = [(16, 32768), (32769, 16), (31, 32767), (64, 16384), (16385, 64)]
+
+
+@pytest.mark.parametrize("shape", FEW)
+def test_few_rows_one_step_element_by_element(shape):
+    x = matrix(shape, 100)
+    want = exact(x, steps=1)
+    lim = om.bound_of_one_step(to64(x)) + 2.0 ** -22 * np.abs(want)
+    assert np.all(np.abs(to64(raw([x], ns_steps=1)[0]) - want) <= lim)
+
+
+@pytest.mark.parametrize("kind", ["noise", "low"])
+@pytest.mark.parametrize("shape", FEW + ENDS)
+def test_few_rows(shape, kind):
+    x = matrix(shape, 101, kind)
+    check(raw([x])[0], x)
+    check(orthogonalize(x), x)
+
+
+@pytest.mark.parametrize("shape", [(5, 1, 600), (3, 40, 600), (2, 700, 20), (4, 30, 30), (2, 3, 1100, 60)])
+def test_batches_of_few_rows(shape):
+    x = matrix(shape, 102, dtype=torch.bfloat16)
+    y = orthogonalize(x)
+    check(y, x)
+    flat = x.reshape(-1, *shape[-2:])
+    assert all(torch.equal(a, orthogonalize(b)) for a, b in zip(y.reshape(flat.shape), flat))
+
+
+@pytest.mark.parametrize("shape", [(20, 1300), (1300, 20), (60, 90), (90, 60)])
+def test_layouts_of_few_rows(shape):
+    """Strided rows, column-major, results into a view whose surroundings stay."""
+    r, c = shape
+    base = matrix((r + 4, c + 9), 103)
+    for x in (base[1:r + 1, 3:c + 3], base[1:r + 1, 3:c + 3].t()):
+        whole = torch.full((x.shape[0] + 3, x.shape[1] + 5), 7.0, dtype=torch.bfloat16, device=DEV)
+        o = whole[2:-1, 3:-2]
+        assert orthogonalize(x, out=o) is o
+        check(o, x)
+        assert torch.equal(orthogonalize(x), o)
+        whole[2:-1, 3:-2] = 7.0
+        assert (whole == 7.0).all()
+    b = base[1:r + 1, 3:c + 3].bfloat16()
+    want = orthogonalize(b)
+    assert torch.equal(orthogonalize(b, out=b), want)  # in place
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("rows,cols", [(30, 20), (900, 40), (12, 2000), (70, 100), (300, 200)])
+def test_non_finite_matrices_of_every_kind(rows, cols, value):
+    x = matrix((3, rows, cols), 104)
+    x[1, rows - 1, cols - 1] = value
+    y = orthogonalize([x, matrix((30, 20), 8)])
+    assert y[0][1].isnan().all() and y[0][0].isfinite().all() and y[0][2].isfinite().all() and y[1].isfinite().all()
+    check(y[0][::2].contiguous(), x[::2].contiguous())
+    p, g, st = init((rows, cols), 105, F, F, F)
+    g[0, 0] = value
+    muon_step([p], [g], [st], lr=0.1)
+    assert p.isnan().all()
+
+
+@pytest.mark.parametrize("shape", [(24, 40), (24, 1400), (100, 200)])
+def test_values_at_the_ends_of_the_range_of_every_kind(shape):
+    x = matrix(shape, 106)
+    want = to64(raw([x])[0])
+    for scale in (1e-30, 1e30):
+        for v in raw([x * scale], eps=0.0):
+            assert np.linalg.norm(to64(v) - want) <= 4e-3 * np.linalg.norm(want)  # (another realization)
+    assert (orthogonalize(torch.zeros(shape, device=DEV)) == 0).all()
+    assert (orthogonalize(torch.zeros(shape, device=DEV), eps=0.0) == 0).all()
+    z = x.clone()
+    z[3] = 0.0
+    z[:, 5] = 0.0
+    o = orthogonalize(z)
+    assert (o[3] == 0).all() and (o[:, 5] == 0).all()
+    check(o, z)
+
+
+def test_long_lists_of_few_rows():
+    """More of each kind than a launch takes: each as it comes out alone."""
+    shapes = [(1 + i % 16, 20 + 3 * i) for i in range(50)] + [(600 + 40 * i, 17 + i % 16) for i in range(18)] + [(40, 64)] * 3
+    xs = [matrix(s, 200 + i) for i, s in enumerate(shapes)]
+    ys = orthogonalize(xs)
+    assert all(torch.equal(y, orthogonalize(x)) for x, y in zip(xs, ys))
+
+
+def test_steps_and_coefficients_of_few_rows():
+    for shape in ((40, 100), (20, 1700)):
+        x = matrix(shape, 107)
+        for steps, coefficients in ((1, om.COEFFICIENTS), (2, om.COEFFICIENTS), (10, (2.0, -1.5, 0.5)),
+                                    (4, [(8.2, -22.9, 16.46), (4.0, -2.9, 0.5), (3.9, -2.8, 0.5), (3.3, -2.4, 0.5)])):
+            check(orthogonalize(x, steps=steps, coefficients=coefficients), x, steps=steps, coefficients=coefficients)
+
+
 # ------------------------------------------------------------------------------ the Muon step
 
 def init(shape, seed, param, grad, state, scale=1e-3):
@@ -290,6 +388,35 @@ def test_step(param, grad, state, nesterov, adjust_lr):
     muon_step(ps, gs, sts, momentum=0.9, **kw)
     for p, st, (p0, g, m0) in zip(ps, sts, before):
         check_step(p, st, p0, g, m0, str(state).split(".")[1], momentum_=0.9, **kw)
+
+
+@pytest.mark.parametrize("param,grad,state", [(F, F, F), (F, B, I), (B, B, B), (B, F, I), (F, F, B)])
+def test_step_of_few_rows(param, grad, state):
+    """One strip and several, either way round, odd sizes, a batch (8-bit: whole groups)."""
+    shapes = [(16, 512), (40, 1003), (1030, 10), (3, 16, 1024), (2, 640, 32), (31, 30), (61, 513), (1, 1), (4097, 2)]
+    made = [init(s, 300 + i, param, grad, state) for i, s in enumerate(shapes)]
+    ps, gs, sts = ([v[k] for v in made] for k in range(3))
+    before = [(to64(p), g.float().cpu().numpy(), momentum_of(st)) for p, g, st in made]
+    kw = dict(lr=0.05, weight_decay=0.1, adjust_lr="match_rms_adamw")
+    muon_step(ps, gs, sts, momentum=0.9, **kw)
+    for p, st, (p0, g, m0) in zip(ps, sts, before):
+        check_step(p, st, p0, g, m0, str(state).split(".")[1], momentum_=0.9, **kw)
+
+
+@pytest.mark.parametrize("shape", [(16, 77), (77, 16), (30, 1203), (1203, 30)])
+def test_unaligned_tensors_of_few_rows(shape):
+    for param, grad, state in ((F, B, F), (B, F, B), (F, F, I)):
+        p, g, st = init(shape, 108, param, grad, state)
+        t = {}
+        for name, v in (("p", p), ("g", g), ("m", st["exp_avg"])):
+            buf = torch.full((v.numel() + 2,), 3, dtype=v.dtype, device=DEV)
+            buf[1:-1] = v.view(-1)
+            t[name] = (buf, buf[1:-1].view(shape))
+        p0, m0 = to64(p), momentum_of(st)
+        new = dict(st, exp_avg=t["m"][1])
+        muon_step([t["p"][1]], [t["g"][1]], [new], lr=0.1)
+        check_step(t["p"][1], new, p0, g.float().cpu().numpy(), m0, str(state).split(".")[1], lr=0.1)
+        assert all(b[0] == 3 and b[-1] == 3 for b, _ in t.values())
 
 
 def test_8_bit_momentum_groups():
@@ -404,6 +531,26 @@ def test_captured_and_replayed():
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
         for a, b in zip(made, eager):
             assert torch.equal(a[0], b[0]) and torch.equal(a[2]["exp_avg"], b[2]["exp_avg"])
+
+
+def test_few_rows_captured_and_replayed():
+    shapes = [(40, 50), (20, 1500), (2, 1500, 60), (16, 16), (60, 400)]
+    made, eager = ([init(s, 110 + i, F, B, I if i % 2 else F) for i, s in enumerate(shapes)] for _ in range(2))
+    hp = _lib.muon_hparams(lr=0.1)
+    args = [[v[k] for v in made] for k in range(3)]
+    ws = _lib.workspace(_lib.meo_muon_workspace_size(hp, *args), DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _lib.meo_muon_step(hp, 1, *args, ws)
+    for i in range(4):
+        for a, b in zip(made, eager):
+            b[1].copy_(a[1].mul_(-1.25))
+        graph.replay()
+        muon_step(*([v[k] for v in eager] for k in range(3)), lr=0.1)
+        torch.cuda.synchronize()
+        for a, b in zip(made, eager):
+            assert torch.equal(a[0], b[0]) and all(torch.equal(a[2][k], b[2][k]) for k in a[2])
 
 
 def test_memory_refusals():
