@@ -2767,8 +2767,12 @@ struct MuIn {
     bool empty() const { return batch == 0 || rows == 0 || cols == 0; }
     int few() const { return mu_few(std::min(rows, cols), std::max(rows, cols)); }
     int64_t mp() const { return few() ? few() : ceil_div(std::min(rows, cols), kMuPad) * kMuPad; }
-    int64_t np() const { return ceil_div(std::max(rows, cols), few() ? kMuStrip : kMuPad) * (few() ? kMuStrip : kMuPad); }
-    bool whole() const { return few() && np() == kMuStrip; }  // all steps in one launch
+    int64_t np() const {
+        const int64_t unit = few() ? mu_strip(few()) : kMuPad;
+        return ceil_div(std::max(rows, cols), unit) * unit;
+    }
+    int64_t strips() const { return few() ? np() / mu_strip(few()) : 0; }
+    bool whole() const { return strips() == 1; }  // all steps in one launch
     // The power of two that values are held times: about the square root of the longer side, so that
     // entries of a matrix with orthonormal rows are about 1.
     int lift() const { return std::min(12, static_cast<int>(std::lround(0.5 * std::log2(static_cast<double>(std::max(rows, cols)))))); }
@@ -2810,7 +2814,7 @@ int64_t mu_norm_span(const MuIn& t) { return ceil_div(mu_norm_tiles(t), kMuMaxPa
 int64_t mu_norm_parts(const MuIn& t) { return ceil_div(mu_norm_tiles(t), mu_norm_span(t)); }
 
 int64_t mu_stride(const MuIn& t) {
-    if (t.few()) return align256(MuStripPlace(t.mp(), t.np()).total);
+    if (t.few()) return align256(MuStripPlace(t.mp(), t.np(), t.strips()).total);
     int64_t parts, steps;
     mu_gram_parts(t.mp(), t.np(), &parts, &steps);
     return align256(MuPlace(t.mp(), t.np(), parts).total);
@@ -3059,7 +3063,7 @@ int mu_run(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, MuS
                           static_cast<float>(hp.coefficients[k][2])};
         };
         if (c.rows) {
-            count(t, [&](const MuTensor& d) { return int64_t{d.batch} * (d.np / kMuStrip); });
+            count(t, [&](const MuTensor& d) { return int64_t{d.batch} * (d.np / mu_strip(c.rows)); });
             launch_mu_strip_start(t, c.rows, a, s);
             pt.mark(kPassMuScatter);
             for (int k = 0; k < hp.steps; ++k) {

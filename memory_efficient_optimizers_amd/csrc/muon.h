@@ -106,21 +106,21 @@ using MuLast = MuLastOf<kMuBatch>;
 // ---- matrices with few rows
 
 // A matrix whose shorter side is at most 64 takes 16, 32 or 64 rows, and its longer side strips of
-// kMuStrip columns, one to a thread block: of one strip, all steps are one launch; of up to 64 (32 of
+// mu_strip columns, one to a thread block: of one strip, all steps are one launch; of up to 64 (32 of
 // 64 rows), a launch each. The rows; 0: the matrix is worked on in tiles. From the matrix
 // alone: its result does not depend on the list.
-constexpr int kMuStrip = 512;
+__host__ __device__ constexpr int mu_strip(int rows) { return rows == 64 ? 256 : 512; }
 __host__ __device__ constexpr int mu_few(int64_t m, int64_t n) {
-    return m <= 16 && n <= 64 * kMuStrip ? 16 : m <= 32 && n <= 64 * kMuStrip ? 32 : m <= 64 && n <= 32 * kMuStrip ? 64 : 0;
+    return m <= 16 && n <= 64 * mu_strip(16) ? 16 : m <= 32 && n <= 64 * mu_strip(32) ? 32 : m <= 64 && n <= 32 * mu_strip(64) ? 64 : 0;
 }
 // The workspace of one in strips (np: whole strips): the iterate's high and low parts, and two buffers
 // of the strips' parts of A.
 struct MuStripPlace {
     int64_t lo, part, total;
-    __host__ __device__ MuStripPlace(int64_t rows, int64_t np) {
+    __host__ __device__ MuStripPlace(int64_t rows, int64_t np, int64_t strips) {
         lo = rows * np * 2;
         part = 2 * lo;
-        total = part + 2 * (np / kMuStrip) * rows * rows * 4;
+        total = part + 2 * strips * rows * rows * 4;
     }
 };
 constexpr int kMuFewBatch = 48;     // tensors per launch

@@ -1,18 +1,21 @@
-// Orthogonalization and the Muon step of matrices with few rows (a shorter side of at most 64): the
-// mathematics and roundings of muon.hip, where each pass over such a matrix is a launch of 3 to
-// 5 us, 17 and more of them.
+// Orthogonalization and the Muon step of matrices with few rows (a shorter side of at most 64), where
+// each pass of muon.hip over such a matrix is a launch of 3 to 5 us, 17 and more of them.
 //
-// The longer side goes by blocks of 32 columns, 16 of them (a strip) to a thread block, of which a
-// wave has two: the step X' = a X + B X needs nothing else of X. A = X X^T is summed over the waves
-// through LDS, over strips through the workspace. Every wave then forms B for itself: in an accumulator
-// of a symmetric matrix a lane holds four consecutive rows of a column, which are four
+// The mathematics is muon.hip's, but X, A and B are held as two fp16 parts in every product (hi hi +
+// hi lo + lo hi: 22 bits): products are what such matrices have little of, and small ones would lose
+// more to fp16 than large ones do (16 x 16: 1.3e-3 of the result with one part, 3e-7 so).
+//
+// The longer side goes by blocks of 32 columns, a strip of them to a thread block, of which a wave has
+// two (one of 64 rows): the step X' = a X + B X needs nothing else of X. A = X X^T is summed over the
+// waves through LDS, over strips through the workspace. Every wave then forms B for itself: in an
+// accumulator of a symmetric matrix a lane holds four consecutive rows of a column, which are four
 // consecutive values of the contraction of that column as an operand, so A, A^2 and B go from
-// product to product in registers. A matrix of one strip is one launch, with the iterate in LDS (high
-// parts) and registers (low parts); one of more strips is a launch per step and two before them.
+// product to product in registers. A matrix of one strip is one launch, with the iterate in LDS; one of
+// more strips is a launch per step and two before them.
 //
-// What bounds it: latencies (launches, barriers, LDS, dependent products). The work per value is
-// some 8 vector instructions a step, 2 us for 16 x 4096 on one CU: that many in one block took 59 us
-// (4096 x 16: 87).
+// What bounds it: latencies (launches, barriers, LDS, dependent products). The work per value is some
+// 8 vector instructions a step, too many for one CU from 16 x 1024 on: 16 x 4096 in one block took
+// 59 us, 4096 x 16 87.
 #include "muon_device.h"
 
 namespace meo {
@@ -27,7 +30,6 @@ typedef __attribute__((address_space(3))) double D1;
 typedef __attribute__((address_space(3))) uint16_t H1;
 
 constexpr int kMuFewWaves = kMuFewThreads / 64;
-static_assert(kMuStrip == 2 * 32 * kMuFewWaves, "two blocks per wave");
 
 // An LDS access of a wave to what its other lanes wrote is not moved over this.
 __device__ __forceinline__ void mu_order() { __asm__ volatile("" ::: "memory"); }
@@ -53,17 +55,19 @@ __device__ __forceinline__ uint32_t mu_few_at(int r, int c8) {
     return r * 64 + (((c8 >> 1) ^ ((r >> 2) & 3)) << 4) + (c8 & 1) * 8;
 }
 
-// The products of a strip of R rows at LDS address x. Accumulators: tiles of T x T, where a lane holds
+// The products of a strip of R rows, its high parts at LDS address x, its low parts kBytes on. Accumulators: tiles of T x T, where a lane holds
 // rows 8 v + 4 h + 0 .. 3 of its column, v < V. A block of 32 columns: SB parts of NT tiles.
 template <int R>
 struct MuFew {
     static constexpr int T = R == 16 ? 16 : 32, NT = R / T, V = T == 16 ? 1 : 4, SB = 32 / T;
-    static constexpr int kBytes = R * kMuStrip * 2;  // of one part of the strip
+    static constexpr int kStrip = mu_strip(R), NB = kStrip / 32 / kMuFewWaves;  // columns; blocks per wave
+    static constexpr int kBytes = R * kStrip * 2;  // of one part of the strip
     // A's parts: by wave; R = 64: by pairs of waves, which have a column of tiles each.
     static constexpr int kParts = R == 64 ? kMuFewWaves / 2 : kMuFewWaves;
     static constexpr int kPart = R * R * 4, kSums = kParts * kPart;
     struct Acc { f32x4 v[V]; };
     struct Op { u32x2 v[V]; };  // T values of the contraction
+    struct Ops { Op hi, lo; };
     typedef u32x2 Block[SB][NT][V];  // of the iterate, as accumulators have it
 
     uint32_t x, sums;
@@ -86,6 +90,11 @@ struct MuFew {
                              u32x4{b.v[2 * s].x, b.v[2 * s].y, b.v[2 * s + 1].x, b.v[2 * s + 1].y}, w);
             c = __builtin_bit_cast(Acc, w);
         }
+    }
+    static __device__ __forceinline__ void mul(Acc& c, const Ops& a, const Ops& b) {
+        mul(c, a.hi, b.lo);
+        mul(c, a.lo, b.hi);
+        mul(c, a.hi, b.hi);
     }
     static __device__ __forceinline__ void zero(Acc& c) {
 #pragma unroll
@@ -117,16 +126,27 @@ struct MuFew {
             const uint32_t o = x + blk * (R * 64);
             if constexpr (T == 16) {
                 const half8 w = __builtin_bit_cast(half8, mu_lds(o + mu_few_at(col, 2 * h)));
+                const half8 z = __builtin_bit_cast(half8, mu_lds(o + kBytes + mu_few_at(col, 2 * h)));
+                g[0].v[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, z, g[0].v[0], 0, 0, 0);
+                g[0].v[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(z, w, g[0].v[0], 0, 0, 0);
                 g[0].v[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, w, g[0].v[0], 0, 0, 0);
             } else {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    u32x4 w[NT];
+                    u32x4 w[NT], z[NT];
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) w[i] = mu_lds(o + mu_few_at(i * T + col, 4 * c + 2 * h));
-                    const u32x4 z = NT == 1 || tj == 0 ? w[0] : w[NT - 1];
+                    for (int i = 0; i < NT; ++i) {
+                        w[i] = mu_lds(o + mu_few_at(i * T + col, 4 * c + 2 * h));
+                        z[i] = mu_lds(o + kBytes + mu_few_at(i * T + col, 4 * c + 2 * h));
+                    }
+                    const u32x4 wj = NT == 1 || tj == 0 ? w[0] : w[NT - 1], zj = NT == 1 || tj == 0 ? z[0] : z[NT - 1];
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) g[i] = __builtin_bit_cast(Acc, mfma_f16(w[i], z, __builtin_bit_cast(f32x16, g[i])));
+                    for (int i = 0; i < NT; ++i) {
+                        f32x16 y = __builtin_bit_cast(f32x16, g[i]);
+                        y = mfma_f16(w[i], zj, y);
+                        y = mfma_f16(z[i], wj, y);
+                        g[i] = __builtin_bit_cast(Acc, mfma_f16(w[i], wj, y));
+                    }
                 }
             }
         }
@@ -144,13 +164,20 @@ struct MuFew {
         return w;
     }
 
+    // Four fp32 values as two fp16 parts.
+    static __device__ __forceinline__ u32x2 parts(const f32x4& y, u32x2& lo) {
+        const u32x2 w = mu_pack4(y.x, y.y, y.z, y.w);
+        lo = mu_pack4(y.x - mu_half(w, 0), y.y - mu_half(w, 1), y.z - mu_half(w, 2), y.w - mu_half(w, 3));
+        return w;
+    }
+
     // From X X^T (times 4^lift, at `sums`): the wave's B, 2^8 times off the diagonal, as operands, and
-    // of its lanes' columns q = a + B_ii and t = a + B_ii min(1, d_i^2), 2^8 times.
-    Op B[NT][NT];  // [column][row]
-    float q[NT], tl[NT];
+    // of its lanes' columns q = a + B_ii, 2^8 times.
+    Ops B[NT][NT];  // [column][row]
+    float q[NT];
     __device__ __forceinline__ void poly(const MuPoly& p, float un) {
         const int holder = col + T * ((col >> 2) & (64 / T - 1));  // the lane with the diagonal of column `col`
-        Op O[NT][NT];
+        Ops O[NT][NT];
         float d[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -166,8 +193,7 @@ struct MuFew {
                             own = w[e];
                             w[e] = 0.0f;
                         }
-                    w *= kMuLift;
-                    O[j][i].v[v] = mu_pack4(w.x, w.y, w.z, w.w);
+                    O[j][i].hi.v[v] = parts(w * kMuLift, O[j][i].lo.v[v]);
                 }
             d[j] = __shfl(own, holder, 64);
         }
@@ -188,39 +214,39 @@ struct MuFew {
                 float own = 0.0f;
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    float y[4];
+                    f32x4 y;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        y[e] = fmaf(mu_half(O[j][i].v[v], e), fmaf(p.c, di[v][e] + d[j], p.b), sq.v[v][e] * cs);
+                        const float o = mu_half(O[j][i].hi.v[v], e) + mu_half(O[j][i].lo.v[v], e);
+                        y[e] = fmaf(o, fmaf(p.c, di[v][e] + d[j], p.b), sq.v[v][e] * cs);
                         if (i == j && 8 * v + 4 * h + e == col) {
                             own = p.a + fmaf(p.b, d[j], p.c * fmaf(d[j], d[j], sq.v[v][e] * (kMuUnlift * kMuUnlift)));
                             y[e] = 0.0f;
                         }
                     }
-                    B[j][i].v[v] = mu_pack4(y[0], y[1], y[2], y[3]);
+                    B[j][i].hi.v[v] = parts(y, B[j][i].lo.v[v]);
                 }
-                if (i == j) {
-                    const float al = p.a * kMuLift;
-                    q[j] = __shfl(own, holder, 64) * kMuLift;
-                    tl[j] = fmaf(q[j] - al, fminf(d[j] * d[j], 1.0f), al);
-                }
+                if (i == j) q[j] = __shfl(own, holder, 64) * kMuLift;
             }
         }
     }
 
-    // X' of a block from its high parts in LDS and the low ones `lo`: f(sb, it, v, four values, 2^8 times).
+    // X' of a block of LDS: f(sb, it, v, four values, 2^8 times).
     template <class Fn>
-    __device__ __forceinline__ void apply(int blk, const Block& lo, Fn f) const {
+    __device__ __forceinline__ void apply(int blk, Fn f) const {
         mu_order();
 #pragma unroll
         for (int sb = 0; sb < SB; ++sb) {
-            Op xt[NT];  // X^T's part: 4 rows of X of the lane's column each
+            Ops xt[NT];  // X^T's part: 4 rows of X of the lane's column each
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    xt[i].v[v] = mu_lds_tr(x + blk * (R * 64) + mu_few_at(i * T + 8 * v + 4 * h + ((lane >> 2) & 3),
-                                                                        T == 16 ? 4 * sb + (lane & 3) : ((lane >> 4) & 1) * 4 + (lane & 3)));
+                for (int v = 0; v < V; ++v) {
+                    const uint32_t at = x + blk * (R * 64) + mu_few_at(i * T + 8 * v + 4 * h + ((lane >> 2) & 3),
+                                                                       T == 16 ? 4 * sb + (lane & 3) : ((lane >> 4) & 1) * 4 + (lane & 3));
+                    xt[i].hi.v[v] = mu_lds_tr(at);
+                    xt[i].lo.v[v] = mu_lds_tr(at + kBytes);
+                }
             mu_order();
 #pragma unroll
             for (int it = 0; it < NT; ++it) {
@@ -230,21 +256,22 @@ struct MuFew {
                 for (int i = 0; i < NT; ++i) mul(c, xt[i], B[it][i]);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const u32x2 xh = *(const L2*)static_cast<uintptr_t>(place(blk, sb, it, v)), xl = lo[sb][it][v];
+                    const uint32_t at = place(blk, sb, it, v);
+                    const u32x2 xh = *(const L2*)static_cast<uintptr_t>(at), xl = *(const L2*)static_cast<uintptr_t>(at + kBytes);
                     f32x4 y;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = fmaf(tl[it], mu_half(xl, e), fmaf(q[it], mu_half(xh, e), c.v[v][e]));
+                    for (int e = 0; e < 4; ++e) y[e] = fmaf(q[it], mu_half(xl, e), fmaf(q[it], mu_half(xh, e), c.v[v][e]));
                     f(sb, it, v, y);
                 }
             }
         }
     }
-    // As an iterate's high parts (also into LDS) and low parts.
-    __device__ __forceinline__ u32x2 split(int blk, int sb, int it, int v, f32x4 y, u32x2& lo) const {
-        y *= kMuUnlift;
-        const u32x2 w = mu_pack4(y.x, y.y, y.z, y.w);
-        *(L2*)static_cast<uintptr_t>(place(blk, sb, it, v)) = w;
-        lo = mu_pack4(y.x - mu_half(w, 0), y.y - mu_half(w, 1), y.z - mu_half(w, 2), y.w - mu_half(w, 3));
+    // As an iterate's parts, into LDS.
+    __device__ __forceinline__ u32x2 split(int blk, int sb, int it, int v, const f32x4& y, u32x2& lo) const {
+        const u32x2 w = parts(y * kMuUnlift, lo);
+        const uint32_t at = place(blk, sb, it, v);
+        *(L2*)static_cast<uintptr_t>(at) = w;
+        *(L2*)static_cast<uintptr_t>(at + kBytes) = lo;
         return w;
     }
     // The first column, in a block, of four values.
@@ -253,6 +280,19 @@ struct MuFew {
 
 __device__ __forceinline__ void mu_few_clear(uint32_t at, uint32_t bytes) {
     for (uint32_t o = threadIdx.x * 16; o < bytes; o += kMuFewThreads * 16) *(L4*)static_cast<uintptr_t>(at + o) = u32x4{0u, 0u, 0u, 0u};
+}
+// 8 values of a row, and one, of a strip in LDS.
+template <int R>
+__device__ __forceinline__ void mu_few_put(uint32_t x, int r, int c, const uint32_t* hi, const uint32_t* lo) {
+    const uint32_t at = x + (c >> 5) * (R * 64) + mu_few_at(r, (c & 31) >> 2);
+    *(L4*)static_cast<uintptr_t>(at) = u32x4{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16};
+    *(L4*)static_cast<uintptr_t>(at + MuFew<R>::kBytes) = u32x4{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16};
+}
+template <int R>
+__device__ __forceinline__ void mu_few_put1(uint32_t x, int r, int c, uint32_t hi, uint32_t lo) {
+    const uint32_t at = x + (c >> 5) * (R * 64) + mu_few_at(r, (c & 31) >> 2) + (c & 3) * 2;
+    *(H1*)static_cast<uintptr_t>(at) = static_cast<uint16_t>(hi);
+    *(H1*)static_cast<uintptr_t>(at + MuFew<R>::kBytes) = static_cast<uint16_t>(lo);
 }
 // The sum over the block, in order; `at`: 8 bytes of LDS per wave.
 __device__ __forceinline__ double mu_few_sum(double s, uint32_t at) {
@@ -309,8 +349,8 @@ __device__ __forceinline__ void mu_few_store(const MuTensor& t, bool update, flo
 template <int R, int N>
 __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_few(MuListOf<MuFewTensor, N> l, MuFewArgs a) {
     using M = MuFew<R>;
-    constexpr int kTurn = kMuFewThreads * kVec, kTurns = R * kMuStrip / kTurn;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[M::kBytes + M::kSums];
+    constexpr int kTurn = kMuFewThreads * kVec, kTurns = R * M::kStrip / kTurn;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * M::kBytes + M::kSums];
     const int k = mu_find(l, blockIdx.x);
     const int b = static_cast<int>(mu_item(l, k, blockIdx.x));
     const MuFewTensor& s = l.d[k];
@@ -324,10 +364,11 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_few(MuListOf<MuFewTenso
     const int size = t.rows * t.cols;
     const int nb = uniform((max(t.rows, t.cols) + 31) / 32);
     const uint32_t x0 = uniform(static_cast<int>(lds_addr(lds)));
-    M m(x0, x0 + M::kBytes);
+    M m(x0, x0 + 2 * M::kBytes);
 
     // the directions and their squares' sum
     mu_few_clear(x0, nb * R * 64);
+    mu_few_clear(x0 + M::kBytes, nb * R * 64);
     const int turns = uniform((size + kTurn - 1) / kTurn);
     float u[kTurns][kVec];
     double sum = 0.0;
@@ -345,50 +386,33 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_few(MuListOf<MuFewTenso
     }
     const double f = mu_factor_of(mu_few_sum(sum, m.sums), a.step.eps, s.lift);
 
-    // X0 in two parts: the low ones through LDS to the lanes that keep them, then the high ones
-    auto scatter = [&](bool low) {
+    // X0 in two parts
 #pragma unroll 1
-        for (int p = 0; p < turns; ++p) {
-            const int i = p * kTurn + threadIdx.x * kVec;
-            float z[kVec];
-            mu_case<kTurns>(p, [&](auto q) {
+    for (int p = 0; p < turns; ++p) {
+        const int i = p * kTurn + threadIdx.x * kVec;
+        float z[kVec];
+        mu_case<kTurns>(p, [&](auto q) {
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) z[e] = u[q][e];
-            });
-            uint32_t w[kVec];
+            for (int e = 0; e < kVec; ++e) z[e] = u[q][e];
+        });
+        uint32_t hi[kVec], lo[kVec];
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                uint32_t hi, lo;
-                mu_split(static_cast<float>(z[e] * f), hi, lo);
-                w[e] = low ? lo : hi;
-            }
-            if (i >= size) continue;
-            int row = static_cast<uint32_t>(i) / static_cast<uint32_t>(t.cols), col = i - row * t.cols;
-            if (!t.tall && col % kVec == 0 && col + kVec <= t.cols) {
-                *(L4*)static_cast<uintptr_t>(x0 + (col >> 5) * (R * 64) + mu_few_at(row, (col & 31) >> 2)) =
-                    u32x4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
-                continue;
-            }
+        for (int e = 0; e < kVec; ++e) mu_split(static_cast<float>(z[e] * f), hi[e], lo[e]);
+        if (i >= size) continue;
+        int row = static_cast<uint32_t>(i) / static_cast<uint32_t>(t.cols), col = i - row * t.cols;
+        if (!t.tall && col % kVec == 0 && col + kVec <= t.cols) {
+            mu_few_put<R>(x0, row, col, hi, lo);
+            continue;
+        }
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                const int r = t.tall ? col : row, c = t.tall ? row : col;
-                if (i + e < size)
-                    *(H1*)static_cast<uintptr_t>(x0 + (c >> 5) * (R * 64) + mu_few_at(r, (c & 31) >> 2) + (c & 3) * 2) = static_cast<uint16_t>(w[e]);
-                if (++col == t.cols) {
-                    col = 0;
-                    ++row;
-                }
+        for (int e = 0; e < kVec; ++e) {
+            if (i + e < size) mu_few_put1<R>(x0, t.tall ? col : row, t.tall ? row : col, hi[e], lo[e]);
+            if (++col == t.cols) {
+                col = 0;
+                ++row;
             }
         }
-    };
-    scatter(true);
-    __syncthreads();
-    typename M::Block low[2];
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-        if (m.block(n) < nb) M::each([&](int sb, int it, int v) { low[n][sb][it][v] = *(const L2*)static_cast<uintptr_t>(m.place(m.block(n), sb, it, v)); });
-    __syncthreads();
-    scatter(false);
+    }
     __syncthreads();
 
     const float lift = ldexpf(1.0f, s.lift), un = 1.0f / (lift * lift), out = 1.0f / lift * kMuUnlift;
@@ -400,24 +424,20 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_few(MuListOf<MuFewTenso
         for (int c = threadIdx.x; c < M::kPart / 16; c += kMuFewThreads) *(F4*)static_cast<uintptr_t>(m.sums + c * 16) = m.joined(c);
         __syncthreads();
         m.poly(a.poly[step], un);
-        if (step + 1 < a.steps) {
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int blk = m.block(n);
-                if (blk < nb) m.apply(blk, low[n], [&](int sb, int it, int v, const f32x4& y) { m.split(blk, sb, it, v, y, low[n][sb][it][v]); });
-            }
-        } else {
+        if (step + 1 == a.steps) {
 #pragma unroll 1
-            for (int n = 0; n < 2; ++n) {
-                const int blk = m.block(n);
-                if (blk >= nb) continue;
-                typename M::Block lo;
-                mu_case<2>(n, [&](auto z) { M::each([&](int sb, int it, int v) { lo[sb][it][v] = low[z][sb][it][v]; }); });
-                m.apply(blk, lo, [&](int sb, int it, int v, const f32x4& y) {
+            for (int blk = m.wave; blk < nb; blk += kMuFewWaves)
+                m.apply(blk, [&](int sb, int it, int v, const f32x4& y) {
                     mu_few_store(t, a.update, a.decay, first, it * M::T + m.col, 32 * blk + m.column(sb, v), y * out);
                 });
-            }
+            return;
         }
+#pragma unroll 1
+        for (int blk = m.wave; blk < nb; blk += kMuFewWaves)
+            m.apply(blk, [&](int sb, int it, int v, const f32x4& y) {
+                u32x2 lo;
+                m.split(blk, sb, it, v, y, lo);
+            });
         mu_order();
         __syncthreads();  // A's sums have been read; R = 64: X' is read by two waves
     }
@@ -427,23 +447,20 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_few(MuListOf<MuFewTenso
 template <int R, int N>
 __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_start(MuListOf<MuTensor, N> l, MuStepArgs a) {
     using M = MuFew<R>;
-    constexpr int kLow = M::kBytes > M::kSums ? M::kBytes : M::kSums;  // the low parts, then A's sums
-    __shared__ __attribute__((aligned(16))) uint8_t lds[M::kBytes + kLow];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * M::kBytes + M::kSums];
     const int k = mu_find(l, blockIdx.x);
     const MuTensor& t = l.d[k];
     const uint32_t item = mu_item(l, k, blockIdx.x);
-    const int strips = t.np / kMuStrip, b = uniform(static_cast<int>(item / strips)), strip = uniform(static_cast<int>(item % strips));
-    const uint32_t x0 = uniform(static_cast<int>(lds_addr(lds))), y0 = x0 + M::kBytes;
-    M m(x0, y0);
+    const int strips = t.np / M::kStrip, b = uniform(static_cast<int>(item / strips)), strip = uniform(static_cast<int>(item % strips));
+    const uint32_t x0 = uniform(static_cast<int>(lds_addr(lds)));
+    M m(x0, x0 + 2 * M::kBytes);
+    mu_few_clear(x0, 2 * M::kBytes);
     double sum = 0.0;
     const double* p = t.norm + static_cast<int64_t>(b) * t.parts;
     for (int i = threadIdx.x; i < t.parts; i += kMuFewThreads) sum += *gld<double>(p + i);
-    const double f = mu_factor_of(mu_few_sum(sum, y0), a.eps, t.lift);
-    __syncthreads();
-    mu_few_clear(x0, 2 * M::kBytes);
-    __syncthreads();
-    const int c0 = strip * kMuStrip, per = t.tall ? (t.cols + kVec - 1) / kVec : kMuStrip / kVec;  // 8 values each of a row
-    const int rows = t.tall ? min(kMuStrip, t.rows - c0) : t.rows;
+    const double f = mu_factor_of(mu_few_sum(sum, m.sums), a.eps, t.lift);
+    const int c0 = strip * M::kStrip, per = t.tall ? (t.cols + kVec - 1) / kVec : M::kStrip / kVec;  // 8 values each of a row
+    const int rows = t.tall ? min(M::kStrip, t.rows - c0) : t.rows;
 #pragma unroll 2
     for (int e0 = threadIdx.x; e0 < rows * per; e0 += kMuFewThreads) {
         const int r = e0 / per, c = e0 % per * kVec;
@@ -464,24 +481,18 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_start(MuListOf<Mu
 #pragma unroll
         for (int e = 0; e < kVec; ++e) mu_split(e < valid ? static_cast<float>(u[e] * f) : 0.0f, hi[e], lo[e]);
         if (!t.tall) {
-            const uint32_t at = (c >> 5) * (R * 64) + mu_few_at(r, (c & 31) >> 2);
-            *(L4*)static_cast<uintptr_t>(x0 + at) = u32x4{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16};
-            *(L4*)static_cast<uintptr_t>(y0 + at) = u32x4{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16};
+            mu_few_put<R>(x0, r, c, hi, lo);
         } else {
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                if (e >= valid) break;
-                const uint32_t at = (r >> 5) * (R * 64) + mu_few_at(c + e, (r & 31) >> 2) + (r & 3) * 2;
-                *(H1*)static_cast<uintptr_t>(x0 + at) = static_cast<uint16_t>(hi[e]);
-                *(H1*)static_cast<uintptr_t>(y0 + at) = static_cast<uint16_t>(lo[e]);
-            }
+            for (int e = 0; e < kVec; ++e)
+                if (e < valid) mu_few_put1<R>(x0, c + e, r, hi[e], lo[e]);
         }
     }
     __syncthreads();
-    const MuStripPlace at(t.mp, t.np);
+    const MuStripPlace at(t.mp, t.np, strips);
     uint8_t* const ws = t.ws + b * t.stride;
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int n = 0; n < M::NB; ++n) {
         const int blk = m.block(n);
         uint8_t* const w = ws + strip * M::kBytes + blk * (R * 64) + m.lane * 8;
         M::each([&](int sb, int it, int v) {
@@ -491,8 +502,7 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_start(MuListOf<Mu
             *gst<u32x2>(w + at.lo + o) = *(const L2*)static_cast<uintptr_t>(z + M::kBytes);
         });
     }
-    __syncthreads();
-    m.gram(kMuStrip / 32);
+    m.gram(M::kStrip / 32);
     __syncthreads();
     float* const o = reinterpret_cast<float*>(ws + at.part) + static_cast<int64_t>(strip) * R * R;
     for (int c = threadIdx.x; c < M::kPart / 16; c += kMuFewThreads) *gst<f32x4>(o + c * 4) = m.joined(c);
@@ -504,19 +514,19 @@ template <int R, int N>
 __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_step(MuListOf<MuTensor, N> l, MuPoly poly, int src, int last, int update,
                                                                     float decay) {
     using M = MuFew<R>;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[M::kBytes + M::kSums];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * M::kBytes + M::kSums];
     const int k = mu_find(l, blockIdx.x);
     const MuTensor& t = l.d[k];
     const uint32_t item = mu_item(l, k, blockIdx.x);
-    const int strips = t.np / kMuStrip, b = uniform(static_cast<int>(item / strips)), strip = uniform(static_cast<int>(item % strips));
+    const int strips = t.np / M::kStrip, b = uniform(static_cast<int>(item / strips)), strip = uniform(static_cast<int>(item % strips));
     const uint32_t x0 = uniform(static_cast<int>(lds_addr(lds)));
-    M m(x0, x0 + M::kBytes);
-    const MuStripPlace at(t.mp, t.np);
+    M m(x0, x0 + 2 * M::kBytes);
+    const MuStripPlace at(t.mp, t.np, strips);
     uint8_t* const ws = t.ws + b * t.stride;
     uint8_t* const w = ws + strip * M::kBytes + m.lane * 8;
-    typename M::Block high[2], low[2];
+    typename M::Block high[M::NB], low[M::NB];
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < M::NB; ++n)
         M::each([&](int sb, int it, int v) {
             const int64_t o = m.block(n) * (R * 64) + ((sb * M::NT + it) * M::V + v) * 512;
             high[n][sb][it][v] = *gld<u32x2>(w + o);
@@ -534,8 +544,12 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_step(MuListOf<MuT
         *(F4*)static_cast<uintptr_t>(m.sums + group * M::kPart + c * 16) = s;
     }
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
-        M::each([&](int sb, int it, int v) { *(L2*)static_cast<uintptr_t>(m.place(m.block(n), sb, it, v)) = high[n][sb][it][v]; });
+    for (int n = 0; n < M::NB; ++n)
+        M::each([&](int sb, int it, int v) {
+            const uint32_t z = m.place(m.block(n), sb, it, v);
+            *(L2*)static_cast<uintptr_t>(z) = high[n][sb][it][v];
+            *(L2*)static_cast<uintptr_t>(z + M::kBytes) = low[n][sb][it][v];
+        });
     __syncthreads();
     if (kGroups > 1) {
         if (threadIdx.x < kChunks) {
@@ -551,16 +565,16 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_step(MuListOf<MuT
     if (last) {
         const int64_t first = static_cast<int64_t>(b) * t.rows * t.ldx;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-            m.apply(m.block(n), low[n], [&](int sb, int it, int v, const f32x4& y) {
-                mu_few_store(t, update, decay, first, it * M::T + m.col, strip * kMuStrip + 32 * m.block(n) + m.column(sb, v),
+        for (int n = 0; n < M::NB; ++n)
+            m.apply(m.block(n), [&](int sb, int it, int v, const f32x4& y) {
+                mu_few_store(t, update, decay, first, it * M::T + m.col, strip * M::kStrip + 32 * m.block(n) + m.column(sb, v),
                              y * (1.0f / lift * kMuUnlift));
             });
         return;
     }
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
-        m.apply(m.block(n), low[n], [&](int sb, int it, int v, const f32x4& y) {
+    for (int n = 0; n < M::NB; ++n)
+        m.apply(m.block(n), [&](int sb, int it, int v, const f32x4& y) {
             const int64_t o = m.block(n) * (R * 64) + ((sb * M::NT + it) * M::V + v) * 512;
             u32x2 lo;
             *gst<u32x2>(w + o) = m.split(m.block(n), sb, it, v, y, lo);
@@ -568,7 +582,7 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_step(MuListOf<MuT
         });
     mu_order();
     __syncthreads();  // A's sums have been read; R = 64: X' is read by two waves
-    m.gram(kMuStrip / 32);
+    m.gram(M::kStrip / 32);
     __syncthreads();
     float* const o = reinterpret_cast<float*>(ws + at.part) + static_cast<int64_t>((src ^ 1) * strips + strip) * R * R;
     for (int c = threadIdx.x; c < M::kPart / 16; c += kMuFewThreads) *gst<f32x4>(o + c * 4) = m.joined(c);
