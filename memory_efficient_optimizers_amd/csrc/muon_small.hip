@@ -26,6 +26,7 @@ typedef _Float16 half4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) u32x2 L2;
 typedef __attribute__((address_space(3))) u32x4 L4;
 typedef __attribute__((address_space(3))) f32x4 F4;
+typedef __attribute__((address_space(3))) float F1;
 typedef __attribute__((address_space(3))) double D1;
 typedef __attribute__((address_space(3))) uint16_t H1;
 
@@ -65,6 +66,7 @@ struct MuFew {
     // A's parts: by wave; R = 64: by pairs of waves, which have a column of tiles each.
     static constexpr int kParts = R == 64 ? kMuFewWaves / 2 : kMuFewWaves;
     static constexpr int kPart = R * R * 4, kSums = kParts * kPart;
+    static constexpr int kLds = 2 * kBytes + kSums + 2 * R * 4;
     struct Acc { f32x4 v[V]; };
     struct Op { u32x2 v[V]; };  // T values of the contraction
     struct Ops { Op hi, lo; };
@@ -171,64 +173,91 @@ struct MuFew {
         return w;
     }
 
-    // From X X^T (times 4^lift, at `sums`): the wave's B, 2^8 times off the diagonal, as operands, and
-    // of its lanes' columns q = a + B_ii, 2^8 times.
+    // A chunk of X X^T (times 4^lift) becomes O's, 2^8 times, its two parts in the chunk's place;
+    // the diagonal goes to diag().
+    __device__ uint32_t diag() const { return sums + kSums; }
+    __device__ uint32_t rows() const { return sums + kSums + R * 4; }  // q
+    __device__ __forceinline__ void put_o(int chunk, f32x4 w, float un) const {
+        const int z = chunk & 63, v = chunk / 64 % V, i = chunk / 64 / V % NT, j = chunk / 64 / V / NT;
+        const int c = z & (T - 1), r = 8 * v + 4 * (z / T);
+        w *= un;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (i == j && r + e == c) {
+                *(F1*)static_cast<uintptr_t>(diag() + (j * T + c) * 4) = w[e];
+                w[e] = 0.0f;
+            }
+        u32x2 lo;
+        const u32x2 hi = parts(w * kMuLift, lo);
+        *(L4*)static_cast<uintptr_t>(sums + chunk * 16) = u32x4{hi.x, hi.y, lo.x, lo.y};
+    }
+    __device__ __forceinline__ Ops operand(uint32_t at, int j, int i) const {  // a tile of chunks
+        Ops o;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const u32x4 w = mu_lds(at + (((j * NT + i) * V + v) * 64 + lane) * 16);
+            o.hi.v[v] = u32x2{w.x, w.y};
+            o.lo.v[v] = u32x2{w.z, w.w};
+        }
+        return o;
+    }
+
+    // From O (put_o, then a barrier): B, 2^8 times off the diagonal, as operands, and of the lane's columns
+    // q = a + B_ii, 2^8 times. With 16 rows each wave forms B, with more a part of it each
+    // (64 rows in every wave: 8 us of a step's arithmetic).
     Ops B[NT][NT];  // [column][row]
     float q[NT];
-    __device__ __forceinline__ void poly(const MuPoly& p, float un) {
-        const int holder = col + T * ((col >> 2) & (64 / T - 1));  // the lane with the diagonal of column `col`
-        Ops O[NT][NT];
-        float d[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            float own = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    f32x4 w = *(const F4*)static_cast<uintptr_t>(sums + (((j * NT + i) * V + v) * 64 + lane) * 16) * un;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (i == j && 8 * v + 4 * h + e == col) {
-                            own = w[e];
-                            w[e] = 0.0f;
-                        }
-                    O[j][i].hi.v[v] = parts(w * kMuLift, O[j][i].lo.v[v]);
-                }
-            d[j] = __shfl(own, holder, 64);
-        }
+    __device__ __forceinline__ void poly(const MuPoly& p) {
+        constexpr int kUnits = NT * NT * V, kPer = kUnits > kMuFewWaves ? kUnits / kMuFewWaves : 1;  // four values each
         const float cs = p.c * kMuUnlift;
+        if (R == 16 || wave < kUnits) {
+            const int tile = R == 16 ? 0 : wave * kPer / V, j = tile / NT, i = tile % NT;
+            Ops a[NT], b[NT];
+            Acc sq;
+            zero(sq);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            f32x4 di[V];
+            for (int z = 0; z < NT; ++z) {
+                a[z] = operand(sums, i, z);
+                b[z] = NT == 1 ? a[z] : operand(sums, j, z);
+                mul(sq, a[z], b[z]);
+            }
+            const float dj = *(const F1*)static_cast<uintptr_t>(diag() + (j * T + col) * 4);
 #pragma unroll
-            for (int v = 0; v < V; ++v)
+            for (int v = 0; v < V; ++v) {
+                if (R != 16 && v / kPer != wave % (V / kPer)) continue;
+                const f32x4 di = *(const F4*)static_cast<uintptr_t>(diag() + (i * T + 8 * v + 4 * h) * 4);
+                const u32x4 o = mu_lds(sums + (((j * NT + i) * V + v) * 64 + lane) * 16);
+                f32x4 y;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) di[v][e] = __shfl(d[i], 8 * v + 4 * h + e, 64);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                Acc sq;
-                zero(sq);
-#pragma unroll
-                for (int z = 0; z < NT; ++z) mul(sq, O[i][z], O[j][z]);
-                float own = 0.0f;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    f32x4 y;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float o = mu_half(O[j][i].hi.v[v], e) + mu_half(O[j][i].lo.v[v], e);
-                        y[e] = fmaf(o, fmaf(p.c, di[v][e] + d[j], p.b), sq.v[v][e] * cs);
-                        if (i == j && 8 * v + 4 * h + e == col) {
-                            own = p.a + fmaf(p.b, d[j], p.c * fmaf(d[j], d[j], sq.v[v][e] * (kMuUnlift * kMuUnlift)));
-                            y[e] = 0.0f;
-                        }
+                for (int e = 0; e < 4; ++e) {
+                    y[e] = fmaf(mu_half(u32x2{o.x, o.y}, e) + mu_half(u32x2{o.z, o.w}, e), fmaf(p.c, di[e] + dj, p.b), sq.v[v][e] * cs);
+                    if (i == j && 8 * v + 4 * h + e == col) {
+                        *(F1*)static_cast<uintptr_t>(rows() + (j * T + col) * 4) =
+                            (p.a + fmaf(p.b, dj, p.c * fmaf(dj, dj, sq.v[v][e] * (kMuUnlift * kMuUnlift)))) * kMuLift;
+                        y[e] = 0.0f;
                     }
-                    B[j][i].hi.v[v] = parts(y, B[j][i].lo.v[v]);
                 }
-                if (i == j) q[j] = __shfl(own, holder, 64) * kMuLift;
+                u32x2 lo;
+                const u32x2 hi = parts(y, lo);
+                if constexpr (R == 16) {
+                    B[0][0].hi.v[0] = hi;
+                    B[0][0].lo.v[0] = lo;
+                } else {
+                    *(L4*)static_cast<uintptr_t>(sums + kPart + (((j * NT + i) * V + v) * 64 + lane) * 16) = u32x4{hi.x, hi.y, lo.x, lo.y};
+                }
             }
         }
+        if (R == 16) {
+            mu_order();  // (waves write the same q)
+        } else {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < NT; ++i) B[j][i] = operand(sums + kPart, j, i);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) q[j] = *(const F1*)static_cast<uintptr_t>(rows() + (j * T + col) * 4);
     }
 
     // X' of a block of LDS: f(sb, it, v, four values, 2^8 times).
@@ -350,7 +379,7 @@ template <int R, int N>
 __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_few(MuListOf<MuFewTensor, N> l, MuFewArgs a) {
     using M = MuFew<R>;
     constexpr int kTurn = kMuFewThreads * kVec, kTurns = R * M::kStrip / kTurn;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * M::kBytes + M::kSums];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[M::kLds];
     const int k = mu_find(l, blockIdx.x);
     const int b = static_cast<int>(mu_item(l, k, blockIdx.x));
     const MuFewTensor& s = l.d[k];
@@ -421,9 +450,9 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_few(MuListOf<MuFewTenso
     for (int step = 0; step < a.steps; ++step) {
         m.gram(nb);
         __syncthreads();
-        for (int c = threadIdx.x; c < M::kPart / 16; c += kMuFewThreads) *(F4*)static_cast<uintptr_t>(m.sums + c * 16) = m.joined(c);
+        for (int c = threadIdx.x; c < M::kPart / 16; c += kMuFewThreads) m.put_o(c, m.joined(c), un);
         __syncthreads();
-        m.poly(a.poly[step], un);
+        m.poly(a.poly[step]);
         if (step + 1 == a.steps) {
 #pragma unroll 1
             for (int blk = m.wave; blk < nb; blk += kMuFewWaves)
@@ -447,7 +476,7 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_few(MuListOf<MuFewTenso
 template <int R, int N>
 __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_start(MuListOf<MuTensor, N> l, MuStepArgs a) {
     using M = MuFew<R>;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * M::kBytes + M::kSums];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[M::kLds];
     const int k = mu_find(l, blockIdx.x);
     const MuTensor& t = l.d[k];
     const uint32_t item = mu_item(l, k, blockIdx.x);
@@ -514,7 +543,7 @@ template <int R, int N>
 __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_step(MuListOf<MuTensor, N> l, MuPoly poly, int src, int last, int update,
                                                                     float decay) {
     using M = MuFew<R>;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * M::kBytes + M::kSums];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[M::kLds];
     const int k = mu_find(l, blockIdx.x);
     const MuTensor& t = l.d[k];
     const uint32_t item = mu_item(l, k, blockIdx.x);
@@ -532,6 +561,7 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_step(MuListOf<MuT
             high[n][sb][it][v] = *gld<u32x2>(w + o);
             low[n][sb][it][v] = *gld<u32x2>(w + at.lo + o);
         });
+    const float lift = ldexpf(1.0f, t.lift), un = 1.0f / (lift * lift);
     // the parts' sums, in order of groups of parts
     constexpr int kChunks = M::kPart / 16, kGroups = kChunks < kMuFewThreads ? kMuFewThreads / kChunks : 1;
     const float* const parts = reinterpret_cast<const float*>(ws + at.part) + static_cast<int64_t>(src) * strips * R * R;
@@ -541,7 +571,8 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_step(MuListOf<MuT
         f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
         for (int e = group; e < strips; e += kGroups) s += *gld<f32x4>(parts + static_cast<int64_t>(e) * R * R + c * 4);
-        *(F4*)static_cast<uintptr_t>(m.sums + group * M::kPart + c * 16) = s;
+        if (kGroups > 1) *(F4*)static_cast<uintptr_t>(m.sums + group * M::kPart + c * 16) = s;
+        else m.put_o(c, s, un);
     }
 #pragma unroll
     for (int n = 0; n < M::NB; ++n)
@@ -556,12 +587,11 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_step(MuListOf<MuT
             f32x4 s = *(const F4*)static_cast<uintptr_t>(m.sums + threadIdx.x * 16);
 #pragma unroll
             for (int e = 1; e < kGroups; ++e) s += *(const F4*)static_cast<uintptr_t>(m.sums + e * M::kPart + threadIdx.x * 16);
-            *(F4*)static_cast<uintptr_t>(m.sums + threadIdx.x * 16) = s;
+            m.put_o(threadIdx.x, s, un);
         }
         __syncthreads();
     }
-    const float lift = ldexpf(1.0f, t.lift);
-    m.poly(poly, 1.0f / (lift * lift));
+    m.poly(poly);
     if (last) {
         const int64_t first = static_cast<int64_t>(b) * t.rows * t.ldx;
 #pragma unroll
