@@ -263,6 +263,29 @@ def test_few_rows(shape, kind):
     check(orthogonalize(x), x)
 
 
+def single_newton_schulz(u):
+    """In float32 throughout."""
+    x, tall = om.start(u, 1e-7)
+    x = x.astype(np.float32)
+    a, b, c = (np.float32(v) for v in om.COEFFICIENTS)
+    for _ in range(5):
+        g = x @ x.T
+        x = a * x + (b * g + c * (g @ g)) @ x
+    return (x.T if tall else x).astype(np.float64)
+
+
+@pytest.mark.parametrize("kind", ["noise", "low"])
+@pytest.mark.parametrize("shape", FEW + [(1, 1), (3, 2), (16, 16), (32, 32), (31, 33), (64, 64), (48, 200)])
+def test_few_rows_keep_22_bits(shape, kind):
+    """Two fp16 parts hold 22 bits, 2^-22 against float32's 2^-24: four times float32's errors, and once more for
+    the float32 sums in another order; twice for the chance in both realizations. The result's own rounding 2^-22."""
+    x = matrix(shape, 109, kind)
+    u = to64(x)
+    want, got = om.newton_schulz(u), to64(raw([x])[0])
+    lim = 2 * 5 * np.linalg.norm(single_newton_schulz(u) - want) + 2.0 ** -22 * np.linalg.norm(want)
+    assert np.linalg.norm(got - want) <= lim, (np.linalg.norm(got - want), lim)
+
+
 @pytest.mark.parametrize("shape", [(5, 1, 600), (3, 40, 600), (2, 700, 20), (4, 30, 30), (2, 3, 1100, 60)])
 def test_batches_of_few_rows(shape):
     x = matrix(shape, 102, dtype=torch.bfloat16)
