@@ -2858,17 +2858,20 @@ int64_t mu_chunks(const std::vector<MuIn>& ts, std::vector<MuChunk>* out) {
 
 // The tile form of a pass: the one whose tiles, dealt to the CUs, are done first. A tile takes
 // kMuTileStart (kMuApplyStart where it also moves X) and kMuTileStep per 64 values of the
-// contraction, in microseconds, beside the others that a CU holds. Fitted to (measured, model):
+// contraction, in microseconds, beside the others that a CU holds; where large tiles move X, a round
+// that leaves CUs idle is done sooner, since memory bounds it. Fitted to (measured, model):
 // A of 4096 x 4096 in 64-, 128-, 192- and 256-tiles 108 (116), 92 (97), 74 (67), 90 (94); of four of
 // them 430, 268, 261, 283 (426, 290, 268, 282); of 1024 x 1024 8, 12, 20, 28; X' of 4096 x 4096 205,
-// 144, 148, 134 and of four 1024 x 1024 20, 18, 27, 41. No form changes a result.
+// 144, 148, 134 (205, 142, 140, 131), of 4096 x 11008 544, 372, 373, 351 (552, 387, 368, 351), of four
+// 1024 x 1024 20, 18, 27, 41. No form changes a result.
 constexpr double kMuTileStart[kMuForms] = {2, 4, 17, 20};
 constexpr double kMuApplyStart[kMuForms] = {2, 7, 24, 57};
 constexpr double kMuTileStep[kMuForms] = {0.17, 0.44, 0.78, 1.15};
 
 // tiles(tensor, side): its matrices' tiles and the steps of each.
 template <class Tiles>
-int mu_form(const std::vector<MuIn>& ts, const MuChunk& c, const double* start, Tiles tiles) {
+int mu_form(const std::vector<MuIn>& ts, const MuChunk& c, bool apply, Tiles tiles) {
+    const double* const start = apply ? kMuApplyStart : kMuTileStart;
     int best = kMuSmall;
     double cost = 0.0;
     for (int f = 0; f < kMuForms; ++f) {
@@ -2883,7 +2886,8 @@ int mu_form(const std::vector<MuIn>& ts, const MuChunk& c, const double* start, 
             if (count > 0) longest = std::max(longest, one);
         }
         if (n == 0) return kMuSmall;
-        const double w = std::max(longest, all / static_cast<double>(n) * static_cast<double>(ceil_div(n, kCus)));
+        const double rounds = apply && f >= kMuThreeQuarters ? std::max(1.0, static_cast<double>(n) / kCus) : static_cast<double>(ceil_div(n, kCus));
+        const double w = std::max(longest, all / static_cast<double>(n) * rounds);
         if (f == 0 || w < cost) {
             best = f;
             cost = w;
@@ -3073,16 +3077,16 @@ int mu_run(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, MuS
             continue;
         }
         auto square = [](int64_t side, int64_t tile) { const int64_t q = ceil_div(side, tile); return q * (q + 1) / 2; };
-        const int fg = mu_form(ts, c, kMuTileStart, [&](const MuIn& q, int64_t tile, int64_t* n, int64_t* steps) {
+        const int fg = mu_form(ts, c, false, [&](const MuIn& q, int64_t tile, int64_t* n, int64_t* steps) {
             int64_t parts;
             mu_gram_parts(q.mp(), q.np(), &parts, steps);
             *n = parts > 1 ? 0 : square(q.mp(), tile);
         });
-        const int fp = mu_form(ts, c, kMuTileStart, [&](const MuIn& q, int64_t tile, int64_t* n, int64_t* steps) {
+        const int fp = mu_form(ts, c, false, [&](const MuIn& q, int64_t tile, int64_t* n, int64_t* steps) {
             *n = square(q.mp(), tile);
             *steps = q.mp() / 64;
         });
-        const int fa = mu_form(ts, c, kMuApplyStart, [&](const MuIn& q, int64_t tile, int64_t* n, int64_t* steps) {
+        const int fa = mu_form(ts, c, true, [&](const MuIn& q, int64_t tile, int64_t* n, int64_t* steps) {
             *n = ceil_div(q.mp(), tile) * ceil_div(q.np(), tile);
             *steps = q.mp() / 64;
         });
