@@ -650,8 +650,9 @@ int32_t meo_mx4_matmul_rows(int64_t m, int64_t n);
  *
  * Precision. Products are fp16 with float32 sums; the iterate itself is held in 22 bits and the
  * diagonals of A and of b A + c A^2 in float32. The result is within about 1e-3 (relative, in
- * the Frobenius norm; 2e-3 for the smallest matrices) of the exact polynomial's, at any
- * conditioning; a bfloat16 result is rounded once, to nearest even. Values are held times powers of two; a result whose
+ * the Frobenius norm) of the exact polynomial's, at any conditioning. Matrices whose shorter
+ * side is at most 64 and whose longer side at most 32768 (8192 from 33 on) have operands of two
+ * fp16 parts, 22 bits: within about 1e-6 of the exact result. A bfloat16 result is rounded once, to nearest even. Values are held times powers of two; a result whose
  * entries are below about 2^-24 of those of a matrix with orthonormal rows (eps far above |U|)
  * loses them.
  *
@@ -684,8 +685,8 @@ typedef struct meo_ns_matrices {
 /* The result of a matrix does not depend on the rest of its list, bit for bit. The calls
  * allocate nothing and keep nothing: descriptors travel as kernel arguments, so that a call can
  * be captured into a graph. The workspace holds part of the list at a time (6 bytes per value
- * and 4 per value of A, of about 2^26 values or the largest matrix); lists are worked off in
- * that order. Errors as for the steps; MEO_ESHAPE also for a side past 2^22, a matrix past
+ * and 4 per value of A, of about 2^26 values or the largest matrix; less for the matrices with
+ * a short side above); lists are worked off in parts, those matrices first. Errors as for the steps; MEO_ESHAPE also for a side past 2^22, a matrix past
  * 2^35 values (both after rounding up to 64) or a leading dimension below the row length. */
 void   meo_orthogonalize_defaults(meo_orthogonalize_hparams* hp);
 size_t meo_orthogonalize_workspace_size(const meo_orthogonalize_hparams* hp, int32_t n, const meo_ns_matrices* matrices);

@@ -374,7 +374,8 @@ __device__ __forceinline__ void mu_few_store(const MuTensor& t, bool update, flo
     }
 }
 
-// A matrix of one strip per block, all steps.
+// A matrix of one strip per block, all steps. In a captured graph: 16 x 16 8.8 us, 32 x 64 13.8, 64 x 64
+// 24.9 (five steps; in tiles, 17 launches, 32 x 64 took 64).
 template <int R, int N>
 __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_few(MuListOf<MuFewTensor, N> l, MuFewArgs a) {
     using M = MuFew<R>;
@@ -472,7 +473,8 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_few(MuListOf<MuFewTenso
     }
 }
 
-// Strips: X0 of one, into the workspace as accumulators have it, and its part of A.
+// Strips: X0 of one, into the workspace as accumulators have it, and its part of A. Four of 16 x 4096 and
+// 4096 x 16: 7 us.
 template <int R, int N>
 __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_start(MuListOf<MuTensor, N> l, MuStepArgs a) {
     using M = MuFew<R>;
@@ -538,7 +540,8 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_start(MuListOf<Mu
 }
 
 // One step of a strip: A from all strips' parts (buffer src), X', its part of the next A; the last
-// step's X' goes to the caller's tensors.
+// step's X' goes to the caller's tensors. Every strip joins all parts, which costs less than a launch for
+// it: 16 x 4096 (8 parts of 1 KB) 4.3 us a step, 64 x 4096 (16 of 16 KB) 10.8.
 template <int R, int N>
 __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_step(MuListOf<MuTensor, N> l, MuPoly poly, int src, int last, int update,
                                                                     float decay) {

@@ -14,7 +14,7 @@ mkdir -p "$D/obj"
 FL="-x hip --offload-arch=gfx950 -O1 -g -std=c++17 -fPIC -Wno-unused-command-line-argument -Xclang -target-feature -Xclang -packed-fp32-ops -ffp-contract=off -I $R/include -I $C"
 SAN="-Xarch_host -fsanitize=address -Xarch_host -fsanitize=undefined -Xarch_host -fno-sanitize-recover=undefined -Xarch_host -fno-omit-frame-pointer"
 pids=()
-for f in abi.cpp passes.hip adafactor.hip came.hip lamb.hip shard.hip galore.hip galore_refresh.hip mx4.hip galore_mx4.hip; do
+for f in abi.cpp passes.hip adafactor.hip came.hip lamb.hip shard.hip galore.hip galore_refresh.hip mx4.hip galore_mx4.hip muon.hip muon_small.hip; do
   "$HIPCC" $FL $SAN -c "$C/$f" -o "$D/obj/${f%.*}.o" 2> "$D/obj/${f%.*}.log" & pids+=($!)
 done
 for p in "${pids[@]}"; do wait "$p"; done
