@@ -352,6 +352,33 @@ def test_long_lists_of_few_rows():
     assert all(torch.equal(y, orthogonalize(x)) for x, y in zip(xs, ys))
 
 
+def test_more_matrices_than_a_launch_or_a_part_takes():
+    """Past 2^22 matrices of one strip, past 2^26 values in strips: as they come out alone."""
+    x = matrix((2 ** 22 + 9, 1, 1), 111)
+    y, one = orthogonalize([x, matrix((2, 3), 112)])[0], orthogonalize(torch.ones(1, 1, device=DEV))
+    want = one * x.sign().bfloat16()
+    for k in (x.abs().flatten() < 1e-7).nonzero().flatten().tolist():  # (X_0 = x / eps there, not its sign)
+        want[k] = orthogonalize(x[k])
+    assert torch.equal(y, want)
+    x = matrix((4200, 16, 1000), 113, dtype=torch.bfloat16)
+    y = orthogonalize(x)
+    for k in (0, 1, 2099, 4095, 4096, 4199):
+        assert torch.equal(y[k], orthogonalize(x[k]))
+
+
+def test_offsets_past_32_bits():
+    """Matrices behind 2^31 values of their tensor."""
+    for shape in ((2 ** 22 + 3, 20, 30), (33000, 60, 1100), (33000, 200, 400)):
+        x = torch.zeros(shape, dtype=torch.bfloat16, device=DEV)
+        last = matrix(shape[1:], 114, dtype=torch.bfloat16)
+        x[-1] = last
+        x[-3] = last
+        y = orthogonalize(x)
+        want = orthogonalize(last)
+        assert torch.equal(y[-1], want) and torch.equal(y[-3], want) and not y[-2].any() and not y[0].any()
+        del x, y
+
+
 def test_steps_and_coefficients_of_few_rows():
     for shape in ((40, 100), (20, 1700)):
         x = matrix(shape, 107)
