@@ -3,19 +3,19 @@
 //
 // The mathematics is muon.hip's, but X, A and B are held as two fp16 parts in every product (hi hi +
 // hi lo + lo hi: 22 bits): products are what such matrices have little of, and small ones would lose
-// more to fp16 than large ones do (16 x 16: 1.3e-3 of the result with one part, 3e-7 so).
+// more to fp16 than large ones do (16 x 16: 1.3e-3 of the result with one part, 5e-7 so).
 //
-// The longer side goes by blocks of 32 columns, a strip of them to a thread block, of which a wave has
-// two (one of 64 rows): the step X' = a X + B X needs nothing else of X. A = X X^T is summed over the
-// waves through LDS, over strips through the workspace. Every wave then forms B for itself: in an
-// accumulator of a symmetric matrix a lane holds four consecutive rows of a column, which are four
-// consecutive values of the contraction of that column as an operand, so A, A^2 and B go from
-// product to product in registers. A matrix of one strip is one launch, with the iterate in LDS; one of
-// more strips is a launch per step and two before them.
+// The longer side goes by blocks of 32 columns, a strip of 16 (64 rows: 8) to a thread block, each
+// wave's its own: the step X' = a X + B X needs nothing else of X. A = X X^T is summed over the waves
+// through LDS, over strips through the workspace. In an accumulator of a symmetric matrix a lane holds
+// four consecutive rows of a column, which are four consecutive values of the contraction of that column
+// as an operand: A, A^2 and B go from product to product as they are, in registers (16 rows) or through
+// LDS by 16 bytes. A matrix of one strip is one launch, with the iterate in LDS; one of more strips is a
+// launch per step and two before them.
 //
 // What bounds it: latencies (launches, barriers, LDS, dependent products). The work per value is some
 // 8 vector instructions a step, too many for one CU from 16 x 1024 on: 16 x 4096 in one block took
-// 59 us, 4096 x 16 87.
+// 59 us (in 8 strips 29), 4096 x 16 87 (31).
 #include "muon_device.h"
 
 namespace meo {
