@@ -2,8 +2,8 @@
 //
 // With X0 = U / max(|U|, eps) (Frobenius norm; the shorter side as rows, m <= n), each step is
 //     A = X X^T,   X <- a X + (b A + c A^2) X.
-// The products run on fp16 matrix cores with fp32 sums. What is rounded to fp16 (relative 2^-12,
-// bf16 would be 2^-9 at the same rate) and why that is enough:
+// The products run on fp16 matrix cores with fp32 sums. What is rounded to fp16 (relative 2^-11,
+// bf16 would be 2^-8 at the same rate) and why that is enough:
 //   * X as an operand. The linear term, which alone carries the small singular values, takes X
 //     as the sum of two fp16 parts (hi + lo, 22 bits): with hi alone a matrix of rank 8 plus 1%
 //     noise came out 3.7e-2 off, so 4e-4. B takes hi only; the diagonal of B takes lo as well
@@ -17,6 +17,7 @@
 //     well-conditioned matrices (1.2e-3 to 6e-4).
 // Values are held times powers of two, so that entries of ordinary size are normal fp16
 // numbers: X times 2^lift, about the square root of its longer side, O and B times 2^8.
+// Matrices with few rows are worked on in muon_small.hip.
 #include "muon_device.h"
 
 namespace meo {
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(kMuThreads) void k_mu_scatter(MuListOf<MuTensor, N>
 
 // A T x T tile of a product of NW waves, WM along P's rows and NW / WM along Q's: 32 MB x 32 NB
 // values each. LDS: a ring of kDepth stages of 32 values of the contraction of both operands.
-// What bounds the products is the way from L2 to LDS: with two stages of 64 values (64 KB in
+// What bounds the products is the way from L2 to LDS (256 x 256): with two stages of 64 values (64 KB in
 // flight per CU) a step took 1.16 us without any multiplication, and 0.85 us is what its
 // multiplications take; with five of 32 there are 128 KB in flight.
 template <int T, int WM, int NW>
