@@ -652,9 +652,8 @@ int32_t meo_mx4_matmul_rows(int64_t m, int64_t n);
  * diagonals of A and of b A + c A^2 in float32. The result is within about 1e-3 (relative, in
  * the Frobenius norm) of the exact polynomial's, at any conditioning. Matrices whose shorter
  * side is at most 64 and whose longer side at most 32768 (8192 from 33 on) have operands of two
- * fp16 parts, 22 bits: within about 1e-6 of the exact result. A bfloat16 result is rounded once, to nearest even. Values are held times powers of two; a result whose
- * entries are below about 2^-24 of those of a matrix with orthonormal rows (eps far above |U|)
- * loses them.
+ * fp16 parts, 22 bits: within about 1e-6 of the exact result. A bfloat16 result is rounded once, to nearest even. The iterate
+ * is held to 2^-37, half a step: entries below 2^-14 have fewer bits than 22 in it, in proportion.
  *
  * Hyperparameters: eps, the steps (1 to MEO_NS_MAX_STEPS) and the coefficients of each. Defaults
  * (meo_orthogonalize_defaults): eps 1e-7, 5 steps of (3.4445, -4.7750, 2.0315), the values Muon

@@ -2773,9 +2773,6 @@ struct MuIn {
     }
     int64_t strips() const { return few() ? np() / mu_strip(few()) : 0; }
     bool whole() const { return strips() == 1; }  // all steps in one launch
-    // The power of two that values are held times: about the square root of the longer side, so that
-    // entries of a matrix with orthonormal rows are about 1.
-    int lift() const { return std::min(12, static_cast<int>(std::lround(0.5 * std::log2(static_cast<double>(std::max(rows, cols)))))); }
     const void* g_at(int64_t b) const { return static_cast<const uint8_t*>(g) + b * rows * ldg * (gbf16 ? 2 : 4); }
     void* x_at(int64_t b) const { return static_cast<uint8_t*>(x) + b * rows * ldx * (xbf16 ? 2 : 4); }
     void* m_at(int64_t b) const { return m ? static_cast<uint8_t*>(m) + b * rows * cols * (mkind == 2 ? 1 : mkind == 1 ? 2 : 4) : nullptr; }
@@ -2920,7 +2917,7 @@ int check_ns_hp(const meo_orthogonalize_hparams* hp) {
         }
         for (double v : x)
             if (v > 0.0 && v < s2) next = std::max(next, std::abs(std::sqrt(v) * (a + b * v + c * v * v)));
-        if (!(next <= 8.0) || !(poly <= 100.0))
+        if (!(next <= kMuMaxSingular) || !(poly <= 100.0))
             return fail(MEO_EINVAL, "coefficients of step " + std::to_string(k) + " let singular values grow too large");
         top = next;
     }
@@ -2991,7 +2988,6 @@ void mu_run_few(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts
                 d.gbf16 = t.gbf16;
                 d.xbf16 = t.xbf16;
                 d.mkind = t.mkind;
-                d.lift = static_cast<int16_t>(t.lift());
                 l.blocks += static_cast<uint32_t>(count);
                 b += count;
             }
@@ -3039,8 +3035,6 @@ int mu_run(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, MuS
             d.np = m.np = static_cast<int32_t>(in.np());
             d.parts = static_cast<int32_t>(mu_norm_parts(in));
             d.tiles_per_part = static_cast<int32_t>(mu_norm_span(in));
-            d.lift = in.lift();
-            m.lift = static_cast<float>(std::ldexp(1.0, d.lift));
             d.coef = in.coef;
             d.gbf16 = in.gbf16;
             d.xbf16 = in.xbf16;

@@ -12,6 +12,15 @@ constexpr int kMuTile = 64;        // scatter pass: square tiles of the matrix i
 constexpr int64_t kMuPart = 2048;  // values per part of the momentum pass, up to kMuMaxParts of them
 constexpr int64_t kMuMaxParts = 1024;
 constexpr int64_t kMuMaxSide = 1 << 22;  // longer side of a matrix (32-bit offsets in a tile)
+// The workspace holds X times 2^12. Its entries are at most 8, as its singular values are (check_ns_hp in
+// abi.cpp refuses coefficients otherwise), so 2^15 there, below fp16's 65504. Two fp16 parts, whose
+// smallest step is 2^-24, then hold X to 2^-37: 22 bits of an entry above 2^-14. (With a smaller power,
+// entries from 1/8 of an orthonormal matrix' down lost bits, and every step multiplies what is lost by the
+// linear coefficient: 64 x 64 with one strong entry over 1e-6 of noise, times 2^3, was 9.8e-5 off, 2.4e-3 after
+// ten steps.)
+constexpr float kMuXLift = 4096.0f, kMuXUnlift = 1.0f / 4096, kMuGramUnlift = kMuXUnlift * kMuXUnlift;
+constexpr double kMuMaxSingular = 8.0;
+static_assert(kMuXLift * kMuMaxSingular <= 32768.0, "half of fp16's range, for roundings");
 
 // What the passes over the caller's tensors need of one of them ([batch] matrices).
 struct MuTensor {
@@ -26,7 +35,6 @@ struct MuTensor {
     int32_t rows, cols, batch;
     int32_t mp, np;   // padded shorter and longer side
     int32_t parts, tiles_per_part;  // of the momentum pass: kMuPart values per tile
-    int32_t lift;     // the workspace holds values times 2^lift
     float coef;       // Muon: lr times the scale of the matrix' shape
     int16_t gbf16, xbf16, mkind;  // mkind: Storage of m (0 fp32, 1 bf16, 2 int8)
     int16_t tall;     // rows > cols: the workspace holds the transpose
@@ -38,7 +46,6 @@ struct MuMatrix {
     int64_t stride;
     int32_t mp, np, batch;
     int32_t parts, steps;  // A = X X^T: parts of the contraction, steps of 64 in each
-    float lift;            // 2^lift
 };
 
 // The blocks of a launch, by tensor: those before tensor i > 0 in first[i] (past the last one
@@ -133,7 +140,7 @@ struct MuFewTensor {  // fields as MuTensor's
     void* x;
     int32_t ldg, ldx, rows, cols, batch;
     float coef;
-    int16_t gbf16, xbf16, mkind, lift;
+    int16_t gbf16, xbf16, mkind;
 };
 using MuFewTensors = MuListOf<MuFewTensor, kMuFewBatch>;
 

@@ -15,8 +15,8 @@
 //     A, are held in fp32 (d, and q = a + B_ii) and enter by row: (A^2)_ij = (O^2)_ij +
 //     O_ij (d_i + d_j) off the diagonal, with O the rest of A. That halves the error of
 //     well-conditioned matrices (1.2e-3 to 6e-4).
-// Values are held times powers of two, so that entries of ordinary size are normal fp16
-// numbers: X times 2^lift, about the square root of its longer side, O and B times 2^8.
+// Values are held times powers of two, so that they are normal fp16 numbers far down: X times 2^12
+// (muon.h), O and B times 2^8.
 // Matrices with few rows are worked on in muon_small.hip.
 #include "muon_device.h"
 
@@ -59,7 +59,7 @@ __device__ __forceinline__ double mu_factor(const MuTensor& t, int b, double eps
     double s = 0.0;
     for (int i = threadIdx.x; i < t.parts; i += kMuThreads) s += *gld<double>(p + i);
     s = block_sum_d(s, sums);
-    if (threadIdx.x == 0) sums[kMuThreads / 64] = mu_factor_of(s, eps, t.lift);
+    if (threadIdx.x == 0) sums[kMuThreads / 64] = mu_factor_of(s, eps);
     __syncthreads();
     return sums[kMuThreads / 64];
 }
@@ -522,7 +522,7 @@ __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_gram
     const MuRound<M> r(lds, ti * M::kT, tj * M::kT, MuRound<M>::kBytes);
     uint16_t* const o = reinterpret_cast<uint16_t*>(w + at.a);
     float* const d = reinterpret_cast<float*>(w + at.d);
-    const float un = 1.0f / (m.lift * m.lift), scale = kMuLift * un;  // powers of two: exact
+    constexpr float un = kMuGramUnlift, scale = kMuLift * un;  // powers of two: exact
 #pragma unroll
     for (int jj = 0; jj < M::NB; ++jj) {
         const int j0 = r.jb + 32 * jj;
@@ -565,7 +565,7 @@ __global__ __launch_bounds__(kMuThreads) void k_mu_join(MuListOf<MuMatrix, N> l)
     const float* p = reinterpret_cast<const float*>(w + at.part) + static_cast<int64_t>(j) * m.mp + i;
     f32x4 s = *gld<f32x4>(p);
     for (int e = 1; e < m.parts; ++e) s += *gld<f32x4>(p + static_cast<int64_t>(e) * m.mp * m.mp);
-    const float un = 1.0f / (m.lift * m.lift);
+    constexpr float un = kMuGramUnlift;
     float v[4] = {s.x * un, s.y * un, s.z * un, s.w * un};
     float* const d = reinterpret_cast<float*>(w + at.d);
 #pragma unroll
@@ -718,7 +718,7 @@ __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_appl
     mu_accumulate<M, true>(x, m.np, m.np, reinterpret_cast<const uint16_t*>(w + at.b), m.mp, m.mp, ti * M::kT, tj * M::kT, 0,
                            m.mp / 32, lds, acc);
     if (M::kT == 256) load(r.jb, next);
-    const float un = 1.0f / m.lift * kMuUnlift;
+    constexpr float un = kMuXUnlift * kMuUnlift;
     const float* const d = reinterpret_cast<const float*>(w + at.d);
 #pragma unroll
     for (int jj = 0; jj < M::NB; ++jj) {

@@ -143,10 +143,10 @@ __device__ __forceinline__ void mu_take8(const MuTensor& t, const MuStepArgs& a,
     mu_direction(a, g, m, u);
 }
 
-// 2^lift / max(norm, eps); a norm that is not finite gives NaN, one of zero (with eps zero) 0.
-__device__ __forceinline__ double mu_factor_of(double squares, double eps, int lift) {
+// 2^12 / max(norm, eps); a norm that is not finite gives NaN, one of zero (with eps zero) 0.
+__device__ __forceinline__ double mu_factor_of(double squares, double eps) {
     const double norm = sqrt(squares), top = norm > eps ? norm : eps;
-    return !(norm <= 1.7976931348623157e308) ? __builtin_nan("") : top > 0.0 ? ldexp(1.0, lift) / top : 0.0;
+    return !(norm <= 1.7976931348623157e308) ? __builtin_nan("") : top > 0.0 ? static_cast<double>(kMuXLift) / top : 0.0;
 }
 
 // ----------------------------------------------------------------------------- fp16 values, LDS

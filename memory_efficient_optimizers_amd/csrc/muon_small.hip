@@ -173,7 +173,7 @@ struct MuFew {
         return w;
     }
 
-    // A chunk of X X^T (times 4^lift) becomes O's, 2^8 times, its two parts in the chunk's place;
+    // A chunk of X X^T (times 4^12) becomes O's, 2^8 times, its two parts in the chunk's place;
     // the diagonal goes to diag().
     __device__ uint32_t diag() const { return sums + kSums; }
     __device__ uint32_t rows() const { return sums + kSums + R * 4; }  // q
@@ -414,7 +414,7 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_few(MuListOf<MuFewTenso
             for (int e = 0; e < kVec; ++e) u[q][e] = w[e];
         });
     }
-    const double f = mu_factor_of(mu_few_sum(sum, m.sums), a.step.eps, s.lift);
+    const double f = mu_factor_of(mu_few_sum(sum, m.sums), a.step.eps);
 
     // X0 in two parts
 #pragma unroll 1
@@ -445,7 +445,7 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_few(MuListOf<MuFewTenso
     }
     __syncthreads();
 
-    const float lift = ldexpf(1.0f, s.lift), un = 1.0f / (lift * lift), out = 1.0f / lift * kMuUnlift;
+    constexpr float un = kMuGramUnlift, out = kMuXUnlift * kMuUnlift;
     const int64_t first = static_cast<int64_t>(b) * t.rows * t.ldx;
 #pragma unroll 1
     for (int step = 0; step < a.steps; ++step) {
@@ -489,7 +489,7 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_start(MuListOf<Mu
     double sum = 0.0;
     const double* p = t.norm + static_cast<int64_t>(b) * t.parts;
     for (int i = threadIdx.x; i < t.parts; i += kMuFewThreads) sum += *gld<double>(p + i);
-    const double f = mu_factor_of(mu_few_sum(sum, m.sums), a.eps, t.lift);
+    const double f = mu_factor_of(mu_few_sum(sum, m.sums), a.eps);
     const int c0 = strip * M::kStrip, per = t.tall ? (t.cols + kVec - 1) / kVec : M::kStrip / kVec;  // 8 values each of a row
     const int rows = t.tall ? min(M::kStrip, t.rows - c0) : t.rows;
 #pragma unroll 2
@@ -564,7 +564,7 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_step(MuListOf<MuT
             high[n][sb][it][v] = *gld<u32x2>(w + o);
             low[n][sb][it][v] = *gld<u32x2>(w + at.lo + o);
         });
-    const float lift = ldexpf(1.0f, t.lift), un = 1.0f / (lift * lift);
+    constexpr float un = kMuGramUnlift;
     // the parts' sums, in order of groups of parts
     constexpr int kChunks = M::kPart / 16, kGroups = kChunks < kMuFewThreads ? kMuFewThreads / kChunks : 1;
     const float* const parts = reinterpret_cast<const float*>(ws + at.part) + static_cast<int64_t>(src) * strips * R * R;
@@ -601,7 +601,7 @@ __global__ __launch_bounds__(kMuFewThreads, 2) void k_mu_strip_step(MuListOf<MuT
         for (int n = 0; n < M::NB; ++n)
             m.apply(m.block(n), [&](int sb, int it, int v, const f32x4& y) {
                 mu_few_store(t, update, decay, first, it * M::T + m.col, strip * M::kStrip + 32 * m.block(n) + m.column(sb, v),
-                             y * (1.0f / lift * kMuUnlift));
+                             y * (kMuXUnlift * kMuUnlift));
             });
         return;
     }

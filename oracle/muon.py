@@ -3,7 +3,8 @@
     X_0 = U / max(|U|, eps),  A = X X^T,  X <- a X + (b A + c A^2) X   (U's shorter side as rows)
 
 ``rounded_newton_schulz`` is the same with the roundings that the library's products make, in
-fp64 otherwise: what its results may be off by is judged against that.
+fp64 otherwise: what its results may be off by is judged against that. ``single_newton_schulz`` is
+the same in fp32 throughout.
 """
 from __future__ import annotations
 
@@ -14,6 +15,7 @@ import numpy as np
 from .optimizers import round_bf16
 
 COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+LIFT = 2.0 ** 12  # the library holds the iterate times this in fp16
 
 
 def per_step(coefficients, steps):
@@ -46,13 +48,16 @@ def _half(v, scale):
     return np.asarray(v * scale, np.float32).astype(np.float16).astype(np.float64) / scale
 
 
-def rounded_newton_schulz(u, steps=5, coefficients=COEFFICIENTS, eps=1e-7):
+def rounded_newton_schulz(u, steps=5, coefficients=COEFFICIENTS, eps=1e-7, parts=1):
+    """``parts``: of fp16 that the products' operands have (2: matrices with few rows)."""
     x, tall = start(u, eps)
-    lift = 2.0 ** min(12, round(0.5 * math.log2(max(u.shape))))
+    if parts == 2:
+        x = _rounded_in_two_parts(x, per_step(coefficients, steps))
+        return x.T if tall else x
 
     def parts(v):
-        hi = _half(v, lift)
-        return hi, _half(v - hi, lift)
+        hi = _half(v, LIFT)
+        return hi, _half(v - hi, LIFT)
 
     hi, lo = parts(x)
     for a, b, c in per_step(coefficients, steps):
@@ -69,6 +74,37 @@ def rounded_newton_schulz(u, steps=5, coefficients=COEFFICIENTS, eps=1e-7):
     return x.T if tall else x
 
 
+def _rounded_in_two_parts(x, coefficients):
+    """Every operand as hi + lo, products without lo lo."""
+    def parts(v, lift):
+        hi = _half(v, lift)
+        return hi, _half(v - hi, lift)
+
+    def mul(p, q):
+        return p[0] @ q[0] + p[0] @ q[1] + p[1] @ q[0]
+
+    for a, b, c in coefficients:
+        x = parts(x, LIFT)
+        g = mul(x, (x[0].T, x[1].T))
+        d = np.diag(g).astype(np.float32).astype(np.float64)
+        o = parts(g - np.diag(np.diag(g)), 256.0)
+        sq = mul(o, o)
+        p = (o[0] + o[1]) * (b + c * (d[:, None] + d[None, :])) + c * sq
+        q = (a + b * d + c * (d * d + np.diag(sq))).astype(np.float32).astype(np.float64)
+        p = parts(p - np.diag(np.diag(p)), 256.0)
+        x = q[:, None] * (x[0] + x[1]) + mul(p, x)
+    return x
+
+
+def single_newton_schulz(u, steps=5, coefficients=COEFFICIENTS, eps=1e-7):
+    x, tall = start(u, eps)
+    x = x.astype(np.float32)
+    for a, b, c in np.asarray(per_step(coefficients, steps), np.float32):
+        g = x @ x.T
+        x = a * x + (b * g + c * (g @ g)) @ x
+    return (x.T if tall else x).astype(np.float64)
+
+
 def bound_of_one_step(u, coefficients=COEFFICIENTS, eps=1e-7):
     """How far one step's result may be off, element by element: every rounding counted at its
     most (fp16 2^-11 of the value, sums in fp32 2^-23 of the terms' magnitudes per term)."""
@@ -77,8 +113,7 @@ def bound_of_one_step(u, coefficients=COEFFICIENTS, eps=1e-7):
     m, n = x.shape
     h, s, tiny = 2.0 ** -11, (n + m + 8) * 2.0 ** -23, 2.0 ** -24 / 256  # (smallest fp16 step of O and B)
     ax = np.abs(x)
-    lift = 2.0 ** min(12, round(0.5 * math.log2(max(u.shape))))
-    ex = h * ax + 2.0 ** -24 / lift  # of an operand
+    ex = h * ax + 2.0 ** -24 / LIFT  # of an operand
     ag = ax @ ax.T
     eg = ex @ ax.T + ax @ ex.T + ex @ ex.T + s * ag
     eo = eg + h * (ag + eg) + tiny  # (the diagonal is not rounded: more than it needs)
@@ -86,7 +121,7 @@ def bound_of_one_step(u, coefficients=COEFFICIENTS, eps=1e-7):
     ep = abs(b) * eo + abs(c) * (ag2 @ eo + eo @ ag2) + s * (abs(b) * ag2 + abs(c) * (ag2 @ ag2))
     ap = abs(b) * ag2 + abs(c) * (ag2 @ ag2)
     ep = ep + h * (ap + ep) + tiny
-    ey = ep @ ax + ap @ ex + ep @ ex + (s + 2.0 ** -21) * (abs(a) * ax + ap @ ax) + abs(a) * 2.0 ** -24 / lift / 2048
+    ey = ep @ ax + ap @ ex + ep @ ex + (s + 2.0 ** -21) * (abs(a) * ax + ap @ ax) + abs(a) * 2.0 ** -25 / LIFT
     return ey.T if tall else ey
 
 

@@ -182,6 +182,19 @@ def test_norms_near_and_below_eps():
     assert np.max(np.abs(y - want)) <= 485 * 2.0 ** -24 / math.sqrt(30) * 2
 
 
+@pytest.mark.parametrize("shape", [(1, 1), (2, 2), (40, 60), (20, 1500), (70, 130)])
+def test_singular_values_up_to_8(shape):
+    """The largest that coefficients may let grow, in a matrix of rank 1 (entries 8 and less). Beside the
+    products' roundings one entry has most of the norm: X_0 to float32, two splits (2^-23), two sums, lr s, its product: 9 x 2^-24."""
+    x = torch.ones(shape, device=DEV)
+    x[0] = 2.0 ** -20  # (one row, or one entry, has most of it)
+    x[:, 0] *= 2.0 ** 20
+    for coefficients in ([(8.0, 0.0, 0.0), (0.9, -0.02, 0.0002)], [(8.0, 0.0, 0.0), (0.125, 0.0, 0.0)]):
+        got, want = to64(raw([x], ns_steps=2, ns_coefficients=coefficients)[0]), exact(x, steps=2, coefficients=coefficients)
+        lim = slack(x, steps=2, coefficients=coefficients)[0] + 9 * 2.0 ** -24 * np.linalg.norm(want)
+        assert np.linalg.norm(got - want) <= lim, (np.linalg.norm(got - want), lim)
+
+
 @pytest.mark.parametrize("steps,coefficients", [(1, om.COEFFICIENTS), (2, om.COEFFICIENTS), (8, om.COEFFICIENTS), (10, (2.0, -1.5, 0.5)),
                                                 (4, [(8.2, -22.9, 16.46), (4.0, -2.9, 0.5), (3.9, -2.8, 0.5), (3.3, -2.4, 0.5)])])
 def test_coefficients_and_steps(steps, coefficients):
@@ -387,6 +400,39 @@ def test_steps_and_coefficients_of_few_rows():
             check(orthogonalize(x, steps=steps, coefficients=coefficients), x, steps=steps, coefficients=coefficients)
 
 
+def scaled(shape, seed, kind):
+    """Matrices whose entries have very different size: one strong entry over noise of 1e-6, sizes of the
+    shorter side's rows over five decades, rank 1."""
+    gen = torch.Generator().manual_seed(seed)
+    m, n = min(shape), max(shape)
+    x = torch.randn(m, n, generator=gen)
+    if kind == "entry":
+        x = 1e-6 * x
+        x[m // 3, n // 2] = 1.0
+    if kind == "decades":
+        x = x * torch.logspace(0, -5, m).unsqueeze(1)
+    if kind == "one":
+        x = torch.randn(m, 1, generator=gen) @ torch.randn(1, n, generator=gen)
+    return (x if shape[0] == m else x.t().contiguous()).to(DEV)
+
+
+def few_slack(u, **kw):
+    """Of matrices with few rows: operands in two parts and float32's own roundings, each in two realizations."""
+    want = om.newton_schulz(u, **kw)
+    return 2 * (np.linalg.norm(om.rounded_newton_schulz(u, parts=2, **kw) - want) + np.linalg.norm(om.single_newton_schulz(u, **kw) - want))
+
+
+@pytest.mark.parametrize("kind,steps", [("entry", 5), ("entry", 10), ("decades", 5), ("decades", 10), ("one", 5)])
+@pytest.mark.parametrize("shape", [(16, 16), (30, 20), (64, 64), (48, 200), (16, 900), (900, 16), (60, 2000), (2000, 32)])
+def test_few_rows_of_very_different_size(shape, kind, steps):
+    """The result's own rounding: 2^-22."""
+    x = scaled(shape, 115, kind)
+    u = to64(x)
+    want, got = om.newton_schulz(u, steps), to64(raw([x], ns_steps=steps)[0])
+    lim = few_slack(u, steps=steps) + 2.0 ** -22 * np.linalg.norm(want)
+    assert np.linalg.norm(got - want) <= lim, (np.linalg.norm(got - want), lim)
+
+
 # ------------------------------------------------------------------------------ the Muon step
 
 def init(shape, seed, param, grad, state, scale=1e-3):
@@ -451,6 +497,29 @@ def test_step_of_few_rows(param, grad, state):
     muon_step(ps, gs, sts, momentum=0.9, **kw)
     for p, st, (p0, g, m0) in zip(ps, sts, before):
         check_step(p, st, p0, g, m0, str(state).split(".")[1], momentum_=0.9, **kw)
+
+
+@pytest.mark.parametrize("kind", ["noise", "entry", "decades"])
+@pytest.mark.parametrize("nesterov", [True, False])
+@pytest.mark.parametrize("state", [torch.float32, torch.bfloat16, torch.int8])
+def test_step_of_few_rows_keeps_22_bits(state, nesterov, kind):
+    """On parameters of zeros without decay, so that what is stored is the update, rounded by 2^-22 of it at most
+    (the product with lr s, the store)."""
+    kw = dict(lr=0.5, weight_decay=0.0, nesterov=nesterov, adjust_lr="match_rms_adamw")
+    for i, shape in enumerate(((16, 16), (40, 64), (64, 30), (16, 1024), (1100, 20), (60, 700))):
+        p, g, st = init(shape, 320 + i, torch.float32, torch.float32, state)
+        if kind != "noise":
+            g = scaled(shape, 330 + i, kind)
+            st = {k: torch.zeros_like(v) for k, v in st.items()}
+        p.zero_()
+        m0 = momentum_of(st)
+        muon_step([p], [g], [st], momentum=0.9, **kw)
+        m, _ = om.momentum(m0, g.cpu().numpy(), 0.9, str(state).split(".")[1])
+        assert np.array_equal(momentum_of(st), m)
+        u = om.direction(m, g.cpu().numpy(), 0.9, nesterov)
+        want, c = om.newton_schulz(u), 0.5 * om.shape_scale("match_rms_adamw", *shape)
+        lim = few_slack(u) + 2.0 ** -22 * np.linalg.norm(want)
+        assert np.linalg.norm(to64(p) + c * want) <= c * lim, (shape, np.linalg.norm(to64(p) + c * want) / c, lim)
 
 
 @pytest.mark.parametrize("shape", [(16, 77), (77, 16), (30, 1203), (1203, 30)])
