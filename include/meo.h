@@ -659,7 +659,8 @@ int32_t meo_mx4_matmul_rows(int64_t m, int64_t n);
  * (meo_orthogonalize_defaults): eps 1e-7, 5 steps of (3.4445, -4.7750, 2.0315), the values Muon
  * was published with. MEO_EINVAL for non-finite values, negative eps, steps out of range, and
  * for coefficients under which a singular value of at most 1 could grow past 8, or
- * |b s^2 + c s^4| past 100, in any step (the range that the fp16 operands have).
+ * |b s^2 + c s^4| past 100, in any step, or no singular value could be above 1/64 after a step
+ * other than the last (the range that the fp16 operands have).
  */
 #define MEO_NS_MAX_STEPS 16
 typedef struct meo_orthogonalize_hparams {

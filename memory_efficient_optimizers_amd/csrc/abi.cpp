@@ -2919,6 +2919,10 @@ int check_ns_hp(const meo_orthogonalize_hparams* hp) {
             if (v > 0.0 && v < s2) next = std::max(next, std::abs(std::sqrt(v) * (a + b * v + c * v * v)));
         if (!(next <= kMuMaxSingular) || !(poly <= 100.0))
             return fail(MEO_EINVAL, "coefficients of step " + std::to_string(k) + " let singular values grow too large");
+        // (what comes after would multiply zeros, or what fp16 has left; the last step's results are not held in fp16.
+        // It bounds the coefficients too, which are float32 in the kernels.)
+        if (k + 1 < hp->steps && !(next >= kMuMinSingular))
+            return fail(MEO_EINVAL, "coefficients of step " + std::to_string(k) + " make singular values too small for the next step");
         top = next;
     }
     return MEO_OK;

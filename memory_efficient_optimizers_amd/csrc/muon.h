@@ -19,7 +19,7 @@ constexpr int64_t kMuMaxSide = 1 << 22;  // longer side of a matrix (32-bit offs
 // linear coefficient: 64 x 64 with one strong entry over 1e-6 of noise, times 2^3, was 9.8e-5 off, 2.4e-3 after
 // ten steps.)
 constexpr float kMuXLift = 4096.0f, kMuXUnlift = 1.0f / 4096, kMuGramUnlift = kMuXUnlift * kMuXUnlift;
-constexpr double kMuMaxSingular = 8.0;
+constexpr double kMuMaxSingular = 8.0, kMuMinSingular = 1.0 / 64;  // of the largest singular value, between steps
 static_assert(kMuXLift * kMuMaxSingular <= 32768.0, "half of fp16's range, for roundings");
 
 // What the passes over the caller's tensors need of one of them ([batch] matrices).

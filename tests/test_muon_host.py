@@ -105,6 +105,34 @@ def test_hyperparameter_refusals(kw, why):
         _lib.meo_muon_validate(hp, 1, [], [], [])
 
 
+@pytest.mark.parametrize("coefficients", [
+    [(0.0, 0.0, 0.0), (1e300, 0.0, 0.0)],    # zeros times a float's infinity
+    [(0.0, 0.0, 0.0), (1.0, -1e300, 0.0)], [(0.0, 0.0, 0.0), (1.0, 0.0, 1e39)],
+    [(1e-4, 0.0, 0.0), (5e4, 0.0, 0.0)],     # down to where fp16 holds few bits, and up again
+    [(1.0, -1.0, 0.0), (0.04, 0.0, 0.0), (20.0, 0.0, 0.0)],  # s (1 - s^2) <= 0.385, times 0.04
+])
+def test_coefficients_that_shrink_every_singular_value(coefficients):
+    """Refused, except in the last step, whose results are not held in fp16."""
+    steps = len(coefficients)
+    with pytest.raises(MeoError, match="too small") as e:
+        _lib.meo_orthogonalize_validate(_lib.orthogonalize_hparams(steps, coefficients), [], [])
+    assert e.value.code == _lib.MEO_EINVAL
+    with pytest.raises(MeoError, match="too small"):
+        _lib.meo_muon_validate(_lib.muon_hparams(ns_steps=steps, ns_coefficients=coefficients), 1, [], [], [])
+    _lib.meo_orthogonalize_validate(_lib.orthogonalize_hparams(steps - 1, coefficients[:-1]), [], [])
+
+
+def test_smallest_values_between_steps():
+    """2^-6, held to 2^-37: 22 bits of entries that the longer side of 2^16 values spreads it over."""
+    for a, ok in ((2.0 ** -6, True), (0.9 * 2.0 ** -6, False)):
+        hp = _lib.orthogonalize_hparams(2, [(a, 0.0, 0.0), (64.0, 0.0, 0.0)])
+        if ok:
+            _lib.meo_orthogonalize_validate(hp, [], [])
+        else:
+            with pytest.raises(MeoError, match="too small"):
+                _lib.meo_orthogonalize_validate(hp, [], [])
+
+
 @pytest.mark.parametrize("coefficients,steps", [
     ((2.0, -1.5, 0.5), 10), ((1.5, -0.5, 0.0), 16), ((2.0, 0.0, 0.0), 3), (om.COEFFICIENTS, 16),
     ([(8.2, -22.9, 16.46), (4.0, -2.9, 0.5), (3.9, -2.8, 0.5), (3.3, -2.4, 0.5)], 4)])
