@@ -70,9 +70,10 @@ __host__ __device__ constexpr int64_t mu_rows(int64_t r, int64_t cols) { return 
 
 // A matrix in the workspace (offsets in bytes): two buffers of X's high parts and one of the
 // low parts ([mp][np] fp16), off-diagonal A and B ([mp][mp] fp16), the diagonal of A and
-// the row factors a + B_ii ([mp] fp32), partial sums of A.
+// the row factors a + B_ii ([mp] fp32), what the low parts add to the diagonal (two buffers of [mp] int32,
+// mu_fix), partial sums of A.
 struct MuPlace {
-    int64_t x, lo, a, b, d, q, part, total;
+    int64_t x, lo, a, b, d, q, e, part, total;
     __host__ __device__ MuPlace(int64_t mp, int64_t np, int64_t parts) {
         const int64_t s = mp * mp * 2;
         x = mp * np * 2;
@@ -81,10 +82,12 @@ struct MuPlace {
         b = a + s;
         d = b + s;
         q = d + mp * 4;
-        part = (q + mp * 4 + 255) / 256 * 256;
+        e = q + mp * 4;
+        part = (e + 2 * mp * 4 + 255) / 256 * 256;
         total = part + (parts > 1 ? parts * mp * mp * 4 : 0);
     }
     __host__ __device__ int64_t hi(int buffer) const { return buffer ? x : 0; }
+    __host__ __device__ int64_t low(int buffer, int64_t mp) const { return e + buffer * mp * 4; }  // of the diagonal, beside hi(buffer)
 };
 
 struct MuStepArgs {   // momentum pass and scatter

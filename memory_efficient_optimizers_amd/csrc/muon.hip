@@ -14,7 +14,9 @@
 //   * A and B = b A + c A^2 off their diagonals. The diagonals, which near the end are most of
 //     A, are held in fp32 (d, and q = a + B_ii) and enter by row: (A^2)_ij = (O^2)_ij +
 //     O_ij (d_i + d_j) off the diagonal, with O the rest of A. That halves the error of
-//     well-conditioned matrices (1.2e-3 to 6e-4).
+//     well-conditioned matrices (1.2e-3 to 6e-4). d is that of both parts of X: the product has the hi
+//     parts', and whoever stores X adds up what the lo parts make of it (mu_fix). In rows with few
+//     entries of any size hi's roundings do not average out (identity of 343 rows: 8.4e-3 off without).
 // Values are held times powers of two, so that they are normal fp16 numbers far down: X times 2^12
 // (muon.h), O and B times 2^8.
 // Matrices with few rows are worked on in muon_small.hip.
@@ -41,6 +43,10 @@ __global__ __launch_bounds__(kMuThreads) void k_mu_momentum(MuListOf<MuTensor, N
     const int b = static_cast<int>(item / t.parts), part = static_cast<int>(item % t.parts);
     const int64_t size = static_cast<int64_t>(t.rows) * t.cols, base = b * size;
     const int64_t i0 = part * t.tiles_per_part * kMuPart, i1 = min(size, i0 + t.tiles_per_part * kMuPart);
+    if (part == 0 && mu_few(min(t.rows, t.cols), max(t.rows, t.cols)) == 0) {  // for k_mu_scatter's sums
+        int32_t* const e = reinterpret_cast<int32_t*>(t.ws + b * t.stride + MuPlace(t.mp, t.np, 1).low(0, t.mp));
+        for (int i = threadIdx.x; i < t.mp; i += kMuThreads) *gst<int32_t>(e + i) = 0;
+    }
     double sum = 0.0;
     for (int64_t i = i0 + threadIdx.x * kVec; i - threadIdx.x * kVec < i1; i += kMuThreads * kVec) {
         const int valid = clamp_valid(i1 - i);
@@ -81,6 +87,25 @@ __global__ __launch_bounds__(kMuThreads) void k_mu_scatter(MuListOf<MuTensor, N>
     const double f = mu_factor(t, b, a.eps, sums);
     const MuPlace at(t.mp, t.np, 1);
     uint8_t* const w = t.ws + b * t.stride;
+    // the piece of row r that a thread stores: in two parts, and what the low ones add to the diagonal
+    auto store = [&](int r, const float* v) {
+        const int q = threadIdx.x & 7;
+        uint32_t h[kVec], o[kVec];
+        float low = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            mu_split(v[e], h[e], o[e]);
+            const float hi = mu_half(u32x2{h[e], 0u}, 0);
+            low = fmaf(v[e] - hi, hi, low);
+        }
+        const int64_t i = mu_at(r0 + r, c0 + q * kVec, t.np) * 2;
+        *gst<u32x4>(w + at.hi(0) + i) = u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+        *gst<u32x4>(w + at.lo + i) = u32x4{o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16};
+        uint32_t sum = mu_fix(low);
+#pragma unroll
+        for (int k = 1; k < 8; k *= 2) sum += __shfl_xor(sum, k);
+        if (q == 0 && sum != 0) mu_fixed_add(reinterpret_cast<int32_t*>(w + at.low(0, t.mp)) + r0 + r, sum);
+    };
     const int64_t size = static_cast<int64_t>(t.rows) * t.cols;
     const int s0 = t.tall ? c0 : r0, z0 = t.tall ? r0 : c0;  // the source's first row and column
     const int q = threadIdx.x & 7;
@@ -104,16 +129,13 @@ __global__ __launch_bounds__(kMuThreads) void k_mu_scatter(MuListOf<MuTensor, N>
                 for (int e = 0; e < kVec; ++e) u[e] = g[e];
             }
         }
-        if (!t.tall) {
-            uint32_t h[kVec], o[kVec];
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) mu_split(e < valid ? static_cast<float>(u[e] * f) : 0.0f, h[e], o[e]);
-            const int64_t i = mu_at(r0 + r, c0 + q * kVec, t.np) * 2;
-            *gst<u32x4>(w + at.hi(0) + i) = u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
-            *gst<u32x4>(w + at.lo + i) = u32x4{o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16};
+        for (int e = 0; e < kVec; ++e) u[e] = e < valid ? static_cast<float>(u[e] * f) : 0.0f;
+        if (!t.tall) {
+            store(r, u);
         } else {
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) tile[r][q * kVec + e] = e < valid ? static_cast<float>(u[e] * f) : 0.0f;
+            for (int e = 0; e < kVec; ++e) tile[r][q * kVec + e] = u[e];
         }
     }
     if (!t.tall) return;
@@ -121,12 +143,10 @@ __global__ __launch_bounds__(kMuThreads) void k_mu_scatter(MuListOf<MuTensor, N>
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
         const int r = (threadIdx.x >> 3) + 32 * p;
-        uint32_t h[kVec], o[kVec];
+        float v[kVec];
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) mu_split(tile[q * kVec + e][r], h[e], o[e]);
-        const int64_t i = mu_at(r0 + r, c0 + q * kVec, t.np) * 2;
-        *gst<u32x4>(w + at.hi(0) + i) = u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
-        *gst<u32x4>(w + at.lo + i) = u32x4{o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16};
+        for (int e = 0; e < kVec; ++e) v[e] = tile[q * kVec + e][r];
+        store(r, v);
     }
 }
 
@@ -500,11 +520,21 @@ __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_gram
     uint8_t* const w = m.ws + b * m.stride;
     const uint16_t* x = reinterpret_cast<const uint16_t*>(w + at.hi(src));
     const int k0 = part * m.steps * 2, steps = min(m.steps, m.np / 64 - part * m.steps);
+    const MuRound<M> r(lds, ti * M::kT, tj * M::kT, MuRound<M>::kBytes);
+    // What the low parts add to the diagonal, of the lane's columns (read here, by all tiles: the product hides it).
+    int32_t low[M::NB];
+#pragma unroll
+    for (int jj = 0; jj < M::NB; ++jj)
+        low[jj] = *gld<int32_t>(reinterpret_cast<const int32_t*>(w + at.low(src, m.mp)) + min(r.jb + 32 * jj + r.j, m.mp - 1));
     f32x16 acc[M::MB][M::NB];
     mu_zero<M>(acc);
     mu_accumulate<M, false>(x, m.np, m.mp, x, m.np, m.mp, ti * M::kT, tj * M::kT, k0, 2 * steps, lds, acc);
+    if (r.ib == r.jb && part == 0) {  // k_mu_apply adds up the next ones
+        int32_t* const next = reinterpret_cast<int32_t*>(w + at.low(src ^ 1, m.mp));
+        for (int j = r.lane; j < 32 * M::NB; j += 64)
+            if (r.jb + j < m.mp) *gst<int32_t>(next + r.jb + j) = 0;
+    }
     if (F == kMuSmall && m.parts > 1) {
-        const MuRound<M> r(lds, ti * M::kT, tj * M::kT, 0);
         float* const o = reinterpret_cast<float*>(w + at.part) + static_cast<int64_t>(part) * m.mp * m.mp;
 #pragma unroll
         for (int jj = 0; jj < M::NB; ++jj)
@@ -513,13 +543,15 @@ __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_gram
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     const int i = r.ib + 32 * ii + 8 * v + 4 * r.h, j = r.jb + 32 * jj + r.j;
-                    const f32x16& c = acc[ii][jj];
-                    if (i < m.mp && j < m.mp)
-                        *gst<f32x4>(o + static_cast<int64_t>(j) * m.mp + i) = f32x4{c[4 * v], c[4 * v + 1], c[4 * v + 2], c[4 * v + 3]};
+                    const f32x16& a = acc[ii][jj];
+                    f32x4 c = {a[4 * v], a[4 * v + 1], a[4 * v + 2], a[4 * v + 3]};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (i + e == j && part == 0) c[e] += mu_unfix(low[jj]);
+                    if (i < m.mp && j < m.mp) *gst<f32x4>(o + static_cast<int64_t>(j) * m.mp + i) = c;
                 }
         return;
     }
-    const MuRound<M> r(lds, ti * M::kT, tj * M::kT, MuRound<M>::kBytes);
     uint16_t* const o = reinterpret_cast<uint16_t*>(w + at.a);
     float* const d = reinterpret_cast<float*>(w + at.d);
     constexpr float un = kMuGramUnlift, scale = kMuLift * un;  // powers of two: exact
@@ -539,7 +571,7 @@ __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_gram
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (8 * v + 4 * r.h + e == r.j) {
-                            if (j0 + r.j < m.mp) stf(d + j0 + r.j, c[4 * v + e] * un);
+                            if (j0 + r.j < m.mp) stf(d + j0 + r.j, (c[4 * v + e] + mu_unfix(low[jj])) * un);
                             r.put(0, ii, v, mu_pack4(e == 0 ? 0.0f : c[4 * v] * scale, e == 1 ? 0.0f : c[4 * v + 1] * scale,
                                                      e == 2 ? 0.0f : c[4 * v + 2] * scale, e == 3 ? 0.0f : c[4 * v + 3] * scale));
                         }
@@ -732,9 +764,11 @@ __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_appl
         if (jj + 1 < M::NB) load(j0 + 32, next);
         const float dj = ldf(d + min(j0 + r.j, m.mp - 1)), qj = ldf(q + min(j0 + r.j, m.mp - 1)) * kMuLift;
         const float al = linear * kMuLift, tl = fmaf(qj - al, fminf(dj * dj, 1.0f), al);
+        uint32_t sum = 0;  // what the low parts add to row j's norm
 #pragma unroll
         for (int ii = 0; ii < M::MB; ++ii) {
             const f32x16& c = acc[ii][jj];
+            float low = 0.0f;
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
                 const u32x2 xh = r.get(0, ii, v), xl = r.get(1, ii, v);
@@ -748,11 +782,21 @@ __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_appl
                     for (int e = 0; e < 4; ++e) y[e] *= kMuUnlift;
                     const u32x2 n = mu_pack4(y[0], y[1], y[2], y[3]);
                     r.put(0, ii, v, n);
-                    r.put(1, ii, v, mu_pack4(y[0] - mu_half(n, 0), y[1] - mu_half(n, 1), y[2] - mu_half(n, 2), y[3] - mu_half(n, 3)));
+                    float o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        o[e] = y[e] - mu_half(n, e);
+                        low = fmaf(o[e], mu_half(n, e), low);
+                    }
+                    r.put(1, ii, v, mu_pack4(o[0], o[1], o[2], o[3]));
                 }
             }
+            if (!kLast && r.ib + 32 * ii < m.np) sum += mu_fix(low);
         }
         if constexpr (!kLast) {
+            sum = mu_halves(sum);
+            if (r.h == 0 && j0 < m.mp && r.ib < m.np)
+                mu_fixed_add(reinterpret_cast<int32_t*>(w + at.low(src ^ 1, m.mp)) + j0 + r.j, sum);
 #pragma unroll
             for (int e = 0; e < R::kIters; ++e) {
                 if (!r.has(m.mp, m.np, j0, e)) continue;

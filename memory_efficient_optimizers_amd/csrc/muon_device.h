@@ -149,6 +149,24 @@ __device__ __forceinline__ double mu_factor_of(double squares, double eps) {
     return !(norm <= 1.7976931348623157e308) ? __builtin_nan("") : top > 0.0 ? static_cast<double>(kMuXLift) / top : 0.0;
 }
 
+// What the low parts add to a row's norm: 2 sum of hi lo (lo^2 is 2^-24 of hi^2 and less), X times 2^12, in
+// fixed point: integers, so that neither the order of the sum nor the tiles change it. Of d at most 64 it
+// is 2^-10 and less, here 2^27; a summand is rounded by 2^-33 of X's own unit. (Of a row with a NaN: anything finite, the
+// product has the NaN.)
+constexpr float kMuFixed = 256.0f;  // of hi lo
+__device__ __forceinline__ int mu_fix(float v) {
+    return static_cast<int>(rintf(fminf(fmaxf(v * kMuFixed, -1073741824.0f), 1073741824.0f)));
+}
+__device__ __forceinline__ float mu_unfix(int v) { return static_cast<float>(v) * (2.0f / kMuFixed); }
+// Lanes 0 .. 31: the sum with lane + 32.
+__device__ __forceinline__ uint32_t mu_halves(uint32_t v) {
+    const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return p[0] + p[1];
+}
+__device__ __forceinline__ void mu_fixed_add(int32_t* p, uint32_t v) {
+    __hip_atomic_fetch_add(gst<uint32_t>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // ----------------------------------------------------------------------------- fp16 values, LDS
 
 __device__ __forceinline__ void mu_split(float v, uint32_t& hi, uint32_t& lo) {

@@ -62,7 +62,7 @@ def rounded_newton_schulz(u, steps=5, coefficients=COEFFICIENTS, eps=1e-7, parts
     hi, lo = parts(x)
     for a, b, c in per_step(coefficients, steps):
         g = hi @ hi.T
-        d = np.diag(g).astype(np.float32).astype(np.float64)
+        d = (np.diag(g) + np.sum(lo * (2 * hi + lo), axis=1)).astype(np.float32).astype(np.float64)
         o = _half(g - np.diag(np.diag(g)), 256.0)
         sq = o @ o
         p = o * (b + c * (d[:, None] + d[None, :])) + c * sq

@@ -182,6 +182,42 @@ def test_norms_near_and_below_eps():
     assert np.max(np.abs(y - want)) <= 485 * 2.0 ** -24 / math.sqrt(30) * 2
 
 
+def one_entry_rows(shape, kind):
+    """Rows with one entry each, in order or not, of one size or not."""
+    m, n = min(shape), max(shape)
+    gen = torch.Generator().manual_seed(116)
+    x = torch.zeros(m, n)
+    at = torch.arange(m) if kind == "identity" else torch.randperm(n, generator=gen)[:m]
+    x[torch.arange(m), at] = (torch.exp(1.5 * torch.randn(m, generator=gen)) if kind == "sizes"
+                              else 1.0 - 2.0 * (torch.rand(m, generator=gen) < 0.5) if kind == "signs" else torch.ones(m))
+    return (x if shape[0] == m else x.t().contiguous()).to(DEV)
+
+
+@pytest.mark.parametrize("steps", [1, 5, 10])
+@pytest.mark.parametrize("kind", ["identity", "signs", "sizes"])
+@pytest.mark.parametrize("shape", [(100, 100), (300, 300), (343, 343), (481, 481), (364, 700), (700, 130), (1000, 1100), (65, 33000)])
+def test_rows_of_one_entry(shape, kind, steps):
+    """A's diagonal from both parts of X. Roundings to float32 do not average out either (X_0, the split's 2^-23, two
+    sums, a row's factor, lr s and its product: 8 x 2^-24)."""
+    x = one_entry_rows(shape, kind)
+    got, want = to64(raw([x], ns_steps=steps)[0]), exact(x, steps=steps)
+    err, norm = np.linalg.norm(got - want), np.linalg.norm(want)
+    assert err <= slack(x, steps=steps)[0] + 8 * 2.0 ** -24 * norm
+    if steps == 5 and kind != "sizes":  # the bound of tests/test_muon_host.py
+        assert err <= 3.1e-3 * norm
+
+
+@pytest.mark.parametrize("shape", [(4096, 4096), (4096, 11008), (2048, 2048), (1024, 4096)])
+def test_rows_of_one_entry_in_large_tiles(shape):
+    """The same in every form (bound as above)."""
+    x = one_entry_rows(shape, "signs")
+    s = 1.0 / math.sqrt(shape[0])
+    for a, b, c in [om.COEFFICIENTS] * 5:
+        s = a * s + b * s ** 3 + c * s ** 5
+    for v in (x, x.t().contiguous()):
+        assert (raw([v])[0].double() - s * v.double()).norm() <= 3.1e-3 * s * math.sqrt(shape[0])
+
+
 @pytest.mark.parametrize("shape", [(1, 1), (2, 2), (40, 60), (20, 1500), (70, 130)])
 def test_singular_values_up_to_8(shape):
     """The largest that coefficients may let grow, in a matrix of rank 1 (entries 8 and less). Beside the
