@@ -649,11 +649,22 @@ int32_t meo_mx4_matmul_rows(int64_t m, int64_t n);
  * eps = 0 too); one that holds a NaN or an infinity gives NaN throughout.
  *
  * Precision. Products are fp16 with float32 sums; the iterate itself is held in 22 bits and the
- * diagonals of A and of b A + c A^2 in float32. The result is within about 1e-3 (relative, in
- * the Frobenius norm) of the exact polynomial's, at any conditioning. Matrices whose shorter
- * side is at most 64 and whose longer side at most 32768 (8192 from 33 on) have operands of two
- * fp16 parts, 22 bits: within about 1e-6 of the exact result. A bfloat16 result is rounded once, to nearest even. The iterate
- * is held to 2^-37, half a step: entries below 2^-14 have fewer bits than 22 in it, in proportion.
+ * diagonals of A and of b A + c A^2 in float32. With the default coefficients the result was at
+ * most this far from the exact polynomial's (relative, in the Frobenius norm; 65 to 4096 rows):
+ *                                            5 steps     10 steps
+ *     random entries                         1.2e-3      3e-3
+ *     singular values spread over decades    1.2e-3      1.5e-2
+ *     singular values all equal              2.5e-3      2.5e-2
+ *     entries equal, all or in blocks        1.2e-2      4e-2     (roundings all point one way)
+ * Matrices whose shorter side is at most 64 and whose longer side at most 32768 (8192 from 33 on)
+ * have operands of two fp16 parts, 22 bits, and come out as in float32 arithmetic: 5e-6 with 5
+ * steps, 1e-4 where the rank is low or singular values are spread over decades.
+ * A step multiplies what is lost by then as it does the matrix: by a in directions of small singular
+ * values, by up to 2 where they are near 1. Coefficients that do so more lose more. Where X_0 holds
+ * nothing but rounding noise in some directions (low rank), 10 steps bring it to 4e-2 of the
+ * result and 16 to the size of the others, in float32 too.
+ * A bfloat16 result is rounded once, to nearest even. The iterate is held to 2^-37, half a
+ * step: entries below 2^-14 have fewer than 22 bits in it, in proportion.
  *
  * Hyperparameters: eps, the steps (1 to MEO_NS_MAX_STEPS) and the coefficients of each. Defaults
  * (meo_orthogonalize_defaults): eps 1e-7, 5 steps of (3.4445, -4.7750, 2.0315), the values Muon

@@ -5,18 +5,21 @@
 // The products run on fp16 matrix cores with fp32 sums. What is rounded to fp16 (relative 2^-11,
 // bf16 would be 2^-8 at the same rate) and why that is enough:
 //   * X as an operand. The linear term, which alone carries the small singular values, takes X
-//     as the sum of two fp16 parts (hi + lo, 22 bits): with hi alone a matrix of rank 8 plus 1%
-//     noise came out 3.7e-2 off, so 4e-4. B takes hi only; the diagonal of B takes lo as well
+//     as the sum of two fp16 parts (hi + lo, 22 bits): with hi alone 300 x 300 of rank 8 plus 1%
+//     noise came out 2.3e-2 off, so 2.6e-4. B takes hi only; the diagonal of B takes lo as well
 //     as far as the row's norm is that of a finished matrix (B_ii min(1, d_i^2)). Where singular
 //     values are all near 1 that is most of what B lo is (gaussian 256 x 256: 9.6e-4 off, without
-//     it 1.3e-3); where few are, it would add a noise of full rank (16 x 16, rank 1 plus 1e-4 noise:
-//     1.5e-2 with B_ii lo whole, 1.7e-3 so).
+//     it 1.3e-3); where few are, it would add a noise of full rank (100 x 100, rank 1 plus 1e-4
+//     noise: 4e-3 with B_ii lo whole, 5e-4 so).
 //   * A and B = b A + c A^2 off their diagonals. The diagonals, which near the end are most of
 //     A, are held in fp32 (d, and q = a + B_ii) and enter by row: (A^2)_ij = (O^2)_ij +
 //     O_ij (d_i + d_j) off the diagonal, with O the rest of A. That halves the error of
-//     well-conditioned matrices (1.2e-3 to 6e-4). d is that of both parts of X: the product has the hi
+//     well-conditioned matrices (gaussian 256 x 256: 1.7e-3 to 9.6e-4). d is that of both parts of X: the product has the hi
 //     parts', and whoever stores X adds up what the lo parts make of it (mu_fix). In rows with few
-//     entries of any size hi's roundings do not average out (identity of 343 rows: 8.4e-3 off without).
+//     entries of any size hi's roundings do not average out (identity of 343 rows: 8.4e-3 off without,
+//     1.9e-3 so).
+// What is left is two roundings of every off-diagonal product a step, 1e-3 of the result where they
+// average out, more where they do not (meo.h has the figures).
 // Values are held times powers of two, so that they are normal fp16 numbers far down: X times 2^12
 // (muon.h), O and B times 2^8.
 // Matrices with few rows are worked on in muon_small.hip.

@@ -20,6 +20,7 @@ from memory_efficient_optimizers_amd import MeoError, Muon, _lib, orthogonalize
 from oracle import galore as ga
 from oracle import muon as om
 from tests.harness import to64
+from tests.test_muon_host import DOCUMENTED, _documented
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -180,6 +181,25 @@ def test_norms_near_and_below_eps():
     # far below: entries lose what is under 2^-24 of an orthonormal row's
     y, want = to64(raw([x * 1e-5], eps=1.0)[0]), exact(x * 1e-5, eps=1.0)
     assert np.max(np.abs(y - want)) <= 485 * 2.0 ** -24 / math.sqrt(30) * 2
+
+
+@pytest.mark.parametrize("steps", [5, 10])
+@pytest.mark.parametrize("kind", list(DOCUMENTED))
+def test_documented_precision_on_the_gpu(kind, steps):
+    """meo.h's table, and what the roundings of the very same matrices cost in the oracle. Not so where entries are
+    equal, all or in blocks: the error is that of one or a few values, not a norm over many, and may vanish in the
+    oracle by chance. One rounding of A that a float32 sum in another order turns round, 2^-11 of A, moves such a value
+    by |b s^2 + 2 c s^4| 2^-11 <= 2.5 x 2^-11 = 1.2e-3 of it, in every step."""
+    rng = np.random.default_rng(117)
+    for m, n in ((70, 90), (128, 128), (200, 333), (500, 520), (700, 1400)):
+        x = torch.from_numpy(_documented(kind, rng, m, n)).float().to(DEV)
+        x = x.t().contiguous() if m == 200 else x
+        if min(x.shape) <= 64:
+            continue
+        got, want = to64(raw([x], ns_steps=steps)[0]), exact(x, steps=steps)
+        err, norm = np.linalg.norm(got - want), np.linalg.norm(want)
+        assert err <= DOCUMENTED[kind][steps // 10] * norm, (x.shape, err / norm)
+        assert kind in ("ones", "blocks") or err <= slack(x, steps=steps)[0] + 8 * 2.0 ** -24 * norm, (x.shape, err / norm)
 
 
 def one_entry_rows(shape, kind):

@@ -61,6 +61,66 @@ def test_the_roundings_cost_little_at_any_conditioning(shape, kind):
     assert np.linalg.norm(om.rounded_newton_schulz(x) - want) <= 4e-3 * np.linalg.norm(want)
 
 
+def _documented(kind, rng, m, n):
+    if kind == "random":
+        return rng.standard_normal((m, n))
+    if kind == "decades":
+        u, s, v = np.linalg.svd(rng.standard_normal((m, n)), full_matrices=False)
+        return u @ np.diag(np.logspace(0, -rng.uniform(1, 6), m)) @ v
+    if kind == "equal":
+        return np.linalg.qr(rng.standard_normal((n, n)))[0][:m]
+    if kind == "identity":
+        return np.eye(m, n)
+    if kind == "ones":
+        return np.ones((m, n))
+    p, q = rng.integers(2, 9, 2)
+    return np.kron(np.eye(m // p + 1), np.ones((p, q)))
+
+
+# meo.h's table
+DOCUMENTED = {"random": (1.2e-3, 3e-3), "decades": (1.2e-3, 1.5e-2), "equal": (2.5e-3, 2.5e-2), "identity": (2.5e-3, 2.5e-2),
+              "ones": (1.2e-2, 4e-2), "blocks": (1.2e-2, 4e-2)}
+
+
+@pytest.mark.parametrize("steps", [5, 10])
+@pytest.mark.parametrize("kind", list(DOCUMENTED))
+def test_documented_precision(kind, steps):
+    """The figures of the header hold for the roundings, over sizes drawn from a range."""
+    rng = np.random.default_rng(3)
+    for _ in range(12):
+        m = int(rng.integers(66, 300))
+        x = _documented(kind, rng, m, m + int(rng.integers(0, 100)))
+        if min(x.shape) <= 64:
+            continue
+        want = om.newton_schulz(x, steps)
+        err = np.linalg.norm(om.rounded_newton_schulz(x, steps) - want) / np.linalg.norm(want)
+        assert err <= DOCUMENTED[kind][steps // 10], (x.shape, err)
+
+
+@pytest.mark.parametrize("kind", ["random", "equal", "identity", "ones", "blocks", "decades", "rank 1"])
+def test_documented_precision_of_few_rows(kind):
+    rng = np.random.default_rng(4)
+    for _ in range(20):
+        m = int(rng.integers(2, 56))  # (blocks: up to 8 rows more)
+        n = m + int(rng.integers(0, 300))
+        x = rng.standard_normal((m, 1)) @ rng.standard_normal((1, n)) if kind == "rank 1" else _documented(kind, rng, m, n)
+        want = om.newton_schulz(x)
+        err = np.linalg.norm(om.rounded_newton_schulz(x, parts=2) - want) / np.linalg.norm(want)
+        assert err <= (1e-4 if kind in ("decades", "rank 1") else 5e-6), (x.shape, err)
+
+
+def test_rounding_noise_of_low_rank_grows_in_float32_as_well():
+    """What the header says of 10 and 16 steps: as far off in float32 as with two parts, all the same. Where
+    all columns are equal there is no such noise: they round alike, and X stays of rank 1."""
+    rng = np.random.default_rng(5)
+    equal = rng.standard_normal((60, 1)) @ np.ones((1, 90))
+    for x, steps, least, most in ((equal, 10, 0.0, 1e-4), (equal, 16, 0.0, 1e-4),
+                                  (equal * rng.standard_normal(90), 10, 1e-3, 4e-2), (equal * rng.standard_normal(90), 16, 0.3, 10.0)):
+        want = om.newton_schulz(x, steps)
+        for got in (om.single_newton_schulz(x, steps), om.rounded_newton_schulz(x, steps, parts=2)):
+            assert least <= np.linalg.norm(got - want) / np.linalg.norm(want) <= most
+
+
 @pytest.mark.parametrize("rows", [65, 100, 300, 343, 353, 364, 481, 494])
 def test_identities_keep_their_diagonal(rows):
     """A matrix whose rows have one entry each: all roundings of X to its high part point one way, so A's diagonal
