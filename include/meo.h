@@ -695,10 +695,13 @@ typedef struct meo_ns_matrices {
 
 /* The result of a matrix does not depend on the rest of its list, bit for bit. The calls
  * allocate nothing and keep nothing: descriptors travel as kernel arguments, so that a call can
- * be captured into a graph. The workspace holds part of the list at a time (6 bytes per value
- * and 4 per value of A, of about 2^26 values or the largest matrix; less for the matrices with
- * a short side above); lists are worked off in parts, those matrices first. Errors as for the steps; MEO_ESHAPE also for a side past 2^22, a matrix past
- * 2^35 values (both after rounding up to 64) or a leading dimension below the row length. */
+ * be captured into a graph. Lists are worked off in parts of about 2^26 values or one larger
+ * matrix, those with a short side above first; the workspace holds one part. It takes 6 bytes per
+ * value of X and 4 per value of A, sides rounded up to 64, and where A's contraction is split over blocks
+ * (up to 960 rows and a longer side several times that) 4 more per value of A for each of its pieces:
+ * at most 14 bytes per value in all (448 x 2304), 10 where nothing is split. Errors as for the
+ * steps; MEO_ESHAPE also for a side past 2^22, a matrix past 2^35 values (both after rounding up
+ * to 64) or a leading dimension below the row length. */
 void   meo_orthogonalize_defaults(meo_orthogonalize_hparams* hp);
 size_t meo_orthogonalize_workspace_size(const meo_orthogonalize_hparams* hp, int32_t n, const meo_ns_matrices* matrices);
 int    meo_orthogonalize_validate(const meo_orthogonalize_hparams* hp, int32_t n, const meo_ns_matrices* matrices);

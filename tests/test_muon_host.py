@@ -304,6 +304,26 @@ def test_workspace_grows_to_a_bound():
     assert size(3, 32000, 4096) == size(1, 32000, 4096)  # larger than a part: one at a time
 
 
+def test_workspace_of_split_contractions():
+    """meo.h: 6 bytes per value of X, 4 per value of A and 4 for each piece of a split A; 14 per value at most."""
+    def size(m, n, batch=1):
+        t = _lib.meo_tensor(P, P, batch, m, n, 3 if batch > 1 else 2, 0, 0, 0)
+        return _lib.load().meo_muon_workspace_size(_lib.muon_hparams(), 1, (_lib.meo_tensor * 1)(t))
+
+    up = lambda v: -(-v // 64) * 64  # noqa: E731
+    for m, n, split in ((704, 2816, True), (128, 2560, True), (65, 32768, True), (448, 2304, True), (320, 2624, True),
+                        (65, 2000, False), (1024, 4096, False), (2048, 5461, False), (704, 1408, False)):
+        x, a = up(m) * up(n), up(m) ** 2
+        tiles, every = up(m) // 64 * (up(m) // 64 + 1) // 2, up(n) // 64
+        pieces = -(-every // max(-(-every * tiles // 256), 4)) if split else 1  # of at least 4 x 64 values, for 256 CUs
+        least = 6 * x + 4 * a + (4 * a * pieces if pieces > 1 else 0)
+        for shape in ((m, n), (n, m)):
+            assert least <= size(*shape) <= least + 32 * up(m) + 8 * 1024 + 3 * 256, (m, n, size(m, n), least)
+        assert size(m, n) <= 14 * x
+        for batch in (7, 3000):  # a part's worth of them
+            assert size(m, n, batch) == min(batch, 2 ** 26 // x) * size(m, n) or size(m, n, batch) <= 14 * max(2 ** 26, x)
+
+
 # ------------------------------------------------------------------------------ front ends
 
 def test_orthogonalize_refusals():
