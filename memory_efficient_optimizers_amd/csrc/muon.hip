@@ -178,10 +178,14 @@ template <> struct MuTiles<kMuLarge> : MuTileOf<256, 2, 4> {};
 
 // 16 bytes per lane from base + offset into LDS, lane l at dst + 16 l. In asm, because before
 // every LDS read the compiler would wait for all of its own transfers (it cannot tell what they
-// write); it writes no vector registers, mu_arrive waits for it, and nothing else here uses m0.
+// write); it writes no vector registers, and mu_arrive waits for it. (m0 is the compiler's own, which it warns
+// of; told so, it keeps no value there over a transfer.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void mu_fetch16(const uint8_t* base, uint32_t offset, uint32_t dst) {
-    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(offset), "s"(base));
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(offset), "s"(base) : "m0");
 }
+#pragma clang diagnostic pop
 // At most N of the wave's transfers are outstanding; then the same for the block.
 template <int N>
 __device__ __forceinline__ void mu_arrive() {

@@ -1,6 +1,9 @@
 """Muon's operators on the host (no GPU): the oracle against closed forms, the refusals of the
 entry points and front ends, which all come before any device work, and the layout rules."""
+import glob
 import math
+import os
+import re
 
 import numpy as np
 import pytest
@@ -382,3 +385,17 @@ def test_muon_state_checks():
             _lib.meo_muon_step(hp, 1, [p], [g], [st])
     with pytest.raises(TypeError):
         _lib.meo_muon_step(hp, 1, [p], [g], [dict(exp_avg=torch.zeros(64, 64, dtype=torch.float16))])
+
+
+# ------------------------------------------------------------------------------ sources
+
+def test_assembly_that_writes_m0_says_so():
+    """The compiler may keep a value in m0 over a statement that does not."""
+    found = 0
+    for f in glob.glob(os.path.join(os.path.dirname(_lib.__file__), "csrc", "*")):
+        with open(f) as src:
+            for s in re.findall(r"__asm__\s+volatile\((.*?)\);", src.read(), re.S):
+                if re.search(r"\\tm0|[ ,]m0,", s):
+                    found += 1
+                    assert re.search(r':\s*"m0"\s*$', s), (f, s)
+    assert found
