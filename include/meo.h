@@ -74,7 +74,7 @@
 extern "C" {
 #endif
 
-#define MEO_VERSION 11
+#define MEO_VERSION 12
 
 /* Return codes. */
 #define MEO_OK          0
@@ -707,6 +707,21 @@ size_t meo_orthogonalize_workspace_size(const meo_orthogonalize_hparams* hp, int
 int    meo_orthogonalize_validate(const meo_orthogonalize_hparams* hp, int32_t n, const meo_ns_matrices* matrices);
 int    meo_orthogonalize(const meo_orthogonalize_hparams* hp, int32_t n, const meo_ns_matrices* matrices,
                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * For tests and diagnostics: the kernel forms that the sizes of a list choose, one record per
+ * tensor (zeros for an empty one; of a batch that goes in several parts, its first). Host only; no
+ * pointer is followed. No form changes a result. Errors as meo_orthogonalize_validate, and MEO_ENULL for
+ * NULL forms with n > 0.
+ */
+typedef struct meo_ns_form {
+    int32_t rows;    /* 16, 32 or 64: few rows, in strips; 0: in tiles                        */
+    int32_t pieces;  /* strips, or the blocks that A's contraction is split over               */
+    int32_t gram, poly, apply;  /* sides of the tiles of A, of b A + c A^2 and of X; 0: strips */
+} meo_ns_form;
+
+int    meo_orthogonalize_forms(const meo_orthogonalize_hparams* hp, int32_t n, const meo_ns_matrices* matrices,
+                               meo_ns_form* forms);
 
 /*
  * Muon. Per tensor of two or more dims (its matrices independent, as everywhere in this file):

@@ -49,6 +49,7 @@ EXPORTS = [
     "meo_galore_mx4_workspace_size", "meo_galore_mx4_validate", "meo_galore_mx4_step", "meo_galore_mx4_refresh",
     "meo_galore_mx4_forms", "meo_mx4_matmul_rows",
     "meo_orthogonalize_defaults", "meo_orthogonalize_workspace_size", "meo_orthogonalize_validate", "meo_orthogonalize",
+    "meo_orthogonalize_forms",
     "meo_muon_defaults", "meo_muon_workspace_size", "meo_muon_validate", "meo_muon_step",
 ]
 MEO_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -151,6 +152,10 @@ class meo_orthogonalize_hparams(ctypes.Structure):
 class meo_ns_matrices(ctypes.Structure):
     _fields_ = [("x", c_void_p), ("out", c_void_p), ("batch", c_int64), ("rows", c_int64), ("cols", c_int64),
                 ("ldx", c_int64), ("ldo", c_int64), ("dtype", c_int32), ("reserved", c_int32)]
+
+
+class meo_ns_form(ctypes.Structure):
+    _fields_ = [(k, c_int32) for k in ("rows", "pieces", "gram", "poly", "apply")]
 
 
 MEO_MUON_ORIGINAL, MEO_MUON_MATCH_RMS_ADAMW = 0, 1
@@ -277,6 +282,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                             ("orthogonalize_workspace_size", [OH, c_int32, OM], c_size_t),
                             ("orthogonalize_validate", [OH, c_int32, OM], ctypes.c_int),
                             ("orthogonalize", [OH, c_int32, OM, c_void_p, c_size_t, c_void_p], ctypes.c_int),
+                            ("orthogonalize_forms", [OH, c_int32, OM, ctypes.POINTER(meo_ns_form)], ctypes.c_int),
                             ("muon_defaults", [UH], None), ("muon_workspace_size", [UH, c_int32, T], c_size_t),
                             ("muon_validate", [UH, c_int64, c_int32, T, US], ctypes.c_int),
                             ("muon_step", [UH, c_int64, c_int32, T, US, c_void_p, c_size_t, c_void_p], ctypes.c_int)):
@@ -1173,6 +1179,13 @@ def meo_orthogonalize(hp, xs, outs, workspace=None, stream=None) -> None:
     tensor of ``outs`` beside it."""
     ws, nb = _ws(workspace)
     _check(load().meo_orthogonalize(ctypes.byref(hp), len(xs), _ns_matrices(xs, outs), ws, nb, _stream(stream)))
+
+
+def meo_orthogonalize_forms(hp, xs, outs) -> List[meo_ns_form]:
+    """The kernel forms that the list's sizes choose, one record per tensor (host only)."""
+    forms = (meo_ns_form * max(len(xs), 1))()
+    _check(load().meo_orthogonalize_forms(ctypes.byref(hp), len(xs), _ns_matrices(xs, outs), forms))
+    return list(forms)[:len(xs)]
 
 
 def meo_muon_workspace_size(hp, params, grads, states=None) -> int:

@@ -2893,6 +2893,32 @@ int mu_form(const std::vector<MuIn>& ts, const MuChunk& c, bool apply, Tiles til
     return best;
 }
 
+// The tile forms of a part's three products.
+struct MuForms { int gram, poly, apply; };
+
+int64_t mu_square(int64_t side, int64_t tile) {  // tiles of the upper triangle
+    const int64_t q = ceil_div(side, tile);
+    return q * (q + 1) / 2;
+}
+
+MuForms mu_forms(const std::vector<MuIn>& ts, const MuChunk& c) {
+    MuForms f;
+    f.gram = mu_form(ts, c, false, [&](const MuIn& q, int64_t tile, int64_t* n, int64_t* steps) {
+        int64_t parts;
+        mu_gram_parts(q.mp(), q.np(), &parts, steps);
+        *n = parts > 1 ? 0 : mu_square(q.mp(), tile);
+    });
+    f.poly = mu_form(ts, c, false, [&](const MuIn& q, int64_t tile, int64_t* n, int64_t* steps) {
+        *n = mu_square(q.mp(), tile);
+        *steps = q.mp() / 64;
+    });
+    f.apply = mu_form(ts, c, true, [&](const MuIn& q, int64_t tile, int64_t* n, int64_t* steps) {
+        *n = ceil_div(q.mp(), tile) * ceil_div(q.np(), tile);
+        *steps = q.mp() / 64;
+    });
+    return f;
+}
+
 int check_ns_hp(const meo_orthogonalize_hparams* hp) {
     if (!hp) return fail(MEO_ENULL, "hparams is NULL");
     if (!(finite(hp->eps) && hp->eps >= 0.0)) return fail(MEO_EINVAL, "Invalid epsilon value");
@@ -3074,38 +3100,25 @@ int mu_run(const meo_orthogonalize_hparams& hp, const std::vector<MuIn>& ts, MuS
             }
             continue;
         }
-        auto square = [](int64_t side, int64_t tile) { const int64_t q = ceil_div(side, tile); return q * (q + 1) / 2; };
-        const int fg = mu_form(ts, c, false, [&](const MuIn& q, int64_t tile, int64_t* n, int64_t* steps) {
-            int64_t parts;
-            mu_gram_parts(q.mp(), q.np(), &parts, steps);
-            *n = parts > 1 ? 0 : square(q.mp(), tile);
-        });
-        const int fp = mu_form(ts, c, false, [&](const MuIn& q, int64_t tile, int64_t* n, int64_t* steps) {
-            *n = square(q.mp(), tile);
-            *steps = q.mp() / 64;
-        });
-        const int fa = mu_form(ts, c, true, [&](const MuIn& q, int64_t tile, int64_t* n, int64_t* steps) {
-            *n = ceil_div(q.mp(), tile) * ceil_div(q.np(), tile);
-            *steps = q.mp() / 64;
-        });
+        const MuForms f = mu_forms(ts, c);
         MuMatrices gram = all, parts = all, join = all, poly = all, apply = all;
-        count(gram, [&](const MuMatrix& m) { return m.parts > 1 ? 0 : m.batch * square(m.mp, kMuFormTile[fg]); });
-        count(parts, [&](const MuMatrix& m) { return m.parts > 1 ? m.batch * square(m.mp, kMuFormTile[kMuSmall]) * m.parts : 0; });
+        count(gram, [&](const MuMatrix& m) { return m.parts > 1 ? 0 : m.batch * mu_square(m.mp, kMuFormTile[f.gram]); });
+        count(parts, [&](const MuMatrix& m) { return m.parts > 1 ? m.batch * mu_square(m.mp, kMuFormTile[kMuSmall]) * m.parts : 0; });
         count(join, [&](const MuMatrix& m) { return m.parts > 1 ? m.batch * (int64_t{m.mp} / 4 * m.mp / kMuThreads) : 0; });
-        count(poly, [&](const MuMatrix& m) { return m.batch * square(m.mp, kMuFormTile[fp]); });
-        count(apply, [&](const MuMatrix& m) { return m.batch * ceil_div(m.mp, kMuFormTile[fa]) * ceil_div(m.np, kMuFormTile[fa]); });
+        count(poly, [&](const MuMatrix& m) { return m.batch * mu_square(m.mp, kMuFormTile[f.poly]); });
+        count(apply, [&](const MuMatrix& m) { return m.batch * ceil_div(m.mp, kMuFormTile[f.apply]) * ceil_div(m.np, kMuFormTile[f.apply]); });
         count(t, [&](const MuTensor& d) { return d.batch * (int64_t{d.mp} / kMuTile) * (d.np / kMuTile); });
         launch_mu_scatter(t, a, s);
         pt.mark(kPassMuScatter);
         for (int k = 0; k < hp.steps; ++k) {
             const MuPoly p = poly_of(k);
-            launch_mu_gram(gram, fg, k & 1, s);
+            launch_mu_gram(gram, f.gram, k & 1, s);
             launch_mu_gram(parts, kMuSmall, k & 1, s);
             launch_mu_join(join, s);
             pt.mark(kPassMuGram);
-            launch_mu_poly(poly, fp, p, s);
+            launch_mu_poly(poly, f.poly, p, s);
             pt.mark(kPassMuPoly);
-            launch_mu_apply(apply, fa, k & 1, p.a, k + 1 == hp.steps ? &last : nullptr, s);
+            launch_mu_apply(apply, f.apply, k & 1, p.a, k + 1 == hp.steps ? &last : nullptr, s);
             pt.mark(kPassMuApply);
         }
     }
@@ -3258,6 +3271,38 @@ size_t meo_orthogonalize_workspace_size(const meo_orthogonalize_hparams* hp, int
     for (int32_t k = 0; k < n; ++k)  // (what the call refuses)
         if (ms[k].batch < 0 || ms[k].rows < 0 || ms[k].cols < 0 || check_mu_shape("", ms[k].rows, ms[k].cols)) return 0;
     return static_cast<size_t>(mu_chunks(mu_list(n, ms), nullptr));
+}
+
+int meo_orthogonalize_forms(const meo_orthogonalize_hparams* hp, int32_t n, const meo_ns_matrices* ms, meo_ns_form* forms) {
+    const int rc = meo_orthogonalize_validate(hp, n, ms);
+    if (rc || n == 0) return rc;
+    if (!forms) return fail(MEO_ENULL, "forms is NULL");
+    const std::vector<MuIn> ts = mu_list(n, ms);
+    std::memset(forms, 0, sizeof *forms * n);
+    for (int32_t k = 0; k < n; ++k) {
+        if (ts[k].empty()) continue;
+        forms[k].rows = ts[k].few();
+        if (ts[k].few()) {
+            forms[k].pieces = static_cast<int32_t>(ts[k].strips());
+            continue;
+        }
+        int64_t parts, steps;
+        mu_gram_parts(ts[k].mp(), ts[k].np(), &parts, &steps);
+        forms[k].pieces = static_cast<int32_t>(parts);
+    }
+    std::vector<MuChunk> chunks;
+    mu_chunks(ts, &chunks);
+    for (const MuChunk& c : chunks) {
+        if (c.rows) continue;
+        const MuForms f = mu_forms(ts, c);
+        for (const MuItem& i : c.items) {
+            if (i.b0 != 0) continue;
+            forms[i.k].gram = kMuFormTile[forms[i.k].pieces > 1 ? kMuSmall : f.gram];
+            forms[i.k].poly = kMuFormTile[f.poly];
+            forms[i.k].apply = kMuFormTile[f.apply];
+        }
+    }
+    return MEO_OK;
 }
 
 int meo_orthogonalize(const meo_orthogonalize_hparams* hp, int32_t n, const meo_ns_matrices* ms, void* ws, size_t ws_bytes,

@@ -296,6 +296,46 @@ def test_large(shape):
     assert (y - want).norm() <= (4e-3 + 2.0 ** -8) * want.norm()
 
 
+# Matrices whose ends lie inside a tile of every size, wide and tall; companions in a list that bring its tiles to
+# every form, and the forms (of A, the polynomial, X).
+ENDED = [(1250, 1700), (1600, 1300)]
+COMPANIONS = [([(500, 500)], (64, 64, 64)), ([(1000, 1000)] * 4, (64, 64, 192)), ([(500, 500)] * 8, (64, 128, 128)),
+              ([(500, 500)] * 2, (128, 128, 64)), ([(500, 500)] * 4, (128, 128, 128)), ([(750, 750)] * 8, (128, 128, 192)),
+              ([(4096, 4096)], (128, 128, 256)), ([(2000, 2000)] * 3, (192, 192, 192)), ([(2500, 2500)] * 8, (256, 256, 128)),
+              ([(2250, 2250)] * 4, (256, 256, 192)), ([(2500, 2500)] * 4, (256, 256, 256))]
+
+
+@pytest.mark.parametrize("param,steps", [(torch.float32, 1), (torch.float32, 3), (torch.bfloat16, 2)])
+def test_every_tile_form_gives_the_same_bits(param, steps):
+    """As the matrices come out alone, which test_ends_of_tiles_element_by_element holds to the formula."""
+    made = [matrix(s, 118 + i) for i, s in enumerate(ENDED)]
+
+    def step(xs):
+        ps = [torch.full(x.shape, 0.5, dtype=param, device=DEV) for x in xs]
+        muon_step(ps, xs, [dict(exp_avg=torch.zeros(x.shape, device=DEV)) for x in xs], lr=0.1, momentum=0.0, nesterov=False,
+                  ns_steps=steps)
+        return ps
+
+    want = [step([x])[0] for x in made]
+    decayed = step([torch.zeros(70, 70, device=DEV)])[0][0, 0]
+    for more, form in COMPANIONS:
+        xs = made + [torch.zeros(s, device=DEV) for s in more]
+        got = _lib.meo_orthogonalize_forms(_lib.orthogonalize_hparams(steps), xs, [x.bfloat16() for x in xs])
+        assert all((f.pieces, f.gram, f.poly, f.apply) == (1, *form) for f in got), (more, form)
+        ps = step(xs)
+        assert all(torch.equal(a, b) for a, b in zip(ps, want)), (more, form)
+        assert all((p == decayed).all() for p in ps[2:]), (more, form)
+
+
+@pytest.mark.parametrize("shape", ENDED)
+def test_ends_of_tiles_element_by_element(shape):
+    x = matrix(shape, 118 + ENDED.index(shape))
+    want = exact(x, steps=1)
+    lim = om.bound_of_one_step(to64(x)) + 2.0 ** -22 * np.abs(want)
+    assert np.all(np.abs(to64(raw([x], ns_steps=1)[0]) - want) <= lim)
+    check(raw([x], ns_steps=3)[0], x, steps=3)
+
+
 def test_several_parts_of_a_list():
     """Matrices past what is worked on together (2^26 values)."""
     xs = [torch.randn(s, generator=torch.Generator(device=DEV).manual_seed(i), device=DEV).bfloat16()

@@ -327,6 +327,27 @@ def test_workspace_of_split_contractions():
             assert size(m, n, batch) == min(batch, 2 ** 26 // x) * size(m, n) or size(m, n, batch) <= 14 * max(2 ** 26, x)
 
 
+def _forms(*shapes):
+    """(rows, pieces, gram, poly, apply) of matrices of these (batch, rows, cols)."""
+    arr = (_lib.meo_ns_matrices * len(shapes))(*[_mat(batch=b, rows=r, cols=c, ldx=c, ldo=c) for b, r, c in shapes])
+    forms = _lib.meo_orthogonalize_forms(_lib.orthogonalize_hparams(), arr, arr)
+    return [(f.rows, f.pieces, f.gram, f.poly, f.apply) for f in forms]
+
+
+def test_forms():
+    """One strip, several, tiles, a split contraction, empty tensors, either way round."""
+    assert _forms((1, 16, 512), (3, 64, 8192), (1, 0, 5), (1, 20, 30)) == [(16, 1, 0, 0, 0), (64, 32, 0, 0, 0), (0, 0, 0, 0, 0), (32, 1, 0, 0, 0)]
+    assert _forms((1, 16, 32769), (1, 64, 8193)) == [(0, 129, 64, 64, 64), (0, 33, 64, 64, 64)]
+    assert _forms((1, 704, 2816)) == _forms((1, 2816, 704)) == [(0, 4, 64, 64, 64)]
+    assert _forms((1, 704, 2816), (4, 4096, 4096)) == [(0, 4, 64, 256, 256), (0, 1, 256, 256, 256)]
+    assert _forms((9, 4096, 4096), (1, 100, 100))[0][2:] == _forms((4, 4096, 4096))[0][2:]  # parts of four
+    lib, hp = _lib.load(), _lib.orthogonalize_hparams()
+    assert lib.meo_orthogonalize_forms(hp, 0, None, None) == _lib.MEO_OK
+    assert lib.meo_orthogonalize_forms(hp, 1, _mat(), None) == _lib.MEO_ENULL
+    assert lib.meo_orthogonalize_forms(hp, 1, _mat(ldx=5), None) == _lib.MEO_ESHAPE
+    assert lib.meo_orthogonalize_forms(None, 1, _mat(), None) == _lib.MEO_ENULL
+
+
 # ------------------------------------------------------------------------------ front ends
 
 def test_orthogonalize_refusals():
