@@ -2932,17 +2932,11 @@ int check_ns_hp(const meo_orthogonalize_hparams* hp) {
         double poly = std::abs(b * s2 + c * s2 * s2), next = std::abs(top * (a + b * s2 + c * s2 * s2));
         const double turn = c != 0.0 ? -b / (2.0 * c) : -1.0;  // of b x + c x^2
         if (turn > 0.0 && turn < s2) poly = std::max(poly, std::abs(b * turn + c * turn * turn));
-        // of a s + b s^3 + c s^5: a + 3 b x + 5 c x^2 = 0, x = s^2
-        double x[2] = {-1.0, -1.0};
-        const double disc = 9.0 * b * b - 20.0 * a * c;
-        if (c != 0.0 && disc >= 0.0) {
-            x[0] = (-3.0 * b + std::sqrt(disc)) / (10.0 * c);
-            x[1] = (-3.0 * b - std::sqrt(disc)) / (10.0 * c);
-        } else if (c == 0.0 && b != 0.0) {
-            x[0] = -a / (3.0 * b);
-        }
-        for (double v : x)
-            if (v > 0.0 && v < s2) next = std::max(next, std::abs(std::sqrt(v) * (a + b * v + c * v * v)));
+        // of a s + b s^3 + c s^5: a + 3 b x + 5 c x^2 = 0, x = s^2. (Both roots from the sum that does not cancel,
+        // which finds the one there is without c, or with next to none of it.)
+        const double disc = 9.0 * b * b - 20.0 * a * c, q = -0.5 * (3.0 * b + std::copysign(std::sqrt(std::max(disc, 0.0)), b));
+        for (double v : {q / (5.0 * c), a / q})
+            if (disc >= 0.0 && v > 0.0 && v < s2) next = std::max(next, std::abs(std::sqrt(v) * (a + b * v + c * v * v)));
         if (!(next <= kMuMaxSingular) || !(poly <= 100.0))
             return fail(MEO_EINVAL, "coefficients of step " + std::to_string(k) + " let singular values grow too large");
         // (what comes after would multiply zeros, or what fp16 has left; the last step's results are not held in fp16.

@@ -180,6 +180,43 @@ def test_hyperparameter_refusals(kw, why):
         _lib.meo_muon_validate(hp, 1, [], [], [])
 
 
+@pytest.mark.parametrize("c", [0.0, 1e-30, -1e-30, 1e-200, -1e-200, 5e-324, 1e-6, -1e-6])
+def test_growth_inside_the_range_with_next_to_no_fifth_power(c):
+    """30 s - 30 s^3 is 11.5 at s = 0.577, 0 at 1; 20 s - 20 s^3 is 7.7."""
+    with pytest.raises(MeoError, match="too large"):
+        _lib.meo_orthogonalize_validate(_lib.orthogonalize_hparams(1, (30.0, -30.0, c)), [], [])
+    _lib.meo_orthogonalize_validate(_lib.orthogonalize_hparams(1, (20.0, -20.0, c)), [], [])
+
+
+def test_growth_against_a_search():
+    """Random coefficients: taken if, and only if, a search over [0, top] finds the bounds kept (but for borders)."""
+    rng = np.random.default_rng(6)
+    taken = 0
+    for _ in range(3000):
+        steps = int(rng.integers(1, 4))
+        co = rng.standard_normal((steps, 3)) * 10.0 ** rng.uniform(-1, 1.2, (steps, 3))
+        co[rng.random((steps, 3)) < 0.1] = 0.0
+        top, ok, near = 1.0, True, False
+        for k, (a, b, c) in enumerate(co):
+            s = np.linspace(0.0, top, 4001)
+            p, q = np.abs(a * s + b * s ** 3 + c * s ** 5).max(), np.abs(b * s ** 2 + c * s ** 4).max()
+            for v, border in ((p, 8.0), (q, 100.0), (p, 1 / 64)):
+                near |= abs(v / border - 1) < 1e-3
+            if p > 8.0 or q > 100.0 or (k + 1 < steps and p < 1 / 64):
+                ok = False
+                break
+            top = p
+        if near:
+            continue
+        taken += ok
+        try:
+            _lib.meo_orthogonalize_validate(_lib.orthogonalize_hparams(steps, co.tolist()), [], [])
+            assert ok, co
+        except MeoError:
+            assert not ok, co
+    assert 300 < taken < 2700
+
+
 @pytest.mark.parametrize("coefficients", [
     [(0.0, 0.0, 0.0), (1e300, 0.0, 0.0)],    # zeros times a float's infinity
     [(0.0, 0.0, 0.0), (1.0, -1e300, 0.0)], [(0.0, 0.0, 0.0), (1.0, 0.0, 1e39)],
