@@ -2846,6 +2846,8 @@ int64_t mu_chunks(const std::vector<MuIn>& ts, std::vector<MuChunk>* out) {
                 c.items.push_back(i);
                 values += count * size;
                 b += count;
+                // a size alone: parts full of one tensor's matrices are alike
+                if (!out && c.items.size() == 1 && c.items[0].k == static_cast<int32_t>(k)) b += (t.batch - b) / count * count;
             }
         }
         close();
@@ -2948,7 +2950,8 @@ int check_ns_hp(const meo_orthogonalize_hparams* hp) {
     return MEO_OK;
 }
 
-int check_mu_shape(const std::string& who, int64_t rows, int64_t cols) {
+int check_mu_shape(const std::string& who, int64_t batch, int64_t rows, int64_t cols) {
+    if (batch > kMaxDim) return fail(MEO_ESHAPE, who + "batch exceeds 2^31 - 1");
     const int64_t m = ceil_div(std::min(rows, cols), kMuPad) * kMuPad, n = ceil_div(std::max(rows, cols), kMuPad) * kMuPad;
     if (n > kMuMaxSide) return fail(MEO_ESHAPE, who + "rows or cols exceed 2^22");
     if (m * n > kMuMaxValues) return fail(MEO_ESHAPE, who + "a matrix exceeds 2^35 values");
@@ -3170,9 +3173,8 @@ int check_ns_matrices(int32_t n, const meo_ns_matrices* ms) {
         if (m.dtype != MEO_F32 && m.dtype != MEO_BF16) return fail(MEO_EDTYPE, who + "dtype must be MEO_F32 or MEO_BF16");
         if (m.ldx < m.cols || m.ldo < m.cols) return fail(MEO_ESHAPE, who + "leading dimension below the row length");
         if (m.batch == 0 || m.rows == 0 || m.cols == 0) continue;
-        if (m.batch > kMaxDim || m.rows > kMaxDim || m.ldx > kMaxDim || m.ldo > kMaxDim)
-            return fail(MEO_ESHAPE, who + "batch, rows or a leading dimension exceeds 2^31 - 1");
-        const int rc = check_mu_shape(who, m.rows, m.cols);
+        if (m.ldx > kMaxDim || m.ldo > kMaxDim) return fail(MEO_ESHAPE, who + "a leading dimension exceeds 2^31 - 1");
+        const int rc = check_mu_shape(who, m.batch, m.rows, m.cols);
         if (rc) return rc;
         if (static_cast<__int128>(m.batch) * m.rows * std::max(m.ldx, m.ldo) > (static_cast<__int128>(1) << 60))
             return fail(MEO_ESHAPE, who + "too many elements");
@@ -3206,8 +3208,7 @@ int check_muon_tensors(int64_t step, int32_t n, const meo_tensor* ts, const meo_
         if (numel == 0) continue;
         if (t.ndim < 2) return fail(MEO_ESHAPE, who + "Muon takes tensors of two or more dims");
         if (t.ndim == 2 && t.batch != 1) return fail(MEO_ESHAPE, who + "a 2-D tensor has batch 1");
-        if (t.batch > kMaxDim) return fail(MEO_ESHAPE, who + "batch exceeds 2^31 - 1");
-        const int rc = check_mu_shape(who, t.rows, t.cols);
+        const int rc = check_mu_shape(who, t.batch, t.rows, t.cols);
         if (rc) return rc;
         if (!t.param) return fail(MEO_ENULL, who + "param is NULL");
         if (!t.grad) return fail(MEO_ENULL, who + "grad is NULL");
@@ -3263,7 +3264,7 @@ int meo_orthogonalize_validate(const meo_orthogonalize_hparams* hp, int32_t n, c
 size_t meo_orthogonalize_workspace_size(const meo_orthogonalize_hparams* hp, int32_t n, const meo_ns_matrices* ms) {
     if (!hp || n <= 0 || !ms) return 0;
     for (int32_t k = 0; k < n; ++k)  // (what the call refuses)
-        if (ms[k].batch < 0 || ms[k].rows < 0 || ms[k].cols < 0 || check_mu_shape("", ms[k].rows, ms[k].cols)) return 0;
+        if (ms[k].batch < 0 || ms[k].rows < 0 || ms[k].cols < 0 || check_mu_shape("", ms[k].batch, ms[k].rows, ms[k].cols)) return 0;
     return static_cast<size_t>(mu_chunks(mu_list(n, ms), nullptr));
 }
 
@@ -3338,7 +3339,7 @@ int meo_muon_validate(const meo_muon_hparams* hp, int64_t step, int32_t n, const
 size_t meo_muon_workspace_size(const meo_muon_hparams* hp, int32_t n, const meo_tensor* ts) {
     if (!hp || n <= 0 || !ts) return 0;
     for (int32_t k = 0; k < n; ++k)
-        if (ts[k].batch < 0 || ts[k].rows < 0 || ts[k].cols < 0 || check_mu_shape("", ts[k].rows, ts[k].cols)) return 0;
+        if (ts[k].batch < 0 || ts[k].rows < 0 || ts[k].cols < 0 || check_mu_shape("", ts[k].batch, ts[k].rows, ts[k].cols)) return 0;
     return static_cast<size_t>(mu_chunks(mu_list(hp, n, ts, nullptr), nullptr));
 }
 

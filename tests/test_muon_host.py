@@ -364,6 +364,25 @@ def test_workspace_of_split_contractions():
             assert size(m, n, batch) == min(batch, 2 ** 26 // x) * size(m, n) or size(m, n, batch) <= 14 * max(2 ** 26, x)
 
 
+@pytest.mark.timeout(60)
+def test_workspace_of_enormous_batches():
+    """Sizes are asked for before anything is checked: a batch that no memory holds is answered at once, one that the
+    call refuses with 0."""
+    lib, hp, u = _lib.load(), _lib.orthogonalize_hparams(), _lib.muon_hparams()
+
+    def size(batch, m, n):
+        got = lib.meo_orthogonalize_workspace_size(hp, 1, _mat(batch=batch, rows=m, cols=n, ldx=n, ldo=n))
+        assert got == lib.meo_muon_workspace_size(u, 1, _lib.meo_tensor(P, P, batch, m, n, 3, 0, 0, 0))
+        return got
+
+    for m, n in ((4096, 8192), (8192, 8192), (100, 100), (60, 1000), (3, 3)):
+        assert size(2 ** 31 - 1, m, n) == size(2 ** 20, m, n) > 0
+        assert size(2 ** 31, m, n) == size(2 ** 62, m, n) == 0
+    # (a part's rest takes what follows in the list)
+    one, rest = _lib.meo_tensor(P, P, 9, 4096, 4096, 3, 0, 0, 0), _lib.meo_tensor(P, P, 3, 4096, 4096, 3, 0, 0, 0)
+    assert lib.meo_muon_workspace_size(u, 2, (_lib.meo_tensor * 2)(one, rest)) == size(4, 4096, 4096)
+
+
 def _forms(*shapes):
     """(rows, pieces, gram, poly, apply) of matrices of these (batch, rows, cols)."""
     arr = (_lib.meo_ns_matrices * len(shapes))(*[_mat(batch=b, rows=r, cols=c, ldx=c, ldo=c) for b, r, c in shapes])
