@@ -27,6 +27,7 @@ caller.
 """
 from __future__ import annotations
 
+import warnings
 from collections import defaultdict
 from typing import Dict, List, Optional, Tuple
 
@@ -540,7 +541,8 @@ class Muon(_MeoOptimizer):
     with s = sqrt(max(1, rows / cols)) for ``adjust_lr="original"`` and 0.2 sqrt(max(rows, cols))
     for ``"match_rms_adamw"`` (updates of AdamW's size: its lr and weight decay can be kept). A
     parameter with more than two dims is a batch of matrices (its last two dims); a
-    convolution's weight is viewed as a matrix by the caller. ``ns_coefficients``: one (a, b, c)
+    convolution's weight is viewed as a matrix by the caller (one passed with its window as the
+    last two dims is warned of). ``ns_coefficients``: one (a, b, c)
     for all ``ns_steps``, or one for each.
 
     Muon is for hidden matrices. A parameter group with ``muon=False`` (embeddings, the output
@@ -577,6 +579,10 @@ class Muon(_MeoOptimizer):
             raise ValueError(f"ns_steps must be 1 to {_lib.MEO_NS_MAX_STEPS}")
         self._muon_hp(g)  # the rest
         super().add_param_group(param_group)
+        for p in self.param_groups[-1]["params"] if g["muon"] else ():
+            if p.dim() >= 4 and max(p.shape[-2:]) <= 16:
+                warnings.warn(f"Muon takes a parameter of shape {tuple(p.shape)} as a batch of {p.shape[-2]} x {p.shape[-1]} "
+                              "matrices; view a convolution's weight as the matrix that is meant", stacklevel=2)
 
     @staticmethod
     def _muon_hp(group):

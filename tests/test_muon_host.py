@@ -4,6 +4,7 @@ import glob
 import math
 import os
 import re
+import warnings
 
 import numpy as np
 import pytest
@@ -443,6 +444,22 @@ def test_muon_front_end_refusals(kw):
         opt.add_param_group(dict(params=[torch.nn.Parameter(torch.zeros(2, 2))], **kw))
     with pytest.raises(TypeError):
         Muon([p], state_dtype=torch.float16)
+
+
+def test_muon_warns_of_convolutions():
+    """Weights whose last two dims are a window are a batch of tiny matrices to Muon; experts and matrices are meant."""
+    new = lambda *s: torch.nn.Parameter(torch.zeros(s))  # noqa: E731
+    conv = new(8, 4, 3, 3)
+    with pytest.warns(UserWarning, match=r"\(8, 4, 3, 3\).*convolution"):
+        Muon([new(4, 4), conv])
+    opt = Muon([new(4, 4)])
+    with pytest.warns(UserWarning, match="convolution"):
+        opt.add_param_group(dict(params=iter([new(8, 4, 2, 3, 3)])))
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        Muon([new(4, 4), new(3, 3, 3), new(2, 6, 64, 48), new(7)])
+        Muon([dict(params=[conv], muon=False)])
+        Muon([conv.data.view(8, -1).requires_grad_()])
 
 
 def test_momentum_dtype():
