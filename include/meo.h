@@ -736,7 +736,8 @@ int    meo_orthogonalize_forms(const meo_orthogonalize_hparams* hp, int32_t n, c
  *
  * Storage: param and grad fp32 or bf16; exp_avg in the tensor's state_dtype, fp32, bf16 or 8-bit
  * as for the other steps (groups of 128 values in row-major order, which may cross rows; with
- * batch > 1 rows * cols must be a multiple of 128, MEO_ESHAPE otherwise). The step uses the
+ * batch > 1 rows * cols must be a multiple of 128, MEO_ESHAPE otherwise; the scale is max|m|
+ * times the float32 1/127, which may differ from the quotient in its last bit). The step uses the
  * stored exp_avg. It starts at zero. The arithmetic outside the products is float32.
  *
  * Defaults (meo_muon_defaults): lr 1e-3, momentum 0.95, nesterov, weight_decay 0.1,

@@ -83,6 +83,28 @@ __device__ __forceinline__ void mu_load_m(const MuTensor& t, int64_t i, int vali
         f[e] = static_cast<float>(static_cast<int8_t>(w[e >> 2] >> (8 * (e & 3)))) * (((i + e) >> 7) == (i >> 7) ? s0 : s1);
 }
 
+// As quant_i8x8, with the scale as max|m| times 1/127: no division before the codes' own.
+__device__ __forceinline__ void mu_quantize8(float* m, uint32_t& lo, uint32_t& hi, float& scale) {
+    float a = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) a = max_nan(a, fabsf(m[e]));
+    a = max_nan(a, dpp<0xb1>(a));   // over the 16 lanes of a group: swap neighbours,
+    a = max_nan(a, dpp<0x4e>(a));   // swap pairs,
+    a = max_nan(a, dpp<0x141>(a));  // mirror halves,
+    a = max_nan(a, dpp<0x140>(a));  // mirror the row
+    scale = a * (1.0f / 127.0f);
+    const bool ok = scale > 0.0f && scale <= 3.402823466e38f;  // finite and nonzero
+    if (!(scale <= 3.402823466e38f)) scale = __builtin_nanf("");
+    lo = hi = 0u;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+        const float q = fminf(fmaxf(ok ? rintf(m[e] / scale) : 0.0f, -128.0f), 127.0f);
+        const uint32_t byte = static_cast<uint32_t>(static_cast<int32_t>(q)) & 0xffu;
+        if (e < 4) lo |= byte << (8 * e); else hi |= byte << (8 * (e - 4));
+        m[e] = q * scale;
+    }
+}
+
 // The direction from the gradient and the stored momentum.
 __device__ __forceinline__ void mu_direction(const MuStepArgs& a, const float* g, const float* m, float* u) {
 #pragma unroll
@@ -110,7 +132,7 @@ __device__ __forceinline__ void mu_take8(const MuTensor& t, const MuStepArgs& a,
     if (t.mkind == 2) {
         uint32_t lo, hi;
         float scale;
-        quant_i8x8(m, lo, hi, scale);
+        mu_quantize8(m, lo, hi, scale);
         store_i8x8(t.m, t.ms, base + i, valid, (reinterpret_cast<uintptr_t>(t.m) & 7) == 0, lo, hi, scale);
     } else if (valid > 0) {
         if (t.mkind == 1)

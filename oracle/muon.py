@@ -130,12 +130,12 @@ def shape_scale(adjust_lr, rows, cols):
 
 
 def quantize(m):
-    """The momentum's 8-bit form: scale max|m| / 127 per 128 values, codes to nearest even."""
+    """The momentum's 8-bit form: scale max|m| times fp32 1/127 per 128 values, codes to nearest even."""
     v = np.asarray(m, np.float32).reshape(-1)
     n = v.size
     v = np.concatenate([v, np.zeros(-n % 128, np.float32)]).reshape(-1, 128)
     with np.errstate(all="ignore"):
-        scale = np.max(np.abs(v), axis=1) / np.float32(127.0)
+        scale = np.max(np.abs(v), axis=1) * (np.float32(1.0) / np.float32(127.0))
         ok = np.isfinite(scale) & (scale > 0)
         codes = np.where(ok[:, None], np.rint(v / np.where(ok, scale, np.float32(1.0))[:, None]), np.float32(0.0))
     scale = np.where(np.isfinite(scale), scale, np.float32(np.nan)).astype(np.float32)
