@@ -2858,7 +2858,8 @@ int64_t mu_chunks(const std::vector<MuIn>& ts, std::vector<MuChunk>* out) {
 // The tile form of a pass: the one whose tiles, dealt to the CUs, are done first. A tile takes
 // kMuTileStart (kMuApplyStart where it also moves X) and kMuTileStep per 64 values of the
 // contraction, in microseconds, beside the others that a CU holds; where large tiles move X, a round
-// that leaves CUs idle is done sooner, since memory bounds it. Fitted to (measured, model):
+// that leaves CUs idle is done sooner, since memory bounds it. Fitted to (least time measured, model; the low parts' sums
+// for A's diagonal have added 1 to 2% to every form of A and X' since):
 // A of 4096 x 4096 in 64-, 128-, 192- and 256-tiles 108 (116), 92 (97), 74 (67), 90 (94); of four of
 // them 430, 268, 261, 283 (426, 290, 268, 282); of 1024 x 1024 8, 12, 20, 28; X' of 4096 x 4096 205,
 // 144, 148, 134 (205, 142, 140, 131), of 4096 x 11008 544, 372, 373, 351 (552, 387, 368, 351), of four

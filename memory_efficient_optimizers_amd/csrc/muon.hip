@@ -35,8 +35,8 @@ struct MuNone {};
 
 // The momentum's update and the sum of squares of the direction, in fp64 (the squares of any
 // fp32 value neither vanish nor overflow). One block per part of a matrix; parts are joined by
-// every block of the next pass, in order. Bound by memory: 12.6 M values, all fp32, in 26.6 us (151 MB at
-// 5.7 TB/s).
+// every block of the next pass, in order. Bound by memory: 12.6 M values, all fp32, in 27 us (151 MB at
+// 5.6 TB/s).
 template <int N>
 __global__ __launch_bounds__(kMuThreads) void k_mu_momentum(MuListOf<MuTensor, N> l, MuStepArgs a) {
     __shared__ double sums[kMuThreads / 64];
@@ -75,8 +75,8 @@ __device__ __forceinline__ double mu_factor(const MuTensor& t, int b, double eps
 
 // The directions, scaled, into the workspace: a square tile of the padded matrix per block,
 // zeros outside the matrix. A tall matrix is transposed on the way, through LDS. Bound by memory: 12.6 M
-// values in 26.3 us (gradient and momentum again, two parts out: 151 MB at 5.7 TB/s); the direction is formed
-// twice, since keeping it between the passes would move more.
+// values in 27.5 us (gradient and momentum again, two parts out: 151 MB at 5.5 TB/s); the direction is formed
+// twice, since keeping it between the passes would move more. The low parts' sums for A's diagonal are 1 to 1.5 us of it.
 template <int N>
 __global__ __launch_bounds__(kMuThreads) void k_mu_scatter(MuListOf<MuTensor, N> l, MuStepArgs a) {
     __shared__ double sums[kMuThreads / 64 + 1];
@@ -504,9 +504,9 @@ __device__ __forceinline__ void mu_store_sym(const MuRound<M>& r, uint16_t* s, i
 
 // A = X X^T: tiles of the upper triangle, stored both ways round (sums over k in the same
 // order, so A is symmetric to the bit), 2^8 times; the diagonal in fp32. A contraction in parts
-// (small tiles only) leaves each part's fp32 sums for k_mu_join. 4096 x 4096: 74 us (192-tiles, 253 of
-// them; 67% of the matrix units' cycles, the library's product with twice the work 102 us), 4096 x 11008
-// 175 us; 256 x 512: 5.7 us, ten tiles' latency.
+// (small tiles only) leaves each part's fp32 sums for k_mu_join. Median times: 4096 x 4096 76 to 80 us (192-tiles, 253 of
+// them; 65% of the matrix units' cycles, the library's product with twice the work 102 us), 4096 x 11008
+// 182 us; 256 x 512 5.9 us, ten tiles' latency. The low parts' sums are 1 to 1.5 us of a large tile.
 template <int F, int N>
 __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_gram(MuListOf<MuMatrix, N> l, int src) {
     using M = MuTiles<F>;
@@ -624,7 +624,7 @@ __global__ __launch_bounds__(kMuThreads) void k_mu_join(MuListOf<MuMatrix, N> l)
 }
 
 // B = b A + c A^2 from A's off-diagonal part O and its diagonal d, 2^8 times off the diagonal,
-// q = a + B_ii on it. As k_mu_gram, with O's tile read in the end: 4096 x 4096 in 78 us.
+// q = a + B_ii on it. As k_mu_gram, with O's tile read in the end: 4096 x 4096 in 78 to 83 us (medians).
 template <int F, int N>
 __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_poly(MuListOf<MuMatrix, N> l, MuPoly p) {
     using M = MuTiles<F>;
@@ -701,9 +701,10 @@ __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_poly
 
 // X' = q hi + t lo + B hi (t = a + B_ii min(1, d_i^2)): X^T's tile (rows: X's columns) times B (symmetric: its rows), so that a
 // lane's four values are consecutive in a row of X'. Into the other buffer, and the low part in place;
-// the last step's into the caller's tensors. 4096 x 4096 in 138 us with 256-tiles (60% of the matrix units'
+// the last step's into the caller's tensors. Medians: 4096 x 4096 in 141 to 145 us with 256-tiles (58% of the matrix units'
 // cycles; the two parts in and out are 134 MB, 28 us of it, which the one round of tiles does not overlap),
-// 4096 x 11008 in 370 us; 24 x 256 x 688 in 13 us, memory.
+// 4096 x 11008 in 383 us; 24 x 256 x 688 in 14 us, memory. What the low parts add to the next A's diagonal is 2 us
+// of a 4096 x 4096 step.
 
 // 8 values of the result in a row, from element i on, the first `valid` of them: the
 // parameter's update or the rounded values.
