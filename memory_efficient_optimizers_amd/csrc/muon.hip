@@ -14,10 +14,10 @@
 //   * A and B = b A + c A^2 off their diagonals. The diagonals, which near the end are most of
 //     A, are held in fp32 (d, and q = a + B_ii) and enter by row: (A^2)_ij = (O^2)_ij +
 //     O_ij (d_i + d_j) off the diagonal, with O the rest of A. That halves the error of
-//     well-conditioned matrices (gaussian 256 x 256: 1.7e-3 to 9.6e-4). d is that of both parts of X: the product has the hi
-//     parts', and whoever stores X adds up what the lo parts make of it (mu_fix). In rows with few
-//     entries of any size hi's roundings do not average out (identity of 343 rows: 8.4e-3 off without,
-//     1.9e-3 so).
+//     well-conditioned matrices (gaussian 256 x 256: 1.7e-3 to 9.6e-4). d is that of both parts of
+//     X: the product has the hi parts', and whoever stores X adds up what the lo parts make of it
+//     (mu_fix). In rows with few entries of any size hi's roundings do not average out (identity of
+//     343 rows: 8.4e-3 off without, 1.9e-3 so).
 // What is left is two roundings of every off-diagonal product a step, 1e-3 of the result where they
 // average out, more where they do not (meo.h has the figures).
 // Values are held times powers of two, so that they are normal fp16 numbers far down: X times 2^12
@@ -76,7 +76,8 @@ __device__ __forceinline__ double mu_factor(const MuTensor& t, int b, double eps
 // The directions, scaled, into the workspace: a square tile of the padded matrix per block,
 // zeros outside the matrix. A tall matrix is transposed on the way, through LDS. Bound by memory: 12.6 M
 // values in 27.5 us (gradient and momentum again, two parts out: 151 MB at 5.5 TB/s); the direction is formed
-// twice, since keeping it between the passes would move more. The low parts' sums for A's diagonal are 1 to 1.5 us of it.
+// twice, since keeping it between the passes would move more. The low parts' sums for A's diagonal are
+// 1 to 1.5 us of it.
 template <int N>
 __global__ __launch_bounds__(kMuThreads) void k_mu_scatter(MuListOf<MuTensor, N> l, MuStepArgs a) {
     __shared__ double sums[kMuThreads / 64 + 1];
@@ -504,9 +505,10 @@ __device__ __forceinline__ void mu_store_sym(const MuRound<M>& r, uint16_t* s, i
 
 // A = X X^T: tiles of the upper triangle, stored both ways round (sums over k in the same
 // order, so A is symmetric to the bit), 2^8 times; the diagonal in fp32. A contraction in parts
-// (small tiles only) leaves each part's fp32 sums for k_mu_join. Median times: 4096 x 4096 76 to 80 us (192-tiles, 253 of
-// them; 65% of the matrix units' cycles, the library's product with twice the work 102 us), 4096 x 11008
-// 182 us; 256 x 512 5.9 us, ten tiles' latency. The low parts' sums are 1 to 1.5 us of a large tile.
+// (small tiles only) leaves each part's fp32 sums for k_mu_join. Median times: 4096 x 4096 76 to 80 us
+// (192-tiles, 253 of them; 65% of the matrix units' cycles, the library's product with twice the work
+// 102 us), 4096 x 11008 182 us; 256 x 512 5.9 us, ten tiles' latency. The low parts' sums are 1 to 1.5 us of
+// a large tile.
 template <int F, int N>
 __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_gram(MuListOf<MuMatrix, N> l, int src) {
     using M = MuTiles<F>;
@@ -528,7 +530,8 @@ __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_gram
     const uint16_t* x = reinterpret_cast<const uint16_t*>(w + at.hi(src));
     const int k0 = part * m.steps * 2, steps = min(m.steps, m.np / 64 - part * m.steps);
     const MuRound<M> r(lds, ti * M::kT, tj * M::kT, MuRound<M>::kBytes);
-    // What the low parts add to the diagonal, of the lane's columns (read here, by all tiles: the product hides it).
+    // What the low parts add to the diagonal, of the lane's columns (read here, by all tiles: the product
+    // hides it; behind a branch for tiles on the diagonal the compiler waited for it there).
     int32_t low[M::NB];
 #pragma unroll
     for (int jj = 0; jj < M::NB; ++jj)
@@ -701,10 +704,10 @@ __global__ __launch_bounds__(kMuTileThreads, MuTiles<F>::kBlocks) void k_mu_poly
 
 // X' = q hi + t lo + B hi (t = a + B_ii min(1, d_i^2)): X^T's tile (rows: X's columns) times B (symmetric: its rows), so that a
 // lane's four values are consecutive in a row of X'. Into the other buffer, and the low part in place;
-// the last step's into the caller's tensors. Medians: 4096 x 4096 in 141 to 145 us with 256-tiles (58% of the matrix units'
-// cycles; the two parts in and out are 134 MB, 28 us of it, which the one round of tiles does not overlap),
-// 4096 x 11008 in 383 us; 24 x 256 x 688 in 14 us, memory. What the low parts add to the next A's diagonal is 2 us
-// of a 4096 x 4096 step.
+// the last step's into the caller's tensors. Medians: 4096 x 4096 in 141 to 145 us with 256-tiles (58% of
+// the matrix units' cycles; the two parts in and out are 134 MB, 28 us of it, which the one round of tiles
+// does not overlap), 4096 x 11008 in 383 us; 24 x 256 x 688 in 14 us, memory. What the low parts add to the
+// next A's diagonal is 2 us of a 4096 x 4096 step.
 
 // 8 values of the result in a row, from element i on, the first `valid` of them: the
 // parameter's update or the rounded values.

@@ -145,16 +145,16 @@ __device__ __forceinline__ void mu_take8(const MuTensor& t, const MuStepArgs& a,
     mu_direction(a, g, m, u);
 }
 
-// 2^12 / max(norm, eps); a norm that is not finite gives NaN, one of zero (with eps zero) 0.
+// 2^12 / max(norm, eps); a norm that is not finite gives NaN, one of zero 0 (1 / eps need not be finite).
 __device__ __forceinline__ double mu_factor_of(double squares, double eps) {
     const double norm = sqrt(squares), top = norm > eps ? norm : eps;
-    return !(norm <= 1.7976931348623157e308) ? __builtin_nan("") : top > 0.0 ? static_cast<double>(kMuXLift) / top : 0.0;
+    return !(norm <= 1.7976931348623157e308) ? __builtin_nan("") : norm > 0.0 ? static_cast<double>(kMuXLift) / top : 0.0;
 }
 
 // What the low parts add to a row's norm: 2 sum of hi lo (lo^2 is 2^-24 of hi^2 and less), X times 2^12, in
 // fixed point: integers, so that neither the order of the sum nor the tiles change it. Of d at most 64 it
-// is 2^-10 and less, here 2^27; a summand is rounded by 2^-33 of X's own unit. (Of a row with a NaN: anything finite, the
-// product has the NaN.)
+// is 2^-10 and less, here 2^27; a summand is rounded by 2^-33 of X's own unit. (Of a row with a NaN: anything
+// finite, the product has the NaN.)
 constexpr float kMuFixed = 256.0f;  // of hi lo
 __device__ __forceinline__ int mu_fix(float v) {
     return static_cast<int>(rintf(fminf(fmaxf(v * kMuFixed, -1073741824.0f), 1073741824.0f)));

@@ -202,6 +202,19 @@ def test_documented_precision_on_the_gpu(kind, steps):
         assert kind in ("ones", "blocks") or err <= slack(x, steps=steps)[0] + 8 * 2.0 ** -24 * norm, (x.shape, err / norm)
 
 
+@pytest.mark.parametrize("shape", [(24, 40), (24, 1400), (100, 200), (3, 70, 40)])
+def test_zero_matrices_at_any_eps(shape):
+    """Zeros whatever eps is, also where 1 / eps is not finite; a matrix beside them is itself."""
+    z, x = torch.zeros(shape, device=DEV), matrix(shape, 121)
+    for eps in (0.0, 5e-324, 1e-310, 1e-305, 1e-300, 1e300):
+        assert (orthogonalize(z, eps=eps) == 0).all()
+        if eps < 1.0:
+            assert torch.equal(orthogonalize([z, x], eps=eps)[1], orthogonalize(x))
+        p = torch.ones(shape, device=DEV)
+        muon_step([p], [z], [dict(exp_avg=z.clone())], lr=0.5, weight_decay=0.0, eps=eps)
+        assert (p == 1).all()
+
+
 def one_entry_rows(shape, kind):
     """Rows with one entry each, in order or not, of one size or not."""
     m, n = min(shape), max(shape)
