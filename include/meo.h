@@ -644,8 +644,8 @@ int32_t meo_mx4_matmul_rows(int64_t m, int64_t n);
  *     X_0 = U / max(|U|, eps)                     (|U| the Frobenius norm)
  *     A = X_k X_k^T,  X_{k+1} = a X_k + (b A + c A^2) X_k      for each step's (a, b, c),
  * and the result is the last X (transposed back). Singular values go through the odd
- * polynomials a s + b s^3 + c s^5; with the defaults they end between 0.68 and 1.14 unless they
- * were below about 1e-3 of the norm, and singular vectors stay. A zero matrix gives zeros (with
+ * polynomials a s + b s^3 + c s^5; with the defaults they end between 0.68 and 1.21 unless they
+ * were below 1.6e-3 of the norm, and singular vectors stay. A zero matrix gives zeros (with
  * eps = 0 too); one that holds a NaN or an infinity gives NaN throughout.
  *
  * Precision. Products are fp16 with float32 sums; the iterate itself is held in 22 bits and the
@@ -696,11 +696,10 @@ typedef struct meo_ns_matrices {
 /* The result of a matrix does not depend on the rest of its list, bit for bit. The calls
  * allocate nothing and keep nothing: descriptors travel as kernel arguments, so that a call can
  * be captured into a graph. Lists are worked off in parts of about 2^26 values or one larger
- * matrix, those with a short side above first; the workspace holds one part. It takes 6 bytes per
- * value of X and 4 per value of A, sides rounded up to 64, and where A's contraction is split over blocks
- * (up to 960 rows and a longer side several times that) 4 more per value of A for each of its pieces:
- * at most 14 bytes per value in all (448 x 2304), 10 where nothing is split. Errors as for the
- * steps; MEO_ESHAPE also for a side past 2^22, a matrix past 2^35 values (both after rounding up
+ * matrix; the workspace holds one part. It takes 6 bytes per value of X and 4 per value of A, sides
+ * rounded up to 64, and where A's contraction is split over blocks (up to 960 rows and a longer side
+ * several times that) 4 more per value of A for each of its pieces: at most 14 bytes per value in
+ * all (448 x 2304), 10 where nothing is split; few rows up to 12. Errors as for the steps; MEO_ESHAPE also for a side past 2^22, a matrix past 2^35 values (both after rounding up
  * to 64) or a leading dimension below the row length. */
 void   meo_orthogonalize_defaults(meo_orthogonalize_hparams* hp);
 size_t meo_orthogonalize_workspace_size(const meo_orthogonalize_hparams* hp, int32_t n, const meo_ns_matrices* matrices);

@@ -32,6 +32,15 @@ def test_singular_values_go_through_the_polynomial():
         assert np.allclose(got, exp if x.shape == (6, 9) else exp.T, atol=1e-12)
 
 
+def test_where_singular_values_end():
+    """meo.h: between 0.68 and 1.21 from 1.6e-3 of the norm on, lower from below."""
+    s = np.logspace(math.log10(1.6e-3), 0.0, 200001)
+    low = 1.2e-3
+    for a, b, c in [om.COEFFICIENTS] * 5:
+        s, low = a * s + b * s ** 3 + c * s ** 5, a * low + b * low ** 3 + c * low ** 5
+    assert 0.68 <= s.min() <= 0.69 and 1.20 <= s.max() <= 1.21 and low < 0.6
+
+
 def test_one_by_one_zero_and_eps():
     s = 1.0
     for _ in range(5):
